@@ -28,6 +28,13 @@ FP8BS_MAX_M = 64
 FP8BS_FLAG_PDL = 1
 FP8BS_STATIC_MAX_K = 16384
 FP8BS_STATIC_MAX_SMS = 160
+FP8BS_W4_MXFP4 = 0
+FP8BS_W4_INT4 = 1
+FP8BS_W4_MAX_M = 16
+FP8BS_ROUTE_MAX_E = 1024
+FP8BS_ROUTE_MAX_K = 32
+FP8BS_ROUTE_MAX_M = 1024
+FP8BS_MOE_W4_MAX_I = 8192
 
 STATUS = {
     0: "FP8BS_OK", -1: "FP8BS_ERR_ARG", -2: "FP8BS_ERR_SHAPE", -3: "FP8BS_ERR_ALIGN",
@@ -98,6 +105,13 @@ def lib() -> ctypes.CDLL:
             "fp8bs_moe_workspace_bytes": ([i64, i64, i64, i64], ctypes.c_size_t),
             "fp8bs_moe_w8a16": ([vp, i64, i64, vp, vp, i64, vp, vp, vp, vp, i64, i64, vp, vp,
                                  ctypes.c_size_t, vp], ci),
+            "fp8bs_quant_weight_w4": ([vp, i64, i64, i64, ci, ci, vp, vp, vp], ci),
+            "fp8bs_gemv_w4a16": ([vp, i64, i64, vp, i64, vp, i64, i64, i64, ci, ci, vp, i64, c.c_uint, vp], ci),
+            "fp8bs_moe_route_workspace_bytes": ([i64, i64, i64], sz),
+            "fp8bs_moe_route": ([vp, i64, i64, i64, vp, i64, i64, ci, ci, vp, vp, vp, sz, vp], ci),
+            "fp8bs_moe_w4a16_workspace_bytes": ([i64, i64, i64], sz),
+            "fp8bs_moe_w4a16": ([vp, i64, i64, i64, vp, vp, i64, vp, vp, vp, vp, i64, i64, ci, ci, vp, vp, sz, vp],
+                                ci),
             "fp8bs_quant_weight": ([vp, i64, i64, i64, ci, vp, vp, vp], ci),
             "fp8bs_packed_weight_bytes": ([i64, i64, ci], sz),
             "fp8bs_prepack_weight": ([vp, i64, vp, i64, i64, ci, vp, sz, vp], ci),
@@ -258,6 +272,155 @@ def fp8bs_moe_w8a16(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tenso
                                _ptr(w2), _ptr(s2), E, I, _ptr(y), _ptr(workspace),
                                workspace.numel(), _stream(stream))
     _check(rc, "fp8bs_moe_w8a16")
+    return y
+
+
+_W4_FORMATS = {(FP8BS_W4_MXFP4, 32): torch.uint8, (FP8BS_W4_INT4, 32): torch.bfloat16,
+               (FP8BS_W4_INT4, 64): torch.bfloat16, (FP8BS_W4_INT4, 128): torch.bfloat16}
+
+
+def _w4_scale_dtype(fmt: int, group: int, where: str):
+    dtype = _W4_FORMATS.get((fmt, group))
+    if dtype is None:
+        raise Fp8bsError(FP8BS_ERR_ARG, where)  # not a 4-bit format, or not one of its group sizes
+    return dtype
+
+
+def fp8bs_quant_weight_w4(w: torch.Tensor, fmt: int = FP8BS_W4_MXFP4, group: int = 32,
+                          codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """fp32 w [N, K] -> (codes uint8 [N, K/2], scales [N, K/group]) in a 4-bit
+    format: FP8BS_W4_MXFP4 (group 32, uint8 e8m0 scales) or FP8BS_W4_INT4
+    (group 32, 64 or 128, bf16 scales)."""
+    _require_cuda(w, codes, scales)
+    scale_dtype = _w4_scale_dtype(fmt, group, "fp8bs_quant_weight_w4")
+    assert w.dtype == torch.float32 and w.dim() == 2 and w.stride(1) == 1
+    N, K = w.shape
+    if codes is None:
+        codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
+    if scales is None:
+        scales = torch.empty((N, K // group), dtype=scale_dtype, device=w.device)
+    assert codes.dtype == torch.uint8 and codes.is_contiguous() and codes.shape == (N, K // 2)
+    assert scales.dtype == scale_dtype and scales.is_contiguous() and scales.shape == (N, K // group)
+    rc = lib().fp8bs_quant_weight_w4(_ptr(w), N, K, w.stride(0), int(fmt), int(group), _ptr(codes), _ptr(scales),
+                                     _stream(stream))
+    _check(rc, "fp8bs_quant_weight_w4")
+    return codes, scales
+
+
+def fp8bs_gemv_w4a16(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, fmt: int = FP8BS_W4_MXFP4,
+                     group: int = 32, y: torch.Tensor | None = None, pdl: bool = False,
+                     stream=None) -> torch.Tensor:
+    """Y = bf16(x . W^T) for bf16 x [M <= 16, K] and a 4-bit weight: codes uint8
+    [N, K/2], scales [N, K/group] (rows may be strided).  pdl=True launches with
+    programmatic dependent launch; use it only when the work just before this
+    call on the stream does not write the weight."""
+    _require_cuda(x, codes, scales, y)
+    scale_dtype = _w4_scale_dtype(fmt, group, "fp8bs_gemv_w4a16")
+    M, K = x.shape
+    N = codes.shape[0]
+    assert x.dtype == torch.bfloat16 and x.stride(1) == 1
+    assert codes.dtype == torch.uint8 and codes.shape[1] * 2 == K and codes.stride(1) == 1
+    assert scales.dtype == scale_dtype and scales.shape == (N, K // group) and scales.stride(1) == 1
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    else:
+        assert y.dtype == torch.bfloat16 and y.shape == (M, N) and y.stride(1) == 1
+    rc = lib().fp8bs_gemv_w4a16(x.data_ptr(), M, x.stride(0), codes.data_ptr(), codes.stride(0), scales.data_ptr(),
+                                scales.stride(0), N, K, fmt, group, y.data_ptr(), y.stride(0),
+                                FP8BS_FLAG_PDL if pdl else 0, _stream(stream))
+    _check(rc, "fp8bs_gemv_w4a16")
+    return y
+
+
+_ROUTE_SHARED = {"none": 0, "one": 1, "gate": 2}
+
+
+def fp8bs_moe_route_workspace_bytes(M: int, E: int, H: int) -> int:
+    return int(lib().fp8bs_moe_route_workspace_bytes(int(M), int(E), int(H)))
+
+
+def new_moe_route_workspace(M: int, E: int, H: int, device=None) -> torch.Tensor:
+    """Allocate (with torch) a zeroed router workspace for up to M tokens."""
+    device = device or torch.device("cuda", torch.cuda.current_device())
+    n = fp8bs_moe_route_workspace_bytes(M, E, H)
+    if n == 0:
+        raise Fp8bsError(FP8BS_ERR_SHAPE, "fp8bs_moe_route_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def fp8bs_moe_route(x: torch.Tensor, w: torch.Tensor, k: int, renorm: bool = True, shared: str = "none",
+                    ids: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """Router: bf16 x [M, H] and w [E, H] -> (int32 ids, fp32 weights) [M, S],
+    the k experts with the largest logits per token, softmax weights
+    (renormalised over them or not).  shared="one" appends expert E with
+    weight 1, shared="gate" with weight sigmoid(x . w[E]) (w then has E + 1
+    rows)."""
+    _require_cuda(x, w, ids, weights, workspace)
+    M, H = x.shape
+    code = _ROUTE_SHARED[shared]
+    E = w.shape[0] - (1 if code == 2 else 0)
+    S = k + (1 if code else 0)
+    assert x.dtype == torch.bfloat16 and x.stride(1) == 1
+    assert w.dtype == torch.bfloat16 and w.is_contiguous() and w.shape[1] == H
+    if ids is None:
+        ids = torch.empty((M, S), dtype=torch.int32, device=x.device)
+    if weights is None:
+        weights = torch.empty((M, S), dtype=torch.float32, device=x.device)
+    assert ids.dtype == torch.int32 and ids.is_contiguous() and ids.shape == (M, S)
+    assert weights.dtype == torch.float32 and weights.is_contiguous() and weights.shape == (M, S)
+    if workspace is None:
+        workspace = new_moe_route_workspace(M, E, H, x.device)
+    rc = lib().fp8bs_moe_route(x.data_ptr(), M, H, x.stride(0), w.data_ptr(), E, k, 1 if renorm else 0, code,
+                               ids.data_ptr(), weights.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                               _stream(stream))
+    _check(rc, "fp8bs_moe_route")
+    return ids, weights
+
+
+def fp8bs_moe_w4a16_workspace_bytes(M: int, S: int, I: int) -> int:
+    return int(lib().fp8bs_moe_w4a16_workspace_bytes(int(M), int(S), int(I)))
+
+
+def new_moe_w4_workspace(M: int, S: int, I: int, device=None) -> torch.Tensor:
+    """Allocate (with torch) a zeroed 4-bit MoE workspace for up to M tokens x S slots."""
+    device = device or torch.device("cuda", torch.cuda.current_device())
+    n = fp8bs_moe_w4a16_workspace_bytes(M, S, I)
+    if n == 0:
+        raise Fp8bsError(FP8BS_ERR_SHAPE, "fp8bs_moe_w4a16_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def fp8bs_moe_w4a16(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, w13: torch.Tensor,
+                    s13: torch.Tensor, w2: torch.Tensor, s2: torch.Tensor, fmt: int = FP8BS_W4_MXFP4,
+                    group: int = 32, y: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """One small-batch MoE layer on 4-bit weights: bf16 x [M, H]; int32 topk_ids
+    and fp32 topk_w [M, S]; codes w13 [E, 2I, H/2], w2 [E, H, I/2] (uint8) with
+    scales s13 [E, 2I, H/group], s2 [E, H, I/group].  Returns bf16 y [M, H]."""
+    _require_cuda(x, topk_ids, topk_w, w13, s13, w2, s2, y, workspace)
+    scale_dtype = _w4_scale_dtype(fmt, group, "fp8bs_moe_w4a16")
+    M, H = x.shape
+    S = topk_ids.shape[1]
+    E, H2, I2 = w2.shape
+    I = 2 * I2
+    assert x.dtype == torch.bfloat16 and x.stride(1) == 1
+    assert topk_ids.dtype == torch.int32 and topk_ids.is_contiguous() and topk_ids.shape == (M, S)
+    assert topk_w.dtype == torch.float32 and topk_w.is_contiguous() and topk_w.shape == (M, S)
+    assert w13.dtype == torch.uint8 and w13.is_contiguous() and w13.shape == (E, 2 * I, H // 2)
+    assert w2.dtype == torch.uint8 and w2.is_contiguous() and H2 == H
+    assert s13.dtype == s2.dtype == scale_dtype and s13.is_contiguous() and s2.is_contiguous()
+    assert s13.shape == (E, 2 * I, H // group) and s2.shape == (E, H, I // group)
+    if y is None:
+        y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
+    else:
+        assert y.dtype == torch.bfloat16 and y.is_contiguous() and y.shape == (M, H)
+    if workspace is None:
+        workspace = new_moe_w4_workspace(M, S, I, x.device)
+    rc = lib().fp8bs_moe_w4a16(x.data_ptr(), M, H, x.stride(0), topk_ids.data_ptr(), topk_w.data_ptr(), S,
+                               w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), E, I, fmt, group,
+                               y.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream))
+    _check(rc, "fp8bs_moe_w4a16")
     return y
 
 

@@ -19,6 +19,7 @@
 #include "moe.cuh"
 #include "producer.cuh"
 #include "trace.cuh"
+#include "w4.cuh"
 
 namespace {
 
@@ -77,6 +78,13 @@ int current_sm_count(int* out) {
     *out = n;
     return FP8BS_OK;
 }
+
+// A 4-bit weight format with a group size that it has.
+bool w4_ok(int format, int group) {
+    return format == FP8BS_W4_MXFP4 ? group == 32
+                                    : format == FP8BS_W4_INT4 && (group == 32 || group == 64 || group == 128);
+}
+int64_t w4_scale_size(int format) { return format == FP8BS_W4_MXFP4 ? 1 : 2; }
 
 size_t workspace_bytes_for(int64_t K, int sm_count) { return ws_total_bytes(sm_count, K); }
 
@@ -247,6 +255,135 @@ int fp8bs_quant_weight(const float* w, int64_t N, int64_t K, int64_t ldw, int sc
         (scale_kind == FP8BS_SCALE_F32 && !aligned(ws, 4)))
         return FP8BS_ERR_ALIGN;
     return status_of(launch_quant_weight(w, N, K, ldw, scale_kind, wq, ws, as_stream(stream)));
+}
+
+int fp8bs_quant_weight_w4(const float* w, int64_t N, int64_t K, int64_t ldw, int format, int group, uint8_t* codes,
+                          void* scales, void* stream) {
+    if (!w4_ok(format, group)) return FP8BS_ERR_ARG;
+    if (N < 1 || N > kMaxDim || K < kTile || K % kTile != 0 || K > kMaxDim) return FP8BS_ERR_SHAPE;
+    if (!w || !codes || !scales) return FP8BS_ERR_ARG;
+    if (ldw < K) return FP8BS_ERR_ARG;
+    if (!aligned(w, 16) || ldw % 4 != 0 || !aligned(codes, 4) || !aligned(scales, w4_scale_size(format)))
+        return FP8BS_ERR_ALIGN;
+    return status_of(launch_quant_weight_w4(w, N, K, ldw, format, group, codes, scales, as_stream(stream)));
+}
+
+int fp8bs_gemv_w4a16(const uint16_t* x, int64_t M, int64_t ldx, const uint8_t* codes, int64_t ldc, const void* scales,
+                     int64_t lds, int64_t N, int64_t K, int format, int group, uint16_t* y, int64_t ldy,
+                     unsigned flags, void* stream) {
+    if (!w4_ok(format, group) || (flags & ~static_cast<unsigned>(FP8BS_FLAG_PDL)) != 0) return FP8BS_ERR_ARG;
+    if (M < 0 || M > FP8BS_W4_MAX_M || N < 1 || N > kMaxDim || K < kTile || K % kTile != 0 || K > kMaxDim)
+        return FP8BS_ERR_SHAPE;
+    if (M == 0) return FP8BS_OK;
+    if (!x || !codes || !scales || !y) return FP8BS_ERR_ARG;
+    if (ldx < K || ldc < K / 2 || lds < K / group || ldy < N) return FP8BS_ERR_ARG;
+    const int64_t size = w4_scale_size(format), chunk = size * (kTile / group);
+    if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(codes, 16) || ldc % 16 != 0 || !aligned(scales, chunk) ||
+        lds * size % chunk != 0 || !aligned(y, 2))
+        return FP8BS_ERR_ALIGN;
+    int sm = 0;
+    const int rc = current_sm_count(&sm);
+    if (rc != FP8BS_OK) return rc;
+    GemvW4Args a;
+    a.x = x;
+    a.ldx = ldx;
+    a.codes = codes;
+    a.ldc = ldc;
+    a.scales = static_cast<const uint8_t*>(scales);
+    a.lds = lds * size;
+    a.y = y;
+    a.ldy = ldy;
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.K = static_cast<int>(K);
+    a.format = format;
+    a.group = group;
+    a.sm_count = sm;
+    a.pdl = (flags & FP8BS_FLAG_PDL) ? 1 : 0;
+    return status_of(launch_gemv_w4(a, as_stream(stream)));
+}
+
+size_t fp8bs_moe_route_workspace_bytes(int64_t M, int64_t E, int64_t H) {
+    if (M < 0 || M > FP8BS_ROUTE_MAX_M || E < 1 || E > FP8BS_ROUTE_MAX_E || H < kTile || H % kTile != 0 || H > kMaxDim)
+        return 0;
+    return moe_route_workspace_bytes(M, E, H);
+}
+
+int fp8bs_moe_route(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const uint16_t* w, int64_t E, int64_t k,
+                    int renorm, int shared, int32_t* topk_ids, float* topk_w, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+    if (shared < FP8BS_ROUTE_SHARED_NONE || shared > FP8BS_ROUTE_SHARED_GATE) return FP8BS_ERR_ARG;
+    if (M < 0 || M > FP8BS_ROUTE_MAX_M || E < 1 || E > FP8BS_ROUTE_MAX_E || k < 1 || k > E || k > FP8BS_ROUTE_MAX_K ||
+        H < kTile || H % kTile != 0 || H > kMaxDim)
+        return FP8BS_ERR_SHAPE;
+    if (M == 0) return FP8BS_OK;
+    if (!x || !w || !topk_ids || !topk_w || !workspace) return FP8BS_ERR_ARG;
+    if (ldx < H) return FP8BS_ERR_ARG;
+    if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(w, 16) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
+        !aligned(workspace, 256))
+        return FP8BS_ERR_ALIGN;
+    if (workspace_bytes < moe_route_workspace_bytes(M, E, H)) return FP8BS_ERR_WORKSPACE;
+    MoeRouteArgs a;
+    a.x = x;
+    a.ldx = ldx;
+    a.w = w;
+    a.ids = topk_ids;
+    a.weights = topk_w;
+    a.workspace = static_cast<uint8_t*>(workspace);
+    a.M = static_cast<int>(M);
+    a.H = static_cast<int>(H);
+    a.E = static_cast<int>(E);
+    a.k = static_cast<int>(k);
+    a.renorm = renorm != 0;
+    a.shared = shared;
+    return status_of(launch_moe_route(a, as_stream(stream)));
+}
+
+size_t fp8bs_moe_w4a16_workspace_bytes(int64_t M, int64_t S, int64_t I) {
+    if (M < 0 || S < 1 || M > FP8BS_MOE_MAX_PAIRS || S > FP8BS_MOE_MAX_PAIRS || M * S > FP8BS_MOE_MAX_PAIRS ||
+        I < kTile || I % kTile != 0 || I > FP8BS_MOE_W4_MAX_I)
+        return 0;
+    return moe_w4_workspace_bytes(M, S, I);
+}
+
+int fp8bs_moe_w4a16(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const int32_t* topk_ids, const float* topk_w,
+                    int64_t S, const uint8_t* w13, const void* s13, const uint8_t* w2, const void* s2, int64_t E,
+                    int64_t I, int format, int group, uint16_t* y, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+    if (!w4_ok(format, group)) return FP8BS_ERR_ARG;
+    if (fp8bs_moe_w4a16_workspace_bytes(M, S, I) == 0 || E < 1 || E > FP8BS_MOE_MAX_EXPERTS || H < kTile ||
+        H % kTile != 0 || H > kMaxDim)
+        return FP8BS_ERR_SHAPE;
+    if (M == 0) return FP8BS_OK;
+    if (!x || !topk_ids || !topk_w || !w13 || !s13 || !w2 || !s2 || !y || !workspace) return FP8BS_ERR_ARG;
+    if (ldx < H) return FP8BS_ERR_ARG;
+    if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(w13, 16) ||
+        !aligned(s13, 8) || !aligned(w2, 16) || !aligned(s2, 8) || !aligned(y, 2) || !aligned(workspace, 256))
+        return FP8BS_ERR_ALIGN;
+    if (workspace_bytes < moe_w4_workspace_bytes(M, S, I)) return FP8BS_ERR_WORKSPACE;
+    int sm = 0;
+    const int rc = current_sm_count(&sm);
+    if (rc != FP8BS_OK) return rc;
+    MoeW4Args a;
+    a.x = x;
+    a.ldx = ldx;
+    a.ids = topk_ids;
+    a.tw = topk_w;
+    a.w13 = w13;
+    a.s13 = static_cast<const uint8_t*>(s13);
+    a.w2 = w2;
+    a.s2 = static_cast<const uint8_t*>(s2);
+    a.y = y;
+    a.workspace = static_cast<uint8_t*>(workspace);
+    a.M = static_cast<int>(M);
+    a.S = static_cast<int>(S);
+    a.H = static_cast<int>(H);
+    a.I = static_cast<int>(I);
+    a.E = static_cast<int>(E);
+    a.format = format;
+    a.group = group;
+    a.sm_count = sm;
+    return status_of(launch_moe_w4(a, as_stream(stream)));
 }
 
 size_t fp8bs_packed_weight_bytes(int64_t N, int64_t K, int scale_kind) {

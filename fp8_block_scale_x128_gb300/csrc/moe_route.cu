@@ -1,0 +1,325 @@
+// Mixture-of-experts router: l = x . w^T (bf16 in, fp32 sums), softmax over the
+// experts, the k largest per token (ties to the lowest index), their weights.
+//
+// The logits are a skinny matrix product bound by the bytes of w and, at one
+// token, by latency: 16 expert rows x one slice of H per warp (bf16 matrix
+// instructions straight from global memory, each operand read as 16-byte words
+// in a k order both share), the slices of a block summed in warp order, those
+// of several blocks through the workspace.  The last block to arrive (a
+// counter that it also resets) sums them in slice order and selects, one warp
+// per token; no block waits for another.
+//
+// The order of the chosen experts is decided by fp32 logits unless two of them
+// (or the last chosen and the first left out) are within 2^-16 of the largest
+// logit: those are summed again with a compensated sum, which orders them as a
+// 64-bit sum would.
+#include "internal.cuh"
+#include "w4.cuh"
+
+namespace fp8bs {
+namespace {
+
+using namespace w4;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTok = 32;  // tokens of one pass: 4 MMA column tiles
+constexpr size_t kHeader = 256;  // workspace: the arrival counter, then the partial logits
+constexpr int kTargetBlocks = 152;
+constexpr int kMaxCand = 64;
+
+struct RouteParams {
+    const uint16_t* x;
+    int64_t ldx;
+    const uint16_t* w;  // [rows, H]
+    int32_t* ids;
+    float* weights;
+    uint32_t* counter;
+    float* part;  // [KS][M][rows16]
+    int M, H, E, k, S;
+    int rows, rows16, KS;
+    int renorm, shared;
+};
+
+// K slices over blocks: enough blocks for the machine, at least one chunk per warp.
+__host__ int k_splits(int64_t rows, int64_t H) {
+    const int64_t tiles = (rows + kTileRows - 1) / kTileRows, chunks = H / kChunk;
+    const int64_t want = (kTargetBlocks + tiles - 1) / tiles, most = (chunks + kWarps - 1) / kWarps;
+    return static_cast<int>(want < most ? want : most);
+}
+
+__device__ __forceinline__ void mma16816_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Order-preserving key of a logit; NaN ranks below everything, 0 is "taken".
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __float_as_uint(v);
+    if (v != v) return 1u;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// x[m] . w[e] with a compensated fp32 sum (products of two bf16 are exact in
+// fp32; each addition's rounding error is kept: D. E. Knuth's two-sum), the
+// lanes' sums joined in 64 bits.  Every lane returns it.
+__device__ double exact_logit(const RouteParams& p, int m, int e, int lane) {
+    float s = 0.0f, c = 0.0f;
+    for (int k = 8 * lane; k < p.H; k += 256) {
+        float a[8], b[8];
+        unpack8(*reinterpret_cast<const uint4*>(p.x + m * p.ldx + k), a);
+        unpack8(*reinterpret_cast<const uint4*>(p.w + static_cast<int64_t>(e) * p.H + k), b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float v = __fmul_rn(a[i], b[i]), t = __fadd_rn(s, v), z = __fsub_rn(t, s);
+            c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(v, z)));
+            s = t;
+        }
+    }
+    double d = static_cast<double>(s) + static_cast<double>(c);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, off);
+    return d;
+}
+
+struct Select {
+    float value[kWarps][FP8BS_ROUTE_MAX_K + 1];
+    int16_t expert[kWarps][FP8BS_ROUTE_MAX_K + 1];
+    double cand_value[kWarps][kMaxCand];
+    int16_t cand[kWarps][kMaxCand];
+};
+
+// The k + 1 largest of a token's logits in order, by one warp.  v[j]: expert
+// lane + 32 j.
+template <int PER>
+__device__ void select_token(const RouteParams& p, Select& sel, int m, int warp, int lane) {
+    float v[PER];
+    uint32_t key[PER];
+    uint32_t top_abs = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int e = lane + 32 * j;
+        v[j] = 0.0f;
+        key[j] = 0;
+        if (e < p.E) {
+            for (int ks = 0; ks < p.KS; ++ks) v[j] += __ldcg(p.part + (static_cast<int64_t>(ks) * p.M + m) * p.rows16 + e);
+            key[j] = order_key(v[j]);
+            top_abs = max(top_abs, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        }
+    }
+    top_abs = __reduce_max_sync(0xFFFFFFFFu, top_abs);
+    uint32_t best = 0;
+    int best_e = 0;
+    auto rescan = [&]() {
+        best = 0;
+        best_e = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (key[j] > best) best = key[j], best_e = lane + 32 * j;
+    };
+    rescan();
+    const int kk = min(p.k + 1, p.E);
+    for (int r = 0; r < kk; ++r) {
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
+        const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, best == top ? static_cast<uint32_t>(best_e) : 0xFFFFFFFFu);
+        if (best == top && static_cast<uint32_t>(best_e) == e) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (lane + 32 * j == best_e) {
+                    sel.value[warp][r] = v[j];
+                    sel.expert[warp][r] = static_cast<int16_t>(best_e);
+                    key[j] = 0;
+                }
+            rescan();
+        }
+    }
+    __syncwarp();
+    const float largest = sel.value[warp][0];
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+        if (lane + 32 * j < p.E) sum += expf(v[j] - largest);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+
+    // near ties: order them by their exact values
+    const float tol = top_abs < 0x7F800000u ? __uint_as_float(top_abs) * 0x1p-16f : 0.0f;
+    bool close = false;
+    for (int r = lane; r + 1 < kk; r += 32) close |= sel.value[warp][r] - sel.value[warp][r + 1] < tol;
+    if (__any_sync(0xFFFFFFFFu, close)) {
+        const float floor_v = sel.value[warp][p.k - 1] - tol;
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const bool in = lane + 32 * j < p.E && v[j] >= floor_v;
+            const uint32_t bal = __ballot_sync(0xFFFFFFFFu, in);
+            const int at = n + __popc(bal & ((1u << lane) - 1u));
+            if (in && at < kMaxCand) {
+                sel.cand[warp][at] = static_cast<int16_t>(lane + 32 * j);
+                sel.cand_value[warp][at] = v[j];
+            }
+            n += __popc(bal);
+        }
+        __syncwarp();
+        if (n <= kMaxCand) {
+            uint64_t unclear = 0;
+            for (int i = 0; i < n; ++i) {
+                bool near = false;
+                for (int o = lane; o < n; o += 32)
+                    near |= o != i && fabs(sel.cand_value[warp][i] - sel.cand_value[warp][o]) < tol;
+                if (__any_sync(0xFFFFFFFFu, near)) unclear |= uint64_t(1) << i;
+            }
+            __syncwarp();
+            for (int i = 0; i < n; ++i)
+                if (unclear >> i & 1) {
+                    const double d = exact_logit(p, m, sel.cand[warp][i], lane);
+                    if (lane == 0) sel.cand_value[warp][i] = d;
+                }
+            __syncwarp();
+            // the candidates are in ascending blocks of 32 experts, not sorted: rank each one
+            for (int i = lane; i < n; i += 32) {
+                const double a = sel.cand_value[warp][i];
+                const int e = sel.cand[warp][i];
+                int rank = 0;
+                for (int o = 0; o < n; ++o) {
+                    const double b = sel.cand_value[warp][o];
+                    rank += b > a || (b == a && sel.cand[warp][o] < e);
+                }
+                if (rank < p.k) {
+                    sel.expert[warp][rank] = static_cast<int16_t>(e);
+                    sel.value[warp][rank] = static_cast<float>(a);
+                }
+            }
+            __syncwarp();
+        }
+    }
+
+    float chosen = 0.0f;
+    for (int r = lane; r < p.k; r += 32) chosen += expf(sel.value[warp][r] - largest);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) chosen += __shfl_xor_sync(0xFFFFFFFFu, chosen, off);
+    const float denom = sum != sum ? sum : (p.renorm ? chosen : sum);
+    for (int r = lane; r < p.k; r += 32) {
+        p.ids[m * p.S + r] = sel.expert[warp][r];
+        p.weights[m * p.S + r] = expf(sel.value[warp][r] - largest) / denom;
+    }
+    if (p.shared && lane == 0) {
+        float g = 1.0f;
+        if (p.shared == FP8BS_ROUTE_SHARED_GATE) {
+            float l = 0.0f;
+            for (int ks = 0; ks < p.KS; ++ks) l += __ldcg(p.part + (static_cast<int64_t>(ks) * p.M + m) * p.rows16 + p.E);
+            g = 1.0f / (1.0f + expf(-l));
+        }
+        p.ids[m * p.S + p.k] = p.E;
+        p.weights[m * p.S + p.k] = g;
+    }
+    __syncwarp();
+}
+
+__global__ void __launch_bounds__(kThreads) moe_route_kernel(const __grid_constant__ RouteParams p) {
+    __shared__ float red[kWarps][kTileRows][kTok + 1];
+    __shared__ Select sel;
+    __shared__ int is_last;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int tile = blockIdx.x / p.KS, ks = blockIdx.x - tile * p.KS;
+    const int chunks = p.H / kChunk;
+    const int r0 = min(tile * kTileRows + g, p.rows - 1), r1 = min(tile * kTileRows + g + 8, p.rows - 1);
+    const uint16_t* w0 = p.w + static_cast<int64_t>(r0) * p.H + 8 * t;
+    const uint16_t* w1 = p.w + static_cast<int64_t>(r1) * p.H + 8 * t;
+    for (int m0 = 0; m0 < p.M; m0 += kTok) {
+        float acc[kTok / 8][4] = {};
+        for (int c = ks * kWarps + warp; c < chunks; c += p.KS * kWarps) {
+            uint4 a0[4], a1[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a0[i] = ptx::ld_global_v4(w0 + c * kChunk + 32 * i);
+                a1[i] = ptx::ld_global_v4(w1 + c * kChunk + 32 * i);
+            }
+#pragma unroll
+            for (int j = 0; j < kTok / 8; ++j) {
+                if (m0 + 8 * j >= p.M) break;
+                const int m = min(m0 + 8 * j + g, p.M - 1);
+                const uint16_t* x = p.x + m * p.ldx + c * kChunk + 8 * t;
+                float part[4] = {};
+                uint4 b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[i] = *reinterpret_cast<const uint4*>(x + 32 * i);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mma16816_bf16(part, a0[i].x, a1[i].x, a0[i].y, a1[i].y, b[i].x, b[i].y);
+                    mma16816_bf16(part, a0[i].z, a1[i].z, a0[i].w, a1[i].w, b[i].z, b[i].w);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j][i] += part[i];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kTok / 8; ++j) {
+            red[warp][g][8 * j + 2 * t] = acc[j][0];
+            red[warp][g][8 * j + 2 * t + 1] = acc[j][1];
+            red[warp][g + 8][8 * j + 2 * t] = acc[j][2];
+            red[warp][g + 8][8 * j + 2 * t + 1] = acc[j][3];
+        }
+        __syncthreads();
+        const int n = min(kTok, p.M - m0);
+        for (int o = threadIdx.x; o < n * kTileRows; o += kThreads) {
+            const int m = o / kTileRows, r = o % kTileRows;
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += red[w][r][m];
+            p.part[(static_cast<int64_t>(ks) * p.M + m0 + m) * p.rows16 + tile * kTileRows + r] = v;
+        }
+        __threadfence();
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) is_last = atomicAdd(p.counter, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!is_last) return;
+    __threadfence();
+    if (threadIdx.x == 0) *p.counter = 0;
+    for (int m = warp; m < p.M; m += kWarps) {
+        if (p.E <= 256)
+            select_token<8>(p, sel, m, warp, lane);
+        else if (p.E <= 512)
+            select_token<16>(p, sel, m, warp, lane);
+        else
+            select_token<FP8BS_ROUTE_MAX_E / 32>(p, sel, m, warp, lane);
+    }
+}
+
+}  // namespace
+
+size_t moe_route_workspace_bytes(int64_t M, int64_t E, int64_t H) {
+    const int64_t rows = E + 1, rows16 = (rows + kTileRows - 1) / kTileRows * kTileRows;
+    // with and without a gate row: the larger of the two
+    const int64_t ks = k_splits(E, H) > k_splits(rows, H) ? k_splits(E, H) : k_splits(rows, H);
+    return kHeader + static_cast<size_t>(ks) * M * rows16 * sizeof(float);
+}
+
+cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t stream) {
+    RouteParams p;
+    p.x = a.x;
+    p.ldx = a.ldx;
+    p.w = a.w;
+    p.ids = a.ids;
+    p.weights = a.weights;
+    p.counter = reinterpret_cast<uint32_t*>(a.workspace);
+    p.part = reinterpret_cast<float*>(a.workspace + kHeader);
+    p.M = a.M;
+    p.H = a.H;
+    p.E = a.E;
+    p.k = a.k;
+    p.S = a.k + (a.shared != FP8BS_ROUTE_SHARED_NONE ? 1 : 0);
+    p.rows = a.E + (a.shared == FP8BS_ROUTE_SHARED_GATE ? 1 : 0);
+    p.rows16 = (p.rows + kTileRows - 1) / kTileRows * kTileRows;
+    p.KS = k_splits(p.rows, a.H);
+    p.renorm = a.renorm;
+    p.shared = a.shared;
+    const unsigned grid = static_cast<unsigned>(p.rows16 / kTileRows * p.KS);
+    moe_route_kernel<<<grid, kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace fp8bs

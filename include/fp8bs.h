@@ -334,6 +334,139 @@ int fp8bs_moe_w8a16(const uint16_t* x, int64_t M, int64_t H, const int32_t* topk
                     const uint8_t* w2, const float* s2, int64_t E, int64_t I, uint16_t* y,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* 4-bit weights at decode sizes: quantiser, GEMV, router, expert layer      */
+/* ------------------------------------------------------------------------ */
+
+/* Weight formats.  Both keep codes row-major, two a byte (the even k in the
+ * low nibble), and one scale per 1xG group along K, row-major [N, K/G].
+ *   MXFP4: e2m1 codes (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives), e8m0
+ *          scale bytes b for 2^(b - 127) (255 is not a scale: such a group
+ *          gives infinities or NaN), G = 32.
+ *   INT4 : codes q = 0..15 for the value q - 8, bf16 scales, G = 32, 64 or 128.
+ * A weight is its code's value times its group's scale, exactly. */
+typedef enum {
+    FP8BS_W4_MXFP4 = 0,
+    FP8BS_W4_INT4 = 1,
+} fp8bs_w4_format;
+
+/* Quantise an fp32 weight [N, K] to a 4-bit format.
+ *   w      : fp32 [N, K], row stride ldw elements; w and ldw*4 16-byte aligned.
+ *   N, K   : N >= 1, K a multiple of 128, both at most 2^24.
+ *   codes  : [N, K/2] bytes, 4-byte aligned.
+ *   scales : [N, K/group] e8m0 bytes, or bf16 (2-byte aligned).
+ * MXFP4: s = the smallest power of two >= RN32(amax / 6) (2^-127 for a zero
+ * group), code = the e2m1 value nearest to w / s, ties to even.  INT4: s =
+ * bf16(RN32(amax / 7)), q = clamp(rint(RN32(w / s)), -8, 7) + 8, q = 8 where s
+ * is 0.
+ * Errors: FP8BS_ERR_ARG (format, group, null pointer, ldw < K),
+ * FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN, FP8BS_ERR_CUDA. */
+int fp8bs_quant_weight_w4(const float* w, int64_t N, int64_t K, int64_t ldw, int format, int group,
+                          uint8_t* codes, void* scales, void* stream);
+
+/* Largest token count of fp8bs_gemv_w4a16. */
+#define FP8BS_W4_MAX_M 16
+
+/* Y = bf16(x W^T) for a few bf16 tokens and a 4-bit weight, in one launch.
+ *   x      : bf16 [M, K], row stride ldx elements; x and ldx*2 16-byte aligned.
+ *   M      : 0 .. FP8BS_W4_MAX_M (0 enqueues nothing and returns FP8BS_OK).
+ *   codes  : [N, K/2] bytes, row stride ldc bytes; codes and ldc 16-byte
+ *            aligned.
+ *   scales : [N, K/group], row stride lds elements; the scales of a row's 128 k
+ *            (MXFP4 4 bytes; INT4 256/group bytes) aligned to their size.
+ *   N, K   : N >= 1 (any), K a multiple of 128, both at most 2^24.
+ *   y      : bf16 [M, N], row stride ldy >= N elements, 2-byte aligned.
+ *   flags  : 0 or FP8BS_FLAG_PDL (codes and scales may then be read while the
+ *            kernel before is still running; x and y not).
+ * Products of codes and activations are exact, sums fp32 in a fixed order: the
+ * same inputs give the same bits.  Activations are carried in fp16 after an
+ * exact power-of-two scaling per token and K slice: elements below 2^-32 of
+ * their slice's largest magnitude are rounded at 2^-40 of it.  Infinities and
+ * NaN in a token reach that token's outputs only.
+ * No workspace, no device-side errors.
+ * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN, FP8BS_ERR_CUDA. */
+int fp8bs_gemv_w4a16(const uint16_t* x, int64_t M, int64_t ldx, const uint8_t* codes, int64_t ldc,
+                     const void* scales, int64_t lds, int64_t N, int64_t K, int format, int group,
+                     uint16_t* y, int64_t ldy, unsigned flags, void* stream);
+
+#define FP8BS_ROUTE_MAX_E 1024 /* experts                  */
+#define FP8BS_ROUTE_MAX_K 32   /* chosen experts per token */
+#define FP8BS_ROUTE_MAX_M 1024 /* tokens                   */
+
+/* What fp8bs_moe_route appends to each token's chosen experts. */
+typedef enum {
+    FP8BS_ROUTE_SHARED_NONE = 0, /* nothing: S = k                                     */
+    FP8BS_ROUTE_SHARED_ONE = 1,  /* expert E with weight 1: S = k + 1                  */
+    FP8BS_ROUTE_SHARED_GATE = 2, /* expert E with weight sigmoid(x . w[E]): S = k + 1  */
+} fp8bs_route_shared;
+
+/* Workspace bytes of fp8bs_moe_route (0 for an unsupported shape). */
+size_t fp8bs_moe_route_workspace_bytes(int64_t M, int64_t E, int64_t H);
+
+/* Router of a mixture-of-experts layer: per token the logits l[e] = x . w[e],
+ * p = softmax(l), the k experts with the largest logits in descending order
+ * (ties to the lowest index), and their weights.
+ *   x         : bf16 [M, H], row stride ldx elements; x and ldx*2 16-byte aligned.
+ *   M         : 0 .. FP8BS_ROUTE_MAX_M (0 enqueues nothing).
+ *   H         : a multiple of 128, at most 2^24.
+ *   w         : bf16 [E, H], or [E + 1, H] with FP8BS_ROUTE_SHARED_GATE (the
+ *               last row the shared expert's gate), contiguous, 16-byte aligned.
+ *   E, k      : 1 <= k <= E <= FP8BS_ROUTE_MAX_E, k <= FP8BS_ROUTE_MAX_K.
+ *   renorm    : 0: weights p; otherwise p divided by the chosen experts' sum.
+ *   topk_ids  : int32 [M, S], topk_w: fp32 [M, S]: the routing that
+ *               fp8bs_moe_w4a16 and fp8bs_moe_w8a16 take.
+ *   workspace : fp8bs_moe_route_workspace_bytes bytes, 256-byte aligned; its
+ *               first word must be zero before the first call
+ *               (fp8bs_workspace_init) and is zero again after each.  Not to be
+ *               used by two calls that can run at the same time.
+ * Logits are summed in fp32 in a fixed order; experts whose logits are within
+ * 2^-16 of the largest magnitude of each other where their order matters are
+ * summed again with compensation, so the order is that of 64-bit sums (not
+ * where more than 64 candidates are that close: then the fp32 order stands).
+ * A NaN logit ranks below every other and makes the token's chosen weights NaN.
+ * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN,
+ * FP8BS_ERR_WORKSPACE, FP8BS_ERR_CUDA. */
+int fp8bs_moe_route(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const uint16_t* w, int64_t E,
+                    int64_t k, int renorm, int shared, int32_t* topk_ids, float* topk_w,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+#define FP8BS_MOE_W4_MAX_I 8192 /* intermediate size per expert */
+
+/* Workspace bytes of fp8bs_moe_w4a16: a 256-byte error word, then M*S x I fp32.
+ * Returns 0 for an unsupported shape. */
+size_t fp8bs_moe_w4a16_workspace_bytes(int64_t M, int64_t S, int64_t I);
+
+/* One MoE layer at decode sizes on 4-bit weights, in two launches.  Per token m
+ * and slot s, with e = topk_ids[m, s]:
+ *   h    = x[m] . w13[e]^T   (gate rows 0..I-1 over the up rows I..2I-1)
+ *   a    = silu(h_gate) * h_up (fp32; carried in fp16 after an exact
+ *                            power-of-two scaling per pair and 512 k)
+ *   y[m] = bf16(sum over s, in slot order, of topk_w[m, s] * (a . w2[e]^T))
+ *   x        : bf16 [M, H], row stride ldx elements; x and ldx*2 16-byte aligned.
+ *   M, S     : M >= 0 (0 is a no-op), S >= 1, M * S <= FP8BS_MOE_MAX_PAIRS.
+ *   H, I     : multiples of 128, I <= FP8BS_MOE_W4_MAX_I, H at most 2^24.
+ *   topk_ids : int32 [M, S]; an id outside [0, E) makes that slot contribute
+ *              nothing and records FP8BS_ERR_DEVICE in the workspace error word.
+ *   topk_w   : fp32 [M, S].
+ *   w13, s13 : 4-bit codes [E, 2I, H/2] and scales [E, 2I, H/group].
+ *   w2, s2   : 4-bit codes [E, H, I/2] and scales [E, H, I/group].
+ *              Contiguous; codes 16-byte, scales 8-byte aligned; one format and
+ *              group size for both.
+ *   E        : experts (1 .. FP8BS_MOE_MAX_EXPERTS).
+ *   y        : bf16 [M, H], contiguous, 2-byte aligned.
+ *   workspace: fp8bs_moe_w4a16_workspace_bytes(M, S, I) bytes, 256-byte aligned;
+ *              its first word must be zero before the first call;
+ *              fp8bs_check_error reads it.  Not to be used by two calls that
+ *              can run at the same time.
+ * The second launch uses programmatic dependent launch; no cross-block waits;
+ * every sum in a fixed order, so results are deterministic.
+ * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN,
+ * FP8BS_ERR_WORKSPACE, FP8BS_ERR_CUDA. */
+int fp8bs_moe_w4a16(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const int32_t* topk_ids,
+                    const float* topk_w, int64_t S, const uint8_t* w13, const void* s13,
+                    const uint8_t* w2, const void* s2, int64_t E, int64_t I, int format, int group,
+                    uint16_t* y, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Limits of fp8bs_gemm_fused_static's fixed scratch. */
 #define FP8BS_STATIC_MAX_K 16384  /* largest K it accepts                   */
 #define FP8BS_STATIC_MAX_SMS 160  /* CTAs it uses at most (grid cap)        */
