@@ -159,6 +159,14 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
+def _raw_stream(stream, device_index: int) -> int:
+    """The cudaStream_t as an integer: the given stream, else the device's
+    current one (looked up without building a torch.cuda.Stream)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device_index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
 def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -314,21 +322,25 @@ def fp8bs_gemv_w4a16(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     [N, K/2], scales [N, K/group] (rows may be strided).  pdl=True launches with
     programmatic dependent launch; use it only when the work just before this
     call on the stream does not write the weight."""
-    _require_cuda(x, codes, scales, y)
+    if not (x.is_cuda and codes.is_cuda and scales.is_cuda):
+        raise ValueError("fp8bs tensors must live on a CUDA device")
     scale_dtype = _w4_scale_dtype(fmt, group, "fp8bs_gemv_w4a16")
     M, K = x.shape
-    N = codes.shape[0]
-    assert x.dtype == torch.bfloat16 and x.stride(1) == 1
-    assert codes.dtype == torch.uint8 and codes.shape[1] * 2 == K and codes.stride(1) == 1
-    assert scales.dtype == scale_dtype and scales.shape == (N, K // group) and scales.stride(1) == 1
+    N, half = codes.shape
+    ldx, x1 = x.stride()
+    ldc, c1 = codes.stride()
+    lds, s1 = scales.stride()
+    assert x.dtype is torch.bfloat16 and codes.dtype is torch.uint8 and scales.dtype is scale_dtype
+    assert x1 == c1 == s1 == 1 and 2 * half == K and scales.shape == (N, K // group)
     if y is None:
         y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    else:
-        assert y.dtype == torch.bfloat16 and y.shape == (M, N) and y.stride(1) == 1
-    rc = lib().fp8bs_gemv_w4a16(x.data_ptr(), M, x.stride(0), codes.data_ptr(), codes.stride(0), scales.data_ptr(),
-                                scales.stride(0), N, K, fmt, group, y.data_ptr(), y.stride(0),
-                                FP8BS_FLAG_PDL if pdl else 0, _stream(stream))
-    _check(rc, "fp8bs_gemv_w4a16")
+    ldy, y1 = y.stride()
+    assert y.is_cuda and y.dtype is torch.bfloat16 and y1 == 1 and y.shape == (M, N)
+    rc = (_lib or lib()).fp8bs_gemv_w4a16(x.data_ptr(), M, ldx, codes.data_ptr(), ldc, scales.data_ptr(), lds, N, K,
+                                          fmt, group, y.data_ptr(), ldy, FP8BS_FLAG_PDL if pdl else 0,
+                                          _raw_stream(stream, x.get_device()))
+    if rc:
+        raise Fp8bsError(rc, "fp8bs_gemv_w4a16")
     return y
 
 
@@ -356,25 +368,30 @@ def fp8bs_moe_route(x: torch.Tensor, w: torch.Tensor, k: int, renorm: bool = Tru
     (renormalised over them or not).  shared="one" appends expert E with
     weight 1, shared="gate" with weight sigmoid(x . w[E]) (w then has E + 1
     rows)."""
-    _require_cuda(x, w, ids, weights, workspace)
+    if not (x.is_cuda and w.is_cuda):
+        raise ValueError("fp8bs tensors must live on a CUDA device")
     M, H = x.shape
+    rows, Hw = w.shape
+    ldx, x1 = x.stride()
     code = _ROUTE_SHARED[shared]
-    E = w.shape[0] - (1 if code == 2 else 0)
-    S = k + (1 if code else 0)
-    assert x.dtype == torch.bfloat16 and x.stride(1) == 1
-    assert w.dtype == torch.bfloat16 and w.is_contiguous() and w.shape[1] == H
+    E = rows - 1 if code == 2 else rows
+    S = k + 1 if code else k
+    assert x.dtype is torch.bfloat16 and x1 == 1
+    assert w.dtype is torch.bfloat16 and Hw == H and w.is_contiguous()
     if ids is None:
         ids = torch.empty((M, S), dtype=torch.int32, device=x.device)
     if weights is None:
         weights = torch.empty((M, S), dtype=torch.float32, device=x.device)
-    assert ids.dtype == torch.int32 and ids.is_contiguous() and ids.shape == (M, S)
-    assert weights.dtype == torch.float32 and weights.is_contiguous() and weights.shape == (M, S)
+    assert ids.is_cuda and ids.dtype is torch.int32 and ids.is_contiguous() and ids.shape == (M, S)
+    assert weights.is_cuda and weights.dtype is torch.float32 and weights.is_contiguous() and weights.shape == (M, S)
     if workspace is None:
         workspace = new_moe_route_workspace(M, E, H, x.device)
-    rc = lib().fp8bs_moe_route(x.data_ptr(), M, H, x.stride(0), w.data_ptr(), E, k, 1 if renorm else 0, code,
-                               ids.data_ptr(), weights.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                               _stream(stream))
-    _check(rc, "fp8bs_moe_route")
+    assert workspace.is_cuda and workspace.dtype is torch.uint8
+    rc = (_lib or lib()).fp8bs_moe_route(x.data_ptr(), M, H, ldx, w.data_ptr(), E, k, 1 if renorm else 0, code,
+                                         ids.data_ptr(), weights.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                         _raw_stream(stream, x.get_device()))
+    if rc:
+        raise Fp8bsError(rc, "fp8bs_moe_route")
     return ids, weights
 
 
@@ -398,29 +415,35 @@ def fp8bs_moe_w4a16(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tenso
     """One small-batch MoE layer on 4-bit weights: bf16 x [M, H]; int32 topk_ids
     and fp32 topk_w [M, S]; codes w13 [E, 2I, H/2], w2 [E, H, I/2] (uint8) with
     scales s13 [E, 2I, H/group], s2 [E, H, I/group].  Returns bf16 y [M, H]."""
-    _require_cuda(x, topk_ids, topk_w, w13, s13, w2, s2, y, workspace)
+    if not (x.is_cuda and topk_ids.is_cuda and topk_w.is_cuda and w13.is_cuda and s13.is_cuda and w2.is_cuda and
+            s2.is_cuda):
+        raise ValueError("fp8bs tensors must live on a CUDA device")
     scale_dtype = _w4_scale_dtype(fmt, group, "fp8bs_moe_w4a16")
     M, H = x.shape
-    S = topk_ids.shape[1]
-    E, H2, I2 = w2.shape
-    I = 2 * I2
-    assert x.dtype == torch.bfloat16 and x.stride(1) == 1
-    assert topk_ids.dtype == torch.int32 and topk_ids.is_contiguous() and topk_ids.shape == (M, S)
-    assert topk_w.dtype == torch.float32 and topk_w.is_contiguous() and topk_w.shape == (M, S)
-    assert w13.dtype == torch.uint8 and w13.is_contiguous() and w13.shape == (E, 2 * I, H // 2)
-    assert w2.dtype == torch.uint8 and w2.is_contiguous() and H2 == H
-    assert s13.dtype == s2.dtype == scale_dtype and s13.is_contiguous() and s2.is_contiguous()
-    assert s13.shape == (E, 2 * I, H // group) and s2.shape == (E, H, I // group)
+    ldx, x1 = x.stride()
+    routing = topk_ids.shape
+    S = routing[1]
+    E, H2, half = w2.shape
+    I = 2 * half
+    assert x.dtype is torch.bfloat16 and x1 == 1
+    assert topk_ids.dtype is torch.int32 and topk_ids.is_contiguous() and routing[0] == M
+    assert topk_w.dtype is torch.float32 and topk_w.is_contiguous() and topk_w.shape == routing
+    assert w13.dtype is torch.uint8 and w13.is_contiguous() and w13.shape == (E, 2 * I, H // 2)
+    assert w2.dtype is torch.uint8 and w2.is_contiguous() and H2 == H
+    assert s13.dtype is scale_dtype and s13.is_contiguous() and s13.shape == (E, 2 * I, H // group)
+    assert s2.dtype is scale_dtype and s2.is_contiguous() and s2.shape == (E, H, I // group)
     if y is None:
         y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
-    else:
-        assert y.dtype == torch.bfloat16 and y.is_contiguous() and y.shape == (M, H)
+    assert y.is_cuda and y.dtype is torch.bfloat16 and y.is_contiguous() and y.shape == (M, H)
     if workspace is None:
         workspace = new_moe_w4_workspace(M, S, I, x.device)
-    rc = lib().fp8bs_moe_w4a16(x.data_ptr(), M, H, x.stride(0), topk_ids.data_ptr(), topk_w.data_ptr(), S,
-                               w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), E, I, fmt, group,
-                               y.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream))
-    _check(rc, "fp8bs_moe_w4a16")
+    assert workspace.is_cuda and workspace.dtype is torch.uint8
+    rc = (_lib or lib()).fp8bs_moe_w4a16(x.data_ptr(), M, H, ldx, topk_ids.data_ptr(), topk_w.data_ptr(), S,
+                                         w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), E, I, fmt,
+                                         group, y.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                         _raw_stream(stream, x.get_device()))
+    if rc:
+        raise Fp8bsError(rc, "fp8bs_moe_w4a16")
     return y
 
 

@@ -18,9 +18,18 @@
 // holds rows g and g + 8 of the weight and token column g.  The k order
 // within an MMA is free as long as both operands agree, so a lane takes one
 // 32-bit word (8 codes) per 32-wide group: word t of the group is k = 8t ..
-// 8t+7, two MMAs a group.  Codes reach shared memory in row-major order with
-// a row pitch of 16 bytes more than the slice, which makes these word reads
-// conflict-free; activations sit at [token][k] fp16, read as 16-byte words.
+// 8t+7, two MMAs a group.  A row's 16 bytes of a group are a row of an 8x8
+// matrix of 16-bit values to ldmatrix, which hands lane (g, t) word t of row
+// g: one ldmatrix.x4 fetches two groups of 16 rows.  Codes reach shared memory
+// in row-major order with a row pitch of 144 bytes (the 128 of a stage and 16
+// more), conflict-free for that; activations sit at [token][k] fp16, the
+// 64-byte halves of each 128 swapped for odd tokens, read as 16-byte words.
+//
+// Rates measured on GB300, per multiprocessor quarter: this MMA 8 cycles, the
+// e2m1 conversion of a pair 2, integer and fp16 pair operations 2, fp32 FMA 1.
+// Codes at the measured copy bandwidth arrive as 1088 bytes (16 rows x 128 k,
+// e8m0 scales included) per 186 cycles; one tile of token columns takes 64
+// cycles of MMA and 64 of conversion for them, two tiles 128 and 64.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -38,7 +47,7 @@ namespace w4 {
 
 constexpr int kChunk = 128;    // k per chunk: the unit of slices
 constexpr int kTileRows = 16;  // weight rows of a warp tile
-constexpr int kMaxBlockShared = 227 * 1024;  // dynamic shared memory a block may have
+constexpr int kMaxBlockShared = 226 * 1024;  // dynamic shared memory of a block (1 KB of the 227 for static)
 constexpr int kMaxSmShared = 228 * 1024;     // shared memory of a multiprocessor (1 KB of it per block reserved)
 
 // Format constants.  GP: scale groups per chunk; SB: scale bytes per row and chunk.
@@ -47,70 +56,52 @@ struct Format {
     static constexpr int kScaleBytes = FMT == FP8BS_W4_MXFP4 ? GP : 2 * GP;
 };
 
-// Shared memory of one warp's stage: PC chunks of 16 rows.
-template <int GP, int PC>
-struct Stage {
-    static constexpr int kPitch = PC * 64 + 16;                // bytes of a code row
-    static constexpr int kCodeBytes = kTileRows * kPitch;
-    static constexpr int kScalePitch = PC * GP + 4;            // floats of a scale row
-    static constexpr int kScaleTableBytes = kTileRows * kScalePitch * 4;
-    static constexpr int kTokenPitch = PC * 256 + 64;          // bytes of a token's slice
-};
+// A stage: kPC chunks of 16 rows, copied and multiplied together by one warp.
+constexpr int kPC = 2;
+constexpr int kStageK = kPC * kChunk;
+constexpr int kCodePitch = kPC * 64 + 16;  // bytes of a code row
+constexpr int kCodeBytes = kTileRows * kCodePitch;
+constexpr int kTokenBytes = kStageK * 2;   // fp16 of a token
+template <int GP>
+constexpr int kScalePitch = kPC * GP + 4;  // floats of a scale row
+template <int GP>
+constexpr int kTableBytes = kTileRows * kScalePitch<GP> * 4;
 
-// Scale words of a stage as loaded: lane l holds row l / 2, PC / 2 chunks from
-// (l % 2) * PC / 2 on (PC = 1: row l % 16 by the first 16 lanes).
-template <int PC>
-struct RawScales {
-    uint2 w[PC > 1 ? PC / 2 : 1];
-};
-
-__device__ __forceinline__ void cp_async16_zfill(void* dst, const void* src, bool pred) {
-    const uint32_t n = pred ? 16u : 0u;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_addr(dst)), "l"(src), "r"(n) : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Start the copy of nch (1..PC) chunks of 16 code rows to dst.  codes points
-// at row 0's first byte of the slice; row r >= rows repeats the last row (its
+// Start the copy of nch (1..kPC) chunks of 16 code rows to dst.  codes points
+// at row 0's first byte of the stage; row r >= rows repeats the last row (its
 // outputs are dropped), so every access stays inside the weight.
-template <int GP, int PC>
 __device__ __forceinline__ void load_codes(uint8_t* dst, const uint8_t* codes, int64_t ldc, int rows, int nch, int lane) {
-    constexpr int kSegs = PC * 4;  // 16-byte pieces of a row
+    const int s = lane & 7;  // 16-byte piece of the row's 128
+    if (s >= nch * 4) return;
 #pragma unroll
-    for (int j = 0; j < kTileRows * kSegs / 32; ++j) {
-        const int idx = lane + 32 * j, r = idx / kSegs, s = idx % kSegs;
-        if (s < nch * 4)
-            ptx::cp_async16(dst + r * Stage<GP, PC>::kPitch + s * 16, codes + static_cast<int64_t>(r < rows ? r : rows - 1) * ldc + s * 16);
+    for (int j = 0; j < kTileRows / 4; ++j) {
+        const int r = (lane >> 3) + 4 * j;
+        ptx::cp_async16(dst + r * kCodePitch + s * 16, codes + static_cast<int64_t>(min(r, rows - 1)) * ldc + s * 16);
     }
 }
 
-// The stage's scale words into registers (row pitch lds bytes); zeros past nch.
-template <int FMT, int GP, int PC>
-__device__ __forceinline__ RawScales<PC> load_scales(const uint8_t* scales, int64_t lds, int rows, int nch, int lane) {
+// The stage's scale words as loaded: lane l holds row l / 2, chunk l % 2 (row
+// pitch lds bytes); zeros past nch.
+template <int FMT, int GP>
+__device__ __forceinline__ uint2 load_scales(const uint8_t* scales, int64_t lds, int rows, int nch, int lane) {
     constexpr int SB = Format<FMT, GP>::kScaleBytes;
-    constexpr int kPer = PC > 1 ? PC / 2 : 1;
-    RawScales<PC> raw;
-    const int r0 = PC > 1 ? lane >> 1 : lane & 15;
-    const int r = r0 < rows ? r0 : rows - 1;
-    const int c0 = PC > 1 ? (lane & 1) * kPer : 0;
-    const uint8_t* p = scales + static_cast<int64_t>(r) * lds + c0 * SB;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        raw.w[j] = make_uint2(0, 0);
-        if (c0 + j < nch) {
-            if constexpr (SB == 8)
-                raw.w[j] = __ldg(reinterpret_cast<const uint2*>(p + j * SB));
-            else if constexpr (SB == 4)
-                raw.w[j].x = __ldg(reinterpret_cast<const uint32_t*>(p + j * SB));
-            else
-                raw.w[j].x = __ldg(reinterpret_cast<const uint16_t*>(p + j * SB));
-        }
+    uint2 w = make_uint2(0, 0);
+    if ((lane & 1) < nch) {
+        const uint8_t* p = scales + static_cast<int64_t>(min(lane >> 1, rows - 1)) * lds + (lane & 1) * SB;
+        if constexpr (SB == 8)
+            w = __ldg(reinterpret_cast<const uint2*>(p));
+        else if constexpr (SB == 4)
+            w.x = __ldg(reinterpret_cast<const uint32_t*>(p));
+        else
+            w.x = __ldg(reinterpret_cast<const uint16_t*>(p));
     }
-    return raw;
+    return w;
 }
 
 // Their fp32 values into the stage's table [row][chunk * GP + group].  An e8m0
@@ -119,46 +110,30 @@ __device__ __forceinline__ RawScales<PC> load_scales(const uint8_t* scales, int6
 // by 2^64 (kBigScale), so that a group's sum, up to 2^27 at the activations'
 // fixed scaling, times its scale stays finite; returns the factor to put back.
 constexpr float kBigScale = 0x1p64f;
-template <int FMT, int GP, int PC>
-__device__ __forceinline__ float store_scales(float* table, const RawScales<PC>& raw, int lane) {
-    constexpr int kPer = PC > 1 ? PC / 2 : 1;
-    uint32_t high = 0;  // the three top exponent bits of some scale all set
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) high |= (raw.w[j].x & raw.w[j].x << 1 & raw.w[j].x << 2) | (raw.w[j].y & raw.w[j].y << 1 & raw.w[j].y << 2);
+template <int FMT, int GP>
+__device__ __forceinline__ float store_scales(float* table, uint2 raw, int lane) {
+    // some scale's three top exponent bits all set
+    const uint32_t high = (raw.x & raw.x << 1 & raw.x << 2) | (raw.y & raw.y << 1 & raw.y << 2);
     const bool big = __any_sync(0xFFFFFFFFu, (high & (FMT == FP8BS_W4_MXFP4 ? 0x80808080u : 0x40004000u)) != 0);
     const float fit = big ? 1.0f / kBigScale : 1.0f, back = big ? kBigScale : 1.0f;
-    const int r = PC > 1 ? lane >> 1 : lane & 15;
-    const int c0 = PC > 1 ? (lane & 1) * kPer : 0;
-    float* dst = table + r * Stage<GP, PC>::kScalePitch + c0 * GP;
-    if (PC == 1 && lane >= 16) return back;
+    const uint32_t w[2] = {raw.x, raw.y};
+    float v[GP];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const uint32_t w[2] = {raw.w[j].x, raw.w[j].y};
-        float v[GP];
-#pragma unroll
-        for (int i = 0; i < GP; ++i) {
-            if constexpr (FMT == FP8BS_W4_MXFP4)
-                v[i] = __uint_as_float(max(((w[0] >> (8 * i)) & 0xFFu) << 23, 0x00400000u));
-            else
-                v[i] = __uint_as_float((w[i / 2] >> (16 * (i % 2))) << 16);
-            v[i] *= fit;
-        }
-        if constexpr (GP == 4)
-            *reinterpret_cast<float4*>(dst + j * GP) = make_float4(v[0], v[1], v[2], v[3]);
-        else if constexpr (GP == 2)
-            *reinterpret_cast<float2*>(dst + j * GP) = make_float2(v[0], v[1]);
+    for (int i = 0; i < GP; ++i) {
+        if constexpr (FMT == FP8BS_W4_MXFP4)
+            v[i] = __uint_as_float(max(((w[0] >> (8 * i)) & 0xFFu) << 23, 0x00400000u));
         else
-            dst[j] = v[0];
+            v[i] = __uint_as_float((w[i / 2] >> (16 * (i % 2))) << 16);
+        v[i] *= fit;
     }
+    float* dst = table + (lane >> 1) * kScalePitch<GP> + (lane & 1) * GP;
+    if constexpr (GP == 4)
+        *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+    else if constexpr (GP == 2)
+        *reinterpret_cast<float2*>(dst) = make_float2(v[0], v[1]);
+    else
+        dst[0] = v[0];
     return back;
-}
-
-// tot += a stage's sums, their token's and their scales' factors put back.
-__device__ __forceinline__ void add_stage(float (&tot)[4], const float (&acc)[4], float i0, float i1, float back) {
-    tot[0] += acc[0] * i0 * back;
-    tot[1] += acc[1] * i1 * back;
-    tot[2] += acc[2] * i0 * back;
-    tot[3] += acc[3] * i1 * back;
 }
 
 // 2^(14 - e) and its inverse for a slice whose largest magnitude has the
@@ -198,64 +173,79 @@ __device__ __forceinline__ void unpack8(const uint4& raw, float (&v)[8]) {
     }
 }
 
-// One token's slice of nch chunks, bf16 from global memory, into dst (fp16,
-// zeros past nch); returns the inverse scale.  The whole warp takes part.
-template <int FMT, int PC>
-__device__ __forceinline__ float stage_token_bf16(uint8_t* dst, const uint16_t* src, int nch, int lane) {
-    constexpr int kJ = (PC + 1) / 2;  // 256 k per warp-wide 16-byte load
-    uint4 raw[kJ];
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-        raw[j] = make_uint4(0, 0, 0, 0);
-        const int k = 8 * lane + 256 * j;
-        if (k < nch * kChunk) raw[j] = *reinterpret_cast<const uint4*>(src + k);
-        const uint32_t m = __vmaxu2(__vmaxu2(raw[j].x & 0x7FFF7FFFu, raw[j].y & 0x7FFF7FFFu),
-                                    __vmaxu2(raw[j].z & 0x7FFF7FFFu, raw[j].w & 0x7FFF7FFFu));
-        top = max(top, max(m & 0xFFFFu, m >> 16));
-    }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    float inverse;
-    const float s = slice_scale(top >> 7, inverse);
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-        const int k = 8 * lane + 256 * j;
-        float v[8];
-        unpack8(raw[j], v);
-        if (k < PC * kChunk) *reinterpret_cast<uint4*>(dst + 2 * k) = pack_slice8<FMT>(v, s);
-    }
-    return inverse;
-}
+// Where the 16-byte word w (8 k) of a token's stage sits.
+__device__ __forceinline__ int token_word(int token, int w) { return token * kTokenBytes + (w ^ (token & 1) << 2) * 16; }
 
-// The same from fp32 (rounded to fp16's 11 bits: 2^-12 of each value, 16 times
-// finer than the bf16 of the outputs).
-template <int FMT, int PC>
-__device__ __forceinline__ float stage_token_f32(uint8_t* dst, const float* src, int nch, int lane) {
-    constexpr int kJ = (PC + 1) / 2;
-    float v[kJ][8];
-    uint32_t top = 0;
+// A stage of up to four bf16 tokens, as loaded: lane l holds k = 8l .. 8l+7
+// (zeros past nch chunks).  src(i): token i's first element of the stage.
+struct RawBf16 {
+    static constexpr int kTokens = 4;
+    uint4 r[kTokens];
+    template <typename Src>
+    __device__ __forceinline__ void load(int n, int nch, int lane, Src src) {
+        const bool in = lane < nch * (kChunk / 8);
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-        const int k = 8 * lane + 256 * j;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        if (k < nch * kChunk) {
-            a = __ldcg(reinterpret_cast<const float4*>(src + k));
-            b = __ldcg(reinterpret_cast<const float4*>(src + k + 4));
+        for (int i = 0; i < kTokens; ++i) {
+            r[i] = make_uint4(0, 0, 0, 0);
+            if (in && i < n) r[i] = *reinterpret_cast<const uint4*>(src(i) + 8 * lane);
         }
-        v[j][0] = a.x, v[j][1] = a.y, v[j][2] = a.z, v[j][3] = a.w;
-        v[j][4] = b.x, v[j][5] = b.y, v[j][6] = b.z, v[j][7] = b.w;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
     }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    float inverse;
-    const float s = slice_scale(top >> 23, inverse);
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-        const int k = 8 * lane + 256 * j;
-        if (k < PC * kChunk) *reinterpret_cast<uint4*>(dst + 2 * k) = pack_slice8<FMT>(v[j], s);
+    __device__ __forceinline__ uint32_t exponent(int i) const {
+        const uint32_t m = __vmaxu2(__vmaxu2(r[i].x & 0x7FFF7FFFu, r[i].y & 0x7FFF7FFFu),
+                                    __vmaxu2(r[i].z & 0x7FFF7FFFu, r[i].w & 0x7FFF7FFFu));
+        return __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16)) >> 7;
     }
-    return inverse;
+    __device__ __forceinline__ void values(int i, float (&v)[8]) const { unpack8(r[i], v); }
+};
+
+// The same of up to two fp32 tokens (they are rounded to fp16's 11 bits: 2^-12
+// of each value, 16 times finer than the bf16 of the outputs).
+struct RawF32 {
+    static constexpr int kTokens = 2;
+    float4 a[kTokens], b[kTokens];
+    template <typename Src>
+    __device__ __forceinline__ void load(int n, int nch, int lane, Src src) {
+        const bool in = lane < nch * (kChunk / 8);
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) {
+            a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (in && i < n) {
+                a[i] = __ldcg(reinterpret_cast<const float4*>(src(i) + 8 * lane));
+                b[i] = __ldcg(reinterpret_cast<const float4*>(src(i) + 8 * lane + 4));
+            }
+        }
+    }
+    __device__ __forceinline__ void values(int i, float (&v)[8]) const {
+        v[0] = a[i].x, v[1] = a[i].y, v[2] = a[i].z, v[3] = a[i].w;
+        v[4] = b[i].x, v[5] = b[i].y, v[6] = b[i].z, v[7] = b[i].w;
+    }
+    __device__ __forceinline__ uint32_t exponent(int i) const {
+        float v[8];
+        values(i, v);
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        return __reduce_max_sync(0xFFFFFFFFu, top) >> 23;
+    }
+};
+
+// The stage of n tokens as fp16 at dst, with the inverse scales in inv.  raw
+// holds the first tokens, loaded beforehand; the others are loaded here.  The
+// whole warp takes part and must synchronise before it reads.
+template <int FMT, typename Raw, typename Src>
+__device__ __forceinline__ void stage_tokens(uint8_t* dst, float* inv, Raw& raw, int n, int nch, int lane, Src src) {
+    for (int i0 = 0; i0 < n; i0 += Raw::kTokens) {
+        if (i0 > 0) raw.load(n - i0, nch, lane, [&](int i) { return src(i0 + i); });
+#pragma unroll
+        for (int i = 0; i < Raw::kTokens; ++i) {
+            if (i0 + i >= n) break;
+            float inverse, v[8];
+            const float s = slice_scale(raw.exponent(i), inverse);
+            raw.values(i, v);
+            *reinterpret_cast<uint4*>(dst + token_word(i0 + i, lane)) = pack_slice8<FMT>(v, s);
+            if (lane == 0) inv[i0 + i] = inverse;
+        }
+    }
 }
 
 // One word (8 codes) -> four fp16 pairs, exact.  e2m1: the hardware conversion.
@@ -294,49 +284,86 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// acc[j] += the stage's product for token columns 8j .. 8j+7: D fragment
-// (rows g, g + 8; columns 2t, 2t + 1), still carrying the tokens' slice
-// scales.  xs: [token][kTokenPitch]; columns past n repeat token n - 1.
-template <int FMT, int GP, int PC, int NT>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// The stage's product for token columns 8j .. 8j+7, their scale factors put
+// back: D fragment (rows g, g + 8; columns 2t, 2t + 1).  Columns past n repeat
+// token n - 1.
+template <int FMT, int GP, int NT>
 __device__ __forceinline__ void stage_mma(float (&acc)[NT][4], const uint8_t* codes, const float* table, const uint8_t* xs,
-                                          int n, int nch, int lane) {
-    using S = Stage<GP, PC>;
+                                          const float* inv, float back, int n, int nch, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const uint8_t* c0 = codes + g * S::kPitch + t * 4;
-    const float* s0 = table + g * S::kScalePitch;
-    const uint8_t* x[NT];
+    // ldmatrix: lanes 0-15 address rows 0-15 of an even group, 16-31 of the odd one
+    const uint32_t c0 = ptx::smem_addr(codes) + (lane & 15) * kCodePitch + (lane >> 4) * 16;
+    const float* s0 = table + g * kScalePitch<GP>;
+    const uint8_t* x[NT][2];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) x[j] = xs + min(8 * j + g, n - 1) * S::kTokenPitch + t * 16;
+    for (int j = 0; j < NT; ++j) {
+        const int tok = min(8 * j + g, n - 1), odd = tok & 1;
+        x[j][0] = xs + tok * kTokenBytes + t * 16 + odd * 64;  // even groups
+        x[j][1] = xs + tok * kTokenBytes + t * 16 - odd * 64;  // odd ones
+    }
 #pragma unroll
-    for (int c = 0; c < PC; ++c) {
+    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kPC; ++c) {
         if (c >= nch) break;
+        float sa[GP], sb[GP];
+        const float* p = s0 + c * GP;
+        if constexpr (GP == 4) {
+            const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 8 * kScalePitch<GP>);
+            sa[0] = u.x, sa[1] = u.y, sa[2] = u.z, sa[3] = u.w;
+            sb[0] = v.x, sb[1] = v.y, sb[2] = v.z, sb[3] = v.w;
+        } else {
+#pragma unroll
+            for (int q = 0; q < GP; ++q) sa[q] = p[q], sb[q] = p[8 * kScalePitch<GP> + q];
+        }
         constexpr int kPerScale = 4 / GP;  // 32-wide groups under one scale
+        float part[NT][4];
 #pragma unroll
-        for (int q = 0; q < GP; ++q) {
-            float part[NT][4];
+        for (int i2 = 0; i2 < 2; ++i2) {
+            uint32_t w[4];  // group 2 i2: rows g, g + 8; group 2 i2 + 1: the same
+            ldmatrix4(w, c0 + c * 64 + i2 * 32);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) part[j][0] = part[j][1] = part[j][2] = part[j][3] = 0.0f;
+            for (int h = 0; h < 2; ++h) {
+                const int i = 2 * i2 + h;
+                if (i % kPerScale == 0)
 #pragma unroll
-            for (int i = q * kPerScale; i < (q + 1) * kPerScale; ++i) {
+                    for (int j = 0; j < NT; ++j) part[j][0] = part[j][1] = part[j][2] = part[j][3] = 0.0f;
                 uint32_t lo[4], hi[4];
-                decode8<FMT>(*reinterpret_cast<const uint32_t*>(c0 + c * 64 + i * 16), lo);
-                decode8<FMT>(*reinterpret_cast<const uint32_t*>(c0 + 8 * S::kPitch + c * 64 + i * 16), hi);
+                decode8<FMT>(w[2 * h], lo);
+                decode8<FMT>(w[2 * h + 1], hi);
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const uint4 b = *reinterpret_cast<const uint4*>(x[j] + c * 256 + i * 64);
+                    const uint4 b = *reinterpret_cast<const uint4*>(x[j][h] + c * 256 + i * 64);
                     mma16816(part[j], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
                     mma16816(part[j], lo[2], hi[2], lo[3], hi[3], b.z, b.w);
                 }
-            }
-            const float sa = s0[c * GP + q], sb = s0[8 * S::kScalePitch + c * GP + q];
+                if (i % kPerScale == kPerScale - 1) {
+                    const int q = i / kPerScale;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                acc[j][0] = fmaf(part[j][0], sa, acc[j][0]);
-                acc[j][1] = fmaf(part[j][1], sa, acc[j][1]);
-                acc[j][2] = fmaf(part[j][2], sb, acc[j][2]);
-                acc[j][3] = fmaf(part[j][3], sb, acc[j][3]);
+                    for (int j = 0; j < NT; ++j) {
+                        acc[j][0] = fmaf(part[j][0], sa[q], acc[j][0]);
+                        acc[j][1] = fmaf(part[j][1], sa[q], acc[j][1]);
+                        acc[j][2] = fmaf(part[j][2], sb[q], acc[j][2]);
+                        acc[j][3] = fmaf(part[j][3], sb[q], acc[j][3]);
+                    }
+                }
             }
         }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const float i0 = inv[min(8 * j + 2 * t, n - 1)], i1 = inv[min(8 * j + 2 * t + 1, n - 1)];
+        acc[j][0] = acc[j][0] * i0 * back;
+        acc[j][1] = acc[j][1] * i1 * back;
+        acc[j][2] = acc[j][2] * i0 * back;
+        acc[j][3] = acc[j][3] * i1 * back;
     }
 }
 

@@ -1,11 +1,12 @@
 // y[M, N] = bf16(x . W^T) for up to 16 bf16 tokens and a 4-bit weight.
 //
-// One warp works on 16 weight rows and a slice of K (w4.cuh).  The warps of a
-// block are WK slices of K times WR row tiles; each warp keeps its slice of x
-// (fp16, staged once where it fits) and streams codes through a two-stage ring
-// of its own, so the only block-wide steps are the sums over the slices, in
-// slice order: repeated calls give the same bits.  A persistent grid deals out
-// the row tiles.
+// A block owns a contiguous range of 16-row tiles; its warps split K (WK
+// slices), or K and the tiles where K has fewer than 16 chunks.  A warp keeps
+// its slice of x as fp16 (all of it where it fits, else one stage at a time,
+// staged again for every kGroup tiles) and streams its part of the codes
+// through a ring of kDepth stages of its own, so no step but the sums over the
+// slices is block-wide.  Those go in slice order: repeated calls give the same
+// bits.
 #include "internal.cuh"
 #include "w4.cuh"
 
@@ -14,8 +15,9 @@ namespace {
 
 using namespace w4;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
+constexpr int kGroup = 4;  // tiles summed in registers before the slices meet
 
 struct GemvParams {
     const uint16_t* x;
@@ -26,66 +28,88 @@ struct GemvParams {
     int64_t lds;
     uint16_t* y;
     int64_t ldy;
-    int M, N, chunks;  // chunks of 128 k
-    int WK;            // K slices (a power of two, at most kWarps)
-    int slice;         // chunks of a slice
-    int pieces;        // stages of a slice
-    int resident;      // whether the whole slice of x stays staged
+    int M, N, tiles;
+    int chunks;    // chunks of 128 k
+    int WK, WR;    // K slices, row tiles at a time: WK * WR <= kWarps
+    int pieces;    // stages of the longest slice
+    int resident;  // whether all pieces of x stay staged
     int pdl;
 };
 
-template <int GP, int PC>
-__host__ __device__ constexpr int warp_bytes(int M, int staged_pieces) {
-    using S = Stage<GP, PC>;
-    return 2 * S::kCodeBytes + S::kScaleTableBytes + staged_pieces * M * (S::kTokenPitch + 16);
-}
 template <int NT>
-constexpr int reduce_bytes() {
-    return kWarps * kTileRows * 8 * NT * 4;
+constexpr int kRedBytes = kGroup * kTileRows * 8 * NT * 4;  // of a warp
+
+// Bytes of a warp: the ring, the scale table, staged x and its inverse scales,
+// and the partial sums, which take the place of x where that is staged anew.
+template <int GP, int NT, int D>
+__host__ __device__ constexpr int warp_bytes(int M, int pieces, bool resident) {
+    const int x = (resident ? pieces : 1) * M * kTokenBytes, inv = ((resident ? pieces : 1) * M * 4 + 15) / 16 * 16;
+    return D * kCodeBytes + kTableBytes<GP> + inv + (resident ? x + kRedBytes<NT> : (x > kRedBytes<NT> ? x : kRedBytes<NT>));
 }
 
-// PC chunks a stage, NT tiles of 8 token columns.
-template <int FMT, int GP, int PC, int NT>
-__global__ void __launch_bounds__(kThreads, 2) gemv_w4_kernel(const __grid_constant__ GemvParams p) {
-    using S = Stage<GP, PC>;
+// NT: tiles of 8 token columns; D: ring depth.
+template <int FMT, int GP, int NT, int D>
+__global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_constant__ GemvParams p) {
     constexpr int SB = Format<FMT, GP>::kScaleBytes;
     extern __shared__ __align__(16) uint8_t smem[];
-    float* red = reinterpret_cast<float*>(smem);  // [kWarps][16][8 NT]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int wk = warp & (p.WK - 1), wr = warp / p.WK, WR = kWarps / p.WK;
-    const int staged = p.resident ? p.pieces : 1;
-    uint8_t* mine = smem + reduce_bytes<NT>() + warp * warp_bytes<GP, PC>(p.M, staged);
-    uint8_t* codes = mine;                                                  // [2][kCodeBytes]
-    float* table = reinterpret_cast<float*>(mine + 2 * S::kCodeBytes);      // scales
-    uint8_t* xs = mine + 2 * S::kCodeBytes + S::kScaleTableBytes;           // [staged][M][kTokenPitch]
-    float* xinv = reinterpret_cast<float*>(xs + staged * p.M * S::kTokenPitch);  // [staged][M] (16-byte slots)
+    const int wr = warp / p.WK, wk = warp - wr * p.WK;
+    const int kept = p.resident ? p.pieces : 1;
+    const int mine_bytes = warp_bytes<GP, NT, D>(p.M, p.pieces, p.resident);
+    uint8_t* codes = smem + warp * mine_bytes;                          // [D][kCodeBytes]
+    float* table = reinterpret_cast<float*>(codes + D * kCodeBytes);    // scales
+    float* inv = reinterpret_cast<float*>(codes + D * kCodeBytes + kTableBytes<GP>);  // [kept][M]
+    const int x_at = D * kCodeBytes + kTableBytes<GP> + (kept * p.M * 4 + 15) / 16 * 16;
+    uint8_t* xs = codes + x_at;                                         // [kept][M][kTokenBytes]
+    const int red_at = x_at + (p.resident ? kept * p.M * kTokenBytes : 0);
 
-    const int first = wk * p.slice, last = min(first + p.slice, p.chunks);
-    const int tiles = (p.N + kTileRows - 1) / kTileRows;
-    const int rounds = (tiles + WR - 1) / WR;
+    // a warp past WK * WR has no slice; it only takes part in the sums
+    const bool works = wr < p.WR;
+    const int first = works ? wk * p.chunks / p.WK : 0, last = works ? (wk + 1) * p.chunks / p.WK : 0;
+    const int t0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * p.tiles / gridDim.x);
+    const int t1 = static_cast<int>((static_cast<int64_t>(blockIdx.x) + 1) * p.tiles / gridDim.x);
+    const int steps = (t1 - t0 + p.WR - 1) / p.WR;  // tiles of a warp
 
-    RawScales<PC> raw = {};
-    // start stage (round, piece) into ring slot b
-    auto issue = [&](int round, int piece, int b) {
-        const int tile = round * WR + wr, c = first + piece * PC, nch = min(last - c, PC);
-        if (round < rounds && tile < tiles && nch > 0) {
+    // the order of a warp's stages: groups of kGroup tiles, in a group the
+    // pieces of the slice, in a piece the tiles
+    struct Cursor {
+        int group, piece, t;
+    };
+    auto advance = [&](Cursor& c) {
+        if (++c.t == min(kGroup, steps - c.group)) {
+            c.t = 0;
+            if (++c.piece == p.pieces) c.piece = 0, c.group += kGroup;
+        }
+    };
+    auto issue = [&](const Cursor& c, int slot) {
+        uint2 raw = make_uint2(0, 0);
+        const int tile = t0 + (c.group + c.t) * p.WR + wr, at = first + c.piece * kPC, nch = min(last - at, kPC);
+        if (c.group < steps && tile < t1 && nch > 0) {
             const int64_t row = static_cast<int64_t>(tile) * kTileRows;
             const int rows = min(p.N - tile * kTileRows, kTileRows);
-            load_codes<GP, PC>(codes + b * S::kCodeBytes, p.codes + row * p.ldc + c * 64, p.ldc, rows, nch, lane);
-            raw = load_scales<FMT, GP, PC>(p.scales + row * p.lds + c * SB, p.lds, rows, nch, lane);
+            load_codes(codes + slot * kCodeBytes, p.codes + row * p.ldc + at * 64, p.ldc, rows, nch, lane);
+            raw = load_scales<FMT, GP>(p.scales + row * p.lds + at * SB, p.lds, rows, nch, lane);
         }
         cp_async_commit();
+        return raw;
     };
     auto stage_x = [&](int piece, int slot) {
-        const int c = first + piece * PC, nch = min(last - c, PC);
-        if (nch <= 0) return;
-        for (int m = 0; m < p.M; ++m) {
-            const float inv = stage_token_bf16<FMT, PC>(xs + (slot * p.M + m) * S::kTokenPitch, p.x + m * p.ldx + c * kChunk, nch, lane);
-            if (lane == 0) xinv[slot * p.M + m] = inv;
+        const int at = first + piece * kPC, nch = min(last - at, kPC);
+        if (nch > 0) {
+            auto src = [&](int m) { return p.x + m * p.ldx + at * kChunk; };
+            RawBf16 first_tokens;
+            first_tokens.load(p.M, nch, lane, src);
+            stage_tokens<FMT>(xs + slot * p.M * kTokenBytes, inv + slot * p.M, first_tokens, p.M, nch, lane, src);
         }
     };
 
-    issue(blockIdx.x, 0, 0);
+    Cursor ahead = {0, 0, 0};
+    uint2 raw[D - 1];
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) {
+        raw[i] = issue(ahead, i);
+        advance(ahead);
+    }
     if (p.pdl) {
         ptx::griddep_launch_dependents();
         ptx::griddep_wait();
@@ -93,56 +117,95 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_w4_kernel(const __grid_const
     if (p.resident)
         for (int q = 0; q < p.pieces; ++q) stage_x(q, q);
 
-    int b = 0;
-    for (int round = blockIdx.x; round < rounds; round += gridDim.x) {
-        const int tile = round * WR + wr;
-        float tot[NT][4] = {};
-        for (int piece = 0; piece < p.pieces; ++piece, b ^= 1) {
-            const int nch = min(last - first - piece * PC, PC);
-            const RawScales<PC> cur = raw;
-            const bool more = piece + 1 < p.pieces;
-            issue(more ? round : round + static_cast<int>(gridDim.x), more ? piece + 1 : 0, b ^ 1);
-            if (tile < tiles && nch > 0) {
-                const float back = store_scales<FMT, GP, PC>(table, cur, lane);
-                if (!p.resident) stage_x(piece, 0);
-                cp_async_wait<1>();
-                __syncwarp();
-                const int slot = p.resident ? piece : 0;
-                float acc[NT][4] = {};
-                stage_mma<FMT, GP, PC, NT>(acc, codes + b * S::kCodeBytes, table, xs + slot * p.M * S::kTokenPitch, p.M, nch, lane);
+    int slot = 0;
+    for (int group = 0; group < steps; group += kGroup) {
+        const int count = min(kGroup, steps - group);
+        float tot[kGroup][NT][4] = {};
+        for (int piece = 0; piece < p.pieces; ++piece) {
+            if (!p.resident) stage_x(piece, 0);
+            const int nch = min(last - first - piece * kPC, kPC), kept_at = p.resident ? piece : 0;
+            for (int t = 0; t < count; ++t) {
+                const uint2 cur = raw[0];
+#pragma unroll
+                for (int i = 0; i + 2 < D; ++i) raw[i] = raw[i + 1];
+                raw[D - 2] = issue(ahead, slot == 0 ? D - 1 : slot - 1);
+                advance(ahead);
+                if (nch > 0) {
+                    const float back = store_scales<FMT, GP>(table, cur, lane);
+                    cp_async_wait<D - 1>();
+                    __syncwarp();
+                    float acc[NT][4];
+                    stage_mma<FMT, GP, NT>(acc, codes + slot * kCodeBytes, table, xs + kept_at * p.M * kTokenBytes,
+                                           inv + kept_at * p.M, back, p.M, nch, lane);
+#pragma unroll
+                    for (int u = 0; u < kGroup; ++u)
+                        if (u == t)
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) tot[u][j][i] += acc[j][i];
+                }
+                __syncwarp();  // the slot, the table and x are rewritten by later stages
+                slot = slot + 1 == D ? 0 : slot + 1;
+            }
+        }
+        // [warp][tile of the group][row][token]
+        float* r = reinterpret_cast<float*>(codes + red_at) + (lane >> 2) * 8 * NT + 2 * (lane & 3);
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u)
+            if (u < count)
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const int col = 8 * j + 2 * (lane & 3);
-                    const float i0 = xinv[slot * p.M + min(col, p.M - 1)], i1 = xinv[slot * p.M + min(col + 1, p.M - 1)];
-                    add_stage(tot[j], acc[j], i0, i1, back);
+                    *reinterpret_cast<float2*>(r + u * kTileRows * 8 * NT + 8 * j) = make_float2(tot[u][j][0], tot[u][j][1]);
+                    *reinterpret_cast<float2*>(r + (u * kTileRows + 8) * 8 * NT + 8 * j) = make_float2(tot[u][j][2], tot[u][j][3]);
                 }
-            }
-            __syncwarp();  // the slot and the tables are rewritten by the next stage
-        }
-        // [warp][row][token]
-        float* r = red + warp * kTileRows * 8 * NT + (lane >> 2) * 8 * NT + 2 * (lane & 3);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            *reinterpret_cast<float2*>(r + 8 * j) = make_float2(tot[j][0], tot[j][1]);
-            *reinterpret_cast<float2*>(r + 8 * 8 * NT + 8 * j) = make_float2(tot[j][2], tot[j][3]);
-        }
         __syncthreads();
-        for (int o = threadIdx.x; o < p.M * WR * kTileRows; o += kThreads) {
-            const int m = o / (WR * kTileRows), rr = o - m * WR * kTileRows;
-            const int64_t row = static_cast<int64_t>(round) * WR * kTileRows + rr;
-            if (row < p.N) {
-                const float* s = red + (rr / kTileRows * p.WK * kTileRows + rr % kTileRows) * 8 * NT + m;
-                float v = s[0];
-                for (int k = 1; k < p.WK; ++k) v += s[k * kTileRows * 8 * NT];
-                p.y[m * p.ldy + row] = to_bf16(v);
+        const int rows = count * p.WR * kTileRows;
+        const int64_t row0 = static_cast<int64_t>(t0 + group * p.WR) * kTileRows;
+        const int64_t row_end = min(static_cast<int64_t>(p.N), static_cast<int64_t>(t1) * kTileRows);
+        for (int o = threadIdx.x; o < p.M * rows; o += kThreads) {
+            const int m = o / rows, rr = o - m * rows;
+            if (row0 + rr < row_end) {
+                const int tile = rr / kTileRows, u = tile / p.WR, w0 = (tile - u * p.WR) * p.WK;
+                const uint8_t* s = smem + w0 * mine_bytes + red_at + ((u * kTileRows + rr % kTileRows) * 8 * NT + m) * 4;
+                float v = *reinterpret_cast<const float*>(s);
+                for (int k = 1; k < p.WK; ++k) v += *reinterpret_cast<const float*>(s + k * mine_bytes);
+                p.y[m * p.ldy + row0 + rr] = to_bf16(v);
             }
         }
-        __syncthreads();  // red is rewritten by the next round
+        __syncthreads();  // the sums' place is rewritten by the next group
     }
 }
 
-template <int FMT, int GP, int PC, int NT>
-cudaError_t launch(const GemvW4Args& a, cudaStream_t stream) {
+template <int FMT, int GP, int NT, int D>
+cudaError_t launch(const GemvParams& p, int sm_count, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_shared(gemv_w4_kernel<FMT, GP, NT, D>, allowed);
+    if (e != cudaSuccess) return e;
+    const int smem = kWarps * warp_bytes<GP, NT, D>(p.M, p.pieces, p.resident);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(min((p.tiles + p.WR - 1) / p.WR, sm_count)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = p.pdl ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gemv_w4_kernel<FMT, GP, NT, D>, p);
+}
+
+template <int FMT, int GP, int NT, int D>
+cudaError_t launch_depth(GemvParams& p, int sm_count, cudaStream_t stream) {
+    p.resident = kWarps * warp_bytes<GP, NT, D>(p.M, p.pieces, true) <= kMaxBlockShared;
+    static_assert(kWarps * warp_bytes<GP, NT, D>(8 * NT, 1, false) <= kMaxBlockShared, "one stage of x fits");
+    return launch<FMT, GP, NT, D>(p, sm_count, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_gemv_w4(const GemvW4Args& a, cudaStream_t stream) {
     GemvParams p;
     p.x = a.x;
     p.ldx = a.ldx;
@@ -154,39 +217,15 @@ cudaError_t launch(const GemvW4Args& a, cudaStream_t stream) {
     p.ldy = a.ldy;
     p.M = a.M;
     p.N = a.N;
+    p.tiles = (a.N + kTileRows - 1) / kTileRows;
     p.chunks = a.K / kChunk;
-    p.WK = kWarps;
-    while (p.WK > p.chunks) p.WK /= 2;
-    p.slice = (p.chunks + p.WK - 1) / p.WK;
-    p.pieces = (p.slice + PC - 1) / PC;
+    p.WK = min(p.chunks, kWarps);
+    p.WR = kWarps / p.WK;
+    p.pieces = ((p.chunks + p.WK - 1) / p.WK + kPC - 1) / kPC;
     p.pdl = a.pdl;
-    auto bytes = [&](int staged) { return reduce_bytes<NT>() + kWarps * warp_bytes<GP, PC>(p.M, staged); };
-    p.resident = bytes(p.pieces) <= kMaxBlockShared;
-    const int smem = bytes(p.resident ? p.pieces : 1);
-    static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_shared(gemv_w4_kernel<FMT, GP, PC, NT>, allowed);
-    if (e != cudaSuccess) return e;
-    const int per_sm = min(2, kMaxSmShared / (smem + 1024));
-    const int WR = kWarps / p.WK;
-    const int rounds = ((a.N + kTileRows - 1) / kTileRows + WR - 1) / WR;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(min(rounds, a.sm_count * per_sm)));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = a.pdl ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemv_w4_kernel<FMT, GP, PC, NT>, p);
-}
-
-}  // namespace
-
-cudaError_t launch_gemv_w4(const GemvW4Args& a, cudaStream_t stream) {
     return dispatch_format(a.format, a.group, [&](auto fmt, auto gp) {
-        return a.M <= 8 ? launch<fmt(), gp(), 4, 1>(a, stream) : launch<fmt(), gp(), 2, 2>(a, stream);
+        return a.M <= 8 ? launch_depth<fmt(), gp(), 1, 3>(p, a.sm_count, stream)
+                        : launch_depth<fmt(), gp(), 2, 2>(p, a.sm_count, stream);
     });
 }
 

@@ -4,17 +4,17 @@
 //   a = silu(h_gate) * h_up          (fp32, kept in the workspace)
 //   y[m] = bf16(sum over s, in slot order, of tw[m, s] * (a . w2[e]^T))
 //
-// 1. gate/up: items of (expert, up to 8 of its pairs, 16 gate rows and the 16
+// 1. gate/up: items of (expert, up to 8 of its pairs, JT x 16 gate rows and the
 //    up rows that go with them); the 8 warps of a block split H, their sums are
 //    added in warp order and the activation applied to the whole sum.
 // 2. down: a block owns 16 rows of the output for every token, its warps deal
 //    out the experts; the pairs' products meet in shared memory and are summed
 //    in slot order.  No partial sums in global memory, no atomics on values.
 //
-// An expert's codes are read once for up to 8 pairs.  Every block builds the
-// expert lists itself: a histogram of the routed pairs and its running sums.
-// The second launch is a programmatic dependent one: its lists and its first
-// codes do not wait for the first.
+// An expert's codes are read once for a batch of its pairs.  Every block builds
+// the expert lists itself: a histogram of the routed pairs and its running
+// sums.  The second launch is a programmatic dependent one: its lists and its
+// first codes do not wait for the first.
 #include "internal.cuh"
 #include "w4.cuh"
 
@@ -25,7 +25,7 @@ using namespace w4;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBatch = 8;  // pairs of an entry: the token columns of one MMA
+constexpr int kMaxBatch = 8;  // pairs of an entry at most: the token columns of one MMA
 constexpr size_t kHeader = 256;  // workspace: the device error word, then a
 
 struct MoeParams {
@@ -43,24 +43,34 @@ struct MoeParams {
     int M, S, H, I, E;
 };
 
-// Shared-memory tables of the routed pairs, built by every block.
+// Shared-memory tables of the routed pairs, built by every block, of P = M * S
+// elements each.
 struct Lists {
-    int n_entries;
-    int sums[kWarps];
-    int16_t pairs[FP8BS_MOE_MAX_PAIRS];        // pairs grouped by expert, ascending experts
-    int16_t unsorted[FP8BS_MOE_MAX_PAIRS];     // of experts with more than one entry
-    int16_t entry_expert[FP8BS_MOE_MAX_PAIRS];
-    int16_t entry_first[FP8BS_MOE_MAX_PAIRS];  // into pairs
-    int8_t entry_n[FP8BS_MOE_MAX_PAIRS];       // 1..kBatch
+    int16_t* pairs;     // grouped by expert, ascending experts
+    int16_t* unsorted;  // those of experts with more than one entry
+    int16_t* expert;    // of an entry
+    int16_t* first;     // its first pair in pairs
+    int16_t* n;         // its pairs: 1 .. batch
+    int entries;
 };
+__host__ __device__ constexpr int lists_bytes(int P) { return (5 * P * 2 + 15) / 16 * 16; }
+__host__ __device__ constexpr int counts_bytes(int E) { return (E * 4 + 15) / 16 * 16; }
 
 // counts: E ints of shared memory, free afterwards.  The order of the pairs of
 // an expert with one entry may differ between blocks and runs: it only decides
 // which MMA column serves a pair, and columns do not mix.  An expert with more
 // pairs has them sorted, so that every block splits them into the same entries.
-__device__ void build_lists(const MoeParams& p, Lists& L, int* counts) {
+__device__ Lists build_lists(const MoeParams& p, int batch, uint8_t* mem, int* counts) {
+    __shared__ int sums[kWarps];
+    __shared__ int n_entries;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = p.M * p.S;
+    Lists L;
+    L.pairs = reinterpret_cast<int16_t*>(mem);
+    L.unsorted = L.pairs + P;
+    L.expert = L.unsorted + P;
+    L.first = L.expert + P;
+    L.n = L.first + P;
     constexpr int kMine = FP8BS_MOE_MAX_PAIRS / kThreads;
     int id[kMine], rank[kMine];
 #pragma unroll
@@ -81,214 +91,277 @@ __device__ void build_lists(const MoeParams& p, Lists& L, int* counts) {
     const int per = (p.E + kThreads - 1) / kThreads;
     const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
     int mine = 0;
-    for (int e = e0; e < e1; ++e) mine += counts[e] | ((counts[e] + kBatch - 1) / kBatch << 16);
+    for (int e = e0; e < e1; ++e) mine += counts[e] | ((counts[e] + batch - 1) / batch << 16);
     int incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, incl, off);
         if (lane >= off) incl += v;
     }
-    if (lane == 31) L.sums[warp] = incl;
+    if (lane == 31) sums[warp] = incl;
     __syncthreads();
     int at = incl - mine;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-        if (w < warp) at += L.sums[w];
-    if (tid == kThreads - 1) L.n_entries = (at + mine) >> 16;
+        if (w < warp) at += sums[w];
+    if (tid == kThreads - 1) n_entries = (at + mine) >> 16;
     for (int e = e0; e < e1; ++e) {
         const int n = counts[e], first = at & 0xFFFF;
         counts[e] = first | n << 16;
-        for (int b = 0; b * kBatch < n; ++b) {
+        for (int b = 0; b * batch < n; ++b) {
             const int i = (at >> 16) + b;
-            L.entry_expert[i] = static_cast<int16_t>(e);
-            L.entry_first[i] = static_cast<int16_t>(first + b * kBatch);
-            L.entry_n[i] = static_cast<int8_t>(min(n - b * kBatch, kBatch));
+            L.expert[i] = static_cast<int16_t>(e);
+            L.first[i] = static_cast<int16_t>(first + b * batch);
+            L.n[i] = static_cast<int16_t>(min(n - b * batch, batch));
         }
-        at += n | ((n + kBatch - 1) / kBatch << 16);
+        at += n | ((n + batch - 1) / batch << 16);
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kMine; ++j)
         if (id[j] >= 0) {
             const int c = counts[id[j]];
-            (c >> 16 > kBatch ? L.unsorted : L.pairs)[(c & 0xFFFF) + rank[j]] = static_cast<int16_t>(tid + j * kThreads);
+            (c >> 16 > batch ? L.unsorted : L.pairs)[(c & 0xFFFF) + rank[j]] = static_cast<int16_t>(tid + j * kThreads);
         }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kMine; ++j)
-        if (id[j] >= 0 && counts[id[j]] >> 16 > kBatch) {
+        if (id[j] >= 0 && counts[id[j]] >> 16 > batch) {
             const int n = counts[id[j]] >> 16, first = counts[id[j]] & 0xFFFF, q = tid + j * kThreads;
             int r = 0;
             for (int i = 0; i < n; ++i) r += L.unsorted[first + i] < q;
             L.pairs[first + r] = static_cast<int16_t>(q);
         }
+    L.entries = n_entries;
     __syncthreads();
+    return L;
 }
 
-__host__ __device__ constexpr int lists_bytes() { return (sizeof(Lists) + 15) / 16 * 16; }
-__host__ __device__ constexpr int counts_bytes(int E) { return (E * 4 + 15) / 16 * 16; }
+constexpr int kDepth = 3;  // stages of a warp's ring
 
-template <int GP, int PC>
-__host__ __device__ constexpr int warp_bytes(int n) {
-    using S = Stage<GP, PC>;
-    return 2 * S::kCodeBytes + S::kScaleTableBytes + n * (S::kTokenPitch + 16);
+// Bytes of a warp: the ring, the scale table, a stage of tokens with its
+// inverse scales (whose place the gate/up sums take, red bytes).
+template <int GP>
+__host__ __device__ constexpr int warp_bytes(int n, int red) {
+    const int x = n * kTokenBytes;
+    return kDepth * kCodeBytes + kTableBytes<GP> + 32 + (x > red ? x : red);
 }
 
 // ---- 1. gate / up ------------------------------------------------------------
-constexpr int kUpPC = 4;
-constexpr int kRedBytes = kWarps * 2 * kTileRows * kBatch * 4;
+template <int JT>
+constexpr int kUpRed = 2 * JT * kTileRows * kMaxBatch * 4;  // of a warp
 
-template <int FMT, int GP>
-__global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_constant__ MoeParams p) {
-    constexpr int PC = kUpPC, SB = Format<FMT, GP>::kScaleBytes;
-    using S = Stage<GP, PC>;
+template <int FMT, int GP, int JT>
+__global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_constant__ MoeParams p, int batch) {
+    constexpr int SB = Format<FMT, GP>::kScaleBytes, D = kDepth;
     extern __shared__ __align__(16) uint8_t smem[];
-    Lists& L = *reinterpret_cast<Lists*>(smem);
-    float* red = reinterpret_cast<float*>(smem + lists_bytes());  // [kWarps][2][16][kBatch]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nmax = min(p.M * p.S, kBatch);
-    uint8_t* base = smem + lists_bytes() + kRedBytes;
-    uint8_t* codes = base + warp * warp_bytes<GP, PC>(nmax);
-    float* table = reinterpret_cast<float*>(codes + 2 * S::kCodeBytes);
-    uint8_t* xs = codes + 2 * S::kCodeBytes + S::kScaleTableBytes;
-    float* xinv = reinterpret_cast<float*>(xs + nmax * S::kTokenPitch);
-    build_lists(p, L, reinterpret_cast<int*>(base));
+    const int P = p.M * p.S;
+    uint8_t* base = smem + lists_bytes(P);
+    const int mine_bytes = warp_bytes<GP>(min(P, batch), kUpRed<JT>);
+    uint8_t* codes = base + warp * mine_bytes;
+    float* table = reinterpret_cast<float*>(codes + D * kCodeBytes);
+    float* inv = reinterpret_cast<float*>(codes + D * kCodeBytes + kTableBytes<GP>);
+    constexpr int kXsAt = D * kCodeBytes + kTableBytes<GP> + 32;
+    uint8_t* xs = codes + kXsAt;
+    const Lists L = build_lists(p, batch, smem, reinterpret_cast<int*>(base));
     ptx::griddep_launch_dependents();
 
-    const int chunks = p.H / kChunk, slice = (chunks + kWarps - 1) / kWarps, pieces = (slice + PC - 1) / PC;
-    const int first = warp * slice, last = min(first + slice, chunks);
-    const int per = p.I / kTileRows, items = L.n_entries * per;
+    const int chunks = p.H / kChunk;
+    const int first = warp * chunks / kWarps, last = (warp + 1) * chunks / kWarps;
+    const int pieces = ((chunks + kWarps - 1) / kWarps + kPC - 1) / kPC;
+    const int per = p.I / (JT * kTileRows), items = L.entries * per;
     const int64_t ldc = p.H / 2, lds = static_cast<int64_t>(chunks) * SB;
 
-    RawScales<PC> raw = {};
-    // stage u of an item: piece u / 2, gate (0) or up (1) rows u % 2
-    auto issue = [&](int item, int u, int b) {
-        const int c = first + u / 2 * PC, nch = min(last - c, PC);
-        if (item < items && nch > 0) {
-            const int entry = item / per, j = item - entry * per;
-            const int64_t row = static_cast<int64_t>(L.entry_expert[entry]) * 2 * p.I + (u & 1) * p.I + j * kTileRows;
-            load_codes<GP, PC>(codes + b * S::kCodeBytes, p.w13 + row * ldc + c * 64, ldc, kTileRows, nch, lane);
-            raw = load_scales<FMT, GP, PC>(p.s13 + row * lds + c * SB, lds, kTileRows, nch, lane);
+    // a warp's stages: the items of the block, in an item the pieces of the
+    // slice, in a piece the JT gate tiles and the JT up tiles
+    struct Cursor {
+        int item, piece, t;
+    };
+    auto advance = [&](Cursor& c) {
+        if (++c.t == 2 * JT) {
+            c.t = 0;
+            if (++c.piece == pieces) c.piece = 0, c.item += gridDim.x;
+        }
+    };
+    auto issue = [&](const Cursor& c, int slot) {
+        uint2 raw = make_uint2(0, 0);
+        const int at = first + c.piece * kPC, nch = min(last - at, kPC);
+        if (c.item < items && nch > 0) {
+            const int entry = c.item / per, j = c.item - entry * per;
+            const int64_t row = static_cast<int64_t>(L.expert[entry]) * 2 * p.I + (c.t / JT) * p.I + (j * JT + c.t % JT) * kTileRows;
+            load_codes(codes + slot * kCodeBytes, p.w13 + row * ldc + at * 64, ldc, kTileRows, nch, lane);
+            raw = load_scales<FMT, GP>(p.s13 + row * lds + at * SB, lds, kTileRows, nch, lane);
         }
         cp_async_commit();
+        return raw;
     };
-    issue(blockIdx.x, 0, 0);
-    int b = 0;
+    auto source = [&](int item, int piece) {
+        const int pf = L.first[item / per];
+        const int16_t* pairs = L.pairs + pf;
+        const uint16_t* x = p.x + (first + piece * kPC) * kChunk;
+        const int64_t ldx = p.ldx;
+        const int S = p.S;
+        return [=](int i) { return x + pairs[i] / S * ldx; };
+    };
+    RawBf16 tokens;
+    auto load_tokens = [&](int item, int piece) {
+        const int nch = min(last - first - piece * kPC, kPC);
+        if (item < items && nch > 0) tokens.load(L.n[item / per], nch, lane, source(item, piece));
+    };
+
+    Cursor ahead = {static_cast<int>(blockIdx.x), 0, 0};
+    uint2 raw[D - 1];
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) {
+        raw[i] = issue(ahead, i);
+        advance(ahead);
+    }
+    load_tokens(blockIdx.x, 0);
+    int slot = 0;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const int entry = item / per, j = item - entry * per;
-        const int n = L.entry_n[entry], pf = L.entry_first[entry];
-        float tot[2][4] = {};
+        const int n = L.n[entry], pf = L.first[entry];
+        float tot[2 * JT][4] = {};
         for (int piece = 0; piece < pieces; ++piece) {
-            const int c = first + piece * PC, nch = min(last - c, PC);
+            const int nch = min(last - first - piece * kPC, kPC);
+            if (nch > 0) stage_tokens<FMT>(xs, inv, tokens, n, nch, lane, source(item, piece));
+            if (piece + 1 < pieces)
+                load_tokens(item, piece + 1);
+            else
+                load_tokens(item + gridDim.x, 0);
 #pragma unroll
-            for (int half = 0; half < 2; ++half, b ^= 1) {
-                const RawScales<PC> cur = raw;
-                const int u = 2 * piece + half + 1;
-                const bool more = u < 2 * pieces;
-                issue(more ? item : item + static_cast<int>(gridDim.x), more ? u : 0, b ^ 1);
+            for (int t = 0; t < 2 * JT; ++t) {
+                const uint2 cur = raw[0];
+#pragma unroll
+                for (int i = 0; i + 2 < D; ++i) raw[i] = raw[i + 1];
+                raw[D - 2] = issue(ahead, slot == 0 ? D - 1 : slot - 1);
+                advance(ahead);
                 if (nch > 0) {
-                    if (half == 0)
-                        for (int i = 0; i < n; ++i) {
-                            const int m = L.pairs[pf + i] / p.S;
-                            const float inv = stage_token_bf16<FMT, PC>(xs + i * S::kTokenPitch, p.x + m * p.ldx + c * kChunk, nch, lane);
-                            if (lane == 0) xinv[i] = inv;
-                        }
-                    const float back = store_scales<FMT, GP, PC>(table, cur, lane);
-                    cp_async_wait<1>();
+                    const float back = store_scales<FMT, GP>(table, cur, lane);
+                    cp_async_wait<D - 1>();
                     __syncwarp();
-                    float acc[1][4] = {};
-                    stage_mma<FMT, GP, PC, 1>(acc, codes + b * S::kCodeBytes, table, xs, n, nch, lane);
-                    const int col = 2 * (lane & 3);
-                    const float i0 = xinv[min(col, n - 1)], i1 = xinv[min(col + 1, n - 1)];
-                    add_stage(tot[half], acc[0], i0, i1, back);
+                    float acc[1][4];
+                    stage_mma<FMT, GP, 1>(acc, codes + slot * kCodeBytes, table, xs, inv, back, n, nch, lane);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tot[t][i] += acc[0][i];
                 }
-                __syncwarp();
+                __syncwarp();  // the slot, the table and the tokens are rewritten by later stages
+                slot = slot + 1 == D ? 0 : slot + 1;
             }
         }
-        float* r = red + (warp * 2 * kTileRows + (lane >> 2)) * kBatch + 2 * (lane & 3);
+        // [warp][tile][row][pair]
+        float* r = reinterpret_cast<float*>(xs) + (lane >> 2) * kMaxBatch + 2 * (lane & 3);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            *reinterpret_cast<float2*>(r + half * kTileRows * kBatch) = make_float2(tot[half][0], tot[half][1]);
-            *reinterpret_cast<float2*>(r + (half * kTileRows + 8) * kBatch) = make_float2(tot[half][2], tot[half][3]);
+        for (int t = 0; t < 2 * JT; ++t) {
+            *reinterpret_cast<float2*>(r + t * kTileRows * kMaxBatch) = make_float2(tot[t][0], tot[t][1]);
+            *reinterpret_cast<float2*>(r + (t * kTileRows + 8) * kMaxBatch) = make_float2(tot[t][2], tot[t][3]);
         }
         __syncthreads();
-        if (threadIdx.x < kTileRows * kBatch) {
-            const int i = threadIdx.x / kTileRows, row = threadIdx.x % kTileRows;
-            if (i < n) {
-                float g = 0.0f, v = 0.0f;
+        for (int o = threadIdx.x; o < n * JT * kTileRows; o += kThreads) {
+            const int i = o / (JT * kTileRows), row = o - i * JT * kTileRows;
+            const uint8_t* s = base + kXsAt + (row * kMaxBatch + i) * 4;
+            float g = 0.0f, v = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    g += red[(w * 2 * kTileRows + row) * kBatch + i];
-                    v += red[((w * 2 + 1) * kTileRows + row) * kBatch + i];
-                }
-                p.a[static_cast<int64_t>(L.pairs[pf + i]) * p.I + j * kTileRows + row] = g / (1.0f + expf(-g)) * v;
+            for (int w = 0; w < kWarps; ++w) {
+                g += *reinterpret_cast<const float*>(s + w * mine_bytes);
+                v += *reinterpret_cast<const float*>(s + w * mine_bytes + JT * kTileRows * kMaxBatch * 4);
             }
+            p.a[static_cast<int64_t>(L.pairs[pf + i]) * p.I + j * JT * kTileRows + row] = g / (1.0f + expf(-g)) * v;
         }
-        __syncthreads();  // red is rewritten by the next item
+        __syncthreads();  // the sums' place is rewritten by the next item
     }
 }
 
 // ---- 2. down -----------------------------------------------------------------
-template <int FMT, int GP, int PC>
-__global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_constant__ MoeParams p) {
-    constexpr int SB = Format<FMT, GP>::kScaleBytes;
-    using S = Stage<GP, PC>;
+template <int FMT, int GP>
+__global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_constant__ MoeParams p, int batch) {
+    constexpr int SB = Format<FMT, GP>::kScaleBytes, D = kDepth;
     extern __shared__ __align__(16) uint8_t smem[];
-    Lists& L = *reinterpret_cast<Lists*>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int P = p.M * p.S, nmax = min(P, kBatch);
-    float* out = reinterpret_cast<float*>(smem + lists_bytes());  // [P][16]
-    uint8_t* base = smem + lists_bytes() + P * kTileRows * 4;
-    uint8_t* codes = base + warp * warp_bytes<GP, PC>(nmax);
-    float* table = reinterpret_cast<float*>(codes + 2 * S::kCodeBytes);
-    uint8_t* xs = codes + 2 * S::kCodeBytes + S::kScaleTableBytes;
-    float* xinv = reinterpret_cast<float*>(xs + nmax * S::kTokenPitch);
-    build_lists(p, L, reinterpret_cast<int*>(base));
+    const int P = p.M * p.S;
+    float* out = reinterpret_cast<float*>(smem + lists_bytes(P));  // [P][16]
+    uint8_t* base = smem + lists_bytes(P) + P * kTileRows * 4;
+    uint8_t* codes = base + warp * warp_bytes<GP>(min(P, batch), 0);
+    float* table = reinterpret_cast<float*>(codes + D * kCodeBytes);
+    float* inv = reinterpret_cast<float*>(codes + D * kCodeBytes + kTableBytes<GP>);
+    uint8_t* xs = codes + D * kCodeBytes + kTableBytes<GP> + 32;
+    const Lists L = build_lists(p, batch, smem, reinterpret_cast<int*>(base));
 
-    const int chunks = p.I / kChunk, pieces = (chunks + PC - 1) / PC;
+    const int chunks = p.I / kChunk, pieces = (chunks + kPC - 1) / kPC;
     const int64_t ldc = p.I / 2, lds = static_cast<int64_t>(chunks) * SB;
     const int tiles = p.H / kTileRows;
-    RawScales<PC> raw = {};
-    auto issue = [&](int tile, int entry, int piece, int b) {
-        if (tile < tiles && entry < L.n_entries) {
-            const int c = piece * PC, nch = min(chunks - c, PC);
-            const int64_t row = static_cast<int64_t>(L.entry_expert[entry]) * p.H + tile * kTileRows;
-            load_codes<GP, PC>(codes + b * S::kCodeBytes, p.w2 + row * ldc + c * 64, ldc, kTileRows, nch, lane);
-            raw = load_scales<FMT, GP, PC>(p.s2 + row * lds + c * SB, lds, kTileRows, nch, lane);
+
+    // a warp's stages: the tiles of the block, in a tile the warp's entries,
+    // in an entry the pieces of I
+    struct Cursor {
+        int tile, entry, piece;
+    };
+    auto advance = [&](Cursor& c) {
+        if (++c.piece == pieces) {
+            c.piece = 0;
+            if ((c.entry += kWarps) >= L.entries) c.entry = warp, c.tile += gridDim.x;
+        }
+    };
+    auto issue = [&](const Cursor& c, int slot) {
+        uint2 raw = make_uint2(0, 0);
+        if (c.tile < tiles && c.entry < L.entries) {
+            const int at = c.piece * kPC, nch = min(chunks - at, kPC);
+            const int64_t row = static_cast<int64_t>(L.expert[c.entry]) * p.H + c.tile * kTileRows;
+            load_codes(codes + slot * kCodeBytes, p.w2 + row * ldc + at * 64, ldc, kTileRows, nch, lane);
+            raw = load_scales<FMT, GP>(p.s2 + row * lds + at * SB, lds, kTileRows, nch, lane);
         }
         cp_async_commit();
+        return raw;
     };
-    issue(blockIdx.x, warp, 0, 0);
+    auto source = [&](int entry, int piece) {
+        const int16_t* pairs = L.pairs + L.first[entry];
+        const float* a = p.a + piece * kStageK;
+        const int I = p.I;
+        return [=](int i) { return a + static_cast<int64_t>(pairs[i]) * I; };
+    };
+    RawF32 tokens;
+    auto load_tokens = [&](int entry, int piece) {
+        if (entry < L.entries) tokens.load(L.n[entry], min(chunks - piece * kPC, kPC), lane, source(entry, piece));
+    };
+
+    Cursor ahead = {static_cast<int>(blockIdx.x), warp, 0};
+    uint2 raw[D - 1];
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) {
+        raw[i] = issue(ahead, i);
+        advance(ahead);
+    }
     ptx::griddep_wait();
-    int b = 0;
+    load_tokens(warp, 0);
+    int slot = 0;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         for (int q = tid; q < P * kTileRows; q += kThreads) out[q] = 0.0f;  // pairs with an invalid id stay 0
         __syncthreads();
-        for (int entry = warp; entry < L.n_entries; entry += kWarps) {
-            const int n = L.entry_n[entry], pf = L.entry_first[entry];
+        for (int entry = warp; entry < L.entries; entry += kWarps) {
+            const int n = L.n[entry], pf = L.first[entry];
             float tot[4] = {};
-            for (int piece = 0; piece < pieces; ++piece, b ^= 1) {
-                const int c = piece * PC, nch = min(chunks - c, PC);
-                const RawScales<PC> cur = raw;
+            for (int piece = 0; piece < pieces; ++piece) {
+                const int nch = min(chunks - piece * kPC, kPC);
+                stage_tokens<FMT>(xs, inv, tokens, n, nch, lane, source(entry, piece));
                 if (piece + 1 < pieces)
-                    issue(tile, entry, piece + 1, b ^ 1);
-                else if (entry + kWarps < L.n_entries)
-                    issue(tile, entry + kWarps, 0, b ^ 1);
+                    load_tokens(entry, piece + 1);
                 else
-                    issue(tile + gridDim.x, warp, 0, b ^ 1);
-                for (int i = 0; i < n; ++i) {
-                    const float inv = stage_token_f32<FMT, PC>(xs + i * S::kTokenPitch, p.a + static_cast<int64_t>(L.pairs[pf + i]) * p.I + c * kChunk, nch, lane);
-                    if (lane == 0) xinv[i] = inv;
-                }
-                const float back = store_scales<FMT, GP, PC>(table, cur, lane);
-                cp_async_wait<1>();
+                    load_tokens(entry + kWarps < L.entries ? entry + kWarps : warp, 0);
+                const uint2 cur = raw[0];
+#pragma unroll
+                for (int i = 0; i + 2 < D; ++i) raw[i] = raw[i + 1];
+                raw[D - 2] = issue(ahead, slot == 0 ? D - 1 : slot - 1);
+                advance(ahead);
+                const float back = store_scales<FMT, GP>(table, cur, lane);
+                cp_async_wait<D - 1>();
                 __syncwarp();
-                float acc[1][4] = {};
-                stage_mma<FMT, GP, PC, 1>(acc, codes + b * S::kCodeBytes, table, xs, n, nch, lane);
-                const int col = 2 * (lane & 3);
-                const float i0 = xinv[min(col, n - 1)], i1 = xinv[min(col + 1, n - 1)];
-                add_stage(tot, acc[0], i0, i1, back);
-                __syncwarp();
+                float acc[1][4];
+                stage_mma<FMT, GP, 1>(acc, codes + slot * kCodeBytes, table, xs, inv, back, n, nch, lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tot[i] += acc[0][i];
+                __syncwarp();  // the slot, the table and the tokens are rewritten by later stages
+                slot = slot + 1 == D ? 0 : slot + 1;
             }
             const int col = 2 * (lane & 3), row = lane >> 2;
 #pragma unroll
@@ -313,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
     }
 }
 
-cudaError_t launch_pdl(void (*kernel)(MoeParams), const MoeParams& p, int grid, int smem, bool pdl, cudaStream_t stream) {
+cudaError_t launch_pdl(void (*kernel)(MoeParams, int), const MoeParams& p, int batch, int grid, int smem, bool pdl, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kThreads);
@@ -324,30 +397,35 @@ cudaError_t launch_pdl(void (*kernel)(MoeParams), const MoeParams& p, int grid, 
     attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p, batch);
+}
+
+template <int FMT, int GP, int JT>
+cudaError_t launch_up(const MoeParams& p, int sm_count, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_shared(moe_w4_up_kernel<FMT, GP, JT>, allowed);
+    if (e != cudaSuccess) return e;
+    const int P = p.M * p.S, batch = kMaxBatch;
+    const int smem = lists_bytes(P) + max(counts_bytes(p.E), kWarps * warp_bytes<GP>(min(P, batch), kUpRed<JT>));
+    const int per_sm = min(2, kMaxSmShared / (smem + 1024));
+    const int64_t most = static_cast<int64_t>(P) * (p.I / (JT * kTileRows));
+    const int grid = static_cast<int>(min(most, static_cast<int64_t>(sm_count) * per_sm));
+    return launch_pdl(moe_w4_up_kernel<FMT, GP, JT>, p, batch, grid, smem, false, stream);
 }
 
 template <int FMT, int GP>
-cudaError_t launch_up(const MoeParams& p, int sm_count, cudaStream_t stream) {
-    static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_shared(moe_w4_up_kernel<FMT, GP>, allowed);
-    if (e != cudaSuccess) return e;
-    const int P = p.M * p.S;
-    const int smem = lists_bytes() + kRedBytes + max(counts_bytes(p.E), kWarps * warp_bytes<GP, kUpPC>(min(P, kBatch)));
-    const int per_sm = min(2, kMaxSmShared / (smem + 1024));
-    const int grid = static_cast<int>(min(static_cast<int64_t>(P) * (p.I / kTileRows), static_cast<int64_t>(sm_count) * per_sm));
-    return launch_pdl(moe_w4_up_kernel<FMT, GP>, p, grid, smem, false, stream);
-}
-
-template <int FMT, int GP, int PC>
 cudaError_t launch_down(const MoeParams& p, int sm_count, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_shared(moe_w4_down_kernel<FMT, GP, PC>, allowed);
+    cudaError_t e = allow_shared(moe_w4_down_kernel<FMT, GP>, allowed);
     if (e != cudaSuccess) return e;
     const int P = p.M * p.S;
-    const int smem = lists_bytes() + P * kTileRows * 4 + max(counts_bytes(p.E), kWarps * warp_bytes<GP, PC>(min(P, kBatch)));
-    const int per_sm = min(2, kMaxSmShared / (smem + 1024));
-    return launch_pdl(moe_w4_down_kernel<FMT, GP, PC>, p, min(p.H / kTileRows, sm_count * per_sm), smem, true, stream);
+    auto bytes = [&](int batch) {
+        return lists_bytes(P) + P * kTileRows * 4 + max(counts_bytes(p.E), kWarps * warp_bytes<GP>(min(P, batch), 0));
+    };
+    // half the pairs of an entry where that lets two blocks share a multiprocessor
+    const int batch = bytes(kMaxBatch) + 1024 > kMaxSmShared / 2 && bytes(kMaxBatch / 2) + 1024 <= kMaxSmShared / 2 ? kMaxBatch / 2 : kMaxBatch;
+    const int smem = bytes(batch), per_sm = min(2, kMaxSmShared / (smem + 1024));
+    return launch_pdl(moe_w4_down_kernel<FMT, GP>, p, batch, min(p.H / kTileRows, sm_count * per_sm), smem, true, stream);
 }
 
 }  // namespace
@@ -375,11 +453,8 @@ cudaError_t launch_moe_w4(const MoeW4Args& a, cudaStream_t stream) {
     p.I = a.I;
     p.E = a.E;
     return dispatch_format(a.format, a.group, [&](auto fmt, auto gp) {
-        const cudaError_t e = launch_up<fmt(), gp()>(p, a.sm_count, stream);
-        if (e != cudaSuccess) return e;
-        if (p.I == 128) return launch_down<fmt(), gp(), 1>(p, a.sm_count, stream);
-        if (p.I == 256) return launch_down<fmt(), gp(), 2>(p, a.sm_count, stream);
-        return launch_down<fmt(), gp(), 4>(p, a.sm_count, stream);
+        const cudaError_t e = launch_up<fmt(), gp(), 1>(p, a.sm_count, stream);
+        return e != cudaSuccess ? e : launch_down<fmt(), gp()>(p, a.sm_count, stream);
     });
 }
 
