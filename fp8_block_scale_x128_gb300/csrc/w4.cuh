@@ -73,33 +73,39 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Start the copy of nch (1..kPC) chunks of 16 code rows to dst.  codes points
-// at row 0's first byte of the stage; row r >= rows repeats the last row (its
-// outputs are dropped), so every access stays inside the weight.
-__device__ __forceinline__ void load_codes(uint8_t* dst, const uint8_t* codes, int64_t ldc, int rows, int nch, int lane) {
-    const int s = lane & 7;  // 16-byte piece of the row's 128
-    if (s >= nch * 4) return;
+// Start the copy of a stage: nch (1..kPC) chunks of 16 code rows to dst.  src
+// points at this lane's first 16 bytes: row lane / 8 of the tile, byte
+// 16 (lane % 8) of the stage; it takes the rows 4, 8 and 12 further on as well.
+// last: the tile's last row; rows past it repeat it (their outputs are
+// dropped), so every access stays inside the weight.
+__device__ __forceinline__ void load_codes(uint8_t* dst, const uint8_t* src, int64_t ldc, int last, int nch, int lane) {
+    if ((lane & 7) >= nch * 4) return;
+    uint8_t* to = dst + (lane >> 3) * kCodePitch + (lane & 7) * 16;
+    if (last == kTileRows - 1) {
 #pragma unroll
-    for (int j = 0; j < kTileRows / 4; ++j) {
-        const int r = (lane >> 3) + 4 * j;
-        ptx::cp_async16(dst + r * kCodePitch + s * 16, codes + static_cast<int64_t>(min(r, rows - 1)) * ldc + s * 16);
+        for (int j = 0; j < kTileRows / 4; ++j) ptx::cp_async16(to + 4 * j * kCodePitch, src + 4 * j * ldc);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kTileRows / 4; ++j) {
+            const int r = (lane >> 3) + 4 * j;
+            ptx::cp_async16(to + 4 * j * kCodePitch, src + (min(r, last) - (lane >> 3)) * ldc);
+        }
     }
 }
 
-// The stage's scale words as loaded: lane l holds row l / 2, chunk l % 2 (row
-// pitch lds bytes); zeros past nch.
+// The stage's scale words as loaded: lane l holds row l / 2, chunk l % 2; zeros
+// past nch.  src points at the lane's own scales (row min(l / 2, last)).
 template <int FMT, int GP>
-__device__ __forceinline__ uint2 load_scales(const uint8_t* scales, int64_t lds, int rows, int nch, int lane) {
+__device__ __forceinline__ uint2 load_scales(const uint8_t* src, int nch, int lane) {
     constexpr int SB = Format<FMT, GP>::kScaleBytes;
     uint2 w = make_uint2(0, 0);
     if ((lane & 1) < nch) {
-        const uint8_t* p = scales + static_cast<int64_t>(min(lane >> 1, rows - 1)) * lds + (lane & 1) * SB;
         if constexpr (SB == 8)
-            w = __ldg(reinterpret_cast<const uint2*>(p));
+            w = __ldg(reinterpret_cast<const uint2*>(src));
         else if constexpr (SB == 4)
-            w.x = __ldg(reinterpret_cast<const uint32_t*>(p));
+            w.x = __ldg(reinterpret_cast<const uint32_t*>(src));
         else
-            w.x = __ldg(reinterpret_cast<const uint16_t*>(p));
+            w.x = __ldg(reinterpret_cast<const uint16_t*>(src));
     }
     return w;
 }
@@ -110,12 +116,13 @@ __device__ __forceinline__ uint2 load_scales(const uint8_t* scales, int64_t lds,
 // by 2^64 (kBigScale), so that a group's sum, up to 2^27 at the activations'
 // fixed scaling, times its scale stays finite; returns the factor to put back.
 constexpr float kBigScale = 0x1p64f;
-template <int FMT, int GP>
-__device__ __forceinline__ float store_scales(float* table, uint2 raw, int lane) {
-    // some scale's three top exponent bits all set
+template <int FMT>
+__device__ __forceinline__ bool big_scale(uint2 raw) {  // some scale's three top exponent bits all set
     const uint32_t high = (raw.x & raw.x << 1 & raw.x << 2) | (raw.y & raw.y << 1 & raw.y << 2);
-    const bool big = __any_sync(0xFFFFFFFFu, (high & (FMT == FP8BS_W4_MXFP4 ? 0x80808080u : 0x40004000u)) != 0);
-    const float fit = big ? 1.0f / kBigScale : 1.0f, back = big ? kBigScale : 1.0f;
+    return (high & (FMT == FP8BS_W4_MXFP4 ? 0x80808080u : 0x40004000u)) != 0;
+}
+template <int FMT, int GP>
+__device__ __forceinline__ void store_scales_by(float* table, uint2 raw, bool big, int lane) {
     const uint32_t w[2] = {raw.x, raw.y};
     float v[GP];
 #pragma unroll
@@ -124,8 +131,10 @@ __device__ __forceinline__ float store_scales(float* table, uint2 raw, int lane)
             v[i] = __uint_as_float(max(((w[0] >> (8 * i)) & 0xFFu) << 23, 0x00400000u));
         else
             v[i] = __uint_as_float((w[i / 2] >> (16 * (i % 2))) << 16);
-        v[i] *= fit;
     }
+    if (big)
+#pragma unroll
+        for (int i = 0; i < GP; ++i) v[i] *= 1.0f / kBigScale;
     float* dst = table + (lane >> 1) * kScalePitch<GP> + (lane & 1) * GP;
     if constexpr (GP == 4)
         *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
@@ -133,7 +142,20 @@ __device__ __forceinline__ float store_scales(float* table, uint2 raw, int lane)
         *reinterpret_cast<float2*>(dst) = make_float2(v[0], v[1]);
     else
         dst[0] = v[0];
-    return back;
+}
+template <int FMT, int GP>
+__device__ __forceinline__ float store_scales(float* table, uint2 raw, int lane) {
+    const bool big = __any_sync(0xFFFFFFFFu, big_scale<FMT>(raw));
+    store_scales_by<FMT, GP>(table, raw, big, lane);
+    return big ? kBigScale : 1.0f;
+}
+// Of a stage of two tiles.
+template <int FMT, int GP>
+__device__ __forceinline__ float store_scales(float* table, uint2 raw0, uint2 raw1, int lane) {
+    const bool big = __any_sync(0xFFFFFFFFu, big_scale<FMT>(raw0) || big_scale<FMT>(raw1));
+    store_scales_by<FMT, GP>(table, raw0, big, lane);
+    store_scales_by<FMT, GP>(table + kTileRows * kScalePitch<GP>, raw1, big, lane);
+    return big ? kBigScale : 1.0f;
 }
 
 // 2^(14 - e) and its inverse for a slice whose largest magnitude has the
@@ -284,6 +306,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// d = a b
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -291,11 +321,12 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                  : "memory");
 }
 
-// The stage's product for token columns 8j .. 8j+7, their scale factors put
-// back: D fragment (rows g, g + 8; columns 2t, 2t + 1).  Columns past n repeat
-// token n - 1.
-template <int FMT, int GP, int NT>
-__device__ __forceinline__ void stage_mma(float (&acc)[NT][4], const uint8_t* codes, const float* table, const uint8_t* xs,
+// tot[i][j] += the stage's products of tile i and token columns 8j .. 8j+7, as D
+// fragments (rows g, g + 8; columns 2t, 2t + 1).  Tile i's codes and scale
+// table follow tile i - 1's.  inv holds 8 NT factors; columns past n repeat
+// token n - 1 and take whatever factor is there, they are never read.
+template <int FMT, int GP, int NT, int T>
+__device__ __forceinline__ void stage_mma(float (&tot)[T][NT][4], const uint8_t* codes, const float* table, const uint8_t* xs,
                                           const float* inv, float back, int n, int nch, int lane) {
     const int g = lane >> 2, t = lane & 3;
     // ldmatrix: lanes 0-15 address rows 0-15 of an even group, 16-31 of the odd one
@@ -308,62 +339,101 @@ __device__ __forceinline__ void stage_mma(float (&acc)[NT][4], const uint8_t* co
         x[j][0] = xs + tok * kTokenBytes + t * 16 + odd * 64;  // even groups
         x[j][1] = xs + tok * kTokenBytes + t * 16 - odd * 64;  // odd ones
     }
+    float acc[T][NT][4];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+    for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.0f;
 #pragma unroll
     for (int c = 0; c < kPC; ++c) {
         if (c >= nch) break;
-        float sa[GP], sb[GP];
-        const float* p = s0 + c * GP;
-        if constexpr (GP == 4) {
-            const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 8 * kScalePitch<GP>);
-            sa[0] = u.x, sa[1] = u.y, sa[2] = u.z, sa[3] = u.w;
-            sb[0] = v.x, sb[1] = v.y, sb[2] = v.z, sb[3] = v.w;
-        } else {
+        float sa[T][GP], sb[T][GP];
 #pragma unroll
-            for (int q = 0; q < GP; ++q) sa[q] = p[q], sb[q] = p[8 * kScalePitch<GP> + q];
+        for (int i = 0; i < T; ++i) {
+            const float* p = s0 + i * kTileRows * kScalePitch<GP> + c * GP;
+            if constexpr (GP == 4) {
+                const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 8 * kScalePitch<GP>);
+                sa[i][0] = u.x, sa[i][1] = u.y, sa[i][2] = u.z, sa[i][3] = u.w;
+                sb[i][0] = v.x, sb[i][1] = v.y, sb[i][2] = v.z, sb[i][3] = v.w;
+            } else {
+#pragma unroll
+                for (int q = 0; q < GP; ++q) sa[i][q] = p[q], sb[i][q] = p[8 * kScalePitch<GP> + q];
+            }
         }
         constexpr int kPerScale = 4 / GP;  // 32-wide groups under one scale
-        float part[NT][4];
+        float part[T][NT][4];
 #pragma unroll
         for (int i2 = 0; i2 < 2; ++i2) {
-            uint32_t w[4];  // group 2 i2: rows g, g + 8; group 2 i2 + 1: the same
-            ldmatrix4(w, c0 + c * 64 + i2 * 32);
+            uint32_t w[T][4];  // group 2 i2: rows g, g + 8; group 2 i2 + 1: the same
+#pragma unroll
+            for (int i = 0; i < T; ++i) ldmatrix4(w[i], c0 + i * kCodeBytes + c * 64 + i2 * 32);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int i = 2 * i2 + h;
-                if (i % kPerScale == 0)
+                const int grp = 2 * i2 + h;
+                uint4 b[NT];
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) part[j][0] = part[j][1] = part[j][2] = part[j][3] = 0.0f;
-                uint32_t lo[4], hi[4];
-                decode8<FMT>(w[2 * h], lo);
-                decode8<FMT>(w[2 * h + 1], hi);
+                for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const uint4*>(x[j][h] + c * 256 + grp * 64);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const uint4 b = *reinterpret_cast<const uint4*>(x[j][h] + c * 256 + i * 64);
-                    mma16816(part[j], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
-                    mma16816(part[j], lo[2], hi[2], lo[3], hi[3], b.z, b.w);
-                }
-                if (i % kPerScale == kPerScale - 1) {
-                    const int q = i / kPerScale;
+                for (int i = 0; i < T; ++i) {
+                    uint32_t lo[4], hi[4];
+                    decode8<FMT>(w[i][2 * h], lo);
+                    decode8<FMT>(w[i][2 * h + 1], hi);
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        acc[j][0] = fmaf(part[j][0], sa[q], acc[j][0]);
-                        acc[j][1] = fmaf(part[j][1], sa[q], acc[j][1]);
-                        acc[j][2] = fmaf(part[j][2], sb[q], acc[j][2]);
-                        acc[j][3] = fmaf(part[j][3], sb[q], acc[j][3]);
+                        if (grp % kPerScale == 0)
+                            mma16816_zero(part[i][j], lo[0], hi[0], lo[1], hi[1], b[j].x, b[j].y);
+                        else
+                            mma16816(part[i][j], lo[0], hi[0], lo[1], hi[1], b[j].x, b[j].y);
+                        mma16816(part[i][j], lo[2], hi[2], lo[3], hi[3], b[j].z, b[j].w);
+                    }
+                    if (grp % kPerScale == kPerScale - 1) {
+                        const int q = grp / kPerScale;
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            acc[i][j][0] = fmaf(part[i][j][0], sa[i][q], acc[i][j][0]);
+                            acc[i][j][1] = fmaf(part[i][j][1], sa[i][q], acc[i][j][1]);
+                            acc[i][j][2] = fmaf(part[i][j][2], sb[i][q], acc[i][j][2]);
+                            acc[i][j][3] = fmaf(part[i][j][3], sb[i][q], acc[i][j][3]);
+                        }
                     }
                 }
             }
         }
     }
+    // the factors one after the other: their product may leave fp32's range
+    // where the result does not
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        const float i0 = inv[min(8 * j + 2 * t, n - 1)], i1 = inv[min(8 * j + 2 * t + 1, n - 1)];
-        acc[j][0] = acc[j][0] * i0 * back;
-        acc[j][1] = acc[j][1] * i1 * back;
-        acc[j][2] = acc[j][2] * i0 * back;
-        acc[j][3] = acc[j][3] * i1 * back;
+        const float2 f = *reinterpret_cast<const float2*>(inv + 8 * j + 2 * t);
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+            if (back == 1.0f) {
+                tot[i][j][0] = fmaf(acc[i][j][0], f.x, tot[i][j][0]);
+                tot[i][j][1] = fmaf(acc[i][j][1], f.y, tot[i][j][1]);
+                tot[i][j][2] = fmaf(acc[i][j][2], f.x, tot[i][j][2]);
+                tot[i][j][3] = fmaf(acc[i][j][3], f.y, tot[i][j][3]);
+            } else {
+                tot[i][j][0] = fmaf(acc[i][j][0] * f.x, back, tot[i][j][0]);
+                tot[i][j][1] = fmaf(acc[i][j][1] * f.y, back, tot[i][j][1]);
+                tot[i][j][2] = fmaf(acc[i][j][2] * f.x, back, tot[i][j][2]);
+                tot[i][j][3] = fmaf(acc[i][j][3] * f.y, back, tot[i][j][3]);
+            }
+    }
+}
+
+// D fragments of a warp as [column][kSumPitch], conflict-free to write and read.
+constexpr int kSumPitch = kTileRows + 4;  // floats
+template <int NT>
+constexpr int kSumBytes = 8 * NT * kSumPitch * 4;  // of a tile
+template <int NT>
+__device__ __forceinline__ void store_sums(float* dst, const float (&tot)[NT][4], int lane) {
+    float* r = dst + 2 * (lane & 3) * kSumPitch + (lane >> 2);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        r[8 * j * kSumPitch] = tot[j][0];
+        r[(8 * j + 1) * kSumPitch] = tot[j][1];
+        r[8 * j * kSumPitch + 8] = tot[j][2];
+        r[(8 * j + 1) * kSumPitch + 8] = tot[j][3];
     }
 }
 

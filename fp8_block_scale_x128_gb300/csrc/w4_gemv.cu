@@ -37,13 +37,13 @@ struct GemvParams {
 };
 
 template <int NT>
-constexpr int kRedBytes = kGroup * kTileRows * 8 * NT * 4;  // of a warp
+constexpr int kRedBytes = kGroup * kSumBytes<NT>;  // of a warp
 
 // Bytes of a warp: the ring, the scale table, staged x and its inverse scales,
 // and the partial sums, which take the place of x where that is staged anew.
 template <int GP, int NT, int D>
 __host__ __device__ constexpr int warp_bytes(int M, int pieces, bool resident) {
-    const int x = (resident ? pieces : 1) * M * kTokenBytes, inv = ((resident ? pieces : 1) * M * 4 + 15) / 16 * 16;
+    const int kept = resident ? pieces : 1, x = kept * M * kTokenBytes, inv = kept * 8 * NT * 4;
     return D * kCodeBytes + kTableBytes<GP> + inv + (resident ? x + kRedBytes<NT> : (x > kRedBytes<NT> ? x : kRedBytes<NT>));
 }
 
@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
     const int mine_bytes = warp_bytes<GP, NT, D>(p.M, p.pieces, p.resident);
     uint8_t* codes = smem + warp * mine_bytes;                          // [D][kCodeBytes]
     float* table = reinterpret_cast<float*>(codes + D * kCodeBytes);    // scales
-    float* inv = reinterpret_cast<float*>(codes + D * kCodeBytes + kTableBytes<GP>);  // [kept][M]
-    const int x_at = D * kCodeBytes + kTableBytes<GP> + (kept * p.M * 4 + 15) / 16 * 16;
+    float* inv = reinterpret_cast<float*>(codes + D * kCodeBytes + kTableBytes<GP>);  // [kept][8 NT]
+    const int x_at = D * kCodeBytes + kTableBytes<GP> + kept * 8 * NT * 4;
     uint8_t* xs = codes + x_at;                                         // [kept][M][kTokenBytes]
     const int red_at = x_at + (p.resident ? kept * p.M * kTokenBytes : 0);
 
@@ -71,26 +71,45 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
     const int steps = (t1 - t0 + p.WR - 1) / p.WR;  // tiles of a warp
 
     // the order of a warp's stages: groups of kGroup tiles, in a group the
-    // pieces of the slice, in a piece the tiles
+    // pieces of the slice, in a piece the tiles; codes and scales are this
+    // lane's pointers into the stage
     struct Cursor {
-        int group, piece, t;
+        int group, piece, t, tile;
+        const uint8_t *codes, *scales;
     };
-    auto advance = [&](Cursor& c) {
-        if (++c.t == min(kGroup, steps - c.group)) {
-            c.t = 0;
-            if (++c.piece == p.pieces) c.piece = 0, c.group += kGroup;
-        }
-    };
-    auto issue = [&](const Cursor& c, int slot) {
+    const int64_t tile_codes = kTileRows * p.WR * p.ldc, tile_scales = kTileRows * p.WR * p.lds;
+    Cursor ahead = {0, 0, 0, t0 + wr, nullptr, nullptr};
+    ahead.codes = p.codes + (static_cast<int64_t>(t0 + wr) * kTileRows + (lane >> 3)) * p.ldc + first * 64 + (lane & 7) * 16;
+    ahead.scales = p.scales + (static_cast<int64_t>(t0 + wr) * kTileRows + (lane >> 1)) * p.lds + (first + (lane & 1)) * SB;
+    auto issue = [&](int slot) {
         uint2 raw = make_uint2(0, 0);
-        const int tile = t0 + (c.group + c.t) * p.WR + wr, at = first + c.piece * kPC, nch = min(last - at, kPC);
-        if (c.group < steps && tile < t1 && nch > 0) {
-            const int64_t row = static_cast<int64_t>(tile) * kTileRows;
-            const int rows = min(p.N - tile * kTileRows, kTileRows);
-            load_codes(codes + slot * kCodeBytes, p.codes + row * p.ldc + at * 64, p.ldc, rows, nch, lane);
-            raw = load_scales<FMT, GP>(p.scales + row * p.lds + at * SB, p.lds, rows, nch, lane);
+        const int nch = min(last - first - ahead.piece * kPC, kPC);
+        if (ahead.group < steps && ahead.tile < t1 && nch > 0) {
+            const int last_row = min(p.N - ahead.tile * kTileRows, kTileRows) - 1;
+            load_codes(codes + slot * kCodeBytes, ahead.codes, p.ldc, last_row, nch, lane);
+            raw = load_scales<FMT, GP>(ahead.scales - max((lane >> 1) - last_row, 0) * p.lds, nch, lane);
         }
         cp_async_commit();
+        // on to the next stage
+        const int count = min(kGroup, steps - ahead.group);
+        if (++ahead.t < count) {
+            ahead.tile += p.WR;
+            ahead.codes += tile_codes;
+            ahead.scales += tile_scales;
+        } else {
+            ahead.t = 0;
+            if (++ahead.piece < p.pieces) {
+                ahead.tile -= (count - 1) * p.WR;
+                ahead.codes += kPC * 64 - (count - 1) * tile_codes;
+                ahead.scales += kPC * SB - (count - 1) * tile_scales;
+            } else {
+                ahead.piece = 0;
+                ahead.group += kGroup;
+                ahead.tile += p.WR;
+                ahead.codes += tile_codes - (p.pieces - 1) * kPC * 64;
+                ahead.scales += tile_scales - (p.pieces - 1) * kPC * SB;
+            }
+        }
         return raw;
     };
     auto stage_x = [&](int piece, int slot) {
@@ -99,17 +118,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
             auto src = [&](int m) { return p.x + m * p.ldx + at * kChunk; };
             RawBf16 first_tokens;
             first_tokens.load(p.M, nch, lane, src);
-            stage_tokens<FMT>(xs + slot * p.M * kTokenBytes, inv + slot * p.M, first_tokens, p.M, nch, lane, src);
+            stage_tokens<FMT>(xs + slot * p.M * kTokenBytes, inv + slot * 8 * NT, first_tokens, p.M, nch, lane, src);
         }
     };
 
-    Cursor ahead = {0, 0, 0};
     uint2 raw[D - 1];
 #pragma unroll
-    for (int i = 0; i < D - 1; ++i) {
-        raw[i] = issue(ahead, i);
-        advance(ahead);
-    }
+    for (int i = 0; i < D - 1; ++i) raw[i] = issue(i);
     if (p.pdl) {
         ptx::griddep_launch_dependents();
         ptx::griddep_wait();
@@ -120,45 +135,32 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
     int slot = 0;
     for (int group = 0; group < steps; group += kGroup) {
         const int count = min(kGroup, steps - group);
-        float tot[kGroup][NT][4] = {};
+        float tot[kGroup][1][NT][4] = {};
         for (int piece = 0; piece < p.pieces; ++piece) {
             if (!p.resident) stage_x(piece, 0);
             const int nch = min(last - first - piece * kPC, kPC), kept_at = p.resident ? piece : 0;
-            for (int t = 0; t < count; ++t) {
+#pragma unroll
+            for (int t = 0; t < kGroup; ++t) {
+                if (t >= count) break;
                 const uint2 cur = raw[0];
 #pragma unroll
                 for (int i = 0; i + 2 < D; ++i) raw[i] = raw[i + 1];
-                raw[D - 2] = issue(ahead, slot == 0 ? D - 1 : slot - 1);
-                advance(ahead);
+                raw[D - 2] = issue(slot == 0 ? D - 1 : slot - 1);
                 if (nch > 0) {
                     const float back = store_scales<FMT, GP>(table, cur, lane);
                     cp_async_wait<D - 1>();
                     __syncwarp();
-                    float acc[NT][4];
-                    stage_mma<FMT, GP, NT>(acc, codes + slot * kCodeBytes, table, xs + kept_at * p.M * kTokenBytes,
-                                           inv + kept_at * p.M, back, p.M, nch, lane);
-#pragma unroll
-                    for (int u = 0; u < kGroup; ++u)
-                        if (u == t)
-#pragma unroll
-                            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) tot[u][j][i] += acc[j][i];
+                    stage_mma<FMT, GP, NT, 1>(tot[t], codes + slot * kCodeBytes, table, xs + kept_at * p.M * kTokenBytes,
+                                              inv + kept_at * 8 * NT, back, p.M, nch, lane);
                 }
                 __syncwarp();  // the slot, the table and x are rewritten by later stages
                 slot = slot + 1 == D ? 0 : slot + 1;
             }
         }
-        // [warp][tile of the group][row][token]
-        float* r = reinterpret_cast<float*>(codes + red_at) + (lane >> 2) * 8 * NT + 2 * (lane & 3);
+        // [warp][tile of the group][token][row]
 #pragma unroll
         for (int u = 0; u < kGroup; ++u)
-            if (u < count)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    *reinterpret_cast<float2*>(r + u * kTileRows * 8 * NT + 8 * j) = make_float2(tot[u][j][0], tot[u][j][1]);
-                    *reinterpret_cast<float2*>(r + (u * kTileRows + 8) * 8 * NT + 8 * j) = make_float2(tot[u][j][2], tot[u][j][3]);
-                }
+            if (u < count) store_sums<NT>(reinterpret_cast<float*>(codes + red_at + u * kSumBytes<NT>), tot[u][0], lane);
         __syncthreads();
         const int rows = count * p.WR * kTileRows;
         const int64_t row0 = static_cast<int64_t>(t0 + group * p.WR) * kTileRows;
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
             const int m = o / rows, rr = o - m * rows;
             if (row0 + rr < row_end) {
                 const int tile = rr / kTileRows, u = tile / p.WR, w0 = (tile - u * p.WR) * p.WK;
-                const uint8_t* s = smem + w0 * mine_bytes + red_at + ((u * kTileRows + rr % kTileRows) * 8 * NT + m) * 4;
+                const uint8_t* s = smem + w0 * mine_bytes + red_at + u * kSumBytes<NT> + (m * kSumPitch + rr % kTileRows) * 4;
                 float v = *reinterpret_cast<const float*>(s);
                 for (int k = 1; k < p.WK; ++k) v += *reinterpret_cast<const float*>(s + k * mine_bytes);
                 p.y[m * p.ldy + row0 + rr] = to_bf16(v);

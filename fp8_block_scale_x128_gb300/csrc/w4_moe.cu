@@ -4,7 +4,7 @@
 //   a = silu(h_gate) * h_up          (fp32, kept in the workspace)
 //   y[m] = bf16(sum over s, in slot order, of tw[m, s] * (a . w2[e]^T))
 //
-// 1. gate/up: items of (expert, up to 8 of its pairs, JT x 16 gate rows and the
+// 1. gate/up: items of (expert, up to 8 of its pairs, 16 gate rows and the 16
 //    up rows that go with them); the 8 warps of a block split H, their sums are
 //    added in warp order and the activation applied to the whole sum.
 // 2. down: a block owns 16 rows of the output for every token, its warps deal
@@ -137,32 +137,30 @@ __device__ Lists build_lists(const MoeParams& p, int batch, uint8_t* mem, int* c
     return L;
 }
 
-constexpr int kDepth = 3;  // stages of a warp's ring
-
-// Bytes of a warp: the ring, the scale table, a stage of tokens with its
-// inverse scales (whose place the gate/up sums take, red bytes).
-template <int GP>
+// Bytes of a warp: a ring of D stages of T tiles, their scale table, a stage of
+// tokens with its inverse scales (whose place the gate/up sums take, red bytes).
+template <int GP, int D, int T>
 __host__ __device__ constexpr int warp_bytes(int n, int red) {
     const int x = n * kTokenBytes;
-    return kDepth * kCodeBytes + kTableBytes<GP> + 32 + (x > red ? x : red);
+    return D * T * kCodeBytes + T * kTableBytes<GP> + 32 + (x > red ? x : red);
 }
 
 // ---- 1. gate / up ------------------------------------------------------------
-template <int JT>
-constexpr int kUpRed = 2 * JT * kTileRows * kMaxBatch * 4;  // of a warp
+constexpr int kUpDepth = 2;
+constexpr int kUpRed = 2 * kSumBytes<1>;  // of a warp
 
-template <int FMT, int GP, int JT>
+template <int FMT, int GP>
 __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_constant__ MoeParams p, int batch) {
-    constexpr int SB = Format<FMT, GP>::kScaleBytes, D = kDepth;
+    constexpr int SB = Format<FMT, GP>::kScaleBytes, D = kUpDepth, kSlot = 2 * kCodeBytes;
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int P = p.M * p.S;
     uint8_t* base = smem + lists_bytes(P);
-    const int mine_bytes = warp_bytes<GP>(min(P, batch), kUpRed<JT>);
-    uint8_t* codes = base + warp * mine_bytes;
-    float* table = reinterpret_cast<float*>(codes + D * kCodeBytes);
-    float* inv = reinterpret_cast<float*>(codes + D * kCodeBytes + kTableBytes<GP>);
-    constexpr int kXsAt = D * kCodeBytes + kTableBytes<GP> + 32;
+    const int mine_bytes = warp_bytes<GP, D, 2>(min(P, batch), kUpRed);
+    uint8_t* codes = base + warp * mine_bytes;  // [D][gate, up]
+    float* table = reinterpret_cast<float*>(codes + D * kSlot);
+    float* inv = reinterpret_cast<float*>(codes + D * kSlot + 2 * kTableBytes<GP>);
+    constexpr int kXsAt = D * kSlot + 2 * kTableBytes<GP> + 32;
     uint8_t* xs = codes + kXsAt;
     const Lists L = build_lists(p, batch, smem, reinterpret_cast<int*>(base));
     ptx::griddep_launch_dependents();
@@ -170,35 +168,43 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
     const int chunks = p.H / kChunk;
     const int first = warp * chunks / kWarps, last = (warp + 1) * chunks / kWarps;
     const int pieces = ((chunks + kWarps - 1) / kWarps + kPC - 1) / kPC;
-    const int per = p.I / (JT * kTileRows), items = L.entries * per;
+    const int per = p.I / kTileRows, items = L.entries * per;
     const int64_t ldc = p.H / 2, lds = static_cast<int64_t>(chunks) * SB;
+    const int64_t up_codes = p.I * ldc, up_scales = p.I * lds;  // from a gate tile to its up tile
 
-    // a warp's stages: the items of the block, in an item the pieces of the
-    // slice, in a piece the JT gate tiles and the JT up tiles
+    // a warp's stages: the items of the block, in an item the pieces of the slice
     struct Cursor {
-        int item, piece, t;
+        int item, piece;
+        const uint8_t *codes, *scales;  // this lane's, of the gate tile
     };
-    auto advance = [&](Cursor& c) {
-        if (++c.t == 2 * JT) {
-            c.t = 0;
-            if (++c.piece == pieces) c.piece = 0, c.item += gridDim.x;
-        }
+    Cursor ahead = {static_cast<int>(blockIdx.x), 0, nullptr, nullptr};
+    auto locate = [&]() {
+        if (ahead.item >= items) return;
+        const int entry = ahead.item / per, j = ahead.item - entry * per;
+        const int64_t row = static_cast<int64_t>(L.expert[entry]) * 2 * p.I + j * kTileRows;
+        ahead.codes = p.w13 + (row + (lane >> 3)) * ldc + first * 64 + (lane & 7) * 16;
+        ahead.scales = p.s13 + (row + (lane >> 1)) * lds + (first + (lane & 1)) * SB;
     };
-    auto issue = [&](const Cursor& c, int slot) {
-        uint2 raw = make_uint2(0, 0);
-        const int at = first + c.piece * kPC, nch = min(last - at, kPC);
-        if (c.item < items && nch > 0) {
-            const int entry = c.item / per, j = c.item - entry * per;
-            const int64_t row = static_cast<int64_t>(L.expert[entry]) * 2 * p.I + (c.t / JT) * p.I + (j * JT + c.t % JT) * kTileRows;
-            load_codes(codes + slot * kCodeBytes, p.w13 + row * ldc + at * 64, ldc, kTileRows, nch, lane);
-            raw = load_scales<FMT, GP>(p.s13 + row * lds + at * SB, lds, kTileRows, nch, lane);
+    auto issue = [&](int slot, uint2 (&raw)[2]) {
+        const int nch = min(last - first - ahead.piece * kPC, kPC);
+        if (ahead.item < items && nch > 0) {
+            load_codes(codes + slot * kSlot, ahead.codes, ldc, kTileRows - 1, nch, lane);
+            load_codes(codes + slot * kSlot + kCodeBytes, ahead.codes + up_codes, ldc, kTileRows - 1, nch, lane);
+            raw[0] = load_scales<FMT, GP>(ahead.scales, nch, lane);
+            raw[1] = load_scales<FMT, GP>(ahead.scales + up_scales, nch, lane);
         }
         cp_async_commit();
-        return raw;
+        if (++ahead.piece < pieces) {
+            ahead.codes += kPC * 64;
+            ahead.scales += kPC * SB;
+        } else {
+            ahead.piece = 0;
+            ahead.item += gridDim.x;
+            locate();
+        }
     };
-    auto source = [&](int item, int piece) {
-        const int pf = L.first[item / per];
-        const int16_t* pairs = L.pairs + pf;
+    auto source = [&](int entry, int piece) {
+        const int16_t* pairs = L.pairs + L.first[entry];
         const uint16_t* x = p.x + (first + piece * kPC) * kChunk;
         const int64_t ldx = p.ldx;
         const int S = p.S;
@@ -207,85 +213,84 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
     RawBf16 tokens;
     auto load_tokens = [&](int item, int piece) {
         const int nch = min(last - first - piece * kPC, kPC);
-        if (item < items && nch > 0) tokens.load(L.n[item / per], nch, lane, source(item, piece));
+        if (item < items && nch > 0) tokens.load(L.n[item / per], nch, lane, source(item / per, piece));
     };
 
-    Cursor ahead = {static_cast<int>(blockIdx.x), 0, 0};
-    uint2 raw[D - 1];
+    locate();
+    uint2 raw[D - 1][2];
 #pragma unroll
-    for (int i = 0; i < D - 1; ++i) {
-        raw[i] = issue(ahead, i);
-        advance(ahead);
-    }
+    for (int i = 0; i < D - 1; ++i) issue(i, raw[i]);
     load_tokens(blockIdx.x, 0);
     int slot = 0;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const int entry = item / per, j = item - entry * per;
         const int n = L.n[entry], pf = L.first[entry];
-        float tot[2 * JT][4] = {};
+        float tot[2][1][4] = {};
         for (int piece = 0; piece < pieces; ++piece) {
             const int nch = min(last - first - piece * kPC, kPC);
-            if (nch > 0) stage_tokens<FMT>(xs, inv, tokens, n, nch, lane, source(item, piece));
-            if (piece + 1 < pieces)
-                load_tokens(item, piece + 1);
-            else
+            const uint2 gate = raw[0][0], up = raw[0][1];
+#pragma unroll
+            for (int i = 0; i + 2 < D; ++i) raw[i][0] = raw[i + 1][0], raw[i][1] = raw[i + 1][1];
+            issue(slot == 0 ? D - 1 : slot - 1, raw[D - 2]);
+            if (nch > 0) {
+                stage_tokens<FMT>(xs, inv, tokens, n, nch, lane, source(entry, piece));
+                if (piece + 1 < pieces)
+                    load_tokens(item, piece + 1);
+                else
+                    load_tokens(item + gridDim.x, 0);
+                const float back = store_scales<FMT, GP>(table, gate, up, lane);
+                cp_async_wait<D - 1>();
+                __syncwarp();
+                stage_mma<FMT, GP, 1, 2>(tot, codes + slot * kSlot, table, xs, inv, back, n, nch, lane);
+            } else if (piece + 1 == pieces) {
                 load_tokens(item + gridDim.x, 0);
-#pragma unroll
-            for (int t = 0; t < 2 * JT; ++t) {
-                const uint2 cur = raw[0];
-#pragma unroll
-                for (int i = 0; i + 2 < D; ++i) raw[i] = raw[i + 1];
-                raw[D - 2] = issue(ahead, slot == 0 ? D - 1 : slot - 1);
-                advance(ahead);
-                if (nch > 0) {
-                    const float back = store_scales<FMT, GP>(table, cur, lane);
-                    cp_async_wait<D - 1>();
-                    __syncwarp();
-                    float acc[1][4];
-                    stage_mma<FMT, GP, 1>(acc, codes + slot * kCodeBytes, table, xs, inv, back, n, nch, lane);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tot[t][i] += acc[0][i];
-                }
-                __syncwarp();  // the slot, the table and the tokens are rewritten by later stages
-                slot = slot + 1 == D ? 0 : slot + 1;
             }
+            __syncwarp();  // the slot, the table and the tokens are rewritten by later stages
+            slot = slot + 1 == D ? 0 : slot + 1;
         }
-        // [warp][tile][row][pair]
-        float* r = reinterpret_cast<float*>(xs) + (lane >> 2) * kMaxBatch + 2 * (lane & 3);
-#pragma unroll
-        for (int t = 0; t < 2 * JT; ++t) {
-            *reinterpret_cast<float2*>(r + t * kTileRows * kMaxBatch) = make_float2(tot[t][0], tot[t][1]);
-            *reinterpret_cast<float2*>(r + (t * kTileRows + 8) * kMaxBatch) = make_float2(tot[t][2], tot[t][3]);
-        }
+        // [warp][gate, up][pair][row]
+        store_sums<1>(reinterpret_cast<float*>(xs), tot[0], lane);
+        store_sums<1>(reinterpret_cast<float*>(xs + kSumBytes<1>), tot[1], lane);
         __syncthreads();
-        for (int o = threadIdx.x; o < n * JT * kTileRows; o += kThreads) {
-            const int i = o / (JT * kTileRows), row = o - i * JT * kTileRows;
-            const uint8_t* s = base + kXsAt + (row * kMaxBatch + i) * 4;
+        for (int o = threadIdx.x; o < n * kTileRows; o += kThreads) {
+            const int i = o / kTileRows, row = o % kTileRows;
+            const uint8_t* s = base + kXsAt + (i * kSumPitch + row) * 4;
             float g = 0.0f, v = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 g += *reinterpret_cast<const float*>(s + w * mine_bytes);
-                v += *reinterpret_cast<const float*>(s + w * mine_bytes + JT * kTileRows * kMaxBatch * 4);
+                v += *reinterpret_cast<const float*>(s + w * mine_bytes + kSumBytes<1>);
             }
-            p.a[static_cast<int64_t>(L.pairs[pf + i]) * p.I + j * JT * kTileRows + row] = g / (1.0f + expf(-g)) * v;
+            p.a[static_cast<int64_t>(L.pairs[pf + i]) * p.I + j * kTileRows + row] = g / (1.0f + expf(-g)) * v;
         }
         __syncthreads();  // the sums' place is rewritten by the next item
     }
 }
 
 // ---- 2. down -----------------------------------------------------------------
+constexpr int kDownDepth = 3;
+
+// the pairs' products for 16 rows, and their routing weights
+__host__ __device__ constexpr int out_bytes(int P) { return (P * (kTileRows + 1) * 4 + 15) / 16 * 16; }
+
 template <int FMT, int GP>
 __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_constant__ MoeParams p, int batch) {
-    constexpr int SB = Format<FMT, GP>::kScaleBytes, D = kDepth;
+    constexpr int SB = Format<FMT, GP>::kScaleBytes, D = kDownDepth;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = p.M * p.S;
     float* out = reinterpret_cast<float*>(smem + lists_bytes(P));  // [P][16]
-    uint8_t* base = smem + lists_bytes(P) + P * kTileRows * 4;
-    uint8_t* codes = base + warp * warp_bytes<GP>(min(P, batch), 0);
+    uint8_t* base = smem + lists_bytes(P) + out_bytes(P);
+    uint8_t* codes = base + warp * warp_bytes<GP, kDownDepth, 1>(min(P, batch), 0);
     float* table = reinterpret_cast<float*>(codes + D * kCodeBytes);
     float* inv = reinterpret_cast<float*>(codes + D * kCodeBytes + kTableBytes<GP>);
     uint8_t* xs = codes + D * kCodeBytes + kTableBytes<GP> + 32;
+    // the pairs' routing weights, 0 for an invalid id
+    float* weight = out + P * kTileRows;
+    for (int q = tid; q < P; q += kThreads) {
+        const int e = p.ids[q];
+        weight[q] = e >= 0 && e < p.E ? p.tw[q] : 0.0f;
+    }
     const Lists L = build_lists(p, batch, smem, reinterpret_cast<int*>(base));
 
     const int chunks = p.I / kChunk, pieces = (chunks + kPC - 1) / kPC;
@@ -296,22 +301,31 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
     // in an entry the pieces of I
     struct Cursor {
         int tile, entry, piece;
+        const uint8_t *codes, *scales;  // this lane's
     };
-    auto advance = [&](Cursor& c) {
-        if (++c.piece == pieces) {
-            c.piece = 0;
-            if ((c.entry += kWarps) >= L.entries) c.entry = warp, c.tile += gridDim.x;
-        }
+    Cursor ahead = {static_cast<int>(blockIdx.x), warp, 0, nullptr, nullptr};
+    auto locate = [&]() {
+        if (ahead.tile >= tiles || ahead.entry >= L.entries) return;
+        const int64_t row = static_cast<int64_t>(L.expert[ahead.entry]) * p.H + ahead.tile * kTileRows;
+        ahead.codes = p.w2 + (row + (lane >> 3)) * ldc + (lane & 7) * 16;
+        ahead.scales = p.s2 + (row + (lane >> 1)) * lds + (lane & 1) * SB;
     };
-    auto issue = [&](const Cursor& c, int slot) {
+    auto issue = [&](int slot) {
         uint2 raw = make_uint2(0, 0);
-        if (c.tile < tiles && c.entry < L.entries) {
-            const int at = c.piece * kPC, nch = min(chunks - at, kPC);
-            const int64_t row = static_cast<int64_t>(L.expert[c.entry]) * p.H + c.tile * kTileRows;
-            load_codes(codes + slot * kCodeBytes, p.w2 + row * ldc + at * 64, ldc, kTileRows, nch, lane);
-            raw = load_scales<FMT, GP>(p.s2 + row * lds + at * SB, lds, kTileRows, nch, lane);
+        if (ahead.tile < tiles && ahead.entry < L.entries) {
+            const int nch = min(chunks - ahead.piece * kPC, kPC);
+            load_codes(codes + slot * kCodeBytes, ahead.codes, ldc, kTileRows - 1, nch, lane);
+            raw = load_scales<FMT, GP>(ahead.scales, nch, lane);
         }
         cp_async_commit();
+        if (++ahead.piece < pieces) {
+            ahead.codes += kPC * 64;
+            ahead.scales += kPC * SB;
+        } else {
+            ahead.piece = 0;
+            if ((ahead.entry += kWarps) >= L.entries) ahead.entry = warp, ahead.tile += gridDim.x;
+            locate();
+        }
         return raw;
     };
     auto source = [&](int entry, int piece) {
@@ -325,13 +339,10 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
         if (entry < L.entries) tokens.load(L.n[entry], min(chunks - piece * kPC, kPC), lane, source(entry, piece));
     };
 
-    Cursor ahead = {static_cast<int>(blockIdx.x), warp, 0};
+    locate();
     uint2 raw[D - 1];
 #pragma unroll
-    for (int i = 0; i < D - 1; ++i) {
-        raw[i] = issue(ahead, i);
-        advance(ahead);
-    }
+    for (int i = 0; i < D - 1; ++i) raw[i] = issue(i);
     ptx::griddep_wait();
     load_tokens(warp, 0);
     int slot = 0;
@@ -340,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
         __syncthreads();
         for (int entry = warp; entry < L.entries; entry += kWarps) {
             const int n = L.n[entry], pf = L.first[entry];
-            float tot[4] = {};
+            float tot[1][1][4] = {};
             for (int piece = 0; piece < pieces; ++piece) {
                 const int nch = min(chunks - piece * kPC, kPC);
                 stage_tokens<FMT>(xs, inv, tokens, n, nch, lane, source(entry, piece));
@@ -351,15 +362,11 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
                 const uint2 cur = raw[0];
 #pragma unroll
                 for (int i = 0; i + 2 < D; ++i) raw[i] = raw[i + 1];
-                raw[D - 2] = issue(ahead, slot == 0 ? D - 1 : slot - 1);
-                advance(ahead);
+                raw[D - 2] = issue(slot == 0 ? D - 1 : slot - 1);
                 const float back = store_scales<FMT, GP>(table, cur, lane);
                 cp_async_wait<D - 1>();
                 __syncwarp();
-                float acc[1][4];
-                stage_mma<FMT, GP, 1>(acc, codes + slot * kCodeBytes, table, xs, inv, back, n, nch, lane);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tot[i] += acc[0][i];
+                stage_mma<FMT, GP, 1, 1>(tot, codes + slot * kCodeBytes, table, xs, inv, back, n, nch, lane);
                 __syncwarp();  // the slot, the table and the tokens are rewritten by later stages
                 slot = slot + 1 == D ? 0 : slot + 1;
             }
@@ -368,18 +375,16 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
             for (int h = 0; h < 2; ++h)
                 if (col + h < n) {
                     float* o = out + L.pairs[pf + col + h] * kTileRows + row;
-                    o[0] = tot[h];
-                    o[8] = tot[2 + h];
+                    o[0] = tot[0][0][h];
+                    o[8] = tot[0][0][2 + h];
                 }
         }
         __syncthreads();
         for (int o = tid; o < p.M * kTileRows; o += kThreads) {
             const int m = o / kTileRows, row = o % kTileRows;
             float v = 0.0f;
-            for (int s = 0; s < p.S; ++s) {
-                const int q = m * p.S + s, e = p.ids[q];
-                if (e >= 0 && e < p.E) v = fmaf(p.tw[q], out[q * kTileRows + row], v);
-            }
+#pragma unroll 4
+            for (int q = m * p.S; q < (m + 1) * p.S; ++q) v = fmaf(weight[q], out[q * kTileRows + row], v);
             p.y[static_cast<int64_t>(m) * p.H + tile * kTileRows + row] = to_bf16(v);
         }
         __syncthreads();  // out is cleared for the next tile
@@ -400,17 +405,28 @@ cudaError_t launch_pdl(void (*kernel)(MoeParams, int), const MoeParams& p, int b
     return cudaLaunchKernelEx(&cfg, kernel, p, batch);
 }
 
-template <int FMT, int GP, int JT>
+// The pairs of an entry: half as many where that lets two blocks share a
+// multiprocessor.
+template <typename F>
+int batch_of(F&& bytes) {
+    constexpr int kHalf = kMaxSmShared / 2 - 1024 - 64;  // a block's reserved and static shared memory
+    return bytes(kMaxBatch) > kHalf && bytes(kMaxBatch / 2) <= kHalf ? kMaxBatch / 2 : kMaxBatch;
+}
+
+template <int FMT, int GP>
 cudaError_t launch_up(const MoeParams& p, int sm_count, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_shared(moe_w4_up_kernel<FMT, GP, JT>, allowed);
+    cudaError_t e = allow_shared(moe_w4_up_kernel<FMT, GP>, allowed);
     if (e != cudaSuccess) return e;
-    const int P = p.M * p.S, batch = kMaxBatch;
-    const int smem = lists_bytes(P) + max(counts_bytes(p.E), kWarps * warp_bytes<GP>(min(P, batch), kUpRed<JT>));
+    const int P = p.M * p.S;
+    auto bytes = [&](int batch) {
+        return lists_bytes(P) + max(counts_bytes(p.E), kWarps * warp_bytes<GP, kUpDepth, 2>(min(P, batch), kUpRed));
+    };
+    const int batch = batch_of(bytes), smem = bytes(batch);
     const int per_sm = min(2, kMaxSmShared / (smem + 1024));
-    const int64_t most = static_cast<int64_t>(P) * (p.I / (JT * kTileRows));
+    const int64_t most = static_cast<int64_t>(P) * (p.I / kTileRows);
     const int grid = static_cast<int>(min(most, static_cast<int64_t>(sm_count) * per_sm));
-    return launch_pdl(moe_w4_up_kernel<FMT, GP, JT>, p, batch, grid, smem, false, stream);
+    return launch_pdl(moe_w4_up_kernel<FMT, GP>, p, batch, grid, smem, false, stream);
 }
 
 template <int FMT, int GP>
@@ -420,11 +436,9 @@ cudaError_t launch_down(const MoeParams& p, int sm_count, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int P = p.M * p.S;
     auto bytes = [&](int batch) {
-        return lists_bytes(P) + P * kTileRows * 4 + max(counts_bytes(p.E), kWarps * warp_bytes<GP>(min(P, batch), 0));
+        return lists_bytes(P) + out_bytes(P) + max(counts_bytes(p.E), kWarps * warp_bytes<GP, kDownDepth, 1>(min(P, batch), 0));
     };
-    // half the pairs of an entry where that lets two blocks share a multiprocessor
-    const int batch = bytes(kMaxBatch) + 1024 > kMaxSmShared / 2 && bytes(kMaxBatch / 2) + 1024 <= kMaxSmShared / 2 ? kMaxBatch / 2 : kMaxBatch;
-    const int smem = bytes(batch), per_sm = min(2, kMaxSmShared / (smem + 1024));
+    const int batch = batch_of(bytes), smem = bytes(batch), per_sm = min(2, kMaxSmShared / (smem + 1024));
     return launch_pdl(moe_w4_down_kernel<FMT, GP>, p, batch, min(p.H / kTileRows, sm_count * per_sm), smem, true, stream);
 }
 
@@ -453,7 +467,7 @@ cudaError_t launch_moe_w4(const MoeW4Args& a, cudaStream_t stream) {
     p.I = a.I;
     p.E = a.E;
     return dispatch_format(a.format, a.group, [&](auto fmt, auto gp) {
-        const cudaError_t e = launch_up<fmt(), gp(), 1>(p, a.sm_count, stream);
+        const cudaError_t e = launch_up<fmt(), gp()>(p, a.sm_count, stream);
         return e != cudaSuccess ? e : launch_down<fmt(), gp()>(p, a.sm_count, stream);
     });
 }
