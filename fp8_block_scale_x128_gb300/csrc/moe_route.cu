@@ -5,9 +5,12 @@
 // token, by latency: 16 expert rows x one slice of H per warp (bf16 matrix
 // instructions straight from global memory, each operand read as 16-byte words
 // in a k order both share), the slices of a block summed in warp order, those
-// of several blocks through the workspace.  The last block to arrive (a
-// counter that it also resets) sums them in slice order and selects, one warp
-// per token; no block waits for another.
+// of several blocks through the workspace, in slice order.  One warp selects
+// for a token.  Up to kOneLaunchM tokens that is done by the last block to
+// arrive (a counter that it also resets; no block waits for another), which
+// saves a launch; with more tokens one block's warps would take them in turn,
+// so a second kernel, a block per token, selects (programmatic dependent
+// launch).
 //
 // The order of the chosen experts is decided by fp32 logits unless two of them
 // (or the last chosen and the first left out) are within 2^-16 of the largest
@@ -23,7 +26,7 @@ using namespace w4;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTok = 32;  // tokens of one pass: 4 MMA column tiles
+constexpr int kOneLaunchM = kWarps;  // a warp per token in the last block
 constexpr size_t kHeader = 256;  // workspace: the arrival counter, then the partial logits
 constexpr int kTargetBlocks = 152;
 constexpr int kMaxCand = 64;
@@ -84,30 +87,43 @@ __device__ double exact_logit(const RouteParams& p, int m, int e, int lane) {
     return d;
 }
 
+// A warp's scratch.
 struct Select {
-    float value[kWarps][FP8BS_ROUTE_MAX_K + 1];
-    int16_t expert[kWarps][FP8BS_ROUTE_MAX_K + 1];
-    double cand_value[kWarps][kMaxCand];
-    int16_t cand[kWarps][kMaxCand];
+    double cand_value[kMaxCand];
+    float value[FP8BS_ROUTE_MAX_K + 1];
+    int16_t expert[FP8BS_ROUTE_MAX_K + 1];
+    int16_t cand[kMaxCand];
 };
 
 // The k + 1 largest of a token's logits in order, by one warp.  v[j]: expert
 // lane + 32 j.
 template <int PER>
-__device__ void select_token(const RouteParams& p, Select& sel, int m, int warp, int lane) {
+__device__ void select_token(const RouteParams& p, Select& sel, int m, int lane) {
     float v[PER];
     uint32_t key[PER];
     uint32_t top_abs = 0;
+    const float* part = p.part + static_cast<int64_t>(m) * p.rows16 + lane;
+    const int64_t pitch = static_cast<int64_t>(p.M) * p.rows16;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) v[j] = 0.0f;
+    // four slices' loads in flight together, added in slice order
+    for (int ks = 0; ks < p.KS; ks += 4) {
+        float u[4][PER];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                u[i][j] = ks + i < p.KS && lane + 32 * j < p.E ? __ldcg(part + (ks + i) * pitch + 32 * j) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < PER; ++j) v[j] += u[i][j];
+    }
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-        const int e = lane + 32 * j;
-        v[j] = 0.0f;
-        key[j] = 0;
-        if (e < p.E) {
-            for (int ks = 0; ks < p.KS; ++ks) v[j] += __ldcg(p.part + (static_cast<int64_t>(ks) * p.M + m) * p.rows16 + e);
-            key[j] = order_key(v[j]);
-            top_abs = max(top_abs, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-        }
+        const bool in = lane + 32 * j < p.E;
+        key[j] = in ? order_key(v[j]) : 0;
+        if (in) top_abs = max(top_abs, __float_as_uint(v[j]) & 0x7FFFFFFFu);
     }
     top_abs = __reduce_max_sync(0xFFFFFFFFu, top_abs);
     uint32_t best = 0;
@@ -128,15 +144,15 @@ __device__ void select_token(const RouteParams& p, Select& sel, int m, int warp,
 #pragma unroll
             for (int j = 0; j < PER; ++j)
                 if (lane + 32 * j == best_e) {
-                    sel.value[warp][r] = v[j];
-                    sel.expert[warp][r] = static_cast<int16_t>(best_e);
+                    sel.value[r] = v[j];
+                    sel.expert[r] = static_cast<int16_t>(best_e);
                     key[j] = 0;
                 }
             rescan();
         }
     }
     __syncwarp();
-    const float largest = sel.value[warp][0];
+    const float largest = sel.value[0];
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < PER; ++j)
@@ -147,9 +163,9 @@ __device__ void select_token(const RouteParams& p, Select& sel, int m, int warp,
     // near ties: order them by their exact values
     const float tol = top_abs < 0x7F800000u ? __uint_as_float(top_abs) * 0x1p-16f : 0.0f;
     bool close = false;
-    for (int r = lane; r + 1 < kk; r += 32) close |= sel.value[warp][r] - sel.value[warp][r + 1] < tol;
+    for (int r = lane; r + 1 < kk; r += 32) close |= sel.value[r] - sel.value[r + 1] < tol;
     if (__any_sync(0xFFFFFFFFu, close)) {
-        const float floor_v = sel.value[warp][p.k - 1] - tol;
+        const float floor_v = sel.value[p.k - 1] - tol;
         int n = 0;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
@@ -157,8 +173,8 @@ __device__ void select_token(const RouteParams& p, Select& sel, int m, int warp,
             const uint32_t bal = __ballot_sync(0xFFFFFFFFu, in);
             const int at = n + __popc(bal & ((1u << lane) - 1u));
             if (in && at < kMaxCand) {
-                sel.cand[warp][at] = static_cast<int16_t>(lane + 32 * j);
-                sel.cand_value[warp][at] = v[j];
+                sel.cand[at] = static_cast<int16_t>(lane + 32 * j);
+                sel.cand_value[at] = v[j];
             }
             n += __popc(bal);
         }
@@ -168,28 +184,28 @@ __device__ void select_token(const RouteParams& p, Select& sel, int m, int warp,
             for (int i = 0; i < n; ++i) {
                 bool near = false;
                 for (int o = lane; o < n; o += 32)
-                    near |= o != i && fabs(sel.cand_value[warp][i] - sel.cand_value[warp][o]) < tol;
+                    near |= o != i && fabs(sel.cand_value[i] - sel.cand_value[o]) < tol;
                 if (__any_sync(0xFFFFFFFFu, near)) unclear |= uint64_t(1) << i;
             }
             __syncwarp();
             for (int i = 0; i < n; ++i)
                 if (unclear >> i & 1) {
-                    const double d = exact_logit(p, m, sel.cand[warp][i], lane);
-                    if (lane == 0) sel.cand_value[warp][i] = d;
+                    const double d = exact_logit(p, m, sel.cand[i], lane);
+                    if (lane == 0) sel.cand_value[i] = d;
                 }
             __syncwarp();
             // the candidates are in ascending blocks of 32 experts, not sorted: rank each one
             for (int i = lane; i < n; i += 32) {
-                const double a = sel.cand_value[warp][i];
-                const int e = sel.cand[warp][i];
+                const double a = sel.cand_value[i];
+                const int e = sel.cand[i];
                 int rank = 0;
                 for (int o = 0; o < n; ++o) {
-                    const double b = sel.cand_value[warp][o];
-                    rank += b > a || (b == a && sel.cand[warp][o] < e);
+                    const double b = sel.cand_value[o];
+                    rank += b > a || (b == a && sel.cand[o] < e);
                 }
                 if (rank < p.k) {
-                    sel.expert[warp][rank] = static_cast<int16_t>(e);
-                    sel.value[warp][rank] = static_cast<float>(a);
+                    sel.expert[rank] = static_cast<int16_t>(e);
+                    sel.value[rank] = static_cast<float>(a);
                 }
             }
             __syncwarp();
@@ -197,13 +213,13 @@ __device__ void select_token(const RouteParams& p, Select& sel, int m, int warp,
     }
 
     float chosen = 0.0f;
-    for (int r = lane; r < p.k; r += 32) chosen += expf(sel.value[warp][r] - largest);
+    for (int r = lane; r < p.k; r += 32) chosen += expf(sel.value[r] - largest);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) chosen += __shfl_xor_sync(0xFFFFFFFFu, chosen, off);
     const float denom = sum != sum ? sum : (p.renorm ? chosen : sum);
     for (int r = lane; r < p.k; r += 32) {
-        p.ids[m * p.S + r] = sel.expert[warp][r];
-        p.weights[m * p.S + r] = expf(sel.value[warp][r] - largest) / denom;
+        p.ids[m * p.S + r] = sel.expert[r];
+        p.weights[m * p.S + r] = expf(sel.value[r] - largest) / denom;
     }
     if (p.shared && lane == 0) {
         float g = 1.0f;
@@ -218,18 +234,29 @@ __device__ void select_token(const RouteParams& p, Select& sel, int m, int warp,
     __syncwarp();
 }
 
+__device__ void select_any(const RouteParams& p, Select& sel, int m, int lane) {
+    if (p.E <= 256)
+        select_token<8>(p, sel, m, lane);
+    else if (p.E <= 512)
+        select_token<16>(p, sel, m, lane);
+    else
+        select_token<FP8BS_ROUTE_MAX_E / 32>(p, sel, m, lane);
+}
+
+// NT: tiles of 8 tokens taken together (their operands are in flight together).
+template <int NT, bool LAST>
 __global__ void __launch_bounds__(kThreads) moe_route_kernel(const __grid_constant__ RouteParams p) {
-    __shared__ float red[kWarps][kTileRows][kTok + 1];
-    __shared__ Select sel;
-    __shared__ int is_last;
+    constexpr int kTok = 8 * NT, kPitch = kTok + 1;
+    __shared__ float red[kWarps][kTileRows][kPitch];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int tile = blockIdx.x / p.KS, ks = blockIdx.x - tile * p.KS;
     const int chunks = p.H / kChunk;
     const int r0 = min(tile * kTileRows + g, p.rows - 1), r1 = min(tile * kTileRows + g + 8, p.rows - 1);
     const uint16_t* w0 = p.w + static_cast<int64_t>(r0) * p.H + 8 * t;
     const uint16_t* w1 = p.w + static_cast<int64_t>(r1) * p.H + 8 * t;
+    if (!LAST) ptx::griddep_launch_dependents();
     for (int m0 = 0; m0 < p.M; m0 += kTok) {
-        float acc[kTok / 8][4] = {};
+        float acc[NT][4] = {};
         for (int c = ks * kWarps + warp; c < chunks; c += p.KS * kWarps) {
             uint4 a0[4], a1[4];
 #pragma unroll
@@ -238,14 +265,13 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(const __grid_consta
                 a1[i] = ptx::ld_global_v4(w1 + c * kChunk + 32 * i);
             }
 #pragma unroll
-            for (int j = 0; j < kTok / 8; ++j) {
-                if (m0 + 8 * j >= p.M) break;
-                const int m = min(m0 + 8 * j + g, p.M - 1);
-                const uint16_t* x = p.x + m * p.ldx + c * kChunk + 8 * t;
-                float part[4] = {};
+            for (int j = 0; j < NT; ++j) {
+                // columns past M repeat the last token and are not stored
+                const uint16_t* x = p.x + min(m0 + 8 * j + g, p.M - 1) * p.ldx + c * kChunk + 8 * t;
                 uint4 b[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) b[i] = *reinterpret_cast<const uint4*>(x + 32 * i);
+                float part[4] = {};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     mma16816_bf16(part, a0[i].x, a1[i].x, a0[i].y, a1[i].y, b[i].x, b[i].y);
@@ -256,7 +282,7 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(const __grid_consta
             }
         }
 #pragma unroll
-        for (int j = 0; j < kTok / 8; ++j) {
+        for (int j = 0; j < NT; ++j) {
             red[warp][g][8 * j + 2 * t] = acc[j][0];
             red[warp][g][8 * j + 2 * t + 1] = acc[j][1];
             red[warp][g + 8][8 * j + 2 * t] = acc[j][2];
@@ -271,22 +297,26 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(const __grid_consta
             for (int w = 0; w < kWarps; ++w) v += red[w][r][m];
             p.part[(static_cast<int64_t>(ks) * p.M + m0 + m) * p.rows16 + tile * kTileRows + r] = v;
         }
-        __threadfence();
         __syncthreads();
     }
-    if (threadIdx.x == 0) is_last = atomicAdd(p.counter, 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (!is_last) return;
-    __threadfence();
-    if (threadIdx.x == 0) *p.counter = 0;
-    for (int m = warp; m < p.M; m += kWarps) {
-        if (p.E <= 256)
-            select_token<8>(p, sel, m, warp, lane);
-        else if (p.E <= 512)
-            select_token<16>(p, sel, m, warp, lane);
-        else
-            select_token<FP8BS_ROUTE_MAX_E / 32>(p, sel, m, warp, lane);
+    if constexpr (LAST) {
+        __shared__ Select sel[kWarps];
+        __shared__ int is_last;
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) is_last = atomicAdd(p.counter, 1u) == gridDim.x - 1;
+        __syncthreads();
+        if (!is_last) return;
+        __threadfence();
+        if (threadIdx.x == 0) *p.counter = 0;
+        if (warp < p.M) select_any(p, sel[warp], warp, lane);
     }
+}
+
+__global__ void __launch_bounds__(32) moe_select_kernel(const __grid_constant__ RouteParams p) {
+    __shared__ Select sel;
+    ptx::griddep_wait();
+    select_any(p, sel, blockIdx.x, threadIdx.x);
 }
 
 }  // namespace
@@ -318,8 +348,28 @@ cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t stream) {
     p.renorm = a.renorm;
     p.shared = a.shared;
     const unsigned grid = static_cast<unsigned>(p.rows16 / kTileRows * p.KS);
-    moe_route_kernel<<<grid, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    if (a.M <= kOneLaunchM) {
+        moe_route_kernel<1, true><<<grid, kThreads, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
+    if (a.M <= 16)
+        moe_route_kernel<2, false><<<grid, kThreads, 0, stream>>>(p);
+    else if (a.M <= 32)
+        moe_route_kernel<4, false><<<grid, kThreads, 0, stream>>>(p);
+    else
+        moe_route_kernel<8, false><<<grid, kThreads, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.M));
+    cfg.blockDim = dim3(32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, moe_select_kernel, p);
 }
 
 }  // namespace fp8bs
