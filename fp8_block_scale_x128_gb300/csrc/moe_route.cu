@@ -13,7 +13,7 @@
 // launch).
 //
 // The order of the chosen experts is decided by fp32 logits unless two of them
-// (or the last chosen and the first left out) are within 2^-16 of the largest
+// (or the last chosen and the first left out) are within 2^-18 of the largest
 // logit: those are summed again with a compensated sum, which orders them as a
 // 64-bit sum would.
 #include "internal.cuh"
@@ -65,20 +65,36 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+__device__ __forceinline__ float key_value(uint32_t key) {
+    if (key == 1u) return __uint_as_float(0x7FC00000u);
+    return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
 // x[m] . w[e] with a compensated fp32 sum (products of two bf16 are exact in
 // fp32; each addition's rounding error is kept: D. E. Knuth's two-sum), the
 // lanes' sums joined in 64 bits.  Every lane returns it.
 __device__ double exact_logit(const RouteParams& p, int m, int e, int lane) {
     float s = 0.0f, c = 0.0f;
-    for (int k = 8 * lane; k < p.H; k += 256) {
-        float a[8], b[8];
-        unpack8(*reinterpret_cast<const uint4*>(p.x + m * p.ldx + k), a);
-        unpack8(*reinterpret_cast<const uint4*>(p.w + static_cast<int64_t>(e) * p.H + k), b);
+    const uint16_t *x = p.x + m * p.ldx, *w = p.w + static_cast<int64_t>(e) * p.H;
+    for (int k0 = 8 * lane; k0 < p.H; k0 += 4 * 256) {
+        uint4 xr[4], wr[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float v = __fmul_rn(a[i], b[i]), t = __fadd_rn(s, v), z = __fsub_rn(t, s);
-            c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(v, z)));
-            s = t;
+        for (int j = 0; j < 4; ++j) {
+            const int k = k0 + 256 * j;
+            xr[j] = wr[j] = make_uint4(0, 0, 0, 0);
+            if (k < p.H) xr[j] = *reinterpret_cast<const uint4*>(x + k), wr[j] = ptx::ld_global_v4(w + k);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a[8], b[8];
+            unpack8(xr[j], a);
+            unpack8(wr[j], b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float v = __fmul_rn(a[i], b[i]), t = __fadd_rn(s, v), z = __fsub_rn(t, s);
+                c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(v, z)));
+                s = t;
+            }
         }
     }
     double d = static_cast<double>(s) + static_cast<double>(c);
@@ -126,28 +142,41 @@ __device__ void select_token(const RouteParams& p, Select& sel, int m, int lane)
         if (in) top_abs = max(top_abs, __float_as_uint(v[j]) & 0x7FFFFFFFu);
     }
     top_abs = __reduce_max_sync(0xFFFFFFFFu, top_abs);
-    uint32_t best = 0;
-    int best_e = 0;
+    // every lane holds its best, the warp's best of them is taken round by round
+    uint32_t best;
+    int best_j;
     auto rescan = [&]() {
-        best = 0;
-        best_e = 0;
+        uint32_t m[PER];
+        int at[PER];
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (key[j] > best) best = key[j], best_e = lane + 32 * j;
+        for (int j = 0; j < PER; ++j) m[j] = key[j];
+#pragma unroll
+        for (int w = PER / 2; w > 0; w /= 2)
+#pragma unroll
+            for (int j = 0; j < w; ++j) m[j] = max(m[j], m[j + w]);
+        best = m[0];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) at[j] = key[j] == best ? j : PER;
+#pragma unroll
+        for (int w = PER / 2; w > 0; w /= 2)
+#pragma unroll
+            for (int j = 0; j < w; ++j) at[j] = min(at[j], at[j + w]);
+        best_j = at[0];
     };
     rescan();
     const int kk = min(p.k + 1, p.E);
     for (int r = 0; r < kk; ++r) {
         const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-        const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, best == top ? static_cast<uint32_t>(best_e) : 0xFFFFFFFFu);
-        if (best == top && static_cast<uint32_t>(best_e) == e) {
+        const uint32_t who = __ballot_sync(0xFFFFFFFFu, best == top);
+        int e = best_j * 32 + lane;
+        if (who & (who - 1))  // several lanes: the lowest expert of them
+            e = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, best == top ? static_cast<uint32_t>(e) : 0xFFFFFFFFu));
+        if (best == top && e == best_j * 32 + lane) {
+            sel.value[r] = key_value(top);
+            sel.expert[r] = static_cast<int16_t>(e);
 #pragma unroll
             for (int j = 0; j < PER; ++j)
-                if (lane + 32 * j == best_e) {
-                    sel.value[r] = v[j];
-                    sel.expert[r] = static_cast<int16_t>(best_e);
-                    key[j] = 0;
-                }
+                if (j == best_j) key[j] = 0;
             rescan();
         }
     }
@@ -161,7 +190,7 @@ __device__ void select_token(const RouteParams& p, Select& sel, int m, int lane)
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
 
     // near ties: order them by their exact values
-    const float tol = top_abs < 0x7F800000u ? __uint_as_float(top_abs) * 0x1p-16f : 0.0f;
+    const float tol = top_abs < 0x7F800000u ? __uint_as_float(top_abs) * 0x1p-18f : 0.0f;
     bool close = false;
     for (int r = lane; r + 1 < kk; r += 32) close |= sel.value[r] - sel.value[r + 1] < tol;
     if (__any_sync(0xFFFFFFFFu, close)) {
@@ -254,7 +283,8 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(const __grid_consta
     const int r0 = min(tile * kTileRows + g, p.rows - 1), r1 = min(tile * kTileRows + g + 8, p.rows - 1);
     const uint16_t* w0 = p.w + static_cast<int64_t>(r0) * p.H + 8 * t;
     const uint16_t* w1 = p.w + static_cast<int64_t>(r1) * p.H + 8 * t;
-    if (!LAST) ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     for (int m0 = 0; m0 < p.M; m0 += kTok) {
         float acc[NT][4] = {};
         for (int c = ks * kWarps + warp; c < chunks; c += p.KS * kWarps) {
@@ -316,6 +346,7 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(const __grid_consta
 __global__ void __launch_bounds__(32) moe_select_kernel(const __grid_constant__ RouteParams p) {
     __shared__ Select sel;
     ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     select_any(p, sel, blockIdx.x, threadIdx.x);
 }
 
@@ -347,29 +378,12 @@ cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t stream) {
     p.KS = k_splits(p.rows, a.H);
     p.renorm = a.renorm;
     p.shared = a.shared;
-    const unsigned grid = static_cast<unsigned>(p.rows16 / kTileRows * p.KS);
-    if (a.M <= kOneLaunchM) {
-        moe_route_kernel<1, true><<<grid, kThreads, 0, stream>>>(p);
-        return cudaGetLastError();
-    }
-    if (a.M <= 16)
-        moe_route_kernel<2, false><<<grid, kThreads, 0, stream>>>(p);
-    else if (a.M <= 32)
-        moe_route_kernel<4, false><<<grid, kThreads, 0, stream>>>(p);
-    else
-        moe_route_kernel<8, false><<<grid, kThreads, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.M));
-    cfg.blockDim = dim3(32);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, moe_select_kernel, p);
+    const int grid = p.rows16 / kTileRows * p.KS;
+    if (a.M <= kOneLaunchM) return launch_dependent(moe_route_kernel<1, true>, grid, kThreads, 0, stream, p);
+    const cudaError_t e = a.M <= 16   ? launch_dependent(moe_route_kernel<2, false>, grid, kThreads, 0, stream, p)
+                          : a.M <= 32 ? launch_dependent(moe_route_kernel<4, false>, grid, kThreads, 0, stream, p)
+                                      : launch_dependent(moe_route_kernel<8, false>, grid, kThreads, 0, stream, p);
+    return e != cudaSuccess ? e : launch_dependent(moe_select_kernel, a.M, 32, 0, stream, p);
 }
 
 }  // namespace fp8bs

@@ -469,6 +469,27 @@ cudaError_t allow_shared(K* kernel, std::atomic<uint64_t>& done) {
     return e;
 }
 
+// Every kernel of these files is launched with programmatic dependent launch:
+// it waits for its predecessor (griddep_wait) before it touches memory -- but
+// for weights that the caller says the predecessor does not write -- and lets
+// its successor start (launch_dependents) only after that wait, so that what a
+// successor reads before its own wait is complete up to the kernel before it.
+// Back-to-back calls overlap one call's start-up with the other's tail.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), int grid, int block, int smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(block));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace w4
 
 // Launchers (argument checks are done by the C ABI before these run).

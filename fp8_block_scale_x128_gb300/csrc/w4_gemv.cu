@@ -122,13 +122,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
         }
     };
 
+    if (!p.pdl) ptx::griddep_wait();
     uint2 raw[D - 1];
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) raw[i] = issue(i);
-    if (p.pdl) {
-        ptx::griddep_launch_dependents();
-        ptx::griddep_wait();
-    }
+    if (p.pdl) ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     if (p.resident)
         for (int q = 0; q < p.pieces; ++q) stage_x(q, q);
 
@@ -185,17 +184,7 @@ cudaError_t launch(const GemvParams& p, int sm_count, cudaStream_t stream) {
     cudaError_t e = allow_shared(gemv_w4_kernel<FMT, GP, NT, D>, allowed);
     if (e != cudaSuccess) return e;
     const int smem = kWarps * warp_bytes<GP, NT, D>(p.M, p.pieces, p.resident);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(min((p.tiles + p.WR - 1) / p.WR, sm_count)));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = p.pdl ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemv_w4_kernel<FMT, GP, NT, D>, p);
+    return launch_dependent(gemv_w4_kernel<FMT, GP, NT, D>, min((p.tiles + p.WR - 1) / p.WR, sm_count), kThreads, smem, stream, p);
 }
 
 template <int FMT, int GP, int NT, int D>

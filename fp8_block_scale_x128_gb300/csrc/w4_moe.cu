@@ -13,8 +13,7 @@
 //
 // An expert's codes are read once for a batch of its pairs.  Every block builds
 // the expert lists itself: a histogram of the routed pairs and its running
-// sums.  The second launch is a programmatic dependent one: its lists and its
-// first codes do not wait for the first.
+// sums.  The second launch's lists and first codes do not wait for the first.
 #include "internal.cuh"
 #include "w4.cuh"
 
@@ -162,8 +161,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
     float* inv = reinterpret_cast<float*>(codes + D * kSlot + 2 * kTableBytes<GP>);
     constexpr int kXsAt = D * kSlot + 2 * kTableBytes<GP> + 32;
     uint8_t* xs = codes + kXsAt;
-    const Lists L = build_lists(p, batch, smem, reinterpret_cast<int*>(base));
+    ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    const Lists L = build_lists(p, batch, smem, reinterpret_cast<int*>(base));
 
     const int chunks = p.H / kChunk;
     const int first = warp * chunks / kWarps, last = (warp + 1) * chunks / kWarps;
@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
     float* table = reinterpret_cast<float*>(codes + D * kCodeBytes);
     float* inv = reinterpret_cast<float*>(codes + D * kCodeBytes + kTableBytes<GP>);
     uint8_t* xs = codes + D * kCodeBytes + kTableBytes<GP> + 32;
-    // the pairs' routing weights, 0 for an invalid id
+    // the pairs' routing weights, 0 for an invalid id (the first launch has
+    // waited for whatever wrote the routing)
     float* weight = out + P * kTileRows;
     for (int q = tid; q < P; q += kThreads) {
         const int e = p.ids[q];
@@ -344,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) raw[i] = issue(i);
     ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     load_tokens(warp, 0);
     int slot = 0;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -391,20 +393,6 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
     }
 }
 
-cudaError_t launch_pdl(void (*kernel)(MoeParams, int), const MoeParams& p, int batch, int grid, int smem, bool pdl, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, batch);
-}
-
 // The pairs of an entry: half as many where that lets two blocks share a
 // multiprocessor.
 template <typename F>
@@ -426,7 +414,7 @@ cudaError_t launch_up(const MoeParams& p, int sm_count, cudaStream_t stream) {
     const int per_sm = min(2, kMaxSmShared / (smem + 1024));
     const int64_t most = static_cast<int64_t>(P) * (p.I / kTileRows);
     const int grid = static_cast<int>(min(most, static_cast<int64_t>(sm_count) * per_sm));
-    return launch_pdl(moe_w4_up_kernel<FMT, GP>, p, batch, grid, smem, false, stream);
+    return launch_dependent(moe_w4_up_kernel<FMT, GP>, grid, kThreads, smem, stream, p, batch);
 }
 
 template <int FMT, int GP>
@@ -439,7 +427,7 @@ cudaError_t launch_down(const MoeParams& p, int sm_count, cudaStream_t stream) {
         return lists_bytes(P) + out_bytes(P) + max(counts_bytes(p.E), kWarps * warp_bytes<GP, kDownDepth, 1>(min(P, batch), 0));
     };
     const int batch = batch_of(bytes), smem = bytes(batch), per_sm = min(2, kMaxSmShared / (smem + 1024));
-    return launch_pdl(moe_w4_down_kernel<FMT, GP>, p, batch, min(p.H / kTileRows, sm_count * per_sm), smem, true, stream);
+    return launch_dependent(moe_w4_down_kernel<FMT, GP>, min(p.H / kTileRows, sm_count * per_sm), kThreads, smem, stream, p, batch);
 }
 
 }  // namespace
