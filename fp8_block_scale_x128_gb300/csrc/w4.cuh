@@ -110,9 +110,7 @@ __device__ __forceinline__ uint2 load_scales(const uint8_t* src, int nch, int la
     return w;
 }
 
-// Their fp32 values into the stage's table [row][chunk * GP + group].  An e8m0
-// byte b is 2^(b - 127): its bits shifted into the exponent, 0 being the
-// subnormal 2^-127.  A stage with a scale of 2^97 or more has its table divided
+// Their fp32 values into the stage's table [row][chunk * GP + group].  A stage with a scale of 2^97 or more has its table divided
 // by 2^64 (kBigScale), so that a group's sum, up to 2^27 at the activations'
 // fixed scaling, times its scale stays finite; returns the factor to put back.
 constexpr float kBigScale = 0x1p64f;
@@ -123,15 +121,14 @@ __device__ __forceinline__ bool big_scale(uint2 raw) {  // some scale's three to
 }
 template <int FMT, int GP>
 __device__ __forceinline__ void store_scales_by(float* table, uint2 raw, bool big, int lane) {
-    const uint32_t w[2] = {raw.x, raw.y};
+    uint32_t w[2] = {raw.x, raw.y};
+    if constexpr (FMT == FP8BS_W4_MXFP4)  // four e8m0 bytes to four bf16
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;\n\tcvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
+            : "=r"(w[0]), "=r"(w[1])
+            : "r"(raw.x));
     float v[GP];
 #pragma unroll
-    for (int i = 0; i < GP; ++i) {
-        if constexpr (FMT == FP8BS_W4_MXFP4)
-            v[i] = __uint_as_float(max(((w[0] >> (8 * i)) & 0xFFu) << 23, 0x00400000u));
-        else
-            v[i] = __uint_as_float((w[i / 2] >> (16 * (i % 2))) << 16);
-    }
+    for (int i = 0; i < GP; ++i) v[i] = __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
     if (big)
 #pragma unroll
         for (int i = 0; i < GP; ++i) v[i] *= 1.0f / kBigScale;
@@ -220,46 +217,73 @@ struct RawBf16 {
     __device__ __forceinline__ void values(int i, float (&v)[8]) const { unpack8(r[i], v); }
 };
 
-// The same of up to two fp32 tokens (they are rounded to fp16's 11 bits: 2^-12
-// of each value, 16 times finer than the bf16 of the outputs).
-struct RawF32 {
-    static constexpr int kTokens = 2;
-    float4 a[kTokens], b[kTokens];
-    template <typename Src>
-    __device__ __forceinline__ void load(int n, int nch, int lane, Src src) {
+// The same of up to four tokens kept as fp16 with a biased exponent (as
+// slice_scale takes it) per 16 values, in the decode's pair order.  A stage's
+// values are brought to its largest exponent.
+struct RawFp16 {
+    static constexpr int kTokens = 4;
+    uint4 r[kTokens];
+    int e[kTokens];
+    // src(i): token i's first value of the stage; exp(i): its first exponent
+    template <typename Src, typename Exp>
+    __device__ __forceinline__ void load(int n, int nch, int lane, Src src, Exp exp) {
         const bool in = lane < nch * (kChunk / 8);
 #pragma unroll
         for (int i = 0; i < kTokens; ++i) {
-            a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            r[i] = make_uint4(0, 0, 0, 0);
+            e[i] = 0;
             if (in && i < n) {
-                a[i] = __ldcg(reinterpret_cast<const float4*>(src(i) + 8 * lane));
-                b[i] = __ldcg(reinterpret_cast<const float4*>(src(i) + 8 * lane + 4));
+                r[i] = __ldcg(reinterpret_cast<const uint4*>(src(i) + 8 * lane));
+                e[i] = __ldcg(exp(i) + (lane >> 1));
             }
         }
     }
-    __device__ __forceinline__ void values(int i, float (&v)[8]) const {
-        v[0] = a[i].x, v[1] = a[i].y, v[2] = a[i].z, v[3] = a[i].w;
-        v[4] = b[i].x, v[5] = b[i].y, v[6] = b[i].z, v[7] = b[i].w;
-    }
-    __device__ __forceinline__ uint32_t exponent(int i) const {
-        float v[8];
-        values(i, v);
-        uint32_t top = 0;
+    __device__ __forceinline__ void store(uint8_t* dst, float* inv, int i0, int n, int lane) const {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-        return __reduce_max_sync(0xFFFFFFFFu, top) >> 23;
+        for (int i = 0; i < kTokens; ++i) {
+            if (i0 + i >= n) break;
+            const int top = __reduce_max_sync(0xFFFFFFFFu, e[i]);
+            // 2^(e - top), in two factors where one would leave fp16's exact powers of two
+            const int down = e[i] > 0 ? top - e[i] : 0, first = min(down, 14);  // (no values: 0)
+            uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+            const __half2 f = __half2half2(__ushort_as_half(static_cast<unsigned short>((15 - first) << 10)));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __half2 h = __hmul2(*reinterpret_cast<__half2*>(&w[j]), f);
+                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            if (__any_sync(0xFFFFFFFFu, down > 14)) {
+                const int rest = min(down - first, 14), last = min(down - first - rest, 14);
+                const __half2 f1 = __half2half2(__ushort_as_half(static_cast<unsigned short>((15 - rest) << 10)));
+                const __half2 f2 = __half2half2(__ushort_as_half(static_cast<unsigned short>((15 - last) << 10)));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const __half2 h = __hmul2(__hmul2(*reinterpret_cast<__half2*>(&w[j]), f1), f2);
+                    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+            }
+            *reinterpret_cast<uint4*>(dst + token_word(i0 + i, lane)) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (lane == 0) inv[i0 + i] = __uint_as_float(static_cast<uint32_t>(max(top, 15) - 14) << 23);
+        }
     }
 };
+
+// Where value k of a 16-value run sits in the decode's pair order.
+template <int FMT>
+__device__ __forceinline__ int paired(int k) {
+    if constexpr (FMT == FP8BS_W4_MXFP4) return k;
+    return (k & 8) | (k & 3) << 1 | (k >> 2 & 1);
+}
 
 // The stage of n tokens as fp16 at dst, with the inverse scales in inv.  raw
 // holds the first tokens, loaded beforehand; the others are loaded here.  The
 // whole warp takes part and must synchronise before it reads.
-template <int FMT, typename Raw, typename Src>
-__device__ __forceinline__ void stage_tokens(uint8_t* dst, float* inv, Raw& raw, int n, int nch, int lane, Src src) {
-    for (int i0 = 0; i0 < n; i0 += Raw::kTokens) {
+template <int FMT, typename Src>
+__device__ __forceinline__ void stage_tokens(uint8_t* dst, float* inv, RawBf16& raw, int n, int nch, int lane, Src src) {
+    for (int i0 = 0; i0 < n; i0 += RawBf16::kTokens) {
         if (i0 > 0) raw.load(n - i0, nch, lane, [&](int i) { return src(i0 + i); });
 #pragma unroll
-        for (int i = 0; i < Raw::kTokens; ++i) {
+        for (int i = 0; i < RawBf16::kTokens; ++i) {
             if (i0 + i >= n) break;
             float inverse, v[8];
             const float s = slice_scale(raw.exponent(i), inverse);
@@ -268,6 +292,14 @@ __device__ __forceinline__ void stage_tokens(uint8_t* dst, float* inv, Raw& raw,
             if (lane == 0) inv[i0 + i] = inverse;
         }
     }
+}
+
+// (a & b) | c as one instruction (written out: a compiler that sees both
+// constants makes two of it).
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
 }
 
 // One word (8 codes) -> four fp16 pairs, exact.  e2m1: the hardware conversion.
@@ -284,8 +316,8 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t (&r)[4]) {
             : "r"(w));
     } else {
         const uint32_t u = w >> 8;
-        const uint32_t p[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x64006400u,
-                               (u & 0x000F000Fu) | 0x64006400u, (u & 0x00F000F0u) | 0x64006400u};
+        const uint32_t p[4] = {and_or(w, 0x000F000Fu, 0x64006400u), and_or(w, 0x00F000F0u, 0x64006400u),
+                               and_or(u, 0x000F000Fu, 0x64006400u), and_or(u, 0x00F000F0u, 0x64006400u)};
         const __half2 sub = __half2half2(__ushort_as_half(0xE408));   // -1032
         const __half2 mul = __half2half2(__ushort_as_half(0x2C00));   // 1/16
         const __half2 add = __half2half2(__ushort_as_half(0xD480));   // -72

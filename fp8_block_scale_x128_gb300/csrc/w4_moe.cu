@@ -1,7 +1,9 @@
 // Small-batch mixture-of-experts layer on 4-bit weights, two launches.
 //
 //   h = x[m] . w13[e]^T              (gate rows 0..I-1 over up rows I..2I-1)
-//   a = silu(h_gate) * h_up          (fp32, kept in the workspace)
+//   a = silu(h_gate) * h_up          (kept in the workspace as fp16 with an
+//                                     exponent per 16 values: rounded to 2^-12
+//                                     of each, 16 times finer than the bf16 of y)
 //   y[m] = bf16(sum over s, in slot order, of tw[m, s] * (a . w2[e]^T))
 //
 // 1. gate/up: items of (expert, up to 8 of its pairs, 16 gate rows and the 16
@@ -38,7 +40,8 @@ struct MoeParams {
     const uint8_t* s2;
     uint16_t* y;    // [M, H]
     uint32_t* err;  // workspace error word
-    float* a;       // [M*S][I]
+    uint16_t* a;    // [M*S][I] fp16, 16 values at a time in the decode's pair order
+    uint8_t* ae;    // [M*S][I/16] their biased exponents
     int M, S, H, I, E;
 };
 
@@ -46,13 +49,14 @@ struct MoeParams {
 // elements each.
 struct Lists {
     int16_t* pairs;     // grouped by expert, ascending experts
+    int16_t* tokens;    // of pairs
     int16_t* unsorted;  // those of experts with more than one entry
     int16_t* expert;    // of an entry
     int16_t* first;     // its first pair in pairs
     int16_t* n;         // its pairs: 1 .. batch
     int entries;
 };
-__host__ __device__ constexpr int lists_bytes(int P) { return (5 * P * 2 + 15) / 16 * 16; }
+__host__ __device__ constexpr int lists_bytes(int P) { return (6 * P * 2 + 15) / 16 * 16; }
 __host__ __device__ constexpr int counts_bytes(int E) { return (E * 4 + 15) / 16 * 16; }
 
 // counts: E ints of shared memory, free afterwards.  The order of the pairs of
@@ -66,7 +70,8 @@ __device__ Lists build_lists(const MoeParams& p, int batch, uint8_t* mem, int* c
     const int P = p.M * p.S;
     Lists L;
     L.pairs = reinterpret_cast<int16_t*>(mem);
-    L.unsorted = L.pairs + P;
+    L.tokens = L.pairs + P;
+    L.unsorted = L.tokens + P;
     L.expert = L.unsorted + P;
     L.first = L.expert + P;
     L.n = L.first + P;
@@ -120,7 +125,13 @@ __device__ Lists build_lists(const MoeParams& p, int batch, uint8_t* mem, int* c
     for (int j = 0; j < kMine; ++j)
         if (id[j] >= 0) {
             const int c = counts[id[j]];
-            (c >> 16 > batch ? L.unsorted : L.pairs)[(c & 0xFFFF) + rank[j]] = static_cast<int16_t>(tid + j * kThreads);
+            const int q = tid + j * kThreads, at = (c & 0xFFFF) + rank[j];
+            if (c >> 16 > batch) {
+                L.unsorted[at] = static_cast<int16_t>(q);
+            } else {
+                L.pairs[at] = static_cast<int16_t>(q);
+                L.tokens[at] = static_cast<int16_t>(q / p.S);
+            }
         }
     __syncthreads();
 #pragma unroll
@@ -130,6 +141,7 @@ __device__ Lists build_lists(const MoeParams& p, int batch, uint8_t* mem, int* c
             int r = 0;
             for (int i = 0; i < n; ++i) r += L.unsorted[first + i] < q;
             L.pairs[first + r] = static_cast<int16_t>(q);
+            L.tokens[first + r] = static_cast<int16_t>(q / p.S);
         }
     L.entries = n_entries;
     __syncthreads();
@@ -168,26 +180,37 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
     const int chunks = p.H / kChunk;
     const int first = warp * chunks / kWarps, last = (warp + 1) * chunks / kWarps;
     const int pieces = ((chunks + kWarps - 1) / kWarps + kPC - 1) / kPC;
-    const int per = p.I / kTileRows, items = L.entries * per;
+    const int per = p.I / kTileRows;
     const int64_t ldc = p.H / 2, lds = static_cast<int64_t>(chunks) * SB;
     const int64_t up_codes = p.I * ldc, up_scales = p.I * lds;  // from a gate tile to its up tile
 
+    // an item is a tile j of an entry; the block's items are gridDim.x apart
+    struct Item {
+        int entry, j;
+    };
+    const int step_entry = gridDim.x / per, step_j = gridDim.x - step_entry * per;
+    auto next = [&](Item& it) {
+        it.entry += step_entry;
+        if ((it.j += step_j) >= per) it.j -= per, ++it.entry;
+    };
+    Item now = {static_cast<int>(blockIdx.x) / per, 0};
+    now.j = blockIdx.x - now.entry * per;
     // a warp's stages: the items of the block, in an item the pieces of the slice
     struct Cursor {
-        int item, piece;
+        Item it;
+        int piece;
         const uint8_t *codes, *scales;  // this lane's, of the gate tile
     };
-    Cursor ahead = {static_cast<int>(blockIdx.x), 0, nullptr, nullptr};
+    Cursor ahead = {now, 0, nullptr, nullptr};
     auto locate = [&]() {
-        if (ahead.item >= items) return;
-        const int entry = ahead.item / per, j = ahead.item - entry * per;
-        const int64_t row = static_cast<int64_t>(L.expert[entry]) * 2 * p.I + j * kTileRows;
+        if (ahead.it.entry >= L.entries) return;
+        const int64_t row = static_cast<int64_t>(L.expert[ahead.it.entry]) * 2 * p.I + ahead.it.j * kTileRows;
         ahead.codes = p.w13 + (row + (lane >> 3)) * ldc + first * 64 + (lane & 7) * 16;
         ahead.scales = p.s13 + (row + (lane >> 1)) * lds + (first + (lane & 1)) * SB;
     };
     auto issue = [&](int slot, uint2 (&raw)[2]) {
         const int nch = min(last - first - ahead.piece * kPC, kPC);
-        if (ahead.item < items && nch > 0) {
+        if (ahead.it.entry < L.entries && nch > 0) {
             load_codes(codes + slot * kSlot, ahead.codes, ldc, kTileRows - 1, nch, lane);
             load_codes(codes + slot * kSlot + kCodeBytes, ahead.codes + up_codes, ldc, kTileRows - 1, nch, lane);
             raw[0] = load_scales<FMT, GP>(ahead.scales, nch, lane);
@@ -199,32 +222,31 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
             ahead.scales += kPC * SB;
         } else {
             ahead.piece = 0;
-            ahead.item += gridDim.x;
+            next(ahead.it);
             locate();
         }
     };
     auto source = [&](int entry, int piece) {
-        const int16_t* pairs = L.pairs + L.first[entry];
+        const int16_t* tokens = L.tokens + L.first[entry];
         const uint16_t* x = p.x + (first + piece * kPC) * kChunk;
         const int64_t ldx = p.ldx;
-        const int S = p.S;
-        return [=](int i) { return x + pairs[i] / S * ldx; };
+        return [=](int i) { return x + tokens[i] * ldx; };
     };
     RawBf16 tokens;
-    auto load_tokens = [&](int item, int piece) {
+    auto load_tokens = [&](int entry, int piece) {
         const int nch = min(last - first - piece * kPC, kPC);
-        if (item < items && nch > 0) tokens.load(L.n[item / per], nch, lane, source(item / per, piece));
+        if (entry < L.entries && nch > 0) tokens.load(L.n[entry], nch, lane, source(entry, piece));
     };
 
     locate();
     uint2 raw[D - 1][2];
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) issue(i, raw[i]);
-    load_tokens(blockIdx.x, 0);
+    load_tokens(now.entry, 0);
     int slot = 0;
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const int entry = item / per, j = item - entry * per;
-        const int n = L.n[entry], pf = L.first[entry];
+    while (now.entry < L.entries) {
+        const int entry = now.entry, j = now.j, n = L.n[entry], pf = L.first[entry];
+        next(now);
         float tot[2][1][4] = {};
         for (int piece = 0; piece < pieces; ++piece) {
             const int nch = min(last - first - piece * kPC, kPC);
@@ -235,15 +257,15 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
             if (nch > 0) {
                 stage_tokens<FMT>(xs, inv, tokens, n, nch, lane, source(entry, piece));
                 if (piece + 1 < pieces)
-                    load_tokens(item, piece + 1);
+                    load_tokens(entry, piece + 1);
                 else
-                    load_tokens(item + gridDim.x, 0);
+                    load_tokens(now.entry, 0);
                 const float back = store_scales<FMT, GP>(table, gate, up, lane);
                 cp_async_wait<D - 1>();
                 __syncwarp();
                 stage_mma<FMT, GP, 1, 2>(tot, codes + slot * kSlot, table, xs, inv, back, n, nch, lane);
             } else if (piece + 1 == pieces) {
-                load_tokens(item + gridDim.x, 0);
+                load_tokens(now.entry, 0);
             }
             __syncwarp();  // the slot, the table and the tokens are rewritten by later stages
             slot = slot + 1 == D ? 0 : slot + 1;
@@ -252,8 +274,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
         store_sums<1>(reinterpret_cast<float*>(xs), tot[0], lane);
         store_sums<1>(reinterpret_cast<float*>(xs + kSumBytes<1>), tot[1], lane);
         __syncthreads();
-        for (int o = threadIdx.x; o < n * kTileRows; o += kThreads) {
-            const int i = o / kTileRows, row = o % kTileRows;
+        if (threadIdx.x < kMaxBatch * kTileRows) {  // 16 lanes a pair
+            const int i = min(static_cast<int>(threadIdx.x) / kTileRows, n - 1), row = threadIdx.x % kTileRows;
             const uint8_t* s = base + kXsAt + (i * kSumPitch + row) * 4;
             float g = 0.0f, v = 0.0f;
 #pragma unroll
@@ -261,7 +283,18 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
                 g += *reinterpret_cast<const float*>(s + w * mine_bytes);
                 v += *reinterpret_cast<const float*>(s + w * mine_bytes + kSumBytes<1>);
             }
-            p.a[static_cast<int64_t>(L.pairs[pf + i]) * p.I + j * kTileRows + row] = g / (1.0f + expf(-g)) * v;
+            const float a = g / (1.0f + expf(-g)) * v;
+            // the largest exponent of the pair's 16 values
+            uint32_t ef = (__float_as_uint(a) & 0x7FFFFFFFu) >> 23;
+#pragma unroll
+            for (int off = 8; off > 0; off /= 2) ef = max(ef, __shfl_xor_sync(0xFFFFFFFFu, ef, off));
+            float inverse;
+            const float scale = slice_scale(ef, inverse);
+            if (static_cast<int>(threadIdx.x) < n * kTileRows) {
+                const int64_t at = static_cast<int64_t>(L.pairs[pf + i]) * p.I + j * kTileRows;
+                p.a[at + paired<FMT>(row)] = __half_as_ushort(__float2half_rn(a * scale));
+                if (row == 0) p.ae[at / kTileRows] = static_cast<uint8_t>(min(max(ef, 15u), 254u));
+            }
         }
         __syncthreads();  // the sums' place is rewritten by the next item
     }
@@ -329,15 +362,15 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
         }
         return raw;
     };
-    auto source = [&](int entry, int piece) {
-        const int16_t* pairs = L.pairs + L.first[entry];
-        const float* a = p.a + piece * kStageK;
+    RawFp16 tokens;
+    auto load_tokens = [&](int entry, int piece, int i0) {
+        const int16_t* pairs = L.pairs + L.first[entry] + i0;
+        const uint16_t* a = p.a + piece * kStageK;
+        const uint8_t* ae = p.ae + piece * (kStageK / kTileRows);
         const int I = p.I;
-        return [=](int i) { return a + static_cast<int64_t>(pairs[i]) * I; };
-    };
-    RawF32 tokens;
-    auto load_tokens = [&](int entry, int piece) {
-        if (entry < L.entries) tokens.load(L.n[entry], min(chunks - piece * kPC, kPC), lane, source(entry, piece));
+        tokens.load(L.n[entry] - i0, min(chunks - piece * kPC, kPC), lane,
+                    [=](int i) { return a + static_cast<int64_t>(pairs[i]) * I; },
+                    [=](int i) { return ae + static_cast<int64_t>(pairs[i]) * (I / kTileRows); });
     };
 
     locate();
@@ -346,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
     for (int i = 0; i < D - 1; ++i) raw[i] = issue(i);
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    load_tokens(warp, 0);
+    if (warp < L.entries) load_tokens(warp, 0, 0);
     int slot = 0;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         for (int q = tid; q < P * kTileRows; q += kThreads) out[q] = 0.0f;  // pairs with an invalid id stay 0
@@ -356,11 +389,15 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
             float tot[1][1][4] = {};
             for (int piece = 0; piece < pieces; ++piece) {
                 const int nch = min(chunks - piece * kPC, kPC);
-                stage_tokens<FMT>(xs, inv, tokens, n, nch, lane, source(entry, piece));
+                tokens.store(xs, inv, 0, n, lane);
+                for (int i0 = RawFp16::kTokens; i0 < n; i0 += RawFp16::kTokens) {
+                    load_tokens(entry, piece, i0);
+                    tokens.store(xs, inv, i0, n, lane);
+                }
                 if (piece + 1 < pieces)
-                    load_tokens(entry, piece + 1);
+                    load_tokens(entry, piece + 1, 0);
                 else
-                    load_tokens(entry + kWarps < L.entries ? entry + kWarps : warp, 0);
+                    load_tokens(entry + kWarps < L.entries ? entry + kWarps : warp, 0, 0);
                 const uint2 cur = raw[0];
 #pragma unroll
                 for (int i = 0; i + 2 < D; ++i) raw[i] = raw[i + 1];
@@ -448,7 +485,8 @@ cudaError_t launch_moe_w4(const MoeW4Args& a, cudaStream_t stream) {
     p.s2 = a.s2;
     p.y = a.y;
     p.err = reinterpret_cast<uint32_t*>(a.workspace);
-    p.a = reinterpret_cast<float*>(a.workspace + kHeader);
+    p.a = reinterpret_cast<uint16_t*>(a.workspace + kHeader);
+    p.ae = a.workspace + kHeader + static_cast<size_t>(a.M) * a.S * a.I * sizeof(uint16_t);
     p.M = a.M;
     p.S = a.S;
     p.H = a.H;
