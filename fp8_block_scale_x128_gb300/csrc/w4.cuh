@@ -67,28 +67,60 @@ constexpr int kScalePitch = kPC * GP + 4;  // floats of a scale row
 template <int GP>
 constexpr int kTableBytes = kTileRows * kScalePitch<GP> * 4;
 
+// Shared memory by its 32-bit address: the loops below keep every address as a
+// lane constant plus a slot's offset.
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float2 lds_float2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float lds_float(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts_float2(uint32_t a, float x, float y) {
+    asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void sts_float(uint32_t a, float x) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Start the copy of a stage: nch (1..kPC) chunks of 16 code rows to dst.  src
-// points at this lane's first 16 bytes: row lane / 8 of the tile, byte
-// 16 (lane % 8) of the stage; it takes the rows 4, 8 and 12 further on as well.
-// last: the tile's last row; rows past it repeat it (their outputs are
-// dropped), so every access stays inside the weight.
-__device__ __forceinline__ void load_codes(uint8_t* dst, const uint8_t* src, int64_t ldc, int last, int nch, int lane) {
+// Start the copy of a stage: nch (1..kPC) chunks of 16 code rows.  src points
+// at this lane's first 16 bytes: row lane / 8 of the tile, byte 16 (lane % 8)
+// of the stage, dst at their place (code_dst); it takes the rows 4, 8 and 12
+// further on as well.  last: the tile's last row; rows past it repeat it (their
+// outputs are dropped), so every access stays inside the weight.
+__device__ __forceinline__ uint32_t code_dst(int lane) { return (lane >> 3) * kCodePitch + (lane & 7) * 16; }
+__device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* src, int64_t ldc, int last, int nch, int lane) {
     if ((lane & 7) >= nch * 4) return;
-    uint8_t* to = dst + (lane >> 3) * kCodePitch + (lane & 7) * 16;
     if (last == kTileRows - 1) {
-#pragma unroll
-        for (int j = 0; j < kTileRows / 4; ++j) ptx::cp_async16(to + 4 * j * kCodePitch, src + 4 * j * ldc);
+        const int64_t step = 4 * ldc;
+        cp_async16(dst, src);
+        cp_async16(dst + 4 * kCodePitch, src += step);
+        cp_async16(dst + 8 * kCodePitch, src += step);
+        cp_async16(dst + 12 * kCodePitch, src += step);
     } else {
 #pragma unroll
         for (int j = 0; j < kTileRows / 4; ++j) {
             const int r = (lane >> 3) + 4 * j;
-            ptx::cp_async16(to + 4 * j * kCodePitch, src + (min(r, last) - (lane >> 3)) * ldc);
+            cp_async16(dst + 4 * j * kCodePitch, src + (min(r, last) - (lane >> 3)) * ldc);
         }
     }
 }
@@ -120,7 +152,7 @@ __device__ __forceinline__ bool big_scale(uint2 raw) {  // some scale's three to
     return (high & (FMT == FP8BS_W4_MXFP4 ? 0x80808080u : 0x40004000u)) != 0;
 }
 template <int FMT, int GP>
-__device__ __forceinline__ void store_scales_by(float* table, uint2 raw, bool big, int lane) {
+__device__ __forceinline__ void store_scales_by(uint32_t dst, uint2 raw, bool big) {
     uint32_t w[2] = {raw.x, raw.y};
     if constexpr (FMT == FP8BS_W4_MXFP4)  // four e8m0 bytes to four bf16
         asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;\n\tcvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
@@ -132,26 +164,25 @@ __device__ __forceinline__ void store_scales_by(float* table, uint2 raw, bool bi
     if (big)
 #pragma unroll
         for (int i = 0; i < GP; ++i) v[i] *= 1.0f / kBigScale;
-    float* dst = table + (lane >> 1) * kScalePitch<GP> + (lane & 1) * GP;
     if constexpr (GP == 4)
-        *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+        sts128(dst, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
     else if constexpr (GP == 2)
-        *reinterpret_cast<float2*>(dst) = make_float2(v[0], v[1]);
+        sts_float2(dst, v[0], v[1]);
     else
-        dst[0] = v[0];
+        sts_float(dst, v[0]);
 }
-template <int FMT, int GP>
-__device__ __forceinline__ float store_scales(float* table, uint2 raw, int lane) {
-    const bool big = __any_sync(0xFFFFFFFFu, big_scale<FMT>(raw));
-    store_scales_by<FMT, GP>(table, raw, big, lane);
-    return big ? kBigScale : 1.0f;
+// dst: this lane's place in the table (scale_dst).
+template <int GP>
+__device__ __forceinline__ uint32_t scale_dst(int lane) {
+    return ((lane >> 1) * kScalePitch<GP> + (lane & 1) * GP) * 4;
 }
-// Of a stage of two tiles.
-template <int FMT, int GP>
-__device__ __forceinline__ float store_scales(float* table, uint2 raw0, uint2 raw1, int lane) {
-    const bool big = __any_sync(0xFFFFFFFFu, big_scale<FMT>(raw0) || big_scale<FMT>(raw1));
-    store_scales_by<FMT, GP>(table, raw0, big, lane);
-    store_scales_by<FMT, GP>(table + kTileRows * kScalePitch<GP>, raw1, big, lane);
+template <int FMT, int GP, int T>
+__device__ __forceinline__ float store_scales(uint32_t dst, const uint2 (&raw)[T]) {
+    bool big = big_scale<FMT>(raw[0]);
+    if constexpr (T == 2) big |= big_scale<FMT>(raw[1]);
+    big = __any_sync(0xFFFFFFFFu, big);
+#pragma unroll
+    for (int i = 0; i < T; ++i) store_scales_by<FMT, GP>(dst + i * kTableBytes<GP>, raw[i], big);
     return big ? kBigScale : 1.0f;
 }
 
@@ -193,7 +224,7 @@ __device__ __forceinline__ void unpack8(const uint4& raw, float (&v)[8]) {
 }
 
 // Where the 16-byte word w (8 k) of a token's stage sits.
-__device__ __forceinline__ int token_word(int token, int w) { return token * kTokenBytes + (w ^ (token & 1) << 2) * 16; }
+__device__ __forceinline__ uint32_t token_word(int token, int w) { return token * kTokenBytes + (w ^ (token & 1) << 2) * 16; }
 
 // A stage of up to four bf16 tokens, as loaded: lane l holds k = 8l .. 8l+7
 // (zeros past nch chunks).  src(i): token i's first element of the stage.
@@ -205,8 +236,9 @@ struct RawBf16 {
         const bool in = lane < nch * (kChunk / 8);
 #pragma unroll
         for (int i = 0; i < kTokens; ++i) {
+            if (i >= n) break;
             r[i] = make_uint4(0, 0, 0, 0);
-            if (in && i < n) r[i] = *reinterpret_cast<const uint4*>(src(i) + 8 * lane);
+            if (in) r[i] = *reinterpret_cast<const uint4*>(src(i) + 8 * lane);
         }
     }
     __device__ __forceinline__ uint32_t exponent(int i) const {
@@ -230,15 +262,16 @@ struct RawFp16 {
         const bool in = lane < nch * (kChunk / 8);
 #pragma unroll
         for (int i = 0; i < kTokens; ++i) {
+            if (i >= n) break;
             r[i] = make_uint4(0, 0, 0, 0);
             e[i] = 0;
-            if (in && i < n) {
+            if (in) {
                 r[i] = __ldcg(reinterpret_cast<const uint4*>(src(i) + 8 * lane));
                 e[i] = __ldcg(exp(i) + (lane >> 1));
             }
         }
     }
-    __device__ __forceinline__ void store(uint8_t* dst, float* inv, int i0, int n, int lane) const {
+    __device__ __forceinline__ void store(uint32_t dst, uint32_t inv, int i0, int n, int lane) const {
 #pragma unroll
         for (int i = 0; i < kTokens; ++i) {
             if (i0 + i >= n) break;
@@ -262,8 +295,8 @@ struct RawFp16 {
                     w[j] = *reinterpret_cast<const uint32_t*>(&h);
                 }
             }
-            *reinterpret_cast<uint4*>(dst + token_word(i0 + i, lane)) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (lane == 0) inv[i0 + i] = __uint_as_float(static_cast<uint32_t>(max(top, 15) - 14) << 23);
+            sts128(dst + token_word(i0 + i, lane), make_uint4(w[0], w[1], w[2], w[3]));
+            if (lane == 0) sts_float(inv + 4 * (i0 + i), __uint_as_float(static_cast<uint32_t>(max(top, 15) - 14) << 23));
         }
     }
 };
@@ -279,7 +312,7 @@ __device__ __forceinline__ int paired(int k) {
 // holds the first tokens, loaded beforehand; the others are loaded here.  The
 // whole warp takes part and must synchronise before it reads.
 template <int FMT, typename Src>
-__device__ __forceinline__ void stage_tokens(uint8_t* dst, float* inv, RawBf16& raw, int n, int nch, int lane, Src src) {
+__device__ __forceinline__ void stage_tokens(uint32_t dst, uint32_t inv, RawBf16& raw, int n, int nch, int lane, Src src) {
     for (int i0 = 0; i0 < n; i0 += RawBf16::kTokens) {
         if (i0 > 0) raw.load(n - i0, nch, lane, [&](int i) { return src(i0 + i); });
 #pragma unroll
@@ -288,8 +321,8 @@ __device__ __forceinline__ void stage_tokens(uint8_t* dst, float* inv, RawBf16& 
             float inverse, v[8];
             const float s = slice_scale(raw.exponent(i), inverse);
             raw.values(i, v);
-            *reinterpret_cast<uint4*>(dst + token_word(i0 + i, lane)) = pack_slice8<FMT>(v, s);
-            if (lane == 0) inv[i0 + i] = inverse;
+            sts128(dst + token_word(i0 + i, lane), pack_slice8<FMT>(v, s));
+            if (lane == 0) sts_float(inv + 4 * (i0 + i), inverse);
         }
     }
 }
@@ -349,28 +382,33 @@ __device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
 }
 
 // tot[i][j] += the stage's products of tile i and token columns 8j .. 8j+7, as D
 // fragments (rows g, g + 8; columns 2t, 2t + 1).  Tile i's codes and scale
 // table follow tile i - 1's.  inv holds 8 NT factors; columns past n repeat
 // token n - 1 and take whatever factor is there, they are never read.
+//
+// All addresses are a lane's: codes at code_src, table at scale_src, inv at
+// inv_src, x[j] at token_src of column 8j + g.
+__device__ __forceinline__ uint32_t code_src(int lane) {  // ldmatrix: lanes 0-15 rows 0-15 of an even group, 16-31 of the odd one
+    return (lane & 15) * kCodePitch + (lane >> 4) * 16;
+}
+template <int GP>
+__device__ __forceinline__ uint32_t scale_src(int lane) {
+    return (lane >> 2) * kScalePitch<GP> * 4;
+}
+__device__ __forceinline__ uint32_t inv_src(int lane) { return (lane & 3) * 8; }
+// Relative to a 128-byte aligned stage of n tokens; bit 6 says which half of
+// each 128 bytes the even groups are in.
+__device__ __forceinline__ uint32_t token_src(int column, int n, int lane) {
+    const int tok = min(column, n - 1);
+    return tok * kTokenBytes + (tok & 1) * 64 + (lane & 3) * 16;
+}
 template <int FMT, int GP, int NT, int T>
-__device__ __forceinline__ void stage_mma(float (&tot)[T][NT][4], const uint8_t* codes, const float* table, const uint8_t* xs,
-                                          const float* inv, float back, int n, int nch, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    // ldmatrix: lanes 0-15 address rows 0-15 of an even group, 16-31 of the odd one
-    const uint32_t c0 = ptx::smem_addr(codes) + (lane & 15) * kCodePitch + (lane >> 4) * 16;
-    const float* s0 = table + g * kScalePitch<GP>;
-    const uint8_t* x[NT][2];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int tok = min(8 * j + g, n - 1), odd = tok & 1;
-        x[j][0] = xs + tok * kTokenBytes + t * 16 + odd * 64;  // even groups
-        x[j][1] = xs + tok * kTokenBytes + t * 16 - odd * 64;  // odd ones
-    }
+__device__ __forceinline__ void stage_mma(float (&tot)[T][NT][4], uint32_t codes, uint32_t table, const uint32_t (&x)[NT],
+                                          uint32_t inv, float back, int nch) {
     float acc[T][NT][4];
 #pragma unroll
     for (int i = 0; i < T; ++i)
@@ -382,14 +420,14 @@ __device__ __forceinline__ void stage_mma(float (&tot)[T][NT][4], const uint8_t*
         float sa[T][GP], sb[T][GP];
 #pragma unroll
         for (int i = 0; i < T; ++i) {
-            const float* p = s0 + i * kTileRows * kScalePitch<GP> + c * GP;
+            const uint32_t p = table + i * kTableBytes<GP> + c * GP * 4;
             if constexpr (GP == 4) {
-                const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 8 * kScalePitch<GP>);
-                sa[i][0] = u.x, sa[i][1] = u.y, sa[i][2] = u.z, sa[i][3] = u.w;
-                sb[i][0] = v.x, sb[i][1] = v.y, sb[i][2] = v.z, sb[i][3] = v.w;
+                const uint4 u = lds128(p), v = lds128(p + 8 * kScalePitch<GP> * 4);
+                sa[i][0] = __uint_as_float(u.x), sa[i][1] = __uint_as_float(u.y), sa[i][2] = __uint_as_float(u.z), sa[i][3] = __uint_as_float(u.w);
+                sb[i][0] = __uint_as_float(v.x), sb[i][1] = __uint_as_float(v.y), sb[i][2] = __uint_as_float(v.z), sb[i][3] = __uint_as_float(v.w);
             } else {
 #pragma unroll
-                for (int q = 0; q < GP; ++q) sa[i][q] = p[q], sb[i][q] = p[8 * kScalePitch<GP> + q];
+                for (int q = 0; q < GP; ++q) sa[i][q] = lds_float(p + 4 * q), sb[i][q] = lds_float(p + 8 * kScalePitch<GP> * 4 + 4 * q);
             }
         }
         constexpr int kPerScale = 4 / GP;  // 32-wide groups under one scale
@@ -398,13 +436,13 @@ __device__ __forceinline__ void stage_mma(float (&tot)[T][NT][4], const uint8_t*
         for (int i2 = 0; i2 < 2; ++i2) {
             uint32_t w[T][4];  // group 2 i2: rows g, g + 8; group 2 i2 + 1: the same
 #pragma unroll
-            for (int i = 0; i < T; ++i) ldmatrix4(w[i], c0 + i * kCodeBytes + c * 64 + i2 * 32);
+            for (int i = 0; i < T; ++i) ldmatrix4(w[i], codes + i * kCodeBytes + c * 64 + i2 * 32);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int grp = 2 * i2 + h;
                 uint4 b[NT];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const uint4*>(x[j][h] + c * 256 + grp * 64);
+                for (int j = 0; j < NT; ++j) b[j] = lds128((h ? x[j] ^ 64 : x[j]) + c * 256 + i2 * 128);
 #pragma unroll
                 for (int i = 0; i < T; ++i) {
                     uint32_t lo[4], hi[4];
@@ -436,7 +474,7 @@ __device__ __forceinline__ void stage_mma(float (&tot)[T][NT][4], const uint8_t*
     // where the result does not
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        const float2 f = *reinterpret_cast<const float2*>(inv + 8 * j + 2 * t);
+        const float2 f = lds_float2(inv + 32 * j);
 #pragma unroll
         for (int i = 0; i < T; ++i)
             if (back == 1.0f) {
@@ -458,14 +496,14 @@ constexpr int kSumPitch = kTileRows + 4;  // floats
 template <int NT>
 constexpr int kSumBytes = 8 * NT * kSumPitch * 4;  // of a tile
 template <int NT>
-__device__ __forceinline__ void store_sums(float* dst, const float (&tot)[NT][4], int lane) {
-    float* r = dst + 2 * (lane & 3) * kSumPitch + (lane >> 2);
+__device__ __forceinline__ void store_sums(uint32_t dst, const float (&tot)[NT][4], int lane) {
+    const uint32_t r = dst + (2 * (lane & 3) * kSumPitch + (lane >> 2)) * 4;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        r[8 * j * kSumPitch] = tot[j][0];
-        r[(8 * j + 1) * kSumPitch] = tot[j][1];
-        r[8 * j * kSumPitch + 8] = tot[j][2];
-        r[(8 * j + 1) * kSumPitch + 8] = tot[j][3];
+        sts_float(r + 8 * j * kSumPitch * 4, tot[j][0]);
+        sts_float(r + (8 * j + 1) * kSumPitch * 4, tot[j][1]);
+        sts_float(r + (8 * j * kSumPitch + 8) * 4, tot[j][2]);
+        sts_float(r + ((8 * j + 1) * kSumPitch + 8) * 4, tot[j][3]);
     }
 }
 

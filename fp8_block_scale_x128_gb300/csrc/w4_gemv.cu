@@ -17,6 +17,7 @@ using namespace w4;
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
+constexpr int kPairM = 5;  // tokens up to which two tiles make a stage
 constexpr int kGroup = 4;  // tiles summed in registers before the slices meet
 
 struct GemvParams {
@@ -41,27 +42,33 @@ constexpr int kRedBytes = kGroup * kSumBytes<NT>;  // of a warp
 
 // Bytes of a warp: the ring, the scale table, staged x and its inverse scales,
 // and the partial sums, which take the place of x where that is staged anew.
-template <int GP, int NT, int D>
+template <int GP, int NT, int T, int D>
 __host__ __device__ constexpr int warp_bytes(int M, int pieces, bool resident) {
-    const int kept = resident ? pieces : 1, x = kept * M * kTokenBytes, inv = kept * 8 * NT * 4;
-    return D * kCodeBytes + kTableBytes<GP> + inv + (resident ? x + kRedBytes<NT> : (x > kRedBytes<NT> ? x : kRedBytes<NT>));
+    const int kept = resident ? pieces : 1, x = kept * M * kTokenBytes, inv = (kept * 8 * NT * 4 + 127) / 128 * 128;
+    return D * T * kCodeBytes + T * kTableBytes<GP> + inv + (resident ? x + kRedBytes<NT> : (x > kRedBytes<NT> ? x : kRedBytes<NT>));
 }
 
-// NT: tiles of 8 token columns; D: ring depth.
-template <int FMT, int GP, int NT, int D>
+// NT: tiles of 8 token columns; T: tiles of a stage; D: ring depth.
+template <int FMT, int GP, int NT, int T, int D>
 __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_constant__ GemvParams p) {
     constexpr int SB = Format<FMT, GP>::kScaleBytes;
-    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int kSlot = T * kCodeBytes, kTableAt = D * kSlot, kInvAt = kTableAt + T * kTableBytes<GP>;
+    extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int wr = warp / p.WK, wk = warp - wr * p.WK;
     const int kept = p.resident ? p.pieces : 1;
-    const int mine_bytes = warp_bytes<GP, NT, D>(p.M, p.pieces, p.resident);
-    uint8_t* codes = smem + warp * mine_bytes;                          // [D][kCodeBytes]
-    float* table = reinterpret_cast<float*>(codes + D * kCodeBytes);    // scales
-    float* inv = reinterpret_cast<float*>(codes + D * kCodeBytes + kTableBytes<GP>);  // [kept][8 NT]
-    const int x_at = D * kCodeBytes + kTableBytes<GP> + kept * 8 * NT * 4;
-    uint8_t* xs = codes + x_at;                                         // [kept][M][kTokenBytes]
+    const int mine_bytes = warp_bytes<GP, NT, T, D>(p.M, p.pieces, p.resident);
+    // a warp's memory: codes [D][T], scale tables [T], inv [kept][8 NT],
+    // x [kept][M][kTokenBytes], and the sums behind x or in its place
+    const int x_at = kInvAt + (kept * 8 * NT * 4 + 127) / 128 * 128;
     const int red_at = x_at + (p.resident ? kept * p.M * kTokenBytes : 0);
+    const uint32_t mine = ptx::smem_addr(smem) + warp * mine_bytes, xs = mine + x_at;
+    const uint32_t to_codes = mine + code_dst(lane), to_table = mine + kTableAt + scale_dst<GP>(lane);
+    const uint32_t from_codes = mine + code_src(lane), from_table = mine + kTableAt + scale_src<GP>(lane);
+    const uint32_t from_inv = mine + kInvAt + inv_src(lane);
+    uint32_t from_x[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) from_x[j] = xs + token_src(8 * j + (lane >> 2), p.M, lane);
 
     // a warp past WK * WR has no slice; it only takes part in the sums
     const bool works = wr < p.WR;
@@ -71,8 +78,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
     const int steps = (t1 - t0 + p.WR - 1) / p.WR;  // tiles of a warp
 
     // the order of a warp's stages: groups of kGroup tiles, in a group the
-    // pieces of the slice, in a piece the tiles; codes and scales are this
-    // lane's pointers into the stage
+    // pieces of the slice, in a piece the tiles, T at a time (of two the second
+    // may be missing at the end of a range); codes and scales are this lane's
+    // pointers into the stage
     struct Cursor {
         int group, piece, t, tile;
         const uint8_t *codes, *scales;
@@ -81,36 +89,42 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
     Cursor ahead = {0, 0, 0, t0 + wr, nullptr, nullptr};
     ahead.codes = p.codes + (static_cast<int64_t>(t0 + wr) * kTileRows + (lane >> 3)) * p.ldc + first * 64 + (lane & 7) * 16;
     ahead.scales = p.scales + (static_cast<int64_t>(t0 + wr) * kTileRows + (lane >> 1)) * p.lds + (first + (lane & 1)) * SB;
-    auto issue = [&](int slot) {
-        uint2 raw = make_uint2(0, 0);
+    auto issue = [&](int slot, uint2 (&raw)[T]) {
         const int nch = min(last - first - ahead.piece * kPC, kPC);
-        if (ahead.group < steps && ahead.tile < t1 && nch > 0) {
-            const int last_row = min(p.N - ahead.tile * kTileRows, kTileRows) - 1;
-            load_codes(codes + slot * kCodeBytes, ahead.codes, p.ldc, last_row, nch, lane);
-            raw = load_scales<FMT, GP>(ahead.scales - max((lane >> 1) - last_row, 0) * p.lds, nch, lane);
+        if (ahead.group < steps && nch > 0) {
+#pragma unroll
+            for (int i = 0; i < T; ++i) {
+                const int tile = ahead.tile + i * p.WR;
+                raw[i] = make_uint2(0, 0);
+                if (tile < t1 && ahead.t + i < kGroup) {
+                    const int last_row = min(p.N - tile * kTileRows, kTileRows) - 1;
+                    load_codes(to_codes + slot * kSlot + i * kCodeBytes, ahead.codes + i * tile_codes, p.ldc, last_row, nch, lane);
+                    raw[i] = load_scales<FMT, GP>(ahead.scales + i * tile_scales - max((lane >> 1) - last_row, 0) * p.lds, nch, lane);
+                }
+            }
         }
         cp_async_commit();
         // on to the next stage
         const int count = min(kGroup, steps - ahead.group);
-        if (++ahead.t < count) {
-            ahead.tile += p.WR;
-            ahead.codes += tile_codes;
-            ahead.scales += tile_scales;
+        if ((ahead.t += T) < count) {
+            ahead.tile += T * p.WR;
+            ahead.codes += T * tile_codes;
+            ahead.scales += T * tile_scales;
         } else {
+            const int back = ahead.t - T;
             ahead.t = 0;
             if (++ahead.piece < p.pieces) {
-                ahead.tile -= (count - 1) * p.WR;
-                ahead.codes += kPC * 64 - (count - 1) * tile_codes;
-                ahead.scales += kPC * SB - (count - 1) * tile_scales;
+                ahead.tile -= back * p.WR;
+                ahead.codes += kPC * 64 - back * tile_codes;
+                ahead.scales += kPC * SB - back * tile_scales;
             } else {
                 ahead.piece = 0;
                 ahead.group += kGroup;
-                ahead.tile += p.WR;
-                ahead.codes += tile_codes - (p.pieces - 1) * kPC * 64;
-                ahead.scales += tile_scales - (p.pieces - 1) * kPC * SB;
+                ahead.tile += T * p.WR;
+                ahead.codes += T * tile_codes - (p.pieces - 1) * kPC * 64;
+                ahead.scales += T * tile_scales - (p.pieces - 1) * kPC * SB;
             }
         }
-        return raw;
     };
     auto stage_x = [&](int piece, int slot) {
         const int at = first + piece * kPC, nch = min(last - at, kPC);
@@ -118,14 +132,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
             auto src = [&](int m) { return p.x + m * p.ldx + at * kChunk; };
             RawBf16 first_tokens;
             first_tokens.load(p.M, nch, lane, src);
-            stage_tokens<FMT>(xs + slot * p.M * kTokenBytes, inv + slot * 8 * NT, first_tokens, p.M, nch, lane, src);
+            stage_tokens<FMT>(xs + slot * p.M * kTokenBytes, mine + kInvAt + slot * 8 * NT * 4, first_tokens, p.M, nch, lane, src);
         }
     };
 
     if (!p.pdl) ptx::griddep_wait();
-    uint2 raw[D - 1];
+    uint2 raw[D - 1][T] = {};
 #pragma unroll
-    for (int i = 0; i < D - 1; ++i) raw[i] = issue(i);
+    for (int i = 0; i < D - 1; ++i) issue(i, raw[i]);
     if (p.pdl) ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     if (p.resident)
@@ -134,23 +148,29 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
     int slot = 0;
     for (int group = 0; group < steps; group += kGroup) {
         const int count = min(kGroup, steps - group);
-        float tot[kGroup][1][NT][4] = {};
+        float tot[kGroup / T][T][NT][4] = {};
         for (int piece = 0; piece < p.pieces; ++piece) {
             if (!p.resident) stage_x(piece, 0);
             const int nch = min(last - first - piece * kPC, kPC), kept_at = p.resident ? piece : 0;
 #pragma unroll
-            for (int t = 0; t < kGroup; ++t) {
-                if (t >= count) break;
-                const uint2 cur = raw[0];
+            for (int t = 0; t < kGroup / T; ++t) {
+                if (t * T >= count) break;
+                uint2 cur[T];
 #pragma unroll
-                for (int i = 0; i + 2 < D; ++i) raw[i] = raw[i + 1];
-                raw[D - 2] = issue(slot == 0 ? D - 1 : slot - 1);
+                for (int i = 0; i < T; ++i) {
+                    cur[i] = raw[0][i];
+#pragma unroll
+                    for (int k = 0; k + 2 < D; ++k) raw[k][i] = raw[k + 1][i];
+                }
+                issue(slot == 0 ? D - 1 : slot - 1, raw[D - 2]);
                 if (nch > 0) {
-                    const float back = store_scales<FMT, GP>(table, cur, lane);
+                    const float back = store_scales<FMT, GP, T>(to_table, cur);
+                    uint32_t x[NT];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) x[j] = from_x[j] + kept_at * p.M * kTokenBytes;
                     cp_async_wait<D - 1>();
                     __syncwarp();
-                    stage_mma<FMT, GP, NT, 1>(tot[t], codes + slot * kCodeBytes, table, xs + kept_at * p.M * kTokenBytes,
-                                              inv + kept_at * 8 * NT, back, p.M, nch, lane);
+                    stage_mma<FMT, GP, NT, T>(tot[t], from_codes + slot * kSlot, from_table, x, from_inv + kept_at * 8 * NT * 4, back, nch);
                 }
                 __syncwarp();  // the slot, the table and x are rewritten by later stages
                 slot = slot + 1 == D ? 0 : slot + 1;
@@ -159,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
         // [warp][tile of the group][token][row]
 #pragma unroll
         for (int u = 0; u < kGroup; ++u)
-            if (u < count) store_sums<NT>(reinterpret_cast<float*>(codes + red_at + u * kSumBytes<NT>), tot[u][0], lane);
+            if (u < count) store_sums<NT>(mine + red_at + u * kSumBytes<NT>, tot[u / T][u % T], lane);
         __syncthreads();
         const int rows = count * p.WR * kTileRows;
         const int64_t row0 = static_cast<int64_t>(t0 + group * p.WR) * kTileRows;
@@ -178,20 +198,20 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
     }
 }
 
-template <int FMT, int GP, int NT, int D>
+template <int FMT, int GP, int NT, int T, int D>
 cudaError_t launch(const GemvParams& p, int sm_count, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_shared(gemv_w4_kernel<FMT, GP, NT, D>, allowed);
+    cudaError_t e = allow_shared(gemv_w4_kernel<FMT, GP, NT, T, D>, allowed);
     if (e != cudaSuccess) return e;
-    const int smem = kWarps * warp_bytes<GP, NT, D>(p.M, p.pieces, p.resident);
-    return launch_dependent(gemv_w4_kernel<FMT, GP, NT, D>, min((p.tiles + p.WR - 1) / p.WR, sm_count), kThreads, smem, stream, p);
+    const int smem = kWarps * warp_bytes<GP, NT, T, D>(p.M, p.pieces, p.resident);
+    return launch_dependent(gemv_w4_kernel<FMT, GP, NT, T, D>, min((p.tiles + p.WR - 1) / p.WR, sm_count), kThreads, smem, stream, p);
 }
 
-template <int FMT, int GP, int NT, int D>
+template <int FMT, int GP, int NT, int T, int D>
 cudaError_t launch_depth(GemvParams& p, int sm_count, cudaStream_t stream) {
-    p.resident = kWarps * warp_bytes<GP, NT, D>(p.M, p.pieces, true) <= kMaxBlockShared;
-    static_assert(kWarps * warp_bytes<GP, NT, D>(8 * NT, 1, false) <= kMaxBlockShared, "one stage of x fits");
-    return launch<FMT, GP, NT, D>(p, sm_count, stream);
+    p.resident = kWarps * warp_bytes<GP, NT, T, D>(p.M, p.pieces, true) <= kMaxBlockShared;
+    static_assert(kWarps * warp_bytes<GP, NT, T, D>(T == 2 ? kPairM : 8 * NT, 1, false) <= kMaxBlockShared, "one stage of x fits");
+    return launch<FMT, GP, NT, T, D>(p, sm_count, stream);
 }
 
 }  // namespace
@@ -215,8 +235,9 @@ cudaError_t launch_gemv_w4(const GemvW4Args& a, cudaStream_t stream) {
     p.pieces = ((p.chunks + p.WK - 1) / p.WK + kPC - 1) / kPC;
     p.pdl = a.pdl;
     return dispatch_format(a.format, a.group, [&](auto fmt, auto gp) {
-        return a.M <= 8 ? launch_depth<fmt(), gp(), 1, 3>(p, a.sm_count, stream)
-                        : launch_depth<fmt(), gp(), 2, 2>(p, a.sm_count, stream);
+        if (a.M <= kPairM) return launch_depth<fmt(), gp(), 1, 2, 2>(p, a.sm_count, stream);
+        if (a.M <= 8) return launch_depth<fmt(), gp(), 1, 1, 3>(p, a.sm_count, stream);
+        return launch_depth<fmt(), gp(), 2, 1, 2>(p, a.sm_count, stream);
     });
 }
 

@@ -56,7 +56,7 @@ struct Lists {
     int16_t* n;         // its pairs: 1 .. batch
     int entries;
 };
-__host__ __device__ constexpr int lists_bytes(int P) { return (6 * P * 2 + 15) / 16 * 16; }
+__host__ __device__ constexpr int lists_bytes(int P) { return (6 * P * 2 + 127) / 128 * 128; }
 __host__ __device__ constexpr int counts_bytes(int E) { return (E * 4 + 15) / 16 * 16; }
 
 // counts: E ints of shared memory, free afterwards.  The order of the pairs of
@@ -148,12 +148,14 @@ __device__ Lists build_lists(const MoeParams& p, int batch, uint8_t* mem, int* c
     return L;
 }
 
+constexpr int kInvBytes = 128;  // 8 factors, the next part aligned
+
 // Bytes of a warp: a ring of D stages of T tiles, their scale table, a stage of
 // tokens with its inverse scales (whose place the gate/up sums take, red bytes).
 template <int GP, int D, int T>
 __host__ __device__ constexpr int warp_bytes(int n, int red) {
     const int x = n * kTokenBytes;
-    return D * T * kCodeBytes + T * kTableBytes<GP> + 32 + (x > red ? x : red);
+    return D * T * kCodeBytes + T * kTableBytes<GP> + kInvBytes + (x > red ? x : red);
 }
 
 // ---- 1. gate / up ------------------------------------------------------------
@@ -163,16 +165,17 @@ constexpr int kUpRed = 2 * kSumBytes<1>;  // of a warp
 template <int FMT, int GP>
 __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_constant__ MoeParams p, int batch) {
     constexpr int SB = Format<FMT, GP>::kScaleBytes, D = kUpDepth, kSlot = 2 * kCodeBytes;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int P = p.M * p.S;
     uint8_t* base = smem + lists_bytes(P);
     const int mine_bytes = warp_bytes<GP, D, 2>(min(P, batch), kUpRed);
-    uint8_t* codes = base + warp * mine_bytes;  // [D][gate, up]
-    float* table = reinterpret_cast<float*>(codes + D * kSlot);
-    float* inv = reinterpret_cast<float*>(codes + D * kSlot + 2 * kTableBytes<GP>);
-    constexpr int kXsAt = D * kSlot + 2 * kTableBytes<GP> + 32;
-    uint8_t* xs = codes + kXsAt;
+    // a warp's memory: codes [D][gate, up], their scale tables, inv, x
+    constexpr int kTableAt = D * kSlot, kInvAt = kTableAt + 2 * kTableBytes<GP>, kXsAt = kInvAt + kInvBytes;
+    const uint32_t mine = ptx::smem_addr(base) + warp * mine_bytes, xs = mine + kXsAt;
+    const uint32_t to_codes = mine + code_dst(lane), to_table = mine + kTableAt + scale_dst<GP>(lane);
+    const uint32_t from_codes = mine + code_src(lane), from_table = mine + kTableAt + scale_src<GP>(lane);
+    const uint32_t from_inv = mine + kInvAt + inv_src(lane);
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const Lists L = build_lists(p, batch, smem, reinterpret_cast<int*>(base));
@@ -211,8 +214,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
     auto issue = [&](int slot, uint2 (&raw)[2]) {
         const int nch = min(last - first - ahead.piece * kPC, kPC);
         if (ahead.it.entry < L.entries && nch > 0) {
-            load_codes(codes + slot * kSlot, ahead.codes, ldc, kTileRows - 1, nch, lane);
-            load_codes(codes + slot * kSlot + kCodeBytes, ahead.codes + up_codes, ldc, kTileRows - 1, nch, lane);
+            load_codes(to_codes + slot * kSlot, ahead.codes, ldc, kTileRows - 1, nch, lane);
+            load_codes(to_codes + slot * kSlot + kCodeBytes, ahead.codes + up_codes, ldc, kTileRows - 1, nch, lane);
             raw[0] = load_scales<FMT, GP>(ahead.scales, nch, lane);
             raw[1] = load_scales<FMT, GP>(ahead.scales + up_scales, nch, lane);
         }
@@ -247,23 +250,24 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
     while (now.entry < L.entries) {
         const int entry = now.entry, j = now.j, n = L.n[entry], pf = L.first[entry];
         next(now);
+        const uint32_t x[1] = {xs + token_src(lane >> 2, n, lane)};
         float tot[2][1][4] = {};
         for (int piece = 0; piece < pieces; ++piece) {
             const int nch = min(last - first - piece * kPC, kPC);
-            const uint2 gate = raw[0][0], up = raw[0][1];
+            const uint2 cur[2] = {raw[0][0], raw[0][1]};
 #pragma unroll
             for (int i = 0; i + 2 < D; ++i) raw[i][0] = raw[i + 1][0], raw[i][1] = raw[i + 1][1];
             issue(slot == 0 ? D - 1 : slot - 1, raw[D - 2]);
             if (nch > 0) {
-                stage_tokens<FMT>(xs, inv, tokens, n, nch, lane, source(entry, piece));
+                stage_tokens<FMT>(xs, mine + kInvAt, tokens, n, nch, lane, source(entry, piece));
                 if (piece + 1 < pieces)
                     load_tokens(entry, piece + 1);
                 else
                     load_tokens(now.entry, 0);
-                const float back = store_scales<FMT, GP>(table, gate, up, lane);
+                const float back = store_scales<FMT, GP, 2>(to_table, cur);
                 cp_async_wait<D - 1>();
                 __syncwarp();
-                stage_mma<FMT, GP, 1, 2>(tot, codes + slot * kSlot, table, xs, inv, back, n, nch, lane);
+                stage_mma<FMT, GP, 1, 2>(tot, from_codes + slot * kSlot, from_table, x, from_inv, back, nch);
             } else if (piece + 1 == pieces) {
                 load_tokens(now.entry, 0);
             }
@@ -271,8 +275,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
             slot = slot + 1 == D ? 0 : slot + 1;
         }
         // [warp][gate, up][pair][row]
-        store_sums<1>(reinterpret_cast<float*>(xs), tot[0], lane);
-        store_sums<1>(reinterpret_cast<float*>(xs + kSumBytes<1>), tot[1], lane);
+        store_sums<1>(xs, tot[0], lane);
+        store_sums<1>(xs + kSumBytes<1>, tot[1], lane);
         __syncthreads();
         if (threadIdx.x < kMaxBatch * kTileRows) {  // 16 lanes a pair
             const int i = min(static_cast<int>(threadIdx.x) / kTileRows, n - 1), row = threadIdx.x % kTileRows;
@@ -304,20 +308,22 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
 constexpr int kDownDepth = 3;
 
 // the pairs' products for 16 rows, and their routing weights
-__host__ __device__ constexpr int out_bytes(int P) { return (P * (kTileRows + 1) * 4 + 15) / 16 * 16; }
+__host__ __device__ constexpr int out_bytes(int P) { return (P * (kTileRows + 1) * 4 + 127) / 128 * 128; }
 
 template <int FMT, int GP>
 __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_constant__ MoeParams p, int batch) {
     constexpr int SB = Format<FMT, GP>::kScaleBytes, D = kDownDepth;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = p.M * p.S;
     float* out = reinterpret_cast<float*>(smem + lists_bytes(P));  // [P][16]
     uint8_t* base = smem + lists_bytes(P) + out_bytes(P);
-    uint8_t* codes = base + warp * warp_bytes<GP, kDownDepth, 1>(min(P, batch), 0);
-    float* table = reinterpret_cast<float*>(codes + D * kCodeBytes);
-    float* inv = reinterpret_cast<float*>(codes + D * kCodeBytes + kTableBytes<GP>);
-    uint8_t* xs = codes + D * kCodeBytes + kTableBytes<GP> + 32;
+    // a warp's memory: codes [D], the scale table, inv, the entry's a
+    constexpr int kTableAt = D * kCodeBytes, kInvAt = kTableAt + kTableBytes<GP>;
+    const uint32_t mine = ptx::smem_addr(base) + warp * warp_bytes<GP, D, 1>(min(P, batch), 0), xs = mine + kInvAt + kInvBytes;
+    const uint32_t to_codes = mine + code_dst(lane), to_table = mine + kTableAt + scale_dst<GP>(lane);
+    const uint32_t from_codes = mine + code_src(lane), from_table = mine + kTableAt + scale_src<GP>(lane);
+    const uint32_t from_inv = mine + kInvAt + inv_src(lane);
     // the pairs' routing weights, 0 for an invalid id (the first launch has
     // waited for whatever wrote the routing)
     float* weight = out + P * kTileRows;
@@ -348,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
         uint2 raw = make_uint2(0, 0);
         if (ahead.tile < tiles && ahead.entry < L.entries) {
             const int nch = min(chunks - ahead.piece * kPC, kPC);
-            load_codes(codes + slot * kCodeBytes, ahead.codes, ldc, kTileRows - 1, nch, lane);
+            load_codes(to_codes + slot * kCodeBytes, ahead.codes, ldc, kTileRows - 1, nch, lane);
             raw = load_scales<FMT, GP>(ahead.scales, nch, lane);
         }
         cp_async_commit();
@@ -386,26 +392,27 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
         __syncthreads();
         for (int entry = warp; entry < L.entries; entry += kWarps) {
             const int n = L.n[entry], pf = L.first[entry];
+            const uint32_t x[1] = {xs + token_src(lane >> 2, n, lane)};
             float tot[1][1][4] = {};
             for (int piece = 0; piece < pieces; ++piece) {
                 const int nch = min(chunks - piece * kPC, kPC);
-                tokens.store(xs, inv, 0, n, lane);
+                tokens.store(xs, mine + kInvAt, 0, n, lane);
                 for (int i0 = RawFp16::kTokens; i0 < n; i0 += RawFp16::kTokens) {
                     load_tokens(entry, piece, i0);
-                    tokens.store(xs, inv, i0, n, lane);
+                    tokens.store(xs, mine + kInvAt, i0, n, lane);
                 }
                 if (piece + 1 < pieces)
                     load_tokens(entry, piece + 1, 0);
                 else
                     load_tokens(entry + kWarps < L.entries ? entry + kWarps : warp, 0, 0);
-                const uint2 cur = raw[0];
+                const uint2 cur[1] = {raw[0]};
 #pragma unroll
                 for (int i = 0; i + 2 < D; ++i) raw[i] = raw[i + 1];
                 raw[D - 2] = issue(slot == 0 ? D - 1 : slot - 1);
-                const float back = store_scales<FMT, GP>(table, cur, lane);
+                const float back = store_scales<FMT, GP, 1>(to_table, cur);
                 cp_async_wait<D - 1>();
                 __syncwarp();
-                stage_mma<FMT, GP, 1, 1>(tot, codes + slot * kCodeBytes, table, xs, inv, back, n, nch, lane);
+                stage_mma<FMT, GP, 1, 1>(tot, from_codes + slot * kCodeBytes, from_table, x, from_inv, back, nch);
                 __syncwarp();  // the slot, the table and the tokens are rewritten by later stages
                 slot = slot + 1 == D ? 0 : slot + 1;
             }
@@ -434,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
 // multiprocessor.
 template <typename F>
 int batch_of(F&& bytes) {
-    constexpr int kHalf = kMaxSmShared / 2 - 1024 - 64;  // a block's reserved and static shared memory
+    constexpr int kHalf = kMaxSmShared / 2 - 1024 - 128;  // a block's reserved and static shared memory
     return bytes(kMaxBatch) > kHalf && bytes(kMaxBatch / 2) <= kHalf ? kMaxBatch / 2 : kMaxBatch;
 }
 
