@@ -35,6 +35,7 @@ FP8BS_ROUTE_MAX_E = 1024
 FP8BS_ROUTE_MAX_K = 32
 FP8BS_ROUTE_MAX_M = 1024
 FP8BS_MOE_W4_MAX_I = 8192
+FP8BS_MOE_W4_MAX_H = 32768
 
 STATUS = {
     0: "FP8BS_OK", -1: "FP8BS_ERR_ARG", -2: "FP8BS_ERR_SHAPE", -3: "FP8BS_ERR_ALIGN",

@@ -352,7 +352,7 @@ int fp8bs_moe_w4a16(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const 
                     void* stream) {
     if (!w4_ok(format, group)) return FP8BS_ERR_ARG;
     if (fp8bs_moe_w4a16_workspace_bytes(M, S, I) == 0 || E < 1 || E > FP8BS_MOE_MAX_EXPERTS || H < kTile ||
-        H % kTile != 0 || H > kMaxDim)
+        H % kTile != 0 || H > FP8BS_MOE_W4_MAX_H)
         return FP8BS_ERR_SHAPE;
     if (M == 0) return FP8BS_OK;
     if (!x || !topk_ids || !topk_w || !w13 || !s13 || !w2 || !s2 || !y || !workspace) return FP8BS_ERR_ARG;

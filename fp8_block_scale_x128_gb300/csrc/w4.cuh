@@ -63,7 +63,7 @@ constexpr int kCodePitch = kPC * 64 + 16;  // bytes of a code row
 constexpr int kCodeBytes = kTileRows * kCodePitch;
 constexpr int kTokenBytes = kStageK * 2;   // fp16 of a token
 template <int GP>
-constexpr int kScalePitch = kPC * GP + 4;  // floats of a scale row
+constexpr int kScalePitch = kPC * GP;  // floats of a scale row
 template <int GP>
 constexpr int kTableBytes = kTileRows * kScalePitch<GP> * 4;
 
@@ -142,9 +142,10 @@ __device__ __forceinline__ uint2 load_scales(const uint8_t* src, int nch, int la
     return w;
 }
 
-// Their fp32 values into the stage's table [row][chunk * GP + group].  A stage with a scale of 2^97 or more has its table divided
-// by 2^64 (kBigScale), so that a group's sum, up to 2^27 at the activations'
-// fixed scaling, times its scale stays finite; returns the factor to put back.
+// Their fp32 values into the stage's table [row][chunk * GP + group].  A stage
+// with a scale of 2^97 or more has its table divided by 2^64 (kBigScale), so
+// that a group's sum, up to 2^27 at the activations' fixed scaling, times its
+// scale stays finite; returns the factor to put back.
 constexpr float kBigScale = 0x1p64f;
 template <int FMT>
 __device__ __forceinline__ bool big_scale(uint2 raw) {  // some scale's three top exponent bits all set

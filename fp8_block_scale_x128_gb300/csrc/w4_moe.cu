@@ -7,8 +7,10 @@
 //   y[m] = bf16(sum over s, in slot order, of tw[m, s] * (a . w2[e]^T))
 //
 // 1. gate/up: items of (expert, up to 8 of its pairs, 16 gate rows and the 16
-//    up rows that go with them); the 8 warps of a block split H, their sums are
-//    added in warp order and the activation applied to the whole sum.
+//    up rows that go with them), dealt out in contiguous runs, so that a block
+//    stages an expert's tokens once for its run; the 8 warps of a block split
+//    H, their sums are added in warp order and the activation applied to the
+//    whole sum.
 // 2. down: a block owns 16 rows of the output for every token, its warps deal
 //    out the experts; the pairs' products meet in shared memory and are summed
 //    in slot order.  No partial sums in global memory, no atomics on values.
@@ -148,31 +150,33 @@ __device__ Lists build_lists(const MoeParams& p, int batch, uint8_t* mem, int* c
     return L;
 }
 
-constexpr int kInvBytes = 128;  // 8 factors, the next part aligned
-
-// Bytes of a warp: a ring of D stages of T tiles, their scale table, a stage of
-// tokens with its inverse scales (whose place the gate/up sums take, red bytes).
-template <int GP, int D, int T>
-__host__ __device__ constexpr int warp_bytes(int n, int red) {
-    const int x = n * kTokenBytes;
-    return D * T * kCodeBytes + T * kTableBytes<GP> + kInvBytes + (x > red ? x : red);
-}
-
 // ---- 1. gate / up ------------------------------------------------------------
 constexpr int kUpDepth = 2;
-constexpr int kUpRed = 2 * kSumBytes<1>;  // of a warp
+
+// Bytes of a warp: the ring of gate and up tiles, their scale tables (whose
+// place the sums take between items), the inverse scales and the tokens of the
+// whole slice (pieces stages) for n pairs.
+template <int GP>
+constexpr int kUpTableBytes = 2 * (kTableBytes<GP> > kSumBytes<1> ? kTableBytes<GP> : kSumBytes<1>);
+__host__ __device__ constexpr int up_inv_bytes(int pieces) { return (pieces * kMaxBatch * 4 + 127) / 128 * 128; }
+template <int GP>
+__host__ __device__ constexpr int up_bytes(int n, int pieces) {
+    return kUpDepth * 2 * kCodeBytes + kUpTableBytes<GP> + up_inv_bytes(pieces) + pieces * n * kTokenBytes;
+}
+__host__ __device__ constexpr int up_pieces(int H) { return ((H / kChunk + kWarps - 1) / kWarps + kPC - 1) / kPC; }
 
 template <int FMT, int GP>
 __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_constant__ MoeParams p, int batch) {
     constexpr int SB = Format<FMT, GP>::kScaleBytes, D = kUpDepth, kSlot = 2 * kCodeBytes;
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int P = p.M * p.S;
+    const int P = p.M * p.S, kept = min(P, batch), pieces = up_pieces(p.H);
     uint8_t* base = smem + lists_bytes(P);
-    const int mine_bytes = warp_bytes<GP, D, 2>(min(P, batch), kUpRed);
-    // a warp's memory: codes [D][gate, up], their scale tables, inv, x
-    constexpr int kTableAt = D * kSlot, kInvAt = kTableAt + 2 * kTableBytes<GP>, kXsAt = kInvAt + kInvBytes;
-    const uint32_t mine = ptx::smem_addr(base) + warp * mine_bytes, xs = mine + kXsAt;
+    const int mine_bytes = up_bytes<GP>(kept, pieces);
+    // a warp's memory: codes [D][gate, up], their scale tables, inv [pieces][8],
+    // x [pieces][kept]
+    constexpr int kTableAt = D * kSlot, kInvAt = kTableAt + kUpTableBytes<GP>;
+    const uint32_t mine = ptx::smem_addr(base) + warp * mine_bytes, xs = mine + kInvAt + up_inv_bytes(pieces);
     const uint32_t to_codes = mine + code_dst(lane), to_table = mine + kTableAt + scale_dst<GP>(lane);
     const uint32_t from_codes = mine + code_src(lane), from_table = mine + kTableAt + scale_src<GP>(lane);
     const uint32_t from_inv = mine + kInvAt + inv_src(lane);
@@ -182,75 +186,87 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
 
     const int chunks = p.H / kChunk;
     const int first = warp * chunks / kWarps, last = (warp + 1) * chunks / kWarps;
-    const int pieces = ((chunks + kWarps - 1) / kWarps + kPC - 1) / kPC;
     const int per = p.I / kTileRows;
     const int64_t ldc = p.H / 2, lds = static_cast<int64_t>(chunks) * SB;
     const int64_t up_codes = p.I * ldc, up_scales = p.I * lds;  // from a gate tile to its up tile
 
-    // an item is a tile j of an entry; the block's items are gridDim.x apart
-    struct Item {
-        int entry, j;
-    };
-    const int step_entry = gridDim.x / per, step_j = gridDim.x - step_entry * per;
-    auto next = [&](Item& it) {
-        it.entry += step_entry;
-        if ((it.j += step_j) >= per) it.j -= per, ++it.entry;
-    };
-    Item now = {static_cast<int>(blockIdx.x) / per, 0};
-    now.j = blockIdx.x - now.entry * per;
-    // a warp's stages: the items of the block, in an item the pieces of the slice
+    // the block's run of items (entry, tile j)
+    const int64_t items = static_cast<int64_t>(L.entries) * per;
+    const int item0 = static_cast<int>(blockIdx.x * items / gridDim.x);
+    const int count = static_cast<int>((blockIdx.x + 1) * items / gridDim.x) - item0;
+    int entry = item0 / per, j = item0 - entry * per;
+
+    // a warp's stages: the items of the run, in an item the pieces of the slice
     struct Cursor {
-        Item it;
-        int piece;
-        const uint8_t *codes, *scales;  // this lane's, of the gate tile
+        int entry, j, piece, left;
+        const uint8_t *gate, *up, *gate_scales, *up_scales;  // this lane's
     };
-    Cursor ahead = {now, 0, nullptr, nullptr};
+    Cursor ahead = {entry, j, 0, count, nullptr, nullptr, nullptr, nullptr};
     auto locate = [&]() {
-        if (ahead.it.entry >= L.entries) return;
-        const int64_t row = static_cast<int64_t>(L.expert[ahead.it.entry]) * 2 * p.I + ahead.it.j * kTileRows;
-        ahead.codes = p.w13 + (row + (lane >> 3)) * ldc + first * 64 + (lane & 7) * 16;
-        ahead.scales = p.s13 + (row + (lane >> 1)) * lds + (first + (lane & 1)) * SB;
+        if (ahead.left <= 0) return;
+        const int64_t row = static_cast<int64_t>(L.expert[ahead.entry]) * 2 * p.I + ahead.j * kTileRows;
+        ahead.gate = p.w13 + (row + (lane >> 3)) * ldc + first * 64 + (lane & 7) * 16;
+        ahead.up = ahead.gate + up_codes;
+        ahead.gate_scales = p.s13 + (row + (lane >> 1)) * lds + (first + (lane & 1)) * SB;
+        ahead.up_scales = ahead.gate_scales + up_scales;
     };
+    const int64_t next_codes = kTileRows * ldc - (pieces - 1) * kPC * 64, next_scales = kTileRows * lds - (pieces - 1) * kPC * SB;
     auto issue = [&](int slot, uint2 (&raw)[2]) {
         const int nch = min(last - first - ahead.piece * kPC, kPC);
-        if (ahead.it.entry < L.entries && nch > 0) {
-            load_codes(to_codes + slot * kSlot, ahead.codes, ldc, kTileRows - 1, nch, lane);
-            load_codes(to_codes + slot * kSlot + kCodeBytes, ahead.codes + up_codes, ldc, kTileRows - 1, nch, lane);
-            raw[0] = load_scales<FMT, GP>(ahead.scales, nch, lane);
-            raw[1] = load_scales<FMT, GP>(ahead.scales + up_scales, nch, lane);
+        if (ahead.left > 0 && nch > 0) {
+            load_codes(to_codes + slot * kSlot, ahead.gate, ldc, kTileRows - 1, nch, lane);
+            load_codes(to_codes + slot * kSlot + kCodeBytes, ahead.up, ldc, kTileRows - 1, nch, lane);
+            raw[0] = load_scales<FMT, GP>(ahead.gate_scales, nch, lane);
+            raw[1] = load_scales<FMT, GP>(ahead.up_scales, nch, lane);
         }
         cp_async_commit();
         if (++ahead.piece < pieces) {
-            ahead.codes += kPC * 64;
-            ahead.scales += kPC * SB;
+            ahead.gate += kPC * 64;
+            ahead.up += kPC * 64;
+            ahead.gate_scales += kPC * SB;
+            ahead.up_scales += kPC * SB;
+            return;
+        }
+        ahead.piece = 0;
+        --ahead.left;
+        if (++ahead.j < per) {
+            ahead.gate += next_codes;
+            ahead.up += next_codes;
+            ahead.gate_scales += next_scales;
+            ahead.up_scales += next_scales;
         } else {
-            ahead.piece = 0;
-            next(ahead.it);
+            ahead.j = 0;
+            ++ahead.entry;
             locate();
         }
     };
-    auto source = [&](int entry, int piece) {
-        const int16_t* tokens = L.tokens + L.first[entry];
-        const uint16_t* x = p.x + (first + piece * kPC) * kChunk;
-        const int64_t ldx = p.ldx;
-        return [=](int i) { return x + tokens[i] * ldx; };
-    };
-    RawBf16 tokens;
-    auto load_tokens = [&](int entry, int piece) {
-        const int nch = min(last - first - piece * kPC, kPC);
-        if (entry < L.entries && nch > 0) tokens.load(L.n[entry], nch, lane, source(entry, piece));
-    };
 
     locate();
-    uint2 raw[D - 1][2];
+    uint2 raw[D - 1][2] = {};
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) issue(i, raw[i]);
-    load_tokens(now.entry, 0);
-    int slot = 0;
-    while (now.entry < L.entries) {
-        const int entry = now.entry, j = now.j, n = L.n[entry], pf = L.first[entry];
-        next(now);
-        const uint32_t x[1] = {xs + token_src(lane >> 2, n, lane)};
+    int slot = 0, staged = -1, n = 0, pf = 0;
+    uint32_t x0 = 0;
+    for (int item = 0; item < count; ++item) {
+        if (entry != staged) {  // the expert's tokens, two pieces' loads in flight together
+            staged = entry;
+            n = L.n[entry];
+            pf = L.first[entry];
+            x0 = xs + token_src(lane >> 2, n, lane);
+            auto source = [&](int piece) {
+                const int16_t* tokens = L.tokens + pf;
+                const uint16_t* x = p.x + (first + piece * kPC) * kChunk;
+                return [=](int i) { return x + tokens[i] * p.ldx; };
+            };
+            for (int q = 0; q < pieces; q += 2) {
+                const int nch0 = min(last - first - q * kPC, kPC), nch1 = min(last - first - (q + 1) * kPC, kPC);
+                RawBf16 t0, t1;
+                if (nch0 > 0) t0.load(n, nch0, lane, source(q));
+                if (nch1 > 0) t1.load(n, nch1, lane, source(q + 1));
+                if (nch0 > 0) stage_tokens<FMT>(xs + q * kept * kTokenBytes, mine + kInvAt + q * kMaxBatch * 4, t0, n, nch0, lane, source(q));
+                if (nch1 > 0) stage_tokens<FMT>(xs + (q + 1) * kept * kTokenBytes, mine + kInvAt + (q + 1) * kMaxBatch * 4, t1, n, nch1, lane, source(q + 1));
+            }
+        }
         float tot[2][1][4] = {};
         for (int piece = 0; piece < pieces; ++piece) {
             const int nch = min(last - first - piece * kPC, kPC);
@@ -259,28 +275,22 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
             for (int i = 0; i + 2 < D; ++i) raw[i][0] = raw[i + 1][0], raw[i][1] = raw[i + 1][1];
             issue(slot == 0 ? D - 1 : slot - 1, raw[D - 2]);
             if (nch > 0) {
-                stage_tokens<FMT>(xs, mine + kInvAt, tokens, n, nch, lane, source(entry, piece));
-                if (piece + 1 < pieces)
-                    load_tokens(entry, piece + 1);
-                else
-                    load_tokens(now.entry, 0);
                 const float back = store_scales<FMT, GP, 2>(to_table, cur);
+                const uint32_t x[1] = {x0 + piece * kept * kTokenBytes};
                 cp_async_wait<D - 1>();
                 __syncwarp();
-                stage_mma<FMT, GP, 1, 2>(tot, from_codes + slot * kSlot, from_table, x, from_inv, back, nch);
-            } else if (piece + 1 == pieces) {
-                load_tokens(now.entry, 0);
+                stage_mma<FMT, GP, 1, 2>(tot, from_codes + slot * kSlot, from_table, x, from_inv + piece * kMaxBatch * 4, back, nch);
             }
-            __syncwarp();  // the slot, the table and the tokens are rewritten by later stages
+            __syncwarp();  // the slot and the table are rewritten by later stages
             slot = slot + 1 == D ? 0 : slot + 1;
         }
         // [warp][gate, up][pair][row]
-        store_sums<1>(xs, tot[0], lane);
-        store_sums<1>(xs + kSumBytes<1>, tot[1], lane);
+        store_sums<1>(mine + kTableAt, tot[0], lane);
+        store_sums<1>(mine + kTableAt + kSumBytes<1>, tot[1], lane);
         __syncthreads();
         if (threadIdx.x < kMaxBatch * kTileRows) {  // 16 lanes a pair
             const int i = min(static_cast<int>(threadIdx.x) / kTileRows, n - 1), row = threadIdx.x % kTileRows;
-            const uint8_t* s = base + kXsAt + (i * kSumPitch + row) * 4;
+            const uint8_t* s = base + kTableAt + (i * kSumPitch + row) * 4;
             float g = 0.0f, v = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
@@ -301,11 +311,20 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
             }
         }
         __syncthreads();  // the sums' place is rewritten by the next item
+        if (++j == per) j = 0, ++entry;
     }
 }
 
 // ---- 2. down -----------------------------------------------------------------
 constexpr int kDownDepth = 3;
+
+// Bytes of a warp: the ring, the scale table, the inverse scales and a stage of
+// a for n pairs.
+constexpr int kInvBytes = 128;  // 8 factors, the next part aligned
+template <int GP>
+__host__ __device__ constexpr int down_bytes(int n) {
+    return kDownDepth * kCodeBytes + kTableBytes<GP> + kInvBytes + n * kTokenBytes;
+}
 
 // the pairs' products for 16 rows, and their routing weights
 __host__ __device__ constexpr int out_bytes(int P) { return (P * (kTileRows + 1) * 4 + 127) / 128 * 128; }
@@ -320,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
     uint8_t* base = smem + lists_bytes(P) + out_bytes(P);
     // a warp's memory: codes [D], the scale table, inv, the entry's a
     constexpr int kTableAt = D * kCodeBytes, kInvAt = kTableAt + kTableBytes<GP>;
-    const uint32_t mine = ptx::smem_addr(base) + warp * warp_bytes<GP, D, 1>(min(P, batch), 0), xs = mine + kInvAt + kInvBytes;
+    const uint32_t mine = ptx::smem_addr(base) + warp * down_bytes<GP>(min(P, batch)), xs = mine + kInvAt + kInvBytes;
     const uint32_t to_codes = mine + code_dst(lane), to_table = mine + kTableAt + scale_dst<GP>(lane);
     const uint32_t from_codes = mine + code_src(lane), from_table = mine + kTableAt + scale_src<GP>(lane);
     const uint32_t from_inv = mine + kInvAt + inv_src(lane);
@@ -437,12 +456,19 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_c
     }
 }
 
-// The pairs of an entry: half as many where that lets two blocks share a
-// multiprocessor.
+// The pairs of an entry and the blocks of a multiprocessor: two blocks, with as
+// many pairs as then fit, unless the experts have more than twice as many on
+// average (their codes would be fetched and decoded over and over): then one.
 template <typename F>
-int batch_of(F&& bytes) {
-    constexpr int kHalf = kMaxSmShared / 2 - 1024 - 128;  // a block's reserved and static shared memory
-    return bytes(kMaxBatch) > kHalf && bytes(kMaxBatch / 2) <= kHalf ? kMaxBatch / 2 : kMaxBatch;
+int batch_of(const MoeParams& p, F&& bytes, int& per_sm) {
+    constexpr int kHalf = kMaxSmShared / 2 - 1024 - 128;  // less a block's reserved and static shared memory
+    int batch = kMaxBatch;
+    while (batch > 0 && bytes(batch) > kHalf) --batch;
+    per_sm = 2;
+    if (batch > 0 && (batch == kMaxBatch || p.M * p.S <= 2 * batch * p.E)) return batch;
+    per_sm = 1;
+    for (batch = kMaxBatch; batch > 1 && bytes(batch) > kMaxBlockShared; --batch) {}
+    return batch;
 }
 
 template <int FMT, int GP>
@@ -450,12 +476,13 @@ cudaError_t launch_up(const MoeParams& p, int sm_count, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_shared(moe_w4_up_kernel<FMT, GP>, allowed);
     if (e != cudaSuccess) return e;
-    const int P = p.M * p.S;
+    const int P = p.M * p.S, pieces = up_pieces(p.H);
     auto bytes = [&](int batch) {
-        return lists_bytes(P) + max(counts_bytes(p.E), kWarps * warp_bytes<GP, kUpDepth, 2>(min(P, batch), kUpRed));
+        return lists_bytes(P) + max(counts_bytes(p.E), kWarps * up_bytes<GP>(min(P, batch), pieces));
     };
-    const int batch = batch_of(bytes), smem = bytes(batch);
-    const int per_sm = min(2, kMaxSmShared / (smem + 1024));
+    int per_sm;
+    const int batch = batch_of(p, bytes, per_sm), smem = bytes(batch);
+    if (smem > kMaxBlockShared) return cudaErrorInvalidValue;
     const int64_t most = static_cast<int64_t>(P) * (p.I / kTileRows);
     const int grid = static_cast<int>(min(most, static_cast<int64_t>(sm_count) * per_sm));
     return launch_dependent(moe_w4_up_kernel<FMT, GP>, grid, kThreads, smem, stream, p, batch);
@@ -468,10 +495,11 @@ cudaError_t launch_down(const MoeParams& p, int sm_count, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int P = p.M * p.S;
     auto bytes = [&](int batch) {
-        return lists_bytes(P) + out_bytes(P) + max(counts_bytes(p.E), kWarps * warp_bytes<GP, kDownDepth, 1>(min(P, batch), 0));
+        return lists_bytes(P) + out_bytes(P) + max(counts_bytes(p.E), kWarps * down_bytes<GP>(min(P, batch)));
     };
-    const int batch = batch_of(bytes), smem = bytes(batch), per_sm = min(2, kMaxSmShared / (smem + 1024));
-    return launch_dependent(moe_w4_down_kernel<FMT, GP>, min(p.H / kTileRows, sm_count * per_sm), kThreads, smem, stream, p, batch);
+    int per_sm;
+    const int batch = batch_of(p, bytes, per_sm);
+    return launch_dependent(moe_w4_down_kernel<FMT, GP>, min(p.H / kTileRows, sm_count * per_sm), kThreads, bytes(batch), stream, p, batch);
 }
 
 }  // namespace

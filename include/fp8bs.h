@@ -430,7 +430,8 @@ int fp8bs_moe_route(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const 
                     int64_t k, int renorm, int shared, int32_t* topk_ids, float* topk_w,
                     void* workspace, size_t workspace_bytes, void* stream);
 
-#define FP8BS_MOE_W4_MAX_I 8192 /* intermediate size per expert */
+#define FP8BS_MOE_W4_MAX_I 8192  /* intermediate size per expert */
+#define FP8BS_MOE_W4_MAX_H 32768 /* hidden size                  */
 
 /* Workspace bytes of fp8bs_moe_w4a16: a 256-byte error word, then M*S x I fp32.
  * Returns 0 for an unsupported shape. */
@@ -439,12 +440,12 @@ size_t fp8bs_moe_w4a16_workspace_bytes(int64_t M, int64_t S, int64_t I);
 /* One MoE layer at decode sizes on 4-bit weights, in two launches.  Per token m
  * and slot s, with e = topk_ids[m, s]:
  *   h    = x[m] . w13[e]^T   (gate rows 0..I-1 over the up rows I..2I-1)
- *   a    = silu(h_gate) * h_up (fp32; carried in fp16 after an exact
- *                            power-of-two scaling per pair and 512 k)
+ *   a    = silu(h_gate) * h_up (rounded to fp16 with an exponent per 16
+ *                            values: 2^-12 of each)
  *   y[m] = bf16(sum over s, in slot order, of topk_w[m, s] * (a . w2[e]^T))
  *   x        : bf16 [M, H], row stride ldx elements; x and ldx*2 16-byte aligned.
  *   M, S     : M >= 0 (0 is a no-op), S >= 1, M * S <= FP8BS_MOE_MAX_PAIRS.
- *   H, I     : multiples of 128, I <= FP8BS_MOE_W4_MAX_I, H at most 2^24.
+ *   H, I     : multiples of 128, up to FP8BS_MOE_W4_MAX_H and _MAX_I.
  *   topk_ids : int32 [M, S]; an id outside [0, E) makes that slot contribute
  *              nothing and records FP8BS_ERR_DEVICE in the workspace error word.
  *   topk_w   : fp32 [M, S].

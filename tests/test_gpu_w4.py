@@ -346,6 +346,10 @@ def test_moe_wide_hidden_size(dev):
     assert run_moe(dev, 4, 5, 12, 5120, 128, INT4, 64, seed=310) == 0
 
 
+def test_moe_largest_hidden_size(dev):
+    assert run_moe(dev, 2, 2, 2, 32768, 128, MXFP4, 32, seed=320) == 0
+
+
 def test_moe_experts_with_many_pairs(dev):
     M, S, E = 40, 3, 5
     ids = np.tile(np.array([[0, 1, 4]], np.int32), (M, 1))

@@ -89,7 +89,7 @@ def moe(L, x=P, M=4, H=4096, ldx=4096, ids=P, tw=P, S=11, w13=P, s13=P, w2=P, s2
 @pytest.mark.parametrize("kw,status", [
     (dict(fmt=5), ARG), (dict(group=128), ARG), (dict(M=-1), SHAPE), (dict(S=0), SHAPE), (dict(M=94), SHAPE),
     (dict(M=1 << 40, S=1 << 40), SHAPE), (dict(E=0), SHAPE), (dict(E=4097), SHAPE), (dict(I=200), SHAPE),
-    (dict(I=8320), SHAPE), (dict(H=4000), SHAPE), (dict(x=None), ARG), (dict(ids=None), ARG), (dict(tw=None), ARG),
+    (dict(I=8320), SHAPE), (dict(H=4000), SHAPE), (dict(H=32896, ldx=32896), SHAPE), (dict(x=None), ARG), (dict(ids=None), ARG), (dict(tw=None), ARG),
     (dict(w13=None), ARG), (dict(s13=None), ARG), (dict(w2=None), ARG), (dict(s2=None), ARG), (dict(y=None), ARG),
     (dict(ws=None), ARG), (dict(ldx=4088), ARG), (dict(x=P + 8), ALIGN), (dict(ldx=4100), ALIGN),
     (dict(ids=P + 2), ALIGN), (dict(w13=P + 8), ALIGN), (dict(s13=P + 4), ALIGN), (dict(w2=P + 8), ALIGN),
