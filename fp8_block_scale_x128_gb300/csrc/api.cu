@@ -276,7 +276,7 @@ int fp8bs_gemv_w4a16(const uint16_t* x, int64_t M, int64_t ldx, const uint8_t* c
         return FP8BS_ERR_SHAPE;
     if (M == 0) return FP8BS_OK;
     if (!x || !codes || !scales || !y) return FP8BS_ERR_ARG;
-    if (ldx < K || ldc < K / 2 || lds < K / group || ldy < N) return FP8BS_ERR_ARG;
+    if (ldx < K || ldc < K / 2 || ldc > FP8BS_W4_MAX_LDC || lds < K / group || ldy < N) return FP8BS_ERR_ARG;
     const int64_t size = w4_scale_size(format), chunk = size * (kTile / group);
     if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(codes, 16) || ldc % 16 != 0 || !aligned(scales, chunk) ||
         lds * size % chunk != 0 || !aligned(y, 2))

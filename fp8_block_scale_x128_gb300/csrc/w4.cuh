@@ -102,25 +102,29 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// p + a * b bytes as one wide multiply-add.
+__device__ __forceinline__ const uint8_t* at(const uint8_t* p, uint32_t a, uint32_t b) {
+    return p + static_cast<uint64_t>(a) * b;
+}
+
 // Start the copy of a stage: nch (1..kPC) chunks of 16 code rows.  src points
 // at this lane's first 16 bytes: row lane / 8 of the tile, byte 16 (lane % 8)
 // of the stage, dst at their place (code_dst); it takes the rows 4, 8 and 12
 // further on as well.  last: the tile's last row; rows past it repeat it (their
 // outputs are dropped), so every access stays inside the weight.
 __device__ __forceinline__ uint32_t code_dst(int lane) { return (lane >> 3) * kCodePitch + (lane & 7) * 16; }
-__device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* src, int64_t ldc, int last, int nch, int lane) {
+__device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* src, uint32_t ldc, int last, int nch, int lane) {
     if ((lane & 7) >= nch * 4) return;
     if (last == kTileRows - 1) {
-        const int64_t step = 4 * ldc;
         cp_async16(dst, src);
-        cp_async16(dst + 4 * kCodePitch, src += step);
-        cp_async16(dst + 8 * kCodePitch, src += step);
-        cp_async16(dst + 12 * kCodePitch, src += step);
+        cp_async16(dst + 4 * kCodePitch, at(src, ldc, 4));
+        cp_async16(dst + 8 * kCodePitch, at(src, ldc, 8));
+        cp_async16(dst + 12 * kCodePitch, at(src, ldc, 12));
     } else {
 #pragma unroll
         for (int j = 0; j < kTileRows / 4; ++j) {
             const int r = (lane >> 3) + 4 * j;
-            cp_async16(dst + 4 * j * kCodePitch, src + (min(r, last) - (lane >> 3)) * ldc);
+            cp_async16(dst + 4 * j * kCodePitch, src + static_cast<int64_t>(min(r, last) - (lane >> 3)) * ldc);
         }
     }
 }
@@ -257,9 +261,11 @@ struct RawFp16 {
     static constexpr int kTokens = 4;
     uint4 r[kTokens];
     int e[kTokens];
-    // src(i): token i's first value of the stage; exp(i): its first exponent
-    template <typename Src, typename Exp>
-    __device__ __forceinline__ void load(int n, int nch, int lane, Src src, Exp exp) {
+    // a, ae: this lane's values and exponent of pair 0's stage, la and le bytes
+    // a pair; pair(i): the i-th pair
+    template <typename Pair>
+    __device__ __forceinline__ void load(const uint8_t* a, const uint8_t* ae, uint32_t la, uint32_t le, int n, int nch,
+                                         int lane, Pair pair) {
         const bool in = lane < nch * (kChunk / 8);
 #pragma unroll
         for (int i = 0; i < kTokens; ++i) {
@@ -267,8 +273,9 @@ struct RawFp16 {
             r[i] = make_uint4(0, 0, 0, 0);
             e[i] = 0;
             if (in) {
-                r[i] = __ldcg(reinterpret_cast<const uint4*>(src(i) + 8 * lane));
-                e[i] = __ldcg(exp(i) + (lane >> 1));
+                const uint32_t q = pair(i);
+                r[i] = __ldcg(reinterpret_cast<const uint4*>(at(a, q, la)));
+                e[i] = __ldcg(at(ae, q, le));
             }
         }
     }
@@ -415,9 +422,8 @@ __device__ __forceinline__ void stage_mma(float (&tot)[T][NT][4], uint32_t codes
     for (int i = 0; i < T; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.0f;
-#pragma unroll
-    for (int c = 0; c < kPC; ++c) {
-        if (c >= nch) break;
+#pragma unroll 1
+    for (int c = 0; c < nch; ++c) {
         float sa[T][GP], sb[T][GP];
 #pragma unroll
         for (int i = 0; i < T; ++i) {

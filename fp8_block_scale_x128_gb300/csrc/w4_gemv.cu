@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
                 raw[i] = make_uint2(0, 0);
                 if (tile < t1 && ahead.t + i < kGroup) {
                     const int last_row = min(p.N - tile * kTileRows, kTileRows) - 1;
-                    load_codes(to_codes + slot * kSlot + i * kCodeBytes, ahead.codes + i * tile_codes, p.ldc, last_row, nch, lane);
+                    load_codes(to_codes + slot * kSlot + i * kCodeBytes, ahead.codes + i * tile_codes, static_cast<uint32_t>(p.ldc), last_row, nch, lane);
                     raw[i] = load_scales<FMT, GP>(ahead.scales + i * tile_scales - max((lane >> 1) - last_row, 0) * p.lds, nch, lane);
                 }
             }

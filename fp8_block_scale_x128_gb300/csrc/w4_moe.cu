@@ -50,51 +50,48 @@ struct MoeParams {
 // Shared-memory tables of the routed pairs, built by every block, of P = M * S
 // elements each.
 struct Lists {
-    int16_t* pairs;     // grouped by expert, ascending experts
-    int16_t* tokens;    // of pairs
-    int16_t* unsorted;  // those of experts with more than one entry
-    int16_t* expert;    // of an entry
-    int16_t* first;     // its first pair in pairs
-    int16_t* n;         // its pairs: 1 .. batch
+    ushort4* entry;      // expert, first (place of its first pair), n (its pairs: 1 .. batch)
+    uint32_t* pair;      // by place, grouped by expert, ascending experts: pair | token << 16
+    uint16_t* place;     // of a pair
+    uint16_t* unsorted;  // pairs of experts with more than one entry
     int entries;
 };
-__host__ __device__ constexpr int lists_bytes(int P) { return (6 * P * 2 + 127) / 128 * 128; }
+__host__ __device__ constexpr int lists_bytes(int P) { return (16 * P + 127) / 128 * 128; }
 __host__ __device__ constexpr int counts_bytes(int E) { return (E * 4 + 15) / 16 * 16; }
 
 // counts: E ints of shared memory, free afterwards.  The order of the pairs of
 // an expert with one entry may differ between blocks and runs: it only decides
 // which MMA column serves a pair, and columns do not mix.  An expert with more
 // pairs has them sorted, so that every block splits them into the same entries.
+template <int THREADS>
 __device__ Lists build_lists(const MoeParams& p, int batch, uint8_t* mem, int* counts) {
-    __shared__ int sums[kWarps];
+    __shared__ int sums[THREADS / 32];
     __shared__ int n_entries;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = p.M * p.S;
     Lists L;
-    L.pairs = reinterpret_cast<int16_t*>(mem);
-    L.tokens = L.pairs + P;
-    L.unsorted = L.tokens + P;
-    L.expert = L.unsorted + P;
-    L.first = L.expert + P;
-    L.n = L.first + P;
-    constexpr int kMine = FP8BS_MOE_MAX_PAIRS / kThreads;
+    L.entry = reinterpret_cast<ushort4*>(mem);
+    L.pair = reinterpret_cast<uint32_t*>(L.entry + P);
+    L.place = reinterpret_cast<uint16_t*>(L.pair + P);
+    L.unsorted = L.place + P;
+    constexpr int kMine = (FP8BS_MOE_MAX_PAIRS + THREADS - 1) / THREADS;
     int id[kMine], rank[kMine];
 #pragma unroll
     for (int j = 0; j < kMine; ++j) {
-        const int q = tid + j * kThreads;
+        const int q = tid + j * THREADS;
         id[j] = q < P ? p.ids[q] : -1;
         if (q < P && (id[j] < 0 || id[j] >= p.E)) {
             record_error(p.err, FP8BS_ERR_DEVICE);
             id[j] = -1;
         }
     }
-    for (int e = tid; e < p.E; e += kThreads) counts[e] = 0;
+    for (int e = tid; e < p.E; e += THREADS) counts[e] = 0;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kMine; ++j) rank[j] = id[j] >= 0 ? atomicAdd(&counts[id[j]], 1) : 0;
     __syncthreads();
     // running sums over the experts: pairs in the low half, entries in the high one
-    const int per = (p.E + kThreads - 1) / kThreads;
+    const int per = (p.E + THREADS - 1) / THREADS;
     const int e0 = min(tid * per, p.E), e1 = min(e0 + per, p.E);
     int mine = 0;
     for (int e = e0; e < e1; ++e) mine += counts[e] | ((counts[e] + batch - 1) / batch << 16);
@@ -108,42 +105,43 @@ __device__ Lists build_lists(const MoeParams& p, int batch, uint8_t* mem, int* c
     __syncthreads();
     int at = incl - mine;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
+    for (int w = 0; w < THREADS / 32; ++w)
         if (w < warp) at += sums[w];
-    if (tid == kThreads - 1) n_entries = (at + mine) >> 16;
+    if (tid == THREADS - 1) n_entries = (at + mine) >> 16;
     for (int e = e0; e < e1; ++e) {
         const int n = counts[e], first = at & 0xFFFF;
         counts[e] = first | n << 16;
-        for (int b = 0; b * batch < n; ++b) {
-            const int i = (at >> 16) + b;
-            L.expert[i] = static_cast<int16_t>(e);
-            L.first[i] = static_cast<int16_t>(first + b * batch);
-            L.n[i] = static_cast<int16_t>(min(n - b * batch, batch));
-        }
+        for (int b = 0; b * batch < n; ++b)
+            L.entry[(at >> 16) + b] = make_ushort4(static_cast<unsigned short>(e), static_cast<unsigned short>(first + b * batch),
+                                                   static_cast<unsigned short>(min(n - b * batch, batch)), 0);
         at += n | ((n + batch - 1) / batch << 16);
+    }
+    __syncthreads();
+    auto set = [&](int place, int q) {
+        L.pair[place] = static_cast<uint32_t>(q) | static_cast<uint32_t>(q / p.S) << 16;
+        L.place[q] = static_cast<uint16_t>(place);
+    };
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        const int q = tid + j * THREADS;
+        if (id[j] >= 0) {
+            const int c = counts[id[j]], place = (c & 0xFFFF) + rank[j];
+            if (c >> 16 > batch)
+                L.unsorted[place] = static_cast<uint16_t>(q);
+            else
+                set(place, q);
+        } else if (q < P) {
+            L.place[q] = 0xFFFF;
+        }
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kMine; ++j)
-        if (id[j] >= 0) {
-            const int c = counts[id[j]];
-            const int q = tid + j * kThreads, at = (c & 0xFFFF) + rank[j];
-            if (c >> 16 > batch) {
-                L.unsorted[at] = static_cast<int16_t>(q);
-            } else {
-                L.pairs[at] = static_cast<int16_t>(q);
-                L.tokens[at] = static_cast<int16_t>(q / p.S);
-            }
-        }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kMine; ++j)
         if (id[j] >= 0 && counts[id[j]] >> 16 > batch) {
-            const int n = counts[id[j]] >> 16, first = counts[id[j]] & 0xFFFF, q = tid + j * kThreads;
+            const int n = counts[id[j]] >> 16, first = counts[id[j]] & 0xFFFF, q = tid + j * THREADS;
             int r = 0;
             for (int i = 0; i < n; ++i) r += L.unsorted[first + i] < q;
-            L.pairs[first + r] = static_cast<int16_t>(q);
-            L.tokens[first + r] = static_cast<int16_t>(q / p.S);
+            set(first + r, q);
         }
     L.entries = n_entries;
     __syncthreads();
@@ -182,13 +180,15 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
     const uint32_t from_inv = mine + kInvAt + inv_src(lane);
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const Lists L = build_lists(p, batch, smem, reinterpret_cast<int*>(base));
+    const Lists L = build_lists<kThreads>(p, batch, smem, reinterpret_cast<int*>(base));
 
     const int chunks = p.H / kChunk;
     const int first = warp * chunks / kWarps, last = (warp + 1) * chunks / kWarps;
     const int per = p.I / kTileRows;
-    const int64_t ldc = p.H / 2, lds = static_cast<int64_t>(chunks) * SB;
-    const int64_t up_codes = p.I * ldc, up_scales = p.I * lds;  // from a gate tile to its up tile
+    const uint32_t ldc = p.H / 2, lds = chunks * SB;
+    const uint32_t up_codes = p.I * ldc, up_scales = p.I * lds;  // from a gate tile to its up tile
+    const uint8_t* lane_codes = p.w13 + static_cast<int64_t>(lane >> 3) * ldc + first * 64 + (lane & 7) * 16;
+    const uint8_t* lane_scales = p.s13 + static_cast<int64_t>(lane >> 1) * lds + (first + (lane & 1)) * SB;
 
     // the block's run of items (entry, tile j)
     const int64_t items = static_cast<int64_t>(L.entries) * per;
@@ -204,13 +204,13 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
     Cursor ahead = {entry, j, 0, count, nullptr, nullptr, nullptr, nullptr};
     auto locate = [&]() {
         if (ahead.left <= 0) return;
-        const int64_t row = static_cast<int64_t>(L.expert[ahead.entry]) * 2 * p.I + ahead.j * kTileRows;
-        ahead.gate = p.w13 + (row + (lane >> 3)) * ldc + first * 64 + (lane & 7) * 16;
+        const uint32_t e = L.entry[ahead.entry].x;
+        ahead.gate = at(at(lane_codes, e, 2 * up_codes), ahead.j * kTileRows, ldc);
         ahead.up = ahead.gate + up_codes;
-        ahead.gate_scales = p.s13 + (row + (lane >> 1)) * lds + (first + (lane & 1)) * SB;
+        ahead.gate_scales = at(at(lane_scales, e, 2 * up_scales), ahead.j * kTileRows, lds);
         ahead.up_scales = ahead.gate_scales + up_scales;
     };
-    const int64_t next_codes = kTileRows * ldc - (pieces - 1) * kPC * 64, next_scales = kTileRows * lds - (pieces - 1) * kPC * SB;
+    const int next_codes = static_cast<int>(kTileRows * ldc) - (pieces - 1) * kPC * 64, next_scales = static_cast<int>(kTileRows * lds) - (pieces - 1) * kPC * SB;
     auto issue = [&](int slot, uint2 (&raw)[2]) {
         const int nch = min(last - first - ahead.piece * kPC, kPC);
         if (ahead.left > 0 && nch > 0) {
@@ -250,13 +250,13 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
     for (int item = 0; item < count; ++item) {
         if (entry != staged) {  // the expert's tokens, two pieces' loads in flight together
             staged = entry;
-            n = L.n[entry];
-            pf = L.first[entry];
+            n = L.entry[entry].z;
+            pf = L.entry[entry].y;
             x0 = xs + token_src(lane >> 2, n, lane);
             auto source = [&](int piece) {
-                const int16_t* tokens = L.tokens + pf;
+                const uint32_t* pair = L.pair + pf;
                 const uint16_t* x = p.x + (first + piece * kPC) * kChunk;
-                return [=](int i) { return x + tokens[i] * p.ldx; };
+                return [=](int i) { return x + (pair[i] >> 16) * p.ldx; };
             };
             for (int q = 0; q < pieces; q += 2) {
                 const int nch0 = min(last - first - q * kPC, kPC), nch1 = min(last - first - (q + 1) * kPC, kPC);
@@ -305,9 +305,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
             float inverse;
             const float scale = slice_scale(ef, inverse);
             if (static_cast<int>(threadIdx.x) < n * kTileRows) {
-                const int64_t at = static_cast<int64_t>(L.pairs[pf + i]) * p.I + j * kTileRows;
-                p.a[at + paired<FMT>(row)] = __half_as_ushort(__float2half_rn(a * scale));
-                if (row == 0) p.ae[at / kTileRows] = static_cast<uint8_t>(min(max(ef, 15u), 254u));
+                const int64_t to = static_cast<int64_t>(L.pair[pf + i] & 0xFFFF) * p.I + j * kTileRows;
+                p.a[to + paired<FMT>(row)] = __half_as_ushort(__float2half_rn(a * scale));
+                if (row == 0) p.ae[to / kTileRows] = static_cast<uint8_t>(min(max(ef, 15u), 254u));
             }
         }
         __syncthreads();  // the sums' place is rewritten by the next item
@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
 
 // ---- 2. down -----------------------------------------------------------------
 constexpr int kDownDepth = 3;
+constexpr int kDownWarps = 8, kDownThreads = kDownWarps * 32;
 
 // Bytes of a warp: the ring, the scale table, the inverse scales and a stage of
 // a for n pairs.
@@ -325,134 +326,115 @@ template <int GP>
 __host__ __device__ constexpr int down_bytes(int n) {
     return kDownDepth * kCodeBytes + kTableBytes<GP> + kInvBytes + n * kTokenBytes;
 }
-
-// the pairs' products for 16 rows, and their routing weights
+// the pairs' products for 16 rows by place, and the pairs' routing weights
 __host__ __device__ constexpr int out_bytes(int P) { return (P * (kTileRows + 1) * 4 + 127) / 128 * 128; }
 
-template <int FMT, int GP>
-__global__ void __launch_bounds__(kThreads, 2) moe_w4_down_kernel(const __grid_constant__ MoeParams p, int batch) {
+// ONE: the whole of I in one stage.
+template <int FMT, int GP, bool ONE>
+__global__ void __launch_bounds__(kDownThreads, 2) moe_w4_down_kernel(const __grid_constant__ MoeParams p, int batch) {
     constexpr int SB = Format<FMT, GP>::kScaleBytes, D = kDownDepth;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = p.M * p.S;
     float* out = reinterpret_cast<float*>(smem + lists_bytes(P));  // [P][16]
+    float* weight = out + P * kTileRows;
     uint8_t* base = smem + lists_bytes(P) + out_bytes(P);
     // a warp's memory: codes [D], the scale table, inv, the entry's a
-    constexpr int kTableAt = D * kCodeBytes, kInvAt = kTableAt + kTableBytes<GP>;
-    const uint32_t mine = ptx::smem_addr(base) + warp * down_bytes<GP>(min(P, batch)), xs = mine + kInvAt + kInvBytes;
+    constexpr int kTableAt = D * kCodeBytes, kInvAt = kTableAt + kTableBytes<GP>, kXsAt = kInvAt + kInvBytes;
+    const uint32_t mine = ptx::smem_addr(base) + warp * down_bytes<GP>(min(P, batch)), xs = mine + kXsAt;
     const uint32_t to_codes = mine + code_dst(lane), to_table = mine + kTableAt + scale_dst<GP>(lane);
     const uint32_t from_codes = mine + code_src(lane), from_table = mine + kTableAt + scale_src<GP>(lane);
     const uint32_t from_inv = mine + kInvAt + inv_src(lane);
-    // the pairs' routing weights, 0 for an invalid id (the first launch has
-    // waited for whatever wrote the routing)
-    float* weight = out + P * kTileRows;
-    for (int q = tid; q < P; q += kThreads) {
-        const int e = p.ids[q];
-        weight[q] = e >= 0 && e < p.E ? p.tw[q] : 0.0f;
-    }
-    const Lists L = build_lists(p, batch, smem, reinterpret_cast<int*>(base));
+    // the routing is complete: the first launch has waited for what wrote it
+    for (int q = tid; q < P; q += kDownThreads) weight[q] = p.tw[q];
+    const Lists L = build_lists<kDownThreads>(p, batch, smem, reinterpret_cast<int*>(base));
 
-    const int chunks = p.I / kChunk, pieces = (chunks + kPC - 1) / kPC;
-    const int64_t ldc = p.I / 2, lds = static_cast<int64_t>(chunks) * SB;
+    const int chunks = p.I / kChunk, pieces = ONE ? 1 : (chunks + kPC - 1) / kPC;
+    const uint32_t ldc = p.I / 2, lds = chunks * SB;
+    const uint32_t expert_codes = p.H * ldc, expert_scales = p.H * lds;
+    const uint8_t* lane_a = reinterpret_cast<const uint8_t*>(p.a) + 16 * lane;
+    const uint8_t* lane_ae = p.ae + (lane >> 1);
+    const uint32_t la = p.I * 2, le = p.I / kTileRows;
     const int tiles = p.H / kTileRows;
-
-    // a warp's stages: the tiles of the block, in a tile the warp's entries,
-    // in an entry the pieces of I
-    struct Cursor {
-        int tile, entry, piece;
-        const uint8_t *codes, *scales;  // this lane's
-    };
-    Cursor ahead = {static_cast<int>(blockIdx.x), warp, 0, nullptr, nullptr};
-    auto locate = [&]() {
-        if (ahead.tile >= tiles || ahead.entry >= L.entries) return;
-        const int64_t row = static_cast<int64_t>(L.expert[ahead.entry]) * p.H + ahead.tile * kTileRows;
-        ahead.codes = p.w2 + (row + (lane >> 3)) * ldc + (lane & 7) * 16;
-        ahead.scales = p.s2 + (row + (lane >> 1)) * lds + (lane & 1) * SB;
-    };
-    auto issue = [&](int slot) {
-        uint2 raw = make_uint2(0, 0);
-        if (ahead.tile < tiles && ahead.entry < L.entries) {
-            const int nch = min(chunks - ahead.piece * kPC, kPC);
-            load_codes(to_codes + slot * kCodeBytes, ahead.codes, ldc, kTileRows - 1, nch, lane);
-            raw = load_scales<FMT, GP>(ahead.scales, nch, lane);
-        }
-        cp_async_commit();
-        if (++ahead.piece < pieces) {
-            ahead.codes += kPC * 64;
-            ahead.scales += kPC * SB;
-        } else {
-            ahead.piece = 0;
-            if ((ahead.entry += kWarps) >= L.entries) ahead.entry = warp, ahead.tile += gridDim.x;
-            locate();
-        }
-        return raw;
-    };
     RawFp16 tokens;
-    auto load_tokens = [&](int entry, int piece, int i0) {
-        const int16_t* pairs = L.pairs + L.first[entry] + i0;
-        const uint16_t* a = p.a + piece * kStageK;
-        const uint8_t* ae = p.ae + piece * (kStageK / kTileRows);
-        const int I = p.I;
-        tokens.load(L.n[entry] - i0, min(chunks - piece * kPC, kPC), lane,
-                    [=](int i) { return a + static_cast<int64_t>(pairs[i]) * I; },
-                    [=](int i) { return ae + static_cast<int64_t>(pairs[i]) * (I / kTileRows); });
+    auto load_tokens = [&](const ushort4& entry, int piece, int i0) {
+        const uint32_t* pair = L.pair + entry.y + i0;
+        tokens.load(lane_a + piece * kTokenBytes, lane_ae + piece * (kStageK / kTileRows), la, le, entry.z - i0,
+                    min(chunks - piece * kPC, kPC), lane, [=](int i) { return pair[i] & 0xFFFFu; });
     };
 
-    locate();
-    uint2 raw[D - 1];
-#pragma unroll
-    for (int i = 0; i < D - 1; ++i) raw[i] = issue(i);
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-    if (warp < L.entries) load_tokens(warp, 0, 0);
-    int slot = 0;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        for (int q = tid; q < P * kTileRows; q += kThreads) out[q] = 0.0f;  // pairs with an invalid id stay 0
-        __syncthreads();
-        for (int entry = warp; entry < L.entries; entry += kWarps) {
-            const int n = L.n[entry], pf = L.first[entry];
+        const uint8_t* lane_codes = at(p.w2 + static_cast<int64_t>(lane >> 3) * ldc + (lane & 7) * 16, tile * kTileRows, ldc);
+        const uint8_t* lane_scales = at(p.s2 + static_cast<int64_t>(lane >> 1) * lds + (lane & 1) * SB, tile * kTileRows, lds);
+        // a warp's stages: its entries, in an entry the pieces of I
+        int ahead = warp, ahead_piece = 0;
+        auto issue = [&](uint32_t slot_at) {
+            uint2 raw = make_uint2(0, 0);
+            if (ahead < L.entries) {
+                const uint32_t e = L.entry[ahead].x;
+                const int nch = min(chunks - ahead_piece * kPC, kPC);
+                load_codes(to_codes + slot_at, at(lane_codes, e, expert_codes) + ahead_piece * kPC * 64, ldc, kTileRows - 1, nch, lane);
+                raw = load_scales<FMT, GP>(at(lane_scales, e, expert_scales) + ahead_piece * kPC * SB, nch, lane);
+            }
+            cp_async_commit();
+            if (ONE || ++ahead_piece == pieces) ahead_piece = 0, ahead += kDownWarps;
+            return raw;
+        };
+        uint2 raw[D - 1];
+#pragma unroll
+        for (int i = 0; i < D - 1; ++i) raw[i] = issue(i * kCodeBytes);
+        if (tile == static_cast<int>(blockIdx.x)) {
+            ptx::griddep_wait();
+            ptx::griddep_launch_dependents();
+        }
+        ushort4 now = L.entry[min(warp, max(L.entries - 1, 0))];
+        if (warp < L.entries) load_tokens(now, 0, 0);
+        uint32_t slot_at = 0;
+        for (int entry = warp; entry < L.entries; entry += kDownWarps) {
+            const int n = now.z, pf = now.y;
+            const ushort4 next = L.entry[min(entry + kDownWarps, L.entries - 1)];
             const uint32_t x[1] = {xs + token_src(lane >> 2, n, lane)};
             float tot[1][1][4] = {};
             for (int piece = 0; piece < pieces; ++piece) {
                 const int nch = min(chunks - piece * kPC, kPC);
-                tokens.store(xs, mine + kInvAt, 0, n, lane);
-                for (int i0 = RawFp16::kTokens; i0 < n; i0 += RawFp16::kTokens) {
-                    load_tokens(entry, piece, i0);
-                    tokens.store(xs, mine + kInvAt, i0, n, lane);
-                }
-                if (piece + 1 < pieces)
-                    load_tokens(entry, piece + 1, 0);
-                else
-                    load_tokens(entry + kWarps < L.entries ? entry + kWarps : warp, 0, 0);
                 const uint2 cur[1] = {raw[0]};
 #pragma unroll
                 for (int i = 0; i + 2 < D; ++i) raw[i] = raw[i + 1];
-                raw[D - 2] = issue(slot == 0 ? D - 1 : slot - 1);
+                raw[D - 2] = issue(slot_at == 0 ? (D - 1) * kCodeBytes : slot_at - kCodeBytes);
+                tokens.store(xs, mine + kInvAt, 0, n, lane);
+                for (int i0 = RawFp16::kTokens; i0 < n; i0 += RawFp16::kTokens) {
+                    load_tokens(now, piece, i0);
+                    tokens.store(xs, mine + kInvAt, i0, n, lane);
+                }
+                if (!ONE && piece + 1 < pieces)
+                    load_tokens(now, piece + 1, 0);
+                else
+                    load_tokens(next, 0, 0);
                 const float back = store_scales<FMT, GP, 1>(to_table, cur);
                 cp_async_wait<D - 1>();
                 __syncwarp();
-                stage_mma<FMT, GP, 1, 1>(tot, from_codes + slot * kCodeBytes, from_table, x, from_inv, back, nch);
+                stage_mma<FMT, GP, 1, 1>(tot, from_codes + slot_at, from_table, x, from_inv, back, nch);
                 __syncwarp();  // the slot, the table and the tokens are rewritten by later stages
-                slot = slot + 1 == D ? 0 : slot + 1;
+                slot_at = slot_at == (D - 1) * kCodeBytes ? 0 : slot_at + kCodeBytes;
             }
-            const int col = 2 * (lane & 3), row = lane >> 2;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (col + h < n) {
-                    float* o = out + L.pairs[pf + col + h] * kTileRows + row;
-                    o[0] = tot[0][0][h];
-                    o[8] = tot[0][0][2 + h];
-                }
+            const int col = 2 * (lane & 3);
+            float* o = out + (pf + col) * kTileRows + (lane >> 2);
+            if (col < n) o[0] = tot[0][0][0], o[8] = tot[0][0][2];
+            if (col + 1 < n) o[kTileRows] = tot[0][0][1], o[kTileRows + 8] = tot[0][0][3];
+            now = next;
         }
         __syncthreads();
-        for (int o = tid; o < p.M * kTileRows; o += kThreads) {
+        for (int o = tid; o < p.M * kTileRows; o += kDownThreads) {
             const int m = o / kTileRows, row = o % kTileRows;
             float v = 0.0f;
 #pragma unroll 4
-            for (int q = m * p.S; q < (m + 1) * p.S; ++q) v = fmaf(weight[q], out[q * kTileRows + row], v);
+            for (int q = m * p.S; q < (m + 1) * p.S; ++q) {
+                const int place = L.place[q];  // 0xFFFF: an invalid id contributes nothing
+                if (place != 0xFFFF) v = fmaf(weight[q], out[place * kTileRows + row], v);
+            }
             p.y[static_cast<int64_t>(m) * p.H + tile * kTileRows + row] = to_bf16(v);
         }
-        __syncthreads();  // out is cleared for the next tile
+        __syncthreads();  // out is rewritten for the next tile
     }
 }
 
@@ -488,18 +470,18 @@ cudaError_t launch_up(const MoeParams& p, int sm_count, cudaStream_t stream) {
     return launch_dependent(moe_w4_up_kernel<FMT, GP>, grid, kThreads, smem, stream, p, batch);
 }
 
-template <int FMT, int GP>
+template <int FMT, int GP, bool ONE>
 cudaError_t launch_down(const MoeParams& p, int sm_count, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_shared(moe_w4_down_kernel<FMT, GP>, allowed);
+    cudaError_t e = allow_shared(moe_w4_down_kernel<FMT, GP, ONE>, allowed);
     if (e != cudaSuccess) return e;
     const int P = p.M * p.S;
     auto bytes = [&](int batch) {
-        return lists_bytes(P) + out_bytes(P) + max(counts_bytes(p.E), kWarps * down_bytes<GP>(min(P, batch)));
+        return lists_bytes(P) + out_bytes(P) + max(counts_bytes(p.E), kDownWarps * down_bytes<GP>(min(P, batch)));
     };
     int per_sm;
     const int batch = batch_of(p, bytes, per_sm);
-    return launch_dependent(moe_w4_down_kernel<FMT, GP>, min(p.H / kTileRows, sm_count * per_sm), kThreads, bytes(batch), stream, p, batch);
+    return launch_dependent(moe_w4_down_kernel<FMT, GP, ONE>, min(p.H / kTileRows, sm_count * per_sm), kDownThreads, bytes(batch), stream, p, batch);
 }
 
 }  // namespace
@@ -529,7 +511,9 @@ cudaError_t launch_moe_w4(const MoeW4Args& a, cudaStream_t stream) {
     p.E = a.E;
     return dispatch_format(a.format, a.group, [&](auto fmt, auto gp) {
         const cudaError_t e = launch_up<fmt(), gp()>(p, a.sm_count, stream);
-        return e != cudaSuccess ? e : launch_down<fmt(), gp()>(p, a.sm_count, stream);
+        if (e != cudaSuccess) return e;
+        return p.I <= kStageK ? launch_down<fmt(), gp(), true>(p, a.sm_count, stream)
+                              : launch_down<fmt(), gp(), false>(p, a.sm_count, stream);
     });
 }
 

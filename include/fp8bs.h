@@ -366,12 +366,13 @@ int fp8bs_quant_weight_w4(const float* w, int64_t N, int64_t K, int64_t ldw, int
 
 /* Largest token count of fp8bs_gemv_w4a16. */
 #define FP8BS_W4_MAX_M 16
+#define FP8BS_W4_MAX_LDC (1 << 28) /* largest row stride of the codes, bytes */
 
 /* Y = bf16(x W^T) for a few bf16 tokens and a 4-bit weight, in one launch.
  *   x      : bf16 [M, K], row stride ldx elements; x and ldx*2 16-byte aligned.
  *   M      : 0 .. FP8BS_W4_MAX_M (0 enqueues nothing and returns FP8BS_OK).
- *   codes  : [N, K/2] bytes, row stride ldc bytes; codes and ldc 16-byte
- *            aligned.
+ *   codes  : [N, K/2] bytes, row stride ldc <= FP8BS_W4_MAX_LDC bytes; codes
+ *            and ldc 16-byte aligned.
  *   scales : [N, K/group], row stride lds elements; the scales of a row's 128 k
  *            (MXFP4 4 bytes; INT4 256/group bytes) aligned to their size.
  *   N, K   : N >= 1 (any), K a multiple of 128, both at most 2^24.

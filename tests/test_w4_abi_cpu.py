@@ -31,7 +31,7 @@ def gemv(L, x=P, M=4, ldx=4096, codes=P, ldc=2048, scales=P, lds=128, N=5120, K=
     (dict(fmt=2), ARG), (dict(group=64), ARG), (dict(fmt=1, group=16), ARG), (dict(fmt=1, group=0), ARG),
     (dict(flags=2), ARG), (dict(M=17), SHAPE), (dict(M=-1), SHAPE), (dict(N=0), SHAPE), (dict(K=4000), SHAPE),
     (dict(K=0), SHAPE), (dict(N=(1 << 24) + 1), SHAPE), (dict(x=None), ARG), (dict(codes=None), ARG),
-    (dict(scales=None), ARG), (dict(y=None), ARG), (dict(ldx=4088), ARG), (dict(ldc=2032), ARG), (dict(lds=127), ARG),
+    (dict(scales=None), ARG), (dict(y=None), ARG), (dict(ldx=4088), ARG), (dict(ldc=2032), ARG), (dict(ldc=(1 << 28) + 16), ARG), (dict(lds=127), ARG),
     (dict(ldy=5119), ARG), (dict(x=P + 8), ALIGN), (dict(ldx=4100), ALIGN), (dict(codes=P + 8), ALIGN),
     (dict(ldc=2056), ALIGN), (dict(scales=P + 2), ALIGN), (dict(lds=130), ALIGN), (dict(y=P + 1), ALIGN),
     (dict(fmt=1, scales=P + 4), ALIGN), (dict(fmt=1, lds=130), ALIGN), (dict(fmt=1, group=128, lds=33, scales=P + 1), ALIGN),
