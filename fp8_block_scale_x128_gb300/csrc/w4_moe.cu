@@ -199,41 +199,35 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
     // a warp's stages: the items of the run, in an item the pieces of the slice
     struct Cursor {
         int entry, j, piece, left;
-        const uint8_t *gate, *up, *gate_scales, *up_scales;  // this lane's
+        const uint8_t *gate, *scales;  // this lane's, of the gate tile
     };
-    Cursor ahead = {entry, j, 0, count, nullptr, nullptr, nullptr, nullptr};
+    Cursor ahead = {entry, j, 0, count, nullptr, nullptr};
     auto locate = [&]() {
         if (ahead.left <= 0) return;
         const uint32_t e = L.entry[ahead.entry].x;
         ahead.gate = at(at(lane_codes, e, 2 * up_codes), ahead.j * kTileRows, ldc);
-        ahead.up = ahead.gate + up_codes;
-        ahead.gate_scales = at(at(lane_scales, e, 2 * up_scales), ahead.j * kTileRows, lds);
-        ahead.up_scales = ahead.gate_scales + up_scales;
+        ahead.scales = at(at(lane_scales, e, 2 * up_scales), ahead.j * kTileRows, lds);
     };
     const int next_codes = static_cast<int>(kTileRows * ldc) - (pieces - 1) * kPC * 64, next_scales = static_cast<int>(kTileRows * lds) - (pieces - 1) * kPC * SB;
     auto issue = [&](int slot, uint2 (&raw)[2]) {
         const int nch = min(last - first - ahead.piece * kPC, kPC);
         if (ahead.left > 0 && nch > 0) {
             load_codes(to_codes + slot * kSlot, ahead.gate, ldc, kTileRows - 1, nch, lane);
-            load_codes(to_codes + slot * kSlot + kCodeBytes, ahead.up, ldc, kTileRows - 1, nch, lane);
-            raw[0] = load_scales<FMT, GP>(ahead.gate_scales, nch, lane);
-            raw[1] = load_scales<FMT, GP>(ahead.up_scales, nch, lane);
+            load_codes(to_codes + slot * kSlot + kCodeBytes, ahead.gate + up_codes, ldc, kTileRows - 1, nch, lane);
+            raw[0] = load_scales<FMT, GP>(ahead.scales, nch, lane);
+            raw[1] = load_scales<FMT, GP>(ahead.scales + up_scales, nch, lane);
         }
         cp_async_commit();
         if (++ahead.piece < pieces) {
             ahead.gate += kPC * 64;
-            ahead.up += kPC * 64;
-            ahead.gate_scales += kPC * SB;
-            ahead.up_scales += kPC * SB;
+            ahead.scales += kPC * SB;
             return;
         }
         ahead.piece = 0;
         --ahead.left;
         if (++ahead.j < per) {
             ahead.gate += next_codes;
-            ahead.up += next_codes;
-            ahead.gate_scales += next_scales;
-            ahead.up_scales += next_scales;
+            ahead.scales += next_scales;
         } else {
             ahead.j = 0;
             ++ahead.entry;
