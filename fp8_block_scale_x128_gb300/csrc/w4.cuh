@@ -589,8 +589,6 @@ struct GemvW4Args {
     int pdl;
 };
 cudaError_t launch_gemv_w4(const GemvW4Args& a, cudaStream_t stream);
-bool gemv_w4_tc_serves(const GemvW4Args& a);
-cudaError_t launch_gemv_w4_tc(const GemvW4Args& a, cudaStream_t stream);
 
 struct MoeRouteArgs {
     const uint16_t* x;

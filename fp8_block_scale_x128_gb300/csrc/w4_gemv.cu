@@ -217,7 +217,6 @@ cudaError_t launch_depth(GemvParams& p, int sm_count, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_gemv_w4(const GemvW4Args& a, cudaStream_t stream) {
-    if (gemv_w4_tc_serves(a)) return launch_gemv_w4_tc(a, stream);
     GemvParams p;
     p.x = a.x;
     p.ldx = a.ldx;

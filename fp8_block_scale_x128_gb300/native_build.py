@@ -23,7 +23,7 @@ TRACE_LIB_PATH = os.path.join(BUILD_DIR, "libfp8bs_trace.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cu", "quant.cu", "prepack.cu", "gemm_fused.cu", "rmsnorm_quant.cu", "moe.cu",
-           "w4_quant.cu", "w4_gemv.cu", "w4_gemv_tc.cu", "w4_moe.cu", "moe_route.cu"]
+           "w4_quant.cu", "w4_gemv.cu", "w4_moe.cu", "moe_route.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]
