@@ -2,8 +2,9 @@
 //
 // A block owns a contiguous range of 16-row tiles; its warps split K (WK
 // slices), or K and the tiles where K has fewer than 16 chunks.  A warp keeps
-// its slice of x as fp16 (all of it where it fits, else one stage at a time,
-// staged again for every kGroup tiles) and streams its part of the codes
+// its slice of x as fp16 (all of it where it fits, and then a tile's stages
+// follow each other; else one stage at a time for kGroup tiles, staged again
+// for the next ones) and streams its part of the codes
 // through a ring of kDepth stages of its own, so no step but the sums over the
 // slices is block-wide.  Those go in slice order: repeated calls give the same
 // bits.
@@ -33,7 +34,6 @@ struct GemvParams {
     int chunks;    // chunks of 128 k
     int WK, WR;    // K slices, row tiles at a time: WK * WR <= kWarps
     int pieces;    // stages of the longest slice
-    int resident;  // whether all pieces of x stay staged
     int pdl;
 };
 
@@ -48,20 +48,21 @@ __host__ __device__ constexpr int warp_bytes(int M, int pieces, bool resident) {
     return D * T * kCodeBytes + T * kTableBytes<GP> + inv + (resident ? x + kRedBytes<NT> : (x > kRedBytes<NT> ? x : kRedBytes<NT>));
 }
 
-// NT: tiles of 8 token columns; T: tiles of a stage; D: ring depth.
-template <int FMT, int GP, int NT, int T, int D>
+// NT: tiles of 8 token columns; T: tiles of a stage; D: ring depth; RES: whether
+// all pieces of x stay staged.
+template <int FMT, int GP, int NT, int T, int D, bool RES>
 __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_constant__ GemvParams p) {
     constexpr int SB = Format<FMT, GP>::kScaleBytes;
     constexpr int kSlot = T * kCodeBytes, kTableAt = D * kSlot, kInvAt = kTableAt + T * kTableBytes<GP>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int wr = warp / p.WK, wk = warp - wr * p.WK;
-    const int kept = p.resident ? p.pieces : 1;
-    const int mine_bytes = warp_bytes<GP, NT, T, D>(p.M, p.pieces, p.resident);
+    const int kept = RES ? p.pieces : 1;
+    const int mine_bytes = warp_bytes<GP, NT, T, D>(p.M, p.pieces, RES);
     // a warp's memory: codes [D][T], scale tables [T], inv [kept][8 NT],
     // x [kept][M][kTokenBytes], and the sums behind x or in its place
     const int x_at = kInvAt + (kept * 8 * NT * 4 + 127) / 128 * 128;
-    const int red_at = x_at + (p.resident ? kept * p.M * kTokenBytes : 0);
+    const int red_at = x_at + (RES ? kept * p.M * kTokenBytes : 0);
     const uint32_t mine = ptx::smem_addr(smem) + warp * mine_bytes, xs = mine + x_at;
     const uint32_t to_codes = mine + code_dst(lane), to_table = mine + kTableAt + scale_dst<GP>(lane);
     const uint32_t from_codes = mine + code_src(lane), from_table = mine + kTableAt + scale_src<GP>(lane);
@@ -77,52 +78,71 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
     const int t1 = static_cast<int>((static_cast<int64_t>(blockIdx.x) + 1) * p.tiles / gridDim.x);
     const int steps = (t1 - t0 + p.WR - 1) / p.WR;  // tiles of a warp
 
-    // the order of a warp's stages: groups of kGroup tiles, in a group the
-    // pieces of the slice, in a piece the tiles, T at a time (of two the second
-    // may be missing at the end of a range); codes and scales are this lane's
-    // pointers into the stage
+    // the order of a warp's stages.  RES: its tiles, T at a time, in them the
+    // pieces of the slice; else groups of kGroup tiles, in a group the pieces, in
+    // a piece the tiles.  (Of two tiles the second may be missing at the end of
+    // a range.)  codes and scales are this lane's pointers into the stage.
     struct Cursor {
-        int group, piece, t, tile;
+        int group, piece, t;
         const uint8_t *codes, *scales;
     };
     const int64_t tile_codes = kTileRows * p.WR * p.ldc, tile_scales = kTileRows * p.WR * p.lds;
-    Cursor ahead = {0, 0, 0, t0 + wr, nullptr, nullptr};
+    Cursor ahead = {0, 0, 0, nullptr, nullptr};
     ahead.codes = p.codes + (static_cast<int64_t>(t0 + wr) * kTileRows + (lane >> 3)) * p.ldc + first * 64 + (lane & 7) * 16;
     ahead.scales = p.scales + (static_cast<int64_t>(t0 + wr) * kTileRows + (lane >> 1)) * p.lds + (first + (lane & 1)) * SB;
+    const uint32_t ldc = static_cast<uint32_t>(p.ldc);
+    const int whole = min(t1, p.N / kTileRows);  // tiles before this one have 16 rows
     auto issue = [&](int slot, uint2 (&raw)[T]) {
-        const int nch = min(last - first - ahead.piece * kPC, kPC);
-        if (ahead.group < steps && nch > 0) {
+        const int nch = min(last - first - ahead.piece * kPC, kPC), step = ahead.group + ahead.t;
+        if (step < steps && nch > 0) {
+            const int tile = t0 + wr + step * p.WR;
+            if (tile + (T - 1) * p.WR < whole && (RES || ahead.t + T <= kGroup)) {
 #pragma unroll
-            for (int i = 0; i < T; ++i) {
-                const int tile = ahead.tile + i * p.WR;
-                raw[i] = make_uint2(0, 0);
-                if (tile < t1 && ahead.t + i < kGroup) {
-                    const int last_row = min(p.N - tile * kTileRows, kTileRows) - 1;
-                    load_codes(to_codes + slot * kSlot + i * kCodeBytes, ahead.codes + i * tile_codes, static_cast<uint32_t>(p.ldc), last_row, nch, lane);
-                    raw[i] = load_scales<FMT, GP>(ahead.scales + i * tile_scales - max((lane >> 1) - last_row, 0) * p.lds, nch, lane);
+                for (int i = 0; i < T; ++i) {
+                    load_codes(to_codes + slot * kSlot + i * kCodeBytes, ahead.codes + i * tile_codes, ldc, kTileRows - 1, nch, lane);
+                    raw[i] = load_scales<FMT, GP>(ahead.scales + i * tile_scales, nch, lane);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < T; ++i) {
+                    raw[i] = make_uint2(0, 0);
+                    if (tile + i * p.WR < t1) {
+                        const int last_row = min(p.N - (tile + i * p.WR) * kTileRows, kTileRows) - 1;
+                        load_codes(to_codes + slot * kSlot + i * kCodeBytes, ahead.codes + i * tile_codes, ldc, last_row, nch, lane);
+                        raw[i] = load_scales<FMT, GP>(ahead.scales + i * tile_scales - max((lane >> 1) - last_row, 0) * p.lds, nch, lane);
+                    }
                 }
             }
         }
         cp_async_commit();
         // on to the next stage
-        const int count = min(kGroup, steps - ahead.group);
-        if ((ahead.t += T) < count) {
-            ahead.tile += T * p.WR;
-            ahead.codes += T * tile_codes;
-            ahead.scales += T * tile_scales;
-        } else {
-            const int back = ahead.t - T;
-            ahead.t = 0;
+        if constexpr (RES) {
             if (++ahead.piece < p.pieces) {
-                ahead.tile -= back * p.WR;
-                ahead.codes += kPC * 64 - back * tile_codes;
-                ahead.scales += kPC * SB - back * tile_scales;
+                ahead.codes += kPC * 64;
+                ahead.scales += kPC * SB;
             } else {
                 ahead.piece = 0;
-                ahead.group += kGroup;
-                ahead.tile += T * p.WR;
+                ahead.group += T;
                 ahead.codes += T * tile_codes - (p.pieces - 1) * kPC * 64;
                 ahead.scales += T * tile_scales - (p.pieces - 1) * kPC * SB;
+            }
+        } else {
+            const int count = min(kGroup, steps - ahead.group);
+            if ((ahead.t += T) < count) {
+                ahead.codes += T * tile_codes;
+                ahead.scales += T * tile_scales;
+            } else {
+                const int back = ahead.t - T;
+                ahead.t = 0;
+                if (++ahead.piece < p.pieces) {
+                    ahead.codes += kPC * 64 - back * tile_codes;
+                    ahead.scales += kPC * SB - back * tile_scales;
+                } else {
+                    ahead.piece = 0;
+                    ahead.group += kGroup;
+                    ahead.codes += T * tile_codes - (p.pieces - 1) * kPC * 64;
+                    ahead.scales += T * tile_scales - (p.pieces - 1) * kPC * SB;
+                }
             }
         }
     };
@@ -142,44 +162,55 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
     for (int i = 0; i < D - 1; ++i) issue(i, raw[i]);
     if (p.pdl) ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    if (p.resident)
+    if (RES)
         for (int q = 0; q < p.pieces; ++q) stage_x(q, q);
 
     int slot = 0;
+    // multiply the stage at the front of the ring and start the one that takes
+    // its predecessor's slot
+    auto multiply = [&](float (&tot)[T][NT][4], int nch, int kept_at) {
+        uint2 cur[T];
+#pragma unroll
+        for (int i = 0; i < T; ++i) {
+            cur[i] = raw[0][i];
+#pragma unroll
+            for (int k = 0; k + 2 < D; ++k) raw[k][i] = raw[k + 1][i];
+        }
+        issue(slot == 0 ? D - 1 : slot - 1, raw[D - 2]);
+        if (nch > 0) {
+            const float back = store_scales<FMT, GP, T>(to_table, cur);
+            uint32_t x[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) x[j] = from_x[j] + kept_at * p.M * kTokenBytes;
+            cp_async_wait<D - 1>();
+            __syncwarp();
+            stage_mma<FMT, GP, NT, T>(tot, from_codes + slot * kSlot, from_table, x, from_inv + kept_at * 8 * NT * 4, back, nch);
+        }
+        __syncwarp();  // the slot, the table and x are rewritten by later stages
+        slot = slot + 1 == D ? 0 : slot + 1;
+    };
     for (int group = 0; group < steps; group += kGroup) {
         const int count = min(kGroup, steps - group);
-        float tot[kGroup / T][T][NT][4] = {};
-        for (int piece = 0; piece < p.pieces; ++piece) {
-            if (!p.resident) stage_x(piece, 0);
-            const int nch = min(last - first - piece * kPC, kPC), kept_at = p.resident ? piece : 0;
+        // sums as [warp][tile of the group][token][row]
+        if constexpr (RES) {
+            for (int t = 0; t < count; t += T) {
+                float tot[T][NT][4] = {};
+                for (int piece = 0; piece < p.pieces; ++piece) multiply(tot, min(last - first - piece * kPC, kPC), piece);
 #pragma unroll
-            for (int t = 0; t < kGroup / T; ++t) {
-                if (t * T >= count) break;
-                uint2 cur[T];
-#pragma unroll
-                for (int i = 0; i < T; ++i) {
-                    cur[i] = raw[0][i];
-#pragma unroll
-                    for (int k = 0; k + 2 < D; ++k) raw[k][i] = raw[k + 1][i];
-                }
-                issue(slot == 0 ? D - 1 : slot - 1, raw[D - 2]);
-                if (nch > 0) {
-                    const float back = store_scales<FMT, GP, T>(to_table, cur);
-                    uint32_t x[NT];
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) x[j] = from_x[j] + kept_at * p.M * kTokenBytes;
-                    cp_async_wait<D - 1>();
-                    __syncwarp();
-                    stage_mma<FMT, GP, NT, T>(tot[t], from_codes + slot * kSlot, from_table, x, from_inv + kept_at * 8 * NT * 4, back, nch);
-                }
-                __syncwarp();  // the slot, the table and x are rewritten by later stages
-                slot = slot + 1 == D ? 0 : slot + 1;
+                for (int i = 0; i < T; ++i) store_sums<NT>(mine + red_at + (t + i) * kSumBytes<NT>, tot[i], lane);
             }
-        }
-        // [warp][tile of the group][token][row]
+        } else {
+            float tot[kGroup / T][T][NT][4] = {};
+            for (int piece = 0; piece < p.pieces; ++piece) {
+                stage_x(piece, 0);
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u)
-            if (u < count) store_sums<NT>(mine + red_at + u * kSumBytes<NT>, tot[u / T][u % T], lane);
+                for (int t = 0; t < kGroup / T; ++t)
+                    if (t * T < count) multiply(tot[t], min(last - first - piece * kPC, kPC), 0);
+            }
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u)
+                if (u < count) store_sums<NT>(mine + red_at + u * kSumBytes<NT>, tot[u / T][u % T], lane);
+        }
         __syncthreads();
         const int rows = count * p.WR * kTileRows;
         const int64_t row0 = static_cast<int64_t>(t0 + group * p.WR) * kTileRows;
@@ -198,20 +229,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
     }
 }
 
-template <int FMT, int GP, int NT, int T, int D>
+template <int FMT, int GP, int NT, int T, int D, bool RES>
 cudaError_t launch(const GemvParams& p, int sm_count, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_shared(gemv_w4_kernel<FMT, GP, NT, T, D>, allowed);
+    cudaError_t e = allow_shared(gemv_w4_kernel<FMT, GP, NT, T, D, RES>, allowed);
     if (e != cudaSuccess) return e;
-    const int smem = kWarps * warp_bytes<GP, NT, T, D>(p.M, p.pieces, p.resident);
-    return launch_dependent(gemv_w4_kernel<FMT, GP, NT, T, D>, min((p.tiles + p.WR - 1) / p.WR, sm_count), kThreads, smem, stream, p);
+    const int smem = kWarps * warp_bytes<GP, NT, T, D>(p.M, p.pieces, RES);
+    return launch_dependent(gemv_w4_kernel<FMT, GP, NT, T, D, RES>, min((p.tiles + p.WR - 1) / p.WR, sm_count), kThreads, smem, stream, p);
 }
 
 template <int FMT, int GP, int NT, int T, int D>
-cudaError_t launch_depth(GemvParams& p, int sm_count, cudaStream_t stream) {
-    p.resident = kWarps * warp_bytes<GP, NT, T, D>(p.M, p.pieces, true) <= kMaxBlockShared;
+cudaError_t launch_kept(const GemvParams& p, int sm_count, cudaStream_t stream) {
     static_assert(kWarps * warp_bytes<GP, NT, T, D>(T == 2 ? kPairM : 8 * NT, 1, false) <= kMaxBlockShared, "one stage of x fits");
-    return launch<FMT, GP, NT, T, D>(p, sm_count, stream);
+    if (kWarps * warp_bytes<GP, NT, T, D>(p.M, p.pieces, true) <= kMaxBlockShared)
+        return launch<FMT, GP, NT, T, D, true>(p, sm_count, stream);
+    return launch<FMT, GP, NT, T, D, false>(p, sm_count, stream);
 }
 
 }  // namespace
@@ -235,9 +267,9 @@ cudaError_t launch_gemv_w4(const GemvW4Args& a, cudaStream_t stream) {
     p.pieces = ((p.chunks + p.WK - 1) / p.WK + kPC - 1) / kPC;
     p.pdl = a.pdl;
     return dispatch_format(a.format, a.group, [&](auto fmt, auto gp) {
-        if (a.M <= kPairM) return launch_depth<fmt(), gp(), 1, 2, 2>(p, a.sm_count, stream);
-        if (a.M <= 8) return launch_depth<fmt(), gp(), 1, 1, 3>(p, a.sm_count, stream);
-        return launch_depth<fmt(), gp(), 2, 1, 2>(p, a.sm_count, stream);
+        if (a.M <= kPairM) return launch_kept<fmt(), gp(), 1, 2, 2>(p, a.sm_count, stream);
+        if (a.M <= 8) return launch_kept<fmt(), gp(), 1, 1, 3>(p, a.sm_count, stream);
+        return launch_kept<fmt(), gp(), 2, 1, 2>(p, a.sm_count, stream);
     });
 }
 
