@@ -18,7 +18,6 @@ using namespace w4;
 
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
-constexpr int kPairM = 5;  // tokens up to which two tiles make a stage
 constexpr int kGroup = 4;  // tiles summed in registers before the slices meet
 
 struct GemvParams {
@@ -238,12 +237,10 @@ cudaError_t launch(const GemvParams& p, int sm_count, cudaStream_t stream) {
     return launch_dependent(gemv_w4_kernel<FMT, GP, NT, T, D, RES>, min((p.tiles + p.WR - 1) / p.WR, sm_count), kThreads, smem, stream, p);
 }
 
-template <int FMT, int GP, int NT, int T, int D>
-cudaError_t launch_kept(const GemvParams& p, int sm_count, cudaStream_t stream) {
-    static_assert(kWarps * warp_bytes<GP, NT, T, D>(T == 2 ? kPairM : 8 * NT, 1, false) <= kMaxBlockShared, "one stage of x fits");
-    if (kWarps * warp_bytes<GP, NT, T, D>(p.M, p.pieces, true) <= kMaxBlockShared)
-        return launch<FMT, GP, NT, T, D, true>(p, sm_count, stream);
-    return launch<FMT, GP, NT, T, D, false>(p, sm_count, stream);
+// Whether a block with this ring fits, all of x staged (RES) or a stage of it.
+template <int GP, int NT, int T, int D, bool RES>
+bool fits(const GemvParams& p) {
+    return kWarps * warp_bytes<GP, NT, T, D>(p.M, p.pieces, RES) <= kMaxBlockShared;
 }
 
 }  // namespace
@@ -267,9 +264,22 @@ cudaError_t launch_gemv_w4(const GemvW4Args& a, cudaStream_t stream) {
     p.pieces = ((p.chunks + p.WK - 1) / p.WK + kPC - 1) / kPC;
     p.pdl = a.pdl;
     return dispatch_format(a.format, a.group, [&](auto fmt, auto gp) {
-        if (a.M <= kPairM) return launch_kept<fmt(), gp(), 1, 2, 2>(p, a.sm_count, stream);
-        if (a.M <= 8) return launch_kept<fmt(), gp(), 1, 1, 3>(p, a.sm_count, stream);
-        return launch_kept<fmt(), gp(), 2, 1, 2>(p, a.sm_count, stream);
+        constexpr int F = fmt(), G = gp();
+        const int sm = a.sm_count, blocks = min((p.tiles + p.WR - 1) / p.WR, sm);
+        const int steps = ((p.tiles + blocks - 1) / blocks + p.WR - 1) / p.WR;  // tiles of a warp
+        if (a.M > 8) {
+            if (fits<G, 2, 1, 2, true>(p)) return launch<F, G, 2, 1, 2, true>(p, sm, stream);
+            return launch<F, G, 2, 1, 2, false>(p, sm, stream);
+        }
+        // two tiles a stage share its activations; where a warp has one tile,
+        // half of such a stage would be idle.  (A slice of one stage is staged
+        // once for kGroup tiles without being kept.)
+        if (steps > 1 && fits<G, 1, 2, 2, true>(p)) return launch<F, G, 1, 2, 2, true>(p, sm, stream);
+        if (steps > 1 && p.pieces == 1 && fits<G, 1, 2, 2, false>(p)) return launch<F, G, 1, 2, 2, false>(p, sm, stream);
+        if (fits<G, 1, 1, 3, true>(p)) return launch<F, G, 1, 1, 3, true>(p, sm, stream);
+        if (p.pieces == 1) return launch<F, G, 1, 1, 3, false>(p, sm, stream);
+        if (fits<G, 1, 1, 2, true>(p)) return launch<F, G, 1, 1, 2, true>(p, sm, stream);
+        return launch<F, G, 1, 1, 3, false>(p, sm, stream);
     });
 }
 

@@ -74,6 +74,38 @@ __device__ Lists build_lists(const MoeParams& p, int batch, uint8_t* mem, int* c
     L.pair = reinterpret_cast<uint32_t*>(L.entry + P);
     L.place = reinterpret_cast<uint16_t*>(L.pair + P);
     L.unsorted = L.place + P;
+    if (P <= 32) {  // one warp, lane q pair q, without the histogram: entries by their first pair
+        if (warp == 0) {
+            int e = lane < P ? p.ids[lane] : -1;
+            if (lane < P && (e < 0 || e >= p.E)) record_error(p.err, FP8BS_ERR_DEVICE);
+            if (e >= p.E) e = -1;
+            const bool valid = e >= 0;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, valid ? e : -1 - lane), below = (1u << lane) - 1u;
+            const int rank = __popc(same & below), n = __popc(same);
+            const bool leads = valid && rank % batch == 0;  // the first pair of an entry
+            const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, leads);
+            const int size = leads ? min(batch, n - rank) : 0;
+            int incl = size;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+                if (lane >= off) incl += v;
+            }
+            // the last leader of the same expert at or below this lane
+            const uint32_t mine = leaders & same & (below | 1u << lane);
+            const int from = mine ? 31 - __clz(mine) : lane;
+            const int first = __shfl_sync(0xFFFFFFFFu, incl - size, from);
+            if (leads)
+                L.entry[__popc(leaders & below)] = make_ushort4(static_cast<unsigned short>(e), static_cast<unsigned short>(first),
+                                                                static_cast<unsigned short>(size), 0);
+            if (valid) L.pair[first + rank % batch] = static_cast<uint32_t>(lane) | static_cast<uint32_t>(lane / p.S) << 16;
+            if (lane < P) L.place[lane] = valid ? static_cast<uint16_t>(first + rank % batch) : 0xFFFF;
+            if (lane == 0) n_entries = __popc(leaders);
+        }
+        __syncthreads();
+        L.entries = n_entries;
+        return L;
+    }
     constexpr int kMine = (FP8BS_MOE_MAX_PAIRS + THREADS - 1) / THREADS;
     int id[kMine], rank[kMine];
 #pragma unroll
