@@ -412,3 +412,16 @@ def test_layer_routed_and_captured(dev):
         check(y, ref, bound, "layer experts")
         check(out, *R.gemv(H.torch_u16_to_np(y), R.value(co, so, fmt, group)), "layer projection")
     assert fb.fp8bs_check_error(wsm) == 0
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "int4"])
+def test_example_decode_step(dev, fmt):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_w4.py")
+    spec = importlib.util.spec_from_file_location("decode_w4", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    # two bf16 roundings on the way (y and the output), half a step each, and
+    # fp32 sums far below them
+    assert mod.main(["--format", fmt, "--tokens", "5", "--steps", "2"]) <= 2 * R.HALF_BF16
