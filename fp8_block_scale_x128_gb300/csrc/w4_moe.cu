@@ -343,10 +343,10 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
 
 // ---- 2. down -----------------------------------------------------------------
 constexpr int kDownDepth = 3;
-constexpr int kDownWarps = 8, kDownThreads = kDownWarps * 32;
 
 // Bytes of a warp: the ring, the scale table, the inverse scales and a stage of
 // a for n pairs.
+constexpr int kWideDownPairs = 256;
 constexpr int kInvBytes = 128;  // 8 factors, the next part aligned
 template <int GP>
 __host__ __device__ constexpr int down_bytes(int n) {
@@ -355,9 +355,9 @@ __host__ __device__ constexpr int down_bytes(int n) {
 // the pairs' products for 16 rows by place, and the pairs' routing weights
 __host__ __device__ constexpr int out_bytes(int P) { return (P * (kTileRows + 1) * 4 + 127) / 128 * 128; }
 
-// ONE: the whole of I in one stage.
-template <int FMT, int GP, bool ONE>
-__global__ void __launch_bounds__(kDownThreads, 2) moe_w4_down_kernel(const __grid_constant__ MoeParams p, int batch) {
+// ONE: the whole of I in one stage; WARPS: 8, two blocks a multiprocessor, or 16.
+template <int FMT, int GP, bool ONE, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) moe_w4_down_kernel(const __grid_constant__ MoeParams p, int batch) {
     constexpr int SB = Format<FMT, GP>::kScaleBytes, D = kDownDepth;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -372,8 +372,8 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_w4_down_kernel(const __gr
     const uint32_t from_codes = mine + code_src(lane), from_table = mine + kTableAt + scale_src<GP>(lane);
     const uint32_t from_inv = mine + kInvAt + inv_src(lane);
     // the routing is complete: the first launch has waited for what wrote it
-    for (int q = tid; q < P; q += kDownThreads) weight[q] = p.tw[q];
-    const Lists L = build_lists<kDownThreads>(p, batch, smem, reinterpret_cast<int*>(base));
+    for (int q = tid; q < P; q += (WARPS * 32)) weight[q] = p.tw[q];
+    const Lists L = build_lists<WARPS * 32>(p, batch, smem, reinterpret_cast<int*>(base));
 
     const int chunks = p.I / kChunk, pieces = ONE ? 1 : (chunks + kPC - 1) / kPC;
     const uint32_t ldc = p.I / 2, lds = chunks * SB;
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_w4_down_kernel(const __gr
                 raw = load_scales<FMT, GP>(at(lane_scales, e, expert_scales) + ahead_piece * kPC * SB, nch, lane);
             }
             cp_async_commit();
-            if (ONE || ++ahead_piece == pieces) ahead_piece = 0, ahead += kDownWarps;
+            if (ONE || ++ahead_piece == pieces) ahead_piece = 0, ahead += WARPS;
             return raw;
         };
         uint2 raw[D - 1];
@@ -416,9 +416,9 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_w4_down_kernel(const __gr
         ushort4 now = L.entry[min(warp, max(L.entries - 1, 0))];
         if (warp < L.entries) load_tokens(now, 0, 0);
         uint32_t slot_at = 0;
-        for (int entry = warp; entry < L.entries; entry += kDownWarps) {
+        for (int entry = warp; entry < L.entries; entry += WARPS) {
             const int n = now.z, pf = now.y;
-            const ushort4 next = L.entry[min(entry + kDownWarps, L.entries - 1)];
+            const ushort4 next = L.entry[min(entry + WARPS, L.entries - 1)];
             const uint32_t x[1] = {xs + token_src(lane >> 2, n, lane)};
             float tot[1][1][4] = {};
             for (int piece = 0; piece < pieces; ++piece) {
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_w4_down_kernel(const __gr
             now = next;
         }
         __syncthreads();
-        for (int o = tid; o < p.M * kTileRows; o += kDownThreads) {
+        for (int o = tid; o < p.M * kTileRows; o += (WARPS * 32)) {
             const int m = o / kTileRows, row = o % kTileRows;
             float v = 0.0f;
 #pragma unroll 4
@@ -464,16 +464,16 @@ __global__ void __launch_bounds__(kDownThreads, 2) moe_w4_down_kernel(const __gr
     }
 }
 
-// The pairs of an entry and the blocks of a multiprocessor: two blocks, with as
+// The pairs of an entry and the blocks of a multiprocessor (at most `most`): two blocks, with as
 // many pairs as then fit, unless the experts have more than twice as many on
 // average (their codes would be fetched and decoded over and over): then one.
 template <typename F>
-int batch_of(const MoeParams& p, F&& bytes, int& per_sm) {
+int batch_of(const MoeParams& p, F&& bytes, int most, int& per_sm) {
     constexpr int kHalf = kMaxSmShared / 2 - 1024 - 128;  // less a block's reserved and static shared memory
     int batch = kMaxBatch;
     while (batch > 0 && bytes(batch) > kHalf) --batch;
     per_sm = 2;
-    if (batch > 0 && (batch == kMaxBatch || p.M * p.S <= 2 * batch * p.E)) return batch;
+    if (most > 1 && batch > 0 && (batch == kMaxBatch || p.M * p.S <= 2 * batch * p.E)) return batch;
     per_sm = 1;
     for (batch = kMaxBatch; batch > 1 && bytes(batch) > kMaxBlockShared; --batch) {}
     return batch;
@@ -489,25 +489,34 @@ cudaError_t launch_up(const MoeParams& p, int sm_count, cudaStream_t stream) {
         return lists_bytes(P) + max(counts_bytes(p.E), kWarps * up_bytes<GP>(min(P, batch), pieces));
     };
     int per_sm;
-    const int batch = batch_of(p, bytes, per_sm), smem = bytes(batch);
+    const int batch = batch_of(p, bytes, 2, per_sm), smem = bytes(batch);
     if (smem > kMaxBlockShared) return cudaErrorInvalidValue;
     const int64_t most = static_cast<int64_t>(P) * (p.I / kTileRows);
     const int grid = static_cast<int>(min(most, static_cast<int64_t>(sm_count) * per_sm));
     return launch_dependent(moe_w4_up_kernel<FMT, GP>, grid, kThreads, smem, stream, p, batch);
 }
 
-template <int FMT, int GP, bool ONE>
-cudaError_t launch_down(const MoeParams& p, int sm_count, cudaStream_t stream) {
+template <int FMT, int GP, bool ONE, int WARPS>
+cudaError_t launch_down_warps(const MoeParams& p, int sm_count, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_shared(moe_w4_down_kernel<FMT, GP, ONE>, allowed);
+    cudaError_t e = allow_shared(moe_w4_down_kernel<FMT, GP, ONE, WARPS>, allowed);
     if (e != cudaSuccess) return e;
     const int P = p.M * p.S;
     auto bytes = [&](int batch) {
-        return lists_bytes(P) + out_bytes(P) + max(counts_bytes(p.E), kDownWarps * down_bytes<GP>(min(P, batch)));
+        return lists_bytes(P) + out_bytes(P) + max(counts_bytes(p.E), WARPS * down_bytes<GP>(min(P, batch)));
     };
     int per_sm;
-    const int batch = batch_of(p, bytes, per_sm);
-    return launch_dependent(moe_w4_down_kernel<FMT, GP, ONE>, min(p.H / kTileRows, sm_count * per_sm), kDownThreads, bytes(batch), stream, p, batch);
+    const int batch = batch_of(p, bytes, 16 / WARPS, per_sm), smem = bytes(batch);
+    return launch_dependent(moe_w4_down_kernel<FMT, GP, ONE, WARPS>, min(p.H / kTileRows, sm_count * per_sm), WARPS * 32, smem, stream, p, batch);
+}
+
+template <int FMT, int GP, bool ONE>
+cudaError_t launch_down(const MoeParams& p, int sm_count, cudaStream_t stream) {
+    // with no more tiles than multiprocessors a second block would have none;
+    // the 16 warps of one deal out the experts instead, as long as they fit
+    // beside the pairs' products
+    if (p.H / kTileRows <= sm_count && p.M * p.S <= kWideDownPairs) return launch_down_warps<FMT, GP, ONE, 16>(p, sm_count, stream);
+    return launch_down_warps<FMT, GP, ONE, 8>(p, sm_count, stream);
 }
 
 }  // namespace
