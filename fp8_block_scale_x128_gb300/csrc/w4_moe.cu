@@ -11,8 +11,8 @@
 //    stages an expert's tokens once for its run; the 8 warps of a block split
 //    H, their sums are added in warp order and the activation applied to the
 //    whole sum.
-// 2. down: a block owns 16 rows of the output for every token, its warps deal
-//    out the experts; the pairs' products meet in shared memory and are summed
+// 2. down: a block owns 16 or 32 rows of the output for every token, its warps
+//    deal out the experts; the pairs' products meet in shared memory and are summed
 //    in slot order.  No partial sums in global memory, no atomics on values.
 //
 // An expert's codes are read once for a batch of its pairs.  Every block builds
@@ -342,32 +342,32 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
 }
 
 // ---- 2. down -----------------------------------------------------------------
-constexpr int kDownDepth = 3;
-
-// Bytes of a warp: the ring, the scale table, the inverse scales and a stage of
-// a for n pairs.
+// Bytes of a warp: a ring of stages of T tiles, their scale tables, the inverse
+// scales and a stage of a for n pairs.
 constexpr int kWideDownPairs = 256;
 constexpr int kInvBytes = 128;  // 8 factors, the next part aligned
+__host__ __device__ constexpr int down_depth(int T) { return T == 2 ? 2 : 3; }
 template <int GP>
-__host__ __device__ constexpr int down_bytes(int n) {
-    return kDownDepth * kCodeBytes + kTableBytes<GP> + kInvBytes + n * kTokenBytes;
+__host__ __device__ constexpr int down_bytes(int n, int T) {
+    return down_depth(T) * T * kCodeBytes + T * kTableBytes<GP> + kInvBytes + n * kTokenBytes;
 }
-// the pairs' products for 16 rows by place, and the pairs' routing weights
-__host__ __device__ constexpr int out_bytes(int P) { return (P * (kTileRows + 1) * 4 + 127) / 128 * 128; }
+// the pairs' products for the rows by place, and the pairs' routing weights
+__host__ __device__ constexpr int out_bytes(int P, int T) { return (P * (T * kTileRows + 1) * 4 + 127) / 128 * 128; }
 
-// ONE: the whole of I in one stage; WARPS: 8, two blocks a multiprocessor, or 16.
-template <int FMT, int GP, bool ONE, int WARPS>
+// ONE: the whole of I in one stage; T: tiles of a block; WARPS: 8, two blocks a
+// multiprocessor, or 16.
+template <int FMT, int GP, bool ONE, int T, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) moe_w4_down_kernel(const __grid_constant__ MoeParams p, int batch) {
-    constexpr int SB = Format<FMT, GP>::kScaleBytes, D = kDownDepth;
+    constexpr int SB = Format<FMT, GP>::kScaleBytes, D = down_depth(T), kSlot = T * kCodeBytes, kRows = T * kTileRows;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = p.M * p.S;
-    float* out = reinterpret_cast<float*>(smem + lists_bytes(P));  // [P][16]
-    float* weight = out + P * kTileRows;
-    uint8_t* base = smem + lists_bytes(P) + out_bytes(P);
-    // a warp's memory: codes [D], the scale table, inv, the entry's a
-    constexpr int kTableAt = D * kCodeBytes, kInvAt = kTableAt + kTableBytes<GP>, kXsAt = kInvAt + kInvBytes;
-    const uint32_t mine = ptx::smem_addr(base) + warp * down_bytes<GP>(min(P, batch)), xs = mine + kXsAt;
+    float* out = reinterpret_cast<float*>(smem + lists_bytes(P));  // [P][kRows]
+    float* weight = out + P * kRows;
+    uint8_t* base = smem + lists_bytes(P) + out_bytes(P, T);
+    // a warp's memory: codes [D][T], the scale tables, inv, the entry's a
+    constexpr int kTableAt = D * kSlot, kInvAt = kTableAt + T * kTableBytes<GP>, kXsAt = kInvAt + kInvBytes;
+    const uint32_t mine = ptx::smem_addr(base) + warp * down_bytes<GP>(min(P, batch), T), xs = mine + kXsAt;
     const uint32_t to_codes = mine + code_dst(lane), to_table = mine + kTableAt + scale_dst<GP>(lane);
     const uint32_t from_codes = mine + code_src(lane), from_table = mine + kTableAt + scale_src<GP>(lane);
     const uint32_t from_inv = mine + kInvAt + inv_src(lane);
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) moe_w4_down_kernel(con
     const uint8_t* lane_a = reinterpret_cast<const uint8_t*>(p.a) + 16 * lane;
     const uint8_t* lane_ae = p.ae + (lane >> 1);
     const uint32_t la = p.I * 2, le = p.I / kTileRows;
-    const int tiles = p.H / kTileRows;
+    const int tiles = p.H / kRows;
     RawFp16 tokens;
     auto load_tokens = [&](const ushort4& entry, int piece, int i0) {
         const uint32_t* pair = L.pair + entry.y + i0;
@@ -390,25 +390,28 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) moe_w4_down_kernel(con
     };
 
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const uint8_t* lane_codes = at(p.w2 + static_cast<int64_t>(lane >> 3) * ldc + (lane & 7) * 16, tile * kTileRows, ldc);
-        const uint8_t* lane_scales = at(p.s2 + static_cast<int64_t>(lane >> 1) * lds + (lane & 1) * SB, tile * kTileRows, lds);
+        const uint8_t* lane_codes = at(p.w2 + static_cast<int64_t>(lane >> 3) * ldc + (lane & 7) * 16, tile * kRows, ldc);
+        const uint8_t* lane_scales = at(p.s2 + static_cast<int64_t>(lane >> 1) * lds + (lane & 1) * SB, tile * kRows, lds);
         // a warp's stages: its entries, in an entry the pieces of I
         int ahead = warp, ahead_piece = 0;
-        auto issue = [&](uint32_t slot_at) {
-            uint2 raw = make_uint2(0, 0);
+        auto issue = [&](uint32_t slot_at, uint2 (&raw)[T]) {
             if (ahead < L.entries) {
                 const uint32_t e = L.entry[ahead].x;
                 const int nch = min(chunks - ahead_piece * kPC, kPC);
-                load_codes(to_codes + slot_at, at(lane_codes, e, expert_codes) + ahead_piece * kPC * 64, ldc, kTileRows - 1, nch, lane);
-                raw = load_scales<FMT, GP>(at(lane_scales, e, expert_scales) + ahead_piece * kPC * SB, nch, lane);
+                const uint8_t* c = at(lane_codes, e, expert_codes) + ahead_piece * kPC * 64;
+                const uint8_t* s = at(lane_scales, e, expert_scales) + ahead_piece * kPC * SB;
+#pragma unroll
+                for (int i = 0; i < T; ++i) {
+                    load_codes(to_codes + slot_at + i * kCodeBytes, at(c, ldc, i * kTileRows), ldc, kTileRows - 1, nch, lane);
+                    raw[i] = load_scales<FMT, GP>(at(s, lds, i * kTileRows), nch, lane);
+                }
             }
             cp_async_commit();
             if (ONE || ++ahead_piece == pieces) ahead_piece = 0, ahead += WARPS;
-            return raw;
         };
-        uint2 raw[D - 1];
+        uint2 raw[D - 1][T] = {};
 #pragma unroll
-        for (int i = 0; i < D - 1; ++i) raw[i] = issue(i * kCodeBytes);
+        for (int i = 0; i < D - 1; ++i) issue(i * kSlot, raw[i]);
         if (tile == static_cast<int>(blockIdx.x)) {
             ptx::griddep_wait();
             ptx::griddep_launch_dependents();
@@ -420,13 +423,17 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) moe_w4_down_kernel(con
             const int n = now.z, pf = now.y;
             const ushort4 next = L.entry[min(entry + WARPS, L.entries - 1)];
             const uint32_t x[1] = {xs + token_src(lane >> 2, n, lane)};
-            float tot[1][1][4] = {};
+            float tot[T][1][4] = {};
             for (int piece = 0; piece < pieces; ++piece) {
                 const int nch = min(chunks - piece * kPC, kPC);
-                const uint2 cur[1] = {raw[0]};
+                uint2 cur[T];
 #pragma unroll
-                for (int i = 0; i + 2 < D; ++i) raw[i] = raw[i + 1];
-                raw[D - 2] = issue(slot_at == 0 ? (D - 1) * kCodeBytes : slot_at - kCodeBytes);
+                for (int i = 0; i < T; ++i) {
+                    cur[i] = raw[0][i];
+#pragma unroll
+                    for (int k = 0; k + 2 < D; ++k) raw[k][i] = raw[k + 1][i];
+                }
+                issue(slot_at == 0 ? (D - 1) * kSlot : slot_at - kSlot, raw[D - 2]);
                 tokens.store(xs, mine + kInvAt, 0, n, lane);
                 for (int i0 = RawFp16::kTokens; i0 < n; i0 += RawFp16::kTokens) {
                     load_tokens(now, piece, i0);
@@ -436,29 +443,32 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) moe_w4_down_kernel(con
                     load_tokens(now, piece + 1, 0);
                 else
                     load_tokens(next, 0, 0);
-                const float back = store_scales<FMT, GP, 1>(to_table, cur);
+                const float back = store_scales<FMT, GP, T>(to_table, cur);
                 cp_async_wait<D - 1>();
                 __syncwarp();
-                stage_mma<FMT, GP, 1, 1>(tot, from_codes + slot_at, from_table, x, from_inv, back, nch);
+                stage_mma<FMT, GP, 1, T>(tot, from_codes + slot_at, from_table, x, from_inv, back, nch);
                 __syncwarp();  // the slot, the table and the tokens are rewritten by later stages
-                slot_at = slot_at == (D - 1) * kCodeBytes ? 0 : slot_at + kCodeBytes;
+                slot_at = slot_at == (D - 1) * kSlot ? 0 : slot_at + kSlot;
             }
             const int col = 2 * (lane & 3);
-            float* o = out + (pf + col) * kTileRows + (lane >> 2);
-            if (col < n) o[0] = tot[0][0][0], o[8] = tot[0][0][2];
-            if (col + 1 < n) o[kTileRows] = tot[0][0][1], o[kTileRows + 8] = tot[0][0][3];
+            float* o = out + (pf + col) * kRows + (lane >> 2);
+#pragma unroll
+            for (int i = 0; i < T; ++i, o += kTileRows) {
+                if (col < n) o[0] = tot[i][0][0], o[8] = tot[i][0][2];
+                if (col + 1 < n) o[kRows] = tot[i][0][1], o[kRows + 8] = tot[i][0][3];
+            }
             now = next;
         }
         __syncthreads();
-        for (int o = tid; o < p.M * kTileRows; o += (WARPS * 32)) {
-            const int m = o / kTileRows, row = o % kTileRows;
+        for (int o = tid; o < p.M * kRows; o += WARPS * 32) {
+            const int m = o / kRows, row = o % kRows;
             float v = 0.0f;
 #pragma unroll 4
             for (int q = m * p.S; q < (m + 1) * p.S; ++q) {
                 const int place = L.place[q];  // 0xFFFF: an invalid id contributes nothing
-                if (place != 0xFFFF) v = fmaf(weight[q], out[place * kTileRows + row], v);
+                if (place != 0xFFFF) v = fmaf(weight[q], out[place * kRows + row], v);
             }
-            p.y[static_cast<int64_t>(m) * p.H + tile * kTileRows + row] = to_bf16(v);
+            p.y[static_cast<int64_t>(m) * p.H + tile * kRows + row] = to_bf16(v);
         }
         __syncthreads();  // out is rewritten for the next tile
     }
@@ -496,27 +506,37 @@ cudaError_t launch_up(const MoeParams& p, int sm_count, cudaStream_t stream) {
     return launch_dependent(moe_w4_up_kernel<FMT, GP>, grid, kThreads, smem, stream, p, batch);
 }
 
-template <int FMT, int GP, bool ONE, int WARPS>
-cudaError_t launch_down_warps(const MoeParams& p, int sm_count, cudaStream_t stream) {
-    static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_shared(moe_w4_down_kernel<FMT, GP, ONE, WARPS>, allowed);
-    if (e != cudaSuccess) return e;
+template <int GP, int T, int WARPS>
+int down_block_bytes(const MoeParams& p, int batch) {
     const int P = p.M * p.S;
-    auto bytes = [&](int batch) {
-        return lists_bytes(P) + out_bytes(P) + max(counts_bytes(p.E), WARPS * down_bytes<GP>(min(P, batch)));
-    };
+    return lists_bytes(P) + out_bytes(P, T) + max(counts_bytes(p.E), WARPS * down_bytes<GP>(min(P, batch), T));
+}
+
+template <int FMT, int GP, bool ONE, int T, int WARPS>
+cudaError_t launch_down_as(const MoeParams& p, int sm_count, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_shared(moe_w4_down_kernel<FMT, GP, ONE, T, WARPS>, allowed);
+    if (e != cudaSuccess) return e;
     int per_sm;
-    const int batch = batch_of(p, bytes, 16 / WARPS, per_sm), smem = bytes(batch);
-    return launch_dependent(moe_w4_down_kernel<FMT, GP, ONE, WARPS>, min(p.H / kTileRows, sm_count * per_sm), WARPS * 32, smem, stream, p, batch);
+    const int batch = batch_of(p, [&](int n) { return down_block_bytes<GP, T, WARPS>(p, n); }, 16 / WARPS, per_sm);
+    return launch_dependent(moe_w4_down_kernel<FMT, GP, ONE, T, WARPS>, min(p.H / (T * kTileRows), sm_count * per_sm), WARPS * 32,
+                            down_block_bytes<GP, T, WARPS>(p, batch), stream, p, batch);
 }
 
 template <int FMT, int GP, bool ONE>
 cudaError_t launch_down(const MoeParams& p, int sm_count, cudaStream_t stream) {
-    // with no more tiles than multiprocessors a second block would have none;
-    // the 16 warps of one deal out the experts instead, as long as they fit
-    // beside the pairs' products
-    if (p.H / kTileRows <= sm_count && p.M * p.S <= kWideDownPairs) return launch_down_warps<FMT, GP, ONE, 16>(p, sm_count, stream);
-    return launch_down_warps<FMT, GP, ONE, 8>(p, sm_count, stream);
+    const int tiles = p.H / kTileRows;
+    // Two tiles a stage share its other costs, where they still fill most of the
+    // machine and 16 warps fit beside the pairs' products with three pairs an
+    // entry (8 tokens of 513x128: 13.3 us for 15.7; with 352 pairs only one fits
+    // and an expert's codes are fetched for each of its pairs: 45 us for 43).
+    constexpr int kWant = 3;
+    if (tiles > sm_count && down_block_bytes<GP, 2, 16>(p, kWant) <= kMaxBlockShared)
+        return launch_down_as<FMT, GP, ONE, 2, 16>(p, sm_count, stream);
+    // With no more tiles than multiprocessors a second block would have none (19
+    // tokens of 24x512: 13.6 us for 14.8).
+    if (tiles <= sm_count && p.M * p.S <= kWideDownPairs) return launch_down_as<FMT, GP, ONE, 1, 16>(p, sm_count, stream);
+    return launch_down_as<FMT, GP, ONE, 1, 8>(p, sm_count, stream);
 }
 
 }  // namespace
