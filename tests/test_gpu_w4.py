@@ -226,6 +226,23 @@ def test_gemv_repeats_bit_for_bit_on_another_stream_pdl_and_graph(dev):
         assert torch.equal(o.view(torch.int16), first.view(torch.int16))
 
 
+def test_gemv_codes_beyond_32_bit_offsets(dev):
+    # 5.4 GB of codes; only the first and the last rows are not zero
+    M, N, K, fmt, group = 2, (1 << 20) + 5, 10240, INT4, 128
+    x = synth.x_bf16(M, K, seed=71)
+    c, s = R.weight(64, K, fmt, group, 72)
+    codes = torch.full((N, K // 2), 0x88, dtype=torch.uint8, device=dev)  # the value 0
+    scales = torch.ones((N, K // group), dtype=torch.bfloat16, device=dev)
+    for rows in (slice(0, 32), slice(N - 32, N)):
+        part = slice(0, 32) if rows.start == 0 else slice(32, 64)
+        codes[rows] = to_dev(c[part], dev)
+        scales[rows] = scales_dev(s[part], fmt, dev)
+    y = fb.fp8bs_gemv_w4a16(bf16_dev(x, dev), codes, scales, fmt, group)
+    ref, bound = R.gemv(x, R.value(c, s, fmt, group))
+    check(torch.cat((y[:, :32], y[:, N - 32:]), 1), ref, bound, "large offsets")
+    assert bool((y[:, 32:N - 32] == 0).all())
+
+
 def test_gemv_empty_batch(dev):
     y = torch.full((0, 64), 1.0, dtype=torch.bfloat16, device=dev)
     codes, scales = R.weight(64, 256, MXFP4, 32, 1)
@@ -379,6 +396,43 @@ def test_moe_only_invalid_ids_give_zeros(dev):
     ids = np.full((2, 2), -1, np.int32)
     tw = np.ones((2, 2), np.float32)
     assert run_moe(dev, 2, 2, 3, 256, 128, MXFP4, 32, seed=510, ids=ids, tw=tw) == fb.FP8BS_ERR_DEVICE
+
+
+def test_moe_weights_beyond_32_bit_offsets(dev):
+    # 4.3 GB of gate/up codes: the experts used are the first and the last
+    E, Hd, I, fmt, group, M = 4096, 4096, 256, MXFP4, 32, 3
+    c13, s13, c2, s2 = experts(2, Hd, I, fmt, group, 520)
+    big = [torch.zeros((E, *v.shape[1:]), dtype=torch.uint8, device=dev) for v in (c13, s13, c2, s2)]
+    for b, v in zip(big, (c13, s13, c2, s2)):
+        b[0], b[E - 1] = to_dev(v[0], dev), to_dev(v[1], dev)
+    x = synth.x_bf16(M, Hd, seed=521)
+    small = np.array([[0, 1], [1, 0], [1, 1]], np.int32)
+    tw = np.array([[0.5, 0.5], [1.0, -0.25], [0.75, 0.5]], np.float32)
+    ws = fb.new_moe_w4_workspace(M, 2, I, dev)
+    y = fb.fp8bs_moe_w4a16(bf16_dev(x, dev), to_dev(small * (E - 1), dev), to_dev(tw, dev), *big, fmt, group, workspace=ws)
+    assert fb.fp8bs_check_error(ws) == 0
+    check(y, *R.moe(x, small, tw, R.value(c13, s13, fmt, group), R.value(c2, s2, fmt, group)), "large offsets")
+
+
+@pytest.mark.parametrize("fmt,group", [(MXFP4, 32), (INT4, 64)])
+def test_moe_infinities_and_nan_stay_in_their_token(dev, fmt, group):
+    M, S, E, Hd, I = 5, 3, 4, 512, 256
+    x = synth.x_bf16(M, Hd, seed=530)
+    x[1, 3], x[3, 400] = 0x7F80, 0x7FC0  # inf, NaN
+    ids, tw = synth.moe_routing(M, S, E, seed=531)
+    c13, s13, c2, s2 = experts(E, Hd, I, fmt, group, 532)
+    y = f64(fb.fp8bs_moe_w4a16(bf16_dev(x, dev), to_dev(ids, dev), to_dev(tw, dev), to_dev(c13, dev),
+                               scales_dev(s13, fmt, dev), to_dev(c2, dev), scales_dev(s2, fmt, dev), fmt, group))
+    clean = [0, 2, 4]
+    ref, bound = R.moe(x[clean], ids[clean], tw[clean], R.value(c13, s13, fmt, group), R.value(c2, s2, fmt, group))
+    assert np.all(np.abs(y[clean] - ref) <= bound)
+    assert not np.any(np.isfinite(y[[1, 3]]))
+
+
+@pytest.mark.parametrize("Hd,I,M", [(4096, 128, 8), (4096, 256, 3), (2560, 128, 8), (8192, 128, 2)])
+def test_moe_tile_and_warp_choices_of_the_down_projection(dev, Hd, I, M):
+    # one and two tiles a stage, 8 and 16 warps, more tiles than blocks
+    assert run_moe(dev, M, 4, 12, Hd, I, INT4, 128, seed=540 + M) == 0
 
 
 def test_layer_routed_and_captured(dev):
