@@ -13,7 +13,7 @@
 // launch).
 //
 // The order of the chosen experts is decided by fp32 logits unless two of them
-// (or the last chosen and the first left out) are within 2^-18 of the largest
+// (or the last chosen and the first left out) are within 2^-20 of the largest
 // logit: those are summed again with a compensated sum, which orders them as a
 // 64-bit sum would.
 #include "internal.cuh"
@@ -106,6 +106,7 @@ __device__ double exact_logit(const RouteParams& p, int m, int e, int lane) {
 // A warp's scratch.
 struct Select {
     double cand_value[kMaxCand];
+    uint32_t key[kMaxCand];
     float value[FP8BS_ROUTE_MAX_K + 1];
     int16_t expert[FP8BS_ROUTE_MAX_K + 1];
     int16_t cand[kMaxCand];
@@ -142,42 +143,83 @@ __device__ void select_token(const RouteParams& p, Select& sel, int m, int lane)
         if (in) top_abs = max(top_abs, __float_as_uint(v[j]) & 0x7FFFFFFFu);
     }
     top_abs = __reduce_max_sync(0xFFFFFFFFu, top_abs);
-    // every lane holds its best, the warp's best of them is taken round by round
-    uint32_t best;
-    int best_j;
-    auto rescan = [&]() {
-        uint32_t m[PER];
-        int at[PER];
-#pragma unroll
-        for (int j = 0; j < PER; ++j) m[j] = key[j];
-#pragma unroll
-        for (int w = PER / 2; w > 0; w /= 2)
-#pragma unroll
-            for (int j = 0; j < w; ++j) m[j] = max(m[j], m[j + w]);
-        best = m[0];
-#pragma unroll
-        for (int j = 0; j < PER; ++j) at[j] = key[j] == best ? j : PER;
-#pragma unroll
-        for (int w = PER / 2; w > 0; w /= 2)
-#pragma unroll
-            for (int j = 0; j < w; ++j) at[j] = min(at[j], at[j + w]);
-        best_j = at[0];
-    };
-    rescan();
     const int kk = min(p.k + 1, p.E);
-    for (int r = 0; r < kk; ++r) {
-        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-        const uint32_t who = __ballot_sync(0xFFFFFFFFu, best == top);
-        int e = best_j * 32 + lane;
-        if (who & (who - 1))  // several lanes: the lowest expert of them
-            e = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, best == top ? static_cast<uint32_t>(e) : 0xFFFFFFFFu));
-        if (best == top && e == best_j * 32 + lane) {
-            sel.value[r] = key_value(top);
-            sel.expert[r] = static_cast<int16_t>(e);
+    // The kk-th largest of the lanes' maxima is a bound that at least kk experts
+    // reach; the few that do are ranked against each other.
+    int n_top = kMaxCand + 1;
+    if (kk <= 32) {
+        uint32_t most = key[0];
 #pragma unroll
-            for (int j = 0; j < PER; ++j)
-                if (j == best_j) key[j] = 0;
-            rescan();
+        for (int j = 1; j < PER; ++j) most = max(most, key[j]);
+        int rank = 0;
+#pragma unroll
+        for (int o = 0; o < 32; ++o) {
+            const uint32_t other = __shfl_sync(0xFFFFFFFFu, most, o);
+            rank += other > most || (other == most && o < lane);
+        }
+        const uint32_t bound = max(__shfl_sync(0xFFFFFFFFu, most, __ffs(__ballot_sync(0xFFFFFFFFu, rank == kk - 1)) - 1), 1u);
+        n_top = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const uint32_t bal = __ballot_sync(0xFFFFFFFFu, key[j] >= bound);
+            const int at = n_top + __popc(bal & ((1u << lane) - 1u));
+            if (key[j] >= bound && at < kMaxCand) {
+                sel.key[at] = key[j];
+                sel.cand[at] = static_cast<int16_t>(lane + 32 * j);
+            }
+            n_top += __popc(bal);
+        }
+        __syncwarp();
+    }
+    if (n_top <= kMaxCand) {
+        for (int i = lane; i < n_top; i += 32) {
+            const uint32_t mine = sel.key[i];
+            const int e = sel.cand[i];
+            int rank = 0;
+            for (int o = 0; o < n_top; ++o) rank += sel.key[o] > mine || (sel.key[o] == mine && sel.cand[o] < e);
+            if (rank < kk) {
+                sel.value[rank] = key_value(mine);
+                sel.expert[rank] = static_cast<int16_t>(e);
+            }
+        }
+    } else {
+        // many equal logits (or 32 experts to choose): every lane holds its best,
+        // the warp's best of them is taken round by round
+        uint32_t best;
+        int best_j;
+        auto rescan = [&]() {
+            uint32_t m[PER];
+            int at[PER];
+#pragma unroll
+            for (int j = 0; j < PER; ++j) m[j] = key[j];
+#pragma unroll
+            for (int w = PER / 2; w > 0; w /= 2)
+#pragma unroll
+                for (int j = 0; j < w; ++j) m[j] = max(m[j], m[j + w]);
+            best = m[0];
+#pragma unroll
+            for (int j = 0; j < PER; ++j) at[j] = key[j] == best ? j : PER;
+#pragma unroll
+            for (int w = PER / 2; w > 0; w /= 2)
+#pragma unroll
+                for (int j = 0; j < w; ++j) at[j] = min(at[j], at[j + w]);
+            best_j = at[0];
+        };
+        rescan();
+        for (int r = 0; r < kk; ++r) {
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, best == top);
+            int e = best_j * 32 + lane;
+            if (who & (who - 1))  // several lanes: the lowest expert of them
+                e = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, best == top ? static_cast<uint32_t>(e) : 0xFFFFFFFFu));
+            if (best == top && e == best_j * 32 + lane) {
+                sel.value[r] = key_value(top);
+                sel.expert[r] = static_cast<int16_t>(e);
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    if (j == best_j) key[j] = 0;
+                rescan();
+            }
         }
     }
     __syncwarp();
@@ -190,7 +232,7 @@ __device__ void select_token(const RouteParams& p, Select& sel, int m, int lane)
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
 
     // near ties: order them by their exact values
-    const float tol = top_abs < 0x7F800000u ? __uint_as_float(top_abs) * 0x1p-18f : 0.0f;
+    const float tol = top_abs < 0x7F800000u ? __uint_as_float(top_abs) * 0x1p-20f : 0.0f;
     bool close = false;
     for (int r = lane; r + 1 < kk; r += 32) close |= sel.value[r] - sel.value[r + 1] < tol;
     if (__any_sync(0xFFFFFFFFu, close)) {

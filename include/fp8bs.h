@@ -421,7 +421,7 @@ size_t fp8bs_moe_route_workspace_bytes(int64_t M, int64_t E, int64_t H);
  *               (fp8bs_workspace_init) and is zero again after each.  Not to be
  *               used by two calls that can run at the same time.
  * Logits are summed in fp32 in a fixed order; experts whose logits are within
- * 2^-18 of the largest magnitude of each other where their order matters are
+ * 2^-20 of the largest magnitude of each other where their order matters are
  * summed again with compensation, so the order is that of 64-bit sums (not
  * where more than 64 candidates are that close: then the fp32 order stands).
  * A NaN logit ranks below every other and makes the token's chosen weights NaN.
