@@ -10,7 +10,9 @@
 // arrive (a counter that it also resets; no block waits for another), which
 // saves a launch; with more tokens one block's warps would take them in turn,
 // so a second kernel, a block per token, selects (programmatic dependent
-// launch).
+// launch).  Measured (in a graph, w in the second-level cache): 7.0 us for one
+// token of 512 experts, hidden 4096, 7.4 for 9 in two launches, 10.5 for 64; all
+// of it is latency: two trips to memory, the arrival, the selection.
 //
 // The order of the chosen experts is decided by fp32 logits unless two of them
 // (or the last chosen and the first left out) are within 2^-20 of the largest

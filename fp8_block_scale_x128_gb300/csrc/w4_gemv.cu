@@ -4,10 +4,17 @@
 // slices), or K and the tiles where K has fewer than 16 chunks.  A warp keeps
 // its slice of x as fp16 (all of it where it fits, and then a tile's stages
 // follow each other; else one stage at a time for kGroup tiles, staged again
-// for the next ones) and streams its part of the codes
-// through a ring of kDepth stages of its own, so no step but the sums over the
-// slices is block-wide.  Those go in slice order: repeated calls give the same
-// bits.
+// for the next ones) and streams its part of the codes through a ring of its
+// own, so no step but the sums over the slices is block-wide.  Those go in
+// slice order: repeated calls give the same bits.
+//
+// Bound by instruction issue (w4.cuh), at the smallest sizes by the launch.
+// Measured in a graph on weights that are not in the second-level cache: 3.8 us
+// for 1x4096x2048 (MXFP4; 0.66 at the measured copy bandwidth), 6.3 for
+// 1x5120x4096 (1.65), 18.5 for 1x16384x8192 (10.5, 58% of the bandwidth; the
+// other way round, groups of tiles in pieces, took 21.0), 39 for 16 tokens of
+// it, where x does not fit beside the codes and is staged twice.  16 warps in
+// one block, not 8 in two: the slices are half as long, and x is held once.
 #include "internal.cuh"
 #include "w4.cuh"
 

@@ -17,7 +17,14 @@
 //
 // An expert's codes are read once for a batch of its pairs.  Every block builds
 // the expert lists itself: a histogram of the routed pairs and its running
-// sums.  The second launch's lists and first codes do not wait for the first.
+// sums (up to 32 pairs by one warp with a match across its lanes: 12.1 us
+// instead of 14.4 for one token of 513x256).  The second launch's lists and
+// first codes do not wait for the first.
+//
+// Bound by instruction issue (w4.cuh).  Measured on MXFP4 experts of 513x256,
+// hidden 4096, 32 tokens with 10 routed and a shared one: gate/up 66 us for 271
+// MB read (4.1 TB/s, 0.61 of the measured copy bandwidth), down 43 us for 135 MB
+// (0.46), together 100 us; 12.1 us for one token.
 #include "internal.cuh"
 #include "w4.cuh"
 
