@@ -4,9 +4,9 @@
 // Arithmetic.  A weight is code * scale with an e2m1 value or an integer
 // -8..7 as code: both are exact in fp16.  A bf16 activation has 8 significant
 // bits, so after an exact power-of-two scaling that brings the largest
-// magnitude of a token's slice into [2^14, 2^15) every element down to 2^-32
-// of it is exact in fp16 as well (smaller ones are rounded at 2^-40 of the
-// largest).  Codes times activations go through the warp-level matrix
+// magnitude of a token's slice into [2^14, 2^15) every element down to 2^-31
+// of it is exact in fp16 as well (smaller ones are off by at most 2^-39 of the
+// largest: half of fp16's smallest step over 2^14).  Codes times activations go through the warp-level matrix
 // instruction (fp16 in, fp32 sums): products are exact, one scale group is
 // summed at a time, and the group's sum times its scale is added in fp32.
 // The matrix instruction is used for its decode rate: at a few tokens the
@@ -27,8 +27,8 @@
 //
 // What bounds it.  Measured on GB300, per multiprocessor quarter: this MMA takes
 // 8 cycles, the e2m1 conversion of a pair, an integer operation and an fp16 pair
-// operation 2, an fp32 FMA 1, and the MMA's cycles add to those of the integer
-// pipe.  Codes at the measured copy bandwidth arrive as 1088 bytes (16 rows x
+// operation 2, an fp32 FMA 1; together the MMAs and the integer pipe take about
+// the sum of their cycles.  Codes at the measured copy bandwidth arrive as 1088 bytes (16 rows x
 // 128 k with e8m0 scales) per 186 cycles; decoding, multiplying and scaling
 // them (stage_mma alone, 4 warps a quarter) takes 116 to 135 cycles with one
 // tile of token columns, 220 with two, 150 for integer codes.  What a stage

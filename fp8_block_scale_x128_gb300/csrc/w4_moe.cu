@@ -2,8 +2,9 @@
 //
 //   h = x[m] . w13[e]^T              (gate rows 0..I-1 over up rows I..2I-1)
 //   a = silu(h_gate) * h_up          (kept in the workspace as fp16 with an
-//                                     exponent per 16 values: rounded to 2^-12
-//                                     of each, 16 times finer than the bf16 of y)
+//                                     exponent per 16 values: off by at most
+//                                     2^-11 of each, an eighth of y's bf16 rounding,
+//                                     or 2^-39 of the 16's largest)
 //   y[m] = bf16(sum over s, in slot order, of tw[m, s] * (a . w2[e]^T))
 //
 // 1. gate/up: items of (expert, up to 8 of its pairs, 16 gate rows and the 16
@@ -22,9 +23,10 @@
 // first codes do not wait for the first.
 //
 // Bound by instruction issue (w4.cuh).  Measured on MXFP4 experts of 513x256,
-// hidden 4096, 32 tokens with 10 routed and a shared one: gate/up 66 us for 271
-// MB read (4.1 TB/s, 0.61 of the measured copy bandwidth), down 43 us for 135 MB
-// (0.46), together 100 us; 12.1 us for one token.
+// hidden 4096, 32 tokens with 10 routed and a shared one: gate/up 66.8 us for
+// 271 MB read (0.60 of the measured copy bandwidth), down 44.9 us for 135 MB
+// (0.44), each launched alone; 100.6 us for both in a stream; 12.2 us for one
+// token.
 #include "internal.cuh"
 #include "w4.cuh"
 

@@ -9,7 +9,7 @@
 // Memory-bound: each lane takes 8 consecutive weights (two 16-byte loads) and
 // writes one word of codes, G / 8 lanes share a group's maximum by shuffles.
 // Measured at 16384x8192: 138 us to MXFP4 (4.4 TB/s, 0.65 of the measured copy
-// bandwidth), 165 us to INT4; the IEEE divisions take the rest.
+// bandwidth), 165 us to INT4; what keeps it from the rest was not looked for.
 #include "internal.cuh"
 #include "w4.cuh"
 

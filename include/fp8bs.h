@@ -381,8 +381,8 @@ int fp8bs_quant_weight_w4(const float* w, int64_t N, int64_t K, int64_t ldw, int
  *            kernel before is still running; x and y not).
  * Products of codes and activations are exact, sums fp32 in a fixed order: the
  * same inputs give the same bits.  Activations are carried in fp16 after an
- * exact power-of-two scaling per token and K slice: elements below 2^-32 of
- * their slice's largest magnitude are rounded at 2^-40 of it.  Infinities and
+ * exact power-of-two scaling per token and K slice: elements below 2^-31 of
+ * their slice's largest magnitude are off by at most 2^-39 of it.  Infinities and
  * NaN in a token reach that token's outputs only.
  * No workspace, no device-side errors.
  * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN, FP8BS_ERR_CUDA. */
@@ -434,7 +434,8 @@ int fp8bs_moe_route(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const 
 #define FP8BS_MOE_W4_MAX_I 8192  /* intermediate size per expert */
 #define FP8BS_MOE_W4_MAX_H 32768 /* hidden size                  */
 
-/* Workspace bytes of fp8bs_moe_w4a16: a 256-byte error word, then M*S x I fp32.
+/* Workspace bytes of fp8bs_moe_w4a16: a 256-byte error word, then 4 bytes for each
+ * of the M*S x I kept values.
  * Returns 0 for an unsupported shape. */
 size_t fp8bs_moe_w4a16_workspace_bytes(int64_t M, int64_t S, int64_t I);
 
@@ -442,7 +443,7 @@ size_t fp8bs_moe_w4a16_workspace_bytes(int64_t M, int64_t S, int64_t I);
  * and slot s, with e = topk_ids[m, s]:
  *   h    = x[m] . w13[e]^T   (gate rows 0..I-1 over the up rows I..2I-1)
  *   a    = silu(h_gate) * h_up (rounded to fp16 with an exponent per 16
- *                            values: 2^-12 of each)
+ *                            values: 2^-11 of each)
  *   y[m] = bf16(sum over s, in slot order, of topk_w[m, s] * (a . w2[e]^T))
  *   x        : bf16 [M, H], row stride ldx elements; x and ldx*2 16-byte aligned.
  *   M, S     : M >= 0 (0 is a no-op), S >= 1, M * S <= FP8BS_MOE_MAX_PAIRS.

@@ -8,8 +8,8 @@ counted as two (their internal alignment may truncate), one addition per scale
 group, one per slice of K, and a few constants.  Each is at most 2^-23 of the
 sum of absolute products (2^-24 for a rounding, twice that for a truncation).
 An activation is carried with 11 significant bits in fp16: bf16 values are
-exact down to 2^-32 of their slice's largest magnitude and off by at most
-2^-40 of it below.
+exact down to 2^-31 of their slice's largest magnitude and off by at most
+2^-39 of it below (half of the smallest step, 2^-25, of at least 2^14).
 """
 
 from __future__ import annotations
@@ -81,7 +81,7 @@ def gemv(x: np.ndarray, w: np.ndarray):
     xf = synth.bf16_bits_to_f32(x).astype(np.float64)
     y = xf @ w.T
     total = np.abs(xf) @ np.abs(w).T
-    flush = 2.0 ** -40 * np.abs(xf).max(1, keepdims=True) * np.abs(w).sum(1)
+    flush = 2.0 ** -39 * np.abs(xf).max(1, keepdims=True) * np.abs(w).sum(1)
     err = roundings(x.shape[1]) * 2.0 ** -23 * total + flush
     return y, HALF_BF16 * np.abs(y) + (1 + HALF_BF16) * err
 
@@ -100,13 +100,13 @@ def moe(x, ids, tw, w13, w2):
             if not 0 <= e < E:
                 continue
             h = w13[e] @ xf[m]
-            dh = roundings(H) * 2.0 ** -23 * (np.abs(w13[e]) @ np.abs(xf[m])) + 2.0 ** -40 * np.abs(xf[m]).max() * np.abs(w13[e]).sum(1)
+            dh = roundings(H) * 2.0 ** -23 * (np.abs(w13[e]) @ np.abs(xf[m])) + 2.0 ** -39 * np.abs(xf[m]).max() * np.abs(w13[e]).sum(1)
             g, u = h[:I], h[I:]
             silu = g / (1 + np.exp(-g))
             a = silu * u
             # |silu'| <= 1.1; exp within 2 units, division and products a few roundings
             da = 1.1 * dh[:I] * (np.abs(u) + dh[I:]) + np.abs(silu) * dh[I:] + 2.0 ** -20 * np.abs(a)
-            da = da + 2.0 ** -12 * (np.abs(a) + da) + 2.0 ** -40 * np.abs(a).max()
+            da = da + 2.0 ** -11 * (np.abs(a) + da) + 2.0 ** -39 * np.abs(a).max()
             o = w2[e] @ a
             do = np.abs(w2[e]) @ da + roundings(I) * 2.0 ** -23 * (np.abs(w2[e]) @ (np.abs(a) + da))
             y[m] += t * o
