@@ -226,6 +226,21 @@ __device__ __forceinline__ uint4 pack_slice8(const float (&v)[8], float s) {
                           pack_half2(v[2] * s, v[6] * s), pack_half2(v[3] * s, v[7] * s));
 }
 
+// What that rounding leaves of them, as fp16 in the same order.
+__device__ __forceinline__ uint32_t pack_rest2(float lo, float hi, uint32_t rounded) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&rounded));
+    return pack_half2(lo - f.x, hi - f.y);
+}
+template <int FMT>
+__device__ __forceinline__ uint4 pack_rest8(const float (&v)[8], float s, const uint4& r) {
+    if constexpr (FMT == FP8BS_W4_MXFP4)
+        return make_uint4(pack_rest2(v[0] * s, v[1] * s, r.x), pack_rest2(v[2] * s, v[3] * s, r.y),
+                          pack_rest2(v[4] * s, v[5] * s, r.z), pack_rest2(v[6] * s, v[7] * s, r.w));
+    else
+        return make_uint4(pack_rest2(v[0] * s, v[4] * s, r.x), pack_rest2(v[1] * s, v[5] * s, r.y),
+                          pack_rest2(v[2] * s, v[6] * s, r.z), pack_rest2(v[3] * s, v[7] * s, r.w));
+}
+
 __device__ __forceinline__ void unpack8(const uint4& raw, float (&v)[8]) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
@@ -261,67 +276,58 @@ struct RawBf16 {
     __device__ __forceinline__ void values(int i, float (&v)[8]) const { unpack8(r[i], v); }
 };
 
-// The same of up to four tokens kept as fp16 with a biased exponent (as
-// slice_scale takes it) per 16 values, in the decode's pair order.  A stage's
-// values are brought to its largest exponent.
-struct RawFp16 {
-    static constexpr int kTokens = 4;
-    uint4 r[kTokens];
-    int e[kTokens];
-    // a, ae: this lane's values and exponent of pair 0's stage, la and le bytes
-    // a pair; pair(i): the i-th pair
+// Where value k of a kept fp32 token sits: a chunk's 8l + 4h + i at 64h + 4l + i,
+// so that each of a lane's two 16-byte loads is next to its neighbours'.
+__device__ __forceinline__ int kept_place(int k) { return (k & ~127) | (k & 4) << 4 | (k & 0x78) >> 1 | (k & 3); }
+__device__ __forceinline__ uint32_t kept_src(int lane) { return (lane >> 4) * (kChunk * 4) + (lane & 15) * 16; }
+
+// A stage of up to two fp32 tokens.  A token takes two columns of the matrix
+// product, 2i and 2i + 1: fp16(v s) and fp16 of what that leaves, with one
+// power of two s as for bf16 tokens.  Their sum is off by at most 2^-22 of the
+// value, or 2^-39 of the slice's largest (half of fp16's smallest step over
+// 2^14) where that is more.
+struct RawFp32 {
+    static constexpr int kTokens = 2;
+    uint4 r[kTokens][2];
+    // a: this lane's values (kept_src) of pair 0's stage, la bytes a pair; pair(i): the i-th pair
     template <typename Pair>
-    __device__ __forceinline__ void load(const uint8_t* a, const uint8_t* ae, uint32_t la, uint32_t le, int n, int nch,
-                                         int lane, Pair pair) {
+    __device__ __forceinline__ void load(const uint8_t* a, uint32_t la, int n, int nch, int lane, Pair pair) {
         const bool in = lane < nch * (kChunk / 8);
 #pragma unroll
         for (int i = 0; i < kTokens; ++i) {
             if (i >= n) break;
-            r[i] = make_uint4(0, 0, 0, 0);
-            e[i] = 0;
+            r[i][0] = r[i][1] = make_uint4(0, 0, 0, 0);
             if (in) {
-                const uint32_t q = pair(i);
-                r[i] = __ldcg(reinterpret_cast<const uint4*>(at(a, q, la)));
-                e[i] = __ldcg(at(ae, q, le));
+                const uint4* p = reinterpret_cast<const uint4*>(at(a, pair(i), la));
+                r[i][0] = __ldcg(p);
+                r[i][1] = __ldcg(p + kChunk / 8);
             }
         }
     }
+    template <int FMT>
     __device__ __forceinline__ void store(uint32_t dst, uint32_t inv, int i0, int n, int lane) const {
 #pragma unroll
         for (int i = 0; i < kTokens; ++i) {
             if (i0 + i >= n) break;
-            const int top = __reduce_max_sync(0xFFFFFFFFu, e[i]);
-            // 2^(e - top), in two factors where one would leave fp16's exact powers of two
-            const int down = e[i] > 0 ? top - e[i] : 0, first = min(down, 14);  // (no values: 0)
-            uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-            const __half2 f = __half2half2(__ushort_as_half(static_cast<unsigned short>((15 - first) << 10)));
+            const uint32_t w[8] = {r[i][0].x, r[i][0].y, r[i][0].z, r[i][0].w, r[i][1].x, r[i][1].y, r[i][1].z, r[i][1].w};
+            float v[8], top = 0.0f;  // (a NaN does not reach top, but stays what it is)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __half2 h = __hmul2(*reinterpret_cast<__half2*>(&w[j]), f);
-                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int j = 0; j < 8; ++j) {
+                v[j] = __uint_as_float(w[j]);
+                top = fmaxf(top, fabsf(v[j]));
             }
-            if (__any_sync(0xFFFFFFFFu, down > 14)) {
-                const int rest = min(down - first, 14), last = min(down - first - rest, 14);
-                const __half2 f1 = __half2half2(__ushort_as_half(static_cast<unsigned short>((15 - rest) << 10)));
-                const __half2 f2 = __half2half2(__ushort_as_half(static_cast<unsigned short>((15 - last) << 10)));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const __half2 h = __hmul2(__hmul2(*reinterpret_cast<__half2*>(&w[j]), f1), f2);
-                    w[j] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-            }
-            sts128(dst + token_word(i0 + i, lane), make_uint4(w[0], w[1], w[2], w[3]));
-            if (lane == 0) sts_float(inv + 4 * (i0 + i), __uint_as_float(static_cast<uint32_t>(max(top, 15) - 14) << 23));
+            const uint32_t ef = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)) >> 23;
+            float inverse;
+            const uint4 hi = pack_slice8<FMT>(v, slice_scale(ef, inverse));
+            // infinities and NaN are whole in the first column
+            uint4 lo = make_uint4(0, 0, 0, 0);
+            if (ef < 255) lo = pack_rest8<FMT>(v, slice_scale(ef, inverse), hi);
+            sts128(dst + token_word(2 * (i0 + i), lane), hi);
+            sts128(dst + token_word(2 * (i0 + i) + 1, lane), lo);
+            if (lane == 0) sts_float2(inv + 8 * (i0 + i), inverse, inverse);
         }
     }
 };
-
-// Where value k of a 16-value run sits in the decode's pair order.
-template <int FMT>
-__device__ __forceinline__ int paired(int k) {
-    if constexpr (FMT == FP8BS_W4_MXFP4) return k;
-    return (k & 8) | (k & 3) << 1 | (k >> 2 & 1);
-}
 
 // The stage of n tokens as fp16 at dst, with the inverse scales in inv.  raw
 // holds the first tokens, loaded beforehand; the others are loaded here.  The

@@ -1,10 +1,7 @@
 // Small-batch mixture-of-experts layer on 4-bit weights, two launches.
 //
 //   h = x[m] . w13[e]^T              (gate rows 0..I-1 over up rows I..2I-1)
-//   a = silu(h_gate) * h_up          (kept in the workspace as fp16 with an
-//                                     exponent per 16 values: off by at most
-//                                     2^-11 of each, an eighth of y's bf16 rounding,
-//                                     or 2^-39 of the 16's largest)
+//   a = silu(h_gate) * h_up          (kept in the workspace as fp32)
 //   y[m] = bf16(sum over s, in slot order, of tw[m, s] * (a . w2[e]^T))
 //
 // 1. gate/up: items of (expert, up to 8 of its pairs, 16 gate rows and the 16
@@ -15,6 +12,9 @@
 // 2. down: a block owns 16 or 32 rows of the output for every token, its warps
 //    deal out the experts; the pairs' products meet in shared memory and are summed
 //    in slot order.  No partial sums in global memory, no atomics on values.
+//    a takes two of an MMA's columns, as the sum of two fp16 numbers.  (As one
+//    of 11 bits it left y off from its form in fp32 by 8.6e-4 of the 2-norm, now
+//    2e-5; 32 tokens of 513x256 took 100.6 us, now 103.7.)
 //
 // An expert's codes are read once for a batch of its pairs.  Every block builds
 // the expert lists itself: a histogram of the routed pairs and its running
@@ -37,7 +37,10 @@ using namespace w4;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxBatch = 8;  // pairs of an entry at most: the token columns of one MMA
+// pairs of an entry at most: the token columns of one MMA, two a pair in the
+// down projection
+constexpr int kMaxBatch = 8;
+constexpr int kMaxDownBatch = kMaxBatch / 2;
 constexpr size_t kHeader = 256;  // workspace: the device error word, then a
 
 struct MoeParams {
@@ -51,8 +54,7 @@ struct MoeParams {
     const uint8_t* s2;
     uint16_t* y;    // [M, H]
     uint32_t* err;  // workspace error word
-    uint16_t* a;    // [M*S][I] fp16, 16 values at a time in the decode's pair order
-    uint8_t* ae;    // [M*S][I/16] their biased exponents
+    float* a;       // [M*S][I], in kept_place's order
     int M, S, H, I, E;
 };
 
@@ -333,17 +335,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
                 v += *reinterpret_cast<const float*>(s + w * mine_bytes + kSumBytes<1>);
             }
             const float a = g / (1.0f + expf(-g)) * v;
-            // the largest exponent of the pair's 16 values
-            uint32_t ef = (__float_as_uint(a) & 0x7FFFFFFFu) >> 23;
-#pragma unroll
-            for (int off = 8; off > 0; off /= 2) ef = max(ef, __shfl_xor_sync(0xFFFFFFFFu, ef, off));
-            float inverse;
-            const float scale = slice_scale(ef, inverse);
-            if (static_cast<int>(threadIdx.x) < n * kTileRows) {
-                const int64_t to = static_cast<int64_t>(L.pair[pf + i] & 0xFFFF) * p.I + j * kTileRows;
-                p.a[to + paired<FMT>(row)] = __half_as_ushort(__float2half_rn(a * scale));
-                if (row == 0) p.ae[to / kTileRows] = static_cast<uint8_t>(min(max(ef, 15u), 254u));
-            }
+            if (static_cast<int>(threadIdx.x) < n * kTileRows)
+                p.a[(L.pair[pf + i] & 0xFFFF) * p.I + kept_place(j * kTileRows + row)] = a;
         }
         __syncthreads();  // the sums' place is rewritten by the next item
         if (++j == per) j = 0, ++entry;
@@ -352,13 +345,13 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
 
 // ---- 2. down -----------------------------------------------------------------
 // Bytes of a warp: a ring of stages of T tiles, their scale tables, the inverse
-// scales and a stage of a for n pairs.
+// scales and a stage of a for n pairs, two columns each.
 constexpr int kWideDownPairs = 256;
 constexpr int kInvBytes = 128;  // 8 factors, the next part aligned
 __host__ __device__ constexpr int down_depth(int T) { return T == 2 ? 2 : 3; }
 template <int GP>
 __host__ __device__ constexpr int down_bytes(int n, int T) {
-    return down_depth(T) * T * kCodeBytes + T * kTableBytes<GP> + kInvBytes + n * kTokenBytes;
+    return down_depth(T) * T * kCodeBytes + T * kTableBytes<GP> + kInvBytes + 2 * n * kTokenBytes;
 }
 // the pairs' products for the rows by place, and the pairs' routing weights
 __host__ __device__ constexpr int out_bytes(int P, int T) { return (P * (T * kTileRows + 1) * 4 + 127) / 128 * 128; }
@@ -387,15 +380,14 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) moe_w4_down_kernel(con
     const int chunks = p.I / kChunk, pieces = ONE ? 1 : (chunks + kPC - 1) / kPC;
     const uint32_t ldc = p.I / 2, lds = chunks * SB;
     const uint32_t expert_codes = p.H * ldc, expert_scales = p.H * lds;
-    const uint8_t* lane_a = reinterpret_cast<const uint8_t*>(p.a) + 16 * lane;
-    const uint8_t* lane_ae = p.ae + (lane >> 1);
-    const uint32_t la = p.I * 2, le = p.I / kTileRows;
+    const uint8_t* lane_a = reinterpret_cast<const uint8_t*>(p.a) + kept_src(lane);
+    const uint32_t la = p.I * 4;
     const int tiles = p.H / kRows;
-    RawFp16 tokens;
+    RawFp32 tokens;
     auto load_tokens = [&](const ushort4& entry, int piece, int i0) {
         const uint32_t* pair = L.pair + entry.y + i0;
-        tokens.load(lane_a + piece * kTokenBytes, lane_ae + piece * (kStageK / kTileRows), la, le, entry.z - i0,
-                    min(chunks - piece * kPC, kPC), lane, [=](int i) { return pair[i] & 0xFFFFu; });
+        tokens.load(lane_a + piece * (kStageK * 4), la, entry.z - i0, min(chunks - piece * kPC, kPC), lane,
+                    [=](int i) { return pair[i] & 0xFFFFu; });
     };
 
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -431,7 +423,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) moe_w4_down_kernel(con
         for (int entry = warp; entry < L.entries; entry += WARPS) {
             const int n = now.z, pf = now.y;
             const ushort4 next = L.entry[min(entry + WARPS, L.entries - 1)];
-            const uint32_t x[1] = {xs + token_src(lane >> 2, n, lane)};
+            const uint32_t x[1] = {xs + token_src(lane >> 2, 2 * n, lane)};
             float tot[T][1][4] = {};
             for (int piece = 0; piece < pieces; ++piece) {
                 const int nch = min(chunks - piece * kPC, kPC);
@@ -443,10 +435,10 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) moe_w4_down_kernel(con
                     for (int k = 0; k + 2 < D; ++k) raw[k][i] = raw[k + 1][i];
                 }
                 issue(slot_at == 0 ? (D - 1) * kSlot : slot_at - kSlot, raw[D - 2]);
-                tokens.store(xs, mine + kInvAt, 0, n, lane);
-                for (int i0 = RawFp16::kTokens; i0 < n; i0 += RawFp16::kTokens) {
+                tokens.store<FMT>(xs, mine + kInvAt, 0, n, lane);
+                for (int i0 = RawFp32::kTokens; i0 < n; i0 += RawFp32::kTokens) {
                     load_tokens(now, piece, i0);
-                    tokens.store(xs, mine + kInvAt, i0, n, lane);
+                    tokens.store<FMT>(xs, mine + kInvAt, i0, n, lane);
                 }
                 if (!ONE && piece + 1 < pieces)
                     load_tokens(now, piece + 1, 0);
@@ -459,12 +451,13 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) moe_w4_down_kernel(con
                 __syncwarp();  // the slot, the table and the tokens are rewritten by later stages
                 slot_at = slot_at == (D - 1) * kSlot ? 0 : slot_at + kSlot;
             }
-            const int col = 2 * (lane & 3);
-            float* o = out + (pf + col) * kRows + (lane >> 2);
+            if ((lane & 3) < n) {  // a lane's two columns are one pair's
+                float* o = out + (pf + (lane & 3)) * kRows + (lane >> 2);
 #pragma unroll
-            for (int i = 0; i < T; ++i, o += kTileRows) {
-                if (col < n) o[0] = tot[i][0][0], o[8] = tot[i][0][2];
-                if (col + 1 < n) o[kRows] = tot[i][0][1], o[kRows + 8] = tot[i][0][3];
+                for (int i = 0; i < T; ++i, o += kTileRows) {
+                    o[0] = tot[i][0][0] + tot[i][0][1];
+                    o[8] = tot[i][0][2] + tot[i][0][3];
+                }
             }
             now = next;
         }
@@ -483,18 +476,18 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) moe_w4_down_kernel(con
     }
 }
 
-// The pairs of an entry and the blocks of a multiprocessor (at most `most`): two blocks, with as
-// many pairs as then fit, unless the experts have more than twice as many on
+// The pairs of an entry (at most `largest`) and the blocks of a multiprocessor (at most `most`): two
+// blocks, with as many pairs as then fit, unless the experts have more than twice as many on
 // average (their codes would be fetched and decoded over and over): then one.
 template <typename F>
-int batch_of(const MoeParams& p, F&& bytes, int most, int& per_sm) {
+int batch_of(const MoeParams& p, F&& bytes, int largest, int most, int& per_sm) {
     constexpr int kHalf = kMaxSmShared / 2 - 1024 - 128;  // less a block's reserved and static shared memory
-    int batch = kMaxBatch;
+    int batch = largest;
     while (batch > 0 && bytes(batch) > kHalf) --batch;
     per_sm = 2;
-    if (most > 1 && batch > 0 && (batch == kMaxBatch || p.M * p.S <= 2 * batch * p.E)) return batch;
+    if (most > 1 && batch > 0 && (batch == largest || p.M * p.S <= 2 * batch * p.E)) return batch;
     per_sm = 1;
-    for (batch = kMaxBatch; batch > 1 && bytes(batch) > kMaxBlockShared; --batch) {}
+    for (batch = largest; batch > 1 && bytes(batch) > kMaxBlockShared; --batch) {}
     return batch;
 }
 
@@ -508,7 +501,7 @@ cudaError_t launch_up(const MoeParams& p, int sm_count, cudaStream_t stream) {
         return lists_bytes(P) + max(counts_bytes(p.E), kWarps * up_bytes<GP>(min(P, batch), pieces));
     };
     int per_sm;
-    const int batch = batch_of(p, bytes, 2, per_sm), smem = bytes(batch);
+    const int batch = batch_of(p, bytes, kMaxBatch, 2, per_sm), smem = bytes(batch);
     if (smem > kMaxBlockShared) return cudaErrorInvalidValue;
     const int64_t most = static_cast<int64_t>(P) * (p.I / kTileRows);
     const int grid = static_cast<int>(min(most, static_cast<int64_t>(sm_count) * per_sm));
@@ -527,7 +520,8 @@ cudaError_t launch_down_as(const MoeParams& p, int sm_count, cudaStream_t stream
     cudaError_t e = allow_shared(moe_w4_down_kernel<FMT, GP, ONE, T, WARPS>, allowed);
     if (e != cudaSuccess) return e;
     int per_sm;
-    const int batch = batch_of(p, [&](int n) { return down_block_bytes<GP, T, WARPS>(p, n); }, 16 / WARPS, per_sm);
+    const int batch = batch_of(p, [&](int n) { return down_block_bytes<GP, T, WARPS>(p, n); }, kMaxDownBatch,
+                               16 / WARPS, per_sm);
     return launch_dependent(moe_w4_down_kernel<FMT, GP, ONE, T, WARPS>, min(p.H / (T * kTileRows), sm_count * per_sm), WARPS * 32,
                             down_block_bytes<GP, T, WARPS>(p, batch), stream, p, batch);
 }
@@ -566,8 +560,7 @@ cudaError_t launch_moe_w4(const MoeW4Args& a, cudaStream_t stream) {
     p.s2 = a.s2;
     p.y = a.y;
     p.err = reinterpret_cast<uint32_t*>(a.workspace);
-    p.a = reinterpret_cast<uint16_t*>(a.workspace + kHeader);
-    p.ae = a.workspace + kHeader + static_cast<size_t>(a.M) * a.S * a.I * sizeof(uint16_t);
+    p.a = reinterpret_cast<float*>(a.workspace + kHeader);
     p.M = a.M;
     p.S = a.S;
     p.H = a.H;

@@ -442,8 +442,9 @@ size_t fp8bs_moe_w4a16_workspace_bytes(int64_t M, int64_t S, int64_t I);
 /* One MoE layer at decode sizes on 4-bit weights, in two launches.  Per token m
  * and slot s, with e = topk_ids[m, s]:
  *   h    = x[m] . w13[e]^T   (gate rows 0..I-1 over the up rows I..2I-1)
- *   a    = silu(h_gate) * h_up (rounded to fp16 with an exponent per 16
- *                            values: 2^-11 of each)
+ *   a    = silu(h_gate) * h_up (fp32; in the product below the sum of two fp16
+ *                            numbers: off by at most 2^-22 of each, or 2^-39 of
+ *                            the largest of its 256 neighbours along I)
  *   y[m] = bf16(sum over s, in slot order, of topk_w[m, s] * (a . w2[e]^T))
  *   x        : bf16 [M, H], row stride ldx elements; x and ldx*2 16-byte aligned.
  *   M, S     : M >= 0 (0 is a no-op), S >= 1, M * S <= FP8BS_MOE_MAX_PAIRS.
