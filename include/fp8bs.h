@@ -420,10 +420,13 @@ size_t fp8bs_moe_route_workspace_bytes(int64_t M, int64_t E, int64_t H);
  *               first word must be zero before the first call
  *               (fp8bs_workspace_init) and is zero again after each.  Not to be
  *               used by two calls that can run at the same time.
- * Logits are summed in fp32 in a fixed order; experts whose logits are within
- * 2^-20 of the largest magnitude of each other where their order matters are
- * summed again with compensation, so the order is that of 64-bit sums (not
- * where more than 64 candidates are that close: then the fp32 order stands).
+ * Logits are summed in fp32 in a fixed order.  Experts whose logits are closer
+ * than twice the bound of their fp32 error where their order matters are
+ * summed again with compensation.  The bound goes with S, the token's largest
+ * sum of |x w| over the experts (taken beside the logits), so the order is that
+ * of the exact logits to about 2^-45 S.  Not where S overflows fp32 or has a NaN:
+ * then the fp32 order stands.  Many experts that close to one another cost a
+ * compensated sum each.
  * A NaN logit ranks below every other and makes the token's chosen weights NaN.
  * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN,
  * FP8BS_ERR_WORKSPACE, FP8BS_ERR_CUDA. */
