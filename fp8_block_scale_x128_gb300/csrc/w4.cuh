@@ -153,18 +153,17 @@ __device__ __forceinline__ uint2 load_scales(const uint8_t* src, int nch, int la
     return w;
 }
 
-// Their fp32 values into the stage's table [row][chunk * GP + group].  A stage
-// with a scale of 2^97 or more has its table divided by 2^64 (kBigScale), so
-// that a group's sum, up to 2^27 at the activations' fixed scaling, times its
-// scale stays finite; returns the factor to put back.
-constexpr float kBigScale = 0x1p64f;
+// Their fp32 values into the stage's table [row][chunk * GP + group].  Returns
+// whether one of the stage's scales is 2^97 or more: a group's sum, up to 2^27
+// at the activations' fixed scaling, times such a scale may leave fp32's range
+// where the result does not, and the stage is multiplied by stage_far.
 template <int FMT>
-__device__ __forceinline__ bool big_scale(uint2 raw) {  // some scale's three top exponent bits all set
+__device__ __forceinline__ bool far_scale(uint2 raw) {  // some scale's three top exponent bits all set
     const uint32_t high = (raw.x & raw.x << 1 & raw.x << 2) | (raw.y & raw.y << 1 & raw.y << 2);
     return (high & (FMT == FP8BS_W4_MXFP4 ? 0x80808080u : 0x40004000u)) != 0;
 }
 template <int FMT, int GP>
-__device__ __forceinline__ void store_scales_by(uint32_t dst, uint2 raw, bool big) {
+__device__ __forceinline__ void store_scales_of(uint32_t dst, uint2 raw) {
     uint32_t w[2] = {raw.x, raw.y};
     if constexpr (FMT == FP8BS_W4_MXFP4)  // four e8m0 bytes to four bf16
         asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;\n\tcvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
@@ -173,9 +172,6 @@ __device__ __forceinline__ void store_scales_by(uint32_t dst, uint2 raw, bool bi
     float v[GP];
 #pragma unroll
     for (int i = 0; i < GP; ++i) v[i] = __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
-    if (big)
-#pragma unroll
-        for (int i = 0; i < GP; ++i) v[i] *= 1.0f / kBigScale;
     if constexpr (GP == 4)
         sts128(dst, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
     else if constexpr (GP == 2)
@@ -189,13 +185,12 @@ __device__ __forceinline__ uint32_t scale_dst(int lane) {
     return ((lane >> 1) * kScalePitch<GP> + (lane & 1) * GP) * 4;
 }
 template <int FMT, int GP, int T>
-__device__ __forceinline__ float store_scales(uint32_t dst, const uint2 (&raw)[T]) {
-    bool big = big_scale<FMT>(raw[0]);
-    if constexpr (T == 2) big |= big_scale<FMT>(raw[1]);
-    big = __any_sync(0xFFFFFFFFu, big);
+__device__ __forceinline__ bool store_scales(uint32_t dst, const uint2 (&raw)[T]) {
+    bool far = far_scale<FMT>(raw[0]);
+    if constexpr (T == 2) far |= far_scale<FMT>(raw[1]);
 #pragma unroll
-    for (int i = 0; i < T; ++i) store_scales_by<FMT, GP>(dst + i * kTableBytes<GP>, raw[i], big);
-    return big ? kBigScale : 1.0f;
+    for (int i = 0; i < T; ++i) store_scales_of<FMT, GP>(dst + i * kTableBytes<GP>, raw[i]);
+    return __any_sync(0xFFFFFFFFu, far);
 }
 
 // 2^(14 - e) and its inverse for a slice whose largest magnitude has the
@@ -429,7 +424,7 @@ __device__ __forceinline__ uint32_t token_src(int column, int n, int lane) {
 }
 template <int FMT, int GP, int NT, int T>
 __device__ __forceinline__ void stage_mma(float (&tot)[T][NT][4], uint32_t codes, uint32_t table, const uint32_t (&x)[NT],
-                                          uint32_t inv, float back, int nch) {
+                                          uint32_t inv, int nch) {
     float acc[T][NT][4];
 #pragma unroll
     for (int i = 0; i < T; ++i)
@@ -490,24 +485,93 @@ __device__ __forceinline__ void stage_mma(float (&tot)[T][NT][4], uint32_t codes
             }
         }
     }
-    // the factors one after the other: their product may leave fp32's range
-    // where the result does not
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
         const float2 f = lds_float2(inv + 32 * j);
 #pragma unroll
-        for (int i = 0; i < T; ++i)
-            if (back == 1.0f) {
-                tot[i][j][0] = fmaf(acc[i][j][0], f.x, tot[i][j][0]);
-                tot[i][j][1] = fmaf(acc[i][j][1], f.y, tot[i][j][1]);
-                tot[i][j][2] = fmaf(acc[i][j][2], f.x, tot[i][j][2]);
-                tot[i][j][3] = fmaf(acc[i][j][3], f.y, tot[i][j][3]);
-            } else {
-                tot[i][j][0] = fmaf(acc[i][j][0] * f.x, back, tot[i][j][0]);
-                tot[i][j][1] = fmaf(acc[i][j][1] * f.y, back, tot[i][j][1]);
-                tot[i][j][2] = fmaf(acc[i][j][2] * f.x, back, tot[i][j][2]);
-                tot[i][j][3] = fmaf(acc[i][j][3] * f.y, back, tot[i][j][3]);
+        for (int i = 0; i < T; ++i) {
+            tot[i][j][0] = fmaf(acc[i][j][0], f.x, tot[i][j][0]);
+            tot[i][j][1] = fmaf(acc[i][j][1], f.y, tot[i][j][1]);
+            tot[i][j][2] = fmaf(acc[i][j][2], f.x, tot[i][j][2]);
+            tot[i][j][3] = fmaf(acc[i][j][3], f.y, tot[i][j][3]);
+        }
+    }
+}
+
+// The same for one tile of a stage that has scales of 2^97 and more, whose
+// groups are summed apart at 2^-64 of their size: no other group of the stage,
+// in its row or another, loses range to them.  Never seen in quantised weights,
+// so it is kept out of the kernels' own code.
+template <int NT>
+struct FarTile {
+    uint32_t x[NT];
+    float sum[NT][4];
+};
+constexpr float kFarScale = 0x1p64f;
+template <int FMT, int GP, int NT>
+__device__ __noinline__ void stage_far(FarTile<NT>* tile, uint32_t codes, uint32_t table, uint32_t inv, int nch) {
+    float near[NT][4] = {}, far[NT][4] = {}, part[NT][4] = {};
+#pragma unroll 1
+    for (int i2 = 0; i2 < 2 * nch; ++i2) {
+        uint32_t w[4];
+        ldmatrix4(w, codes + i2 * 32);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            constexpr int kPerScale = 4 / GP;
+            const int grp = 2 * i2 + h;
+            uint32_t lo[4], hi[4];
+            decode8<FMT>(w[2 * h], lo);
+            decode8<FMT>(w[2 * h + 1], hi);
+            const bool ends = grp % kPerScale == kPerScale - 1;
+            const uint32_t p = table + grp / kPerScale * 4;
+            const float scale[2] = {lds_float(p), lds_float(p + 8 * kScalePitch<GP> * 4)};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint4 b = lds128((h ? tile->x[j] ^ 64 : tile->x[j]) + i2 * 128);
+                mma16816(part[j], lo[0], hi[0], lo[1], hi[1], b.x, b.y);
+                mma16816(part[j], lo[2], hi[2], lo[3], hi[3], b.z, b.w);
+                if (!ends) continue;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float s = scale[q / 2];
+                    if ((__float_as_uint(s) & 0x7F800000u) >= 224u << 23)
+                        far[j][q] = fmaf(part[j][q], s * (1.0f / kFarScale), far[j][q]);
+                    else
+                        near[j][q] = fmaf(part[j][q], s, near[j][q]);
+                    part[j][q] = 0.0f;
+                }
             }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const float2 f = lds_float2(inv + 32 * j);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float e = q % 2 ? f.y : f.x;
+            tile->sum[j][q] = fmaf(far[j][q] * e, kFarScale, near[j][q] * e);
+        }
+    }
+}
+
+// A stage by one or the other.
+template <int FMT, int GP, int NT, int T>
+__device__ __forceinline__ void multiply_stage(float (&tot)[T][NT][4], uint32_t codes, uint32_t table, const uint32_t (&x)[NT],
+                                               uint32_t inv, bool far, int nch) {
+    if (!far) {
+        stage_mma<FMT, GP, NT, T>(tot, codes, table, x, inv, nch);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+        FarTile<NT> tile;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) tile.x[j] = x[j];
+        stage_far<FMT, GP, NT>(&tile, codes + i * kCodeBytes, table + i * kTableBytes<GP>, inv, nch);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tot[i][j][q] += tile.sum[j][q];
     }
 }
 

@@ -184,13 +184,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_w4_kernel(const __grid_const
         }
         issue(slot == 0 ? D - 1 : slot - 1, raw[D - 2]);
         if (nch > 0) {
-            const float back = store_scales<FMT, GP, T>(to_table, cur);
+            const bool far = store_scales<FMT, GP, T>(to_table, cur);
             uint32_t x[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j) x[j] = from_x[j] + kept_at * p.M * kTokenBytes;
             cp_async_wait<D - 1>();
             __syncwarp();
-            stage_mma<FMT, GP, NT, T>(tot, from_codes + slot * kSlot, from_table, x, from_inv + kept_at * 8 * NT * 4, back, nch);
+            multiply_stage<FMT, GP, NT, T>(tot, from_codes + slot * kSlot, from_table, x, from_inv + kept_at * 8 * NT * 4, far, nch);
         }
         __syncwarp();  // the slot, the table and x are rewritten by later stages
         slot = slot + 1 == D ? 0 : slot + 1;

@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
     const int per = p.I / kTileRows;
     const uint32_t ldc = p.H / 2, lds = chunks * SB;
     const uint32_t up_codes = p.I * ldc, up_scales = p.I * lds;  // from a gate tile to its up tile
-    const uint8_t* lane_codes = p.w13 + static_cast<int64_t>(lane >> 3) * ldc + first * 64 + (lane & 7) * 16;
-    const uint8_t* lane_scales = p.s13 + static_cast<int64_t>(lane >> 1) * lds + (first + (lane & 1)) * SB;
+    const uint32_t lane_codes = (lane >> 3) * ldc + first * 64 + (lane & 7) * 16;
+    const uint32_t lane_scales = (lane >> 1) * lds + (first + (lane & 1)) * SB;
 
     // the block's run of items (entry, tile j)
     const int64_t items = static_cast<int64_t>(L.entries) * per;
@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
     auto locate = [&]() {
         if (ahead.left <= 0) return;
         const uint32_t e = L.entry[ahead.entry].x;
-        ahead.gate = at(at(lane_codes, e, 2 * up_codes), ahead.j * kTileRows, ldc);
-        ahead.scales = at(at(lane_scales, e, 2 * up_scales), ahead.j * kTileRows, lds);
+        ahead.gate = at(at(p.w13, e, 2 * up_codes), ahead.j * kTileRows, ldc) + lane_codes;
+        ahead.scales = at(at(p.s13, e, 2 * up_scales), ahead.j * kTileRows, lds) + lane_scales;
     };
     const int next_codes = static_cast<int>(kTileRows * ldc) - (pieces - 1) * kPC * 64, next_scales = static_cast<int>(kTileRows * lds) - (pieces - 1) * kPC * SB;
     auto issue = [&](int slot, uint2 (&raw)[2]) {
@@ -312,11 +312,11 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
             for (int i = 0; i + 2 < D; ++i) raw[i][0] = raw[i + 1][0], raw[i][1] = raw[i + 1][1];
             issue(slot == 0 ? D - 1 : slot - 1, raw[D - 2]);
             if (nch > 0) {
-                const float back = store_scales<FMT, GP, 2>(to_table, cur);
+                const bool far = store_scales<FMT, GP, 2>(to_table, cur);
                 const uint32_t x[1] = {x0 + piece * kept * kTokenBytes};
                 cp_async_wait<D - 1>();
                 __syncwarp();
-                stage_mma<FMT, GP, 1, 2>(tot, from_codes + slot * kSlot, from_table, x, from_inv + piece * kMaxBatch * 4, back, nch);
+                multiply_stage<FMT, GP, 1, 2>(tot, from_codes + slot * kSlot, from_table, x, from_inv + piece * kMaxBatch * 4, far, nch);
             }
             __syncwarp();  // the slot and the table are rewritten by later stages
             slot = slot + 1 == D ? 0 : slot + 1;
@@ -327,12 +327,12 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
         __syncthreads();
         if (threadIdx.x < kMaxBatch * kTileRows) {  // 16 lanes a pair
             const int i = min(static_cast<int>(threadIdx.x) / kTileRows, n - 1), row = threadIdx.x % kTileRows;
-            const uint8_t* s = base + kTableAt + (i * kSumPitch + row) * 4;
+            const uint32_t s = mine - warp * mine_bytes + kTableAt + (i * kSumPitch + row) * 4;
             float g = 0.0f, v = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                g += *reinterpret_cast<const float*>(s + w * mine_bytes);
-                v += *reinterpret_cast<const float*>(s + w * mine_bytes + kSumBytes<1>);
+                g += lds_float(s + w * mine_bytes);
+                v += lds_float(s + w * mine_bytes + kSumBytes<1>);
             }
             const float a = g / (1.0f + expf(-g)) * v;
             if (static_cast<int>(threadIdx.x) < n * kTileRows)
@@ -444,10 +444,10 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) moe_w4_down_kernel(con
                     load_tokens(now, piece + 1, 0);
                 else
                     load_tokens(next, 0, 0);
-                const float back = store_scales<FMT, GP, T>(to_table, cur);
+                const bool far = store_scales<FMT, GP, T>(to_table, cur);
                 cp_async_wait<D - 1>();
                 __syncwarp();
-                stage_mma<FMT, GP, 1, T>(tot, from_codes + slot_at, from_table, x, from_inv, back, nch);
+                multiply_stage<FMT, GP, 1, T>(tot, from_codes + slot_at, from_table, x, from_inv, far, nch);
                 __syncwarp();  // the slot, the table and the tokens are rewritten by later stages
                 slot_at = slot_at == (D - 1) * kSlot ? 0 : slot_at + kSlot;
             }
