@@ -15,6 +15,7 @@ dense 128x128 fp8 linears (6/8)".
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -168,6 +169,17 @@ def _raw_stream(stream, device_index: int) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _on_stream(stream, device_index: int):
+    """A context in which new tensors belong to `stream`: set up by it, and their
+    memory not used again before what it has been given is done."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = int(stream)
+        stream = torch.cuda.ExternalStream(raw, device=device_index) if raw else torch.cuda.default_stream(device_index)
+    return torch.cuda.stream(stream)
+
+
 def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -301,17 +313,20 @@ def fp8bs_quant_weight_w4(w: torch.Tensor, fmt: int = FP8BS_W4_MXFP4, group: int
     format: FP8BS_W4_MXFP4 (group 32, uint8 e8m0 scales) or FP8BS_W4_INT4
     (group 32, 64 or 128, bf16 scales)."""
     _require_cuda(w, codes, scales)
+    device = w.get_device()
     scale_dtype = _w4_scale_dtype(fmt, group, "fp8bs_quant_weight_w4")
     assert w.dtype == torch.float32 and w.dim() == 2 and w.stride(1) == 1
     N, K = w.shape
-    if codes is None:
-        codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
-    if scales is None:
-        scales = torch.empty((N, K // group), dtype=scale_dtype, device=w.device)
+    if codes is None or scales is None:
+        with _on_stream(stream, device):
+            if codes is None:
+                codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
+            if scales is None:
+                scales = torch.empty((N, K // group), dtype=scale_dtype, device=w.device)
     assert codes.dtype == torch.uint8 and codes.is_contiguous() and codes.shape == (N, K // 2)
     assert scales.dtype == scale_dtype and scales.is_contiguous() and scales.shape == (N, K // group)
     rc = lib().fp8bs_quant_weight_w4(_ptr(w), N, K, w.stride(0), int(fmt), int(group), _ptr(codes), _ptr(scales),
-                                     _stream(stream))
+                                     _raw_stream(stream, device))
     _check(rc, "fp8bs_quant_weight_w4")
     return codes, scales
 
@@ -325,6 +340,7 @@ def fp8bs_gemv_w4a16(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     call on the stream does not write the weight."""
     if not (x.is_cuda and codes.is_cuda and scales.is_cuda):
         raise ValueError("fp8bs tensors must live on a CUDA device")
+    device = x.get_device()
     scale_dtype = _w4_scale_dtype(fmt, group, "fp8bs_gemv_w4a16")
     M, K = x.shape
     N, half = codes.shape
@@ -334,12 +350,13 @@ def fp8bs_gemv_w4a16(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     assert x.dtype is torch.bfloat16 and codes.dtype is torch.uint8 and scales.dtype is scale_dtype
     assert x1 == c1 == s1 == 1 and 2 * half == K and scales.shape == (N, K // group)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        with _on_stream(stream, device):
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     ldy, y1 = y.stride()
     assert y.is_cuda and y.dtype is torch.bfloat16 and y1 == 1 and y.shape == (M, N)
     rc = (_lib or lib()).fp8bs_gemv_w4a16(x.data_ptr(), M, ldx, codes.data_ptr(), ldc, scales.data_ptr(), lds, N, K,
                                           fmt, group, y.data_ptr(), ldy, FP8BS_FLAG_PDL if pdl else 0,
-                                          _raw_stream(stream, x.get_device()))
+                                          _raw_stream(stream, device))
     if rc:
         raise Fp8bsError(rc, "fp8bs_gemv_w4a16")
     return y
@@ -353,7 +370,7 @@ def fp8bs_moe_route_workspace_bytes(M: int, E: int, H: int) -> int:
 
 
 def new_moe_route_workspace(M: int, E: int, H: int, device=None) -> torch.Tensor:
-    """Allocate (with torch) a zeroed router workspace for up to M tokens."""
+    """Allocate (with torch, zeroed by the current stream) a router workspace for up to M tokens."""
     device = device or torch.device("cuda", torch.cuda.current_device())
     n = fp8bs_moe_route_workspace_bytes(M, E, H)
     if n == 0:
@@ -371,6 +388,7 @@ def fp8bs_moe_route(x: torch.Tensor, w: torch.Tensor, k: int, renorm: bool = Tru
     rows)."""
     if not (x.is_cuda and w.is_cuda):
         raise ValueError("fp8bs tensors must live on a CUDA device")
+    device = x.get_device()
     M, H = x.shape
     rows, Hw = w.shape
     ldx, x1 = x.stride()
@@ -379,18 +397,20 @@ def fp8bs_moe_route(x: torch.Tensor, w: torch.Tensor, k: int, renorm: bool = Tru
     S = k + 1 if code else k
     assert x.dtype is torch.bfloat16 and x1 == 1
     assert w.dtype is torch.bfloat16 and Hw == H and w.is_contiguous()
-    if ids is None:
-        ids = torch.empty((M, S), dtype=torch.int32, device=x.device)
-    if weights is None:
-        weights = torch.empty((M, S), dtype=torch.float32, device=x.device)
+    if ids is None or weights is None or workspace is None:
+        with _on_stream(stream, device):
+            if ids is None:
+                ids = torch.empty((M, S), dtype=torch.int32, device=x.device)
+            if weights is None:
+                weights = torch.empty((M, S), dtype=torch.float32, device=x.device)
+            if workspace is None:
+                workspace = new_moe_route_workspace(M, E, H, x.device)
     assert ids.is_cuda and ids.dtype is torch.int32 and ids.is_contiguous() and ids.shape == (M, S)
     assert weights.is_cuda and weights.dtype is torch.float32 and weights.is_contiguous() and weights.shape == (M, S)
-    if workspace is None:
-        workspace = new_moe_route_workspace(M, E, H, x.device)
     assert workspace.is_cuda and workspace.dtype is torch.uint8
     rc = (_lib or lib()).fp8bs_moe_route(x.data_ptr(), M, H, ldx, w.data_ptr(), E, k, 1 if renorm else 0, code,
                                          ids.data_ptr(), weights.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                         _raw_stream(stream, x.get_device()))
+                                         _raw_stream(stream, device))
     if rc:
         raise Fp8bsError(rc, "fp8bs_moe_route")
     return ids, weights
@@ -401,7 +421,7 @@ def fp8bs_moe_w4a16_workspace_bytes(M: int, S: int, I: int) -> int:
 
 
 def new_moe_w4_workspace(M: int, S: int, I: int, device=None) -> torch.Tensor:
-    """Allocate (with torch) a zeroed 4-bit MoE workspace for up to M tokens x S slots."""
+    """Allocate (with torch, zeroed by the current stream) a 4-bit MoE workspace for up to M tokens x S slots."""
     device = device or torch.device("cuda", torch.cuda.current_device())
     n = fp8bs_moe_w4a16_workspace_bytes(M, S, I)
     if n == 0:
@@ -419,6 +439,7 @@ def fp8bs_moe_w4a16(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tenso
     if not (x.is_cuda and topk_ids.is_cuda and topk_w.is_cuda and w13.is_cuda and s13.is_cuda and w2.is_cuda and
             s2.is_cuda):
         raise ValueError("fp8bs tensors must live on a CUDA device")
+    device = x.get_device()
     scale_dtype = _w4_scale_dtype(fmt, group, "fp8bs_moe_w4a16")
     M, H = x.shape
     ldx, x1 = x.stride()
@@ -433,16 +454,18 @@ def fp8bs_moe_w4a16(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tenso
     assert w2.dtype is torch.uint8 and w2.is_contiguous() and H2 == H
     assert s13.dtype is scale_dtype and s13.is_contiguous() and s13.shape == (E, 2 * I, H // group)
     assert s2.dtype is scale_dtype and s2.is_contiguous() and s2.shape == (E, H, I // group)
-    if y is None:
-        y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
+    if y is None or workspace is None:
+        with _on_stream(stream, device):
+            if y is None:
+                y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
+            if workspace is None:
+                workspace = new_moe_w4_workspace(M, S, I, x.device)
     assert y.is_cuda and y.dtype is torch.bfloat16 and y.is_contiguous() and y.shape == (M, H)
-    if workspace is None:
-        workspace = new_moe_w4_workspace(M, S, I, x.device)
     assert workspace.is_cuda and workspace.dtype is torch.uint8
     rc = (_lib or lib()).fp8bs_moe_w4a16(x.data_ptr(), M, H, ldx, topk_ids.data_ptr(), topk_w.data_ptr(), S,
                                          w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), E, I, fmt,
                                          group, y.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                         _raw_stream(stream, x.get_device()))
+                                         _raw_stream(stream, device))
     if rc:
         raise Fp8bsError(rc, "fp8bs_moe_w4a16")
     return y

@@ -1,0 +1,129 @@
+"""The binding's buffers, streams and devices, without a GPU: tensors and the
+library are stand-ins that record what they are asked for."""
+
+import contextlib
+
+import pytest
+import torch
+
+import fp8_block_scale_x128_gb300 as fb
+
+SIDE = 0x5150  # a raw stream
+
+
+class Tensor:
+    def __init__(self, shape, dtype, device=0, made_on="before the call"):
+        self.shape, self.dtype, self.index, self.made_on = torch.Size(shape), dtype, device, made_on
+        self.device = torch.device("cuda", max(device, 0))
+
+    is_cuda = property(lambda self: self.index >= 0)
+
+    def get_device(self):
+        return self.index
+
+    def stride(self, i=None):
+        s = [1]
+        for n in reversed(self.shape[1:]):
+            s.insert(0, s[0] * n)
+        return tuple(s) if i is None else s[i]
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return torch.empty(0, dtype=self.dtype).element_size()
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x1000
+
+
+class Library:
+    """Every call succeeds and is kept; sizes are small and positive."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            if name.endswith("_bytes"):
+                return 1024
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def box(monkeypatch):
+    """(library, list of the tensors made inside a call); current device 0."""
+    made, now = [], ["the current stream"]
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, now[0] = now[0], s
+        yield
+        now[0] = before
+
+    def new(shape, dtype=None, device=None):
+        made.append(Tensor(shape if isinstance(shape, (tuple, list)) else (shape,), dtype, made_on=now[0]))
+        return made[-1]
+
+    library = Library()
+    monkeypatch.setattr(fb, "_lib", library)
+    monkeypatch.setattr(torch, "empty", new)
+    monkeypatch.setattr(torch, "zeros", new)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda raw, device=None: raw)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0x77, raising=False)
+    return library, made
+
+
+BF16, U8, I32, F32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
+
+
+def operands(name):
+    """The tensors that a call has to be given, by its parameters' names."""
+    return {
+        "fp8bs_quant_weight_w4": dict(w=Tensor((64, 256), F32)),
+        "fp8bs_gemv_w4a16": dict(x=Tensor((2, 256), BF16), codes=Tensor((64, 128), U8), scales=Tensor((64, 8), U8)),
+        "fp8bs_moe_route": dict(x=Tensor((2, 256), BF16), w=Tensor((16, 256), BF16)),
+        "fp8bs_moe_w4a16": dict(x=Tensor((2, 256), BF16), topk_ids=Tensor((2, 3), I32), topk_w=Tensor((2, 3), F32),
+                                w13=Tensor((4, 256, 128), U8), s13=Tensor((4, 256, 8), U8),
+                                w2=Tensor((4, 256, 64), U8), s2=Tensor((4, 256, 4), U8)),
+    }[name]
+
+
+# what each call makes itself where it is not given it
+MADE = {
+    "fp8bs_quant_weight_w4": dict(codes=((64, 128), U8), scales=((64, 8), U8)),
+    "fp8bs_gemv_w4a16": dict(y=((2, 64), BF16)),
+    "fp8bs_moe_route": dict(ids=((2, 4), I32), weights=((2, 4), F32), workspace=((1024,), U8)),
+    "fp8bs_moe_w4a16": dict(y=((2, 256), BF16), workspace=((1024,), U8)),
+}
+EXTRA = {"fp8bs_moe_route": dict(k=4)}
+
+
+def call(name, **kw):
+    return getattr(fb, name)(**{**operands(name), **EXTRA.get(name, {}), **kw})
+
+
+@pytest.mark.parametrize("name", MADE)
+def test_buffers_a_call_makes_belong_to_its_stream(box, name):
+    library, made = box
+    call(name, stream=SIDE)
+    assert len(made) == len(MADE[name]) and all(t.made_on == SIDE for t in made)
+    assert len(library.calls) == 1 and library.calls[0][1][-1] == SIDE
+
+
+@pytest.mark.parametrize("name", MADE)
+def test_buffers_without_a_stream_are_the_current_ones(box, name):
+    library, made = box
+    call(name)
+    assert all(t.made_on == "the current stream" for t in made) and library.calls[0][1][-1] == 0x77
+
