@@ -166,7 +166,11 @@ def _raw_stream(stream, device_index: int) -> int:
     current one (looked up without building a torch.cuda.Stream)."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device_index)
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        return int(stream)
+    if stream.device_index != device_index:
+        raise ValueError(f"the stream is of cuda:{stream.device_index}, the tensors are on cuda:{device_index}")
+    return stream.cuda_stream
 
 
 def _on_stream(stream, device_index: int):
@@ -178,6 +182,19 @@ def _on_stream(stream, device_index: int):
         raw = int(stream)
         stream = torch.cuda.ExternalStream(raw, device=device_index) if raw else torch.cuda.default_stream(device_index)
     return torch.cuda.stream(stream)
+
+
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _wrong_device(*ts):
+    """The library launches on the current device: refuse tensors elsewhere."""
+    where = sorted({t.get_device() for t in ts})
+    if where[0] < 0:
+        raise ValueError("fp8bs tensors must live on a CUDA device")
+    raise ValueError("fp8bs tensors must live on the current CUDA device: they are on "
+                     f"{', '.join(f'cuda:{i}' for i in where)}, it is cuda:{_current_device()}")
 
 
 def _ptr(t: torch.Tensor | None):
@@ -314,6 +331,8 @@ def fp8bs_quant_weight_w4(w: torch.Tensor, fmt: int = FP8BS_W4_MXFP4, group: int
     (group 32, 64 or 128, bf16 scales)."""
     _require_cuda(w, codes, scales)
     device = w.get_device()
+    if device != _current_device():
+        _wrong_device(w)
     scale_dtype = _w4_scale_dtype(fmt, group, "fp8bs_quant_weight_w4")
     assert w.dtype == torch.float32 and w.dim() == 2 and w.stride(1) == 1
     N, K = w.shape
@@ -323,6 +342,8 @@ def fp8bs_quant_weight_w4(w: torch.Tensor, fmt: int = FP8BS_W4_MXFP4, group: int
                 codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
             if scales is None:
                 scales = torch.empty((N, K // group), dtype=scale_dtype, device=w.device)
+    if not device == codes.get_device() == scales.get_device():
+        _wrong_device(w, codes, scales)
     assert codes.dtype == torch.uint8 and codes.is_contiguous() and codes.shape == (N, K // 2)
     assert scales.dtype == scale_dtype and scales.is_contiguous() and scales.shape == (N, K // group)
     rc = lib().fp8bs_quant_weight_w4(_ptr(w), N, K, w.stride(0), int(fmt), int(group), _ptr(codes), _ptr(scales),
@@ -338,9 +359,9 @@ def fp8bs_gemv_w4a16(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     [N, K/2], scales [N, K/group] (rows may be strided).  pdl=True launches with
     programmatic dependent launch; use it only when the work just before this
     call on the stream does not write the weight."""
-    if not (x.is_cuda and codes.is_cuda and scales.is_cuda):
-        raise ValueError("fp8bs tensors must live on a CUDA device")
     device = x.get_device()
+    if device < 0 or not device == codes.get_device() == scales.get_device() == _current_device():
+        _wrong_device(x, codes, scales)
     scale_dtype = _w4_scale_dtype(fmt, group, "fp8bs_gemv_w4a16")
     M, K = x.shape
     N, half = codes.shape
@@ -352,8 +373,10 @@ def fp8bs_gemv_w4a16(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     if y is None:
         with _on_stream(stream, device):
             y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    elif y.get_device() != device:
+        _wrong_device(x, y)
     ldy, y1 = y.stride()
-    assert y.is_cuda and y.dtype is torch.bfloat16 and y1 == 1 and y.shape == (M, N)
+    assert y.dtype is torch.bfloat16 and y1 == 1 and y.shape == (M, N)
     rc = (_lib or lib()).fp8bs_gemv_w4a16(x.data_ptr(), M, ldx, codes.data_ptr(), ldc, scales.data_ptr(), lds, N, K,
                                           fmt, group, y.data_ptr(), ldy, FP8BS_FLAG_PDL if pdl else 0,
                                           _raw_stream(stream, device))
@@ -386,9 +409,9 @@ def fp8bs_moe_route(x: torch.Tensor, w: torch.Tensor, k: int, renorm: bool = Tru
     (renormalised over them or not).  shared="one" appends expert E with
     weight 1, shared="gate" with weight sigmoid(x . w[E]) (w then has E + 1
     rows)."""
-    if not (x.is_cuda and w.is_cuda):
-        raise ValueError("fp8bs tensors must live on a CUDA device")
     device = x.get_device()
+    if device < 0 or not device == w.get_device() == _current_device():
+        _wrong_device(x, w)
     M, H = x.shape
     rows, Hw = w.shape
     ldx, x1 = x.stride()
@@ -405,9 +428,11 @@ def fp8bs_moe_route(x: torch.Tensor, w: torch.Tensor, k: int, renorm: bool = Tru
                 weights = torch.empty((M, S), dtype=torch.float32, device=x.device)
             if workspace is None:
                 workspace = new_moe_route_workspace(M, E, H, x.device)
-    assert ids.is_cuda and ids.dtype is torch.int32 and ids.is_contiguous() and ids.shape == (M, S)
-    assert weights.is_cuda and weights.dtype is torch.float32 and weights.is_contiguous() and weights.shape == (M, S)
-    assert workspace.is_cuda and workspace.dtype is torch.uint8
+    if not device == ids.get_device() == weights.get_device() == workspace.get_device():
+        _wrong_device(x, ids, weights, workspace)
+    assert ids.dtype is torch.int32 and ids.is_contiguous() and ids.shape == (M, S)
+    assert weights.dtype is torch.float32 and weights.is_contiguous() and weights.shape == (M, S)
+    assert workspace.dtype is torch.uint8
     rc = (_lib or lib()).fp8bs_moe_route(x.data_ptr(), M, H, ldx, w.data_ptr(), E, k, 1 if renorm else 0, code,
                                          ids.data_ptr(), weights.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                          _raw_stream(stream, device))
@@ -436,10 +461,10 @@ def fp8bs_moe_w4a16(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tenso
     """One small-batch MoE layer on 4-bit weights: bf16 x [M, H]; int32 topk_ids
     and fp32 topk_w [M, S]; codes w13 [E, 2I, H/2], w2 [E, H, I/2] (uint8) with
     scales s13 [E, 2I, H/group], s2 [E, H, I/group].  Returns bf16 y [M, H]."""
-    if not (x.is_cuda and topk_ids.is_cuda and topk_w.is_cuda and w13.is_cuda and s13.is_cuda and w2.is_cuda and
-            s2.is_cuda):
-        raise ValueError("fp8bs tensors must live on a CUDA device")
     device = x.get_device()
+    if device < 0 or not (device == topk_ids.get_device() == topk_w.get_device() == w13.get_device() ==
+                          s13.get_device() == w2.get_device() == s2.get_device() == _current_device()):
+        _wrong_device(x, topk_ids, topk_w, w13, s13, w2, s2)
     scale_dtype = _w4_scale_dtype(fmt, group, "fp8bs_moe_w4a16")
     M, H = x.shape
     ldx, x1 = x.stride()
@@ -460,8 +485,10 @@ def fp8bs_moe_w4a16(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tenso
                 y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
             if workspace is None:
                 workspace = new_moe_w4_workspace(M, S, I, x.device)
-    assert y.is_cuda and y.dtype is torch.bfloat16 and y.is_contiguous() and y.shape == (M, H)
-    assert workspace.is_cuda and workspace.dtype is torch.uint8
+    if not device == y.get_device() == workspace.get_device():
+        _wrong_device(x, y, workspace)
+    assert y.dtype is torch.bfloat16 and y.is_contiguous() and y.shape == (M, H)
+    assert workspace.dtype is torch.uint8
     rc = (_lib or lib()).fp8bs_moe_w4a16(x.data_ptr(), M, H, ldx, topk_ids.data_ptr(), topk_w.data_ptr(), S,
                                          w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), E, I, fmt,
                                          group, y.data_ptr(), workspace.data_ptr(), workspace.numel(),

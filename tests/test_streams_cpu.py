@@ -127,3 +127,23 @@ def test_buffers_without_a_stream_are_the_current_ones(box, name):
     call(name)
     assert all(t.made_on == "the current stream" for t in made) and library.calls[0][1][-1] == 0x77
 
+
+@pytest.mark.parametrize("device", [-1, 1])
+@pytest.mark.parametrize("name,which", [(n, w) for n in MADE for w in (*operands(n), *MADE[n])])
+def test_a_tensor_elsewhere_is_refused(box, name, which, device):
+    library, _ = box
+    t = operands(name).get(which)
+    shape, dtype = (t.shape, t.dtype) if t is not None else MADE[name][which]
+    with pytest.raises(ValueError):
+        call(name, **{which: Tensor(shape, dtype, device=device)})
+    assert not library.calls
+
+
+@pytest.mark.parametrize("name", MADE)
+def test_another_current_device_is_refused(box, monkeypatch, name):
+    library, _ = box
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    with pytest.raises(ValueError):
+        call(name)
+    assert not library.calls
+
