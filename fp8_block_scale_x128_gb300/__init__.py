@@ -432,7 +432,7 @@ def fp8bs_moe_route(x: torch.Tensor, w: torch.Tensor, k: int, renorm: bool = Tru
         _wrong_device(x, ids, weights, workspace)
     assert ids.dtype is torch.int32 and ids.is_contiguous() and ids.shape == (M, S)
     assert weights.dtype is torch.float32 and weights.is_contiguous() and weights.shape == (M, S)
-    assert workspace.dtype is torch.uint8
+    assert workspace.dtype is torch.uint8 and workspace.is_contiguous()
     rc = (_lib or lib()).fp8bs_moe_route(x.data_ptr(), M, H, ldx, w.data_ptr(), E, k, 1 if renorm else 0, code,
                                          ids.data_ptr(), weights.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                          _raw_stream(stream, device))
@@ -488,7 +488,7 @@ def fp8bs_moe_w4a16(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tenso
     if not device == y.get_device() == workspace.get_device():
         _wrong_device(x, y, workspace)
     assert y.dtype is torch.bfloat16 and y.is_contiguous() and y.shape == (M, H)
-    assert workspace.dtype is torch.uint8
+    assert workspace.dtype is torch.uint8 and workspace.is_contiguous()
     rc = (_lib or lib()).fp8bs_moe_w4a16(x.data_ptr(), M, H, ldx, topk_ids.data_ptr(), topk_w.data_ptr(), S,
                                          w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), E, I, fmt,
                                          group, y.data_ptr(), workspace.data_ptr(), workspace.numel(),

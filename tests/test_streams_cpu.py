@@ -147,3 +147,12 @@ def test_another_current_device_is_refused(box, monkeypatch, name):
         call(name)
     assert not library.calls
 
+
+@pytest.mark.parametrize("name", ["fp8bs_moe_route", "fp8bs_moe_w4a16"])
+def test_a_workspace_that_is_not_one_piece_is_refused(box, name):
+    library, _ = box
+    ws = Tensor((1 << 20,), U8)
+    ws.is_contiguous = lambda: False
+    with pytest.raises(AssertionError):
+        call(name, workspace=ws)
+    assert not library.calls
