@@ -415,8 +415,10 @@ def fp8bs_moe_route(x: torch.Tensor, w: torch.Tensor, k: int, renorm: bool = Tru
     M, H = x.shape
     rows, Hw = w.shape
     ldx, x1 = x.stride()
-    code = _ROUTE_SHARED[shared]
+    code = _ROUTE_SHARED.get(shared, -1)
     E = rows - 1 if code == 2 else rows
+    if code < 0 or not 0 < k <= E:
+        raise Fp8bsError(FP8BS_ERR_ARG if code < 0 else FP8BS_ERR_SHAPE, "fp8bs_moe_route")
     S = k + 1 if code else k
     assert x.dtype is torch.bfloat16 and x1 == 1
     assert w.dtype is torch.bfloat16 and Hw == H and w.is_contiguous()

@@ -49,6 +49,9 @@ class Library:
     def __init__(self):
         self.calls = []
 
+    def fp8bs_status_string(self, status):
+        return b""
+
     def __getattr__(self, name):
         def call(*args):
             if name.endswith("_bytes"):
@@ -156,3 +159,13 @@ def test_a_workspace_that_is_not_one_piece_is_refused(box, name):
     with pytest.raises(AssertionError):
         call(name, workspace=ws)
     assert not library.calls
+
+
+@pytest.mark.parametrize("kw,status", [(dict(shared="both"), fb.FP8BS_ERR_ARG), (dict(shared=None), fb.FP8BS_ERR_ARG),
+                                       (dict(k=0), fb.FP8BS_ERR_SHAPE), (dict(k=-3), fb.FP8BS_ERR_SHAPE),
+                                       (dict(k=17), fb.FP8BS_ERR_SHAPE), (dict(k=16, shared="gate"), fb.FP8BS_ERR_SHAPE)])
+def test_router_refusals_are_the_librarys(box, kw, status):
+    library, made = box
+    with pytest.raises(fb.Fp8bsError) as e:
+        call("fp8bs_moe_route", **kw)
+    assert e.value.status == status and not library.calls and not made
