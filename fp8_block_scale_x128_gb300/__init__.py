@@ -219,8 +219,9 @@ def fp8bs_encode_e4m3(v: torch.Tensor, codes: torch.Tensor | None = None, stream
     """fp32 v [n] (n % 4 == 0) -> uint8 e4m3fn codes [n] (RNE, satfinite)."""
     _require_cuda(v)
     assert v.dtype == torch.float32 and v.is_contiguous()
-    if codes is None:
-        codes = torch.empty(v.numel(), dtype=torch.uint8, device=v.device)
+    with _on_stream(stream, v.get_device()):
+        if codes is None:
+            codes = torch.empty(v.numel(), dtype=torch.uint8, device=v.device)
     rc = lib().fp8bs_encode_e4m3(_ptr(v), v.numel(), _ptr(codes), _stream(stream))
     _check(rc, "fp8bs_encode_e4m3")
     return codes
@@ -232,10 +233,11 @@ def fp8bs_quant(x: torch.Tensor, scale_kind: int = FP8BS_SCALE_F32, xq: torch.Te
     _require_cuda(x)
     assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.stride(1) == 1
     M, K = x.shape
-    if xq is None:
-        xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
-    if xs is None:
-        xs = torch.empty((M, K // 128), dtype=_scale_dtype(scale_kind), device=x.device)
+    with _on_stream(stream, x.get_device()):
+        if xq is None:
+            xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        if xs is None:
+            xs = torch.empty((M, K // 128), dtype=_scale_dtype(scale_kind), device=x.device)
     rc = lib().fp8bs_quant(_ptr(x), M, K, x.stride(0), int(scale_kind), _ptr(xq), _ptr(xs),
                            _stream(stream))
     _check(rc, "fp8bs_quant")
@@ -254,12 +256,13 @@ def fp8bs_rmsnorm_quant(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
     assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.stride(1) == 1
     assert gamma.dtype == torch.bfloat16 and gamma.dim() == 1 and gamma.is_contiguous()
     M, K = x.shape
-    if xq is None:
-        xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
-    if xs is None:
-        xs = torch.empty((M, K // 128), dtype=_scale_dtype(scale_kind), device=x.device)
-    if y is None and want_y:
-        y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+    with _on_stream(stream, x.get_device()):
+        if xq is None:
+            xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        if xs is None:
+            xs = torch.empty((M, K // 128), dtype=_scale_dtype(scale_kind), device=x.device)
+        if y is None and want_y:
+            y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
     if y is not None:
         assert y.dtype == torch.bfloat16 and y.dim() == 2 and y.stride(1) == 1
     rc = lib().fp8bs_rmsnorm_quant(_ptr(x), M, K, x.stride(0), _ptr(gamma), float(eps),
@@ -302,10 +305,11 @@ def fp8bs_moe_w8a16(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tenso
     S = topk_ids.shape[1]
     E, I2, _ = w13.shape
     I = I2 // 2
-    if y is None:
-        y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
-    if workspace is None:
-        workspace = new_moe_workspace(M, S, H, I, x.device)
+    with _on_stream(stream, x.get_device()):
+        if y is None:
+            y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
+        if workspace is None:
+            workspace = new_moe_workspace(M, S, H, I, x.device)
     rc = lib().fp8bs_moe_w8a16(_ptr(x), M, H, _ptr(topk_ids), _ptr(topk_w), S, _ptr(w13), _ptr(s13),
                                _ptr(w2), _ptr(s2), E, I, _ptr(y), _ptr(workspace),
                                workspace.numel(), _stream(stream))
@@ -505,8 +509,9 @@ def fp8bs_quant_weight(w: torch.Tensor, scale_kind: int = FP8BS_SCALE_F32, strea
     _require_cuda(w)
     assert w.dtype == torch.float32 and w.dim() == 2 and w.stride(1) == 1
     N, K = w.shape
-    wq = torch.empty((N, K), dtype=torch.uint8, device=w.device)
-    ws = torch.empty((N // 128, K // 128), dtype=_scale_dtype(scale_kind), device=w.device)
+    with _on_stream(stream, w.get_device()):
+        wq = torch.empty((N, K), dtype=torch.uint8, device=w.device)
+        ws = torch.empty((N // 128, K // 128), dtype=_scale_dtype(scale_kind), device=w.device)
     rc = lib().fp8bs_quant_weight(_ptr(w), N, K, w.stride(0), int(scale_kind), _ptr(wq), _ptr(ws),
                                   _stream(stream))
     _check(rc, "fp8bs_quant_weight")
@@ -528,7 +533,8 @@ def fp8bs_prepack_weight(wq: torch.Tensor, ws: torch.Tensor, scale_kind: int = F
     if nbytes == 0:
         raise Fp8bsError(-2, "fp8bs_packed_weight_bytes")
     if packed is None:
-        packed = torch.empty(nbytes, dtype=torch.uint8, device=wq.device)
+        with _on_stream(stream, wq.get_device()):
+            packed = torch.empty(nbytes, dtype=torch.uint8, device=wq.device)
     rc = lib().fp8bs_prepack_weight(_ptr(wq), wq.stride(0), _ptr(ws), N, K, int(scale_kind),
                                     _ptr(packed), packed.numel(), _stream(stream))
     _check(rc, "fp8bs_prepack_weight")
@@ -552,7 +558,8 @@ def new_workspace(N: int, K: int, device=None, stream=None) -> torch.Tensor:
     n = fp8bs_workspace_bytes(N, K)
     if n == 0:
         raise Fp8bsError(-2, "fp8bs_workspace_bytes")
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    with _on_stream(stream, torch.device(device).index):
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
     fp8bs_workspace_init(ws, stream)
     return ws
 
@@ -572,10 +579,11 @@ def fp8bs_gemm_fused(x: torch.Tensor, packed: torch.Tensor, N: int, K: int,
     assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.stride(1) == 1
     M = x.shape[0]
     assert x.shape[1] == K
-    if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    if workspace is None:
-        workspace = new_workspace(N, K, x.device, stream)
+    with _on_stream(stream, x.get_device()):
+        if y is None:
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        if workspace is None:
+            workspace = new_workspace(N, K, x.device, stream)
     rc = lib().fp8bs_gemm_fused(
         _ptr(x), M, x.stride(0), _ptr(packed), packed.numel(), N, K, int(scale_kind), _ptr(y),
         y.stride(0), _ptr(workspace), workspace.numel(), _ptr(xq_out), _ptr(xs_out),
@@ -595,10 +603,11 @@ def fp8bs_gemm_prequant(xq: torch.Tensor, xs: torch.Tensor, packed: torch.Tensor
     assert xq.dtype == torch.uint8 and xq.dim() == 2 and xq.stride(1) == 1 and xq.shape[1] == K
     assert xs.is_contiguous() and xs.shape == (xq.shape[0], K // 128)
     M = xq.shape[0]
-    if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
-    if workspace is None:
-        workspace = new_workspace(N, K, xq.device, stream)
+    with _on_stream(stream, xq.get_device()):
+        if y is None:
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+        if workspace is None:
+            workspace = new_workspace(N, K, xq.device, stream)
     rc = lib().fp8bs_gemm_prequant(
         _ptr(xq), M, xq.stride(0), _ptr(xs), _ptr(packed), packed.numel(), N, K, int(scale_kind),
         _ptr(y), y.stride(0), _ptr(workspace), workspace.numel(), FP8BS_FLAG_PDL if pdl else 0,
@@ -622,7 +631,8 @@ def fp8bs_gemm_fused_static(x: torch.Tensor, packed: torch.Tensor, N: int, K: in
     M = x.shape[0]
     assert x.shape[1] == K
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        with _on_stream(stream, x.get_device()):
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     rc = lib().fp8bs_gemm_fused_static(
         _ptr(x), M, x.stride(0), _ptr(packed), packed.numel(), N, K, int(scale_kind), _ptr(y),
         y.stride(0), _ptr(xq_out), _ptr(xs_out), _ptr(status_out),

@@ -34,7 +34,7 @@ class Tensor:
         return self.shape.numel()
 
     def element_size(self):
-        return torch.empty(0, dtype=self.dtype).element_size()
+        return self.dtype.itemsize
 
     def is_contiguous(self):
         return True
@@ -100,6 +100,23 @@ def operands(name):
                                 w13=Tensor((4, 256, 128), U8), s13=Tensor((4, 256, 8), U8),
                                 w2=Tensor((4, 256, 64), U8), s2=Tensor((4, 256, 4), U8)),
     }[name]
+
+
+# the 8-bit calls: their tensors and how many they make themselves
+EIGHT_BIT = {
+    "fp8bs_encode_e4m3": (dict(v=Tensor((256,), F32)), 1),
+    "fp8bs_quant": (dict(x=Tensor((2, 256), BF16)), 2),
+    "fp8bs_rmsnorm_quant": (dict(x=Tensor((2, 256), BF16), gamma=Tensor((256,), BF16), want_y=True), 3),
+    "fp8bs_moe_w8a16": (dict(x=Tensor((2, 512), BF16), topk_ids=Tensor((2, 3), I32), topk_w=Tensor((2, 3), F32),
+                             w13=Tensor((4, 256, 512), U8), s13=Tensor((4, 2, 4), F32), w2=Tensor((4, 512, 128), U8),
+                             s2=Tensor((4, 4, 1), F32)), 2),
+    "fp8bs_quant_weight": (dict(w=Tensor((128, 256), F32)), 2),
+    "fp8bs_prepack_weight": (dict(wq=Tensor((128, 256), U8), ws=Tensor((1, 2), F32)), 1),
+    "fp8bs_gemm_fused": (dict(x=Tensor((2, 256), BF16), packed=Tensor((1024,), U8), N=128, K=256), 2),
+    "fp8bs_gemm_prequant": (dict(xq=Tensor((2, 256), U8), xs=Tensor((2, 2), F32), packed=Tensor((1024,), U8), N=128, K=256), 2),
+    "fp8bs_gemm_fused_static": (dict(x=Tensor((2, 256), BF16), packed=Tensor((1024,), U8), N=128, K=256), 1),
+    "new_workspace": (dict(N=128, K=256, device=torch.device("cuda", 0)), 1),
+}
 
 
 # what each call makes itself where it is not given it
@@ -169,3 +186,12 @@ def test_router_refusals_are_the_librarys(box, kw, status):
     with pytest.raises(fb.Fp8bsError) as e:
         call("fp8bs_moe_route", **kw)
     assert e.value.status == status and not library.calls and not made
+
+
+@pytest.mark.parametrize("name", EIGHT_BIT)
+def test_buffers_an_8_bit_call_makes_belong_to_its_stream(box, name):
+    library, made = box
+    given, count = EIGHT_BIT[name]
+    getattr(fb, name)(**given, stream=SIDE)
+    assert len(made) == count and all(t.made_on == SIDE for t in made)
+    assert all(args[-1].value == SIDE for _, args in library.calls)
