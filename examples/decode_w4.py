@@ -70,7 +70,7 @@ class Layer:
                            workspace=self.route_ws)
         fb.fp8bs_moe_w4a16(self.x, self.ids, self.weights, self.w13, self.s13, self.w2, self.s2, self.fmt, self.group,
                            y=self.y, workspace=self.moe_ws)
-        # the projection's weight is never written: it may be read early
+        # nothing unfinished writes the projection's weight: it may be read early
         fb.fp8bs_gemv_w4a16(self.y, self.wo, self.so, self.fmt, self.group, y=self.out, pdl=True)
 
     def reference(self) -> torch.Tensor:

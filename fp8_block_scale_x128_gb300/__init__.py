@@ -361,8 +361,8 @@ def fp8bs_gemv_w4a16(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
                      stream=None) -> torch.Tensor:
     """Y = bf16(x . W^T) for bf16 x [M <= 16, K] and a 4-bit weight: codes uint8
     [N, K/2], scales [N, K/group] (rows may be strided).  pdl=True launches with
-    programmatic dependent launch; use it only when the work just before this
-    call on the stream does not write the weight."""
+    programmatic dependent launch; use it only when no unfinished work on the
+    stream, however far back, writes the weight."""
     device = x.get_device()
     if device < 0 or not device == codes.get_device() == scales.get_device() == _current_device():
         _wrong_device(x, codes, scales)
@@ -572,7 +572,7 @@ def fp8bs_gemm_fused(x: torch.Tensor, packed: torch.Tensor, N: int, K: int,
     """Y = bf16(quant(x) . W^T) for bf16 x [M <= 64, K] and a packed weight.
 
     pdl=True launches with programmatic dependent launch (FP8BS_FLAG_PDL); use
-    it only when the work just before this call on the stream does not write
+    it only when no unfinished work on the stream, however far back, writes
     `packed`.
     """
     _require_cuda(x, packed, y, workspace, xq_out, xs_out)

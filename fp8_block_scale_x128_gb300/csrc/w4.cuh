@@ -625,7 +625,7 @@ cudaError_t allow_shared(K* kernel, std::atomic<uint64_t>& done) {
 
 // Every kernel of these files is launched with programmatic dependent launch:
 // it waits for its predecessor (griddep_wait) before it touches memory -- but
-// for weights that the caller says the predecessor does not write -- and lets
+// for weights that the caller says no unfinished work writes -- and lets
 // its successor start (launch_dependents) only after that wait, so that what a
 // successor reads before its own wait is complete up to the kernel before it.
 // Back-to-back calls overlap one call's start-up with the other's tail.

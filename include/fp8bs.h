@@ -183,14 +183,17 @@ int fp8bs_prepack_weight(const uint8_t* wq, int64_t ldw, const void* ws, int64_t
 /* linear at M <= 32; here up to FP8BS_MAX_M)                                */
 /* ------------------------------------------------------------------------ */
 
-/* Flags of fp8bs_gemm_fused. */
+/* Flags of the GEMM and GEMV calls. */
 enum {
     /* Launch with programmatic dependent launch: the call may start, and read
      * `packed`, while the kernel before it on the stream is still running; x,
      * y, xq_out, xs_out and the workspace are touched only after that kernel
      * has completed.  Back-to-back linears then overlap one call's start-up
-     * and weight stream with the previous call's tail.  Use it only when the
-     * work just before this call on the stream does not write `packed`. */
+     * and weight stream with the previous call's tail.  Use it only when no
+     * unfinished work on the stream writes the weight, however far back: the
+     * kernel before may itself have started early (this library's quant and
+     * fused GEMM let their successor start before they wait for their own
+     * predecessor), so a kernel two back may still be running. */
     FP8BS_FLAG_PDL = 1u,
 };
 
@@ -378,7 +381,8 @@ int fp8bs_quant_weight_w4(const float* w, int64_t N, int64_t K, int64_t ldw, int
  *   N, K   : N >= 1 (any), K a multiple of 128, both at most 2^24.
  *   y      : bf16 [M, N], row stride ldy >= N elements, 2-byte aligned.
  *   flags  : 0 or FP8BS_FLAG_PDL (codes and scales may then be read while the
- *            kernel before is still running; x and y not).
+ *            kernels before are still running, x and y not: no unfinished work
+ *            on the stream may write codes or scales).
  * Products of codes and activations are exact, sums fp32 in a fixed order: the
  * same inputs give the same bits.  Activations are carried in fp16 after an
  * exact power-of-two scaling per token and K slice: elements below 2^-31 of

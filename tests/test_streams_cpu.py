@@ -195,3 +195,15 @@ def test_buffers_an_8_bit_call_makes_belong_to_its_stream(box, name):
     getattr(fb, name)(**given, stream=SIDE)
     assert len(made) == count and all(t.made_on == SIDE for t in made)
     assert all(args[-1].value == SIDE for _, args in library.calls)
+
+
+def test_early_reads_are_documented_for_the_whole_stream():
+    # quant and the fused GEMM let their successor start before they wait for
+    # their own predecessor: "the work just before" is not far enough back
+    with open(fb.HEADER_PATH) as f:
+        header = " ".join(f.read().replace("*", " ").split())
+    for text in (fb.fp8bs_gemm_fused.__doc__, fb.fp8bs_gemv_w4a16.__doc__):
+        text = " ".join(text.split())
+        assert "no unfinished work on the stream" in text and "just before" not in text
+    assert header.count("no unfinished work on the stream") == 2
+    assert "work just before this call" not in header
