@@ -274,17 +274,14 @@ cudaError_t launch_gemv_w4(const GemvW4Args& a, cudaStream_t stream) {
         constexpr int F = fmt(), G = gp();
         const int sm = a.sm_count, blocks = min((p.tiles + p.WR - 1) / p.WR, sm);
         const int steps = ((p.tiles + blocks - 1) / blocks + p.WR - 1) / p.WR;  // tiles of a warp
-        if (a.M > 8) {
-            if (fits<G, 2, 1, 2, true>(p)) return launch<F, G, 2, 1, 2, true>(p, sm, stream);
-            return launch<F, G, 2, 1, 2, false>(p, sm, stream);
-        }
+        // (from 9 tokens on the sums leave no room for x beside them at any size)
+        if (a.M > 8) return launch<F, G, 2, 1, 2, false>(p, sm, stream);
         // two tiles a stage share its activations; where a warp has one tile,
         // half of such a stage would be idle.  (A slice of one stage is staged
         // once for kGroup tiles without being kept.)
         if (steps > 1 && fits<G, 1, 2, 2, true>(p)) return launch<F, G, 1, 2, 2, true>(p, sm, stream);
         if (steps > 1 && p.pieces == 1 && fits<G, 1, 2, 2, false>(p)) return launch<F, G, 1, 2, 2, false>(p, sm, stream);
         if (fits<G, 1, 1, 3, true>(p)) return launch<F, G, 1, 1, 3, true>(p, sm, stream);
-        if (p.pieces == 1) return launch<F, G, 1, 1, 3, false>(p, sm, stream);
         if (fits<G, 1, 1, 2, true>(p)) return launch<F, G, 1, 1, 2, true>(p, sm, stream);
         return launch<F, G, 1, 1, 3, false>(p, sm, stream);
     });
