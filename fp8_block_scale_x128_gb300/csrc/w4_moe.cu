@@ -346,7 +346,6 @@ __global__ void __launch_bounds__(kThreads, 2) moe_w4_up_kernel(const __grid_con
 // ---- 2. down -----------------------------------------------------------------
 // Bytes of a warp: a ring of stages of T tiles, their scale tables, the inverse
 // scales and a stage of a for n pairs, two columns each.
-constexpr int kWideDownPairs = 256;
 constexpr int kInvBytes = 128;  // 8 factors, the next part aligned
 __host__ __device__ constexpr int down_depth(int T) { return T == 2 ? 2 : 3; }
 template <int GP>
@@ -529,16 +528,23 @@ cudaError_t launch_down_as(const MoeParams& p, int sm_count, cudaStream_t stream
 template <int FMT, int GP, bool ONE>
 cudaError_t launch_down(const MoeParams& p, int sm_count, cudaStream_t stream) {
     const int tiles = p.H / kTileRows;
-    // Two tiles a stage share its other costs, where they still fill most of the
-    // machine and 16 warps fit beside the pairs' products with three pairs an
-    // entry (8 tokens of 513x128: 13.3 us for 15.7; with 352 pairs only one fits
-    // and an expert's codes are fetched for each of its pairs: 45 us for 43).
-    constexpr int kWant = 3;
+    // Three forms, the first two where 16 warps fit beside the pairs' products
+    // with kWant pairs an entry (with one an expert's codes are fetched for each of
+    // its pairs).  Whole layers, us, two tiles and 16 warps / one and 8 / one and
+    // 16, INT4: 8 tokens of 64x256, 6 slots, hidden 2560 18.9 / 19.8 / 20.9, 3584
+    // 21.7 / 22.4 / 24.4, 7168 40.2 / 42.5 / 43.5; 24 tokens of 128x256, 8 slots,
+    // hidden 4096 48.3 / 52.3 / 54.0.  Two tiles share a stage's other costs, though
+    // at hidden 2560 they leave half of the multiprocessors without a block; one
+    // token of up to 8 slots takes up to 1 us less with one tile and 8 warps.
+    // With no more tiles than multiprocessors (hidden 2048) a second block of 8
+    // warps would have none: 19 tokens of 24x512, 4 slots 23.8 / 27.3 / 22.4, 64 of
+    // 128x512, 8 slots 112 / 112 / 88.  Past kWant: 128 tokens of 64x256, 8 slots
+    // (one pair an entry with 16 warps) 88 / 88 / 114.
+    constexpr int kWant = 2;
     if (tiles > sm_count && down_block_bytes<GP, 2, 16>(p, kWant) <= kMaxBlockShared)
         return launch_down_as<FMT, GP, ONE, 2, 16>(p, sm_count, stream);
-    // With no more tiles than multiprocessors a second block would have none (19
-    // tokens of 24x512: 13.6 us for 14.8).
-    if (tiles <= sm_count && p.M * p.S <= kWideDownPairs) return launch_down_as<FMT, GP, ONE, 1, 16>(p, sm_count, stream);
+    if (tiles <= sm_count && down_block_bytes<GP, 1, 16>(p, kWant) <= kMaxBlockShared)
+        return launch_down_as<FMT, GP, ONE, 1, 16>(p, sm_count, stream);
     return launch_down_as<FMT, GP, ONE, 1, 8>(p, sm_count, stream);
 }
 

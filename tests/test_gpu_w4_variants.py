@@ -71,10 +71,14 @@ def test_gemv_variants_over_several_groups_of_tiles(dev, fmt, group, M, K):  # n
     (3, 2, 5, 2560, 128),    # two tiles a stage, all of I in it
     (3, 2, 5, 2560, 384),    # two tiles a stage, I in two stages, the second half filled
     (9, 8, 6, 4096, 768),    # two tiles a stage, several entries an expert
-    (20, 9, 7, 2560, 256),   # more pairs than two tiles leave room for: 8 warps
+    (20, 9, 7, 2560, 256),   # two tiles, two or three pairs an entry
     (20, 9, 7, 2560, 640),   # the same, I in three stages
-    (88, 3, 9, 512, 128),    # no more tiles than multiprocessors, many pairs
+    (40, 9, 7, 2560, 256),   # more pairs than two tiles leave room for: 8 warps
+    (40, 9, 7, 2560, 640),   # the same, I in three stages
+    (88, 3, 9, 512, 128),    # no more tiles than multiprocessors: 16 warps
     (88, 3, 9, 512, 384),    # the same, I in two stages
+    (100, 10, 9, 512, 128),  # more pairs than 16 warps leave room for: 8
+    (100, 10, 9, 512, 384),  # the same, I in two stages
     (7, 5, 4, 640, 1536),    # few pairs, I in six stages
 ])
 def test_moe_variants(dev, fmt, group, M, S, E, Hd, I):  # noqa: F811
