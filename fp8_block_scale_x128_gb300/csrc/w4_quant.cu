@@ -4,7 +4,8 @@
 // RN32(amax / 6), so no finite weight saturates; code = the e2m1 value nearest
 // to w / s, ties to even.  INT4 (codes q for q - 8, bf16 scales): s =
 // bf16(RN32(amax / 7)), q = clamp(rint(RN32(w / s)), -8, 7) + 8; a group whose
-// scale is 0 gets q = 8.
+// scale is 0 gets q = 8.  A group with an infinity or a NaN gets a NaN as its
+// scale (the codes have none): e8m0's 255 or bf16's.
 //
 // Memory-bound: each lane takes 8 consecutive weights (two 16-byte loads) and
 // writes one word of codes, G / 8 lanes share a group's maximum by shuffles.
@@ -17,6 +18,12 @@ namespace fp8bs {
 namespace {
 
 constexpr int kThreads = 256;
+
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
 
 template <int FMT, int G>
 __global__ void __launch_bounds__(kThreads)
@@ -42,9 +49,10 @@ __global__ void __launch_bounds__(kThreads)
         }
         float amax = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+        for (int j = 0; j < 8; ++j) amax = max_or_nan(amax, fabsf(v[j]));
 #pragma unroll
-        for (int off = 1; off < G / 8; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
+        for (int off = 1; off < G / 8; off <<= 1) amax = max_or_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
+        const bool finite = amax <= 3.402823466e38f;
         uint32_t word = 0;
         if constexpr (FMT == FP8BS_W4_MXFP4) {
             const uint32_t byte = e8m0_ceil_byte(__fdiv_rn(amax, 6.0f));
@@ -58,7 +66,7 @@ __global__ void __launch_bounds__(kThreads)
                 word |= two << (8 * j);
             }
             if (valid && (col & (G / 8 - 1)) == 0)
-                static_cast<uint8_t*>(scales)[row * (K / G) + col / (G / 8)] = static_cast<uint8_t>(byte);
+                static_cast<uint8_t*>(scales)[row * (K / G) + col / (G / 8)] = finite ? static_cast<uint8_t>(byte) : uint8_t(255);
         } else {
             const uint16_t bits = w4::to_bf16(__fdiv_rn(amax, 7.0f));
             const float s = bf16_bits_to_float(bits);
@@ -67,8 +75,9 @@ __global__ void __launch_bounds__(kThreads)
                 const float q = s > 0.0f ? rintf(__fdiv_rn(v[j], s)) : 0.0f;
                 word |= static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(q, -8.0f), 7.0f)) + 8) << (4 * j);
             }
-            if (valid && (col & (G / 8 - 1)) == 0) static_cast<uint16_t*>(scales)[row * (K / G) + col / (G / 8)] = bits;
+            if (valid && (col & (G / 8 - 1)) == 0) static_cast<uint16_t*>(scales)[row * (K / G) + col / (G / 8)] = finite ? bits : uint16_t(0x7FC0);
         }
+        if (!finite) word = FMT == FP8BS_W4_MXFP4 ? 0u : 0x88888888u;  // zeros, times a NaN
         if (valid) codes[at] = word;
     }
 }

@@ -344,8 +344,7 @@ int fp8bs_moe_w8a16(const uint16_t* x, int64_t M, int64_t H, const int32_t* topk
 /* Weight formats.  Both keep codes row-major, two a byte (the even k in the
  * low nibble), and one scale per 1xG group along K, row-major [N, K/G].
  *   MXFP4: e2m1 codes (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives), e8m0
- *          scale bytes b for 2^(b - 127) (255 is not a scale: such a group
- *          gives infinities or NaN), G = 32.
+ *          scale bytes b for 2^(b - 127) (255: NaN), G = 32.
  *   INT4 : codes q = 0..15 for the value q - 8, bf16 scales, G = 32, 64 or 128.
  * A weight is its code's value times its group's scale, exactly. */
 typedef enum {
@@ -361,7 +360,8 @@ typedef enum {
  * MXFP4: s = the smallest power of two >= RN32(amax / 6) (2^-127 for a zero
  * group), code = the e2m1 value nearest to w / s, ties to even.  INT4: s =
  * bf16(RN32(amax / 7)), q = clamp(rint(RN32(w / s)), -8, 7) + 8, q = 8 where s
- * is 0.
+ * is 0.  A group with an infinity or a NaN gets a NaN as its scale (e8m0's 255,
+ * bf16's 0x7FC0) and zeros as its codes.
  * Errors: FP8BS_ERR_ARG (format, group, null pointer, ldw < K),
  * FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN, FP8BS_ERR_CUDA. */
 int fp8bs_quant_weight_w4(const float* w, int64_t N, int64_t K, int64_t ldw, int format, int group,

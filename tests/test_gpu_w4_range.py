@@ -78,3 +78,28 @@ def test_moe_large_scales_beside_tiny_ones(dev, fmt, group):  # noqa: F811
     ref, bound = R.moe(x, ids, tw, R.value(c13, s13, fmt, group), R.value(c2, s2, fmt, group))
     keep = np.arange(Hd) != 5  # (there the small activations are below 2^-39 of the largest)
     assert np.all(np.abs(y - ref)[:, keep] <= bound[:, keep])
+
+
+@pytest.mark.parametrize("fmt,group", R.FORMATS)
+def test_quantiser_keeps_infinities_and_nan_in_sight(dev, fmt, group):  # noqa: F811
+    # no code stands for them: their group becomes NaN, the others stay what they are
+    N, K = 9, 512
+    w = synth.w_f32(N, K, seed=23)
+    clean_c, clean_s = R.quant(w, fmt, group)
+    bad = w.copy()
+    bad[1, 5], bad[2, 500], bad[3, 130], bad[8, 256] = np.inf, -np.inf, np.nan, np.nan
+    bad[3, 131] = np.inf
+    codes, scales = fb.fp8bs_quant_weight_w4(to_dev(bad, dev), fmt, group)
+    x = R.bf16(np.ones((1, K)))
+    y = f64(fb.fp8bs_gemv_w4a16(bf16_dev(x, dev), codes, scales, fmt, group))[0]
+    assert np.array_equal(np.isnan(y), np.isin(np.arange(N), (1, 2, 3, 8)))
+    codes = codes.cpu().numpy()
+    scales = scales.cpu().numpy() if fmt == MXFP4 else scales.view(torch.int16).cpu().numpy().view(np.uint16)
+    hit = np.zeros((N, K // group), bool)
+    for r, c in ((1, 5), (2, 500), (3, 130), (8, 256)):
+        hit[r, c // group] = True
+    assert np.array_equal(scales[~hit], clean_s[~hit])
+    assert np.all(scales[hit] == (255 if fmt == MXFP4 else 0x7FC0))
+    half = np.repeat(hit, group // 2, 1)
+    assert np.array_equal(codes[~half], clean_c[~half])
+    assert np.all(codes[half] == (0 if fmt == MXFP4 else 0x88))
