@@ -265,7 +265,10 @@ int fp8bs_quant_weight_w4(const float* w, int64_t N, int64_t K, int64_t ldw, int
     if (ldw < K) return FP8BS_ERR_ARG;
     if (!aligned(w, 16) || ldw % 4 != 0 || !aligned(codes, 4) || !aligned(scales, w4_scale_size(format)))
         return FP8BS_ERR_ALIGN;
-    return status_of(launch_quant_weight_w4(w, N, K, ldw, format, group, codes, scales, as_stream(stream)));
+    int sm = 0;
+    const int rc = current_sm_count(&sm);
+    if (rc != FP8BS_OK) return rc;
+    return status_of(launch_quant_weight_w4(w, N, K, ldw, format, group, codes, scales, sm, as_stream(stream)));
 }
 
 int fp8bs_gemv_w4a16(const uint16_t* x, int64_t M, int64_t ldx, const uint8_t* codes, int64_t ldc, const void* scales,

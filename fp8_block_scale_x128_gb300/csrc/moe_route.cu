@@ -39,6 +39,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kOneLaunchM = kWarps;  // a warp per token in the last block
 constexpr size_t kHeader = 256;  // workspace: the arrival counter, then the partial logits
+// Blocks wanted: one a multiprocessor of a GB300.  A constant, not the device's
+// count: the workspace's size goes by it and is asked for without a device.
 constexpr int kTargetBlocks = 152;
 constexpr int kMaxCand = 64;
 

@@ -649,7 +649,7 @@ cudaError_t launch_dependent(void (*kernel)(P...), int grid, int block, int smem
 // Launchers (argument checks are done by the C ABI before these run).
 
 cudaError_t launch_quant_weight_w4(const float* w, int64_t N, int64_t K, int64_t ldw, int format, int group,
-                                   uint8_t* codes, void* scales, cudaStream_t stream);
+                                   uint8_t* codes, void* scales, int sm_count, cudaStream_t stream);
 
 struct GemvW4Args {
     const uint16_t* x;

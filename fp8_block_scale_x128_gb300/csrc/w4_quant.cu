@@ -9,8 +9,10 @@
 //
 // Memory-bound: each lane takes 8 consecutive weights (two 16-byte loads) and
 // writes one word of codes, G / 8 lanes share a group's maximum by shuffles.
-// Measured at 16384x8192: 138 us to MXFP4 (4.4 TB/s, 0.65 of the measured copy
-// bandwidth), 165 us to INT4; what keeps it from the rest was not looked for.
+// Measured at 16384x8192: 134 us to MXFP4 (4.5 TB/s, 0.67 of the measured copy
+// bandwidth), 167 us to INT4; what keeps it from the rest was not looked for.
+#include <algorithm>
+
 #include "internal.cuh"
 #include "w4.cuh"
 
@@ -85,10 +87,11 @@ __global__ void __launch_bounds__(kThreads)
 }  // namespace
 
 cudaError_t launch_quant_weight_w4(const float* w, int64_t N, int64_t K, int64_t ldw, int format, int group,
-                                   uint8_t* codes, void* scales, cudaStream_t stream) {
-    const int64_t words = N * (K / 8);
-    int64_t blocks = (words + kThreads - 1) / kThreads;
-    if (blocks > 152 * 64) blocks = 152 * 64;
+                                   uint8_t* codes, void* scales, int sm_count, cudaStream_t stream) {
+    // 16 blocks a multiprocessor, two or more waves of them (us to MXFP4 with 8, 16,
+    // 32 and 64: 5120x4096 35.5, 35.5, 41.7, 60.1; 16384x8192 156, 134, 139, 140)
+    const int64_t words = N * (K / 8), most = int64_t(sm_count) * 16;
+    const int64_t blocks = std::min((words + kThreads - 1) / kThreads, most);
     return w4::dispatch_format(format, group, [&](auto fmt, auto gp) {
         quant_weight_w4_kernel<fmt(), 128 / gp()><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
             w, words, static_cast<int>(K), ldw, reinterpret_cast<uint32_t*>(codes), scales);
