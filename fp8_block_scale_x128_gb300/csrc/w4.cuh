@@ -352,9 +352,10 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
 }
 
 // One word (8 codes) -> four fp16 pairs, exact.  e2m1: the hardware conversion.
-// Integers: a nibble q in the low mantissa bits under the exponent of 1024 is
-// 1024 + q (16 q one nibble up), so one subtraction, or one multiply-add by
-// 1/16, leaves q - 8.
+// Integers by an offset in the exponent, a published method (Y. J. Kim, R. Henry,
+// R. Fahim, H. H. Awadalla, "Who Says Elephants Can't Run", 2022): a nibble q in
+// the low mantissa bits under the exponent of 1024 is 1024 + q (16 q one nibble
+// up), so one subtraction, or one multiply-add by 1/16, leaves q - 8.
 template <int FMT>
 __device__ __forceinline__ void decode8(uint32_t w, uint32_t (&r)[4]) {
     if constexpr (FMT == FP8BS_W4_MXFP4) {

@@ -62,7 +62,7 @@ struct MoeParams {
 // elements each.
 struct Lists {
     ushort4* entry;      // expert, first (place of its first pair), n (its pairs: 1 .. batch)
-    uint32_t* pair;      // by place, grouped by expert, ascending experts: pair | token << 16
+    uint32_t* pair;      // by place, grouped by entry: pair | token << 16
     uint16_t* place;     // of a pair
     uint16_t* unsorted;  // pairs of experts with more than one entry
     int entries;

@@ -469,8 +469,9 @@ size_t fp8bs_moe_w4a16_workspace_bytes(int64_t M, int64_t S, int64_t I);
  *              its first word must be zero before the first call;
  *              fp8bs_check_error reads it.  Not to be used by two calls that
  *              can run at the same time.
- * The second launch uses programmatic dependent launch; no cross-block waits;
- * every sum in a fixed order, so results are deterministic.
+ * Both launches use programmatic dependent launch and wait for what runs before
+ * the call before they touch memory.  No cross-block waits; every sum in a fixed
+ * order, so results are deterministic.
  * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN,
  * FP8BS_ERR_WORKSPACE, FP8BS_ERR_CUDA. */
 int fp8bs_moe_w4a16(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const int32_t* topk_ids,
