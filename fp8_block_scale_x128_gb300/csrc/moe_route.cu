@@ -161,7 +161,7 @@ __device__ void exact_logits(const RouteParams& p, int m, int e0, int e1, int la
             }
         }
     }
-#pragma unroll
+#pragma unroll 1
     for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -330,6 +330,7 @@ __device__ void select_token(const RouteParams& p, Select& sel, int m, int lane)
             if (lane == r1) d = both[1];
         }
         int rank = 0;
+#pragma unroll 1
         for (int o = 0; o < p.k; ++o) {
             const Exact b = d.shfl(o);
             const int eb = __shfl_sync(0xFFFFFFFFu, e, o);
