@@ -184,17 +184,13 @@ def _on_stream(stream, device_index: int):
     return torch.cuda.stream(stream)
 
 
-def _current_device() -> int:
-    return torch._C._cuda_getDevice()
-
-
 def _wrong_device(*ts):
     """The library launches on the current device: refuse tensors elsewhere."""
     where = sorted({t.get_device() for t in ts})
     if where[0] < 0:
         raise ValueError("fp8bs tensors must live on a CUDA device")
     raise ValueError("fp8bs tensors must live on the current CUDA device: they are on "
-                     f"{', '.join(f'cuda:{i}' for i in where)}, it is cuda:{_current_device()}")
+                     f"{', '.join(f'cuda:{i}' for i in where)}, it is cuda:{torch._C._cuda_getDevice()}")
 
 
 def _ptr(t: torch.Tensor | None):
@@ -335,7 +331,7 @@ def fp8bs_quant_weight_w4(w: torch.Tensor, fmt: int = FP8BS_W4_MXFP4, group: int
     (group 32, 64 or 128, bf16 scales)."""
     _require_cuda(w, codes, scales)
     device = w.get_device()
-    if device != _current_device():
+    if device != torch._C._cuda_getDevice():
         _wrong_device(w)
     scale_dtype = _w4_scale_dtype(fmt, group, "fp8bs_quant_weight_w4")
     assert w.dtype == torch.float32 and w.dim() == 2 and w.stride(1) == 1
@@ -364,7 +360,7 @@ def fp8bs_gemv_w4a16(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     programmatic dependent launch; use it only when no unfinished work on the
     stream, however far back, writes the weight."""
     device = x.get_device()
-    if device < 0 or not device == codes.get_device() == scales.get_device() == _current_device():
+    if device < 0 or not device == codes.get_device() == scales.get_device() == torch._C._cuda_getDevice():
         _wrong_device(x, codes, scales)
     scale_dtype = _w4_scale_dtype(fmt, group, "fp8bs_gemv_w4a16")
     M, K = x.shape
@@ -383,6 +379,7 @@ def fp8bs_gemv_w4a16(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     assert y.dtype is torch.bfloat16 and y1 == 1 and y.shape == (M, N)
     rc = (_lib or lib()).fp8bs_gemv_w4a16(x.data_ptr(), M, ldx, codes.data_ptr(), ldc, scales.data_ptr(), lds, N, K,
                                           fmt, group, y.data_ptr(), ldy, FP8BS_FLAG_PDL if pdl else 0,
+                                          torch._C._cuda_getCurrentRawStream(device) if stream is None else
                                           _raw_stream(stream, device))
     if rc:
         raise Fp8bsError(rc, "fp8bs_gemv_w4a16")
@@ -414,7 +411,7 @@ def fp8bs_moe_route(x: torch.Tensor, w: torch.Tensor, k: int, renorm: bool = Tru
     weight 1, shared="gate" with weight sigmoid(x . w[E]) (w then has E + 1
     rows)."""
     device = x.get_device()
-    if device < 0 or not device == w.get_device() == _current_device():
+    if device < 0 or not device == w.get_device() == torch._C._cuda_getDevice():
         _wrong_device(x, w)
     M, H = x.shape
     rows, Hw = w.shape
@@ -441,6 +438,7 @@ def fp8bs_moe_route(x: torch.Tensor, w: torch.Tensor, k: int, renorm: bool = Tru
     assert workspace.dtype is torch.uint8 and workspace.is_contiguous()
     rc = (_lib or lib()).fp8bs_moe_route(x.data_ptr(), M, H, ldx, w.data_ptr(), E, k, 1 if renorm else 0, code,
                                          ids.data_ptr(), weights.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                         torch._C._cuda_getCurrentRawStream(device) if stream is None else
                                          _raw_stream(stream, device))
     if rc:
         raise Fp8bsError(rc, "fp8bs_moe_route")
@@ -469,7 +467,7 @@ def fp8bs_moe_w4a16(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tenso
     scales s13 [E, 2I, H/group], s2 [E, H, I/group].  Returns bf16 y [M, H]."""
     device = x.get_device()
     if device < 0 or not (device == topk_ids.get_device() == topk_w.get_device() == w13.get_device() ==
-                          s13.get_device() == w2.get_device() == s2.get_device() == _current_device()):
+                          s13.get_device() == w2.get_device() == s2.get_device() == torch._C._cuda_getDevice()):
         _wrong_device(x, topk_ids, topk_w, w13, s13, w2, s2)
     scale_dtype = _w4_scale_dtype(fmt, group, "fp8bs_moe_w4a16")
     M, H = x.shape
@@ -498,6 +496,7 @@ def fp8bs_moe_w4a16(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tenso
     rc = (_lib or lib()).fp8bs_moe_w4a16(x.data_ptr(), M, H, ldx, topk_ids.data_ptr(), topk_w.data_ptr(), S,
                                          w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), E, I, fmt,
                                          group, y.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                         torch._C._cuda_getCurrentRawStream(device) if stream is None else
                                          _raw_stream(stream, device))
     if rc:
         raise Fp8bsError(rc, "fp8bs_moe_w4a16")
