@@ -10,8 +10,8 @@
 // arrive (a counter that it also resets; no block waits for another), which
 // saves a launch; with more tokens one block's warps would take them in turn,
 // so a second kernel, a block per token, selects (programmatic dependent
-// launch).  Measured (in a graph, w in the second-level cache): 7.0 us for one
-// token of 512 experts, hidden 4096, 7.4 for 9 in two launches, 10.5 for 64; all
+// launch).  Measured (in a graph, w in the second-level cache): 7.1 us for one
+// token of 512 experts, hidden 4096, 7.3 for 16 in two launches, 10.3 for 64; all
 // of it is latency: two trips to memory, the arrival, the selection.
 //
 // The order of the chosen experts is decided by fp32 logits unless two of them
@@ -25,8 +25,10 @@
 // MMAs of a chunk, added in pairs, as are the 8 warps' sums, and one for each
 // further chunk of a warp and slice.
 //
-// On N(0, 1) tokens with 1% outliers one token in a hundred has such a pair
-// (hidden 4096, 10 of 512): 3.4 us more for the call.
+// On N(0, 1) tokens with 1% outliers about one token in a hundred has such a pair
+// (hidden 4096, 10 of 512): 3.2 us more for the call, most of it the latency of
+// instructions that are not in the cache.  64 tokens take 12.5 us on average (24
+// inputs), 10.3 without a pair.
 #include "internal.cuh"
 #include "w4.cuh"
 

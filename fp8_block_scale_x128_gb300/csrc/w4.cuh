@@ -28,15 +28,17 @@
 // What bounds it.  Measured on GB300, per multiprocessor quarter: this MMA takes
 // 8 cycles, the e2m1 conversion of a pair, an integer operation and an fp16 pair
 // operation 2, an fp32 FMA 1; together the MMAs and the integer pipe take about
-// the sum of their cycles.  Codes at the measured copy bandwidth arrive as 1088 bytes (16 rows x
-// 128 k with e8m0 scales) per 186 cycles; decoding, multiplying and scaling
-// them (stage_mma alone, 4 warps a quarter) takes 116 to 135 cycles with one
-// tile of token columns, 220 with two, 150 for integer codes.  What a stage
-// needs besides -- addresses, copies, scale tables, sums -- comes on top, so
-// the kernels are bound by instruction issue (0.5 per cycle with 16 warps and
-// 128 registers), not by memory, and stages are made as large as shared memory
-// lets them be: two tiles a stage where they fit, 77 instructions per 16 x 128
-// instead of 91.
+// the sum of their cycles.  Codes at the measured copy bandwidth arrive as 1088
+// bytes (16 rows x 128 k with e8m0 scales) per 186 cycles; decoding, multiplying
+// and scaling them (stage_mma alone, 4 warps a quarter) takes 116 to 135 cycles
+// with one tile of token columns, 220 with two, 150 for integer codes.  What a
+// stage needs besides -- addresses, copies, scale tables, sums -- comes on top.
+// The kernels are bound by latency in that chain, not by memory and by no pipe:
+// with 4 warps a scheduler (128 registers) 0.4 to 0.5 instructions issue a cycle,
+// and a warp waits 1.3 to 1.9 issues on the instruction before, 0.6 to 2.2 on
+// global and 0.7 to 1.1 on shared memory.  Stages are made as large as shared
+// memory lets them be, for fewer instructions in the chain: two tiles a stage
+// where they fit.
 #pragma once
 
 #include <cuda_fp16.h>

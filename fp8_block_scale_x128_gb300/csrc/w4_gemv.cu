@@ -8,13 +8,16 @@
 // own, so no step but the sums over the slices is block-wide.  Those go in
 // slice order: repeated calls give the same bits.
 //
-// Bound by instruction issue (w4.cuh), at the smallest sizes by the launch.
-// Measured in a graph on weights that are not in the second-level cache: 3.8 us
-// for 1x4096x2048 (MXFP4; 0.66 at the measured copy bandwidth), 6.3 for
-// 1x5120x4096 (1.65), 18.5 for 1x16384x8192 (10.5, 58% of the bandwidth; the
-// other way round, groups of tiles in pieces, took 21.0), 39 for 16 tokens of
-// it, where x does not fit beside the codes and is staged twice.  16 warps in
-// one block, not 8 in two: the slices are half as long, and x is held once.
+// Bound by latency in a long chain of instructions (w4.cuh), at the smallest sizes
+// by the launch.  Measured in a graph on weights that are not in the second-level
+// cache: 4.0 us for 1x4096x2048 (MXFP4; 0.66 at the measured copy bandwidth), 7.0
+// for 1x5120x4096 (INT4, groups of 128; 1.6), 18.3 for 1x16384x8192 (MXFP4; 10.5,
+// 58% of the bandwidth; the other way round, groups of tiles in pieces, took
+// 21.0), 24.5 for 8 tokens of it and 39 for 16, where x does not fit beside the
+// codes and is staged twice.  16 warps in one block, not 8 in two: the slices are
+// half as long, and x is held once.  Of 128 registers a thread 16 columns spill 32
+// bytes (MXFP4; 4 with integer groups of 32 or 128), two tiles a stage with kept
+// x 24 (MXFP4) and 16 (integer groups of 32).
 #include "internal.cuh"
 #include "w4.cuh"
 

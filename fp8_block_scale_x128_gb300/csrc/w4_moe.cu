@@ -22,11 +22,13 @@
 // instead of 14.4 for one token of 513x256).  The second launch's lists and
 // first codes do not wait for the first.
 //
-// Bound by instruction issue (w4.cuh).  Measured on MXFP4 experts of 513x256,
-// hidden 4096, 32 tokens with 10 routed and a shared one: gate/up 66.8 us for
-// 271 MB read (0.60 of the measured copy bandwidth), down 44.9 us for 135 MB
-// (0.44), each launched alone; 100.6 us for both in a stream; 12.2 us for one
-// token.
+// Bound by latency in a long chain of instructions (w4.cuh).  Measured on MXFP4
+// experts of 513x256, hidden 4096, 32 tokens with 10 routed and a shared one:
+// gate/up 64.1 us for 271 MB read (0.62 of the measured copy bandwidth), down
+// 48.9 us for 135 MB (0.41), each launched alone; 102.6 us for both in a graph;
+// 11.7 us for one token.  Gate/up spills 20 bytes a thread with 32-wide groups
+// (128 registers, two blocks a multiprocessor; with 48 bytes it took 14 us more),
+// the down projection with two tiles 4.
 #include "internal.cuh"
 #include "w4.cuh"
 
