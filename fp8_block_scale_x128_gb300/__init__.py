@@ -6,6 +6,11 @@ device pointers, sizes and the cudaStream_t of the C ABI declared in
 kernels.  There is no fallback: if the compiled library is missing, or a call
 returns an error status, an exception is raised.
 
+A call given a `stream` (a torch.cuda.Stream or a raw cudaStream_t) runs there
+and not on the current one: its inputs have to be ready on it, and what the call
+allocates itself (outputs, workspaces) belongs to it, as under
+``torch.cuda.stream(stream)``.
+
 The names match the C entry points.  Layout and rounding rules are documented
 in the header; the method is the one of "[AMD] Small-M FP8 block-scale GEMM
 with fused activation quant for gfx950 (Qwen3.5)", "Modifications", with the
