@@ -42,6 +42,14 @@ FP8BS_ROUTE_MAX_K = 32
 FP8BS_ROUTE_MAX_M = 1024
 FP8BS_MOE_W4_MAX_I = 8192
 FP8BS_MOE_W4_MAX_H = 32768
+FP8BS_ROPE_HALF = 0
+FP8BS_ROPE_INTERLEAVED = 1
+FP8BS_ROPE_PLAIN = 0
+FP8BS_ROPE_LINEAR = 1
+FP8BS_ROPE_BY_PARTS = 2
+FP8BS_KV_BF16 = 0
+FP8BS_KV_E4M3 = 1
+FP8BS_ATTN_MAX_SEQS = 1024
 
 STATUS = {
     0: "FP8BS_OK", -1: "FP8BS_ERR_ARG", -2: "FP8BS_ERR_SHAPE", -3: "FP8BS_ERR_ALIGN",
@@ -119,6 +127,15 @@ def lib() -> ctypes.CDLL:
             "fp8bs_moe_w4a16_workspace_bytes": ([i64, i64, i64], sz),
             "fp8bs_moe_w4a16": ([vp, i64, i64, i64, vp, vp, i64, vp, vp, vp, vp, i64, i64, ci, ci, vp, vp, sz, vp],
                                 ci),
+            "fp8bs_rope_freqs": ([ci, c.c_double, ci, c.c_double, c.c_double, c.c_double, c.c_double, vp, vp],
+                                 ci),
+            "fp8bs_qk_norm_rope": ([vp, i64, i64, vp, i64, i64, i64, i64, i64, i64, vp, vp, ci, ci, c.c_float, vp, vp,
+                                    c.c_float, vp, i64, i64, vp, i64, i64, vp], ci),
+            "fp8bs_qk_norm_rope_append": ([vp, i64, i64, vp, i64, i64, vp, i64, i64, i64, i64, vp, vp, vp, ci, ci,
+                                           c.c_float, vp, vp, c.c_float, vp, i64, i64, vp, vp, vp], ci),
+            "fp8bs_attn_paged_workspace_bytes": ([i64, ci], sz),
+            "fp8bs_attn_paged": ([vp, i64, i64, i64, i64, vp, vp, i64, i64, i64, vp, vp, c.c_float, i64, vp, i64, i64,
+                                  vp, sz, vp], ci),
             "fp8bs_quant_weight": ([vp, i64, i64, i64, ci, vp, vp, vp], ci),
             "fp8bs_packed_weight_bytes": ([i64, i64, ci], sz),
             "fp8bs_prepack_weight": ([vp, i64, vp, i64, i64, ci, vp, sz, vp], ci),
@@ -506,6 +523,226 @@ def fp8bs_moe_w4a16(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tenso
     if rc:
         raise Fp8bsError(rc, "fp8bs_moe_w4a16")
     return y
+
+
+class Rope:
+    """Rotary positions of heads: how many dimensions turn, in which pairs and how fast.
+
+    The frequency table is computed on the host (fp8bs_rope_freqs) and lies on `device`;
+    the object is kept and given to every call.  scaling: FP8BS_ROPE_PLAIN, _LINEAR
+    (factor) or _BY_PARTS (factor, original_length, beta_fast, beta_slow).  amplitude
+    multiplies the rotated values; None takes the one that goes with the scaling.
+    rotary_dim 0 turns nothing."""
+
+    def __init__(self, rotary_dim: int, theta: float = 10000.0, layout: int = FP8BS_ROPE_HALF,
+                 scaling: int = FP8BS_ROPE_PLAIN, factor: float = 1.0, original_length: float = 0.0,
+                 beta_fast: float = 32.0, beta_slow: float = 1.0, amplitude: float | None = None, device=None):
+        self.rotary_dim, self.layout = int(rotary_dim), int(layout)
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        host = torch.zeros(max(self.rotary_dim // 2, 1), dtype=torch.int64)
+        own = ctypes.c_float(1.0)
+        if self.rotary_dim:
+            _check(lib().fp8bs_rope_freqs(self.rotary_dim, theta, int(scaling), factor, original_length, beta_fast,
+                                          beta_slow, host.data_ptr(), ctypes.byref(own)), "fp8bs_rope_freqs")
+        self.amplitude = float(own.value if amplitude is None else amplitude)
+        self.freqs = host.to(device)
+
+
+class _KvCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("kind", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("pages", ctypes.c_int64), ("strides", ctypes.c_int64 * 3),
+                ("scale_strides", ctypes.c_int64 * 3)]
+
+
+class KvCache:
+    """A paged cache over tensors of shape [pages, page size, key heads, D], in any
+    order in memory with D contiguous: k and v bf16, or uint8 e4m3 codes with uint8
+    e8m0 scales k_scale and v_scale [pages, page size, key heads].  k and v have the
+    same strides, and so have their scales.  The object holds the tensors and is given
+    to every call; it is not made again for other contents."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        codes = k_scale is not None
+        tensors = (k, v, k_scale, v_scale) if codes else (k, v)
+        self.device_index = k.get_device()
+        if self.device_index < 0 or any(t is None or t.get_device() != self.device_index for t in tensors):
+            raise ValueError("a cache's tensors must live on one CUDA device")
+        assert k.dim() == 4 and k.dtype is (torch.uint8 if codes else torch.bfloat16)
+        assert v.dtype is k.dtype and v.shape == k.shape and v.stride() == k.stride() and k.stride(3) == 1
+        s = _KvCacheStruct()
+        s.k, s.v = k.data_ptr(), v.data_ptr()
+        s.strides[:] = k.stride()[:3]
+        if codes:
+            assert k_scale.dtype is torch.uint8 and v_scale.dtype is torch.uint8
+            assert k_scale.shape == k.shape[:3] == v_scale.shape and k_scale.stride() == v_scale.stride()
+            s.k_scale, s.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+            s.scale_strides[:] = k_scale.stride()
+        else:
+            assert v_scale is None
+        s.kind = FP8BS_KV_E4M3 if codes else FP8BS_KV_BF16
+        s.pages, s.page_size, s.kv_heads, s.head_dim = k.shape
+        self.tensors, self.kind, self.kv_heads, self.head_dim = tensors, s.kind, s.kv_heads, s.head_dim
+        self._struct, self._ref = s, ctypes.addressof(s)
+
+
+def new_kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, kind: int = FP8BS_KV_BF16,
+                 device=None) -> KvCache:
+    """Allocate (with torch, zeroed by the current stream) a cache."""
+    device = device or torch.device("cuda", torch.cuda.current_device())
+    shape = (pages, page_size, kv_heads, head_dim)
+    if kind == FP8BS_KV_BF16:
+        return KvCache(*(torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
+    if kind != FP8BS_KV_E4M3:
+        raise Fp8bsError(FP8BS_ERR_ARG, "new_kv_cache")
+    return KvCache(*(torch.zeros(shape[:n], dtype=torch.uint8, device=device) for n in (4, 4, 3, 3)))
+
+
+def _heads(t: torch.Tensor, T: int, D: int):
+    """(token stride, head stride) of bf16 heads [T, heads, D]."""
+    assert t.dtype is torch.bfloat16
+    T2, _, D2 = t.shape
+    ld, hs, one = t.stride()
+    assert T2 == T and D2 == D and one == 1
+    return ld, hs
+
+
+def _gamma(g: torch.Tensor | None, D: int, device: int):
+    if g is None:
+        return None
+    if g.get_device() != device:
+        _wrong_device(g)
+    assert g.dtype is torch.bfloat16 and g.shape == (D,) and g.is_contiguous()
+    return g.data_ptr()
+
+
+def fp8bs_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, rope: Rope,
+                       gamma_q: torch.Tensor | None = None, gamma_k: torch.Tensor | None = None, eps: float = 1e-6,
+                       q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """Norms (where gamma_q, gamma_k [D] are given) and rotation of bf16 query heads q
+    [T, Hq, D] and key heads k [T, Hk, D] (slices of wider rows do) at int64 positions
+    [T].  Returns (q_out, k_out), which may be given: q and k themselves too."""
+    device = q.get_device()
+    if device < 0 or not device == k.get_device() == positions.get_device() == rope.freqs.get_device() == torch._C._cuda_getDevice():
+        _wrong_device(q, k, positions, rope.freqs)
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    ldq, hsq = _heads(q, T, D)
+    ldk, hsk = _heads(k, T, D)
+    assert positions.dtype is torch.int64 and positions.shape == (T,) and positions.is_contiguous()
+    gq, gk = _gamma(gamma_q, D, device), _gamma(gamma_k, D, device)
+    if q_out is None or k_out is None:
+        with _on_stream(stream, device):
+            if q_out is None:
+                q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+            if k_out is None:
+                k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=q.device)
+    if not device == q_out.get_device() == k_out.get_device():
+        _wrong_device(q, q_out, k_out)
+    assert q_out.shape[1] == Hq and k_out.shape[1] == Hk
+    ldqo, hsqo = _heads(q_out, T, D)
+    ldko, hsko = _heads(k_out, T, D)
+    rc = (_lib or lib()).fp8bs_qk_norm_rope(
+        q.data_ptr(), ldq, hsq, k.data_ptr(), ldk, hsk, T, Hq, Hk, D, positions.data_ptr(), rope.freqs.data_ptr(),
+        rope.rotary_dim, rope.layout, rope.amplitude, gq, gk, eps, q_out.data_ptr(), ldqo, hsqo, k_out.data_ptr(), ldko,
+        hsko, torch._C._cuda_getCurrentRawStream(device) if stream is None else _raw_stream(stream, device))
+    if rc:
+        raise Fp8bsError(rc, "fp8bs_qk_norm_rope")
+    return q_out, k_out
+
+
+def fp8bs_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                              slots: torch.Tensor, rope: Rope, cache: KvCache, gamma_q: torch.Tensor | None = None,
+                              gamma_k: torch.Tensor | None = None, eps: float = 1e-6,
+                              q_out: torch.Tensor | None = None, error: torch.Tensor | None = None,
+                              stream=None) -> torch.Tensor:
+    """fp8bs_qk_norm_rope, the keys going with the value heads v [T, Hk, D] into the
+    cache's int64 slots [T] (page * page size + slot; each at most once, a negative one
+    writes nothing).  Returns q_out.  error: a zeroed uint8 tensor (a workspace does)
+    whose first word takes the status of slots past the cache (fp8bs_check_error)."""
+    device = q.get_device()
+    if device < 0 or not (device == k.get_device() == v.get_device() == positions.get_device() == slots.get_device() ==
+                          rope.freqs.get_device() == cache.device_index == torch._C._cuda_getDevice()):
+        _wrong_device(q, k, v, positions, slots, rope.freqs, cache.tensors[0])
+    T, Hq, D = q.shape
+    Hk = cache.kv_heads
+    ldq, hsq = _heads(q, T, D)
+    ldk, hsk = _heads(k, T, D)
+    ldv, hsv = _heads(v, T, D)
+    assert D == cache.head_dim and k.shape[1] == Hk == v.shape[1]
+    assert positions.dtype is torch.int64 and positions.shape == (T,) and positions.is_contiguous()
+    assert slots.dtype is torch.int64 and slots.shape == (T,) and slots.is_contiguous()
+    gq, gk = _gamma(gamma_q, D, device), _gamma(gamma_k, D, device)
+    if q_out is None:
+        with _on_stream(stream, device):
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if q_out.get_device() != device or (error is not None and error.get_device() != device):
+        _wrong_device(*(t for t in (q, q_out, error) if t is not None))
+    assert q_out.shape[1] == Hq and (error is None or error.dtype is torch.uint8 and error.numel() >= 4)
+    ldqo, hsqo = _heads(q_out, T, D)
+    rc = (_lib or lib()).fp8bs_qk_norm_rope_append(
+        q.data_ptr(), ldq, hsq, k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv, T, Hq, positions.data_ptr(),
+        slots.data_ptr(), rope.freqs.data_ptr(), rope.rotary_dim, rope.layout, rope.amplitude, gq, gk, eps,
+        q_out.data_ptr(), ldqo, hsqo, cache._ref, None if error is None else error.data_ptr(),
+        torch._C._cuda_getCurrentRawStream(device) if stream is None else _raw_stream(stream, device))
+    if rc:
+        raise Fp8bsError(rc, "fp8bs_qk_norm_rope_append")
+    return q_out
+
+
+def fp8bs_attn_paged_workspace_bytes(D: int, sm_count: int = 0) -> int:
+    return int(lib().fp8bs_attn_paged_workspace_bytes(int(D), int(sm_count)))
+
+
+def new_attn_workspace(D: int, device=None) -> torch.Tensor:
+    """Allocate (with torch, zeroed by the current stream) a workspace of fp8bs_attn_paged for heads of D."""
+    device = device or torch.device("cuda", torch.cuda.current_device())
+    n = fp8bs_attn_paged_workspace_bytes(D)
+    if n == 0:
+        raise Fp8bsError(FP8BS_ERR_SHAPE, "fp8bs_attn_paged_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def fp8bs_attn_paged(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, cu_q: torch.Tensor,
+                     kv_len: torch.Tensor, scale: float | None = None, window: int = 0, o: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of bf16 queries q [T, Hq, D], the newest tokens of their sequences,
+    over a paged cache: sequence b has rows cu_q[b] .. cu_q[b + 1] (int32 [B + 1]),
+    kv_len[b] (int32 [B]) tokens with the new ones, and the pages block_table[b]
+    (int32 [B, columns]).  scale: D^-0.5 where None; window: the keys that a row sees
+    at most, 0 for all up to itself.  Returns o [T, Hq, D]; rows of no sequence are
+    left as they were in a given o, and are not set in one that the call makes."""
+    device = q.get_device()
+    if device < 0 or not (device == cache.device_index == block_table.get_device() == cu_q.get_device() ==
+                          kv_len.get_device() == torch._C._cuda_getDevice()):
+        _wrong_device(q, cache.tensors[0], block_table, cu_q, kv_len)
+    T, Hq, D = q.shape
+    B, cols = block_table.shape
+    ldq, hsq = _heads(q, T, D)
+    rows, one = block_table.stride()
+    assert D == cache.head_dim
+    assert block_table.dtype is torch.int32 and (one == 1 or cols < 2)
+    assert cu_q.dtype is torch.int32 and cu_q.shape == (B + 1,) and cu_q.is_contiguous()
+    assert kv_len.dtype is torch.int32 and kv_len.shape == (B,) and kv_len.is_contiguous()
+    if o is None or workspace is None:
+        with _on_stream(stream, device):
+            if o is None:
+                o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+            if workspace is None:
+                workspace = new_attn_workspace(D, q.device)
+    if not device == o.get_device() == workspace.get_device():
+        _wrong_device(q, o, workspace)
+    assert o.shape[1] == Hq
+    assert workspace.dtype is torch.uint8 and workspace.is_contiguous()
+    ldo, hso = _heads(o, T, D)
+    rc = (_lib or lib()).fp8bs_attn_paged(
+        q.data_ptr(), ldq, hsq, T, Hq, cache._ref, block_table.data_ptr(), max(rows, cols), cols, B, cu_q.data_ptr(),
+        kv_len.data_ptr(), D ** -0.5 if scale is None else scale, window, o.data_ptr(), ldo, hso, workspace.data_ptr(),
+        workspace.numel(), torch._C._cuda_getCurrentRawStream(device) if stream is None else _raw_stream(stream, device))
+    if rc:
+        raise Fp8bsError(rc, "fp8bs_attn_paged")
+    return o
 
 
 def fp8bs_quant_weight(w: torch.Tensor, scale_kind: int = FP8BS_SCALE_F32, stream=None):

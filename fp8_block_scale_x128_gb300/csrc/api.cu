@@ -13,8 +13,10 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
+#include "attn.cuh"
 #include "internal.cuh"
 #include "moe.cuh"
 #include "producer.cuh"
@@ -85,6 +87,77 @@ bool w4_ok(int format, int group) {
                                     : format == FP8BS_W4_INT4 && (group == 32 || group == 64 || group == 128);
 }
 int64_t w4_scale_size(int format) { return format == FP8BS_W4_MXFP4 ? 1 : 2; }
+
+// A heads tensor [tokens, heads, D] of bf16: rows on 16 bytes.
+bool heads_aligned(const uint16_t* p, int64_t ld, int64_t hs) { return aligned(p, 16) && ld % 8 == 0 && hs % 8 == 0; }
+
+bool head_dim_ok(int64_t D) { return D == 64 || D == 128 || D == 256; }
+
+constexpr int64_t kMaxHeads = 1024;
+constexpr int64_t kMaxStride = int64_t(1) << 40;  // elements: offsets stay within 64 bits
+
+bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
+
+// The host description of a paged cache: FP8BS_OK or why not.
+int cache_check(const fp8bs_kv_cache* c) {
+    if (!c || (c->kind != FP8BS_KV_BF16 && c->kind != FP8BS_KV_E4M3) || !c->k || !c->v) return FP8BS_ERR_ARG;
+    const bool codes = c->kind == FP8BS_KV_E4M3;
+    if (codes && (!c->k_scale || !c->v_scale)) return FP8BS_ERR_ARG;
+    if (!stride_ok(c->page_stride) || !stride_ok(c->slot_stride) || !stride_ok(c->head_stride)) return FP8BS_ERR_ARG;
+    if (codes && (!stride_ok(c->scale_page_stride) || !stride_ok(c->scale_slot_stride) || !stride_ok(c->scale_head_stride)))
+        return FP8BS_ERR_ARG;
+    if (!head_dim_ok(c->head_dim) || c->kv_heads < 1 || c->kv_heads > kMaxHeads || c->page_size < 1 ||
+        c->page_size > 65536 || (c->page_size & (c->page_size - 1)) != 0 || c->pages < 1 || c->pages > 0x7FFFFFFF)
+        return FP8BS_ERR_SHAPE;
+    // rows of one axis apart from each other
+    if ((c->pages > 1 && c->page_stride < c->head_dim) || (c->page_size > 1 && c->slot_stride < c->head_dim) ||
+        (c->kv_heads > 1 && c->head_stride < c->head_dim))
+        return FP8BS_ERR_ARG;
+    if (codes && ((c->pages > 1 && c->scale_page_stride < 1) || (c->page_size > 1 && c->scale_slot_stride < 1) ||
+                  (c->kv_heads > 1 && c->scale_head_stride < 1)))
+        return FP8BS_ERR_ARG;
+    const int64_t unit = codes ? 16 : 8;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % unit || c->slot_stride % unit || c->head_stride % unit)
+        return FP8BS_ERR_ALIGN;
+    return FP8BS_OK;
+}
+
+// Checks common to the calls that norm and rotate heads.
+int rope_check(const RopeArgs& a) {
+    if (a.layout != FP8BS_ROPE_HALF && a.layout != FP8BS_ROPE_INTERLEAVED) return FP8BS_ERR_ARG;
+    if (!std::isfinite(a.amplitude) || !std::isfinite(a.eps) || a.eps < 0.0f) return FP8BS_ERR_ARG;
+    if (a.T < 0 || a.T > kMaxDim || a.Hq < 0 || a.Hq > kMaxHeads || a.Hk < 0 || a.Hk > kMaxHeads || a.Hq + a.Hk < 1 ||
+        !head_dim_ok(a.D) || a.R < 0 || a.R > a.D || a.R % (a.layout == FP8BS_ROPE_HALF ? 16 : 2) != 0)
+        return FP8BS_ERR_SHAPE;
+    if (a.T == 0) return FP8BS_OK;
+    if (a.Hq && (!a.q || !a.qo)) return FP8BS_ERR_ARG;
+    if (a.Hk && (!a.k || (a.append ? !a.v : !a.ko))) return FP8BS_ERR_ARG;
+    if (a.R && (!a.positions || !a.freqs)) return FP8BS_ERR_ARG;
+    if (a.append && !a.slots) return FP8BS_ERR_ARG;
+    // rows of one tensor apart from each other where they are written, not negative elsewhere
+    auto apart = [&](int64_t ld, int64_t hs, int H) {
+        return stride_ok(ld) && stride_ok(hs) && (H < 2 || hs >= a.D) && (a.T < 2 || ld >= a.D);
+    };
+    if (a.Hq && (!stride_ok(a.ldq) || !stride_ok(a.hsq) || !apart(a.ldqo, a.hsqo, a.Hq))) return FP8BS_ERR_ARG;
+    if (a.Hk && (!stride_ok(a.ldk) || !stride_ok(a.hsk))) return FP8BS_ERR_ARG;
+    if (a.Hk && (a.append ? !stride_ok(a.ldv) || !stride_ok(a.hsv) : !apart(a.ldko, a.hsko, a.Hk))) return FP8BS_ERR_ARG;
+    if (a.Hq && (!heads_aligned(a.q, a.ldq, a.hsq) || !heads_aligned(a.qo, a.ldqo, a.hsqo))) return FP8BS_ERR_ALIGN;
+    if (a.Hk && (!heads_aligned(a.k, a.ldk, a.hsk) ||
+                 !(a.append ? heads_aligned(a.v, a.ldv, a.hsv) : heads_aligned(a.ko, a.ldko, a.hsko))))
+        return FP8BS_ERR_ALIGN;
+    if (a.R && (!aligned(a.positions, 8) || !aligned(a.freqs, 8))) return FP8BS_ERR_ALIGN;
+    if (a.append && (!aligned(a.slots, 8) || (a.err && !aligned(a.err, 256)))) return FP8BS_ERR_ALIGN;
+    if ((a.gq && !aligned(a.gq, 16)) || (a.gk && !aligned(a.gk, 16))) return FP8BS_ERR_ALIGN;
+    return FP8BS_OK;
+}
+
+int run_rope(RopeArgs& a, void* stream) {
+    const int bad = rope_check(a);
+    if (bad != FP8BS_OK || a.T == 0) return bad;
+    const int rc = current_sm_count(&a.sm_count);
+    if (rc != FP8BS_OK) return rc;
+    return status_of(launch_qk_norm_rope(a, as_stream(stream)));
+}
 
 size_t workspace_bytes_for(int64_t K, int sm_count) { return ws_total_bytes(sm_count, K); }
 
@@ -387,6 +460,124 @@ int fp8bs_moe_w4a16(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const 
     a.group = group;
     a.sm_count = sm;
     return status_of(launch_moe_w4(a, as_stream(stream)));
+}
+
+int fp8bs_rope_freqs(int rotary_dim, double theta, int scaling, double factor, double original_length,
+                     double beta_fast, double beta_slow, uint64_t* freqs, float* amplitude) {
+    const double pi = 3.14159265358979323846;
+    if (!freqs || !std::isfinite(theta) || !(theta > 1.0) || scaling < FP8BS_ROPE_PLAIN || scaling > FP8BS_ROPE_BY_PARTS)
+        return FP8BS_ERR_ARG;
+    if (rotary_dim < 2 || rotary_dim > 256 || rotary_dim % 2 != 0) return FP8BS_ERR_SHAPE;
+    if (scaling != FP8BS_ROPE_PLAIN && !(std::isfinite(factor) && factor >= 1.0)) return FP8BS_ERR_ARG;
+    double low = 0.0, span = 1.0;
+    if (scaling == FP8BS_ROPE_BY_PARTS) {
+        if (!(std::isfinite(original_length) && original_length > 0.0 && std::isfinite(beta_fast) && beta_slow > 0.0 &&
+              beta_fast > beta_slow))
+            return FP8BS_ERR_ARG;
+        auto pair = [&](double turns) {
+            return rotary_dim * std::log(original_length / (turns * 2.0 * pi)) / (2.0 * std::log(theta));
+        };
+        low = std::fmax(std::floor(pair(beta_fast)), 0.0);
+        const double high = std::fmin(std::ceil(pair(beta_slow)), rotary_dim - 1.0);
+        span = std::fmax(high - low, 1e-3);
+    }
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+        double f = std::pow(theta, -2.0 * i / rotary_dim);
+        if (scaling == FP8BS_ROPE_LINEAR) f /= factor;
+        if (scaling == FP8BS_ROPE_BY_PARTS) {
+            const double s = std::fmin(std::fmax((i - low) / span, 0.0), 1.0);
+            f = f * (1.0 - s) + f / factor * s;
+        }
+        freqs[i] = static_cast<uint64_t>(std::nearbyint(std::ldexp(f / (2.0 * pi), 64)));  // f <= 1: below 2^62
+    }
+    if (amplitude) *amplitude = scaling == FP8BS_ROPE_BY_PARTS ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return FP8BS_OK;
+}
+
+int fp8bs_qk_norm_rope(const uint16_t* q, int64_t ldq, int64_t hsq, const uint16_t* k, int64_t ldk, int64_t hsk,
+                       int64_t T, int64_t Hq, int64_t Hk, int64_t D, const int64_t* positions,
+                       const uint64_t* freqs, int R, int layout, float amplitude, const uint16_t* gamma_q,
+                       const uint16_t* gamma_k, float eps, uint16_t* q_out, int64_t ldqo, int64_t hsqo,
+                       uint16_t* k_out, int64_t ldko, int64_t hsko, void* stream) {
+    if (Hq < 0 || Hq > kMaxHeads || Hk < 0 || Hk > kMaxHeads || !head_dim_ok(D)) return FP8BS_ERR_SHAPE;
+    RopeArgs a = {};
+    a.q = q, a.ldq = ldq, a.hsq = hsq, a.k = k, a.ldk = ldk, a.hsk = hsk;
+    a.T = T, a.Hq = static_cast<int>(Hq), a.Hk = static_cast<int>(Hk), a.D = static_cast<int>(D);
+    a.positions = positions, a.freqs = freqs, a.R = R, a.layout = layout, a.amplitude = amplitude;
+    a.gq = gamma_q, a.gk = gamma_k, a.eps = eps;
+    a.qo = q_out, a.ldqo = ldqo, a.hsqo = hsqo, a.ko = k_out, a.ldko = ldko, a.hsko = hsko;
+    return run_rope(a, stream);
+}
+
+int fp8bs_qk_norm_rope_append(const uint16_t* q, int64_t ldq, int64_t hsq, const uint16_t* k, int64_t ldk,
+                              int64_t hsk, const uint16_t* v, int64_t ldv, int64_t hsv, int64_t T, int64_t Hq,
+                              const int64_t* positions, const int64_t* slots, const uint64_t* freqs, int R,
+                              int layout, float amplitude, const uint16_t* gamma_q, const uint16_t* gamma_k,
+                              float eps, uint16_t* q_out, int64_t ldqo, int64_t hsqo, const fp8bs_kv_cache* cache,
+                              void* error, void* stream) {
+    const int bad = cache_check(cache);
+    if (bad != FP8BS_OK) return bad;
+    if (Hq < 0 || Hq > kMaxHeads) return FP8BS_ERR_SHAPE;
+    RopeArgs a = {};
+    a.q = q, a.ldq = ldq, a.hsq = hsq, a.k = k, a.ldk = ldk, a.hsk = hsk, a.v = v, a.ldv = ldv, a.hsv = hsv;
+    a.T = T, a.Hq = static_cast<int>(Hq), a.Hk = cache->kv_heads, a.D = cache->head_dim;
+    a.positions = positions, a.freqs = freqs, a.R = R, a.layout = layout, a.amplitude = amplitude;
+    a.gq = gamma_q, a.gk = gamma_k, a.eps = eps;
+    a.qo = q_out, a.ldqo = ldqo, a.hsqo = hsqo;
+    a.slots = slots, a.cache = *cache, a.err = static_cast<uint32_t*>(error), a.append = 1;
+    return run_rope(a, stream);
+}
+
+size_t fp8bs_attn_paged_workspace_bytes(int64_t D, int sm_count) {
+    if (!head_dim_ok(D)) return 0;
+    if (sm_count <= 0 && current_sm_count(&sm_count) != FP8BS_OK) return 0;
+    return sm_count > kMaxCtas ? 0 : attn_workspace_bytes(static_cast<int>(D), sm_count);
+}
+
+int fp8bs_attn_paged(const uint16_t* q, int64_t ldq, int64_t hsq, int64_t T, int64_t Hq,
+                     const fp8bs_kv_cache* cache, const int32_t* block_table, int64_t table_stride, int64_t cols,
+                     int64_t B, const int32_t* cu_q, const int32_t* kv_len, float scale, int64_t window,
+                     uint16_t* o, int64_t ldo, int64_t hso, void* workspace, size_t workspace_bytes, void* stream) {
+    const int bad = cache_check(cache);
+    if (bad != FP8BS_OK) return bad;
+    if (!(scale > 0.0f && scale <= 65536.0f) || window < 0) return FP8BS_ERR_ARG;
+    if (T < 0 || T > kMaxDim || Hq < 1 || Hq > kMaxHeads || Hq % cache->kv_heads != 0 || B < 0 ||
+        B > FP8BS_ATTN_MAX_SEQS || cols < 0 || cols > 0x7FFFFFFF || T * (Hq / cache->kv_heads) > kMaxDim)
+        return FP8BS_ERR_SHAPE;
+    if (T == 0 || B == 0) return FP8BS_OK;
+    if (!q || !o || !block_table || !cu_q || !kv_len || !workspace) return FP8BS_ERR_ARG;
+    const int64_t D = cache->head_dim;
+    if (!stride_ok(ldq) || !stride_ok(hsq) || !stride_ok(ldo) || !stride_ok(hso) || (T > 1 && ldo < D) ||
+        (Hq > 1 && hso < D) || table_stride < cols || table_stride > kMaxStride)
+        return FP8BS_ERR_ARG;
+    if (!heads_aligned(q, ldq, hsq) || !heads_aligned(o, ldo, hso) || !aligned(block_table, 4) || !aligned(cu_q, 4) ||
+        !aligned(kv_len, 4) || !aligned(workspace, 256))
+        return FP8BS_ERR_ALIGN;
+    int sm = 0;
+    const int rc = current_sm_count(&sm);
+    if (rc != FP8BS_OK) return rc;
+    if (sm > kMaxCtas || workspace_bytes < attn_workspace_bytes(static_cast<int>(D), sm)) return FP8BS_ERR_WORKSPACE;
+    const bool codes = cache->kind == FP8BS_KV_E4M3;
+    const int64_t size = codes ? 1 : 2;
+    AttnArgs a = {};
+    a.q = q, a.ldq = ldq, a.hsq = hsq;
+    a.k = static_cast<const uint8_t*>(cache->k), a.v = static_cast<const uint8_t*>(cache->v);
+    a.ks = cache->k_scale, a.vs = cache->v_scale;
+    a.pstride = cache->page_stride * size, a.sstride = cache->slot_stride * size, a.hstride = cache->head_stride * size;
+    a.zpstride = cache->scale_page_stride, a.zsstride = cache->scale_slot_stride, a.zhstride = cache->scale_head_stride;
+    a.pages = cache->pages;
+    while ((1 << a.page_log2) < cache->page_size) ++a.page_log2;
+    a.table = block_table, a.table_stride = table_stride, a.table_cols = static_cast<int>(cols);
+    a.cu = cu_q, a.len = kv_len;
+    a.B = static_cast<int>(B), a.T = static_cast<int>(T);
+    a.Hk = cache->kv_heads, a.G = static_cast<int>(Hq / cache->kv_heads);
+    a.scale_log2 = scale * 1.44269504088896340736f;
+    a.window = static_cast<int>(window < (1 << 30) ? window : (1 << 30));
+    a.o = o, a.ldo = ldo, a.hso = hso;
+    a.err = static_cast<uint32_t*>(workspace);
+    a.ws = static_cast<uint8_t*>(workspace) + kWsErrorBytes;
+    a.D = static_cast<int>(D), a.kind = cache->kind, a.sm_count = sm;
+    return status_of(launch_attn_paged(a, as_stream(stream)));
 }
 
 size_t fp8bs_packed_weight_bytes(int64_t N, int64_t K, int scale_kind) {

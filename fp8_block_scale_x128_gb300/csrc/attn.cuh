@@ -1,0 +1,279 @@
+// Attention block over a paged cache: what its kernels share.  The operators are
+// the norm and rotation of query and key heads (qk_norm_rope.cu), with or
+// without appending to the cache, and attention of new tokens over it
+// (attn_decode.cu, attn_chunk.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstddef>
+#include <cstdint>
+
+#include "internal.cuh"
+#include "ptx.cuh"
+
+namespace fp8bs {
+
+// ---------------------------------------------------------------------------
+// Norm, rotation, append
+// ---------------------------------------------------------------------------
+
+struct RopeArgs {
+    const uint16_t *q, *k, *v;       // v only when appending
+    int64_t ldq, hsq, ldk, hsk, ldv, hsv;  // token and head strides, elements
+    int64_t T;
+    int Hq, Hk, D;
+    const int64_t* positions;
+    const uint64_t* freqs;           // turns a position, in 2^-64
+    int R, layout;
+    float amplitude;
+    const uint16_t *gq, *gk;
+    float eps;
+    uint16_t *qo, *ko;               // ko only without a cache
+    int64_t ldqo, hsqo, ldko, hsko;
+    const int64_t* slots;
+    fp8bs_kv_cache cache;            // used when append
+    uint32_t* err;
+    int append;
+    int sm_count;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Attention: the deal of the work
+// ---------------------------------------------------------------------------
+
+constexpr int kAttnMaxSeqs = FP8BS_ATTN_MAX_SEQS;
+
+struct AttnParams {
+    const uint16_t* q;
+    int64_t ldq, hsq;
+    const uint8_t *k, *v, *ks, *vs;
+    int64_t pstride, sstride, hstride;     // bytes
+    int64_t zpstride, zsstride, zhstride;  // of the scales
+    int64_t pages;
+    int page_log2;
+    const int32_t* table;
+    int64_t table_stride;
+    int table_cols;
+    const int32_t *cu, *len;
+    int B, T, Hk, G;
+    float scale_log2;  // softmax scale * log2(e)
+    int window;        // 0: none
+    uint16_t* o;
+    int64_t ldo, hso;
+    uint32_t* err;
+    uint8_t* ws;  // past the error word
+};
+
+struct AttnArgs : AttnParams {
+    int D, kind;
+    int sm_count;
+};
+size_t attn_workspace_bytes(int D, int sm_count);
+cudaError_t launch_attn_paged(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream);
+
+// The work is dealt out on the device, from the lengths that stand there, so a
+// captured call follows them.  The rows of a sequence are its new tokens times
+// the G query heads of a key head, packed token by token; MT of them make a
+// tile, a tile and a key head an item, BN consecutive keys of an item a unit.
+// All units in the order (sequence, tile, head, key) go to the blocks in equal
+// contiguous shares.  An item that lies in one block's share is finished there;
+// of the others each block leaves (sum, maximum, weighted values) in a slot of
+// its own and a second launch joins them in block order: no atomics, and the
+// same bits each time.
+struct SeqInfo {
+    int q0, nq, kv;
+};
+
+__device__ __forceinline__ SeqInfo attn_seq(const AttnParams& p, int b) {
+    const int c0 = p.cu[b], c1 = p.cu[b + 1], kv = p.len[b];
+    // lengths that do not fit the tensors are cut to them
+    const int most = static_cast<int>(min(static_cast<int64_t>(p.table_cols) << p.page_log2, int64_t(0x7FFFFF00)));
+    SeqInfo s;
+    s.q0 = min(max(c0, 0), p.T);
+    s.nq = max(min(max(c1, 0), p.T) - s.q0, 0);
+    s.kv = min(max(kv, 0), most);
+    if (s.q0 != c0 || s.q0 + s.nq != c1 || s.kv != kv) record_error(p.err, FP8BS_ERR_DEVICE);
+    return s;
+}
+
+// The units [lo, lo + n) of keys that rows [r0, r1) of a sequence need.
+struct TileUnits {
+    int lo, n;
+};
+template <int BN>
+__device__ __forceinline__ TileUnits attn_units(const AttnParams& p, const SeqInfo& s, int r0, int r1) {
+    const int base = s.kv - s.nq;
+    const int hi = base + (r1 - 1) / p.G + 1;  // past the last key seen
+    const int lo = p.window ? max(base + r0 / p.G - p.window + 1, 0) : 0;
+    TileUnits u;
+    u.lo = hi > lo ? lo / BN : 0;
+    u.n = hi > lo ? (hi + BN - 1) / BN - u.lo : 1;  // a tile that sees nothing still writes its rows
+    return u;
+}
+
+// What a block knows of its share.
+struct AttnShare {
+    long long total;     // units of all items
+    int blocks;          // that take part: each has a unit at least
+    long long begin, end;
+    int tile;            // the tile of the first unit,
+    long long before;    // and the units before that tile
+};
+
+struct PlanShared {
+    int first[kAttnMaxSeqs + 1];  // tiles before each sequence
+    long long sum[33];
+    int tile;
+    long long before;
+};
+
+// Inclusive sum over the block; *all: the block's.  Whole block; two barriers.
+template <int THREADS>
+__device__ __forceinline__ long long block_scan(long long v, PlanShared& sh, long long* all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long t = __shfl_up_sync(0xFFFFFFFFu, v, off);
+        if (lane >= off) v += t;
+    }
+    __syncthreads();
+    if (lane == 31) sh.sum[warp] = v;
+    __syncthreads();
+    long long before = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        const long long t = sh.sum[w];
+        if (w < warp) before += t;
+        sum += t;
+    }
+    *all = sum;
+    return before + v;
+}
+
+__device__ __forceinline__ int attn_tile_seq(const PlanShared& sh, int B, int tile) {
+    int lo = 0, hi = B;  // first[lo] <= tile < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sh.first[mid] <= tile) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+template <int MT, int BN>
+__device__ __forceinline__ TileUnits attn_tile_units(const AttnParams& p, const PlanShared& sh, int tile, int b) {
+    const SeqInfo s = attn_seq(p, b);
+    const int r0 = (tile - sh.first[b]) * MT;
+    return attn_units<BN>(p, s, r0, min(r0 + MT, s.nq * p.G));
+}
+
+// Whole block.  sh stays in use by the block.
+template <int MT, int BN, int THREADS>
+__device__ __forceinline__ AttnShare attn_share(const AttnParams& p, PlanShared& sh, int block, int grid) {
+    const int tid = threadIdx.x;
+    AttnShare a;
+    int tiles = 0;
+    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
+        const int b = b0 + tid;
+        long long all;
+        int n = 0;
+        if (b < p.B) n = static_cast<int>((static_cast<long long>(attn_seq(p, b).nq) * p.G + MT - 1) / MT);
+        const int upto = static_cast<int>(block_scan<THREADS>(n, sh, &all));
+        if (b < p.B) sh.first[b + 1] = tiles + upto;
+        tiles += static_cast<int>(all);
+    }
+    if (tid == 0) sh.first[0] = 0, sh.tile = tiles;
+    __syncthreads();
+    long long total = 0, upto = 0;
+    int n = 0;
+    for (int t0 = 0; t0 < tiles; t0 += THREADS) {
+        const int t = t0 + tid;
+        long long all;
+        n = t < tiles ? attn_tile_units<MT, BN>(p, sh, t, attn_tile_seq(sh, p.B, t)).n : 0;
+        upto = block_scan<THREADS>(n, sh, &all);
+        total += all;
+    }
+    a.total = total * p.Hk;
+    a.blocks = static_cast<int>(min(static_cast<long long>(grid), a.total));
+    if (block >= a.blocks) {
+        a.begin = a.end = 0;
+        a.tile = 0;
+        a.before = 0;
+        return a;  // the same for the whole block
+    }
+    a.begin = block * a.total / a.blocks;
+    a.end = (block + 1) * a.total / a.blocks;
+    long long before = 0;
+    for (int t0 = 0; t0 < tiles; t0 += THREADS) {
+        const int t = t0 + tid;
+        long long all;
+        if (tiles > THREADS) {
+            n = t < tiles ? attn_tile_units<MT, BN>(p, sh, t, attn_tile_seq(sh, p.B, t)).n : 0;
+            upto = block_scan<THREADS>(n, sh, &all);
+        } else {
+            all = total;
+        }
+        const long long mine = (before + upto - n) * p.Hk;
+        if (n > 0 && mine <= a.begin && a.begin < mine + static_cast<long long>(n) * p.Hk) sh.tile = t, sh.before = mine;
+        before += all;
+    }
+    __syncthreads();
+    a.tile = sh.tile;
+    a.before = sh.before;
+    return a;
+}
+
+// What a block leaves for the second launch about an item that it begins and
+// does not finish.
+struct AttnSplit {
+    int32_t rows;   // 0: none
+    int32_t q0;     // the sequence's first token
+    int32_t row0;   // the item's first packed row
+    int32_t head;   // key head
+    int32_t last;   // the block that finishes it
+    int32_t pad[3];
+};
+
+// Workspace past the error word: a record a block, then two slots a block:
+// slot 0 for an item begun elsewhere, slot 1 for one begun here.  A slot holds
+// values [rows][D], maxima [rows] (in units of log2) and sums [rows], all fp32.
+__host__ __device__ constexpr size_t attn_slot_floats(int MT, int D) { return static_cast<size_t>(MT) * (D + 2); }
+__host__ __device__ constexpr size_t attn_records_bytes(int grid) {
+    return (static_cast<size_t>(grid) * sizeof(AttnSplit) + 255) / 256 * 256;
+}
+__device__ __forceinline__ float* attn_slot(const AttnParams& p, int grid, int MT, int D, int block, int slot) {
+    return reinterpret_cast<float*>(p.ws + attn_records_bytes(grid)) +
+           (static_cast<size_t>(block) * 2 + slot) * attn_slot_floats(MT, D);
+}
+
+// Key position -> byte offset of its row for one head; false where the table
+// names no page of the cache (recorded).
+__device__ __forceinline__ bool attn_page(const AttnParams& p, const int32_t* table, int j, int* page) {
+    *page = table[j >> p.page_log2];
+    if (*page < 0 || *page >= p.pages) {
+        record_error(p.err, FP8BS_ERR_DEVICE);
+        return false;
+    }
+    return true;
+}
+
+// Raises a kernel's dynamic shared memory limit to `bytes`, once per kernel and device.
+template <typename K>
+cudaError_t attn_allow_shared(K* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done.load(std::memory_order_relaxed) >> dev & 1) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    return e;
+}
+
+cudaError_t launch_attn_join(const AttnArgs& a, int MT, int grid, cudaStream_t stream);
+
+}  // namespace fp8bs

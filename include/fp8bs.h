@@ -479,6 +479,168 @@ int fp8bs_moe_w4a16(const uint16_t* x, int64_t M, int64_t H, int64_t ldx, const 
                     const uint8_t* w2, const void* s2, int64_t E, int64_t I, int format, int group,
                     uint16_t* y, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* The attention block: norms and rotation of heads, a paged cache of keys   */
+/* and values, attention of new tokens over it                               */
+/* ------------------------------------------------------------------------ */
+
+/* How rotated dimensions pair up. */
+typedef enum {
+    FP8BS_ROPE_HALF = 0,        /* dimension i with i + R/2  */
+    FP8BS_ROPE_INTERLEAVED = 1, /* dimension 2i with 2i + 1  */
+} fp8bs_rope_layout;
+
+/* How frequencies are changed for contexts longer than those of training. */
+typedef enum {
+    FP8BS_ROPE_PLAIN = 0,    /* not                                             */
+    FP8BS_ROPE_LINEAR = 1,   /* all divided by factor                           */
+    FP8BS_ROPE_BY_PARTS = 2, /* by how often a pair turns in the original length */
+} fp8bs_rope_scaling;
+
+/* Rotary frequencies, computed on the HOST: pair i of R/2 turns by the angle
+ * f_i a position, f_i = theta^(-2i/R), changed by `scaling`:
+ *   LINEAR   : f_i / factor.
+ *   BY_PARTS : f_i (1 - s_i) + f_i / factor s_i, s_i = clamp((i - low) / (high - low),
+ *              0, 1), low = max(floor(n(beta_fast)), 0), high = min(ceil(n(beta_slow)),
+ *              R - 1) (high - low at least 0.001), n(b) = R ln(original_length /
+ *              (2 pi b)) / (2 ln theta): the pairs that turn more than beta_fast times
+ *              in the original length keep their frequency, those that turn less than
+ *              beta_slow times have it divided (B. Peng et al., "YaRN: Efficient
+ *              Context Window Extension of Large Language Models", 2023, "NTK-by-parts").
+ *   rotary_dim : R, even, 2 .. 256.   theta : > 1, finite.
+ *   factor     : >= 1 (LINEAR, BY_PARTS); original_length > 0, beta_fast > beta_slow
+ *                > 0 (BY_PARTS); otherwise not looked at.
+ *   freqs      : HOST uint64 [R/2]: f_i / (2 pi) in units of 2^-64 turns.  position *
+ *                freqs[i] modulo 2^64 is then the angle's exact fraction of a turn,
+ *                for any int64 position; the table's own rounding is about 2^-52 of f_i
+ *                and 2^-65 turns.
+ *   amplitude  : HOST float, may be NULL: the factor of rotated values that goes with
+ *                it, 0.1 ln(factor) + 1 for BY_PARTS and else 1.
+ * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE (rotary_dim). */
+int fp8bs_rope_freqs(int rotary_dim, double theta, int scaling, double factor, double original_length,
+                     double beta_fast, double beta_slow, uint64_t* freqs, float* amplitude);
+
+/* Norm and rotation of query and key heads in one pass, for each token t and head h:
+ *   y = x / sqrt(mean x^2 + eps) * gamma   (gamma of the queries or the keys; y = x
+ *                                           where that is NULL)
+ *   (u, w) -> amplitude (u cos a - w sin a, w cos a + u sin a) for the R/2 pairs of
+ *             the first R dimensions, a = positions[t] f_i; the others stay
+ * in fp32 (the angle as an exact fraction of a turn, rounded to fp32), rounded once
+ * to bf16.
+ *   q, k       : bf16 [T, heads, D] with token strides ldq, ldk and head strides hsq,
+ *                hsk in elements, D contiguous: slices of a projection's rows do.
+ *   T          : tokens, 0 .. 2^24 (0 enqueues nothing).
+ *   Hq, Hk     : heads, 0 .. 1024 each, one at least; the tensors of none may be NULL.
+ *   D          : 64, 128 or 256.
+ *   positions  : int64 [T], 8-byte aligned (not read where R is 0).
+ *   freqs      : DEVICE uint64 [R/2] from fp8bs_rope_freqs, 8-byte aligned.
+ *   R          : 0 (no rotation) .. D, even; a multiple of 16 in the HALF layout.
+ *   amplitude  : finite.   gamma_q, gamma_k : bf16 [D], 16-byte aligned, or NULL.
+ *   eps        : finite, >= 0.  A row of zeros with eps 0 stays zeros.
+ *   q_out, k_out : bf16 [T, heads, D] with strides of their own; may be q and k
+ *                themselves with the same strides, else apart from them.
+ * All pointers 16-byte aligned and all strides multiples of 8, where not said
+ * otherwise.  One launch, dependent on its predecessor (programmatic dependent
+ * launch), for which it waits before it touches memory.
+ * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN, FP8BS_ERR_CUDA. */
+int fp8bs_qk_norm_rope(const uint16_t* q, int64_t ldq, int64_t hsq, const uint16_t* k, int64_t ldk, int64_t hsk,
+                       int64_t T, int64_t Hq, int64_t Hk, int64_t D, const int64_t* positions,
+                       const uint64_t* freqs, int R, int layout, float amplitude, const uint16_t* gamma_q,
+                       const uint16_t* gamma_k, float eps, uint16_t* q_out, int64_t ldqo, int64_t hsqo,
+                       uint16_t* k_out, int64_t ldko, int64_t hsko, void* stream);
+
+/* What a cache holds. */
+typedef enum {
+    FP8BS_KV_BF16 = 0, /* bf16                                                    */
+    FP8BS_KV_E4M3 = 1, /* e4m3fn codes, one e8m0 scale byte for each row of a head */
+} fp8bs_kv_kind;
+
+/* A paged cache of keys and values, described on the HOST (read during a call only).
+ * Row (page, slot, head) of k and of v is D contiguous elements at
+ *   page * page_stride + slot * slot_stride + head * head_stride
+ * elements from the base; its scale byte b, for 2^(b - 127), likewise in k_scale and
+ * v_scale.  Any order of the three axes does; rows must not overlap.  A row's scale
+ * byte is that of fp8bs_quant's ue8m0 rule over its D values, its codes e4m3fn
+ * RNE-saturated of value / scale; a row with an infinity or a NaN has byte 255 and
+ * stands for NaNs. */
+typedef struct {
+    void* k;
+    void* v;              /* bf16 or codes, 16-byte aligned                       */
+    uint8_t* k_scale;
+    uint8_t* v_scale;     /* E4M3 only                                            */
+    int32_t kind;         /* fp8bs_kv_kind                                        */
+    int32_t head_dim;     /* D: 64, 128 or 256                                    */
+    int32_t kv_heads;     /* 1 .. 1024                                            */
+    int32_t page_size;    /* tokens a page: a power of two, 1 .. 65536            */
+    int64_t pages;        /* 1 .. 2^31 - 1                                        */
+    int64_t page_stride, slot_stride, head_stride; /* multiples of 8 (bf16) or 16 */
+    int64_t scale_page_stride, scale_slot_stride, scale_head_stride; /* E4M3 only */
+} fp8bs_kv_cache;
+
+/* fp8bs_qk_norm_rope, the key heads going into a cache with the value heads beside
+ * them: token t's into slot slots[t], which counts page * page_size + slot.  Keys are
+ * rounded from fp32 to the cache's kind once; values are copied, or rounded from bf16.
+ *   v      : bf16 [T, cache->kv_heads, D], strides ldv, hsv; aligned as q and k.
+ *   Hq     : 0 .. 1024: 0 only appends (q and q_out may then be NULL).
+ *   slots  : int64 [T], 8-byte aligned, each slot at most once.  A negative one writes
+ *            nothing (a padded token; its queries are still written), one past the
+ *            cache neither and records FP8BS_ERR_DEVICE.
+ *   error  : a device word, 256-byte aligned, zero before the first call (such as the
+ *            first of a workspace), which fp8bs_check_error reads; or NULL.
+ * The cache is apart from q, k, v and q_out.  One launch, as fp8bs_qk_norm_rope.
+ * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN, FP8BS_ERR_CUDA. */
+int fp8bs_qk_norm_rope_append(const uint16_t* q, int64_t ldq, int64_t hsq, const uint16_t* k, int64_t ldk,
+                              int64_t hsk, const uint16_t* v, int64_t ldv, int64_t hsv, int64_t T, int64_t Hq,
+                              const int64_t* positions, const int64_t* slots, const uint64_t* freqs, int R,
+                              int layout, float amplitude, const uint16_t* gamma_q, const uint16_t* gamma_k,
+                              float eps, uint16_t* q_out, int64_t ldqo, int64_t hsqo, const fp8bs_kv_cache* cache,
+                              void* error, void* stream);
+
+#define FP8BS_ATTN_MAX_SEQS 1024 /* sequences of a call */
+
+/* Workspace bytes of fp8bs_attn_paged for heads of D (0 for an unsupported D), on
+ * sm_count multiprocessors (0: the current device's). */
+size_t fp8bs_attn_paged_workspace_bytes(int64_t D, int sm_count);
+
+/* Attention of each sequence's newest tokens over its pages.  Sequence b has the
+ * query rows cu_q[b] .. cu_q[b + 1] - 1 and kv_len[b] tokens in the cache, the new
+ * ones at their end: with n rows, row i stands at place kv_len[b] - n + i and sees the
+ * keys j <= place, with a window only those j > place - window.  For each of its
+ * query heads h, with key head h / (Hq / kv_heads):
+ *   o = sum_j w_j v_j,  w = softmax_j(scale q . k_j)
+ * Scores, maxima, sums and products are kept in fp32; see the sources for how weights
+ * enter the product with the values.  A row that sees no key gives zeros.
+ *   q           : bf16 [T, Hq, D], strides ldq, hsq; o: bf16 the same, strides ldo, hso.
+ *                 Pointers 16-byte aligned, strides multiples of 8; o apart from all
+ *                 inputs.  Rows outside all sequences are left as they were.
+ *   T           : rows of q and o, 0 .. 2^24 (0 enqueues nothing).
+ *   Hq          : a multiple of the cache's kv_heads, up to 1024; T * Hq / kv_heads up
+ *                 to 2^24.
+ *   block_table : int32 [B, cols], row stride table_stride >= cols: the pages of each
+ *                 sequence in order; entries past its length are not read.
+ *   B           : sequences, 0 .. FP8BS_ATTN_MAX_SEQS (0 enqueues nothing).
+ *   cu_q        : int32 [B + 1], ascending within 0 .. T.   kv_len : int32 [B].
+ *                 (All three 4-byte aligned; they are read on the device, so a
+ *                 captured call follows their values.)
+ *   scale       : > 0, up to 65536.   window : 0 (none) or the keys that a row sees at most.
+ *   workspace   : fp8bs_attn_paged_workspace_bytes bytes, 256-byte aligned; its first
+ *                 word zero before the first call; fp8bs_check_error reads it.  Not to
+ *                 be used by two calls that can run at the same time.
+ * Lengths that do not fit T or the table, and pages that the cache does not have,
+ * record FP8BS_ERR_DEVICE; the rows of such a sequence are not specified, and nothing
+ * outside the tensors is touched.  Masked keys and values have no part in a row,
+ * whatever they hold; an infinity or a NaN that a row sees makes its results NaN or
+ * infinite.  In a cache of codes q and the values are below 2^63 in
+ * magnitude.  Results are deterministic, and a row's do not depend on whether other
+ * heads or sequences hold NaNs.  Two launches, dependent on their predecessors,
+ * for which they wait before they touch memory.
+ * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN, FP8BS_ERR_WORKSPACE,
+ * FP8BS_ERR_CUDA. */
+int fp8bs_attn_paged(const uint16_t* q, int64_t ldq, int64_t hsq, int64_t T, int64_t Hq,
+                     const fp8bs_kv_cache* cache, const int32_t* block_table, int64_t table_stride, int64_t cols,
+                     int64_t B, const int32_t* cu_q, const int32_t* kv_len, float scale, int64_t window,
+                     uint16_t* o, int64_t ldo, int64_t hso, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Limits of fp8bs_gemm_fused_static's fixed scratch. */
 #define FP8BS_STATIC_MAX_K 16384  /* largest K it accepts                   */
 #define FP8BS_STATIC_MAX_SMS 160  /* CTAs it uses at most (grid cap)        */
