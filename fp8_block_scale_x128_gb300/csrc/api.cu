@@ -576,6 +576,7 @@ int fp8bs_attn_paged(const uint16_t* q, int64_t ldq, int64_t hsq, int64_t T, int
     a.o = o, a.ldo = ldo, a.hso = hso;
     a.err = static_cast<uint32_t*>(workspace);
     a.ws = static_cast<uint8_t*>(workspace) + kWsErrorBytes;
+    a.timeout_cycles = timeout_cycles();
     a.D = static_cast<int>(D), a.kind = cache->kind, a.sm_count = sm;
     return status_of(launch_attn_paged(a, as_stream(stream)));
 }

@@ -65,6 +65,7 @@ struct AttnParams {
     int64_t ldo, hso;
     uint32_t* err;
     uint8_t* ws;  // past the error word
+    long long timeout_cycles;  // of a wait inside the kernel
 };
 
 struct AttnArgs : AttnParams {
@@ -74,6 +75,8 @@ struct AttnArgs : AttnParams {
 size_t attn_workspace_bytes(int D, int sm_count);
 cudaError_t launch_attn_paged(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_chunk(const AttnArgs& a, cudaStream_t stream);
+size_t attn_chunk_slot_floats(int D);
 
 // The work is dealt out on the device, from the lengths that stand there, so a
 // captured call follows them.  The rows of a sequence are its new tokens times
@@ -227,6 +230,44 @@ __device__ __forceinline__ AttnShare attn_share(const AttnParams& p, PlanShared&
     return a;
 }
 
+// The place in the deal of the work: an item and a unit of it.
+template <int ROWS, int UNIT>
+struct Cursor {
+    int tile, b, head, unit, n, lo;  // unit: within the item
+    SeqInfo s;
+    int row0, rows;  // packed rows of the tile
+    int first, past;  // keys that some row sees
+
+    __device__ __forceinline__ void enter(const AttnParams& p, const PlanShared& sh) {
+        s = attn_seq(p, b);
+        row0 = (tile - sh.first[b]) * ROWS;
+        rows = min(ROWS, s.nq * p.G - row0);
+        const TileUnits u = attn_units<UNIT>(p, s, row0, row0 + rows);
+        n = u.n, lo = u.lo;
+        const int base = s.kv - s.nq;
+        past = base + (row0 + rows - 1) / p.G + 1;
+        first = p.window ? max(base + row0 / p.G - p.window + 1, 0) : 0;
+    }
+    __device__ __forceinline__ void start(const AttnParams& p, const PlanShared& sh, const AttnShare& a) {
+        tile = a.tile;
+        b = attn_tile_seq(sh, p.B, tile);
+        enter(p, sh);
+        const long long x = a.begin - a.before;
+        head = static_cast<int>(x / n);
+        unit = static_cast<int>(x - static_cast<long long>(head) * n);
+    }
+    __device__ __forceinline__ void next(const AttnParams& p, const PlanShared& sh) {
+        if (++unit < n) return;
+        unit = 0;
+        if (++head < p.Hk) return;
+        head = 0;
+        ++tile;
+        if (tile >= sh.first[p.B]) return;  // past the last item
+        while (tile >= sh.first[b + 1]) ++b;
+        enter(p, sh);
+    }
+};
+
 // What a block leaves for the second launch about an item that it begins and
 // does not finish.
 struct AttnSplit {
@@ -260,6 +301,38 @@ __device__ __forceinline__ bool attn_page(const AttnParams& p, const int32_t* ta
     }
     return true;
 }
+
+// ---------------------------------------------------------------------------
+// Small device pieces
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 16 bytes, or zeros where !there (nothing is read then).
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Even and odd bytes of a word as two pairs of bf16 numbers, code values * 2^-120.
+__device__ __forceinline__ uint32_t codes_even(uint32_t w) {
+    return ((w << 8) & 0x80008000u) | ((w << 4) & 0x07F007F0u);
+}
+__device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return (w & 0x80008000u) | ((w >> 4) & 0x07F007F0u); }
 
 // Raises a kernel's dynamic shared memory limit to `bytes`, once per kernel and device.
 template <typename K>

@@ -1,0 +1,754 @@
+// Attention of many new tokens a sequence over a paged cache, on the 5th
+// generation tensor core (attn.cuh says how the work is dealt out).
+//
+// A tile is 256 rows (128 with heads of 256), in streams of 128 with their own
+// accumulators in tensor memory.  Warps have one task each:
+//   loaders  copy a unit's keys, then its values, into a ring of shared memory
+//            tiles in the operand layout (128-byte swizzle; a row's 64 dimensions are
+//            a line, so keys are a K-major operand and values an MN-major one of the
+//            same layout); codes become bf16 on the way, times their scale, exactly;
+//   one warp issues the products: scores S = Q K^T into tensor memory, then, once
+//            the weights are there, O += P V with P as the operand in tensor memory
+//            in the place of its scores;
+//   a warpgroup a stream takes its rows' softmax, a thread a row: no shuffles.
+// Two streams (heads up to 128) take turns on the tensor core: while one's weights
+// are computed, the other's products run.  One stream (heads of 256) has two score
+// buffers, and the next unit's scores are under way during a unit's softmax.
+//
+// Weights are rounded to bf16 once (2^-8 of each, at most; they average out) and
+// summed before that in fp32.  The maximum that they are taken against may lag by 8
+// in units of log2, so that outputs are rescaled in tensor memory only rarely.
+//
+// A value that is not finite and that some row of its unit masks would reach that row
+// as zero times it.  In units with masks the loaders put zeros in the place of such
+// values and mark the item; its rows then add those that they see at their end.
+#include <cuda_bf16.h>
+
+#include "attn.cuh"
+#include "w4.cuh"
+
+namespace fp8bs {
+namespace {
+
+constexpr int kRows = 128;  // of a stream
+constexpr float kLag = 8.0f;
+constexpr int kMarks = 8;
+
+template <int D, int KIND>
+struct Cfg {
+    static constexpr bool kCodes = KIND == FP8BS_KV_E4M3;
+    static constexpr int kStreams = D == 256 ? 1 : 2;
+    static constexpr int kTile = kStreams * kRows;
+    static constexpr int kKeys = D == 256 ? 64 : 128;  // of a unit
+    static constexpr int kSoft = kStreams * 4;         // softmax warps
+    static constexpr int kThreads = 384;
+    static constexpr int kLoadWarps = kThreads / 32 - kSoft - 1;
+    static constexpr int kLoaders = kLoadWarps * 32;
+    static constexpr int kTileBytes = kKeys * D * 2;
+    static constexpr int kStages = 4;
+    static constexpr int kQBytes = kTile * D * 2;
+    static constexpr int kSmem = kQBytes + kStages * kTileBytes + 1024;
+    static constexpr uint32_t kOut = 256;  // first column of the outputs
+};
+
+struct Shared {
+    PlanShared plan;
+    uint64_t full[4], empty[4], scores[2], weights[2], joined[2], query[2], drained;
+    long long row_off[3][128];      // of a unit's rows; three units, as loaders may be one apart
+    uint8_t row_scale[3][2][128];
+    uint32_t tmem;
+    int dead;
+    int mark[kMarks];
+};
+
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
+        : "memory");
+}
+
+// Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B bf16 (bits 7-9,
+// 10-12 = 1), A K-major (bit 15 = 0), B's major (bit 16: 1 MN-major), N >> 3 in bits
+// 17-22, M >> 4 in bits 24-28.
+constexpr uint32_t idesc_bf16(uint32_t n, uint32_t b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// smem_desc_sw128 with the leading byte offset that an MN-major operand has: from
+// one 64-element wide part to the next.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lead) {
+    uint64_t d = ptx::smem_desc_sw128(saddr) & ~(uint64_t(0x3FFF) << 16);
+    return d | static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+        "%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(a)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+        "%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(a)
+        : "memory");
+}
+
+// Waits for a phase, with a limit; false when it ran out here or anywhere in the
+// block.  (Out of line: the loop is cold.)
+__device__ __noinline__ bool wait_slow(Shared* sh, uint64_t* bar, uint32_t parity, long long limit, uint32_t* err) {
+    const long long began = clock64();
+    while (!ptx::mbar_test(bar, parity)) {
+        if (*reinterpret_cast<volatile int*>(&sh->dead)) return false;
+        const long long spent = clock64() - began;
+        if (spent > limit) {
+            record_error(err, FP8BS_ERR_TIMEOUT);
+            *reinterpret_cast<volatile int*>(&sh->dead) = 1;
+            return false;
+        }
+        if (spent > 4000) __nanosleep(64);
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity, const AttnParams& p) {
+    if (ptx::mbar_test(bar, parity)) return true;
+    return wait_slow(&sh, bar, parity, p.timeout_cycles, p.err);
+}
+
+// 16 codes -> 16 bf16 numbers times 2^(b - 127) (NaN for b = 255).
+__device__ __forceinline__ void widen(const uint4& c, uint32_t scale, uint4& lo, uint4& hi) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t e = codes_even(w[i]), o = codes_odd(w[i]);
+        r[2 * i] = __byte_perm(e, o, 0x5410), r[2 * i + 1] = __byte_perm(e, o, 0x7632);
+    }
+    // the code's 2^-120 and the scale in one factor; above 2^7 in two
+    const uint32_t first = scale == 255u ? 0x7FC0u : min(scale + 120u, 254u) << 7;
+    const __nv_bfloat162 f = __halves2bfloat162(__ushort_as_bfloat16(static_cast<unsigned short>(first)),
+                                                __ushort_as_bfloat16(static_cast<unsigned short>(first)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<__nv_bfloat162*>(&r[i]) = __hmul2_rn(*reinterpret_cast<__nv_bfloat162*>(&r[i]), f);
+    if (scale > 134u && scale != 255u) {
+        const unsigned short more = static_cast<unsigned short>((scale - 134u + 127u) << 7);
+        const __nv_bfloat162 g = __halves2bfloat162(__ushort_as_bfloat16(more), __ushort_as_bfloat16(more));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<__nv_bfloat162*>(&r[i]) = __hmul2_rn(*reinterpret_cast<__nv_bfloat162*>(&r[i]), g);
+    }
+    lo = make_uint4(r[0], r[1], r[2], r[3]);
+    hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+__device__ __forceinline__ bool odd_pair(uint32_t w) {
+    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+// Whether every row of the item sees every key of the unit at j0.
+template <typename Place, int KEYS>
+__device__ __forceinline__ bool sees_all(const AttnParams& p, const Place& at, int j0) {
+    return j0 + KEYS <= at.s.kv - at.s.nq + at.row0 / p.G + 1 && (p.window == 0 || j0 >= at.past - p.window);
+}
+
+template <int D, int KIND>
+__device__ __forceinline__ void load_units(const AttnParams& p, Shared& sh, const AttnShare& share, uint8_t* ring) {
+    using C = Cfg<D, KIND>;
+    using Place = Cursor<C::kTile, C::kKeys>;
+    constexpr int kPer = C::kCodes ? D / 16 : D / 8;  // 16-byte pieces of a row in the cache
+    constexpr int kRowStep = C::kLoaders / kPer;       // rows between a thread's pieces
+    constexpr int kMine = (C::kKeys + kRowStep - 1) / kRowStep;
+    constexpr int kLook = (C::kKeys + C::kLoaders - 1) / C::kLoaders;
+    const int tid = threadIdx.x - (C::kSoft + 1) * 32;
+    // threads past the last whole row copy nothing: their first row is past the unit
+    const int row0 = tid < kRowStep * kPer ? tid / kPer : C::kKeys, piece = tid % kPer;
+    const long long units = share.end - share.begin;
+    Place at;
+    at.start(p, sh.plan, share);
+    bool alive = true;
+
+    // A unit's rows, looked up a unit ahead and in three steps, so that none of them
+    // waits for the one before: pages, then offsets and scales, then shared memory.
+    int page[kLook];
+    long long off[kLook];
+    uint32_t zk[kLook], zv[kLook];
+    auto find = [&] {
+#pragma unroll
+        for (int i = 0; i < kLook; ++i) {
+            const int r = tid + i * C::kLoaders, j = (at.lo + at.unit) * C::kKeys + r;
+            page[i] = -1;
+            if (r < C::kKeys && j >= at.first && j < at.past) {
+                int id;
+                if (attn_page(p, p.table + at.b * p.table_stride, j, &id)) page[i] = id;
+            }
+        }
+    };
+    auto locate = [&] {
+#pragma unroll
+        for (int i = 0; i < kLook; ++i) {
+            const int j = (at.lo + at.unit) * C::kKeys + tid + i * C::kLoaders, s = j & ((1 << p.page_log2) - 1);
+            off[i] = -1;
+            zk[i] = zv[i] = 127;
+            if (page[i] >= 0) {
+                off[i] = page[i] * p.pstride + s * p.sstride + at.head * p.hstride;
+                if (C::kCodes) {
+                    const long long z = page[i] * p.zpstride + s * p.zsstride + at.head * p.zhstride;
+                    zk[i] = p.ks[z], zv[i] = p.vs[z];
+                }
+            }
+        }
+    };
+    auto keep = [&](int slot) {
+#pragma unroll
+        for (int i = 0; i < kLook; ++i) {
+            const int r = tid + i * C::kLoaders;
+            if (r < C::kKeys) {
+                sh.row_off[slot][r] = off[i];
+                if (C::kCodes) {
+                    sh.row_scale[slot][0][r] = static_cast<uint8_t>(zk[i]);
+                    sh.row_scale[slot][1][r] = static_cast<uint8_t>(zv[i]);
+                }
+            }
+        }
+    };
+    auto room = [&](uint32_t fill) {
+        if (alive && fill >= C::kStages)
+            alive = wait(sh, &sh.empty[fill % C::kStages], ((fill / C::kStages) - 1) & 1, p);
+    };
+    auto place16 = [&](uint8_t* tile, int r, int c) {  // 16-byte piece c of row r of a tile
+        return tile + (c >> 3) * (C::kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    };
+
+    find();
+    locate();
+    keep(0);
+    ptx::named_sync(1, C::kLoaders);
+
+    int item = 0, slot = 0, check = 0;
+    uint32_t fill = 0;
+
+    if constexpr (!C::kCodes) {
+        auto copy = [&](const uint8_t* src) {
+            room(fill);
+            uint8_t* tile = ring + fill % C::kStages * C::kTileBytes;
+            if (alive) {
+#pragma unroll 4
+                for (int i = 0; i < kMine; ++i) {
+                    const int r = row0 + i * kRowStep;
+                    if (r < C::kKeys) {
+                        const long long o = sh.row_off[slot][r];
+                        cp_async16_zfill(ptx::smem_addr(place16(tile, r, piece)), src + (o >= 0 ? o + 16 * piece : 0), o >= 0);
+                    }
+                }
+            }
+            cp_commit();
+        };
+        // the tile before the newest has arrived: values with masks are looked through
+        auto hand_over = [&](uint32_t f) {
+            uint8_t* tile = ring + f % C::kStages * C::kTileBytes;
+            if (alive && check) {
+                for (int r = row0; r < C::kKeys; r += kRowStep) {
+                    uint4* q = reinterpret_cast<uint4*>(place16(tile, r, piece));
+                    uint32_t w[4] = {q->x, q->y, q->z, q->w};
+                    bool found = false;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        found |= odd_pair(w[c]);
+                        if ((w[c] & 0x7F80u) == 0x7F80u) w[c] &= 0xFFFF0000u;
+                        if ((w[c] & 0x7F800000u) == 0x7F800000u) w[c] &= 0x0000FFFFu;
+                    }
+                    if (found) {
+                        *q = make_uint4(w[0], w[1], w[2], w[3]);
+                        sh.mark[(check - 1) & (kMarks - 1)] = check;
+                    }
+                }
+            }
+            if (alive) {
+                ptx::fence_proxy_async_smem();
+                ptx::mbar_arrive(&sh.full[f % C::kStages]);
+            }
+        };
+#pragma unroll 1
+        for (long long u = 0; u < units; ++u) {
+            const int tag = sees_all<Place, C::kKeys>(p, at, (at.lo + at.unit) * C::kKeys) ? 0 : item + 1;
+            const bool more = u + 1 < units;
+            if (more) {
+                const bool last = at.unit + 1 == at.n;
+                at.next(p, sh.plan);
+                item += last;
+                find();
+            }
+            copy(p.k);
+            if (more) locate();
+            if (fill > 0) {
+                cp_wait<1>();
+                hand_over(fill - 1);
+            }
+            ++fill;
+            copy(p.v);
+            const int next = slot == 2 ? 0 : slot + 1;
+            if (more) keep(next);
+            cp_wait<1>();
+            check = 0;
+            hand_over(fill - 1);
+            check = tag;
+            ++fill;
+            ptx::named_sync(1, C::kLoaders);
+            slot = next;
+        }
+        cp_wait<0>();
+        hand_over(fill - 1);
+    } else {
+        uint4 keys[kMine], values[kMine];
+        auto read = [&](uint4(&raw)[kMine], const uint8_t* src) {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int r = row0 + i * kRowStep;
+                raw[i] = make_uint4(0, 0, 0, 0);
+                if (r < C::kKeys) {
+                    const long long o = sh.row_off[slot][r];
+                    if (o >= 0) raw[i] = *reinterpret_cast<const uint4*>(src + o + 16 * piece);
+                }
+            }
+        };
+        auto write = [&](uint4(&raw)[kMine], int kv, int from, int tag) {
+            room(fill);
+            uint8_t* tile = ring + fill % C::kStages * C::kTileBytes;
+            if (alive) {
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    const int r = row0 + i * kRowStep;
+                    if (r < C::kKeys) {
+                        uint32_t scale = sh.row_scale[from][kv][r];
+                        if (tag && scale == 255u) {
+                            scale = 127u;
+                            raw[i] = make_uint4(0, 0, 0, 0);
+                            sh.mark[(tag - 1) & (kMarks - 1)] = tag;
+                        }
+                        uint4 lo, hi;
+                        widen(raw[i], scale, lo, hi);
+                        *reinterpret_cast<uint4*>(place16(tile, r, 2 * piece)) = lo;
+                        *reinterpret_cast<uint4*>(place16(tile, r, 2 * piece + 1)) = hi;
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                ptx::mbar_arrive(&sh.full[fill % C::kStages]);
+            }
+            ++fill;
+        };
+        read(keys, p.k);
+#pragma unroll 1
+        for (long long u = 0; u < units; ++u) {
+            const int tag = sees_all<Place, C::kKeys>(p, at, (at.lo + at.unit) * C::kKeys) ? 0 : item + 1;
+            const bool more = u + 1 < units;
+            if (more) {
+                const bool last = at.unit + 1 == at.n;
+                at.next(p, sh.plan);
+                item += last;
+                find();
+            }
+            read(values, p.v);
+            if (more) locate();
+            write(keys, 0, slot, 0);
+            const int now = slot, next = slot == 2 ? 0 : slot + 1;
+            if (more) keep(next);
+            ptx::named_sync(1, C::kLoaders);
+            slot = next;
+            if (more) read(keys, p.k);
+            write(values, 1, now, tag);
+        }
+    }
+}
+
+template <int D, int KIND>
+__device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, const AttnShare& share, uint32_t query,
+                                               uint32_t ring) {
+    using C = Cfg<D, KIND>;
+    using Place = Cursor<C::kTile, C::kKeys>;
+    constexpr uint32_t kScoreDesc = idesc_bf16(C::kKeys, 0), kValueDesc = idesc_bf16(D, 1);
+    const long long units = share.end - share.begin;
+    Place at;
+    at.start(p, sh.plan, share);
+    uint32_t items = 0;  // whose queries have been waited for
+    auto tile = [&](uint32_t fill) { return ring + fill % C::kStages * C::kTileBytes; };
+    const uint32_t tmem = sh.tmem;
+    // the whole warp goes on together, or returns together
+    auto await = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(sh, bar, parity, p)) != 0; };
+    auto full = [&](uint32_t fill) { return await(&sh.full[fill % C::kStages], (fill / C::kStages) & 1); };
+
+    auto scores = [&](int stream, int buffer, uint32_t keys, int rows) {
+        if (rows > stream * kRows) {
+            const uint32_t q = query + stream * kRows * D * 2;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t in = (k & 3) * 32;
+                mma_f16_ss(tmem + buffer * 128, ptx::smem_desc_sw128(q + (k >> 2) * (kRows * 128) + in),
+                           ptx::smem_desc_sw128(keys + (k >> 2) * (C::kKeys * 128) + in), kScoreDesc, k > 0);
+            }
+        }
+        ptx::mma_commit_warp(&sh.scores[buffer]);
+    };
+    auto values = [&](int stream, int buffer, uint32_t vals, int rows, bool first) {
+        if (rows > stream * kRows) {
+#pragma unroll
+            for (int k = 0; k < C::kKeys / 16; ++k)
+                mma_f16_ts(tmem + C::kOut + stream * D, tmem + buffer * 128 + k * 8,
+                           desc_mn(vals + k * 2048, C::kKeys * 128), kValueDesc, !(first && k == 0));
+        }
+        ptx::mma_commit_warp(&sh.joined[stream]);
+    };
+
+    bool first = true;  // the unit is its item's first here
+    int rows = at.rows;
+    if (!await(&sh.query[0], 0) || (C::kStreams == 2 && !await(&sh.query[1], 0)) || !full(0)) return;
+    ptx::tc_fence_after();
+    for (int s = 0; s < C::kStreams; ++s) scores(s, s, tile(0), rows);
+    ptx::mma_commit_warp(&sh.empty[0]);
+#pragma unroll 1
+    for (long long u = 0; u < units; ++u) {
+        const uint32_t fv = 2 * static_cast<uint32_t>(u) + 1, fk = fv + 1;
+        const bool more = u + 1 < units, last = at.unit + 1 == at.n;
+        const int rows_now = rows;
+        if (more) {
+            at.next(p, sh.plan);
+            rows = at.rows;
+            items += last;
+        }
+        if constexpr (C::kStreams == 2) {
+            if (!full(fv)) return;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (!await(&sh.weights[s], u & 1)) return;
+                ptx::tc_fence_after();
+                values(s, s, tile(fv), rows_now, first);
+                if (s == 1) ptx::mma_commit_warp(&sh.empty[fv % C::kStages]);
+                if (more) {
+                    if (last && !await(&sh.query[s], items & 1)) return;
+                    if (s == 0 && !full(fk)) return;
+                    ptx::tc_fence_after();
+                    scores(s, s, tile(fk), rows);
+                    if (s == 1) ptx::mma_commit_warp(&sh.empty[fk % C::kStages]);
+                }
+            }
+        } else {
+            const int b = u & 1;
+            if (more) {
+                if (last && !await(&sh.query[0], items & 1)) return;
+                if (!full(fk)) return;
+                ptx::tc_fence_after();
+                scores(0, b ^ 1, tile(fk), rows);
+                ptx::mma_commit_warp(&sh.empty[fk % C::kStages]);
+            }
+            if (!full(fv) || !await(&sh.weights[b], (u >> 1) & 1)) return;
+            ptx::tc_fence_after();
+            values(0, b, tile(fv), rows_now, first);
+            ptx::mma_commit_warp(&sh.empty[fv % C::kStages]);
+        }
+        first = last;
+    }
+}
+
+template <int D, int KIND>
+__device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, const AttnShare& share, uint8_t* query) {
+    using C = Cfg<D, KIND>;
+    using Place = Cursor<C::kTile, C::kKeys>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, stream = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;  // of the stream
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const long long units = share.end - share.begin;
+    const uint32_t out = sh.tmem + C::kOut + stream * D + lanes;
+    uint8_t* mine = query + stream * kRows * D * 2;
+    const int t = threadIdx.x & 127;
+    Place at;
+    at.start(p, sh.plan, share);
+
+    auto fetch_query = [&] {
+        constexpr int kPer = D / 8;
+#pragma unroll 4
+        for (int i = 0; i < kRows * kPer / 128; ++i) {
+            const int r = (i * 128 + t) / kPer, c = t % kPer;
+            const int packed = at.row0 + stream * kRows + r;
+            const bool there = stream * kRows + r < at.rows;
+            const uint16_t* src = p.q;
+            if (there)
+                src += static_cast<int64_t>(at.s.q0 + packed / p.G) * p.ldq + (at.head * p.G + packed % p.G) * p.hsq + 8 * c;
+            cp_async16_zfill(ptx::smem_addr(mine + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)), src, there);
+        }
+        cp_commit();
+    };
+    auto query_ready = [&] {
+        cp_wait<0>();
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(&sh.query[stream]);
+    };
+    // The values that are not finite, among the keys that this row sees in units with
+    // masks, for columns col .. col + 31: zeros stood for them.
+    auto add_odd = [&](float* o, int col, const Place& was, int from, int place) {
+        for (int unit = from; unit <= was.unit; ++unit) {
+            const int j0 = (was.lo + unit) * C::kKeys;
+            if (sees_all<Place, C::kKeys>(p, was, j0)) continue;
+            for (int j = max(j0, was.first); j < min(j0 + C::kKeys, was.past); ++j) {
+                int page;
+                if (j > place || (p.window && j <= place - p.window)) continue;
+                if (!attn_page(p, p.table + was.b * p.table_stride, j, &page)) continue;
+                const int s = j & ((1 << p.page_log2) - 1);
+                if constexpr (C::kCodes) {
+                    if (p.vs[page * p.zpstride + s * p.zsstride + was.head * p.zhstride] == 255)
+                        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(0x7FFFFFFFu);
+                } else {
+                    const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v + page * p.pstride + s * p.sstride + was.head * p.hstride) + col;
+                    for (int i = 0; i < 32; ++i)
+                        if ((v[i] & 0x7F80) == 0x7F80) o[i] += bf16_bits_to_float(v[i]);
+                }
+            }
+        }
+    };
+
+    fetch_query();
+    query_ready();
+    float most = -INFINITY, sum = 0.0f;
+    bool first = true;
+    bool begun = at.unit == 0;
+    int from = at.unit, item = 0;
+#pragma unroll 1
+    for (long long u = 0; u < units; ++u) {
+        const int buffer = C::kStreams == 2 ? stream : static_cast<int>(u & 1);
+        const uint32_t parity = C::kStreams == 2 ? u & 1 : (u >> 1) & 1;
+        const uint32_t scores = sh.tmem + buffer * 128 + lanes;
+        const bool active = at.rows > stream * kRows;
+        const bool there = stream * kRows + row < at.rows;
+        // rows that are not there look like the last one and are not written
+        const int packed = at.row0 + min(stream * kRows + row, at.rows - 1);
+        const int place = at.s.kv - at.s.nq + packed / p.G;
+        const int j0 = (at.lo + at.unit) * C::kKeys;
+        const bool last = at.unit + 1 == at.n, done = last || u + 1 == units;
+        if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.scores[buffer], parity, p))) return;
+        ptx::tc_fence_after();
+        if (active) {
+            float s[C::kKeys];
+#pragma unroll
+            for (int i = 0; i < C::kKeys / 32; ++i) tmem_ld32(scores + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
+            ptx::tmem_wait_ld();
+            const bool all = j0 + C::kKeys - 1 <= place && (p.window == 0 || j0 > place - p.window);
+            if (!__all_sync(0xFFFFFFFFu, all)) {
+                const int hi = place - j0, lo = p.window ? place - p.window - j0 : -1;
+#pragma unroll
+                for (int i = 0; i < C::kKeys; ++i)
+                    if (i > hi || i <= lo) s[i] = -INFINITY;
+            }
+            float top = s[0];
+#pragma unroll
+            for (int i = 1; i < C::kKeys; ++i) top = fmaxf(top, s[i]);
+            top *= p.scale_log2;
+            float shrink = 1.0f;
+            if (top > most + kLag) {
+                shrink = ex2(most - top);  // 0 from minus infinity
+                most = top;
+            }
+            if (__any_sync(0xFFFFFFFFu, shrink != 1.0f)) {
+                sum *= shrink;
+                if (!first) {
+                    // the products before this one are in the outputs
+                    if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.joined[stream], (u - 1) & 1, p))) return;
+                    ptx::tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(out + c, o);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
+                        tmem_st32(out + c, o);
+                    }
+                    ptx::tmem_wait_st();
+                }
+            }
+            const float base = most == -INFINITY ? 0.0f : most;
+#pragma unroll
+            for (int c = 0; c < C::kKeys / 32; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float x = ex2(fmaf(s[32 * c + 2 * i], p.scale_log2, -base));
+                    const float y = ex2(fmaf(s[32 * c + 2 * i + 1], p.scale_log2, -base));
+                    sum += x + y;
+                    w[i] = pack_bf16(x, y);
+                }
+                tmem_st16(scores + 16 * c, w);
+            }
+            ptx::tmem_wait_st();
+        }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&sh.weights[buffer]);
+        first = false;
+        if (!done) {
+            ++at.unit;
+            continue;
+        }
+        // the item's last unit here: the next one's queries, then this one's rows
+        const Place was = at;
+        if (u + 1 < units) {
+            at.next(p, sh.plan);
+            fetch_query();
+            query_ready();
+        }
+        if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.joined[stream], u & 1, p))) return;
+        ptx::tc_fence_after();
+        const bool whole = last && begun;
+        if (active) {
+            const bool odd = *reinterpret_cast<volatile int*>(&sh.mark[item & (kMarks - 1)]) == item + 1;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            uint16_t* dst = p.o + static_cast<int64_t>(was.s.q0 + packed / p.G) * p.ldo + (was.head * p.G + packed % p.G) * p.hso;
+            float* slot = attn_slot(p, gridDim.x, C::kTile, D, blockIdx.x, begun);
+            const int at_row = stream * kRows + row;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(out + c, reinterpret_cast<uint32_t*>(o));
+                ptx::tmem_wait_ld();
+                if (odd) add_odd(o, c, was, from, place);
+                if (there && whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        *reinterpret_cast<uint4*>(dst + c + i) =
+                            make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
+                                       pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
+                } else if (there) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4*>(slot + at_row * D + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+            }
+            if (there && !whole) {
+                slot[C::kTile * D + at_row] = most;
+                slot[C::kTile * D + C::kTile + at_row] = sum;
+            }
+        }
+        ptx::tc_fence_before();
+        if (!whole && begun && threadIdx.x == 0) {
+            const long long start = share.begin + u - was.unit;  // where the item begins
+            AttnSplit* rec = reinterpret_cast<AttnSplit*>(p.ws) + blockIdx.x;
+            rec->q0 = was.s.q0;
+            rec->row0 = was.row0;
+            rec->head = was.head;
+            rec->last = static_cast<int32_t>(((start + was.n) * share.blocks - 1) / share.total);
+            rec->rows = was.rows;
+        }
+        most = -INFINITY, sum = 0.0f;
+        first = begun = true;
+        from = 0;
+        ++item;
+    }
+}
+
+template <int D, int KIND>
+__global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(const AttnParams p) {
+    using C = Cfg<D, KIND>;
+    extern __shared__ uint8_t raw[];
+    __shared__ Shared sh;
+    uint8_t* query = raw + ((1024 - (ptx::smem_addr(raw) & 1023)) & 1023);
+    uint8_t* ring = query + C::kQBytes;
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) ptx::mbar_init(&sh.full[i], C::kLoaders), ptx::mbar_init(&sh.empty[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sh.scores[i], 1);
+            ptx::mbar_init(&sh.weights[i], 128);
+            ptx::mbar_init(&sh.joined[i], 1);
+            ptx::mbar_init(&sh.query[i], 128);
+        }
+        ptx::mbar_init(&sh.drained, 1);
+        ptx::fence_mbar_init();
+        sh.dead = 0;
+        for (int i = 0; i < kMarks; ++i) sh.mark[i] = 0;
+    }
+    if (warp == C::kSoft) {
+        ptx::tmem_alloc(&sh.tmem, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    if (threadIdx.x == 0) reinterpret_cast<AttnSplit*>(p.ws)[blockIdx.x].rows = 0;
+    ptx::tc_fence_before();
+    const AttnShare share = attn_share<C::kTile, C::kKeys, C::kThreads>(p, sh.plan, blockIdx.x, gridDim.x);
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (share.begin < share.end) {
+        if (warp < C::kSoft) weigh<D, KIND>(p, sh, share, query);
+        else if (warp == C::kSoft) issue_products<D, KIND>(p, sh, share, ptx::smem_addr(query), ptx::smem_addr(ring));
+        else load_units<D, KIND>(p, sh, share, ring);
+        cp_wait<0>();
+        if (warp == C::kSoft) {
+            // nothing of the tensor core's is under way when the memory is given back
+            ptx::mma_commit_warp(&sh.drained);
+            const long long began = clock64();
+            while (!ptx::mbar_test(&sh.drained, 0) && clock64() - began < p.timeout_cycles) {
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == C::kSoft) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(sh.tmem, 512);
+    }
+}
+
+template <int D, int KIND>
+cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
+    using C = Cfg<D, KIND>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = attn_allow_shared(attn_chunk_kernel<D, KIND>, C::kSmem, done);
+    if (e != cudaSuccess) return e;
+    const cudaError_t r = w4::launch_dependent(attn_chunk_kernel<D, KIND>, a.sm_count, C::kThreads, C::kSmem, stream,
+                                               static_cast<const AttnParams&>(a));
+    return r == cudaSuccess ? launch_attn_join(a, C::kTile, a.sm_count, stream) : r;
+}
+
+}  // namespace
+
+size_t attn_chunk_slot_floats(int D) {
+    return D == 256 ? attn_slot_floats(Cfg<256, 0>::kTile, 256) : attn_slot_floats(Cfg<128, 0>::kTile, D);
+}
+
+cudaError_t launch_attn_chunk(const AttnArgs& a, cudaStream_t stream) {
+    if (a.kind == FP8BS_KV_BF16) {
+        if (a.D == 64) return launch<64, FP8BS_KV_BF16>(a, stream);
+        if (a.D == 128) return launch<128, FP8BS_KV_BF16>(a, stream);
+        return launch<256, FP8BS_KV_BF16>(a, stream);
+    }
+    if (a.D == 64) return launch<64, FP8BS_KV_E4M3>(a, stream);
+    if (a.D == 128) return launch<128, FP8BS_KV_E4M3>(a, stream);
+    return launch<256, FP8BS_KV_E4M3>(a, stream);
+}
+
+}  // namespace fp8bs

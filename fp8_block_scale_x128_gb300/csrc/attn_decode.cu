@@ -49,18 +49,6 @@ struct Cfg {
     static constexpr int kBlocks = kSmem <= 108 * 1024 ? 2 : 1;  // of an SM
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -81,16 +69,6 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t a) {
                  : "memory");
 }
 
-// 16 bytes, or zeros where !there (nothing is read then).
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Byte offset of 16-byte chunk c of row r: no two rows of an ldmatrix phase share
 // a bank.
 template <int RB>
@@ -98,54 +76,10 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return r * RB + ((RB >= 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
 }
 
-// Even and odd bytes of a word as two pairs of bf16 numbers, code values * 2^-120.
-__device__ __forceinline__ uint32_t codes_even(uint32_t w) {
-    return ((w << 8) & 0x80008000u) | ((w << 4) & 0x07F007F0u);
-}
-__device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return (w & 0x80008000u) | ((w >> 4) & 0x07F007F0u); }
-
 // 2^(b - 127), NaN for 255.
 __device__ __forceinline__ float scale_of(uint32_t b) {
     return b == 255u ? __uint_as_float(0x7FFFFFFFu) : e8m0_to_float(b);
 }
-
-// The place in the deal of the work: an item and a unit of it.
-template <int UNIT>
-struct Cursor {
-    int tile, b, head, unit, n, lo;  // unit: within the item
-    SeqInfo s;
-    int row0, rows;  // packed rows of the tile
-    int first, past;  // keys that some row sees
-
-    __device__ __forceinline__ void enter(const AttnParams& p, const PlanShared& sh) {
-        s = attn_seq(p, b);
-        row0 = (tile - sh.first[b]) * kRows;
-        rows = min(kRows, s.nq * p.G - row0);
-        const TileUnits u = attn_units<UNIT>(p, s, row0, row0 + rows);
-        n = u.n, lo = u.lo;
-        const int base = s.kv - s.nq;
-        past = base + (row0 + rows - 1) / p.G + 1;
-        first = p.window ? max(base + row0 / p.G - p.window + 1, 0) : 0;
-    }
-    __device__ __forceinline__ void start(const AttnParams& p, const PlanShared& sh, const AttnShare& a) {
-        tile = a.tile;
-        b = attn_tile_seq(sh, p.B, tile);
-        enter(p, sh);
-        const long long x = a.begin - a.before;
-        head = static_cast<int>(x / n);
-        unit = static_cast<int>(x - static_cast<long long>(head) * n);
-    }
-    __device__ __forceinline__ void next(const AttnParams& p, const PlanShared& sh) {
-        if (++unit < n) return;
-        unit = 0;
-        if (++head < p.Hk) return;
-        head = 0;
-        ++tile;
-        if (tile >= sh.first[p.B]) return;  // past the last item
-        while (tile >= sh.first[b + 1]) ++b;
-        enter(p, sh);
-    }
-};
 
 template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads, Cfg<D, KIND>::kBlocks) attn_decode_kernel(const AttnParams p) {
@@ -175,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND>::kBlocks) attn_decode_k
     }
     if (share.begin >= share.end) return;
 
-    Cursor<C::kUnit> in, at;
+    Cursor<kRows, C::kUnit> in, at;
     in.start(p, plan, share);
     at = in;
     long long left = share.end - share.begin;  // units still to fetch
@@ -654,10 +588,17 @@ cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream) {
 }
 
 size_t attn_workspace_bytes(int D, int sm_count) {
-    const int grid = 2 * sm_count;
-    return kWsErrorBytes + attn_records_bytes(grid) + static_cast<size_t>(grid) * 2 * attn_slot_floats(kRows, D) * sizeof(float);
+    const size_t few = static_cast<size_t>(2 * sm_count) * 2 * attn_slot_floats(kRows, D);
+    const size_t many = static_cast<size_t>(sm_count) * 2 * attn_chunk_slot_floats(D);
+    return kWsErrorBytes + attn_records_bytes(2 * sm_count) + (few > many ? few : many) * sizeof(float);
 }
 
-cudaError_t launch_attn_paged(const AttnArgs& a, cudaStream_t stream) { return launch_attn_decode(a, stream); }
+// Rows of a sequence, on average, from which the tensor core's kernel takes the call.
+constexpr int64_t kChunkRows = 33;
+
+cudaError_t launch_attn_paged(const AttnArgs& a, cudaStream_t stream) {
+    if (static_cast<int64_t>(a.T) * a.G >= kChunkRows * a.B) return launch_attn_chunk(a, stream);
+    return launch_attn_decode(a, stream);
+}
 
 }  // namespace fp8bs

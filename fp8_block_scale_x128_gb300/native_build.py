@@ -23,7 +23,8 @@ TRACE_LIB_PATH = os.path.join(BUILD_DIR, "libfp8bs_trace.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cu", "quant.cu", "prepack.cu", "gemm_fused.cu", "rmsnorm_quant.cu", "moe.cu",
-           "w4_quant.cu", "w4_gemv.cu", "w4_moe.cu", "moe_route.cu", "qk_norm_rope.cu", "attn_decode.cu"]
+           "w4_quant.cu", "w4_gemv.cu", "w4_moe.cu", "moe_route.cu", "qk_norm_rope.cu", "attn_decode.cu",
+           "attn_chunk.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]
