@@ -94,7 +94,7 @@ bool heads_aligned(const uint16_t* p, int64_t ld, int64_t hs) { return aligned(p
 bool head_dim_ok(int64_t D) { return D == 64 || D == 128 || D == 256; }
 
 constexpr int64_t kMaxHeads = 1024;
-constexpr int64_t kMaxStride = int64_t(1) << 40;  // elements: offsets stay within 64 bits
+constexpr int64_t kMaxStride = int64_t(1) << 38;  // elements: a tensor map's strides are below 2^40 bytes
 
 bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
 
@@ -571,6 +571,9 @@ int fp8bs_attn_paged(const uint16_t* q, int64_t ldq, int64_t hsq, int64_t T, int
     a.cu = cu_q, a.len = kv_len;
     a.B = static_cast<int>(B), a.T = static_cast<int>(T);
     a.Hk = cache->kv_heads, a.G = static_cast<int>(Hq / cache->kv_heads);
+    while ((1 << a.g_shift) < a.G) ++a.g_shift;
+    a.g_shift += 31;
+    a.g_mul = static_cast<uint32_t>(((uint64_t(1) << a.g_shift) + a.G - 1) / a.G);
     a.scale_log2 = scale * 1.44269504088896340736f;
     a.window = static_cast<int>(window < (1 << 30) ? window : (1 << 30));
     a.o = o, a.ldo = ldo, a.hso = hso;

@@ -59,6 +59,8 @@ struct AttnParams {
     int table_cols;
     const int32_t *cu, *len;
     int B, T, Hk, G;
+    uint32_t g_mul;    // n / G = n * g_mul >> g_shift for n < 2^31
+    int g_shift;
     float scale_log2;  // softmax scale * log2(e)
     int window;        // 0: none
     uint16_t* o;
@@ -67,6 +69,10 @@ struct AttnParams {
     uint8_t* ws;  // past the error word
     long long timeout_cycles;  // of a wait inside the kernel
 };
+
+__device__ __forceinline__ int div_g(const AttnParams& p, int n) {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * p.g_mul >> p.g_shift);
+}
 
 struct AttnArgs : AttnParams {
     int D, kind;
@@ -110,8 +116,8 @@ struct TileUnits {
 template <int BN>
 __device__ __forceinline__ TileUnits attn_units(const AttnParams& p, const SeqInfo& s, int r0, int r1) {
     const int base = s.kv - s.nq;
-    const int hi = base + (r1 - 1) / p.G + 1;  // past the last key seen
-    const int lo = p.window ? max(base + r0 / p.G - p.window + 1, 0) : 0;
+    const int hi = base + div_g(p, r1 - 1) + 1;  // past the last key seen
+    const int lo = p.window ? max(base + div_g(p, r0) - p.window + 1, 0) : 0;
     TileUnits u;
     u.lo = hi > lo ? lo / BN : 0;
     u.n = hi > lo ? (hi + BN - 1) / BN - u.lo : 1;  // a tile that sees nothing still writes its rows
@@ -120,25 +126,32 @@ __device__ __forceinline__ TileUnits attn_units(const AttnParams& p, const SeqIn
 
 // What a block knows of its share.
 struct AttnShare {
-    long long total;     // units of all items
-    int blocks;          // that take part: each has a unit at least
-    long long begin, end;
-    int tile;            // the tile of the first unit,
-    long long before;    // and the units before that tile
+    long long total;       // units of all items
+    int blocks;            // that take part: each has a unit at least
+    long long begin, end;  // units of this block
+    int tile, b, head, unit;  // the place of the first one
+};
+
+// The place in the deal of the work: an item and a unit of it.
+struct Cursor {
+    int tile, b, head, unit, n, lo;  // unit: within the item
+    int q0, rows, row0;              // the sequence's first token, packed rows of the tile
+    int base;                        // place of the sequence's first new token
+    int first, past;                 // keys that some row sees
+    int lowest;                      // place of the first row
 };
 
 struct PlanShared {
     int first[kAttnMaxSeqs + 1];  // tiles before each sequence
-    long long sum[33];
-    int tile;
-    long long before;
+    long long sum[32];
+    AttnShare share;
 };
 
-// Inclusive sum over the block; *all: the block's.  Whole block; two barriers.
+// Inclusive sum over the block; *all: the block's.  Whole block.
 template <int THREADS>
-__device__ __forceinline__ long long block_scan(long long v, PlanShared& sh, long long* all) {
+__device__ __noinline__ long long block_scan(long long v, PlanShared& sh, long long* all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
+#pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
         const long long t = __shfl_up_sync(0xFFFFFFFFu, v, off);
         if (lane >= off) v += t;
@@ -147,7 +160,7 @@ __device__ __forceinline__ long long block_scan(long long v, PlanShared& sh, lon
     if (lane == 31) sh.sum[warp] = v;
     __syncthreads();
     long long before = 0, sum = 0;
-#pragma unroll
+#pragma unroll 4
     for (int w = 0; w < THREADS / 32; ++w) {
         const long long t = sh.sum[w];
         if (w < warp) before += t;
@@ -167,106 +180,98 @@ __device__ __forceinline__ int attn_tile_seq(const PlanShared& sh, int B, int ti
     return lo;
 }
 
-template <int MT, int BN>
-__device__ __forceinline__ TileUnits attn_tile_units(const AttnParams& p, const PlanShared& sh, int tile, int b) {
-    const SeqInfo s = attn_seq(p, b);
-    const int r0 = (tile - sh.first[b]) * MT;
-    return attn_units<BN>(p, s, r0, min(r0 + MT, s.nq * p.G));
-}
-
-// Whole block.  sh stays in use by the block.
+// Whole block; leaves sh.first and sh.share.
 template <int MT, int BN, int THREADS>
-__device__ __forceinline__ AttnShare attn_share(const AttnParams& p, PlanShared& sh, int block, int grid) {
-    const int tid = threadIdx.x;
-    AttnShare a;
+__device__ __noinline__ void attn_share(const AttnParams& p, PlanShared& sh) {
+    const int tid = threadIdx.x, block = blockIdx.x, grid = gridDim.x;
+    if (tid == 0) sh.first[0] = 0;
     int tiles = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
         const int b = b0 + tid;
         long long all;
-        int n = 0;
-        if (b < p.B) n = static_cast<int>((static_cast<long long>(attn_seq(p, b).nq) * p.G + MT - 1) / MT);
+        const int n = b < p.B ? (attn_seq(p, b).nq * p.G + MT - 1) / MT : 0;
         const int upto = static_cast<int>(block_scan<THREADS>(n, sh, &all));
         if (b < p.B) sh.first[b + 1] = tiles + upto;
         tiles += static_cast<int>(all);
     }
-    if (tid == 0) sh.first[0] = 0, sh.tile = tiles;
     __syncthreads();
-    long long total = 0, upto = 0;
-    int n = 0;
-    for (int t0 = 0; t0 < tiles; t0 += THREADS) {
-        const int t = t0 + tid;
-        long long all;
-        n = t < tiles ? attn_tile_units<MT, BN>(p, sh, t, attn_tile_seq(sh, p.B, t)).n : 0;
-        upto = block_scan<THREADS>(n, sh, &all);
-        total += all;
-    }
-    a.total = total * p.Hk;
-    a.blocks = static_cast<int>(min(static_cast<long long>(grid), a.total));
-    if (block >= a.blocks) {
-        a.begin = a.end = 0;
-        a.tile = 0;
-        a.before = 0;
-        return a;  // the same for the whole block
-    }
-    a.begin = block * a.total / a.blocks;
-    a.end = (block + 1) * a.total / a.blocks;
-    long long before = 0;
-    for (int t0 = 0; t0 < tiles; t0 += THREADS) {
-        const int t = t0 + tid;
-        long long all;
-        if (tiles > THREADS) {
-            n = t < tiles ? attn_tile_units<MT, BN>(p, sh, t, attn_tile_seq(sh, p.B, t)).n : 0;
-            upto = block_scan<THREADS>(n, sh, &all);
-        } else {
-            all = total;
+    // twice over the tiles: the sum of all units, then the tile that this block's first
+    // unit lies in (of up to THREADS tiles once)
+    long long total = 0, begin = 0, before = 0, all = 0, upto = 0;
+    int n = 0, b = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int t0 = 0; t0 < tiles; t0 += THREADS) {
+            const int t = t0 + tid;
+            if (pass == 0 || tiles > THREADS) {
+                n = 0;
+                if (t < tiles) {
+                    b = attn_tile_seq(sh, p.B, t);
+                    const SeqInfo s = attn_seq(p, b);
+                    const int r0 = (t - sh.first[b]) * MT;
+                    n = attn_units<BN>(p, s, r0, min(r0 + MT, s.nq * p.G)).n;
+                }
+                upto = block_scan<THREADS>(n, sh, &all);
+            }
+            if (pass == 0) {
+                total += all;
+                continue;
+            }
+            const long long mine = (before + upto - n) * p.Hk;
+            if (n > 0 && mine <= begin && begin < mine + static_cast<long long>(n) * p.Hk) {
+                sh.share.tile = t, sh.share.b = b;
+                sh.share.head = static_cast<int>((begin - mine) / n);
+                sh.share.unit = static_cast<int>(begin - mine - static_cast<long long>(sh.share.head) * n);
+            }
+            before += all;
         }
-        const long long mine = (before + upto - n) * p.Hk;
-        if (n > 0 && mine <= a.begin && a.begin < mine + static_cast<long long>(n) * p.Hk) sh.tile = t, sh.before = mine;
-        before += all;
+        if (pass == 0) {
+            total *= p.Hk;
+            const long long blocks = min(static_cast<long long>(grid), total);
+            begin = block < blocks ? block * total / blocks : 0;
+            if (tid == 0) {
+                sh.share.total = total;
+                sh.share.blocks = static_cast<int>(blocks);
+                sh.share.begin = begin;
+                sh.share.end = block < blocks ? (block + 1) * total / blocks : 0;
+            }
+        }
     }
     __syncthreads();
-    a.tile = sh.tile;
-    a.before = sh.before;
-    return a;
 }
 
-// The place in the deal of the work: an item and a unit of it.
+// What a tile is, for a cursor that has come to it.
 template <int ROWS, int UNIT>
-struct Cursor {
-    int tile, b, head, unit, n, lo;  // unit: within the item
-    SeqInfo s;
-    int row0, rows;  // packed rows of the tile
-    int first, past;  // keys that some row sees
+__device__ __forceinline__ Cursor attn_enter(const AttnParams& p, const PlanShared& sh, int tile, int b, int head) {
+    while (tile >= sh.first[b + 1]) ++b;
+    const SeqInfo s = attn_seq(p, b);
+    Cursor c;
+    c.tile = tile, c.b = b, c.head = head, c.unit = 0;
+    c.q0 = s.q0;
+    c.row0 = (tile - sh.first[b]) * ROWS;
+    c.rows = min(ROWS, s.nq * p.G - c.row0);
+    const TileUnits u = attn_units<UNIT>(p, s, c.row0, c.row0 + c.rows);
+    c.n = u.n, c.lo = u.lo;
+    c.base = s.kv - s.nq;
+    c.lowest = c.base + div_g(p, c.row0);
+    c.past = c.base + div_g(p, c.row0 + c.rows - 1) + 1;
+    c.first = p.window ? max(c.lowest - p.window + 1, 0) : 0;
+    return c;
+}
 
-    __device__ __forceinline__ void enter(const AttnParams& p, const PlanShared& sh) {
-        s = attn_seq(p, b);
-        row0 = (tile - sh.first[b]) * ROWS;
-        rows = min(ROWS, s.nq * p.G - row0);
-        const TileUnits u = attn_units<UNIT>(p, s, row0, row0 + rows);
-        n = u.n, lo = u.lo;
-        const int base = s.kv - s.nq;
-        past = base + (row0 + rows - 1) / p.G + 1;
-        first = p.window ? max(base + row0 / p.G - p.window + 1, 0) : 0;
-    }
-    __device__ __forceinline__ void start(const AttnParams& p, const PlanShared& sh, const AttnShare& a) {
-        tile = a.tile;
-        b = attn_tile_seq(sh, p.B, tile);
-        enter(p, sh);
-        const long long x = a.begin - a.before;
-        head = static_cast<int>(x / n);
-        unit = static_cast<int>(x - static_cast<long long>(head) * n);
-    }
-    __device__ __forceinline__ void next(const AttnParams& p, const PlanShared& sh) {
-        if (++unit < n) return;
-        unit = 0;
-        if (++head < p.Hk) return;
-        head = 0;
-        ++tile;
-        if (tile >= sh.first[p.B]) return;  // past the last item
-        while (tile >= sh.first[b + 1]) ++b;
-        enter(p, sh);
-    }
-};
+// Whether every row of the item sees every key of a unit.
+template <int UNIT>
+__device__ __forceinline__ bool attn_sees_all(const AttnParams& p, const Cursor& c) {
+    const int j0 = (c.lo + c.unit) * UNIT;
+    return j0 + UNIT <= c.lowest + 1 && (p.window == 0 || j0 >= c.past - p.window);
+}
+
+// The block that finishes an item begun in unit `start` of all.
+static __device__ __noinline__ int attn_last_block(const AttnShare& a, long long start, int n) {
+    return static_cast<int>(((start + n) * a.blocks - 1) / a.total);
+}
 
 // What a block leaves for the second launch about an item that it begins and
 // does not finish.
@@ -318,6 +323,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // 16 bytes, or zeros where !there (nothing is read then).
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");

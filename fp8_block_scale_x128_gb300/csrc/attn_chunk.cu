@@ -22,6 +22,7 @@
 // A value that is not finite and that some row of its unit masks would reach that row
 // as zero times it.  In units with masks the loaders put zeros in the place of such
 // values and mark the item; its rows then add those that they see at their end.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "attn.cuh"
@@ -33,6 +34,7 @@ namespace {
 constexpr int kRows = 128;  // of a stream
 constexpr float kLag = 8.0f;
 constexpr int kMarks = 8;
+constexpr int kItems = 8;  // that may be under way: the loaders are at most three ahead of the outputs
 
 template <int D, int KIND>
 struct Cfg {
@@ -41,7 +43,10 @@ struct Cfg {
     static constexpr int kTile = kStreams * kRows;
     static constexpr int kKeys = D == 256 ? 64 : 128;  // of a unit
     static constexpr int kSoft = kStreams * 4;         // softmax warps
-    static constexpr int kThreads = 384;
+    static constexpr int kThreads = kStreams == 2 ? 512 : 384;
+    // registers of a softmax thread and of the others, where the launch's 128 are dealt
+    // out anew: 2 * 128 * (184 + 72) is what 512 threads of 128 have
+    static constexpr int kMoreRegs = 184, kFewRegs = 72;
     static constexpr int kLoadWarps = kThreads / 32 - kSoft - 1;
     static constexpr int kLoaders = kLoadWarps * 32;
     static constexpr int kTileBytes = kKeys * D * 2;
@@ -53,11 +58,15 @@ struct Cfg {
 
 struct Shared {
     PlanShared plan;
-    uint64_t full[4], empty[4], scores[2], weights[2], joined[2], query[2], drained;
+    Cursor items[kItems];
+    uint64_t known[kItems];  // that an item stands there
+    long long next_start;    // units before the next item
+    uint64_t full[4], raw[2], empty[4], scores[2], weights[2], joined[2], query[2], drained;
     long long row_off[3][128];      // of a unit's rows; three units, as loaders may be one apart
     uint8_t row_scale[3][2][128];
     uint32_t tmem;
     int dead;
+    int looked[2];  // warps that have looked a tile through, of either stage
     int mark[kMarks];
 };
 
@@ -82,6 +91,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t* r) {
         "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
         : "memory");
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B bf16 (bits 7-9,
@@ -123,25 +154,80 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* r) {
 }
 
 // Waits for a phase, with a limit; false when it ran out here or anywhere in the
-// block.  (Out of line: the loop is cold.)
-__device__ __noinline__ bool wait_slow(Shared* sh, uint64_t* bar, uint32_t parity, long long limit, uint32_t* err) {
+// block.  (Inline: a call would have to keep a row's scores over it.)
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity, const AttnParams& p) {
+    if (ptx::mbar_test(bar, parity)) return true;
     const long long began = clock64();
+#pragma unroll 1
     while (!ptx::mbar_test(bar, parity)) {
-        if (*reinterpret_cast<volatile int*>(&sh->dead)) return false;
-        const long long spent = clock64() - began;
-        if (spent > limit) {
-            record_error(err, FP8BS_ERR_TIMEOUT);
-            *reinterpret_cast<volatile int*>(&sh->dead) = 1;
+        if (*reinterpret_cast<volatile int*>(&sh.dead)) return false;
+        if (clock64() - began > p.timeout_cycles) {
+            record_error(p.err, FP8BS_ERR_TIMEOUT);
+            *reinterpret_cast<volatile int*>(&sh.dead) = 1;
             return false;
         }
-        if (spent > 4000) __nanosleep(64);
     }
     return true;
 }
-__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity, const AttnParams& p) {
-    if (ptx::mbar_test(bar, parity)) return true;
-    return wait_slow(&sh, bar, parity, p.timeout_cycles, p.err);
+
+// A box of 64 dimensions x some slots of one head and page, in the 128-byte swizzle.
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int d, int slot, int head, int page, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            ptx::smem_addr(dst)),
+        "l"(map), "r"(d), "r"(slot), "r"(head), "r"(page), "r"(ptx::smem_addr(bar))
+        : "memory");
 }
+
+// The items of the block's share, one after the other: one loader warp finds out what
+// they are, an item ahead, and the other tasks read it.  (The code that does it is
+// long, and there is one copy of it: what the instruction cache does not hold costs
+// more than the look-up.)
+template <int ROWS, int UNIT>
+__device__ __noinline__ void publish(const AttnParams& p, Shared& sh, int item) {
+    Cursor c;
+    if (item == 0) {
+        const AttnShare& s0 = sh.plan.share;
+        c = attn_enter<ROWS, UNIT>(p, sh.plan, s0.tile, s0.b, s0.head);
+    } else {
+        c = sh.items[(item - 1) & (kItems - 1)];
+        if (c.head + 1 < p.Hk) ++c.head;
+        else if (c.tile + 1 < sh.plan.first[p.B]) c = attn_enter<ROWS, UNIT>(p, sh.plan, c.tile + 1, c.b, 0);
+    }
+    const AttnShare& a = sh.plan.share;
+    const long long start = item == 0 ? a.begin - a.unit : sh.next_start;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        sh.next_start = start + c.n;
+        if (start >= a.begin && start < a.end && start + c.n > a.end) {  // begun here, finished elsewhere
+            AttnSplit rec = {c.rows, c.q0, c.row0, c.head, attn_last_block(a, start, c.n), {0, 0, 0}};
+            reinterpret_cast<AttnSplit*>(p.ws)[blockIdx.x] = rec;
+        }
+        sh.items[item & (kItems - 1)] = c;
+        ptx::mbar_arrive(&sh.known[item & (kItems - 1)]);
+    }
+    __syncwarp();
+}
+
+// A task's place: the unit of an item.
+struct Place : Cursor {
+    int item;
+
+    __device__ __forceinline__ bool enter(const AttnParams& p, Shared& sh, int k) {
+        item = k;
+        if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.known[k & (kItems - 1)], (k / kItems) & 1, p))) return false;
+        *static_cast<Cursor*>(this) = sh.items[k & (kItems - 1)];
+        return true;
+    }
+    __device__ __forceinline__ bool start(const AttnParams& p, Shared& sh) {
+        const bool ok = enter(p, sh, 0);
+        unit = sh.plan.share.unit;
+        return ok;
+    }
+    __device__ __forceinline__ bool next(const AttnParams& p, Shared& sh) {
+        return ++unit < n || enter(p, sh, item + 1);
+    }
+};
 
 // 16 codes -> 16 bf16 numbers times 2^(b - 127) (NaN for b = 255).
 __device__ __forceinline__ void widen(const uint4& c, uint32_t scale, uint4& lo, uint4& hi) {
@@ -174,27 +260,149 @@ __device__ __forceinline__ bool odd_pair(uint32_t w) {
     return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
 }
 
-// Whether every row of the item sees every key of the unit at j0.
-template <typename Place, int KEYS>
-__device__ __forceinline__ bool sees_all(const AttnParams& p, const Place& at, int j0) {
-    return j0 + KEYS <= at.s.kv - at.s.nq + at.row0 / p.G + 1 && (p.window == 0 || j0 >= at.past - p.window);
+// bf16 tiles: one warp issues boxes (a lane each) of up to a page's slots.  A unit's
+// values that some row masks land on a barrier of their own, and the other loader
+// warps look them through before they hand them on: rows that are no keys, which the
+// boxes may cover or leave, become zeros, as do values that are not finite.
+template <int D>
+__device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint8_t* ring,
+                                           const CUtensorMap* mk, const CUtensorMap* mv) {
+    using C = Cfg<D, FP8BS_KV_BF16>;
+    constexpr int kMost = C::kKeys / 32;  // boxes of a lane, each for all parts of a row
+    const int lane = threadIdx.x & 31;
+    const int rows = min(1 << p.page_log2, C::kKeys), boxes = C::kKeys / rows;
+    const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
+    Place at;
+    publish<C::kTile, C::kKeys>(p, sh, 0);
+    publish<C::kTile, C::kKeys>(p, sh, 1);
+    bool alive = at.start(p, sh);
+    uint32_t fill = 0;
+    int page[kMost];
+    auto find = [&] {
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+            const int j = (at.lo + at.unit) * C::kKeys + (lane + 32 * i) * rows;
+            page[i] = -1;
+            if (lane + 32 * i < boxes && j < at.past && j + rows > at.first) {
+                int id;
+                if (attn_page(p, p.table + at.b * p.table_stride, j, &id)) page[i] = id;
+            }
+        }
+    };
+    if (alive) find();
+#pragma unroll 1
+    for (int u = 0; u < units && alive; ++u) {
+        const int j0 = (at.lo + at.unit) * C::kKeys, head = at.head;
+        const bool check = !attn_sees_all<C::kKeys>(p, at);
+        int now[kMost], count = 0;
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) now[i] = page[i], count += __popc(__ballot_sync(0xFFFFFFFFu, page[i] >= 0));
+        if (u + 1 < units) {
+            const int item = at.item;
+            alive &= at.next(p, sh);
+            if (alive) find();
+            if (at.item != item) publish<C::kTile, C::kKeys>(p, sh, at.item + 1);
+        }
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv, ++fill) {
+            const uint32_t stage = fill % C::kStages;
+            if (alive && fill >= C::kStages)
+                alive = __all_sync(0xFFFFFFFFu, wait(sh, &sh.empty[stage], ((fill / C::kStages) - 1) & 1, p));
+            if (!alive) break;
+            uint64_t* bar = kv && check ? &sh.raw[stage >> 1] : &sh.full[stage];
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, count * rows * D * 2);
+            __syncwarp();
+            uint8_t* tile = ring + stage * C::kTileBytes;
+#pragma unroll
+            for (int i = 0; i < kMost; ++i)
+                if (now[i] >= 0) {
+                    const int r = (lane + 32 * i) * rows, slot = (j0 + r) & ((1 << p.page_log2) - 1);
+#pragma unroll
+                    for (int part = 0; part < D / 64; ++part)
+                        tma_box(tile + part * (C::kKeys * 128) + r * 128, kv ? mv : mk, 64 * part, slot, head, now[i], bar);
+                }
+        }
+    }
+    if (!alive) {  // what is under way lands before the block leaves
+        const long long began = clock64();
+        for (uint32_t f = fill < 4 ? 0 : fill - 4; f < fill; ++f)
+            while (!ptx::mbar_test(&sh.full[f % C::kStages], (f / C::kStages) & 1) && clock64() - began < 1000000) {
+            }
+    }
 }
 
-template <int D, int KIND>
-__device__ __forceinline__ void load_units(const AttnParams& p, Shared& sh, const AttnShare& share, uint8_t* ring) {
-    using C = Cfg<D, KIND>;
-    using Place = Cursor<C::kTile, C::kKeys>;
-    constexpr int kPer = C::kCodes ? D / 16 : D / 8;  // 16-byte pieces of a row in the cache
+template <int D>
+__device__ __forceinline__ void check_units(const AttnParams& p, Shared& sh, uint8_t* ring) {
+    using C = Cfg<D, FP8BS_KV_BF16>;
+    constexpr int kThreads = C::kLoaders - 32, kPer = D / 8;
+    const int tid = threadIdx.x - (C::kSoft + 2) * 32;
+    const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
+    Place at;
+    bool alive = at.start(p, sh);
+    uint32_t checked[2] = {0, 0};
+#pragma unroll 1
+    for (int u = 0; u < units && alive; ++u) {
+        const int j0 = (at.lo + at.unit) * C::kKeys;
+        if (!attn_sees_all<C::kKeys>(p, at)) {
+            const uint32_t stage = (2 * static_cast<uint32_t>(u) + 1) % C::kStages;
+            alive = __all_sync(0xFFFFFFFFu, wait(sh, &sh.raw[stage >> 1], checked[stage >> 1] & 1, p));
+            ++checked[stage >> 1];
+            if (alive) {
+                uint8_t* tile = ring + stage * C::kTileBytes;
+                for (int i = tid; i < C::kKeys * kPer; i += kThreads) {
+                    const int r = i / kPer, c = i % kPer, j = j0 + r;
+                    uint4* q = reinterpret_cast<uint4*>(tile + (c >> 3) * (C::kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+                    if (j < at.first || j >= at.past) {
+                        *q = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    uint32_t w[4] = {q->x, q->y, q->z, q->w};
+                    bool found = false;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        found |= odd_pair(w[k]);
+                        if ((w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u;
+                        if ((w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0x0000FFFFu;
+                    }
+                    if (found) {
+                        *q = make_uint4(w[0], w[1], w[2], w[3]);
+                        sh.mark[at.item & (kMarks - 1)] = at.item + 1;
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if ((tid & 31) == 0) {  // the last of the warps hands the tile on
+                    __threadfence_block();
+                    if ((atomicAdd(&sh.looked[stage >> 1], 1) + 1) % (kThreads / 32) == 0) {
+                        __threadfence_block();
+                        ptx::mbar_arrive(&sh.full[stage]);
+                    }
+                }
+            }
+        }
+        if (alive && u + 1 < units) alive = at.next(p, sh);
+    }
+}
+
+// Tiles of codes: threads read them, widen them and store them as bf16.
+template <int D>
+__device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, uint8_t* ring) {
+    using C = Cfg<D, FP8BS_KV_E4M3>;
+    constexpr int kPer = D / 16;                  // 16-byte pieces of a row in the cache
     constexpr int kRowStep = C::kLoaders / kPer;       // rows between a thread's pieces
     constexpr int kMine = (C::kKeys + kRowStep - 1) / kRowStep;
     constexpr int kLook = (C::kKeys + C::kLoaders - 1) / C::kLoaders;
     const int tid = threadIdx.x - (C::kSoft + 1) * 32;
     // threads past the last whole row copy nothing: their first row is past the unit
     const int row0 = tid < kRowStep * kPer ? tid / kPer : C::kKeys, piece = tid % kPer;
-    const long long units = share.end - share.begin;
+    const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     Place at;
-    at.start(p, sh.plan, share);
-    bool alive = true;
+    const bool publishes = tid < 32;
+    if (publishes) {
+        publish<C::kTile, C::kKeys>(p, sh, 0);
+        publish<C::kTile, C::kKeys>(p, sh, 1);
+    }
+    bool alive = at.start(p, sh);  // warps that are not still meet the others at the barrier
 
     // A unit's rows, looked up a unit ahead and in three steps, so that none of them
     // waits for the one before: pages, then offsets and scales, then shared memory.
@@ -220,10 +428,8 @@ __device__ __forceinline__ void load_units(const AttnParams& p, Shared& sh, cons
             zk[i] = zv[i] = 127;
             if (page[i] >= 0) {
                 off[i] = page[i] * p.pstride + s * p.sstride + at.head * p.hstride;
-                if (C::kCodes) {
-                    const long long z = page[i] * p.zpstride + s * p.zsstride + at.head * p.zhstride;
-                    zk[i] = p.ks[z], zv[i] = p.vs[z];
-                }
+                const long long z = page[i] * p.zpstride + s * p.zsstride + at.head * p.zhstride;
+                zk[i] = p.ks[z], zv[i] = p.vs[z];
             }
         }
     };
@@ -233,10 +439,8 @@ __device__ __forceinline__ void load_units(const AttnParams& p, Shared& sh, cons
             const int r = tid + i * C::kLoaders;
             if (r < C::kKeys) {
                 sh.row_off[slot][r] = off[i];
-                if (C::kCodes) {
-                    sh.row_scale[slot][0][r] = static_cast<uint8_t>(zk[i]);
-                    sh.row_scale[slot][1][r] = static_cast<uint8_t>(zv[i]);
-                }
+                sh.row_scale[slot][0][r] = static_cast<uint8_t>(zk[i]);
+                sh.row_scale[slot][1][r] = static_cast<uint8_t>(zv[i]);
             }
         }
     };
@@ -248,156 +452,80 @@ __device__ __forceinline__ void load_units(const AttnParams& p, Shared& sh, cons
         return tile + (c >> 3) * (C::kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
     };
 
-    find();
-    locate();
-    keep(0);
+    if (alive) find(), locate(), keep(0);
     ptx::named_sync(1, C::kLoaders);
 
-    int item = 0, slot = 0, check = 0;
+    int slot = 0;
     uint32_t fill = 0;
 
-    if constexpr (!C::kCodes) {
-        auto copy = [&](const uint8_t* src) {
-            room(fill);
-            uint8_t* tile = ring + fill % C::kStages * C::kTileBytes;
-            if (alive) {
-#pragma unroll 4
-                for (int i = 0; i < kMine; ++i) {
-                    const int r = row0 + i * kRowStep;
-                    if (r < C::kKeys) {
-                        const long long o = sh.row_off[slot][r];
-                        cp_async16_zfill(ptx::smem_addr(place16(tile, r, piece)), src + (o >= 0 ? o + 16 * piece : 0), o >= 0);
-                    }
-                }
-            }
-            cp_commit();
-        };
-        // the tile before the newest has arrived: values with masks are looked through
-        auto hand_over = [&](uint32_t f) {
-            uint8_t* tile = ring + f % C::kStages * C::kTileBytes;
-            if (alive && check) {
-                for (int r = row0; r < C::kKeys; r += kRowStep) {
-                    uint4* q = reinterpret_cast<uint4*>(place16(tile, r, piece));
-                    uint32_t w[4] = {q->x, q->y, q->z, q->w};
-                    bool found = false;
+    uint4 keys[kMine], values[kMine];
+    auto read = [&](uint4(&raw)[kMine], const uint8_t* src) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        found |= odd_pair(w[c]);
-                        if ((w[c] & 0x7F80u) == 0x7F80u) w[c] &= 0xFFFF0000u;
-                        if ((w[c] & 0x7F800000u) == 0x7F800000u) w[c] &= 0x0000FFFFu;
-                    }
-                    if (found) {
-                        *q = make_uint4(w[0], w[1], w[2], w[3]);
-                        sh.mark[(check - 1) & (kMarks - 1)] = check;
-                    }
-                }
+        for (int i = 0; i < kMine; ++i) {
+            const int r = row0 + i * kRowStep;
+            raw[i] = make_uint4(0, 0, 0, 0);
+            if (r < C::kKeys) {
+                const long long o = sh.row_off[slot][r];
+                if (o >= 0) raw[i] = *reinterpret_cast<const uint4*>(src + o + 16 * piece);
             }
-            if (alive) {
-                ptx::fence_proxy_async_smem();
-                ptx::mbar_arrive(&sh.full[f % C::kStages]);
-            }
-        };
-#pragma unroll 1
-        for (long long u = 0; u < units; ++u) {
-            const int tag = sees_all<Place, C::kKeys>(p, at, (at.lo + at.unit) * C::kKeys) ? 0 : item + 1;
-            const bool more = u + 1 < units;
-            if (more) {
-                const bool last = at.unit + 1 == at.n;
-                at.next(p, sh.plan);
-                item += last;
-                find();
-            }
-            copy(p.k);
-            if (more) locate();
-            if (fill > 0) {
-                cp_wait<1>();
-                hand_over(fill - 1);
-            }
-            ++fill;
-            copy(p.v);
-            const int next = slot == 2 ? 0 : slot + 1;
-            if (more) keep(next);
-            cp_wait<1>();
-            check = 0;
-            hand_over(fill - 1);
-            check = tag;
-            ++fill;
-            ptx::named_sync(1, C::kLoaders);
-            slot = next;
         }
-        cp_wait<0>();
-        hand_over(fill - 1);
-    } else {
-        uint4 keys[kMine], values[kMine];
-        auto read = [&](uint4(&raw)[kMine], const uint8_t* src) {
+    };
+    auto write = [&](uint4(&raw)[kMine], int kv, int from, int tag) {
+        room(fill);
+        uint8_t* tile = ring + fill % C::kStages * C::kTileBytes;
+        if (alive) {
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
                 const int r = row0 + i * kRowStep;
-                raw[i] = make_uint4(0, 0, 0, 0);
                 if (r < C::kKeys) {
-                    const long long o = sh.row_off[slot][r];
-                    if (o >= 0) raw[i] = *reinterpret_cast<const uint4*>(src + o + 16 * piece);
-                }
-            }
-        };
-        auto write = [&](uint4(&raw)[kMine], int kv, int from, int tag) {
-            room(fill);
-            uint8_t* tile = ring + fill % C::kStages * C::kTileBytes;
-            if (alive) {
-#pragma unroll
-                for (int i = 0; i < kMine; ++i) {
-                    const int r = row0 + i * kRowStep;
-                    if (r < C::kKeys) {
-                        uint32_t scale = sh.row_scale[from][kv][r];
-                        if (tag && scale == 255u) {
-                            scale = 127u;
-                            raw[i] = make_uint4(0, 0, 0, 0);
-                            sh.mark[(tag - 1) & (kMarks - 1)] = tag;
-                        }
-                        uint4 lo, hi;
-                        widen(raw[i], scale, lo, hi);
-                        *reinterpret_cast<uint4*>(place16(tile, r, 2 * piece)) = lo;
-                        *reinterpret_cast<uint4*>(place16(tile, r, 2 * piece + 1)) = hi;
+                    uint32_t scale = sh.row_scale[from][kv][r];
+                    if (tag && scale == 255u) {
+                        scale = 127u;
+                        raw[i] = make_uint4(0, 0, 0, 0);
+                        sh.mark[(tag - 1) & (kMarks - 1)] = tag;
                     }
+                    uint4 lo, hi;
+                    widen(raw[i], scale, lo, hi);
+                    *reinterpret_cast<uint4*>(place16(tile, r, 2 * piece)) = lo;
+                    *reinterpret_cast<uint4*>(place16(tile, r, 2 * piece + 1)) = hi;
                 }
-                ptx::fence_proxy_async_smem();
-                ptx::mbar_arrive(&sh.full[fill % C::kStages]);
             }
-            ++fill;
-        };
-        read(keys, p.k);
-#pragma unroll 1
-        for (long long u = 0; u < units; ++u) {
-            const int tag = sees_all<Place, C::kKeys>(p, at, (at.lo + at.unit) * C::kKeys) ? 0 : item + 1;
-            const bool more = u + 1 < units;
-            if (more) {
-                const bool last = at.unit + 1 == at.n;
-                at.next(p, sh.plan);
-                item += last;
-                find();
-            }
-            read(values, p.v);
-            if (more) locate();
-            write(keys, 0, slot, 0);
-            const int now = slot, next = slot == 2 ? 0 : slot + 1;
-            if (more) keep(next);
-            ptx::named_sync(1, C::kLoaders);
-            slot = next;
-            if (more) read(keys, p.k);
-            write(values, 1, now, tag);
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(&sh.full[fill % C::kStages]);
         }
+        ++fill;
+    };
+    if (alive) read(keys, p.k);
+#pragma unroll 1
+    for (int u = 0; u < units; ++u) {
+        bool more = alive && u + 1 < units;
+        const int tag = alive && attn_sees_all<C::kKeys>(p, at) ? 0 : at.item + 1;
+        if (more) {
+            const int item = at.item;
+            more = alive = at.next(p, sh);
+            if (more) find();
+            if (publishes && at.item != item) publish<C::kTile, C::kKeys>(p, sh, at.item + 1);
+        }
+        if (alive) read(values, p.v);
+        if (more) locate();
+        write(keys, 0, slot, 0);
+        const int now = slot, next = slot == 2 ? 0 : slot + 1;
+        if (more) keep(next);
+        ptx::named_sync(1, C::kLoaders);
+        slot = next;
+        if (more) read(keys, p.k);
+        write(values, 1, now, tag);
     }
 }
 
 template <int D, int KIND>
-__device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, const AttnShare& share, uint32_t query,
+__device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, uint32_t query,
                                                uint32_t ring) {
     using C = Cfg<D, KIND>;
-    using Place = Cursor<C::kTile, C::kKeys>;
     constexpr uint32_t kScoreDesc = idesc_bf16(C::kKeys, 0), kValueDesc = idesc_bf16(D, 1);
-    const long long units = share.end - share.begin;
+    const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     Place at;
-    at.start(p, sh.plan, share);
+    if (!at.start(p, sh)) return;
     uint32_t items = 0;  // whose queries have been waited for
     auto tile = [&](uint32_t fill) { return ring + fill % C::kStages * C::kTileBytes; };
     const uint32_t tmem = sh.tmem;
@@ -431,21 +559,22 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, 
     int rows = at.rows;
     if (!await(&sh.query[0], 0) || (C::kStreams == 2 && !await(&sh.query[1], 0)) || !full(0)) return;
     ptx::tc_fence_after();
+#pragma unroll 1
     for (int s = 0; s < C::kStreams; ++s) scores(s, s, tile(0), rows);
     ptx::mma_commit_warp(&sh.empty[0]);
 #pragma unroll 1
-    for (long long u = 0; u < units; ++u) {
+    for (int u = 0; u < units; ++u) {
         const uint32_t fv = 2 * static_cast<uint32_t>(u) + 1, fk = fv + 1;
         const bool more = u + 1 < units, last = at.unit + 1 == at.n;
         const int rows_now = rows;
         if (more) {
-            at.next(p, sh.plan);
+            if (!at.next(p, sh)) return;
             rows = at.rows;
             items += last;
         }
         if constexpr (C::kStreams == 2) {
             if (!full(fv)) return;
-#pragma unroll
+#pragma unroll 1
             for (int s = 0; s < 2; ++s) {
                 if (!await(&sh.weights[s], u & 1)) return;
                 ptx::tc_fence_after();
@@ -477,30 +606,60 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, 
     }
 }
 
+// The values that are not finite, among the keys that a row sees in the item's units
+// with masks from `from` on, where zeros stood for them: added to what the row has in
+// o or, without that, in a slot.
 template <int D, int KIND>
-__device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, const AttnShare& share, uint8_t* query) {
+__device__ __forceinline__ void add_odd(const AttnParams& p, Cursor c, int from, int place, uint16_t* o, float* slot) {
+    constexpr int kKeys = Cfg<D, KIND>::kKeys;
+    const int upto = c.unit;
+#pragma unroll 1
+    for (c.unit = from; c.unit <= upto; ++c.unit) {
+        if (attn_sees_all<kKeys>(p, c)) continue;
+        const int j0 = (c.lo + c.unit) * kKeys;
+#pragma unroll 1
+        for (int j = max(j0, c.first); j < min(j0 + kKeys, c.past); ++j) {
+            int page;
+            if (j > place || (p.window && j <= place - p.window)) continue;
+            if (!attn_page(p, p.table + c.b * p.table_stride, j, &page)) continue;
+            const int s = j & ((1 << p.page_log2) - 1);
+            const bool codes = KIND == FP8BS_KV_E4M3;
+            if (codes && p.vs[page * p.zpstride + s * p.zsstride + c.head * p.zhstride] != 255) continue;
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v + page * p.pstride + s * p.sstride + c.head * p.hstride);
+#pragma unroll 1
+            for (int i = 0; i < D; ++i) {
+                const float x = codes ? __uint_as_float(0x7FFFFFFFu) : bf16_bits_to_float(v[i]);
+                if (isfinite(x)) continue;
+                if (o) o[i] = static_cast<uint16_t>(pack_bf16(bf16_bits_to_float(o[i]) + x, 0.0f));
+                else slot[i] += x;
+            }
+        }
+    }
+}
+
+template <int D, int KIND>
+__device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* query) {
     using C = Cfg<D, KIND>;
-    using Place = Cursor<C::kTile, C::kKeys>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, stream = warp >> 2;
     const int row = (warp & 3) * 32 + lane;  // of the stream
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const long long units = share.end - share.begin;
+    const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     const uint32_t out = sh.tmem + C::kOut + stream * D + lanes;
     uint8_t* mine = query + stream * kRows * D * 2;
     const int t = threadIdx.x & 127;
     Place at;
-    at.start(p, sh.plan, share);
+    if (!at.start(p, sh)) return;
 
     auto fetch_query = [&] {
         constexpr int kPer = D / 8;
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < kRows * kPer / 128; ++i) {
             const int r = (i * 128 + t) / kPer, c = t % kPer;
-            const int packed = at.row0 + stream * kRows + r;
+            const int packed = at.row0 + stream * kRows + r, token = div_g(p, packed);
             const bool there = stream * kRows + r < at.rows;
             const uint16_t* src = p.q;
             if (there)
-                src += static_cast<int64_t>(at.s.q0 + packed / p.G) * p.ldq + (at.head * p.G + packed % p.G) * p.hsq + 8 * c;
+                src += static_cast<int64_t>(at.q0 + token) * p.ldq + (at.head * p.G + packed - token * p.G) * p.hsq + 8 * c;
             cp_async16_zfill(ptx::smem_addr(mine + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)), src, there);
         }
         cp_commit();
@@ -510,37 +669,14 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, const Att
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(&sh.query[stream]);
     };
-    // The values that are not finite, among the keys that this row sees in units with
-    // masks, for columns col .. col + 31: zeros stood for them.
-    auto add_odd = [&](float* o, int col, const Place& was, int from, int place) {
-        for (int unit = from; unit <= was.unit; ++unit) {
-            const int j0 = (was.lo + unit) * C::kKeys;
-            if (sees_all<Place, C::kKeys>(p, was, j0)) continue;
-            for (int j = max(j0, was.first); j < min(j0 + C::kKeys, was.past); ++j) {
-                int page;
-                if (j > place || (p.window && j <= place - p.window)) continue;
-                if (!attn_page(p, p.table + was.b * p.table_stride, j, &page)) continue;
-                const int s = j & ((1 << p.page_log2) - 1);
-                if constexpr (C::kCodes) {
-                    if (p.vs[page * p.zpstride + s * p.zsstride + was.head * p.zhstride] == 255)
-                        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(0x7FFFFFFFu);
-                } else {
-                    const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v + page * p.pstride + s * p.sstride + was.head * p.hstride) + col;
-                    for (int i = 0; i < 32; ++i)
-                        if ((v[i] & 0x7F80) == 0x7F80) o[i] += bf16_bits_to_float(v[i]);
-                }
-            }
-        }
-    };
-
     fetch_query();
     query_ready();
     float most = -INFINITY, sum = 0.0f;
     bool first = true;
     bool begun = at.unit == 0;
-    int from = at.unit, item = 0;
+    int from = at.unit;
 #pragma unroll 1
-    for (long long u = 0; u < units; ++u) {
+    for (int u = 0; u < units; ++u) {
         const int buffer = C::kStreams == 2 ? stream : static_cast<int>(u & 1);
         const uint32_t parity = C::kStreams == 2 ? u & 1 : (u >> 1) & 1;
         const uint32_t scores = sh.tmem + buffer * 128 + lanes;
@@ -548,7 +684,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, const Att
         const bool there = stream * kRows + row < at.rows;
         // rows that are not there look like the last one and are not written
         const int packed = at.row0 + min(stream * kRows + row, at.rows - 1);
-        const int place = at.s.kv - at.s.nq + packed / p.G;
+        const int token = div_g(p, packed), place = at.base + token;
         const int j0 = (at.lo + at.unit) * C::kKeys;
         const bool last = at.unit + 1 == at.n, done = last || u + 1 == units;
         if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.scores[buffer], parity, p))) return;
@@ -560,15 +696,26 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, const Att
             ptx::tmem_wait_ld();
             const bool all = j0 + C::kKeys - 1 <= place && (p.window == 0 || j0 > place - p.window);
             if (!__all_sync(0xFFFFFFFFu, all)) {
-                const int hi = place - j0, lo = p.window ? place - p.window - j0 : -1;
+                // bit i of a word: this row sees key 32 c + i
+                const int hi = min(place - j0, C::kKeys - 1), lo = p.window ? max(place - p.window - j0 + 1, 0) : 0;
 #pragma unroll
-                for (int i = 0; i < C::kKeys; ++i)
-                    if (i > hi || i <= lo) s[i] = -INFINITY;
+                for (int c = 0; c < C::kKeys / 32; ++c) {
+                    const int h = min(hi - 32 * c, 31), l = lo - 32 * c;
+                    uint32_t seen = h < 0 ? 0u : 0xFFFFFFFFu >> (31 - h);
+                    if (l > 0) seen = l > 31 ? 0u : seen >> l << l;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!(seen >> i & 1)) s[32 * c + i] = -INFINITY;
+                }
             }
-            float top = s[0];
+            // eight chains, so that none is long
+            float tops[8];
 #pragma unroll
-            for (int i = 1; i < C::kKeys; ++i) top = fmaxf(top, s[i]);
-            top *= p.scale_log2;
+            for (int i = 0; i < 8; ++i) tops[i] = fmaxf(s[2 * i], s[2 * i + 1]);
+#pragma unroll
+            for (int i = 16; i < C::kKeys; i += 2) tops[(i >> 1) & 7] = fmaxf(tops[(i >> 1) & 7], fmaxf(s[i], s[i + 1]));
+            const float top = p.scale_log2 * fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
+                                                   fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
             float shrink = 1.0f;
             if (top > most + kLag) {
                 shrink = ex2(most - top);  // 0 from minus infinity
@@ -593,18 +740,22 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, const Att
                 }
             }
             const float base = most == -INFINITY ? 0.0f : most;
+            const uint64_t factor = pair(p.scale_log2, p.scale_log2), minus = pair(-base, -base);
+            uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int c = 0; c < C::kKeys / 32; ++c) {
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float x = ex2(fmaf(s[32 * c + 2 * i], p.scale_log2, -base));
-                    const float y = ex2(fmaf(s[32 * c + 2 * i + 1], p.scale_log2, -base));
-                    sum += x + y;
-                    w[i] = pack_bf16(x, y);
+                    const float2 x = halves(fma2(pair(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), factor, minus));
+                    const float a = ex2(x.x), b = ex2(x.y);
+                    sums[i & 3] = add2(sums[i & 3], pair(a, b));
+                    w[i] = pack_bf16(a, b);
                 }
                 tmem_st16(scores + 16 * c, w);
             }
+            const float2 both = halves(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
+            sum += both.x + both.y;
             ptx::tmem_wait_st();
         }
         ptx::tc_fence_before();
@@ -617,7 +768,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, const Att
         // the item's last unit here: the next one's queries, then this one's rows
         const Place was = at;
         if (u + 1 < units) {
-            at.next(p, sh.plan);
+            if (!at.enter(p, sh, at.item + 1)) return;
             fetch_query();
             query_ready();
         }
@@ -625,9 +776,9 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, const Att
         ptx::tc_fence_after();
         const bool whole = last && begun;
         if (active) {
-            const bool odd = *reinterpret_cast<volatile int*>(&sh.mark[item & (kMarks - 1)]) == item + 1;
+            const bool odd = *reinterpret_cast<volatile int*>(&sh.mark[was.item & (kMarks - 1)]) == was.item + 1;
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            uint16_t* dst = p.o + static_cast<int64_t>(was.s.q0 + packed / p.G) * p.ldo + (was.head * p.G + packed % p.G) * p.hso;
+            uint16_t* dst = p.o + static_cast<int64_t>(was.q0 + token) * p.ldo + (was.head * p.G + packed - token * p.G) * p.hso;
             float* slot = attn_slot(p, gridDim.x, C::kTile, D, blockIdx.x, begun);
             const int at_row = stream * kRows + row;
 #pragma unroll 1
@@ -635,7 +786,6 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, const Att
                 float o[32];
                 tmem_ld32(out + c, reinterpret_cast<uint32_t*>(o));
                 ptx::tmem_wait_ld();
-                if (odd) add_odd(o, c, was, from, place);
                 if (there && whole) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 8)
@@ -652,26 +802,19 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, const Att
                 slot[C::kTile * D + at_row] = most;
                 slot[C::kTile * D + C::kTile + at_row] = sum;
             }
+            if (odd && there) add_odd<D, KIND>(p, was, from, place, whole ? dst : nullptr, slot + at_row * D);
         }
         ptx::tc_fence_before();
-        if (!whole && begun && threadIdx.x == 0) {
-            const long long start = share.begin + u - was.unit;  // where the item begins
-            AttnSplit* rec = reinterpret_cast<AttnSplit*>(p.ws) + blockIdx.x;
-            rec->q0 = was.s.q0;
-            rec->row0 = was.row0;
-            rec->head = was.head;
-            rec->last = static_cast<int32_t>(((start + was.n) * share.blocks - 1) / share.total);
-            rec->rows = was.rows;
-        }
         most = -INFINITY, sum = 0.0f;
         first = begun = true;
         from = 0;
-        ++item;
     }
 }
 
 template <int D, int KIND>
-__global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(const __grid_constant__ AttnParams p,
+                                                                          const __grid_constant__ CUtensorMap mk,
+                                                                          const __grid_constant__ CUtensorMap mv) {
     using C = Cfg<D, KIND>;
     extern __shared__ uint8_t raw[];
     __shared__ Shared sh;
@@ -679,16 +822,19 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
     uint8_t* ring = query + C::kQBytes;
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) ptx::mbar_init(&sh.full[i], C::kLoaders), ptx::mbar_init(&sh.empty[i], 1);
+        for (int i = 0; i < C::kStages; ++i) ptx::mbar_init(&sh.full[i], C::kCodes ? C::kLoaders : 1), ptx::mbar_init(&sh.empty[i], 1);
         for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sh.raw[i], 1);
             ptx::mbar_init(&sh.scores[i], 1);
             ptx::mbar_init(&sh.weights[i], 128);
             ptx::mbar_init(&sh.joined[i], 1);
             ptx::mbar_init(&sh.query[i], 128);
         }
         ptx::mbar_init(&sh.drained, 1);
+        for (int i = 0; i < kItems; ++i) ptx::mbar_init(&sh.known[i], 1);
         ptx::fence_mbar_init();
         sh.dead = 0;
+        sh.looked[0] = sh.looked[1] = 0;
         for (int i = 0; i < kMarks; ++i) sh.mark[i] = 0;
     }
     if (warp == C::kSoft) {
@@ -699,14 +845,19 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
     ptx::griddep_launch_dependents();
     if (threadIdx.x == 0) reinterpret_cast<AttnSplit*>(p.ws)[blockIdx.x].rows = 0;
     ptx::tc_fence_before();
-    const AttnShare share = attn_share<C::kTile, C::kKeys, C::kThreads>(p, sh.plan, blockIdx.x, gridDim.x);
-    __syncthreads();
+    attn_share<C::kTile, C::kKeys, C::kThreads>(p, sh.plan);
     ptx::tc_fence_after();
-    if (share.begin < share.end) {
-        if (warp < C::kSoft) weigh<D, KIND>(p, sh, share, query);
-        else if (warp == C::kSoft) issue_products<D, KIND>(p, sh, share, ptx::smem_addr(query), ptx::smem_addr(ring));
-        else load_units<D, KIND>(p, sh, share, ring);
-        cp_wait<0>();
+    if (sh.plan.share.begin < sh.plan.share.end) {
+        if (C::kStreams == 2) {
+            if (warp < C::kSoft) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMoreRegs));
+            else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kFewRegs));
+        }
+        if (warp < C::kSoft) weigh<D, KIND>(p, sh, query);
+        else if (warp == C::kSoft) issue_products<D, KIND>(p, sh, ptx::smem_addr(query), ptx::smem_addr(ring));
+        else if constexpr (C::kCodes) widen_units<D>(p, sh, ring);
+        else if (warp == C::kSoft + 1) copy_units<D>(p, sh, ring, &mk, &mv);
+        else check_units<D>(p, sh, ring);
+        ptx::cp_async_wait_all();
         if (warp == C::kSoft) {
             // nothing of the tensor core's is under way when the memory is given back
             ptx::mma_commit_warp(&sh.drained);
@@ -723,14 +874,56 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
     }
 }
 
+// The driver's tensor map encoder (looked up once; the library does not link to the driver).
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+Encode encoder() {
+    static std::atomic<Encode> found{nullptr};
+    Encode e = found.load(std::memory_order_acquire);
+    if (!e) {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult got;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &got) != cudaSuccess ||
+            got != cudaDriverEntryPointSuccess)
+            return nullptr;
+        e = reinterpret_cast<Encode>(f);
+        found.store(e, std::memory_order_release);
+    }
+    return e;
+}
+
+// Keys or values as [page][head][slot][D], boxes of 64 dimensions x `rows` slots.  An
+// axis of one place takes any stride.
+bool describe(CUtensorMap* map, const AttnArgs& a, const uint8_t* base, int rows) {
+    const Encode e = encoder();
+    if (!e) return false;
+    const int page = 1 << a.page_log2;
+    const cuuint64_t own = static_cast<cuuint64_t>(a.D) * 2;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(a.Hk),
+                                static_cast<cuuint64_t>(a.pages)};
+    const cuuint64_t strides[3] = {page > 1 ? static_cast<cuuint64_t>(a.sstride) : own,
+                                   a.Hk > 1 ? static_cast<cuuint64_t>(a.hstride) : own,
+                                   a.pages > 1 ? static_cast<cuuint64_t>(a.pstride) : own};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1}, step[4] = {1, 1, 1, 1};
+    return e(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t*>(base), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int KIND>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     using C = Cfg<D, KIND>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = attn_allow_shared(attn_chunk_kernel<D, KIND>, C::kSmem, done);
     if (e != cudaSuccess) return e;
+    CUtensorMap mk = {}, mv = {};
+    if (!C::kCodes) {
+        const int rows = min(1 << a.page_log2, C::kKeys);
+        if (!describe(&mk, a, a.k, rows) || !describe(&mv, a, a.v, rows)) return cudaErrorInvalidValue;
+    }
     const cudaError_t r = w4::launch_dependent(attn_chunk_kernel<D, KIND>, a.sm_count, C::kThreads, C::kSmem, stream,
-                                               static_cast<const AttnParams&>(a));
+                                               static_cast<const AttnParams&>(a), mk, mv);
     return r == cudaSuccess ? launch_attn_join(a, C::kTile, a.sm_count, stream) : r;
 }
 

@@ -1,16 +1,17 @@
 // Attention of a few new tokens a sequence over a paged cache, and the join of
 // items that several blocks share (attn.cuh says how the work is dealt out).
 //
-// A tile is 16 rows, (token, query head) pairs of one key head, so every key is
-// read once for all the query heads that share it.  The four warps of a block
-// take alternate slices of 16 or 32 consecutive keys, each through a ring of its
-// own (cp.async, no block-wide step), and keep their own maximum, sum and
-// weighted values; they meet once an item.  A slice: scores by mma.sync m16n8k16
-// (16 rows x 8 keys a step), softmax weights in registers, whose accumulator
-// layout is the next product's operand layout, values by ldmatrix.trans.
+// A tile is 8 or 16 rows, (token, query head) pairs of one key head, so every key is
+// read once for all the query heads that share it.  The four warps of a block take
+// alternate slices of 16 or 32 consecutive keys, each through a ring of its own
+// (cp.async, no block-wide step), and keep their own maximum, sum and weighted
+// values; they meet once an item.  Keys and values are the 16-row operand of mma.sync
+// m16n8k16, the few query rows its 8 columns: scores are [key][row], a transposition
+// of 8x8 blocks makes the weights the next product's operand, outputs are
+// [dimension][row].
 //
 // Precision.  Scores, maxima, sums and outputs are fp32.  A weight enters the
-// product with the values as the sum of two bf16 numbers (off by at most 2^-18 of
+// product with the values as the sum of two bf16 numbers (off by at most 2^-16 of
 // it), since the memory leaves the tensor cores idle.  The maximum that weights
 // are taken against may lag by 8 in units of log2: the sums then hold values up
 // to 2^8 larger, and most slices need no rescaling.
@@ -19,8 +20,8 @@
 // value times 2^-120, exactly, subnormals included; q carries 2^64 and the weights
 // 2^64 against it.  Scales are powers of two: a key's multiplies its scores, a
 // value's its weights.  The pairing of bytes that the decode gives (even bytes,
-// odd bytes) is met by a permutation of q's dimensions, and by two tiles of even
-// and odd dimensions of the output.
+// odd bytes) is met by a permutation of q's dimensions, and by output tiles whose
+// upper and lower halves are even and odd dimensions.
 #include "attn.cuh"
 #include "w4.cuh"
 
@@ -29,24 +30,31 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16;
 constexpr float kLag = 8.0f;
 
-template <int D, int KIND>
+template <int D, int KIND, int NT>
 struct Cfg {
     static constexpr bool kCodes = KIND == FP8BS_KV_E4M3;
+    static constexpr int kRows = 8 * NT;
     static constexpr int kRowBytes = kCodes ? D : 2 * D;
-    static constexpr int kSlice = kRowBytes * 32 <= 4096 ? 32 : 16;  // keys
+    static constexpr int kSlice = kRowBytes <= 64 ? 32 : 16;  // keys
     static constexpr int kUnit = kSlice * kWarps;
     static constexpr int kStageBytes = 2 * kSlice * kRowBytes;
-    static constexpr int kStages = kStageBytes <= 4096 ? 4 : 3;
-    static constexpr bool kQShared = D == 256;  // else q stays in registers
-    static constexpr int kRedPitch = 136;       // floats; 128 columns at a time
-    static constexpr int kRedBytes = kRows * kRedPitch * 4;
-    static constexpr int kScaleBytes = kCodes ? kWarps * kStages * 2 * kSlice : 0;
+    static constexpr int kStages = kStageBytes <= 4096 ? 3 : 2;
+    static constexpr int kPitch = D + 4;  // floats of a joined row: no bank conflicts
+    static constexpr int kRedBytes = kRows * kPitch * 4;
+    static constexpr int kScaleBytes = kCodes ? kWarps * kStages * 2 * kSlice * 4 : 0;
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kSmem = kRing + kRedBytes + kScaleBytes;
-    static constexpr int kBlocks = kSmem <= 108 * 1024 ? 2 : 1;  // of an SM
+    // of an SM: as many as its shared memory holds (Shared and 1 KB beside), up to four
+    static constexpr int kFit = 228 * 1024 / (kSmem + 7 * 1024);
+    static constexpr int kBlocks = kFit > 4 ? 4 : kFit;
+};
+
+struct Shared {
+    PlanShared plan;
+    Cursor items[kWarps][4];  // of each warp: the ones that it has begun to fetch
+    float2 parts[kWarps][16];  // (maximum, sum)
 };
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -68,6 +76,11 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t a) {
                  : "r"(a)
                  : "memory");
 }
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {  // an 8x8 block of 16-bit numbers
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
 
 // Byte offset of 16-byte chunk c of row r: no two rows of an ldmatrix phase share
 // a bank.
@@ -81,63 +94,86 @@ __device__ __forceinline__ float scale_of(uint32_t b) {
     return b == 255u ? __uint_as_float(0x7FFFFFFFu) : e8m0_to_float(b);
 }
 
-template <int D, int KIND>
-__global__ void __launch_bounds__(kThreads, Cfg<D, KIND>::kBlocks) attn_decode_kernel(const AttnParams p) {
-    using C = Cfg<D, KIND>;
+// The item after `c`, into *to.  Whole warp.
+template <int ROWS, int UNIT>
+__device__ __noinline__ void next_item(const AttnParams& p, const PlanShared& plan, const Cursor* from, Cursor* to) {
+    Cursor c = *from;
+    if (c.head + 1 < p.Hk) {
+        ++c.head;
+        c.unit = 0;
+    } else if (c.tile + 1 < plan.first[p.B]) {
+        c = attn_enter<ROWS, UNIT>(p, plan, c.tile + 1, c.b, 0);
+    }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) *to = c;
+    __syncwarp();
+}
+template <int ROWS, int UNIT>
+__device__ __noinline__ void first_item(const AttnParams& p, const PlanShared& plan, Cursor* to) {
+    const AttnShare& a = plan.share;
+    Cursor c = attn_enter<ROWS, UNIT>(p, plan, a.tile, a.b, a.head);
+    c.unit = a.unit;
+    if ((threadIdx.x & 31) == 0) *to = c;
+    __syncwarp();
+}
+
+template <int D, int KIND, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
+    attn_decode_kernel(const __grid_constant__ AttnParams p) {
+    using C = Cfg<D, KIND, NT>;
     constexpr int RB = C::kRowBytes, SL = C::kSlice, ST = C::kStages;
+    constexpr int KT = SL / 16;                // 16-key tiles of a slice
     constexpr int kChunks = RB / 16;           // of a row
-    constexpr int kRowsACopy = 32 / kChunks;   // rows that one cp.async of the warp covers (kChunks <= 32)
-    constexpr int kSteps = D / 16;             // k16 steps of a score
-    constexpr int kOut = D / 8;                // output tiles
+    constexpr int kRowsACopy = 32 / kChunks;   // rows that one cp.async of the warp covers
+    constexpr int kCopies = SL / kRowsACopy;
+    constexpr int kSteps = D / 16;             // k16 steps of a score, and output tiles
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ PlanShared plan;
-    __shared__ float2 parts[kWarps][kRows];    // (maximum, sum)
+    __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
+    const int mrow = lane & 7, mid = lane >> 3;
     float* red = reinterpret_cast<float*>(smem + C::kRing);
     const uint32_t ring = ptx::smem_addr(smem) + warp * ST * C::kStageBytes;
-    const uint32_t qshared = ptx::smem_addr(red);  // q and the joined rows take turns
-    uint8_t* zring = smem + C::kRing + C::kRedBytes + warp * ST * 2 * SL;
+    float* zring = reinterpret_cast<float*>(smem + C::kRing + C::kRedBytes) + warp * ST * 2 * SL;
 
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
 
-    const AttnShare share = attn_share<kRows, C::kUnit, kThreads>(p, plan, blockIdx.x, gridDim.x);
-    if (threadIdx.x == 0) {
-        AttnSplit* rec = reinterpret_cast<AttnSplit*>(p.ws) + blockIdx.x;
-        rec->rows = 0;
-    }
-    if (share.begin >= share.end) return;
+    if (tid == 0) reinterpret_cast<AttnSplit*>(p.ws)[blockIdx.x].rows = 0;
+    attn_share<C::kRows, C::kUnit, kThreads>(p, sh.plan);
+    const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
+    if (units == 0) return;
 
-    Cursor<kRows, C::kUnit> in, at;
-    in.start(p, plan, share);
-    at = in;
-    long long left = share.end - share.begin;  // units still to fetch
+    Cursor* items = sh.items[warp];
+    first_item<C::kRows, C::kUnit>(p, sh.plan, &items[0]);
+    Cursor in = items[0], at = in;
+    int in_item = 0, at_item = 0;
+    int left = units;  // units still to fetch
 
-    // A slice's rows: lane r < SL looks after row r.  The table's entries are read a
-    // slice before they are used, the scales stored a slice after they are read.
-    int page = -1;
+    // Rows of the next slice to fetch: lane r < SL looks after row r, or all after the
+    // page where one holds the slice.  The table is read a slice before it is used,
+    // scales are stored a slice after they are read.
+    const bool one_page = (1 << p.page_log2) >= SL;
+    int page = -1, fetch_stage = 0, zstage = -1;
     uint32_t zk = 0, zv = 0;
-    int zstage = -1, fetch_stage = 0;
-    auto look_up = [&] {  // the page of this lane's row of `in`'s slice, -1: no key
+    auto look_up = [&] {
         page = -1;
-        const int j = (in.lo + in.unit) * C::kUnit + warp * SL + lane;
-        if (left > 0 && lane < SL && j >= in.first && j < in.past) {
-            int id;
-            if (attn_page(p, p.table + in.b * p.table_stride, j, &id)) page = id;
-        }
+        if (left == 0) return;
+        const int j = (in.lo + in.unit) * C::kUnit + warp * SL + (lane < SL ? lane : 0);
+        int id;
+        if (j >= in.first && j < in.past && attn_page(p, p.table + in.b * p.table_stride, j, &id)) page = id;
     };
     auto store_scales = [&] {
         if (C::kCodes && zstage >= 0 && lane < SL) {
-            zring[zstage * 2 * SL + lane] = static_cast<uint8_t>(zk);
-            zring[zstage * 2 * SL + SL + lane] = static_cast<uint8_t>(zv);
+            zring[zstage * 2 * SL + lane] = scale_of(zk) * (p.scale_log2 * 0x1p56f);
+            zring[zstage * 2 * SL + SL + lane] = scale_of(zv) * 0x1p64f;
         }
         zstage = -1;
     };
     auto fetch = [&] {
         store_scales();
         if (left > 0) {
-            const int j = (in.lo + in.unit) * C::kUnit + warp * SL + lane;
+            const int j = (in.lo + in.unit) * C::kUnit + warp * SL + (lane < SL ? lane : 0);
             const int slot = j & ((1 << p.page_log2) - 1);
             long long off = -1;
             if (page >= 0) off = page * p.pstride + slot * p.sstride + in.head * p.hstride;
@@ -150,18 +186,33 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND>::kBlocks) attn_decode_k
                 }
             }
             const uint32_t base = ring + fetch_stage * C::kStageBytes;
+            const int r0 = lane / kChunks, c = lane % kChunks;
+            if (one_page && __all_sync(0xFFFFFFFFu, page >= 0)) {  // every row is there
+                long long o = __shfl_sync(0xFFFFFFFFu, off, 0) + r0 * p.sstride + 16 * c;
+                const long long step = kRowsACopy * p.sstride;
 #pragma unroll
-            for (int i = 0; i < SL / kRowsACopy; ++i) {
-                const int r = i * kRowsACopy + lane / kChunks, c = lane % kChunks;
-                const long long o = __shfl_sync(0xFFFFFFFFu, off, r);
-                const bool there = o >= 0;
-                const long long src = there ? o + 16 * c : 0;
-                cp_async16_zfill(base + chunk_at<RB>(r, c), p.k + src, there);
-                cp_async16_zfill(base + SL * RB + chunk_at<RB>(r, c), p.v + src, there);
+                for (int i = 0; i < kCopies; ++i, o += step) {
+                    const uint32_t to = base + chunk_at<RB>(i * kRowsACopy + r0, c);
+                    cp_async16(to, p.k + o);
+                    cp_async16(to + SL * RB, p.v + o);
+                }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < kCopies; ++i) {
+                    const int r = i * kRowsACopy + r0;
+                    const long long o = __shfl_sync(0xFFFFFFFFu, off, r);
+                    const long long src = o >= 0 ? o + 16 * c : 0;
+                    const uint32_t to = base + chunk_at<RB>(r, c);
+                    cp_async16_zfill(to, p.k + src, o >= 0);
+                    cp_async16_zfill(to + SL * RB, p.v + src, o >= 0);
+                }
             }
             --left;
-            in.next(p, plan);
             if (++fetch_stage == ST) fetch_stage = 0;
+            if (++in.unit >= in.n && left > 0) {
+                next_item<C::kRows, C::kUnit>(p, sh.plan, &items[in_item & 3], &items[(in_item + 1) & 3]);
+                in = items[++in_item & 3];
+            }
         }
         cp_commit();
         look_up();
@@ -170,273 +221,239 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND>::kBlocks) attn_decode_k
 #pragma unroll 1
     for (int i = 0; i < ST - 1; ++i) fetch();
 
-    uint32_t qf[C::kQShared ? 1 : kSteps][4];
-    float out[kOut][4];
-    float m[2], l[2];
-    int place[2];
-    int stage = 0;
-    int begun = 1;  // whether the item began in this block
+    uint32_t qf[kSteps][NT][2];
+    float out[kSteps][NT][4];
+    float m[NT][2], l[NT][2];  // of rows 8 n + 2 t + i; sums over this lane's keys
+    int place[NT][2];
 
     auto load_q = [&] {
-        const int base = at.s.kv - at.s.nq;
-        const uint16_t* rows[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = at.row0 + g + 8 * i;
-            const bool there = g + 8 * i < at.rows;
-            place[i] = there ? base + r / p.G : -1;
-            const int token = at.s.q0 + r / p.G, head = at.head * p.G + r % p.G;
-            rows[i] = there ? p.q + static_cast<int64_t>(token) * p.ldq + head * p.hsq : nullptr;
-            m[i] = -INFINITY, l[i] = 0.0f;
-        }
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int o = 0; o < kOut; ++o)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) out[o][i] = 0.0f;
-        auto big = [](uint32_t w) {  // * 2^64
-            return pack_bf16(__uint_as_float(w << 16) * 0x1p64f, __uint_as_float(w & 0xFFFF0000u) * 0x1p64f);
-        };
-        auto piece = [&](int i, int ks, uint32_t& lo, uint32_t& hi) {
-            lo = hi = 0;
-            if (!rows[i]) return;
-            if (C::kCodes) {
-                const uint2 w = *reinterpret_cast<const uint2*>(rows[i] + 16 * ks + 4 * t);
-                const uint32_t x = big(w.x), y = big(w.y);
-                lo = __byte_perm(x, y, 0x5410), hi = __byte_perm(x, y, 0x7632);
-            } else {
-                lo = *reinterpret_cast<const uint32_t*>(rows[i] + 16 * ks + 2 * t);
-                hi = *reinterpret_cast<const uint32_t*>(rows[i] + 16 * ks + 8 + 2 * t);
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * n + 2 * t + i;
+                place[n][i] = r < at.rows ? at.base + div_g(p, at.row0 + r) : -1;
+                m[n][i] = -INFINITY, l[n][i] = 0.0f;
             }
-        };
-        if constexpr (C::kQShared) {
-            if (warp == 0) {
-                for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t lo, hi;
-                        piece(i, ks, lo, hi);
-                        uint8_t* q8 = reinterpret_cast<uint8_t*>(red);
-                        *reinterpret_cast<uint32_t*>(q8 + chunk_at<2 * D>(g + 8 * i, 2 * ks) + 4 * t) = lo;
-                        *reinterpret_cast<uint32_t*>(q8 + chunk_at<2 * D>(g + 8 * i, 2 * ks + 1) + 4 * t) = hi;
-                    }
-            }
-            __syncthreads();
-        } else {
+            for (int o = 0; o < kSteps; ++o)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) out[o][n][i] = 0.0f;
+            const int r = at.row0 + 8 * n + g, token = div_g(p, r);
+            const bool there = 8 * n + g < at.rows;
+            const uint16_t* q = p.q;
+            if (there) q += static_cast<int64_t>(at.q0 + token) * p.ldq + (at.head * p.G + r - token * p.G) * p.hsq;
+            auto big = [](uint32_t w) {  // * 2^64
+                return pack_bf16(__uint_as_float(w << 16) * 0x1p64f, __uint_as_float(w & 0xFFFF0000u) * 0x1p64f);
+            };
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks) {
-                piece(0, ks, qf[ks][0], qf[ks][2]);
-                piece(1, ks, qf[ks][1], qf[ks][3]);
+                qf[ks][n][0] = qf[ks][n][1] = 0;
+                if (!there) continue;
+                if (C::kCodes) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(q + 16 * ks + 4 * t);
+                    const uint32_t x = big(w.x), y = big(w.y);
+                    qf[ks][n][0] = __byte_perm(x, y, 0x5410), qf[ks][n][1] = __byte_perm(x, y, 0x7632);
+                } else {
+                    qf[ks][n][0] = *reinterpret_cast<const uint32_t*>(q + 16 * ks + 2 * t);
+                    qf[ks][n][1] = *reinterpret_cast<const uint32_t*>(q + 16 * ks + 8 + 2 * t);
+                }
             }
         }
     };
 
+    int begun = at.unit == 0;  // whether the item began in this block
     // The four warps' parts of the item become one, which goes to o or to a slot.
-    auto finish = [&](bool whole) {
-        float part[2];
+    auto finish = [&](bool whole, int u) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
-            if (t == 0) parts[warp][g + 8 * i] = make_float2(m[i], l[i]);
-        }
-        __syncthreads();  // q in shared memory is read no more, too
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float most = parts[0][g + 8 * i].x;
+            for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) most = fmaxf(most, parts[w][g + 8 * i].x);
-            part[i] = m[i] == -INFINITY ? 0.0f : ex2(m[i] - most);
-            if (C::kCodes) part[i] *= 0x1p56f;
-        }
-        const int row = tid / 8, sub = tid % 8;
-        float most = parts[0][row].x, sum = 0.0f;
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) most = fmaxf(most, parts[w][row].x);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            sum += parts[w][row].x == -INFINITY ? 0.0f : parts[w][row].y * ex2(parts[w][row].x - most);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        float* slot = attn_slot(p, gridDim.x, kRows, D, blockIdx.x, begun);
-        const int r = at.row0 + row;
-        const int token = at.s.q0 + r / p.G, head = at.head * p.G + r % p.G;
-        uint16_t* dst = p.o + static_cast<int64_t>(token) * p.ldo + head * p.hso;
-        constexpr int kCols = D < 128 ? D : 128;
-#pragma unroll
-        for (int cb = 0; cb < D / kCols; ++cb) {
-#pragma unroll 1
-            for (int w = kWarps - 1; w >= 0; --w) {
-                if (warp == w) {
-#pragma unroll
-                    for (int o = 0; o < kCols / 8; ++o)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float* v = &out[cb * kCols / 8 + o][2 * i];
-                            float* to = red + (g + 8 * i) * C::kRedPitch;
-                            float2* both;
-                            if (C::kCodes) {  // even or odd dimensions of 16: one of the lane's four
-                                float* q4 = to + 16 * (o / 2) + 4 * t + (o & 1);
-                                q4[0] = (w == kWarps - 1 ? 0.0f : q4[0]) + v[0] * part[i];
-                                q4[2] = (w == kWarps - 1 ? 0.0f : q4[2]) + v[1] * part[i];
-                            } else {
-                                both = reinterpret_cast<float2*>(to + 8 * o + 2 * t);
-                                float2 x = w == kWarps - 1 ? make_float2(0.0f, 0.0f) : *both;
-                                x.x += v[0] * part[i], x.y += v[1] * part[i];
-                                *both = x;
-                            }
-                        }
-                }
-                __syncthreads();
+                for (int off = 4; off < 32; off <<= 1) l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], off);
+                if (g == 0) sh.parts[warp][8 * n + 2 * t + i] = make_float2(m[n][i], l[n][i]);
             }
-            constexpr int kMine = kCols / 8;  // columns of a thread
-            const float* from = red + row * C::kRedPitch;
-            if (row < at.rows) {
-                if (whole) {
+        __syncthreads();
+        float part[NT][2];
 #pragma unroll
-                    for (int c = 0; c < kMine; c += 8) {
-                        const int col = (c / 8 * 8 + sub) * 8;
-                        const float4 x = *reinterpret_cast<const float4*>(from + col);
-                        const float4 y = *reinterpret_cast<const float4*>(from + col + 4);
-                        *reinterpret_cast<uint4*>(dst + cb * kCols + col) =
-                            make_uint4(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv),
-                                       pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
-                    }
-                } else {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int c = 0; c < kMine; c += 4) {
-                        const int col = (c / 4 * 8 + sub) * 4;
-                        *reinterpret_cast<float4*>(slot + row * D + cb * kCols + col) =
-                            *reinterpret_cast<const float4*>(from + col);
-                    }
-                    if (cb == 0 && sub == 0) {
-                        slot[kRows * D + row] = most;
-                        slot[kRows * D + kRows + row] = sum;
-                    }
-                }
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * n + 2 * t + i;
+                float most = sh.parts[0][r].x;
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) most = fmaxf(most, sh.parts[w][r].x);
+                part[n][i] = m[n][i] == -INFINITY ? 0.0f : ex2(m[n][i] - most);
+                if (C::kCodes) part[n][i] *= 0x1p56f;
+            }
+#pragma unroll 1
+        for (int w = 0; w < kWarps; ++w) {
+            if (warp == w) {
+#pragma unroll
+                for (int o = 0; o < kSteps; ++o)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            // rows 2t, 2t + 1 of dimensions g and g + 8, or 2g and 2g + 1, of 16
+                            float* to = red + (8 * n + 2 * t + (i & 1)) * C::kPitch + 16 * o +
+                                        (C::kCodes ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
+                            *to = (w == 0 ? 0.0f : *to) + out[o][n][i] * part[n][i & 1];
+                        }
             }
             __syncthreads();
         }
-        // the item's unit past this block's share, counted from its start
-        if (!whole && begun && tid == 0) {
-            const long long start = share.end - (at.unit + 1);  // where the item begins
-            AttnSplit* rec = reinterpret_cast<AttnSplit*>(p.ws) + blockIdx.x;
-            rec->q0 = at.s.q0;
-            rec->row0 = at.row0;
-            rec->head = at.head;
-            rec->last = static_cast<int32_t>(((start + at.n) * share.blocks - 1) / share.total);
-            rec->rows = at.rows;
+        float* slot = attn_slot(p, gridDim.x, C::kRows, D, blockIdx.x, begun);
+        constexpr int kPer = D / 8;  // threads of a row
+#pragma unroll 1
+        for (int row = tid / kPer; row < at.rows; row += kThreads / kPer) {
+            const int col = tid % kPer * 8;
+            float most = sh.parts[0][row].x, sum = 0.0f;
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) most = fmaxf(most, sh.parts[w][row].x);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                sum += sh.parts[w][row].x == -INFINITY ? sh.parts[w][row].y : sh.parts[w][row].y * ex2(sh.parts[w][row].x - most);
+            const float4 x = *reinterpret_cast<const float4*>(red + row * C::kPitch + col);
+            const float4 y = *reinterpret_cast<const float4*>(red + row * C::kPitch + col + 4);
+            if (whole) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const int r = at.row0 + row, token = div_g(p, r);
+                uint16_t* dst = p.o + static_cast<int64_t>(at.q0 + token) * p.ldo + (at.head * p.G + r - token * p.G) * p.hso + col;
+                *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv),
+                                                            pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+            } else {
+                *reinterpret_cast<float4*>(slot + row * D + col) = x;
+                *reinterpret_cast<float4*>(slot + row * D + col + 4) = y;
+                if (col == 0) slot[C::kRows * D + row] = most, slot[C::kRows * D + C::kRows + row] = sum;
+            }
         }
+        if (!whole && begun && tid == 0) {
+            const long long start = sh.plan.share.begin + u - at.unit;  // where the item begins
+            AttnSplit rec = {at.rows, at.q0, at.row0, at.head, attn_last_block(sh.plan.share, start, at.n), {0, 0, 0}};
+            reinterpret_cast<AttnSplit*>(p.ws)[blockIdx.x] = rec;
+        }
+        __syncthreads();
     };
 
-    begun = at.unit == 0;
     load_q();
-    const long long units = share.end - share.begin;
+    int stage = 0;
 #pragma unroll 1
-    for (long long u = 0; u < units; ++u) {
+    for (int u = 0; u < units; ++u) {
         fetch();
         cp_wait<ST - 1>();
         __syncwarp();
         const uint32_t ks = ring + stage * C::kStageBytes, vs = ks + SL * RB;
-        const uint8_t* z = zring + stage * 2 * SL;
+        const float* z = zring + stage * 2 * SL;
         const int j0 = (at.lo + at.unit) * C::kUnit + warp * SL;
-        const int base = at.s.kv - at.s.nq;
-        const int lowest = base + at.row0 / p.G;
         if (j0 < at.past && j0 + SL > at.first) {
-            float s[SL / 8][4];
+            float s[KT][NT][4];
 #pragma unroll
-            for (int n = 0; n < SL / 8; ++n)
+            for (int k = 0; k < KT; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[n][i] = 0.0f;
-            const int mrow = lane & 7, mid = lane >> 3;
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int k = 0; k < kSteps; k += C::kCodes ? 2 : 1) {
-                uint32_t a[2][4];
-                if constexpr (C::kQShared) {
-                    ldsm(a[0], qshared + chunk_at<2 * D>(mrow + (mid & 1) * 8, 2 * k + (mid >> 1)));
-                    if (C::kCodes) ldsm(a[1], qshared + chunk_at<2 * D>(mrow + (mid & 1) * 8, 2 * k + 2 + (mid >> 1)));
-                } else {
+                    for (int i = 0; i < 4; ++i) s[k][n][i] = 0.0f;
+            const uint32_t krow = ks + 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        a[0][i] = qf[k][i];
-                        if (C::kCodes) a[1][i] = qf[k + 1 < kSteps ? k + 1 : k][i];
-                    }
-                }
+            for (int i = 0; i < kSteps; i += C::kCodes ? 2 : 1)
 #pragma unroll
-                for (int n = 0; n < SL / 8; n += 2) {
+                for (int k = 0; k < KT; ++k) {
                     uint32_t b[4];
-                    const int row = n * 8 + (mid >> 1) * 8 + mrow;
+                    const int row = k * 16 + (mid & 1) * 8 + mrow;
                     if (C::kCodes) {
-                        ldsm(b, ks + chunk_at<RB>(row, k + (mid & 1)));
-                        mma_bf16(s[n], a[0], codes_even(b[0]), codes_odd(b[0]));
-                        mma_bf16(s[n + 1], a[0], codes_even(b[2]), codes_odd(b[2]));
-                        mma_bf16(s[n], a[1], codes_even(b[1]), codes_odd(b[1]));
-                        mma_bf16(s[n + 1], a[1], codes_even(b[3]), codes_odd(b[3]));
+                        ldsm(b, krow + chunk_at<RB>(row, i + (mid >> 1)));
+                        const uint32_t a0[4] = {codes_even(b[0]), codes_even(b[1]), codes_odd(b[0]), codes_odd(b[1])};
+                        const uint32_t a1[4] = {codes_even(b[2]), codes_even(b[3]), codes_odd(b[2]), codes_odd(b[3])};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma_bf16(s[k][n], a0, qf[i][n][0], qf[i][n][1]);
+                            mma_bf16(s[k][n], a1, qf[i + 1 < kSteps ? i + 1 : i][n][0], qf[i + 1 < kSteps ? i + 1 : i][n][1]);
+                        }
                     } else {
-                        ldsm(b, ks + chunk_at<RB>(row, 2 * k + (mid & 1)));
-                        mma_bf16(s[n], a[0], b[0], b[1]);
-                        mma_bf16(s[n + 1], a[0], b[2], b[3]);
+                        ldsm(b, krow + chunk_at<RB>(row, 2 * i + (mid >> 1)));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_bf16(s[k][n], b, qf[i][n][0], qf[i][n][1]);
                     }
                 }
-            }
             // scores in units of log2, masked ones at minus infinity
-            const bool all = j0 + SL <= lowest + 1 && (p.window == 0 || j0 >= at.past - p.window);
-            float most[2] = {-INFINITY, -INFINITY};
+            const bool all = j0 + SL <= at.lowest + 1 && (p.window == 0 || j0 >= at.past - p.window);
+            float most[NT][2];
 #pragma unroll
-            for (int n = 0; n < SL / 8; ++n)
+            for (int n = 0; n < NT; ++n) most[n][0] = most[n][1] = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float x = s[n][i] * (C::kCodes ? p.scale_log2 * 0x1p56f : p.scale_log2);
-                    if (C::kCodes) x *= scale_of(z[n * 8 + 2 * t + (i & 1)]);
-                    if (!all) {
-                        const int j = j0 + n * 8 + 2 * t + (i & 1);
-                        const int w = place[i >> 1];
-                        if (j > w || (p.window && j <= w - p.window)) x = -INFINITY;
-                    }
-                    s[n][i] = x;
-                    most[i >> 1] = fmaxf(most[i >> 1], x);
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int key = k * 16 + 8 * h + g;
+                    const float factor = C::kCodes ? z[key] : p.scale_log2;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float x = s[k][n][2 * h + i] * factor;
+                            if (!all) {
+                                const int j = j0 + key, w = place[n][i];
+                                if (j > w || (p.window && j <= w - p.window)) x = -INFINITY;
+                            }
+                            s[k][n][2 * h + i] = x;
+                            most[n][i] = fmaxf(most[n][i], x);
+                        }
                 }
             bool grown = false;
-            float shrink[2];
+            float shrink[NT][2], from[NT][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                most[i] = fmaxf(most[i], __shfl_xor_sync(0xFFFFFFFFu, most[i], 1));
-                most[i] = fmaxf(most[i], __shfl_xor_sync(0xFFFFFFFFu, most[i], 2));
-                const bool up = most[i] > m[i] + kLag;
-                shrink[i] = 1.0f;
-                if (up) {
-                    shrink[i] = ex2(m[i] - most[i]);  // 0 from minus infinity
-                    m[i] = most[i];
-                    grown = true;
-                }
-            }
-            if (__any_sync(0xFFFFFFFFu, grown)) {
-#pragma unroll
-                for (int o = 0; o < kOut; ++o)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) out[o][i] *= shrink[i >> 1];
-                l[0] *= shrink[0], l[1] *= shrink[1];
-            }
-            const float from[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
-            uint32_t hi[SL / 8][2], low[SL / 8][2];
-#pragma unroll
-            for (int n = 0; n < SL / 8; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float w0 = ex2(s[n][2 * i] - from[i]), w1 = ex2(s[n][2 * i + 1] - from[i]);
-                    l[i] += w0 + w1;
-                    if (C::kCodes) {
-                        const float v0 = scale_of(z[SL + n * 8 + 2 * t]), v1 = scale_of(z[SL + n * 8 + 2 * t + 1]);
-                        // a masked key's scale may be a NaN
-                        w0 = s[n][2 * i] == -INFINITY ? 0.0f : w0 * 0x1p64f * v0;
-                        w1 = s[n][2 * i + 1] == -INFINITY ? 0.0f : w1 * 0x1p64f * v1;
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) most[n][i] = fmaxf(most[n][i], __shfl_xor_sync(0xFFFFFFFFu, most[n][i], off));
+                    shrink[n][i] = 1.0f;
+                    if (most[n][i] > m[n][i] + kLag) {
+                        shrink[n][i] = ex2(m[n][i] - most[n][i]);  // 0 from minus infinity
+                        m[n][i] = most[n][i];
+                        grown = true;
                     }
-                    s[n][2 * i] = w0, s[n][2 * i + 1] = w1;
-                    hi[n][i] = pack_bf16(w0, w1);
-                    low[n][i] = pack_bf16(w0 - __uint_as_float(hi[n][i] << 16),
-                                          w1 - __uint_as_float(hi[n][i] & 0xFFFF0000u));
+                    from[n][i] = m[n][i] == -INFINITY ? 0.0f : m[n][i];
+                }
+            if (__any_sync(0xFFFFFFFFu, grown)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    l[n][0] *= shrink[n][0], l[n][1] *= shrink[n][1];
+#pragma unroll
+                    for (int o = 0; o < kSteps; ++o)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) out[o][n][i] *= shrink[n][i & 1];
+                }
+            }
+            uint32_t hi[KT][NT][2], low[KT][NT][2];  // [8 keys]: the product's operand
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float value = C::kCodes ? z[SL + k * 16 + 8 * h + g] : 1.0f;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float w[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float x = s[k][n][2 * h + i];
+                            w[i] = ex2(x - from[n][i]);
+                            l[n][i] += w[i];
+                            // a masked key's scale may be a NaN
+                            if (C::kCodes) w[i] = !all && x == -INFINITY ? 0.0f : w[i] * value;
+                            s[k][n][2 * h + i] = w[i];
+                        }
+                        const uint32_t both = pack_bf16(w[0], w[1]);
+                        hi[k][n][h] = transposed(both);
+                        low[k][n][h] = transposed(pack_bf16(w[0] - __uint_as_float(both << 16),
+                                                            w[1] - __uint_as_float(both & 0xFFFF0000u)));
+                    }
                 }
             bool odd = false;  // a value that is not finite where some row masks its key
             if (!C::kCodes && !all) {
                 uint32_t acc = 0;
+#pragma unroll 1
                 for (int i = lane; i < SL * kChunks; i += 32) {
                     const uint4 x = *reinterpret_cast<const uint4*>(smem + (vs - ptx::smem_addr(smem)) + 16 * i);
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -448,64 +465,69 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND>::kBlocks) attn_decode_k
             }
             if (!odd) {
 #pragma unroll
-                for (int n = 0; n < SL / 16; ++n) {
-                    const uint32_t ph[4] = {hi[2 * n][0], hi[2 * n][1], hi[2 * n + 1][0], hi[2 * n + 1][1]};
-                    const uint32_t pl[4] = {low[2 * n][0], low[2 * n][1], low[2 * n + 1][0], low[2 * n + 1][1]};
+                for (int k = 0; k < KT; ++k)
 #pragma unroll
-                    for (int c = 0; c < kChunks; c += 2) {
+                    for (int o = 0; o < kSteps; o += C::kCodes ? 2 : 1) {
                         uint32_t b[4];
-                        ldsm_t(b, vs + chunk_at<RB>(n * 16 + (mid & 1) * 8 + mrow, c + (mid >> 1)));
                         if (C::kCodes) {
+                            ldsm_t(b, vs + chunk_at<RB>(k * 16 + (mid & 1) * 8 + mrow, o + (mid >> 1)));
+                            const uint32_t a0[4] = {codes_even(b[0]), codes_odd(b[0]), codes_even(b[1]), codes_odd(b[1])};
+                            const uint32_t a1[4] = {codes_even(b[2]), codes_odd(b[2]), codes_even(b[3]), codes_odd(b[3])};
+                            const int next = o + 1 < kSteps ? o + 1 : o;
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint32_t e0 = codes_even(b[2 * i]), e1 = codes_even(b[2 * i + 1]);
-                                const uint32_t o0 = codes_odd(b[2 * i]), o1 = codes_odd(b[2 * i + 1]);
-                                mma_bf16(out[2 * (c + i)], ph, e0, e1);
-                                mma_bf16(out[2 * (c + i) + 1], ph, o0, o1);
-                                mma_bf16(out[2 * (c + i)], pl, e0, e1);
-                                mma_bf16(out[2 * (c + i) + 1], pl, o0, o1);
+                            for (int n = 0; n < NT; ++n) {
+                                mma_bf16(out[o][n], a0, hi[k][n][0], hi[k][n][1]);
+                                mma_bf16(out[next][n], a1, hi[k][n][0], hi[k][n][1]);
+                                mma_bf16(out[o][n], a0, low[k][n][0], low[k][n][1]);
+                                mma_bf16(out[next][n], a1, low[k][n][0], low[k][n][1]);
                             }
                         } else {
-                            mma_bf16(out[c], ph, b[0], b[1]);
-                            mma_bf16(out[c + 1], ph, b[2], b[3]);
-                            mma_bf16(out[c], pl, b[0], b[1]);
-                            mma_bf16(out[c + 1], pl, b[2], b[3]);
-                        }
-                    }
-                }
-            } else {
-                // key by key, so that no masked value is multiplied
+                            ldsm_t(b, vs + chunk_at<RB>(k * 16 + (mid >> 1) * 8 + mrow, 2 * o + (mid & 1)));
 #pragma unroll
-                for (int n = 0; n < SL / 8; ++n)
-#pragma unroll 1
-                    for (int k = 0; k < 8; ++k) {
-                        const int src = (lane & 28) | (k >> 1);
-                        const float a0 = __shfl_sync(0xFFFFFFFFu, s[n][0], src), a1 = __shfl_sync(0xFFFFFFFFu, s[n][1], src);
-                        const float b0 = __shfl_sync(0xFFFFFFFFu, s[n][2], src), b1 = __shfl_sync(0xFFFFFFFFu, s[n][3], src);
-                        const float wa = k & 1 ? a1 : a0, wb = k & 1 ? b1 : b0;
-                        const int j = j0 + n * 8 + k;
-                        const bool sa = j <= place[0] && (!p.window || j > place[0] - p.window);
-                        const bool sb = j <= place[1] && (!p.window || j > place[1] - p.window);
-                        const uint32_t row = vs - ptx::smem_addr(smem);
-#pragma unroll
-                        for (int o = 0; o < kOut; ++o) {
-                            if constexpr (!C::kCodes) {
-                                const uint32_t w = *reinterpret_cast<const uint32_t*>(smem + row + chunk_at<RB>(n * 8 + k, o) + 4 * t);
-                                const float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xFFFF0000u);
-                                if (sa) out[o][0] = fmaf(wa, v0, out[o][0]), out[o][1] = fmaf(wa, v1, out[o][1]);
-                                if (sb) out[o][2] = fmaf(wb, v0, out[o][2]), out[o][3] = fmaf(wb, v1, out[o][3]);
+                            for (int n = 0; n < NT; ++n) {
+                                mma_bf16(out[o][n], b, hi[k][n][0], hi[k][n][1]);
+                                mma_bf16(out[o][n], b, low[k][n][0], low[k][n][1]);
                             }
                         }
                     }
+            } else if constexpr (!C::kCodes) {
+                // key by key, so that no masked value is multiplied
+                const uint8_t* rows = smem + (vs - ptx::smem_addr(smem));
+#pragma unroll
+                for (int k = 0; k < KT; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll 1
+                        for (int e = 0; e < 8; ++e) {
+                            const int key = k * 16 + 8 * h + e, j = j0 + key;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                float w[2];
+                                bool sees[2];
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    w[i] = __shfl_sync(0xFFFFFFFFu, s[k][n][2 * h + i], 4 * e + t);
+                                    sees[i] = j <= place[n][i] && (!p.window || j > place[n][i] - p.window);
+                                }
+#pragma unroll
+                                for (int o = 0; o < kSteps; ++o)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const int d = 16 * o + g + 8 * (i >> 1);
+                                        const uint16_t v = *reinterpret_cast<const uint16_t*>(rows + chunk_at<RB>(key, d >> 3) + 2 * (d & 7));
+                                        if (sees[i & 1]) out[o][n][i] = fmaf(w[i & 1], bf16_bits_to_float(v), out[o][n][i]);
+                                    }
+                            }
+                        }
             }
         }
         __syncwarp();  // the stage is read; the warp's next fetch may overwrite it
         if (++stage == ST) stage = 0;
         const bool last = at.unit + 1 == at.n;
         if (last || u + 1 == units) {
-            finish(last && begun);
+            finish(last && begun, u);
             if (u + 1 < units) {
-                at.next(p, plan);
+                at = items[++at_item & 3];
                 begun = 1;
                 load_q();
             }
@@ -518,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND>::kBlocks) attn_decode_k
 // Rows of items that several blocks share: blockIdx.x names the block that began
 // one, blockIdx.y some of its rows, 8 values a thread.
 template <int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int MT, int grid) {
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p, int MT, int grid) {
     constexpr int kTh = D / 8;  // threads of a row
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -541,22 +563,31 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams p, int 
         v[4] = fmaf(w, y.x, v[4]), v[5] = fmaf(w, y.y, v[5]), v[6] = fmaf(w, y.z, v[6]), v[7] = fmaf(w, y.w, v[7]);
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int r = rec.row0 + row;
-    uint16_t* dst = p.o + static_cast<int64_t>(rec.q0 + r / p.G) * p.ldo + (rec.head * p.G + r % p.G) * p.hso + col;
+    const int r = rec.row0 + row, token = div_g(p, r);
+    uint16_t* dst = p.o + static_cast<int64_t>(rec.q0 + token) * p.ldo + (rec.head * p.G + r - token * p.G) * p.hso + col;
     *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
                                                 pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
 }
 
-template <int D, int KIND>
+template <int D, int KIND, int NT>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
-    using C = Cfg<D, KIND>;
+    using C = Cfg<D, KIND, NT>;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = attn_allow_shared(attn_decode_kernel<D, KIND>, C::kSmem, done);
+    const cudaError_t e = attn_allow_shared(attn_decode_kernel<D, KIND, NT>, C::kSmem, done);
     if (e != cudaSuccess) return e;
     const int grid = a.sm_count * C::kBlocks;
-    const cudaError_t r = w4::launch_dependent(attn_decode_kernel<D, KIND>, grid, kThreads, C::kSmem, stream,
+    const cudaError_t r = w4::launch_dependent(attn_decode_kernel<D, KIND, NT>, grid, kThreads, C::kSmem, stream,
                                                static_cast<const AttnParams&>(a));
-    return r == cudaSuccess ? launch_attn_join(a, kRows, grid, stream) : r;
+    return r == cudaSuccess ? launch_attn_join(a, C::kRows, grid, stream) : r;
+}
+
+// 16 rows a tile where a sequence has more than 8 on average: its keys are then read
+// half as often, and every step costs twice as much.
+template <int D, int KIND>
+cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
+    if constexpr (D < 256)
+        if (static_cast<int64_t>(a.T) * a.G > 8 * static_cast<int64_t>(a.B)) return launch<D, KIND, 2>(a, stream);
+    return launch<D, KIND, 1>(a, stream);
 }
 
 }  // namespace
@@ -578,23 +609,23 @@ cudaError_t launch_attn_join(const AttnArgs& a, int MT, int grid, cudaStream_t s
 
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t stream) {
     if (a.kind == FP8BS_KV_BF16) {
-        if (a.D == 64) return launch<64, FP8BS_KV_BF16>(a, stream);
-        if (a.D == 128) return launch<128, FP8BS_KV_BF16>(a, stream);
-        return launch<256, FP8BS_KV_BF16>(a, stream);
+        if (a.D == 64) return launch_rows<64, FP8BS_KV_BF16>(a, stream);
+        if (a.D == 128) return launch_rows<128, FP8BS_KV_BF16>(a, stream);
+        return launch_rows<256, FP8BS_KV_BF16>(a, stream);
     }
-    if (a.D == 64) return launch<64, FP8BS_KV_E4M3>(a, stream);
-    if (a.D == 128) return launch<128, FP8BS_KV_E4M3>(a, stream);
-    return launch<256, FP8BS_KV_E4M3>(a, stream);
+    if (a.D == 64) return launch_rows<64, FP8BS_KV_E4M3>(a, stream);
+    if (a.D == 128) return launch_rows<128, FP8BS_KV_E4M3>(a, stream);
+    return launch_rows<256, FP8BS_KV_E4M3>(a, stream);
 }
 
 size_t attn_workspace_bytes(int D, int sm_count) {
-    const size_t few = static_cast<size_t>(2 * sm_count) * 2 * attn_slot_floats(kRows, D);
+    const size_t few = static_cast<size_t>(4 * sm_count) * 2 * attn_slot_floats(16, D);
     const size_t many = static_cast<size_t>(sm_count) * 2 * attn_chunk_slot_floats(D);
-    return kWsErrorBytes + attn_records_bytes(2 * sm_count) + (few > many ? few : many) * sizeof(float);
+    return kWsErrorBytes + attn_records_bytes(4 * sm_count) + (few > many ? few : many) * sizeof(float);
 }
 
 // Rows of a sequence, on average, from which the tensor core's kernel takes the call.
-constexpr int64_t kChunkRows = 33;
+constexpr int64_t kChunkRows = 17;
 
 cudaError_t launch_attn_paged(const AttnArgs& a, cudaStream_t stream) {
     if (static_cast<int64_t>(a.T) * a.G >= kChunkRows * a.B) return launch_attn_chunk(a, stream);
