@@ -10,18 +10,22 @@
 // of 8x8 blocks makes the weights the next product's operand, outputs are
 // [dimension][row].
 //
-// Precision.  Scores, maxima, sums and outputs are fp32.  A weight enters the
-// product with the values as the sum of two bf16 numbers (off by at most 2^-16 of
+// Precision.  Scores, maxima, sums and outputs are fp32.  Over bf16 keys a weight enters
+// the product with the values as the sum of two bf16 numbers (off by at most 2^-16 of
 // it), since the memory leaves the tensor cores idle.  The maximum that weights
 // are taken against may lag by 8 in units of log2: the sums then hold values up
 // to 2^8 larger, and most slices need no rescaling.
 //
-// Codes.  An e4m3 code's bits shifted into a bf16's exponent and fraction are its
-// value times 2^-120, exactly, subnormals included; q carries 2^64 and the weights
-// 2^64 against it.  Scales are powers of two: a key's multiplies its scores, a
-// value's its weights.  The pairing of bytes that the decode gives (even bytes,
-// odd bytes) is met by a permutation of q's dimensions, and by output tiles whose
-// upper and lower halves are even and odd dimensions.
+// Codes.  e4m3 codes are exact in fp16, and the products run in it.  A row of q is
+// multiplied by the power of two that brings its largest magnitude into [2^14, 2^15):
+// exact down to 2^-31 of that, below off by at most 2^-39 of it.  A key's scale
+// multiplies its score.  A value's scale 2^e is part of its weight, 2^(x + e), the
+// maximum is taken of these (and of x - 80, so that no sum of the weights 2^x alone
+// overflows), and 2^7 more uses fp16's range: a weight is off by at most 2^-11 of
+// itself, or 2^-32 of the largest.  Values below 2^-80 of the others count less exactly.
+// A 16-bit load of two bytes of a row, transposed, gives two dimensions of a key side
+// by side: output tiles hold even dimensions in their upper and odd ones in their lower
+// half.
 #include "attn.cuh"
 #include "w4.cuh"
 
@@ -64,6 +68,13 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -87,6 +98,17 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {  // an 8x8 block of
 template <int RB>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return r * RB + ((RB >= 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+}
+
+// Codes 0 and 1 (WHICH 0) or 2 and 3 of a word as fp16 numbers.
+template <int WHICH>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+    uint32_t r;
+    if (WHICH == 0)
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+    else
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+    return r;
 }
 
 // 2^(b - 127), NaN for 255.
@@ -165,8 +187,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
     };
     auto store_scales = [&] {
         if (C::kCodes && zstage >= 0 && lane < SL) {
-            zring[zstage * 2 * SL + lane] = scale_of(zk) * (p.scale_log2 * 0x1p56f);
-            zring[zstage * 2 * SL + SL + lane] = scale_of(zv) * 0x1p64f;
+            zring[zstage * 2 * SL + lane] = scale_of(zk);
+            zring[zstage * 2 * SL + SL + lane] = zv == 255u ? __uint_as_float(0x7FFFFFFFu) : static_cast<float>(static_cast<int>(zv) - 127);
         }
         zstage = -1;
     };
@@ -225,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
     float out[kSteps][NT][4];
     float m[NT][2], l[NT][2];  // of rows 8 n + 2 t + i; sums over this lane's keys
     int place[NT][2];
+    float unit[NT][2];  // codes: what a row's scores are multiplied by
 
     auto load_q = [&] {
 #pragma unroll
@@ -243,21 +266,41 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
             const bool there = 8 * n + g < at.rows;
             const uint16_t* q = p.q;
             if (there) q += static_cast<int64_t>(at.q0 + token) * p.ldq + (at.head * p.G + r - token * p.G) * p.hsq;
-            auto big = [](uint32_t w) {  // * 2^64
-                return pack_bf16(__uint_as_float(w << 16) * 0x1p64f, __uint_as_float(w & 0xFFFF0000u) * 0x1p64f);
-            };
+            uint32_t most = 0;
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks) {
-                qf[ks][n][0] = qf[ks][n][1] = 0;
-                if (!there) continue;
-                if (C::kCodes) {
-                    const uint2 w = *reinterpret_cast<const uint2*>(q + 16 * ks + 4 * t);
-                    const uint32_t x = big(w.x), y = big(w.y);
-                    qf[ks][n][0] = __byte_perm(x, y, 0x5410), qf[ks][n][1] = __byte_perm(x, y, 0x7632);
-                } else {
-                    qf[ks][n][0] = *reinterpret_cast<const uint32_t*>(q + 16 * ks + 2 * t);
-                    qf[ks][n][1] = *reinterpret_cast<const uint32_t*>(q + 16 * ks + 8 + 2 * t);
+                uint2 w = make_uint2(0, 0);
+                if (there && C::kCodes) w = *reinterpret_cast<const uint2*>(q + 16 * ks + 4 * t);
+                if (there && !C::kCodes) {
+                    w.x = *reinterpret_cast<const uint32_t*>(q + 16 * ks + 2 * t);
+                    w.y = *reinterpret_cast<const uint32_t*>(q + 16 * ks + 8 + 2 * t);
                 }
+                qf[ks][n][0] = w.x, qf[ks][n][1] = w.y;
+                if (C::kCodes)
+                    most = max(max(most, max(w.x & 0x7FFFu, w.y & 0x7FFFu)), max(w.x >> 16 & 0x7FFFu, w.y >> 16 & 0x7FFFu));
+            }
+            if (C::kCodes) {
+                most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+                most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+                // the exponent of the factor 2^(14 - exponent of the largest), within fp32's;
+                // rows of zeros, and with an infinity or a NaN, stay
+                const int e = static_cast<int>(most >> 7);
+                const int up = most == 0 || e == 255 ? 0 : min(14 - (e - 127), 126);
+                const float factor = __int_as_float((up + 127) << 23);
+                auto narrow = [&](uint32_t w) {
+                    uint32_t r;
+                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(w & 0xFFFF0000u) * factor),
+                        "f"(__uint_as_float(w << 16) * factor));
+                    return r;
+                };
+#pragma unroll
+                for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) qf[ks][n][i] = narrow(qf[ks][n][i]);
+                // 2^-up in two factors: up is in -114 .. 126
+                const float back = __int_as_float((127 - up) << 23) * p.scale_log2;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) unit[n][i] = __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t + i));
             }
         }
     };
@@ -284,7 +327,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) most = fmaxf(most, sh.parts[w][r].x);
                 part[n][i] = m[n][i] == -INFINITY ? 0.0f : ex2(m[n][i] - most);
-                if (C::kCodes) part[n][i] *= 0x1p56f;
             }
 #pragma unroll 1
         for (int w = 0; w < kWarps; ++w) {
@@ -354,7 +396,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s[k][n][i] = 0.0f;
-            const uint32_t krow = ks + 0;
 #pragma unroll
             for (int i = 0; i < kSteps; i += C::kCodes ? 2 : 1)
 #pragma unroll
@@ -362,23 +403,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
                     uint32_t b[4];
                     const int row = k * 16 + (mid & 1) * 8 + mrow;
                     if (C::kCodes) {
-                        ldsm(b, krow + chunk_at<RB>(row, i + (mid >> 1)));
-                        const uint32_t a0[4] = {codes_even(b[0]), codes_even(b[1]), codes_odd(b[0]), codes_odd(b[1])};
-                        const uint32_t a1[4] = {codes_even(b[2]), codes_even(b[3]), codes_odd(b[2]), codes_odd(b[3])};
+                        ldsm(b, ks + chunk_at<RB>(row, i + (mid >> 1)));
+                        const uint32_t a0[4] = {code_pair<0>(b[0]), code_pair<0>(b[1]), code_pair<1>(b[0]), code_pair<1>(b[1])};
+                        const uint32_t a1[4] = {code_pair<0>(b[2]), code_pair<0>(b[3]), code_pair<1>(b[2]), code_pair<1>(b[3])};
+                        const int next = i + 1 < kSteps ? i + 1 : i;
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            mma_bf16(s[k][n], a0, qf[i][n][0], qf[i][n][1]);
-                            mma_bf16(s[k][n], a1, qf[i + 1 < kSteps ? i + 1 : i][n][0], qf[i + 1 < kSteps ? i + 1 : i][n][1]);
+                            mma_f16(s[k][n], a0, qf[i][n][0], qf[i][n][1]);
+                            mma_f16(s[k][n], a1, qf[next][n][0], qf[next][n][1]);
                         }
                     } else {
-                        ldsm(b, krow + chunk_at<RB>(row, 2 * i + (mid >> 1)));
+                        ldsm(b, ks + chunk_at<RB>(row, 2 * i + (mid >> 1)));
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma_bf16(s[k][n], b, qf[i][n][0], qf[i][n][1]);
                     }
                 }
             // scores in units of log2, masked ones at minus infinity
             const bool all = j0 + SL <= at.lowest + 1 && (p.window == 0 || j0 >= at.past - p.window);
-            float most[NT][2];
+            float most[NT][2], with[KT][NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n) most[n][0] = most[n][1] = -INFINITY;
 #pragma unroll
@@ -386,18 +428,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int key = k * 16 + 8 * h + g;
-                    const float factor = C::kCodes ? z[key] : p.scale_log2;
+                    const float scale = C::kCodes ? z[key] : 0.0f, more = C::kCodes ? z[SL + key] : 0.0f;
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            float x = s[k][n][2 * h + i] * factor;
+                            // codes: twice a factor, as their product may leave fp32's range
+                            float x = C::kCodes ? s[k][n][2 * h + i] * unit[n][i] * scale : s[k][n][2 * h + i] * p.scale_log2;
+                            float y = x + more;  // with the value's scale
                             if (!all) {
                                 const int j = j0 + key, w = place[n][i];
-                                if (j > w || (p.window && j <= w - p.window)) x = -INFINITY;
+                                if (j > w || (p.window && j <= w - p.window)) x = y = -INFINITY;
                             }
                             s[k][n][2 * h + i] = x;
-                            most[n][i] = fmaxf(most[n][i], x);
+                            if (C::kCodes) with[k][n][2 * h + i] = y;
+                            most[n][i] = fmaxf(most[n][i], C::kCodes ? fmaxf(y, x - 80.0f) : x);
                         }
                 }
             bool grown = false;
@@ -414,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
                         m[n][i] = most[n][i];
                         grown = true;
                     }
-                    from[n][i] = m[n][i] == -INFINITY ? 0.0f : m[n][i];
+                    from[n][i] = (m[n][i] == -INFINITY ? 0.0f : m[n][i]) - (C::kCodes ? 7.0f : 0.0f);
                 }
             if (__any_sync(0xFFFFFFFFu, grown)) {
 #pragma unroll
@@ -431,23 +476,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
             for (int k = 0; k < KT; ++k)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float value = C::kCodes ? z[SL + k * 16 + 8 * h + g] : 1.0f;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float w[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float x = s[k][n][2 * h + i];
-                            w[i] = ex2(x - from[n][i]);
+                            w[i] = ex2(s[k][n][2 * h + i] - from[n][i]);
                             l[n][i] += w[i];
-                            // a masked key's scale may be a NaN
-                            if (C::kCodes) w[i] = !all && x == -INFINITY ? 0.0f : w[i] * value;
+                            if (C::kCodes) w[i] = ex2(with[k][n][2 * h + i] - from[n][i]);
                             s[k][n][2 * h + i] = w[i];
                         }
-                        const uint32_t both = pack_bf16(w[0], w[1]);
-                        hi[k][n][h] = transposed(both);
-                        low[k][n][h] = transposed(pack_bf16(w[0] - __uint_as_float(both << 16),
-                                                            w[1] - __uint_as_float(both & 0xFFFF0000u)));
+                        if (C::kCodes) {
+                            uint32_t both;
+                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(both) : "f"(w[1]), "f"(w[0]));
+                            hi[k][n][h] = transposed(both);
+                        } else {
+                            const uint32_t both = pack_bf16(w[0], w[1]);
+                            hi[k][n][h] = transposed(both);
+                            low[k][n][h] = transposed(pack_bf16(w[0] - __uint_as_float(both << 16),
+                                                                w[1] - __uint_as_float(both & 0xFFFF0000u)));
+                        }
                     }
                 }
             bool odd = false;  // a value that is not finite where some row masks its key
@@ -471,15 +519,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
                         uint32_t b[4];
                         if (C::kCodes) {
                             ldsm_t(b, vs + chunk_at<RB>(k * 16 + (mid & 1) * 8 + mrow, o + (mid >> 1)));
-                            const uint32_t a0[4] = {codes_even(b[0]), codes_odd(b[0]), codes_even(b[1]), codes_odd(b[1])};
-                            const uint32_t a1[4] = {codes_even(b[2]), codes_odd(b[2]), codes_even(b[3]), codes_odd(b[3])};
+                            // a word: (d, d + 1) of a key, then of the next; wanted: pairs of keys
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) b[e] = __byte_perm(b[e], 0, 0x3120);
+                            const uint32_t a0[4] = {code_pair<0>(b[0]), code_pair<1>(b[0]), code_pair<0>(b[1]), code_pair<1>(b[1])};
+                            const uint32_t a1[4] = {code_pair<0>(b[2]), code_pair<1>(b[2]), code_pair<0>(b[3]), code_pair<1>(b[3])};
                             const int next = o + 1 < kSteps ? o + 1 : o;
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                mma_bf16(out[o][n], a0, hi[k][n][0], hi[k][n][1]);
-                                mma_bf16(out[next][n], a1, hi[k][n][0], hi[k][n][1]);
-                                mma_bf16(out[o][n], a0, low[k][n][0], low[k][n][1]);
-                                mma_bf16(out[next][n], a1, low[k][n][0], low[k][n][1]);
+                                mma_f16(out[o][n], a0, hi[k][n][0], hi[k][n][1]);
+                                mma_f16(out[next][n], a1, hi[k][n][0], hi[k][n][1]);
                             }
                         } else {
                             ldsm_t(b, vs + chunk_at<RB>(k * 16 + (mid >> 1) * 8 + mrow, 2 * o + (mid & 1)));
@@ -537,36 +586,71 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
     }
 }
 
-// Rows of items that several blocks share: blockIdx.x names the block that began
-// one, blockIdx.y some of its rows, 8 values a thread.
+// Rows of items that several blocks share: blockIdx.x names the block that began one,
+// 8 values a thread.  An item's parts are dealt to up to 8 threads of the same values,
+// each of which keeps a maximum of its own; they meet in shared memory, in the order
+// of the parts.
+constexpr int kJoin = 256;
 template <int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p, int MT, int grid) {
-    constexpr int kTh = D / 8;  // threads of a row
+__global__ void __launch_bounds__(kJoin) attn_join_kernel(const __grid_constant__ AttnParams p, int MT, int grid) {
+    constexpr int kPer = D / 8, kLanes = kJoin / kPer;  // threads of a row; rows that the block has threads for
+    __shared__ float met[kJoin][11];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const AttnSplit rec = reinterpret_cast<const AttnSplit*>(p.ws)[blockIdx.x];
-    const int row = blockIdx.y * (256 / kTh) + threadIdx.x / kTh, col = threadIdx.x % kTh * 8;
-    if (row >= rec.rows) return;
+    if (rec.rows == 0) return;
     const int first = blockIdx.x, n = rec.last - first + 1;
-    auto slot = [&](int i) { return attn_slot(p, grid, MT, D, first + i, i == 0); };
-    float most = -INFINITY;
-    for (int i = 0; i < n; ++i) most = fmaxf(most, slot(i)[MT * D + row]);
-    float sum = 0.0f, v[8] = {};
+    int ways = 1;
+    while (ways < 8 && 2 * ways < n && ways * rec.rows < 2 * kLanes) ways *= 2;
+    const int col = threadIdx.x % kPer * 8, lane = threadIdx.x / kPer;
+    const int way = lane % ways, per = (n + ways - 1) / ways, rows = kLanes / ways;
+    for (int row0 = blockIdx.y * rows; row0 < rec.rows; row0 += gridDim.y * rows) {
+        const int row = row0 + lane / ways;
+        float most = -INFINITY, sum = 0.0f, v[8] = {};
+        if (row < rec.rows) {
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float* s = slot(i);
-        const float mi = s[MT * D + row], w = mi == -INFINITY ? 0.0f : ex2(mi - most);
-        const float4 x = *reinterpret_cast<const float4*>(s + row * D + col);
-        const float4 y = *reinterpret_cast<const float4*>(s + row * D + col + 4);
-        sum = fmaf(w, s[MT * D + MT + row], sum);
-        v[0] = fmaf(w, x.x, v[0]), v[1] = fmaf(w, x.y, v[1]), v[2] = fmaf(w, x.z, v[2]), v[3] = fmaf(w, x.w, v[3]);
-        v[4] = fmaf(w, y.x, v[4]), v[5] = fmaf(w, y.y, v[5]), v[6] = fmaf(w, y.z, v[6]), v[7] = fmaf(w, y.w, v[7]);
+            for (int i = way * per; i < min(n, (way + 1) * per); ++i) {
+                const float* s = attn_slot(p, grid, MT, D, first + i, i == 0);
+                const float m = s[MT * D + row], l = s[MT * D + MT + row];
+                const float4 x = *reinterpret_cast<const float4*>(s + row * D + col);
+                const float4 y = *reinterpret_cast<const float4*>(s + row * D + col + 4);
+                const float top = fmaxf(most, m), at = top == -INFINITY ? 0.0f : top;
+                const float keep = ex2(most - at), w = ex2(m - at);
+                most = top;
+                sum = fmaf(l, w, sum * keep);
+                v[0] = fmaf(x.x, w, v[0] * keep), v[1] = fmaf(x.y, w, v[1] * keep);
+                v[2] = fmaf(x.z, w, v[2] * keep), v[3] = fmaf(x.w, w, v[3] * keep);
+                v[4] = fmaf(y.x, w, v[4] * keep), v[5] = fmaf(y.y, w, v[5] * keep);
+                v[6] = fmaf(y.z, w, v[6] * keep), v[7] = fmaf(y.w, w, v[7] * keep);
+            }
+        }
+        if (ways > 1) {
+            float* mine = met[threadIdx.x];
+            __syncthreads();
+            mine[0] = most, mine[1] = sum;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mine[2 + i] = v[i];
+            __syncthreads();
+            if (way == 0) {
+                for (int j = 1; j < ways; ++j) {
+                    const float* o = met[threadIdx.x + j * kPer];
+                    const float top = fmaxf(most, o[0]), at = top == -INFINITY ? 0.0f : top;
+                    const float keep = ex2(most - at), w = ex2(o[0] - at);
+                    most = top;
+                    sum = fmaf(o[1], w, sum * keep);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = fmaf(o[2 + i], w, v[i] * keep);
+                }
+            }
+        }
+        if (way == 0 && row < rec.rows) {
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const int r = rec.row0 + row, token = div_g(p, r);
+            uint16_t* dst = p.o + static_cast<int64_t>(rec.q0 + token) * p.ldo + (rec.head * p.G + r - token * p.G) * p.hso + col;
+            *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
+                                                        pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
+        }
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int r = rec.row0 + row, token = div_g(p, r);
-    uint16_t* dst = p.o + static_cast<int64_t>(rec.q0 + token) * p.ldo + (rec.head * p.G + r - token * p.G) * p.hso + col;
-    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
-                                                pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
 }
 
 template <int D, int KIND, int NT>
@@ -594,9 +678,10 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_attn_join(const AttnArgs& a, int MT, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    const int rows = 256 / (a.D / 8);
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>((MT + rows - 1) / rows));
-    cfg.blockDim = dim3(256);
+    const int rows = kJoin / (a.D / 8);  // of a pass, where nothing is dealt out
+    const int most = MT * 8 / rows;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>(most < 1 ? 1 : most > 16 ? 16 : most));
+    cfg.blockDim = dim3(kJoin);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
