@@ -47,7 +47,7 @@ struct Cfg {
     // registers of a softmax thread and of the others, where the launch's 128 are dealt
     // out anew: 2 * 128 * (184 + 72) is what 512 threads of 128 have
     static constexpr int kMoreRegs = 184, kFewRegs = 72;
-    static constexpr int kLoadWarps = kThreads / 32 - kSoft - 1;
+    static constexpr int kLoadWarps = kThreads / 32 - kSoft - 2;
     static constexpr int kLoaders = kLoadWarps * 32;
     static constexpr int kTileBytes = kKeys * D * 2;
     static constexpr int kStages = 4;
@@ -70,19 +70,41 @@ struct Shared {
     int mark[kMarks];
 };
 
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
+// One lane of the warp, the same every time.
+__device__ __forceinline__ bool ptx_elect() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
 }
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
+
+// Steps of 16 along the products' inner dimension, issued by one elected lane: A and B
+// from shared memory (descriptors that advance by `step` every time and by `part` more
+// every fourth time), or A from tensor memory (8 columns a step).
+template <int STEPS>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t a_part, uint32_t b_part, uint32_t idesc) {
+    if (ptx_elect()) {
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                "l"(a + (k >> 2) * a_part + (k & 3) * 2), "l"(b + (k >> 2) * b_part + (k & 3) * 2), "r"(idesc), "r"(k > 0 ? 1 : 0)
+                : "memory");
+    }
+    __syncwarp();
+}
+template <int STEPS>
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if (ptx_elect()) {
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                "r"(a + 8 * k), "l"(b + 128 * k), "r"(idesc), "r"(k > 0 ? 1u : acc)
+                : "memory");
+    }
+    __syncwarp();
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t* r) {
@@ -335,7 +357,7 @@ template <int D>
 __device__ __forceinline__ void check_units(const AttnParams& p, Shared& sh, uint8_t* ring) {
     using C = Cfg<D, FP8BS_KV_BF16>;
     constexpr int kThreads = C::kLoaders - 32, kPer = D / 8;
-    const int tid = threadIdx.x - (C::kSoft + 2) * 32;
+    const int tid = threadIdx.x - (C::kSoft + 3) * 32;
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     Place at;
     bool alive = at.start(p, sh);
@@ -392,7 +414,7 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, uin
     constexpr int kRowStep = C::kLoaders / kPer;       // rows between a thread's pieces
     constexpr int kMine = (C::kKeys + kRowStep - 1) / kRowStep;
     constexpr int kLook = (C::kKeys + C::kLoaders - 1) / C::kLoaders;
-    const int tid = threadIdx.x - (C::kSoft + 1) * 32;
+    const int tid = threadIdx.x - (C::kSoft + 2) * 32;
     // threads past the last whole row copy nothing: their first row is past the unit
     const int row0 = tid < kRowStep * kPer ? tid / kPer : C::kKeys, piece = tid % kPer;
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
@@ -518,72 +540,114 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, uin
     }
 }
 
+// The order of the products, in steps: the watcher waits for what a step needs and
+// lets the issuer go through a hardware barrier, as a probe of a barrier in shared
+// memory from the warp that issues would wait behind the products' own reads.  A step's
+// barrier comes round after eight steps; the watcher is never that far ahead, as it
+// waits for what follows from the issuer's steps.
+//   two streams: (first scores of both), then for each unit and stream
+//     [weights, values there; the next unit's keys, the next item's queries]
+//     O += P V, next S = Q K^T
+//   one stream: (first scores), then for each unit
+//     [the next unit's keys, the next item's queries]  next S = Q K^T in the other buffer
+//     [weights, values there]                          O += P V
+constexpr uint32_t kStepBarrier = 2, kStepBarriers = 8;
+
 template <int D, int KIND>
-__device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, uint32_t query,
-                                               uint32_t ring) {
+__device__ __forceinline__ void watch(const AttnParams& p, Shared& sh) {
+    using C = Cfg<D, KIND>;
+    const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
+    Place at;
+    uint32_t step = 0;
+    bool alive = at.start(p, sh);  // once that fails, every step is let go all the same
+    auto need = [&](uint64_t* bar, uint32_t parity) {
+        if (alive) alive = __all_sync(0xFFFFFFFFu, wait(sh, bar, parity, p));
+    };
+    auto full = [&](uint32_t fill) { need(&sh.full[fill % C::kStages], (fill / C::kStages) & 1); };
+    auto go = [&] { ptx::named_arrive(kStepBarrier + step++ % kStepBarriers, 64); };
+    uint32_t items = 0;
+    need(&sh.query[0], 0);
+    if (C::kStreams == 2) need(&sh.query[1], 0);
+    full(0);
+    go();
+#pragma unroll 1
+    for (int u = 0; u < units; ++u) {
+        const uint32_t fv = 2 * static_cast<uint32_t>(u) + 1, fk = fv + 1;
+        const bool more = u + 1 < units, last = at.unit + 1 == at.n;
+        if (more && alive) alive = at.next(p, sh);
+        items += last;
+        if (C::kStreams == 2) {
+            full(fv);
+            if (more) full(fk);
+            if (more && last) need(&sh.query[0], items & 1);
+            need(&sh.weights[0], u & 1);
+            go();
+            if (more && last) need(&sh.query[1], items & 1);
+            need(&sh.weights[1], u & 1);
+            go();
+        } else {
+            if (more) {
+                full(fk);
+                if (last) need(&sh.query[0], items & 1);
+                go();
+            }
+            full(fv);
+            need(&sh.weights[u & 1], (u >> 1) & 1);
+            go();
+        }
+    }
+}
+
+template <int D, int KIND>
+__device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, uint32_t query, uint32_t ring) {
     using C = Cfg<D, KIND>;
     constexpr uint32_t kScoreDesc = idesc_bf16(C::kKeys, 0), kValueDesc = idesc_bf16(D, 1);
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
-    Place at;
-    if (!at.start(p, sh)) return;
-    uint32_t items = 0;  // whose queries have been waited for
-    auto tile = [&](uint32_t fill) { return ring + fill % C::kStages * C::kTileBytes; };
     const uint32_t tmem = sh.tmem;
-    // the whole warp goes on together, or returns together
-    auto await = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(sh, bar, parity, p)) != 0; };
-    auto full = [&](uint32_t fill) { return await(&sh.full[fill % C::kStages], (fill / C::kStages) & 1); };
-
+    uint32_t step = 0;
+    auto come = [&] {
+        ptx::named_sync(kStepBarrier + step++ % kStepBarriers, 64);
+        ptx::tc_fence_after();
+    };
+    auto tile = [&](uint32_t fill) { return ring + fill % C::kStages * C::kTileBytes; };
     auto scores = [&](int stream, int buffer, uint32_t keys, int rows) {
-        if (rows > stream * kRows) {
-            const uint32_t q = query + stream * kRows * D * 2;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t in = (k & 3) * 32;
-                mma_f16_ss(tmem + buffer * 128, ptx::smem_desc_sw128(q + (k >> 2) * (kRows * 128) + in),
-                           ptx::smem_desc_sw128(keys + (k >> 2) * (C::kKeys * 128) + in), kScoreDesc, k > 0);
-            }
-        }
+        if (rows > stream * kRows)
+            mma_scores<D / 16>(tmem + buffer * 128, ptx::smem_desc_sw128(query + stream * kRows * D * 2), ptx::smem_desc_sw128(keys),
+                               kRows * 128 / 16, C::kKeys * 128 / 16, kScoreDesc);
         ptx::mma_commit_warp(&sh.scores[buffer]);
     };
     auto values = [&](int stream, int buffer, uint32_t vals, int rows, bool first) {
-        if (rows > stream * kRows) {
-#pragma unroll
-            for (int k = 0; k < C::kKeys / 16; ++k)
-                mma_f16_ts(tmem + C::kOut + stream * D, tmem + buffer * 128 + k * 8,
-                           desc_mn(vals + k * 2048, C::kKeys * 128), kValueDesc, !(first && k == 0));
-        }
+        if (rows > stream * kRows)
+            mma_values<C::kKeys / 16>(tmem + C::kOut + stream * D, tmem + buffer * 128, desc_mn(vals, C::kKeys * 128), kValueDesc,
+                                      !first);
         ptx::mma_commit_warp(&sh.joined[stream]);
     };
 
+    come();
+    // (the watcher has seen that the items which are read here are known)
+    int item = 0, unit = sh.plan.share.unit, n = sh.items[0].n, rows = sh.items[0].rows;
     bool first = true;  // the unit is its item's first here
-    int rows = at.rows;
-    if (!await(&sh.query[0], 0) || (C::kStreams == 2 && !await(&sh.query[1], 0)) || !full(0)) return;
-    ptx::tc_fence_after();
 #pragma unroll 1
     for (int s = 0; s < C::kStreams; ++s) scores(s, s, tile(0), rows);
     ptx::mma_commit_warp(&sh.empty[0]);
 #pragma unroll 1
     for (int u = 0; u < units; ++u) {
         const uint32_t fv = 2 * static_cast<uint32_t>(u) + 1, fk = fv + 1;
-        const bool more = u + 1 < units, last = at.unit + 1 == at.n;
+        const bool more = u + 1 < units, last = unit + 1 == n;
         const int rows_now = rows;
-        if (more) {
-            if (!at.next(p, sh)) return;
-            rows = at.rows;
-            items += last;
+        come();
+        if (more && last) {
+            ++item;
+            n = sh.items[item & (kItems - 1)].n, rows = sh.items[item & (kItems - 1)].rows;
         }
+        unit = last ? 0 : unit + 1;
         if constexpr (C::kStreams == 2) {
-            if (!full(fv)) return;
 #pragma unroll 1
             for (int s = 0; s < 2; ++s) {
-                if (!await(&sh.weights[s], u & 1)) return;
-                ptx::tc_fence_after();
+                if (s == 1) come();
                 values(s, s, tile(fv), rows_now, first);
                 if (s == 1) ptx::mma_commit_warp(&sh.empty[fv % C::kStages]);
                 if (more) {
-                    if (last && !await(&sh.query[s], items & 1)) return;
-                    if (s == 0 && !full(fk)) return;
-                    ptx::tc_fence_after();
                     scores(s, s, tile(fk), rows);
                     if (s == 1) ptx::mma_commit_warp(&sh.empty[fk % C::kStages]);
                 }
@@ -591,19 +655,37 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, 
         } else {
             const int b = u & 1;
             if (more) {
-                if (last && !await(&sh.query[0], items & 1)) return;
-                if (!full(fk)) return;
-                ptx::tc_fence_after();
                 scores(0, b ^ 1, tile(fk), rows);
                 ptx::mma_commit_warp(&sh.empty[fk % C::kStages]);
+                come();
             }
-            if (!full(fv) || !await(&sh.weights[b], (u >> 1) & 1)) return;
-            ptx::tc_fence_after();
             values(0, b, tile(fv), rows_now, first);
             ptx::mma_commit_warp(&sh.empty[fv % C::kStages]);
         }
         first = last;
     }
+}
+
+// Minus infinity in the place of the scores of keys past `hi` and before `lo`, in tensor
+// memory: a short loop.  (This and all else that does not run for every unit is kept
+// short: its code comes from far, as the loops over units fill the instruction cache.
+// Masks, unrolled over a row in registers, took 12 us a unit.)
+template <int KEYS>
+__device__ __forceinline__ void mask_scores(uint32_t scores, int hi, int lo) {
+#pragma unroll 1
+    for (int c = 0; c < KEYS; c += 16) {
+        uint32_t s[16];
+        ptx::tmem_ld_32x32b_x16(scores + c, s);
+        ptx::tmem_wait_ld();
+        const int h = min(hi - c, 15), l = lo - c;
+        uint32_t seen = h < 0 ? 0u : 0xFFFFu >> (15 - h);  // bit i: this row sees key c + i
+        if (l > 0) seen = l > 15 ? 0u : seen >> l << l;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (!(seen >> i & 1)) s[i] = 0xFF800000u;
+        tmem_st16(scores + c, s);
+    }
+    ptx::tmem_wait_st();
 }
 
 // The values that are not finite, among the keys that a row sees in the item's units
@@ -652,7 +734,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
 
     auto fetch_query = [&] {
         constexpr int kPer = D / 8;
-#pragma unroll 2
+#pragma unroll 1
         for (int i = 0; i < kRows * kPer / 128; ++i) {
             const int r = (i * 128 + t) / kPer, c = t % kPer;
             const int packed = at.row0 + stream * kRows + r, token = div_g(p, packed);
@@ -690,24 +772,12 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
         if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.scores[buffer], parity, p))) return;
         ptx::tc_fence_after();
         if (active) {
+            const bool all = j0 + C::kKeys - 1 <= place && (p.window == 0 || j0 > place - p.window);
+            if (!__all_sync(0xFFFFFFFFu, all)) mask_scores<C::kKeys>(scores, place - j0, p.window ? place - p.window - j0 + 1 : 0);
             float s[C::kKeys];
 #pragma unroll
             for (int i = 0; i < C::kKeys / 32; ++i) tmem_ld32(scores + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
             ptx::tmem_wait_ld();
-            const bool all = j0 + C::kKeys - 1 <= place && (p.window == 0 || j0 > place - p.window);
-            if (!__all_sync(0xFFFFFFFFu, all)) {
-                // bit i of a word: this row sees key 32 c + i
-                const int hi = min(place - j0, C::kKeys - 1), lo = p.window ? max(place - p.window - j0 + 1, 0) : 0;
-#pragma unroll
-                for (int c = 0; c < C::kKeys / 32; ++c) {
-                    const int h = min(hi - 32 * c, 31), l = lo - 32 * c;
-                    uint32_t seen = h < 0 ? 0u : 0xFFFFFFFFu >> (31 - h);
-                    if (l > 0) seen = l > 31 ? 0u : seen >> l << l;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!(seen >> i & 1)) s[32 * c + i] = -INFINITY;
-                }
-            }
             // eight chains, so that none is long
             float tops[8];
 #pragma unroll
@@ -728,13 +798,13 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
                     if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.joined[stream], (u - 1) & 1, p))) return;
                     ptx::tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(out + c, o);
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        ptx::tmem_ld_32x32b_x16(out + c, o);
                         ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
-                        tmem_st32(out + c, o);
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
+                        tmem_st16(out + c, o);
                     }
                     ptx::tmem_wait_st();
                 }
@@ -777,26 +847,26 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
         const bool whole = last && begun;
         if (active) {
             const bool odd = *reinterpret_cast<volatile int*>(&sh.mark[was.item & (kMarks - 1)]) == was.item + 1;
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : __frcp_rn(sum);
             uint16_t* dst = p.o + static_cast<int64_t>(was.q0 + token) * p.ldo + (was.head * p.G + packed - token * p.G) * p.hso;
             float* slot = attn_slot(p, gridDim.x, C::kTile, D, blockIdx.x, begun);
             const int at_row = stream * kRows + row;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_ld32(out + c, reinterpret_cast<uint32_t*>(o));
+            for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                ptx::tmem_ld_32x32b_x16(out + c, o);
                 ptx::tmem_wait_ld();
-                if (there && whole) {
+                if (!there) continue;
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        *reinterpret_cast<uint4*>(dst + c + i) =
-                            make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
-                                       pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
-                } else if (there) {
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+                if (whole) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<float4*>(slot + at_row * D + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    for (int i = 0; i < 8; ++i) o[i] = pack_bf16(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
                 }
+                uint4* to = whole ? reinterpret_cast<uint4*>(dst + c) : reinterpret_cast<uint4*>(slot + at_row * D + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < 2 || !whole) to[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
             if (there && !whole) {
                 slot[C::kTile * D + at_row] = most;
@@ -854,8 +924,9 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
         }
         if (warp < C::kSoft) weigh<D, KIND>(p, sh, query);
         else if (warp == C::kSoft) issue_products<D, KIND>(p, sh, ptx::smem_addr(query), ptx::smem_addr(ring));
+        else if (warp == C::kSoft + 1) watch<D, KIND>(p, sh);
         else if constexpr (C::kCodes) widen_units<D>(p, sh, ring);
-        else if (warp == C::kSoft + 1) copy_units<D>(p, sh, ring, &mk, &mv);
+        else if (warp == C::kSoft + 2) copy_units<D>(p, sh, ring, &mk, &mv);
         else check_units<D>(p, sh, ring);
         ptx::cp_async_wait_all();
         if (warp == C::kSoft) {
