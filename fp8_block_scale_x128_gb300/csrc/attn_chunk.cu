@@ -42,17 +42,23 @@ struct Cfg {
     static constexpr int kStreams = D == 256 ? 1 : 2;
     static constexpr int kTile = kStreams * kRows;
     static constexpr int kKeys = D == 256 ? 64 : 128;  // of a unit
-    static constexpr int kSoft = kStreams * 4;         // softmax warps
+    static constexpr int kSoft = kStreams * 4;         // softmax warps, a thread a row (two
+    // threads a row, each of half the keys, took 830 us where this takes 720: the softmax
+    // of the two streams together is bound by its instructions, not by one's latency)
     static constexpr int kThreads = kStreams == 2 ? 512 : 384;
-    // registers of a softmax thread and of the others, where the launch's 128 are dealt
-    // out anew: 2 * 128 * (184 + 72) is what 512 threads of 128 have
+    // Registers of a softmax thread and of the others, where the launch's are dealt out
+    // anew: 256 (184 + 72) of 512 * 128.
+    static constexpr bool kDeal = kStreams == 2;
     static constexpr int kMoreRegs = 184, kFewRegs = 72;
+    static_assert(!kDeal || kSoft * 32 * kMoreRegs + (kThreads - kSoft * 32) * kFewRegs <= kThreads * (65536 / kThreads / 8 * 8),
+                  "more registers than the launch has would be waited for without end");
     static constexpr int kLoadWarps = kThreads / 32 - kSoft - 2;
     static constexpr int kLoaders = kLoadWarps * 32;
     static constexpr int kTileBytes = kKeys * D * 2;
     static constexpr int kStages = 4;
     static constexpr int kQBytes = kTile * D * 2;
-    static constexpr int kSmem = kQBytes + kStages * kTileBytes + 1024;
+    static constexpr int kOutBytes = 1024;  // of a softmax warp: outputs on their way
+    static constexpr int kSmem = kQBytes + kStages * kTileBytes + kSoft * kOutBytes + 1024;
     static constexpr uint32_t kOut = 256;  // first column of the outputs
 };
 
@@ -163,17 +169,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* r) {
         : "r"(a)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-        "%30,%31};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(a)
-        : "memory");
-}
 
 // Waits for a phase, with a limit; false when it ran out here or anywhere in the
 // block.  (Inline: a call would have to keep a row's scores over it.)
@@ -278,9 +273,8 @@ __device__ __forceinline__ void widen(const uint4& c, uint32_t scale, uint4& lo,
     hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-__device__ __forceinline__ bool odd_pair(uint32_t w) {
-    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
+// Bits 15 and 31: whether the lower and the upper bf16 of a word have no finite value.
+__device__ __forceinline__ uint32_t odd_pair(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
 // bf16 tiles: one warp issues boxes (a lane each) of up to a page's slots.  A unit's
 // values that some row masks land on a barrier of their own, and the other loader
@@ -290,9 +284,9 @@ template <int D>
 __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint8_t* ring,
                                            const CUtensorMap* mk, const CUtensorMap* mv) {
     using C = Cfg<D, FP8BS_KV_BF16>;
-    constexpr int kMost = C::kKeys / 32;  // boxes of a lane, each for all parts of a row
+    constexpr int kParts = D / 64, kMost = C::kKeys * kParts / 32;  // boxes of a lane
     const int lane = threadIdx.x & 31;
-    const int rows = min(1 << p.page_log2, C::kKeys), boxes = C::kKeys / rows;
+    const int rows = min(1 << p.page_log2, C::kKeys), boxes = C::kKeys / rows * kParts;
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     Place at;
     publish<C::kTile, C::kKeys>(p, sh, 0);
@@ -303,7 +297,8 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
     auto find = [&] {
 #pragma unroll
         for (int i = 0; i < kMost; ++i) {
-            const int j = (at.lo + at.unit) * C::kKeys + (lane + 32 * i) * rows;
+            if (32 * i >= boxes) break;
+            const int j = (at.lo + at.unit) * C::kKeys + (lane + 32 * i) / kParts * rows;
             page[i] = -1;
             if (lane + 32 * i < boxes && j < at.past && j + rows > at.first) {
                 int id;
@@ -318,7 +313,10 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
         const bool check = !attn_sees_all<C::kKeys>(p, at);
         int now[kMost], count = 0;
 #pragma unroll
-        for (int i = 0; i < kMost; ++i) now[i] = page[i], count += __popc(__ballot_sync(0xFFFFFFFFu, page[i] >= 0));
+        for (int i = 0; i < kMost; ++i) {
+            if (32 * i >= boxes) break;
+            now[i] = page[i], count += __popc(__ballot_sync(0xFFFFFFFFu, page[i] >= 0));
+        }
         if (u + 1 < units) {
             const int item = at.item;
             alive &= at.next(p, sh);
@@ -332,17 +330,18 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
                 alive = __all_sync(0xFFFFFFFFu, wait(sh, &sh.empty[stage], ((fill / C::kStages) - 1) & 1, p));
             if (!alive) break;
             uint64_t* bar = kv && check ? &sh.raw[stage >> 1] : &sh.full[stage];
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, count * rows * D * 2);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, count * rows * 128);
             __syncwarp();
             uint8_t* tile = ring + stage * C::kTileBytes;
 #pragma unroll
-            for (int i = 0; i < kMost; ++i)
+            for (int i = 0; i < kMost; ++i) {
+                if (32 * i >= boxes) break;
                 if (now[i] >= 0) {
-                    const int r = (lane + 32 * i) * rows, slot = (j0 + r) & ((1 << p.page_log2) - 1);
-#pragma unroll
-                    for (int part = 0; part < D / 64; ++part)
-                        tma_box(tile + part * (C::kKeys * 128) + r * 128, kv ? mv : mk, 64 * part, slot, head, now[i], bar);
+                    const int q = lane + 32 * i, part = q % kParts, r = q / kParts * rows;
+                    tma_box(tile + part * (C::kKeys * 128) + r * 128, kv ? mv : mk, 64 * part, (j0 + r) & ((1 << p.page_log2) - 1),
+                            head, now[i], bar);
                 }
+            }
         }
     }
     if (!alive) {  // what is under way lands before the block leaves
@@ -379,17 +378,14 @@ __device__ __forceinline__ void check_units(const AttnParams& p, Shared& sh, uin
                         continue;
                     }
                     uint32_t w[4] = {q->x, q->y, q->z, q->w};
-                    bool found = false;
-#pragma unroll
+                    if (!((odd_pair(w[0]) | odd_pair(w[1])) | (odd_pair(w[2]) | odd_pair(w[3])))) continue;
+#pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
-                        found |= odd_pair(w[k]);
-                        if ((w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u;
-                        if ((w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0x0000FFFFu;
+                        const uint32_t x = odd_pair(w[k]);
+                        w[k] &= ((x >> 15 & 1) - 1 & 0xFFFFu) | ((x >> 31) - 1 & 0xFFFF0000u);
+                        reinterpret_cast<uint32_t*>(q)[k] = w[k];
                     }
-                    if (found) {
-                        *q = make_uint4(w[0], w[1], w[2], w[3]);
-                        sh.mark[at.item & (kMarks - 1)] = at.item + 1;
-                    }
+                    sh.mark[at.item & (kMarks - 1)] = at.item + 1;
                 }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
@@ -543,7 +539,7 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, uin
 // The order of the products, in steps: the watcher waits for what a step needs and
 // lets the issuer go through a hardware barrier, as a probe of a barrier in shared
 // memory from the warp that issues would wait behind the products' own reads.  A step's
-// barrier comes round after eight steps; the watcher is never that far ahead, as it
+// barrier comes round after four steps; the watcher is never further ahead, as it
 // waits for what follows from the issuer's steps.
 //   two streams: (first scores of both), then for each unit and stream
 //     [weights, values there; the next unit's keys, the next item's queries]
@@ -551,7 +547,7 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, uin
 //   one stream: (first scores), then for each unit
 //     [the next unit's keys, the next item's queries]  next S = Q K^T in the other buffer
 //     [weights, values there]                          O += P V
-constexpr uint32_t kStepBarrier = 2, kStepBarriers = 8;
+constexpr uint32_t kStepBarrier = 2, kStepBarriers = 4;
 
 template <int D, int KIND>
 __device__ __forceinline__ void watch(const AttnParams& p, Shared& sh) {
@@ -720,29 +716,33 @@ __device__ __forceinline__ void add_odd(const AttnParams& p, Cursor c, int from,
 }
 
 template <int D, int KIND>
-__device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* query) {
+__device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* query, uint8_t* way) {
     using C = Cfg<D, KIND>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, stream = warp >> 2;
-    const int row = (warp & 3) * 32 + lane;  // of the stream
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3, stream = warp >> 2;
+    const int row = quarter * 32 + lane;  // of the stream
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     const uint32_t out = sh.tmem + C::kOut + stream * D + lanes;
-    uint8_t* mine = query + stream * kRows * D * 2;
-    const int t = threadIdx.x & 127;
+    const uint32_t mine = ptx::smem_addr(query) + stream * kRows * D * 2 + row * 128;  // this row of the queries
+    uint8_t* staged = way + warp * C::kOutBytes;
     Place at;
     if (!at.start(p, sh)) return;
 
+    // a thread copies its row
+    auto query_row = [&](int* token, int* head) {
+        // rows that are not there look like the last one and are not written
+        const int packed = at.row0 + min(stream * kRows + row, at.rows - 1);
+        *token = div_g(p, packed);
+        *head = at.head * p.G + packed - *token * p.G;
+    };
     auto fetch_query = [&] {
-        constexpr int kPer = D / 8;
-#pragma unroll 1
-        for (int i = 0; i < kRows * kPer / 128; ++i) {
-            const int r = (i * 128 + t) / kPer, c = t % kPer;
-            const int packed = at.row0 + stream * kRows + r, token = div_g(p, packed);
-            const bool there = stream * kRows + r < at.rows;
-            const uint16_t* src = p.q;
-            if (there)
-                src += static_cast<int64_t>(at.q0 + token) * p.ldq + (at.head * p.G + packed - token * p.G) * p.hsq + 8 * c;
-            cp_async16_zfill(ptx::smem_addr(mine + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)), src, there);
+        int token, head;
+        query_row(&token, &head);
+        const bool there = stream * kRows + row < at.rows;
+        const uint16_t* src = p.q + static_cast<int64_t>(at.q0 + token) * p.ldq + head * p.hsq;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+            cp_async16_zfill(mine + (c >> 3) * (kRows * 128) + (((c & 7) ^ (row & 7)) << 4), src + 8 * c, there);
         }
         cp_commit();
     };
@@ -763,17 +763,17 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
         const uint32_t parity = C::kStreams == 2 ? u & 1 : (u >> 1) & 1;
         const uint32_t scores = sh.tmem + buffer * 128 + lanes;
         const bool active = at.rows > stream * kRows;
-        const bool there = stream * kRows + row < at.rows;
-        // rows that are not there look like the last one and are not written
-        const int packed = at.row0 + min(stream * kRows + row, at.rows - 1);
-        const int token = div_g(p, packed), place = at.base + token;
         const int j0 = (at.lo + at.unit) * C::kKeys;
         const bool last = at.unit + 1 == at.n, done = last || u + 1 == units;
         if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.scores[buffer], parity, p))) return;
         ptx::tc_fence_after();
         if (active) {
-            const bool all = j0 + C::kKeys - 1 <= place && (p.window == 0 || j0 > place - p.window);
-            if (!__all_sync(0xFFFFFFFFu, all)) mask_scores<C::kKeys>(scores, place - j0, p.window ? place - p.window - j0 + 1 : 0);
+            if (!attn_sees_all<C::kKeys>(p, at)) {
+                int token, head;
+                query_row(&token, &head);
+                const int hi = at.base + token - j0;
+                mask_scores<C::kKeys>(scores, hi, p.window ? hi - p.window + 1 : 0);
+            }
             float s[C::kKeys];
 #pragma unroll
             for (int i = 0; i < C::kKeys / 32; ++i) tmem_ld32(scores + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
@@ -837,42 +837,65 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
         }
         // the item's last unit here: the next one's queries, then this one's rows
         const Place was = at;
+        int token, head;
+        query_row(&token, &head);
         if (u + 1 < units) {
             if (!at.enter(p, sh, at.item + 1)) return;
             fetch_query();
-            query_ready();
         }
+        if (u + 1 < units) query_ready();
         if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.joined[stream], u & 1, p))) return;
         ptx::tc_fence_after();
-        const bool whole = last && begun;
         if (active) {
+            const bool whole = last && begun, there = stream * kRows + row < was.rows;
             const bool odd = *reinterpret_cast<volatile int*>(&sh.mark[was.item & (kMarks - 1)]) == was.item + 1;
             const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : __frcp_rn(sum);
-            uint16_t* dst = p.o + static_cast<int64_t>(was.q0 + token) * p.ldo + (was.head * p.G + packed - token * p.G) * p.hso;
-            float* slot = attn_slot(p, gridDim.x, C::kTile, D, blockIdx.x, begun);
+            uint16_t* dst = p.o + static_cast<int64_t>(was.q0 + token) * p.ldo + head * p.hso;
             const int at_row = stream * kRows + row;
+            float* slot = attn_slot(p, gridDim.x, C::kTile, D, blockIdx.x, begun) + at_row * D;
+            // Whole rows go by way of shared memory, so that two lanes write 32 bytes of one:
+            // a store's time goes with the lines that it touches.
+            const unsigned long long own = there ? reinterpret_cast<unsigned long long>(dst) : 0;
+            const unsigned long long to0 = __shfl_sync(0xFFFFFFFFu, own, lane >> 1);
+            const unsigned long long to1 = __shfl_sync(0xFFFFFFFFu, own, 16 + (lane >> 1));
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
                 uint32_t o[16];
                 ptx::tmem_ld_32x32b_x16(out + c, o);
                 ptx::tmem_wait_ld();
-                if (!there) continue;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
                 if (whole) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) o[i] = pack_bf16(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-                }
-                uint4* to = whole ? reinterpret_cast<uint4*>(dst + c) : reinterpret_cast<uint4*>(slot + at_row * D + c);
+                    uint4* to = reinterpret_cast<uint4*>(staged + lane * 32);
+                    const int swizzle = lane >> 2 & 1;
+                    to[swizzle] = make_uint4(o[0], o[1], o[2], o[3]);
+                    to[swizzle ^ 1] = make_uint4(o[4], o[5], o[6], o[7]);
+                    __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < 2 || !whole) to[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = 16 * i + (lane >> 1);
+                        const uint4 v = reinterpret_cast<const uint4*>(staged + r * 32)[(lane & 1) ^ (r >> 2 & 1)];
+                        const unsigned long long d = i ? to1 : to0;
+                        if (d) *reinterpret_cast<uint4*>(d + 2 * c + 16 * (lane & 1)) = v;
+                    }
+                    __syncwarp();
+                } else if (there) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        reinterpret_cast<uint4*>(slot + c)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
             }
             if (there && !whole) {
-                slot[C::kTile * D + at_row] = most;
-                slot[C::kTile * D + C::kTile + at_row] = sum;
+                float* end = attn_slot(p, gridDim.x, C::kTile, D, blockIdx.x, begun) + C::kTile * D;
+                end[at_row] = most;
+                end[C::kTile + at_row] = sum;
             }
-            if (odd && there) add_odd<D, KIND>(p, was, from, place, whole ? dst : nullptr, slot + at_row * D);
+            if (odd) {  // (rows were written by other lanes of the warp)
+                __syncwarp();
+                if (there) add_odd<D, KIND>(p, was, from, was.base + token, whole ? dst : nullptr, slot);
+            }
         }
         ptx::tc_fence_before();
         most = -INFINITY, sum = 0.0f;
@@ -918,11 +941,11 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
     attn_share<C::kTile, C::kKeys, C::kThreads>(p, sh.plan);
     ptx::tc_fence_after();
     if (sh.plan.share.begin < sh.plan.share.end) {
-        if (C::kStreams == 2) {
+        if (C::kDeal) {
             if (warp < C::kSoft) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMoreRegs));
             else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kFewRegs));
         }
-        if (warp < C::kSoft) weigh<D, KIND>(p, sh, query);
+        if (warp < C::kSoft) weigh<D, KIND>(p, sh, query, ring + C::kStages * C::kTileBytes);
         else if (warp == C::kSoft) issue_products<D, KIND>(p, sh, ptx::smem_addr(query), ptx::smem_addr(ring));
         else if (warp == C::kSoft + 1) watch<D, KIND>(p, sh);
         else if constexpr (C::kCodes) widen_units<D>(p, sh, ring);
