@@ -6,7 +6,7 @@
 //   loaders  copy a unit's keys, then its values, into a ring of shared memory
 //            tiles in the operand layout (128-byte swizzle; a row's 64 dimensions are
 //            a line, so keys are a K-major operand and values an MN-major one of the
-//            same layout); codes become bf16 on the way, times their scale, exactly;
+//            same layout); codes become fp16 on the way;
 //   one warp issues the products: scores S = Q K^T into tensor memory, then, once
 //            the weights are there, O += P V with P as the operand in tensor memory
 //            in the place of its scores;
@@ -19,11 +19,19 @@
 // summed before that in fp32.  The maximum that they are taken against may lag by 8
 // in units of log2, so that outputs are rescaled in tensor memory only rarely.
 //
+// Codes.  e4m3 codes are exact in fp16, and the products run in it.  A row of q is
+// multiplied by the power of two that brings its largest magnitude into [2^14, 2^15)
+// (exact down to 2^-31 of that).  A code is multiplied by its scale over the largest of
+// its unit, at most 1 (exact down to 2^-15, below off by at most 2^-25 of the largest);
+// the unit's own scale multiplies the scores, and the values' is part of the weights,
+// 2^(x + e), of which the maximum is taken.  2^7 more uses fp16's range: a weight is off
+// by at most 2^-12 of itself, or 2^-32 of the largest.
+//
 // A value that is not finite and that some row of its unit masks would reach that row
 // as zero times it.  In units with masks the loaders put zeros in the place of such
 // values and mark the item; its rows then add those that they see at their end.
 #include <cuda.h>
-#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "attn.cuh"
 #include "w4.cuh"
@@ -70,6 +78,8 @@ struct Shared {
     uint64_t full[4], raw[2], empty[4], scores[2], weights[2], joined[2], query[2], drained;
     long long row_off[3][128];      // of a unit's rows; three units, as loaders may be one apart
     uint8_t row_scale[3][2][128];
+    uint32_t largest[4][2];         // scale of a unit's keys and values; a fourth to begin anew
+    float2 scales[8];               // of a unit: 2^e of the keys, e of the values
     uint32_t tmem;
     int dead;
     int looked[2];  // warps that have looked a tile through, of either stage
@@ -143,11 +153,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B bf16 (bits 7-9,
-// 10-12 = 1), A K-major (bit 15 = 0), B's major (bit 16: 1 MN-major), N >> 3 in bits
+// Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B bf16 or fp16 (bits
+// 7-9, 10-12 = 1 or 0), A K-major (bit 15 = 0), B's major (bit 16: 1 MN-major), N >> 3 in bits
 // 17-22, M >> 4 in bits 24-28.
-constexpr uint32_t idesc_bf16(uint32_t n, uint32_t b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t idesc_f16(uint32_t n, uint32_t b_mn, bool bf16) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 // smem_desc_sw128 with the leading byte offset that an MN-major operand has: from
@@ -246,31 +256,31 @@ struct Place : Cursor {
     }
 };
 
-// 16 codes -> 16 bf16 numbers times 2^(b - 127) (NaN for b = 255).
-__device__ __forceinline__ void widen(const uint4& c, uint32_t scale, uint4& lo, uint4& hi) {
+// 16 codes -> 16 fp16 numbers times 2^-down (NaN for a scale of 255).
+__device__ __forceinline__ void widen(const uint4& c, uint32_t scale, uint32_t largest, uint4& lo, uint4& hi) {
+    // codes times 2^-14 are exact, so two factors round once
+    const uint32_t down = scale == 255u ? 0u : largest - scale;
+    const uint32_t bits = scale == 255u ? 0x7E00u : (15u - min(down, 14u)) << 10;
+    const __half2 f = __half2half2(__ushort_as_half(static_cast<unsigned short>(bits)));
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t r[8];
+    __half2 r[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t e = codes_even(w[i]), o = codes_odd(w[i]);
-        r[2 * i] = __byte_perm(e, o, 0x5410), r[2 * i + 1] = __byte_perm(e, o, 0x7632);
+        uint32_t a, b;
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(a), "=r"(b)
+            : "r"(w[i]));
+        r[2 * i] = __hmul2_rn(*reinterpret_cast<__half2*>(&a), f), r[2 * i + 1] = __hmul2_rn(*reinterpret_cast<__half2*>(&b), f);
     }
-    // the code's 2^-120 and the scale in one factor; above 2^7 in two
-    const uint32_t first = scale == 255u ? 0x7FC0u : min(scale + 120u, 254u) << 7;
-    const __nv_bfloat162 f = __halves2bfloat162(__ushort_as_bfloat16(static_cast<unsigned short>(first)),
-                                                __ushort_as_bfloat16(static_cast<unsigned short>(first)));
+    if (down > 14u) {
+        const uint32_t more = down - 14u, rest = more <= 14u ? (15u - more) << 10 : more <= 24u ? 1u << (24u - more) : 0u;
+        const __half2 g = __half2half2(__ushort_as_half(static_cast<unsigned short>(rest)));
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<__nv_bfloat162*>(&r[i]) = __hmul2_rn(*reinterpret_cast<__nv_bfloat162*>(&r[i]), f);
-    if (scale > 134u && scale != 255u) {
-        const unsigned short more = static_cast<unsigned short>((scale - 134u + 127u) << 7);
-        const __nv_bfloat162 g = __halves2bfloat162(__ushort_as_bfloat16(more), __ushort_as_bfloat16(more));
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<__nv_bfloat162*>(&r[i]) = __hmul2_rn(*reinterpret_cast<__nv_bfloat162*>(&r[i]), g);
+        for (int i = 0; i < 8; ++i) r[i] = __hmul2_rn(r[i], g);
     }
-    lo = make_uint4(r[0], r[1], r[2], r[3]);
-    hi = make_uint4(r[4], r[5], r[6], r[7]);
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
+    lo = make_uint4(u[0], u[1], u[2], u[3]);
+    hi = make_uint4(u[4], u[5], u[6], u[7]);
 }
 
 // Bits 15 and 31: whether the lower and the upper bf16 of a word have no finite value.
@@ -443,7 +453,7 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, uin
         for (int i = 0; i < kLook; ++i) {
             const int j = (at.lo + at.unit) * C::kKeys + tid + i * C::kLoaders, s = j & ((1 << p.page_log2) - 1);
             off[i] = -1;
-            zk[i] = zv[i] = 127;
+            zk[i] = zv[i] = 0;
             if (page[i] >= 0) {
                 off[i] = page[i] * p.pstride + s * p.sstride + at.head * p.hstride;
                 const long long z = page[i] * p.zpstride + s * p.zsstride + at.head * p.zhstride;
@@ -451,16 +461,24 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, uin
             }
         }
     };
-    auto keep = [&](int slot) {
+    auto keep = [&](int slot, int unit) {
 #pragma unroll
         for (int i = 0; i < kLook; ++i) {
             const int r = tid + i * C::kLoaders;
             if (r < C::kKeys) {
                 sh.row_off[slot][r] = off[i];
+                // a value's scale below 2^-80 counts as that (the sum of the weights, which
+                // are taken against those times values, would leave fp32's range)
+                if (off[i] >= 0) zv[i] = max(zv[i], 47u);
                 sh.row_scale[slot][0][r] = static_cast<uint8_t>(zk[i]);
                 sh.row_scale[slot][1][r] = static_cast<uint8_t>(zv[i]);
+                const uint32_t k = zk[i] == 255u ? 0u : zk[i], v = zv[i] == 255u ? 0u : zv[i];
+                atomicMax(&sh.largest[unit & 3][0], k);
+                atomicMax(&sh.largest[unit & 3][1], v);
             }
         }
+        // (loaders may still read those of the two units before this one)
+        if (tid < 2) sh.largest[unit + 1 & 3][tid] = 0;
     };
     auto room = [&](uint32_t fill) {
         if (alive && fill >= C::kStages)
@@ -470,7 +488,7 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, uin
         return tile + (c >> 3) * (C::kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
     };
 
-    if (alive) find(), locate(), keep(0);
+    if (alive) find(), locate(), keep(0, 0);
     ptx::named_sync(1, C::kLoaders);
 
     int slot = 0;
@@ -488,7 +506,8 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, uin
             }
         }
     };
-    auto write = [&](uint4(&raw)[kMine], int kv, int from, int tag) {
+    auto write = [&](uint4(&raw)[kMine], int kv, int from, int unit, int tag) {
+        const uint32_t largest = sh.largest[unit & 3][kv];
         room(fill);
         uint8_t* tile = ring + fill % C::kStages * C::kTileBytes;
         if (alive) {
@@ -498,12 +517,12 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, uin
                 if (r < C::kKeys) {
                     uint32_t scale = sh.row_scale[from][kv][r];
                     if (tag && scale == 255u) {
-                        scale = 127u;
+                        scale = largest;
                         raw[i] = make_uint4(0, 0, 0, 0);
                         sh.mark[(tag - 1) & (kMarks - 1)] = tag;
                     }
                     uint4 lo, hi;
-                    widen(raw[i], scale, lo, hi);
+                    widen(raw[i], scale, largest, lo, hi);
                     *reinterpret_cast<uint4*>(place16(tile, r, 2 * piece)) = lo;
                     *reinterpret_cast<uint4*>(place16(tile, r, 2 * piece + 1)) = hi;
                 }
@@ -526,13 +545,15 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, uin
         }
         if (alive) read(values, p.v);
         if (more) locate();
-        write(keys, 0, slot, 0);
+        if (tid == 0)
+            sh.scales[u & 7] = make_float2(e8m0_to_float(sh.largest[u & 3][0]), static_cast<float>(static_cast<int>(sh.largest[u & 3][1]) - 127));
+        write(keys, 0, slot, u, 0);
         const int now = slot, next = slot == 2 ? 0 : slot + 1;
-        if (more) keep(next);
+        if (more) keep(next, u + 1);
         ptx::named_sync(1, C::kLoaders);
         slot = next;
         if (more) read(keys, p.k);
-        write(values, 1, now, tag);
+        write(values, 1, now, u, tag);
     }
 }
 
@@ -597,7 +618,7 @@ __device__ __forceinline__ void watch(const AttnParams& p, Shared& sh) {
 template <int D, int KIND>
 __device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, uint32_t query, uint32_t ring) {
     using C = Cfg<D, KIND>;
-    constexpr uint32_t kScoreDesc = idesc_bf16(C::kKeys, 0), kValueDesc = idesc_bf16(D, 1);
+    constexpr uint32_t kScoreDesc = idesc_f16(C::kKeys, 0, !C::kCodes), kValueDesc = idesc_f16(D, 1, !C::kCodes);
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     const uint32_t tmem = sh.tmem;
     uint32_t step = 0;
@@ -746,13 +767,41 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
         }
         cp_commit();
     };
+    float unscale = p.scale_log2;  // what a row's scores are multiplied by, beside their unit's scale
     auto query_ready = [&] {
         cp_wait<0>();
+        if (C::kCodes) {  // the row in fp16, in place
+            uint32_t largest = 0;
+            auto piece = [&](int c) { return reinterpret_cast<uint4*>(query + (mine - ptx::smem_addr(query)) + (c >> 3) * (kRows * 128) + (((c & 7) ^ (row & 7)) << 4)); };
+#pragma unroll 1
+            for (int c = 0; c < D / 8; ++c) {
+                const uint4 v = *piece(c);
+                const uint32_t lo = max(max(v.x & 0x7FFFu, v.y & 0x7FFFu), max(v.z & 0x7FFFu, v.w & 0x7FFFu));
+                const uint32_t hi = max(max(v.x >> 16 & 0x7FFFu, v.y >> 16 & 0x7FFFu), max(v.z >> 16 & 0x7FFFu, v.w >> 16 & 0x7FFFu));
+                largest = max(largest, max(lo, hi));
+            }
+            // zeros, and rows with an infinity or a NaN, stay
+            const int e = static_cast<int>(largest >> 7), up = largest == 0 || e == 255 ? 0 : min(14 - (e - 127), 126);
+            const float factor = __int_as_float((up + 127) << 23);
+#pragma unroll 1
+            for (int c = 0; c < D / 8; ++c) {
+                uint4* v = piece(c);
+                float x[8];
+                unpack_bf16x8(*v, x);
+                uint32_t h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[i]) : "f"(x[2 * i + 1] * factor), "f"(x[2 * i] * factor));
+                *v = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            unscale = __int_as_float((127 - up) << 23) * p.scale_log2;
+        }
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(&sh.query[stream]);
     };
     fetch_query();
     query_ready();
+    float now = unscale;  // of the item whose scores come
     float most = -INFINITY, sum = 0.0f;
     bool first = true;
     bool begun = at.unit == 0;
@@ -784,8 +833,10 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
             for (int i = 0; i < 8; ++i) tops[i] = fmaxf(s[2 * i], s[2 * i + 1]);
 #pragma unroll
             for (int i = 16; i < C::kKeys; i += 2) tops[(i >> 1) & 7] = fmaxf(tops[(i >> 1) & 7], fmaxf(s[i], s[i + 1]));
-            const float top = p.scale_log2 * fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
-                                                   fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
+            const float2 scale = C::kCodes ? sh.scales[u & 7] : make_float2(1.0f, 0.0f);
+            const float factor = C::kCodes ? now * scale.x : p.scale_log2;
+            const float top = scale.y + factor * fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
+                                                       fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
             float shrink = 1.0f;
             if (top > most + kLag) {
                 shrink = ex2(most - top);  // 0 from minus infinity
@@ -809,23 +860,24 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
                     ptx::tmem_wait_st();
                 }
             }
-            const float base = most == -INFINITY ? 0.0f : most;
-            const uint64_t factor = pair(p.scale_log2, p.scale_log2), minus = pair(-base, -base);
+            const float base = (most == -INFINITY ? 0.0f : most) - scale.y - (C::kCodes ? 7.0f : 0.0f);
+            const uint64_t factors = pair(factor, factor), minus = pair(-base, -base);
             uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int c = 0; c < C::kKeys / 32; ++c) {
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 x = halves(fma2(pair(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), factor, minus));
+                    const float2 x = halves(fma2(pair(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), factors, minus));
                     const float a = ex2(x.x), b = ex2(x.y);
                     sums[i & 3] = add2(sums[i & 3], pair(a, b));
-                    w[i] = pack_bf16(a, b);
+                    if (C::kCodes) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(b), "f"(a));
+                    else w[i] = pack_bf16(a, b);
                 }
                 tmem_st16(scores + 16 * c, w);
             }
             const float2 both = halves(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
-            sum += both.x + both.y;
+            sum += C::kCodes ? (both.x + both.y) * ex2(-scale.y) : both.x + both.y;
             ptx::tmem_wait_st();
         }
         ptx::tc_fence_before();
@@ -899,6 +951,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
         }
         ptx::tc_fence_before();
         most = -INFINITY, sum = 0.0f;
+        now = unscale;
         first = begun = true;
         from = 0;
     }
@@ -928,6 +981,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
         ptx::fence_mbar_init();
         sh.dead = 0;
         sh.looked[0] = sh.looked[1] = 0;
+        for (int i = 0; i < 8; ++i) sh.largest[i >> 1][i & 1] = 0;
         for (int i = 0; i < kMarks; ++i) sh.mark[i] = 0;
     }
     if (warp == C::kSoft) {

@@ -20,9 +20,9 @@
 // multiplied by the power of two that brings its largest magnitude into [2^14, 2^15):
 // exact down to 2^-31 of that, below off by at most 2^-39 of it.  A key's scale
 // multiplies its score.  A value's scale 2^e is part of its weight, 2^(x + e), the
-// maximum is taken of these (and of x - 80, so that no sum of the weights 2^x alone
-// overflows), and 2^7 more uses fp16's range: a weight is off by at most 2^-11 of
-// itself, or 2^-32 of the largest.  Values below 2^-80 of the others count less exactly.
+// maximum is taken of these, and 2^7 more uses fp16's range: a weight is off by at most
+// 2^-12 of itself, or 2^-32 of the largest.  (e below -80 counts as that, so that no sum
+// of the weights 2^x alone overflows.)
 // A 16-bit load of two bytes of a row, transposed, gives two dimensions of a key side
 // by side: output tiles hold even dimensions in their upper and odd ones in their lower
 // half.
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
     auto store_scales = [&] {
         if (C::kCodes && zstage >= 0 && lane < SL) {
             zring[zstage * 2 * SL + lane] = scale_of(zk);
-            zring[zstage * 2 * SL + SL + lane] = zv == 255u ? __uint_as_float(0x7FFFFFFFu) : static_cast<float>(static_cast<int>(zv) - 127);
+            zring[zstage * 2 * SL + SL + lane] = zv == 255u ? __uint_as_float(0x7FFFFFFFu) : static_cast<float>(max(static_cast<int>(zv), 47) - 127);
         }
         zstage = -1;
     };
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
                             }
                             s[k][n][2 * h + i] = x;
                             if (C::kCodes) with[k][n][2 * h + i] = y;
-                            most[n][i] = fmaxf(most[n][i], C::kCodes ? fmaxf(y, x - 80.0f) : x);
+                            most[n][i] = fmaxf(most[n][i], C::kCodes ? y : x);
                         }
                 }
             bool grown = false;

@@ -630,8 +630,8 @@ size_t fp8bs_attn_paged_workspace_bytes(int64_t D, int sm_count);
  * record FP8BS_ERR_DEVICE; the rows of such a sequence are not specified, and nothing
  * outside the tensors is touched.  Masked keys and values have no part in a row,
  * whatever they hold; an infinity or a NaN that a row sees makes its results NaN or
- * infinite.  In a cache of codes q and the values are below 2^63 in
- * magnitude.  Results are deterministic, and a row's do not depend on whether other
+ * infinite.  In a cache of codes q, keys and values are below 2^63 in magnitude, and
+ * a value's scale below 2^-80 counts as 2^-80.  Results are deterministic, and a row's do not depend on whether other
  * heads or sequences hold NaNs.  Two launches, dependent on their predecessors,
  * for which they wait before they touch memory.
  * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN, FP8BS_ERR_WORKSPACE,

@@ -14,6 +14,12 @@ matrix unit may cut off instead of rounding.
   from the maximum by 3 steps of |score| and |maximum|; exp2 by 2^-21.  A weight in the
   product is off by `weight` more of itself.  A sum of n weighted values is off by n/16
   + 16 steps of the sum of magnitudes.  Numerator and denominator may each be off so far.
+* Attention over codes, whose products are in fp16 (steps of 2^-24 below 2^-14): a
+  weight times its value's scale, or that of its neighbours, of which 2^7 stands for the
+  largest weight times the largest scale (the maximum may lag, never lead), is off by
+  half a step there, 2^-25 2^-7 of those, and multiplies the value's code; q's largest magnitude is brought to 2^14 at least, and q is
+  off by 2^-25 2^-14 of it; a key or a value, multiplied by its scale over the largest of
+  up to 128 neighbours (here: of all), by 2^-25 of that scale.
 """
 
 import math
@@ -86,9 +92,10 @@ def rows_of(cache, table, n):
     return out
 
 
-def attend(q, k, v, kv, scale, window, weight):
+def attend(q, k, v, kv, scale, window, weight, codes=None):
     """One sequence: q [n, Hq, D] (the newest of kv tokens), k and v [kv, Hk, D].
-    Returns float64 o [n, Hq, D] and its bound; `weight`: the rounding of a weight."""
+    Returns float64 o [n, Hq, D] and its bound; `weight`: the rounding of a weight;
+    `codes`: scales [kv, Hk] of the keys and of the values, where they are codes."""
     q = q.double().cpu()
     n, Hq, D = q.shape
     G = Hq // k.shape[1]
@@ -106,8 +113,13 @@ def attend(q, k, v, kv, scale, window, weight):
         most = s.amax(1, keepdim=True) if kv else torch.full((n, 1), -math.inf, dtype=torch.float64)
         none = ~seen.any(1, keepdim=True)
         w = torch.where(seen, torch.exp(s - torch.where(none, 0.0, most)), 0.0)
-        off = 2.0 ** -23 * (D / 16 + 16) * size + 3 * STEP * 1.5 * (torch.where(seen, s, 0.0).abs() + torch.where(none, 0.0, most).abs()) + 2.0 ** -21
-        off = torch.where(seen, torch.expm1(off), 0.0) + weight
+        if codes:
+            qh = q[:, h].abs()
+            more = 2.0 ** -25 * codes[0][:, h // G].max() * qh.sum(1, keepdim=True) + 2.0 ** -39 * qh.amax(1, keepdim=True) * kh.abs().sum(1)
+        else:
+            more = torch.zeros_like(s)
+        off = scale * more + 2.0 ** -23 * (D / 16 + 16) * size + 3 * STEP * 1.5 * (torch.where(seen, s, 0.0).abs() + torch.where(none, 0.0, most).abs()) + 2.0 ** -21
+        off = torch.where(seen, torch.expm1(torch.nan_to_num(off, nan=0.0, posinf=0.0)), 0.0) + weight
         total = torch.where(none, 1.0, w.sum(1, keepdim=True))
         vs = torch.where(torch.isfinite(vh), vh, 0.0)
         o[:, h] = w @ vs / total
@@ -116,7 +128,11 @@ def attend(q, k, v, kv, scale, window, weight):
             rows = seen[:, j]
             o[rows, h] += bad[j]
         steps = 2 * STEP * (kv / 16 + 16)
-        bound[:, h] = (w * (off + steps)) @ vs.abs() / total + (w * (off + steps)).sum(1, keepdim=True) / total * (w @ vs.abs() / total)
+        least = 0.0
+        if codes:
+            unit = codes[1][:, h // G]
+            least = 2.0 ** -32 * w.amax(1, keepdim=True) * unit.max() * (vs.abs() / unit.unsqueeze(1)).sum(0) / total + 2.0 ** -25 * unit.max()
+        bound[:, h] = (w * (off + steps)) @ vs.abs() / total + (w * (off + steps)).sum(1, keepdim=True) / total * (w @ vs.abs() / total) + least
     return o, bound
 
 

@@ -60,7 +60,12 @@ def check(lengths, q, tensors, table, o, window=0, scale=None):
     D = q.shape[2]
     for b, (n, kv) in enumerate(lengths):
         k, v = A.rows_of(tensors, table[b], kv)
-        ref, bound = A.attend(q[first:first + n], k, v, kv, D ** -0.5 if scale is None else scale, window, WEIGHT)
+        codes = None
+        if len(tensors) == 4 and kv:
+            j = torch.arange(kv)
+            page, at = table[b].cpu().long()[j // tensors[0].shape[1]], j % tensors[0].shape[1]
+            codes = [2.0 ** (torch.where(z == 255, 0, z).double() - 127) for z in (t.cpu()[page, at] for t in tensors[2:])]
+        ref, bound = A.attend(q[first:first + n], k, v, kv, D ** -0.5 if scale is None else scale, window, WEIGHT, codes)
         A.near(o[first:first + n], ref, bound)
         first += n
 
@@ -104,6 +109,21 @@ def test_sharp_and_flat_scores(dev, size, scale, codes):
     q, tensors, table, cu, lens = make(lengths, 8, 2, 128, codes, 16, "slots", dev, seed=7, size=size)
     o = fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens, scale=scale)
     check(lengths, q, tensors, table, o, scale=scale)
+
+
+@pytest.mark.parametrize("lengths", [[(1, 700), (3, 50)], [(100, 400), (40, 40)]])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scales_far_apart(dev, D, lengths):
+    """Rows of zeros, tiny rows and large ones beside each other; queries of all sizes."""
+    q, tensors, table, cu, lens = make(lengths, 8, 2, D, True, 16, "slots", dev, seed=D)
+    g = torch.Generator(device=dev).manual_seed(1)
+    for t in tensors[2:]:
+        t.copy_(torch.randint(90, 125, t.shape, generator=g, device=dev).to(torch.uint8))
+    tensors[3][torch.rand(tensors[3].shape, generator=g, device=dev) < 0.2] = 0
+    tensors[1][tensors[3] == 0] = 0
+    q *= torch.exp2(torch.randint(-60, 3, q.shape[:2], generator=g, device=dev).float()).unsqueeze(2).to(torch.bfloat16)
+    q[0, 0] = 0
+    check(lengths, q, tensors, table, fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens))
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
