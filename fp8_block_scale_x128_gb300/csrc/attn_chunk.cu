@@ -63,10 +63,12 @@ struct Cfg {
     static constexpr int kLoadWarps = kThreads / 32 - kSoft - 2;
     static constexpr int kLoaders = kLoadWarps * 32;
     static constexpr int kTileBytes = kKeys * D * 2;
-    static constexpr int kStages = 4;
+    static constexpr int kStages = kCodes ? 3 : 4;
+    // codes as they are in the cache, on their way
+    static constexpr int kRaw = 3, kRawBytes = kCodes ? kKeys * D : 0;
     static constexpr int kQBytes = kTile * D * 2;
     static constexpr int kOutBytes = 1024;  // of a softmax warp: outputs on their way
-    static constexpr int kSmem = kQBytes + kStages * kTileBytes + kSoft * kOutBytes + 1024;
+    static constexpr int kSmem = kQBytes + kStages * kTileBytes + kRaw * kRawBytes + kSoft * kOutBytes + 1024;
     static constexpr uint32_t kOut = 256;  // first column of the outputs
 };
 
@@ -76,9 +78,9 @@ struct Shared {
     uint64_t known[kItems];  // that an item stands there
     long long next_start;    // units before the next item
     uint64_t full[4], raw[2], empty[4], scores[2], weights[2], joined[2], query[2], drained;
-    long long row_off[3][128];      // of a unit's rows; three units, as loaders may be one apart
-    uint8_t row_scale[3][2][128];
-    uint32_t largest[4][2];         // scale of a unit's keys and values; a fourth to begin anew
+    uint64_t coded[3], widened[3];  // of the tiles of codes: they are there, they are free
+    uint8_t row_scale[4][2][128];   // of a unit's keys and values
+    uint32_t largest[4][2];
     float2 scales[8];               // of a unit: 2^e of the keys, e of the values
     uint32_t tmem;
     int dead;
@@ -286,15 +288,20 @@ __device__ __forceinline__ void widen(const uint4& c, uint32_t scale, uint32_t l
 // Bits 15 and 31: whether the lower and the upper bf16 of a word have no finite value.
 __device__ __forceinline__ uint32_t odd_pair(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
-// bf16 tiles: one warp issues boxes (a lane each) of up to a page's slots.  A unit's
-// values that some row masks land on a barrier of their own, and the other loader
-// warps look them through before they hand them on: rows that are no keys, which the
-// boxes may cover or leave, become zeros, as do values that are not finite.
-template <int D>
-__device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint8_t* ring,
-                                           const CUtensorMap* mk, const CUtensorMap* mv) {
-    using C = Cfg<D, FP8BS_KV_BF16>;
-    constexpr int kParts = D / 64, kMost = C::kKeys * kParts / 32;  // boxes of a lane
+// One warp issues boxes (a lane each) of up to a page's slots.
+// bf16: they go where the products read them.  A unit's values that some row masks
+// land on a barrier of their own, and the other loader warps look them through before
+// they hand them on: rows that are no keys, which the boxes may cover or leave, become
+// zeros, as do values that are not finite.
+// Codes: boxes go to a ring of their own, with a unit's scales beside them (a lane reads
+// those of four keys), and the other loader warps widen them.
+template <int D, int KIND>
+__device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint8_t* ring, const CUtensorMap* mk,
+                                           const CUtensorMap* mv) {
+    using C = Cfg<D, KIND>;
+    constexpr int kParts = C::kCodes ? 1 : D / 64, kWide = C::kCodes ? D : 64;  // boxes over a row, and their width
+    constexpr int kMost = C::kKeys * kParts / 32;  // boxes of a lane
+    constexpr int kRing = C::kCodes ? C::kRaw : C::kStages, kBoxRow = C::kCodes ? D : 128;
     const int lane = threadIdx.x & 31;
     const int rows = min(1 << p.page_log2, C::kKeys), boxes = C::kKeys / rows * kParts;
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
@@ -304,60 +311,95 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
     bool alive = at.start(p, sh);
     uint32_t fill = 0;
     int page[kMost];
+    auto page_of = [&](int j) {
+        int id;
+        return j >= at.first && j < at.past && attn_page(p, p.table + at.b * p.table_stride, j, &id) ? id : -1;
+    };
     auto find = [&] {
 #pragma unroll
         for (int i = 0; i < kMost; ++i) {
             if (32 * i >= boxes) break;
             const int j = (at.lo + at.unit) * C::kKeys + (lane + 32 * i) / kParts * rows;
-            page[i] = -1;
-            if (lane + 32 * i < boxes && j < at.past && j + rows > at.first) {
-                int id;
-                if (attn_page(p, p.table + at.b * p.table_stride, j, &id)) page[i] = id;
+            // (a box may begin before the first key and end past the last)
+            page[i] = lane + 32 * i < boxes && j + rows > at.first ? page_of(max(j, at.first)) : -1;
+        }
+    };
+    uint32_t zk[C::kKeys / 32], zv[C::kKeys / 32];
+    auto read_scales = [&] {
+#pragma unroll
+        for (int i = 0; i < C::kKeys / 32; ++i) {
+            const int j = (at.lo + at.unit) * C::kKeys + lane + 32 * i, id = page_of(j);
+            zk[i] = zv[i] = 0;
+            if (id >= 0) {
+                const long long z = id * p.zpstride + (j & ((1 << p.page_log2) - 1)) * p.zsstride + at.head * p.zhstride;
+                zk[i] = p.ks[z], zv[i] = p.vs[z];
             }
         }
     };
+    auto keep_scales = [&](int u) {
+        uint32_t mostk = 0, mostv = 0;
+#pragma unroll
+        for (int i = 0; i < C::kKeys / 32; ++i) {
+            // a value's scale below 2^-80 counts as that (the sum of the weights, which are
+            // taken against those times values, would leave fp32's range)
+            zv[i] = max(zv[i], 47u);
+            sh.row_scale[u & 3][0][lane + 32 * i] = static_cast<uint8_t>(zk[i]);
+            sh.row_scale[u & 3][1][lane + 32 * i] = static_cast<uint8_t>(zv[i]);
+            mostk = max(mostk, zk[i] == 255u ? 0u : zk[i]), mostv = max(mostv, zv[i] == 255u ? 0u : zv[i]);
+        }
+        mostk = __reduce_max_sync(0xFFFFFFFFu, mostk), mostv = __reduce_max_sync(0xFFFFFFFFu, mostv);
+        if (lane == 0) {
+            sh.largest[u & 3][0] = mostk, sh.largest[u & 3][1] = mostv;
+            sh.scales[u & 7] = make_float2(e8m0_to_float(mostk), static_cast<float>(static_cast<int>(mostv) - 127));
+        }
+        __syncwarp();
+    };
     if (alive) find();
+    if (alive && C::kCodes) read_scales();
 #pragma unroll 1
     for (int u = 0; u < units && alive; ++u) {
         const int j0 = (at.lo + at.unit) * C::kKeys, head = at.head;
-        const bool check = !attn_sees_all<C::kKeys>(p, at);
+        const bool check = !C::kCodes && !attn_sees_all<C::kKeys>(p, at);
         int now[kMost], count = 0;
 #pragma unroll
         for (int i = 0; i < kMost; ++i) {
             if (32 * i >= boxes) break;
             now[i] = page[i], count += __popc(__ballot_sync(0xFFFFFFFFu, page[i] >= 0));
         }
+        if (C::kCodes) keep_scales(u);
         if (u + 1 < units) {
             const int item = at.item;
             alive &= at.next(p, sh);
             if (alive) find();
+            if (alive && C::kCodes) read_scales();
             if (at.item != item) publish<C::kTile, C::kKeys>(p, sh, at.item + 1);
         }
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, ++fill) {
-            const uint32_t stage = fill % C::kStages;
-            if (alive && fill >= C::kStages)
-                alive = __all_sync(0xFFFFFFFFu, wait(sh, &sh.empty[stage], ((fill / C::kStages) - 1) & 1, p));
+            const uint32_t stage = fill % kRing;
+            if (alive && fill >= kRing)
+                alive = __all_sync(0xFFFFFFFFu, wait(sh, C::kCodes ? &sh.widened[stage] : &sh.empty[stage], ((fill / kRing) - 1) & 1, p));
             if (!alive) break;
-            uint64_t* bar = kv && check ? &sh.raw[stage >> 1] : &sh.full[stage];
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, count * rows * 128);
+            uint64_t* bar = C::kCodes ? &sh.coded[stage] : kv && check ? &sh.raw[stage >> 1] : &sh.full[stage];
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, count * rows * kBoxRow);
             __syncwarp();
-            uint8_t* tile = ring + stage * C::kTileBytes;
+            uint8_t* tile = ring + stage * (C::kCodes ? C::kRawBytes : C::kTileBytes);
 #pragma unroll
             for (int i = 0; i < kMost; ++i) {
                 if (32 * i >= boxes) break;
                 if (now[i] >= 0) {
                     const int q = lane + 32 * i, part = q % kParts, r = q / kParts * rows;
-                    tma_box(tile + part * (C::kKeys * 128) + r * 128, kv ? mv : mk, 64 * part, (j0 + r) & ((1 << p.page_log2) - 1),
-                            head, now[i], bar);
+                    tma_box(tile + part * (C::kKeys * 128) + r * kBoxRow, kv ? mv : mk, kWide * part,
+                            (j0 + r) & ((1 << p.page_log2) - 1), head, now[i], bar);
                 }
             }
         }
     }
     if (!alive) {  // what is under way lands before the block leaves
         const long long began = clock64();
-        for (uint32_t f = fill < 4 ? 0 : fill - 4; f < fill; ++f)
-            while (!ptx::mbar_test(&sh.full[f % C::kStages], (f / C::kStages) & 1) && clock64() - began < 1000000) {
+        for (uint32_t f = fill < kRing ? 0 : fill - kRing; f < fill; ++f)
+            while (!ptx::mbar_test(C::kCodes ? &sh.coded[f % kRing] : &sh.full[f % kRing], (f / kRing) & 1) &&
+                   clock64() - began < 1000000) {
             }
     }
 }
@@ -412,148 +454,70 @@ __device__ __forceinline__ void check_units(const AttnParams& p, Shared& sh, uin
     }
 }
 
-// Tiles of codes: threads read them, widen them and store them as bf16.
+// Tiles of codes become the products' tiles.
 template <int D>
-__device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, uint8_t* ring) {
+__device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, const uint8_t* raw, uint8_t* ring) {
     using C = Cfg<D, FP8BS_KV_E4M3>;
-    constexpr int kPer = D / 16;                  // 16-byte pieces of a row in the cache
-    constexpr int kRowStep = C::kLoaders / kPer;       // rows between a thread's pieces
-    constexpr int kMine = (C::kKeys + kRowStep - 1) / kRowStep;
-    constexpr int kLook = (C::kKeys + C::kLoaders - 1) / C::kLoaders;
-    const int tid = threadIdx.x - (C::kSoft + 2) * 32;
-    // threads past the last whole row copy nothing: their first row is past the unit
-    const int row0 = tid < kRowStep * kPer ? tid / kPer : C::kKeys, piece = tid % kPer;
+    constexpr int kThreads = C::kLoaders - 32, kPer = D / 16;  // 16-byte pieces of a row
+    constexpr int kStep = kThreads / kPer, kBatch = 4;          // rows between a thread's pieces
+    const int tid = threadIdx.x - (C::kSoft + 3) * 32, piece = tid % kPer;
+    const int first = tid < kStep * kPer ? tid / kPer : C::kKeys;
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     Place at;
-    const bool publishes = tid < 32;
-    if (publishes) {
-        publish<C::kTile, C::kKeys>(p, sh, 0);
-        publish<C::kTile, C::kKeys>(p, sh, 1);
-    }
-    bool alive = at.start(p, sh);  // warps that are not still meet the others at the barrier
-
-    // A unit's rows, looked up a unit ahead and in three steps, so that none of them
-    // waits for the one before: pages, then offsets and scales, then shared memory.
-    int page[kLook];
-    long long off[kLook];
-    uint32_t zk[kLook], zv[kLook];
-    auto find = [&] {
-#pragma unroll
-        for (int i = 0; i < kLook; ++i) {
-            const int r = tid + i * C::kLoaders, j = (at.lo + at.unit) * C::kKeys + r;
-            page[i] = -1;
-            if (r < C::kKeys && j >= at.first && j < at.past) {
-                int id;
-                if (attn_page(p, p.table + at.b * p.table_stride, j, &id)) page[i] = id;
-            }
-        }
-    };
-    auto locate = [&] {
-#pragma unroll
-        for (int i = 0; i < kLook; ++i) {
-            const int j = (at.lo + at.unit) * C::kKeys + tid + i * C::kLoaders, s = j & ((1 << p.page_log2) - 1);
-            off[i] = -1;
-            zk[i] = zv[i] = 0;
-            if (page[i] >= 0) {
-                off[i] = page[i] * p.pstride + s * p.sstride + at.head * p.hstride;
-                const long long z = page[i] * p.zpstride + s * p.zsstride + at.head * p.zhstride;
-                zk[i] = p.ks[z], zv[i] = p.vs[z];
-            }
-        }
-    };
-    auto keep = [&](int slot, int unit) {
-#pragma unroll
-        for (int i = 0; i < kLook; ++i) {
-            const int r = tid + i * C::kLoaders;
-            if (r < C::kKeys) {
-                sh.row_off[slot][r] = off[i];
-                // a value's scale below 2^-80 counts as that (the sum of the weights, which
-                // are taken against those times values, would leave fp32's range)
-                if (off[i] >= 0) zv[i] = max(zv[i], 47u);
-                sh.row_scale[slot][0][r] = static_cast<uint8_t>(zk[i]);
-                sh.row_scale[slot][1][r] = static_cast<uint8_t>(zv[i]);
-                const uint32_t k = zk[i] == 255u ? 0u : zk[i], v = zv[i] == 255u ? 0u : zv[i];
-                atomicMax(&sh.largest[unit & 3][0], k);
-                atomicMax(&sh.largest[unit & 3][1], v);
-            }
-        }
-        // (loaders may still read those of the two units before this one)
-        if (tid < 2) sh.largest[unit + 1 & 3][tid] = 0;
-    };
-    auto room = [&](uint32_t fill) {
-        if (alive && fill >= C::kStages)
-            alive = wait(sh, &sh.empty[fill % C::kStages], ((fill / C::kStages) - 1) & 1, p);
-    };
-    auto place16 = [&](uint8_t* tile, int r, int c) {  // 16-byte piece c of row r of a tile
-        return tile + (c >> 3) * (C::kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-    };
-
-    if (alive) find(), locate(), keep(0, 0);
-    ptx::named_sync(1, C::kLoaders);
-
-    int slot = 0;
+    bool alive = at.start(p, sh);
     uint32_t fill = 0;
-
-    uint4 keys[kMine], values[kMine];
-    auto read = [&](uint4(&raw)[kMine], const uint8_t* src) {
+#pragma unroll 1
+    for (int u = 0; u < units && alive; ++u) {
+        const int j0 = (at.lo + at.unit) * C::kKeys;
+        const bool masks = !attn_sees_all<C::kKeys>(p, at);
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv, ++fill) {
+            const uint32_t from = fill % C::kRaw, to = fill % C::kStages;
+            alive = wait(sh, &sh.coded[from], (fill / C::kRaw) & 1, p);
+            if (alive && fill >= C::kStages) alive = wait(sh, &sh.empty[to], ((fill / C::kStages) - 1) & 1, p);
+            alive = __all_sync(0xFFFFFFFFu, alive);
+            if (!alive) break;
+            const uint32_t largest = sh.largest[u & 3][kv];
+            uint8_t* tile = ring + to * C::kTileBytes;
+            const uint8_t* source = raw + from * C::kRawBytes + 16 * piece;
+#pragma unroll 1
+            for (int r0 = first; r0 < C::kKeys; r0 += kBatch * kStep) {
+                uint4 codes[kBatch];
+                uint32_t scale[kBatch];
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const int r = row0 + i * kRowStep;
-            raw[i] = make_uint4(0, 0, 0, 0);
-            if (r < C::kKeys) {
-                const long long o = sh.row_off[slot][r];
-                if (o >= 0) raw[i] = *reinterpret_cast<const uint4*>(src + o + 16 * piece);
-            }
-        }
-    };
-    auto write = [&](uint4(&raw)[kMine], int kv, int from, int unit, int tag) {
-        const uint32_t largest = sh.largest[unit & 3][kv];
-        room(fill);
-        uint8_t* tile = ring + fill % C::kStages * C::kTileBytes;
-        if (alive) {
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = min(r0 + i * kStep, C::kKeys - 1);
+                    codes[i] = *reinterpret_cast<const uint4*>(source + r * D);
+                    scale[i] = sh.row_scale[u & 3][kv][r];
+                }
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const int r = row0 + i * kRowStep;
-                if (r < C::kKeys) {
-                    uint32_t scale = sh.row_scale[from][kv][r];
-                    if (tag && scale == 255u) {
-                        scale = largest;
-                        raw[i] = make_uint4(0, 0, 0, 0);
-                        sh.mark[(tag - 1) & (kMarks - 1)] = tag;
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = r0 + i * kStep;
+                    if (r >= C::kKeys) break;
+                    if (kv && masks) {
+                        const bool key = j0 + r >= at.first && j0 + r < at.past;
+                        if (!key || scale[i] == 255u) {  // see the head of this file
+                            if (key) sh.mark[at.item & (kMarks - 1)] = at.item + 1;
+                            scale[i] = largest;
+                            codes[i] = make_uint4(0, 0, 0, 0);
+                        }
                     }
                     uint4 lo, hi;
-                    widen(raw[i], scale, largest, lo, hi);
-                    *reinterpret_cast<uint4*>(place16(tile, r, 2 * piece)) = lo;
-                    *reinterpret_cast<uint4*>(place16(tile, r, 2 * piece + 1)) = hi;
+                    widen(codes[i], scale[i], largest, lo, hi);
+                    uint8_t* line = tile + (piece >> 2) * (C::kKeys * 128) + r * 128;
+                    const int c = 2 * (piece & 3);
+                    *reinterpret_cast<uint4*>(line + ((c ^ (r & 7)) << 4)) = lo;
+                    *reinterpret_cast<uint4*>(line + ((c + 1 ^ (r & 7)) << 4)) = hi;
                 }
             }
             ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(&sh.full[fill % C::kStages]);
+            __syncwarp();
+            if ((tid & 31) == 0) {
+                ptx::mbar_arrive(&sh.widened[from]);
+                ptx::mbar_arrive(&sh.full[to]);
+            }
         }
-        ++fill;
-    };
-    if (alive) read(keys, p.k);
-#pragma unroll 1
-    for (int u = 0; u < units; ++u) {
-        bool more = alive && u + 1 < units;
-        const int tag = alive && attn_sees_all<C::kKeys>(p, at) ? 0 : at.item + 1;
-        if (more) {
-            const int item = at.item;
-            more = alive = at.next(p, sh);
-            if (more) find();
-            if (publishes && at.item != item) publish<C::kTile, C::kKeys>(p, sh, at.item + 1);
-        }
-        if (alive) read(values, p.v);
-        if (more) locate();
-        if (tid == 0)
-            sh.scales[u & 7] = make_float2(e8m0_to_float(sh.largest[u & 3][0]), static_cast<float>(static_cast<int>(sh.largest[u & 3][1]) - 127));
-        write(keys, 0, slot, u, 0);
-        const int now = slot, next = slot == 2 ? 0 : slot + 1;
-        if (more) keep(next, u + 1);
-        ptx::named_sync(1, C::kLoaders);
-        slot = next;
-        if (more) read(keys, p.k);
-        write(values, 1, now, u, tag);
+        if (alive && u + 1 < units) alive = at.next(p, sh);
     }
 }
 
@@ -966,9 +930,11 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
     __shared__ Shared sh;
     uint8_t* query = raw + ((1024 - (ptx::smem_addr(raw) & 1023)) & 1023);
     uint8_t* ring = query + C::kQBytes;
+    uint8_t* raws = ring + C::kStages * C::kTileBytes;
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) ptx::mbar_init(&sh.full[i], C::kCodes ? C::kLoaders : 1), ptx::mbar_init(&sh.empty[i], 1);
+        for (int i = 0; i < C::kStages; ++i) ptx::mbar_init(&sh.full[i], C::kCodes ? C::kLoadWarps - 1 : 1), ptx::mbar_init(&sh.empty[i], 1);
+        for (int i = 0; i < C::kRaw; ++i) ptx::mbar_init(&sh.coded[i], 1), ptx::mbar_init(&sh.widened[i], C::kLoadWarps - 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&sh.raw[i], 1);
             ptx::mbar_init(&sh.scores[i], 1);
@@ -981,7 +947,6 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
         ptx::fence_mbar_init();
         sh.dead = 0;
         sh.looked[0] = sh.looked[1] = 0;
-        for (int i = 0; i < 8; ++i) sh.largest[i >> 1][i & 1] = 0;
         for (int i = 0; i < kMarks; ++i) sh.mark[i] = 0;
     }
     if (warp == C::kSoft) {
@@ -999,11 +964,11 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
             if (warp < C::kSoft) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kMoreRegs));
             else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kFewRegs));
         }
-        if (warp < C::kSoft) weigh<D, KIND>(p, sh, query, ring + C::kStages * C::kTileBytes);
+        if (warp < C::kSoft) weigh<D, KIND>(p, sh, query, raws + C::kRaw * C::kRawBytes);
         else if (warp == C::kSoft) issue_products<D, KIND>(p, sh, ptx::smem_addr(query), ptx::smem_addr(ring));
         else if (warp == C::kSoft + 1) watch<D, KIND>(p, sh);
-        else if constexpr (C::kCodes) widen_units<D>(p, sh, ring);
-        else if (warp == C::kSoft + 2) copy_units<D>(p, sh, ring, &mk, &mv);
+        else if (warp == C::kSoft + 2) copy_units<D, KIND>(p, sh, C::kCodes ? raws : ring, &mk, &mv);
+        else if constexpr (C::kCodes) widen_units<D>(p, sh, raws, ring);
         else check_units<D>(p, sh, ring);
         ptx::cp_async_wait_all();
         if (warp == C::kSoft) {
@@ -1041,22 +1006,23 @@ Encode encoder() {
     return e;
 }
 
-// Keys or values as [page][head][slot][D], boxes of 64 dimensions x `rows` slots.  An
-// axis of one place takes any stride.
+// Keys or values as [page][head][slot][D], boxes of `rows` slots x 64 dimensions in the
+// products' swizzle, or of codes x D.  An axis of one place takes any stride.
 bool describe(CUtensorMap* map, const AttnArgs& a, const uint8_t* base, int rows) {
     const Encode e = encoder();
     if (!e) return false;
+    const bool codes = a.kind == FP8BS_KV_E4M3;
     const int page = 1 << a.page_log2;
-    const cuuint64_t own = static_cast<cuuint64_t>(a.D) * 2;
+    const cuuint64_t own = static_cast<cuuint64_t>(a.D) * (codes ? 1 : 2);
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(a.Hk),
                                 static_cast<cuuint64_t>(a.pages)};
     const cuuint64_t strides[3] = {page > 1 ? static_cast<cuuint64_t>(a.sstride) : own,
                                    a.Hk > 1 ? static_cast<cuuint64_t>(a.hstride) : own,
                                    a.pages > 1 ? static_cast<cuuint64_t>(a.pstride) : own};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1}, step[4] = {1, 1, 1, 1};
-    return e(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t*>(base), dims, strides, box, step,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t box[4] = {codes ? static_cast<cuuint32_t>(a.D) : 64u, static_cast<cuuint32_t>(rows), 1, 1}, step[4] = {1, 1, 1, 1};
+    return e(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t*>(base), dims,
+             strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, int KIND>
@@ -1066,10 +1032,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     const cudaError_t e = attn_allow_shared(attn_chunk_kernel<D, KIND>, C::kSmem, done);
     if (e != cudaSuccess) return e;
     CUtensorMap mk = {}, mv = {};
-    if (!C::kCodes) {
-        const int rows = min(1 << a.page_log2, C::kKeys);
-        if (!describe(&mk, a, a.k, rows) || !describe(&mv, a, a.v, rows)) return cudaErrorInvalidValue;
-    }
+    const int rows = min(1 << a.page_log2, C::kKeys);
+    if (!describe(&mk, a, a.k, rows) || !describe(&mv, a, a.v, rows)) return cudaErrorInvalidValue;
     const cudaError_t r = w4::launch_dependent(attn_chunk_kernel<D, KIND>, a.sm_count, C::kThreads, C::kSmem, stream,
                                                static_cast<const AttnParams&>(a), mk, mv);
     return r == cudaSuccess ? launch_attn_join(a, C::kTile, a.sm_count, stream) : r;

@@ -713,7 +713,9 @@ size_t attn_workspace_bytes(int D, int sm_count) {
 constexpr int64_t kChunkRows = 17;
 
 cudaError_t launch_attn_paged(const AttnArgs& a, cudaStream_t stream) {
-    if (static_cast<int64_t>(a.T) * a.G >= kChunkRows * a.B) return launch_attn_chunk(a, stream);
+    // (boxes of one row of 64 codes would not begin on 128 bytes of shared memory)
+    const bool boxes = a.kind == FP8BS_KV_BF16 || a.D > 64 || a.page_log2 > 0;
+    if (static_cast<int64_t>(a.T) * a.G >= kChunkRows * a.B && boxes) return launch_attn_chunk(a, stream);
     return launch_attn_decode(a, stream);
 }
 
