@@ -138,6 +138,9 @@ int rope_check(const RopeArgs& a) {
     auto apart = [&](int64_t ld, int64_t hs, int H) {
         return stride_ok(ld) && stride_ok(hs) && (H < 2 || hs >= a.D) && (a.T < 2 || ld >= a.D);
     };
+    // (head strides count 32 bits of bytes in the kernel)
+    for (int64_t hs : {a.Hq ? a.hsq : 0, a.Hq ? a.hsqo : 0, a.Hk ? a.hsk : 0, a.Hk && a.append ? a.hsv : 0, a.Hk && !a.append ? a.hsko : 0})
+        if (hs >= int64_t(1) << 31) return FP8BS_ERR_ARG;
     if (a.Hq && (!stride_ok(a.ldq) || !stride_ok(a.hsq) || !apart(a.ldqo, a.hsqo, a.Hq))) return FP8BS_ERR_ARG;
     if (a.Hk && (!stride_ok(a.ldk) || !stride_ok(a.hsk))) return FP8BS_ERR_ARG;
     if (a.Hk && (a.append ? !stride_ok(a.ldv) || !stride_ok(a.hsv) : !apart(a.ldko, a.hsko, a.Hk))) return FP8BS_ERR_ARG;

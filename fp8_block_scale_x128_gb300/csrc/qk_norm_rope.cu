@@ -19,35 +19,32 @@
 namespace fp8bs {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+constexpr int kStages = 8;  // passes under way in a block: 16 KB
 
 struct RopeParams {
     const uint16_t *q, *k, *v;
-    int64_t ldq, hsq, ldk, hsk, ldv, hsv;
+    int64_t ldq, ldk, ldv, ldqo, ldko;     // bytes, as all strides here
+    uint32_t hsq, hsk, hsv, hsqo, hsko;
     int Hq, Hk, rows;  // rows of a token: queries, keys, values
     const int64_t* positions;
     const uint64_t* freqs;
     int half;  // R / 2
-    int interleaved;
     float amplitude, eps;
     const uint16_t *gq, *gk;
     uint16_t *qo, *ko;
-    int64_t ldqo, hsqo, ldko, hsko;
     const int64_t* slots;
     uint8_t *ck, *cv, *zk, *zv;
     int64_t cps, css, chs, zps, zss, zhs;  // bytes
     int64_t cslots;
     int page_log2;
     uint32_t* err;
-    int parts;  // blocks of a token
+    int parts;  // tasks of a token
+    int64_t tasks;
 };
 
 enum { kDense = 0, kBf16 = 1, kE4m3 = 2 };
-
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-}
 
 // A row's codes and scale byte from fp32 values in L lanes: the ue8m0 rule.  Its
 // largest magnitude is compared by bits, so that infinities and NaNs are seen.
@@ -70,138 +67,241 @@ __device__ __forceinline__ uint2 quant_row(const float (&v)[8], uint32_t* byte) 
     return c;
 }
 
-template <int D, int DEST>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeParams p) {
+// Pairs of fp32 operations in one instruction each.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ void widen8(const uint4& w, uint64_t (&v)[4]) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pair(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
+}
+
+template <int D, int DEST, bool HALF>
+__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr int L = D / 8;               // lanes of a row
     constexpr int kRows = kWarps * 32 / L;  // rows of a pass
-    __shared__ float cosines[D / 2], sines[D / 2];
-    const int lane = threadIdx.x & 31, l = lane & (L - 1);
-    const int slot_row = threadIdx.x / L;
-    const int64_t t = blockIdx.x / p.parts;
-    const int part = blockIdx.x - static_cast<int>(t) * p.parts;
+    // what a column is multiplied by, and its partner: 1 and 0 where nothing turns
+    __shared__ __align__(16) float cosines[2][D], sines[2][D];
+    __shared__ __align__(16) float gammas[2][D];  // of queries and keys
+    const int lane = threadIdx.x & 31, l = lane & (L - 1), slot_row = threadIdx.x / L;
+    const int R = 2 * p.half;
+    for (int i = threadIdx.x; i < 2 * D; i += kThreads)
+        if (i % D >= R) cosines[i / D][i % D] = 1.0f, sines[i / D][i % D] = 0.0f;
 
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
 
-    const int first = part * kRows + slot_row;
-    auto load = [&](int r) {
-        const uint16_t* src = r < p.Hq                ? p.q + t * p.ldq + r * p.hsq
-                              : r < p.Hq + p.Hk ? p.k + t * p.ldk + (r - p.Hq) * p.hsk
-                                                : p.v + t * p.ldv + (r - p.Hq - p.Hk) * p.hsv;
-        return r < p.rows ? *reinterpret_cast<const uint4*>(src + 8 * l) : make_uint4(0, 0, 0, 0);
-    };
-    uint4 raw = load(first);
-    int64_t slot = -1;
-    if (DEST != kDense) {
-        slot = p.slots[t];
-        if (slot >= p.cslots) {
-            if (threadIdx.x == 0) record_error(p.err, FP8BS_ERR_DEVICE);
-            slot = -1;
-        }
+    for (int i = threadIdx.x; i < D; i += kThreads) {
+        if (p.gq) gammas[0][i] = bf16_bits_to_float(p.gq[i]);
+        if (p.gk) gammas[1][i] = bf16_bits_to_float(p.gk[i]);
     }
-    for (int i = threadIdx.x; i < p.half; i += kThreads) {
-        const uint64_t turn = static_cast<uint64_t>(p.positions[t]) * p.freqs[i];
-        float s, c;
-        sincospif(__int2float_rn(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
-        sines[i] = s * p.amplitude;
-        cosines[i] = c * p.amplitude;
-    }
-    __syncthreads();
-
-    // the rotation of this lane's columns; untouched ones turn by nothing
-    float co[8], si[8];
-    const int R = 2 * p.half;
-    const bool turns = 8 * l < R;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int col = 8 * l + i;
-        co[i] = 1.0f;
-        si[i] = 0.0f;
-        if (col < R) {
-            const int at = p.interleaved ? col >> 1 : (col < p.half ? col : col - p.half);
-            co[i] = cosines[at];
-            // y = x cos +- partner sin: minus for the first of a pair
-            si[i] = (p.interleaved ? (col & 1) == 0 : col < p.half) ? -sines[at] : sines[at];
-        }
-    }
+    const bool turns = 8 * l < R;  // half layout: all of this lane's columns do
     const int away = p.half >> 3;  // lanes between the halves
     const int partner = 8 * l < p.half ? lane + away : lane - away;
+    const int keys = p.Hq, values = p.Hq + p.Hk;  // first rows
 
-    // a pass is kRows rows; whole warps leave together only past the last row
-    for (int r0 = part * kRows; r0 < p.rows; r0 += p.parts * kRows) {
-        const int r = r0 + slot_row;
-        const uint4 now = raw;
-        if (r0 + p.parts * kRows < p.rows) raw = load(r + p.parts * kRows);
-        float v[8];
-        unpack_bf16x8(now, v);
-        const bool value = r >= p.Hq + p.Hk;
-        const uint16_t* gamma = r < p.Hq ? p.gq : p.gk;
-        const bool norm = !value && gamma != nullptr;
-        if (__any_sync(0xFFFFFFFFu, norm)) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-#pragma unroll
-            for (int off = L / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
-            if (norm) {
-                const float ms = ss * (1.0f / D) + p.eps;
-                const float inv = ms > 0.0f ? __frsqrt_rn(ms) : (ms == 0.0f ? 0.0f : ms);
-                float g[8];
-                unpack_bf16x8(*reinterpret_cast<const uint4*>(gamma + 8 * l), g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * g[i];
+    // A thread's own pieces, kStages - 1 passes ahead, in its own places of shared memory.
+    extern __shared__ __align__(16) uint8_t ring[];
+    const uint32_t mine = ptx::smem_addr(ring) + 16 * threadIdx.x;
+    int64_t task = blockIdx.x;
+    int64_t next_task = task;
+    int next_row = 0, stage_in = 0, stage = 0;  // the pass to fetch
+    const uint8_t *nq, *nk, *nv;                // its token
+    auto next_token = [&] {
+        const int64_t t = p.parts == 1 ? next_task : next_task / p.parts;
+        nq = reinterpret_cast<const uint8_t*>(p.q) + t * p.ldq + 16 * l;
+        nk = reinterpret_cast<const uint8_t*>(p.k) + t * p.ldk + 16 * l;
+        nv = reinterpret_cast<const uint8_t*>(p.v) + t * p.ldv + 16 * l;
+        next_row = static_cast<int>(next_task - t * p.parts) * kRows;
+    };
+    next_token();
+    auto fetch = [&] {
+        if (next_task < p.tasks) {
+            const int r = next_row + slot_row;
+            const uint8_t* base = r < keys ? nq : r < values ? nk : nv;
+            const uint32_t hs = r < keys ? p.hsq : r < values ? p.hsk : p.hsv;
+            const uint32_t h = r - (r < keys ? 0 : r < values ? keys : values);
+            if (r < p.rows) cp_async16(mine + stage_in * (kThreads * 16), base + static_cast<uint64_t>(h) * hs);
+            next_row += p.parts * kRows;
+            if (next_row >= p.rows) {
+                next_task += gridDim.x;
+                if (next_task < p.tasks) next_token();
             }
+            if (++stage_in == kStages) stage_in = 0;
         }
-        if (p.half && __any_sync(0xFFFFFFFFu, !value)) {
-            float w[8];
-            if (p.interleaved) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = v[i ^ 1];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = __shfl_sync(0xFFFFFFFFu, v[i], partner);
-            }
-            if (!value && turns) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (8 * l + i < R) v[i] = fmaf(v[i], co[i], w[i] * si[i]);
-            }
+        cp_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) fetch();
+    int64_t position = 0, slot = -1;
+    auto look = [&](int64_t t) {
+        if (p.half) position = p.positions[t];
+        if (DEST != kDense) slot = p.slots[t];
+    };
+    look(p.parts == 1 ? task : task / p.parts);
+    int buffer = 0;
+#pragma unroll 1
+    for (; task < p.tasks; task += gridDim.x, buffer ^= 1) {
+        const int64_t t = p.parts == 1 ? task : task / p.parts;
+        const int part = static_cast<int>(task - t * p.parts);
+        for (int i = threadIdx.x; i < p.half; i += kThreads) {
+            const uint64_t turn = static_cast<uint64_t>(position) * p.freqs[i];
+            float s, c;
+            sincospif(__int2float_rn(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
+            s *= p.amplitude, c *= p.amplitude;
+            // y = x cos -+ partner sin: minus for the first of a pair
+            const int first = HALF ? i : 2 * i, second = HALF ? i + p.half : 2 * i + 1;
+            cosines[buffer][first] = cosines[buffer][second] = c;
+            sines[buffer][first] = -s, sines[buffer][second] = s;
         }
-        if (DEST == kE4m3 && __any_sync(0xFFFFFFFFu, r >= p.Hq)) {
-            uint32_t byte;
-            const uint2 codes = quant_row<L>(v, &byte);
-            if (r >= p.Hq && r < p.rows && slot >= 0) {
+        __syncthreads();  // (a block that is a token ahead fills the other table)
+        int64_t to = -1, scale_to = -1;  // offsets of the slot in the cache
+        if (DEST != kDense) {
+            if (slot >= p.cslots) {
+                if (threadIdx.x == 0) record_error(p.err, FP8BS_ERR_DEVICE);
+            } else if (slot >= 0) {
                 const int64_t page = slot >> p.page_log2, at = slot & ((int64_t(1) << p.page_log2) - 1);
-                const int h = r - p.Hq - (value ? p.Hk : 0);
-                *reinterpret_cast<uint2*>((value ? p.cv : p.ck) + page * p.cps + at * p.css + h * p.chs + 8 * l) = codes;
-                if (l == 0) (value ? p.zv : p.zk)[page * p.zps + at * p.zss + h * p.zhs] = static_cast<uint8_t>(byte);
+                to = page * p.cps + at * p.css;
+                scale_to = page * p.zps + at * p.zss;
             }
         }
-        if (r < p.Hq) {
-            *reinterpret_cast<uint4*>(p.qo + t * p.ldqo + r * p.hsqo + 8 * l) = pack8(v);
-        } else if (r < p.rows && DEST == kDense) {
-            *reinterpret_cast<uint4*>(p.ko + t * p.ldko + (r - p.Hq) * p.hsko + 8 * l) = pack8(v);
-        } else if (r < p.rows && DEST == kBf16 && slot >= 0) {
-            const int64_t page = slot >> p.page_log2, at = slot & ((int64_t(1) << p.page_log2) - 1);
-            const int h = r - p.Hq - (value ? p.Hk : 0);
-            // values are copied, whatever their bits
-            *reinterpret_cast<uint4*>((value ? p.cv : p.ck) + page * p.cps + at * p.css + h * p.chs + 16 * l) =
-                value ? now : pack8(v);
+        if (task + gridDim.x < p.tasks) look(p.parts == 1 ? task + gridDim.x : (task + gridDim.x) / p.parts);
+        uint64_t co[4], si[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const ulonglong2 c = reinterpret_cast<const ulonglong2*>(&cosines[buffer][8 * l])[i];
+            const ulonglong2 n = reinterpret_cast<const ulonglong2*>(&sines[buffer][8 * l])[i];
+            co[2 * i] = c.x, co[2 * i + 1] = c.y, si[2 * i] = n.x, si[2 * i + 1] = n.y;
+        }
+        uint8_t* oq = reinterpret_cast<uint8_t*>(p.qo) + t * p.ldqo + 16 * l;
+        uint8_t* ok = reinterpret_cast<uint8_t*>(p.ko) + t * p.ldko + 16 * l;
+        uint8_t* ck = p.ck + to + (DEST == kE4m3 ? 8 : 16) * l;
+        uint8_t* cv = p.cv + to + (DEST == kE4m3 ? 8 : 16) * l;
+#pragma unroll 1
+        for (int r0 = part * kRows; r0 < p.rows; r0 += p.parts * kRows) {
+            const int r = r0 + slot_row;
+            fetch();
+            cp_wait<kStages - 1>();
+            // (a row past the last has what was there before: nothing is made of it)
+            const uint4 now = *reinterpret_cast<const uint4*>(ring + stage * (kThreads * 16) + 16 * threadIdx.x);
+            if (++stage == kStages) stage = 0;
+            const bool key = r >= keys && r < values, value = r >= values;
+            uint64_t v[4];
+            widen8(now, v);
+            const bool norm = key ? p.gk != nullptr : !value && p.gq != nullptr;
+            if (__any_sync(0xFFFFFFFFu, norm)) {
+                uint64_t squares = mul2(v[0], v[0]);
+#pragma unroll
+                for (int i = 1; i < 4; ++i) squares = fma2(v[i], v[i], squares);
+                const float2 s2 = halves(squares);
+                float ss = s2.x + s2.y;
+#pragma unroll
+                for (int off = L / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, off);
+                if (norm) {
+                    const float ms = ss * (1.0f / D) + p.eps;
+                    const float inv = ms == 0.0f ? 0.0f : rsqrtf(ms);
+                    const uint64_t inv2 = pair(inv, inv);
+                    const ulonglong2* g = reinterpret_cast<const ulonglong2*>(&gammas[key][8 * l]);
+                    const ulonglong2 g0 = g[0], g1 = g[1];
+                    v[0] = mul2(mul2(v[0], inv2), g0.x), v[1] = mul2(mul2(v[1], inv2), g0.y);
+                    v[2] = mul2(mul2(v[2], inv2), g1.x), v[3] = mul2(mul2(v[3], inv2), g1.y);
+                }
+            }
+            if (p.half && __any_sync(0xFFFFFFFFu, !value)) {
+                if (HALF) {
+                    uint64_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 x = halves(v[i]);
+                        w[i] = pair(__shfl_sync(0xFFFFFFFFu, x.x, partner), __shfl_sync(0xFFFFFFFFu, x.y, partner));
+                    }
+                    // (a column that does not turn keeps its value, whatever other columns hold)
+                    if (turns && !value)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = fma2(w[i], si[i], mul2(v[i], co[i]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (8 * l + 2 * i < R && !value) {
+                            const float2 x = halves(v[i]);
+                            v[i] = fma2(pair(x.y, x.x), si[i], mul2(v[i], co[i]));
+                        }
+                }
+            }
+            if (DEST == kE4m3 && __any_sync(0xFFFFFFFFu, r >= keys)) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[2 * i] = halves(v[i]).x, x[2 * i + 1] = halves(v[i]).y;
+                uint32_t byte;
+                const uint2 codes = quant_row<L>(x, &byte);
+                if (r >= keys && r < p.rows && to >= 0) {
+                    const int h = r - (value ? values : keys);
+                    *reinterpret_cast<uint2*>((value ? cv : ck) + h * p.chs) = codes;
+                    if (l == 0) (value ? p.zv : p.zk)[scale_to + h * p.zhs] = static_cast<uint8_t>(byte);
+                }
+            }
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = pack_bf16(halves(v[i]).x, halves(v[i]).y);
+            const uint4 out = make_uint4(o[0], o[1], o[2], o[3]);
+            if (r < keys) {
+                *reinterpret_cast<uint4*>(oq + static_cast<uint64_t>(r) * p.hsqo) = out;
+            } else if (r < p.rows && DEST == kDense) {
+                *reinterpret_cast<uint4*>(ok + static_cast<uint64_t>(r - keys) * p.hsko) = out;
+            } else if (r < p.rows && DEST == kBf16 && to >= 0) {
+                // values are copied, whatever their bits
+                const int h = r - (value ? values : keys);
+                *reinterpret_cast<uint4*>((value ? cv : ck) + h * p.chs) = value ? now : out;
+            }
         }
     }
 }
 
+template <int D, int DEST, bool HALF>
+cudaError_t launch_to(const RopeParams& p, int sm_count, cudaStream_t stream) {
+    // as many blocks as the device holds at once, each through its share of the tokens:
+    // gammas are read once, and a token's table is computed while others are stored
+    static std::atomic<int> held{0};
+    int blocks = held.load(std::memory_order_relaxed);
+    if (!blocks) {
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, qk_norm_rope_kernel<D, DEST, HALF>, kThreads, kStages * kThreads * 16);
+        if (e != cudaSuccess) return e;
+        held.store(blocks < 1 ? 1 : blocks, std::memory_order_relaxed);
+    }
+    const int64_t most = static_cast<int64_t>(sm_count) * (blocks < 1 ? 1 : blocks);
+    return w4::launch_dependent(qk_norm_rope_kernel<D, DEST, HALF>, static_cast<int>(p.tasks < most ? p.tasks : most), kThreads,
+                                kStages * kThreads * 16, stream, p);
+}
+
 template <int D>
-cudaError_t launch_d(const RopeParams& p0, int64_t T, int dest, int sm_count, cudaStream_t stream) {
+cudaError_t launch_d(const RopeParams& p0, int64_t T, int dest, bool half, int sm_count, cudaStream_t stream) {
     RopeParams p = p0;
     constexpr int kRows = kWarps * 32 / (D / 8);
     const int passes = (p.rows + kRows - 1) / kRows;
-    p.parts = T * passes <= 8 * static_cast<int64_t>(sm_count) ? passes : 1;
-    const int64_t grid = T * p.parts;
-    auto kernel = dest == kDense ? qk_norm_rope_kernel<D, kDense>
-                  : dest == kBf16 ? qk_norm_rope_kernel<D, kBf16>
-                                  : qk_norm_rope_kernel<D, kE4m3>;
-    return w4::launch_dependent(kernel, static_cast<int>(grid), kThreads, 0, stream, p);
+    // a block a pass where that leaves the machine unfilled
+    p.parts = T * passes <= 4 * static_cast<int64_t>(sm_count) ? passes : 1;
+    p.tasks = T * p.parts;
+    if (dest == kDense) return half ? launch_to<D, kDense, true>(p, sm_count, stream) : launch_to<D, kDense, false>(p, sm_count, stream);
+    if (dest == kBf16) return half ? launch_to<D, kBf16, true>(p, sm_count, stream) : launch_to<D, kBf16, false>(p, sm_count, stream);
+    return half ? launch_to<D, kE4m3, true>(p, sm_count, stream) : launch_to<D, kE4m3, false>(p, sm_count, stream);
 }
 
 }  // namespace
@@ -209,16 +309,18 @@ cudaError_t launch_d(const RopeParams& p0, int64_t T, int dest, int sm_count, cu
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream) {
     RopeParams p = {};
     p.q = a.q, p.k = a.k, p.v = a.v;
-    p.ldq = a.ldq, p.hsq = a.hsq, p.ldk = a.ldk, p.hsk = a.hsk, p.ldv = a.ldv, p.hsv = a.hsv;
+    p.ldq = 2 * a.ldq, p.ldk = 2 * a.ldk, p.ldv = 2 * a.ldv;
+    p.hsq = static_cast<uint32_t>(2 * a.hsq), p.hsk = static_cast<uint32_t>(2 * a.hsk), p.hsv = static_cast<uint32_t>(2 * a.hsv);
     p.Hq = a.Hq, p.Hk = a.Hk;
     p.rows = a.Hq + a.Hk + (a.append ? a.Hk : 0);
     p.positions = a.positions, p.freqs = a.freqs;
     p.half = a.R / 2;
-    p.interleaved = a.layout == FP8BS_ROPE_INTERLEAVED;
+    const bool half = a.layout == FP8BS_ROPE_HALF;
     p.amplitude = a.amplitude, p.eps = a.eps;
     p.gq = a.gq, p.gk = a.gk;
     p.qo = a.qo, p.ko = a.ko;
-    p.ldqo = a.ldqo, p.hsqo = a.hsqo, p.ldko = a.ldko, p.hsko = a.hsko;
+    p.ldqo = 2 * a.ldqo, p.ldko = 2 * a.ldko;
+    p.hsqo = static_cast<uint32_t>(2 * a.hsqo), p.hsko = static_cast<uint32_t>(2 * a.hsko);
     int dest = kDense;
     if (a.append) {
         const fp8bs_kv_cache& c = a.cache;
@@ -233,9 +335,9 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream) {
         p.cslots = c.pages << p.page_log2;
         p.err = a.err;
     }
-    if (a.D == 64) return launch_d<64>(p, a.T, dest, a.sm_count, stream);
-    if (a.D == 128) return launch_d<128>(p, a.T, dest, a.sm_count, stream);
-    return launch_d<256>(p, a.T, dest, a.sm_count, stream);
+    if (a.D == 64) return launch_d<64>(p, a.T, dest, half, a.sm_count, stream);
+    if (a.D == 128) return launch_d<128>(p, a.T, dest, half, a.sm_count, stream);
+    return launch_d<256>(p, a.T, dest, half, a.sm_count, stream);
 }
 
 }  // namespace fp8bs

@@ -540,7 +540,7 @@ int fp8bs_rope_freqs(int rotary_dim, double theta, int scaling, double factor, d
  *   q_out, k_out : bf16 [T, heads, D] with strides of their own; may be q and k
  *                themselves with the same strides, else apart from them.
  * All pointers 16-byte aligned and all strides multiples of 8, where not said
- * otherwise.  One launch, dependent on its predecessor (programmatic dependent
+ * otherwise; head strides below 2^31.  One launch, dependent on its predecessor (programmatic dependent
  * launch), for which it waits before it touches memory.
  * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN, FP8BS_ERR_CUDA. */
 int fp8bs_qk_norm_rope(const uint16_t* q, int64_t ldq, int64_t hsq, const uint16_t* k, int64_t ldk, int64_t hsk,
