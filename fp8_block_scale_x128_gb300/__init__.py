@@ -599,22 +599,14 @@ def new_kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, kind:
     return KvCache(*(torch.zeros(shape[:n], dtype=torch.uint8, device=device) for n in (4, 4, 3, 3)))
 
 
-def _heads(t: torch.Tensor, T: int, D: int):
-    """(token stride, head stride) of bf16 heads [T, heads, D]."""
-    assert t.dtype is torch.bfloat16
-    T2, _, D2 = t.shape
-    ld, hs, one = t.stride()
-    assert T2 == T and D2 == D and one == 1
-    return ld, hs
-
-
-def _gamma(g: torch.Tensor | None, D: int, device: int):
-    if g is None:
-        return None
+def _gamma(g: torch.Tensor, shape, device: int) -> int:
     if g.get_device() != device:
         _wrong_device(g)
-    assert g.dtype is torch.bfloat16 and g.shape == (D,) and g.is_contiguous()
+    assert g.dtype is _BF16 and g.shape == shape and g.is_contiguous()
     return g.data_ptr()
+
+
+_BF16 = torch.bfloat16
 
 
 def fp8bs_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, rope: Rope,
@@ -624,27 +616,33 @@ def fp8bs_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor
     [T, Hq, D] and key heads k [T, Hk, D] (slices of wider rows do) at int64 positions
     [T].  Returns (q_out, k_out), which may be given: q and k themselves too."""
     device = q.get_device()
-    if device < 0 or not device == k.get_device() == positions.get_device() == rope.freqs.get_device() == torch._C._cuda_getDevice():
-        _wrong_device(q, k, positions, rope.freqs)
-    T, Hq, D = q.shape
-    Hk = k.shape[1]
-    ldq, hsq = _heads(q, T, D)
-    ldk, hsk = _heads(k, T, D)
-    assert positions.dtype is torch.int64 and positions.shape == (T,) and positions.is_contiguous()
-    gq, gk = _gamma(gamma_q, D, device), _gamma(gamma_k, D, device)
+    freqs = rope.freqs
+    if device < 0 or not (device == k.get_device() == positions.get_device() == freqs.get_device() ==
+                          torch._C._cuda_getDevice()):
+        _wrong_device(q, k, positions, freqs)
+    qshape, kshape = q.shape, k.shape
+    T, Hq, D = qshape
+    Tk, Hk, Dk = kshape
+    ldq, hsq, q1 = q.stride()
+    ldk, hsk, k1 = k.stride()
+    assert q.dtype is _BF16 and k.dtype is _BF16 and q1 == 1 == k1 and Tk == T and Dk == D
+    assert positions.dtype is torch.int64 and positions.shape == qshape[:1] and positions.is_contiguous()
+    gq = None if gamma_q is None else _gamma(gamma_q, qshape[2:], device)
+    gk = None if gamma_k is None else _gamma(gamma_k, qshape[2:], device)
     if q_out is None or k_out is None:
         with _on_stream(stream, device):
             if q_out is None:
-                q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+                q_out = torch.empty(qshape, dtype=_BF16, device=q.device)
             if k_out is None:
-                k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=q.device)
+                k_out = torch.empty(kshape, dtype=_BF16, device=q.device)
     if not device == q_out.get_device() == k_out.get_device():
         _wrong_device(q, q_out, k_out)
-    assert q_out.shape[1] == Hq and k_out.shape[1] == Hk
-    ldqo, hsqo = _heads(q_out, T, D)
-    ldko, hsko = _heads(k_out, T, D)
+    ldqo, hsqo, q1 = q_out.stride()
+    ldko, hsko, k1 = k_out.stride()
+    assert q_out.dtype is _BF16 and k_out.dtype is _BF16 and q1 == 1 == k1
+    assert q_out.shape == qshape and k_out.shape == kshape
     rc = (_lib or lib()).fp8bs_qk_norm_rope(
-        q.data_ptr(), ldq, hsq, k.data_ptr(), ldk, hsk, T, Hq, Hk, D, positions.data_ptr(), rope.freqs.data_ptr(),
+        q.data_ptr(), ldq, hsq, k.data_ptr(), ldk, hsk, T, Hq, Hk, D, positions.data_ptr(), freqs.data_ptr(),
         rope.rotary_dim, rope.layout, rope.amplitude, gq, gk, eps, q_out.data_ptr(), ldqo, hsqo, k_out.data_ptr(), ldko,
         hsko, torch._C._cuda_getCurrentRawStream(device) if stream is None else _raw_stream(stream, device))
     if rc:
@@ -662,28 +660,33 @@ def fp8bs_qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     writes nothing).  Returns q_out.  error: a zeroed uint8 tensor (a workspace does)
     whose first word takes the status of slots past the cache (fp8bs_check_error)."""
     device = q.get_device()
+    freqs = rope.freqs
     if device < 0 or not (device == k.get_device() == v.get_device() == positions.get_device() == slots.get_device() ==
-                          rope.freqs.get_device() == cache.device_index == torch._C._cuda_getDevice()):
-        _wrong_device(q, k, v, positions, slots, rope.freqs, cache.tensors[0])
-    T, Hq, D = q.shape
-    Hk = cache.kv_heads
-    ldq, hsq = _heads(q, T, D)
-    ldk, hsk = _heads(k, T, D)
-    ldv, hsv = _heads(v, T, D)
-    assert D == cache.head_dim and k.shape[1] == Hk == v.shape[1]
-    assert positions.dtype is torch.int64 and positions.shape == (T,) and positions.is_contiguous()
-    assert slots.dtype is torch.int64 and slots.shape == (T,) and slots.is_contiguous()
-    gq, gk = _gamma(gamma_q, D, device), _gamma(gamma_k, D, device)
+                          freqs.get_device() == cache.device_index == torch._C._cuda_getDevice()):
+        _wrong_device(q, k, v, positions, slots, freqs, cache.tensors[0])
+    qshape = q.shape
+    T, Hq, D = qshape
+    ldq, hsq, q1 = q.stride()
+    ldk, hsk, k1 = k.stride()
+    ldv, hsv, v1 = v.stride()
+    assert q.dtype is _BF16 and k.dtype is _BF16 and v.dtype is _BF16 and q1 == 1 == k1 and v1 == 1
+    assert D == cache.head_dim and k.shape == (T, cache.kv_heads, D) == v.shape
+    tokens = qshape[:1]
+    assert positions.dtype is torch.int64 and positions.shape == tokens and positions.is_contiguous()
+    assert slots.dtype is torch.int64 and slots.shape == tokens and slots.is_contiguous()
+    gq = None if gamma_q is None else _gamma(gamma_q, qshape[2:], device)
+    gk = None if gamma_k is None else _gamma(gamma_k, qshape[2:], device)
     if q_out is None:
         with _on_stream(stream, device):
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+            q_out = torch.empty(qshape, dtype=_BF16, device=q.device)
     if q_out.get_device() != device or (error is not None and error.get_device() != device):
         _wrong_device(*(t for t in (q, q_out, error) if t is not None))
-    assert q_out.shape[1] == Hq and (error is None or error.dtype is torch.uint8 and error.numel() >= 4)
-    ldqo, hsqo = _heads(q_out, T, D)
+    ldqo, hsqo, q1 = q_out.stride()
+    assert q_out.dtype is _BF16 and q_out.shape == qshape and q1 == 1
+    assert error is None or error.dtype is torch.uint8 and error.numel() >= 4
     rc = (_lib or lib()).fp8bs_qk_norm_rope_append(
         q.data_ptr(), ldq, hsq, k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv, T, Hq, positions.data_ptr(),
-        slots.data_ptr(), rope.freqs.data_ptr(), rope.rotary_dim, rope.layout, rope.amplitude, gq, gk, eps,
+        slots.data_ptr(), freqs.data_ptr(), rope.rotary_dim, rope.layout, rope.amplitude, gq, gk, eps,
         q_out.data_ptr(), ldqo, hsqo, cache._ref, None if error is None else error.data_ptr(),
         torch._C._cuda_getCurrentRawStream(device) if stream is None else _raw_stream(stream, device))
     if rc:
@@ -717,25 +720,26 @@ def fp8bs_attn_paged(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor,
     if device < 0 or not (device == cache.device_index == block_table.get_device() == cu_q.get_device() ==
                           kv_len.get_device() == torch._C._cuda_getDevice()):
         _wrong_device(q, cache.tensors[0], block_table, cu_q, kv_len)
-    T, Hq, D = q.shape
+    qshape = q.shape
+    T, Hq, D = qshape
     B, cols = block_table.shape
-    ldq, hsq = _heads(q, T, D)
+    ldq, hsq, q1 = q.stride()
     rows, one = block_table.stride()
-    assert D == cache.head_dim
+    assert q.dtype is _BF16 and q1 == 1 and D == cache.head_dim
     assert block_table.dtype is torch.int32 and (one == 1 or cols < 2)
     assert cu_q.dtype is torch.int32 and cu_q.shape == (B + 1,) and cu_q.is_contiguous()
     assert kv_len.dtype is torch.int32 and kv_len.shape == (B,) and kv_len.is_contiguous()
     if o is None or workspace is None:
         with _on_stream(stream, device):
             if o is None:
-                o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+                o = torch.empty(qshape, dtype=_BF16, device=q.device)
             if workspace is None:
                 workspace = new_attn_workspace(D, q.device)
     if not device == o.get_device() == workspace.get_device():
         _wrong_device(q, o, workspace)
-    assert o.shape[1] == Hq
+    ldo, hso, o1 = o.stride()
+    assert o.dtype is _BF16 and o.shape == qshape and o1 == 1
     assert workspace.dtype is torch.uint8 and workspace.is_contiguous()
-    ldo, hso = _heads(o, T, D)
     rc = (_lib or lib()).fp8bs_attn_paged(
         q.data_ptr(), ldq, hsq, T, Hq, cache._ref, block_table.data_ptr(), max(rows, cols), cols, B, cu_q.data_ptr(),
         kv_len.data_ptr(), D ** -0.5 if scale is None else scale, window, o.data_ptr(), ldo, hso, workspace.data_ptr(),
