@@ -61,7 +61,11 @@ struct Cfg {
     static_assert(!kDeal || kSoft * 32 * kMoreRegs + (kThreads - kSoft * 32) * kFewRegs <= kThreads * (65536 / kThreads / 8 * 8),
                   "more registers than the launch has would be waited for without end");
     static constexpr int kLoadWarps = kThreads / 32 - kSoft - 2;
-    static constexpr int kLoaders = kLoadWarps * 32;
+    // warps that issue copies: keys and values each by one, as small pages make for many
+    // boxes and a warp issues them one by one (pages of 16, heads of 256: 171 us by one
+    // warp); of codes there are half as many, and widening needs the warps
+    static constexpr int kCopyWarps = kCodes ? 1 : 2;
+    static constexpr int kOthers = (kLoadWarps - kCopyWarps) * 32;  // threads that check or widen
     static constexpr int kTileBytes = kKeys * D * 2;
     static constexpr int kStages = kCodes ? 3 : 4;
     // codes as they are in the cache, on their way
@@ -297,7 +301,7 @@ __device__ __forceinline__ uint32_t odd_pair(uint32_t w) { return ((w & 0x7F807F
 // those of four keys), and the other loader warps widen them.
 template <int D, int KIND>
 __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint8_t* ring, const CUtensorMap* mk,
-                                           const CUtensorMap* mv) {
+                                           const CUtensorMap* mv, int kv0, int kv1) {  // keys: 0, values: 1
     using C = Cfg<D, KIND>;
     constexpr int kParts = C::kCodes ? 1 : D / 64, kWide = C::kCodes ? D : 64;  // boxes over a row, and their width
     constexpr int kMost = C::kKeys * kParts / 32;  // boxes of a lane
@@ -306,10 +310,12 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
     const int rows = min(1 << p.page_log2, C::kKeys), boxes = C::kKeys / rows * kParts;
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     Place at;
-    publish<C::kTile, C::kKeys>(p, sh, 0);
-    publish<C::kTile, C::kKeys>(p, sh, 1);
+    if (kv0 == 0) {
+        publish<C::kTile, C::kKeys>(p, sh, 0);
+        publish<C::kTile, C::kKeys>(p, sh, 1);
+    }
     bool alive = at.start(p, sh);
-    uint32_t fill = 0;
+    uint32_t fill = 0;  // tiles of both kinds
     int page[kMost];
     auto page_of = [&](int j) {
         int id;
@@ -372,10 +378,11 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
             alive &= at.next(p, sh);
             if (alive) find();
             if (alive && C::kCodes) read_scales();
-            if (at.item != item) publish<C::kTile, C::kKeys>(p, sh, at.item + 1);
+            if (at.item != item && kv0 == 0) publish<C::kTile, C::kKeys>(p, sh, at.item + 1);
         }
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++fill) {
+        for (int kv = kv0; kv <= kv1; ++kv) {
+            fill = 2 * static_cast<uint32_t>(u) + kv;
             const uint32_t stage = fill % kRing;
             if (alive && fill >= kRing)
                 alive = __all_sync(0xFFFFFFFFu, wait(sh, C::kCodes ? &sh.widened[stage] : &sh.empty[stage], ((fill / kRing) - 1) & 1, p));
@@ -397,7 +404,7 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
     }
     if (!alive) {  // what is under way lands before the block leaves
         const long long began = clock64();
-        for (uint32_t f = fill < kRing ? 0 : fill - kRing; f < fill; ++f)
+        for (uint32_t f = fill < kRing ? 0 : fill - kRing; f <= fill; ++f)
             while (!ptx::mbar_test(C::kCodes ? &sh.coded[f % kRing] : &sh.full[f % kRing], (f / kRing) & 1) &&
                    clock64() - began < 1000000) {
             }
@@ -407,8 +414,8 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
 template <int D>
 __device__ __forceinline__ void check_units(const AttnParams& p, Shared& sh, uint8_t* ring) {
     using C = Cfg<D, FP8BS_KV_BF16>;
-    constexpr int kThreads = C::kLoaders - 32, kPer = D / 8;
-    const int tid = threadIdx.x - (C::kSoft + 3) * 32;
+    constexpr int kThreads = C::kOthers, kPer = D / 8;
+    const int tid = threadIdx.x - (C::kThreads - kThreads);
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     Place at;
     bool alive = at.start(p, sh);
@@ -458,9 +465,9 @@ __device__ __forceinline__ void check_units(const AttnParams& p, Shared& sh, uin
 template <int D>
 __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, const uint8_t* raw, uint8_t* ring) {
     using C = Cfg<D, FP8BS_KV_E4M3>;
-    constexpr int kThreads = C::kLoaders - 32, kPer = D / 16;  // 16-byte pieces of a row
+    constexpr int kThreads = C::kOthers, kPer = D / 16;  // 16-byte pieces of a row
     constexpr int kStep = kThreads / kPer, kBatch = 4;          // rows between a thread's pieces
-    const int tid = threadIdx.x - (C::kSoft + 3) * 32, piece = tid % kPer;
+    const int tid = threadIdx.x - (C::kThreads - kThreads), piece = tid % kPer;
     const int first = tid < kStep * kPer ? tid / kPer : C::kKeys;
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     Place at;
@@ -933,8 +940,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
     uint8_t* raws = ring + C::kStages * C::kTileBytes;
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) ptx::mbar_init(&sh.full[i], C::kCodes ? C::kLoadWarps - 1 : 1), ptx::mbar_init(&sh.empty[i], 1);
-        for (int i = 0; i < C::kRaw; ++i) ptx::mbar_init(&sh.coded[i], 1), ptx::mbar_init(&sh.widened[i], C::kLoadWarps - 1);
+        for (int i = 0; i < C::kStages; ++i) ptx::mbar_init(&sh.full[i], C::kCodes ? C::kOthers / 32 : 1), ptx::mbar_init(&sh.empty[i], 1);
+        for (int i = 0; i < C::kRaw; ++i) ptx::mbar_init(&sh.coded[i], 1), ptx::mbar_init(&sh.widened[i], C::kOthers / 32);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&sh.raw[i], 1);
             ptx::mbar_init(&sh.scores[i], 1);
@@ -967,7 +974,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
         if (warp < C::kSoft) weigh<D, KIND>(p, sh, query, raws + C::kRaw * C::kRawBytes);
         else if (warp == C::kSoft) issue_products<D, KIND>(p, sh, ptx::smem_addr(query), ptx::smem_addr(ring));
         else if (warp == C::kSoft + 1) watch<D, KIND>(p, sh);
-        else if (warp == C::kSoft + 2) copy_units<D, KIND>(p, sh, C::kCodes ? raws : ring, &mk, &mv);
+        else if (warp < C::kSoft + 2 + C::kCopyWarps)
+            copy_units<D, KIND>(p, sh, C::kCodes ? raws : ring, &mk, &mv, warp - C::kSoft - 2, C::kCopyWarps == 1 ? 1 : warp - C::kSoft - 2);
         else if constexpr (C::kCodes) widen_units<D>(p, sh, raws, ring);
         else check_units<D>(p, sh, ring);
         ptx::cp_async_wait_all();
