@@ -61,10 +61,12 @@ struct Cfg {
     static_assert(!kDeal || kSoft * 32 * kMoreRegs + (kThreads - kSoft * 32) * kFewRegs <= kThreads * (65536 / kThreads / 8 * 8),
                   "more registers than the launch has would be waited for without end");
     static constexpr int kLoadWarps = kThreads / 32 - kSoft - 2;
-    // warps that issue copies: keys and values each by one, as small pages make for many
-    // boxes and a warp issues them one by one (pages of 16, heads of 256: 171 us by one
-    // warp); of codes there are half as many, and widening needs the warps
-    static constexpr int kCopyWarps = kCodes ? 1 : 2;
+    // warps that issue copies: small pages make for many boxes, and a warp issues them one
+    // by one (1024 tokens over 6000 keys, heads of 256, pages of 16: 171 us by one warp, 119
+    // by two, 99 by four; 4096 over 16384 of 128: 1002, 713 and 736); of codes there are
+    // half as many, and widening needs the warps
+    static constexpr int kCopyWarps = kCodes ? 1 : D == 256 ? 4 : 2;
+    static constexpr int kShare = kCopyWarps == 4 ? 2 : 1;  // of them, a tile
     static constexpr int kOthers = (kLoadWarps - kCopyWarps) * 32;  // threads that check or widen
     static constexpr int kTileBytes = kKeys * D * 2;
     static constexpr int kStages = kCodes ? 3 : 4;
@@ -188,11 +190,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t* r) {
 
 // Waits for a phase, with a limit; false when it ran out here or anywhere in the
 // block.  (Inline: a call would have to keep a row's scores over it.)
+// EASY: probes now and then, as what it waits for is far ahead of its use, and probes
+// take issue slots from the softmax.
+template <bool EASY = false>
 __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity, const AttnParams& p) {
     if (ptx::mbar_test(bar, parity)) return true;
     const long long began = clock64();
 #pragma unroll 1
     while (!ptx::mbar_test(bar, parity)) {
+        if (EASY) __nanosleep(100);
         if (*reinterpret_cast<volatile int*>(&sh.dead)) return false;
         if (clock64() - began > p.timeout_cycles) {
             record_error(p.err, FP8BS_ERR_TIMEOUT);
@@ -248,7 +254,7 @@ struct Place : Cursor {
 
     __device__ __forceinline__ bool enter(const AttnParams& p, Shared& sh, int k) {
         item = k;
-        if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.known[k & (kItems - 1)], (k / kItems) & 1, p))) return false;
+        if (!__all_sync(0xFFFFFFFFu, wait<true>(sh, &sh.known[k & (kItems - 1)], (k / kItems) & 1, p))) return false;
         *static_cast<Cursor*>(this) = sh.items[k & (kItems - 1)];
         return true;
     }
@@ -301,16 +307,18 @@ __device__ __forceinline__ uint32_t odd_pair(uint32_t w) { return ((w & 0x7F807F
 // those of four keys), and the other loader warps widen them.
 template <int D, int KIND>
 __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint8_t* ring, const CUtensorMap* mk,
-                                           const CUtensorMap* mv, int kv0, int kv1) {  // keys: 0, values: 1
+                                           const CUtensorMap* mv, int kv0, int kv1, int which) {  // keys: 0, values: 1
     using C = Cfg<D, KIND>;
     constexpr int kParts = C::kCodes ? 1 : D / 64, kWide = C::kCodes ? D : 64;  // boxes over a row, and their width
-    constexpr int kMost = C::kKeys * kParts / 32;  // boxes of a lane
+    constexpr int kMost = C::kKeys * kParts / (32 * C::kShare);  // boxes of a lane
     constexpr int kRing = C::kCodes ? C::kRaw : C::kStages, kBoxRow = C::kCodes ? D : 128;
     const int lane = threadIdx.x & 31;
     const int rows = min(1 << p.page_log2, C::kKeys), boxes = C::kKeys / rows * kParts;
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     Place at;
-    if (kv0 == 0) {
+    const bool publishes = kv0 == 0 && which == 0;
+    auto box = [&](int i) { return (lane + 32 * i) * C::kShare + which; };  // a lane's boxes
+    if (publishes) {
         publish<C::kTile, C::kKeys>(p, sh, 0);
         publish<C::kTile, C::kKeys>(p, sh, 1);
     }
@@ -324,10 +332,10 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
     auto find = [&] {
 #pragma unroll
         for (int i = 0; i < kMost; ++i) {
-            if (32 * i >= boxes) break;
-            const int j = (at.lo + at.unit) * C::kKeys + (lane + 32 * i) / kParts * rows;
+            if (32 * i * C::kShare >= boxes) break;
+            const int j = (at.lo + at.unit) * C::kKeys + box(i) / kParts * rows;
             // (a box may begin before the first key and end past the last)
-            page[i] = lane + 32 * i < boxes && j + rows > at.first ? page_of(max(j, at.first)) : -1;
+            page[i] = box(i) < boxes && j + rows > at.first ? page_of(max(j, at.first)) : -1;
         }
     };
     uint32_t zk[C::kKeys / 32], zv[C::kKeys / 32];
@@ -369,7 +377,7 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
         int now[kMost], count = 0;
 #pragma unroll
         for (int i = 0; i < kMost; ++i) {
-            if (32 * i >= boxes) break;
+            if (32 * i * C::kShare >= boxes) break;
             now[i] = page[i], count += __popc(__ballot_sync(0xFFFFFFFFu, page[i] >= 0));
         }
         if (C::kCodes) keep_scales(u);
@@ -378,14 +386,14 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
             alive &= at.next(p, sh);
             if (alive) find();
             if (alive && C::kCodes) read_scales();
-            if (at.item != item && kv0 == 0) publish<C::kTile, C::kKeys>(p, sh, at.item + 1);
+            if (at.item != item && publishes) publish<C::kTile, C::kKeys>(p, sh, at.item + 1);
         }
 #pragma unroll 1
         for (int kv = kv0; kv <= kv1; ++kv) {
             fill = 2 * static_cast<uint32_t>(u) + kv;
             const uint32_t stage = fill % kRing;
             if (alive && fill >= kRing)
-                alive = __all_sync(0xFFFFFFFFu, wait(sh, C::kCodes ? &sh.widened[stage] : &sh.empty[stage], ((fill / kRing) - 1) & 1, p));
+                alive = __all_sync(0xFFFFFFFFu, wait<!C::kCodes>(sh, C::kCodes ? &sh.widened[stage] : &sh.empty[stage], ((fill / kRing) - 1) & 1, p));
             if (!alive) break;
             uint64_t* bar = C::kCodes ? &sh.coded[stage] : kv && check ? &sh.raw[stage >> 1] : &sh.full[stage];
             if (lane == 0) ptx::mbar_arrive_expect_tx(bar, count * rows * kBoxRow);
@@ -393,9 +401,9 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
             uint8_t* tile = ring + stage * (C::kCodes ? C::kRawBytes : C::kTileBytes);
 #pragma unroll
             for (int i = 0; i < kMost; ++i) {
-                if (32 * i >= boxes) break;
+                if (32 * i * C::kShare >= boxes) break;
                 if (now[i] >= 0) {
-                    const int q = lane + 32 * i, part = q % kParts, r = q / kParts * rows;
+                    const int q = box(i), part = q % kParts, r = q / kParts * rows;
                     tma_box(tile + part * (C::kKeys * 128) + r * kBoxRow, kv ? mv : mk, kWide * part,
                             (j0 + r) & ((1 << p.page_log2) - 1), head, now[i], bar);
                 }
@@ -425,7 +433,7 @@ __device__ __forceinline__ void check_units(const AttnParams& p, Shared& sh, uin
         const int j0 = (at.lo + at.unit) * C::kKeys;
         if (!attn_sees_all<C::kKeys>(p, at)) {
             const uint32_t stage = (2 * static_cast<uint32_t>(u) + 1) % C::kStages;
-            alive = __all_sync(0xFFFFFFFFu, wait(sh, &sh.raw[stage >> 1], checked[stage >> 1] & 1, p));
+            alive = __all_sync(0xFFFFFFFFu, wait<true>(sh, &sh.raw[stage >> 1], checked[stage >> 1] & 1, p));
             ++checked[stage >> 1];
             if (alive) {
                 uint8_t* tile = ring + stage * C::kTileBytes;
@@ -452,7 +460,7 @@ __device__ __forceinline__ void check_units(const AttnParams& p, Shared& sh, uin
                     __threadfence_block();
                     if ((atomicAdd(&sh.looked[stage >> 1], 1) + 1) % (kThreads / 32) == 0) {
                         __threadfence_block();
-                        ptx::mbar_arrive(&sh.full[stage]);
+                        for (int i = 0; i < C::kShare; ++i) ptx::mbar_arrive(&sh.full[stage]);
                     }
                 }
             }
@@ -940,10 +948,10 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
     uint8_t* raws = ring + C::kStages * C::kTileBytes;
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) ptx::mbar_init(&sh.full[i], C::kCodes ? C::kOthers / 32 : 1), ptx::mbar_init(&sh.empty[i], 1);
+        for (int i = 0; i < C::kStages; ++i) ptx::mbar_init(&sh.full[i], C::kCodes ? C::kOthers / 32 : C::kShare), ptx::mbar_init(&sh.empty[i], 1);
         for (int i = 0; i < C::kRaw; ++i) ptx::mbar_init(&sh.coded[i], 1), ptx::mbar_init(&sh.widened[i], C::kOthers / 32);
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&sh.raw[i], 1);
+            ptx::mbar_init(&sh.raw[i], C::kShare);
             ptx::mbar_init(&sh.scores[i], 1);
             ptx::mbar_init(&sh.weights[i], 128);
             ptx::mbar_init(&sh.joined[i], 1);
@@ -975,7 +983,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
         else if (warp == C::kSoft) issue_products<D, KIND>(p, sh, ptx::smem_addr(query), ptx::smem_addr(ring));
         else if (warp == C::kSoft + 1) watch<D, KIND>(p, sh);
         else if (warp < C::kSoft + 2 + C::kCopyWarps)
-            copy_units<D, KIND>(p, sh, C::kCodes ? raws : ring, &mk, &mv, warp - C::kSoft - 2, C::kCopyWarps == 1 ? 1 : warp - C::kSoft - 2);
+            copy_units<D, KIND>(p, sh, C::kCodes ? raws : ring, &mk, &mv, (warp - C::kSoft - 2) / C::kShare,
+                                C::kCopyWarps == 1 ? 1 : (warp - C::kSoft - 2) / C::kShare, (warp - C::kSoft - 2) % C::kShare);
         else if constexpr (C::kCodes) widen_units<D>(p, sh, raws, ring);
         else check_units<D>(p, sh, ring);
         ptx::cp_async_wait_all();
