@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kJoin) attn_join_kernel(const __grid_constant_
     if (rec.rows == 0) return;
     const int first = blockIdx.x, n = rec.last - first + 1;
     int ways = 1;
-    while (ways < 8 && 2 * ways < n && ways * rec.rows < 2 * kLanes) ways *= 2;
+    while (ways < 8 && 2 * ways < n && 2 * ways * rec.rows <= kLanes * static_cast<int>(gridDim.y)) ways *= 2;
     const int col = threadIdx.x % kPer * 8, lane = threadIdx.x / kPer;
     const int way = lane % ways, per = (n + ways - 1) / ways, rows = kLanes / ways;
     for (int row0 = blockIdx.y * rows; row0 < rec.rows; row0 += gridDim.y * rows) {
