@@ -53,7 +53,7 @@ struct Cfg {
     static constexpr int kSoft = kStreams * 4;         // softmax warps, a thread a row (two
     // threads a row, each of half the keys, took 830 us where this takes 720: the softmax
     // of the two streams together is bound by its instructions, not by one's latency)
-    static constexpr int kThreads = kStreams == 2 ? 512 : 384;
+    static constexpr int kThreads = kStreams == 2 || kCodes ? 512 : 384;
     // Registers of a softmax thread and of the others, where the launch's are dealt out
     // anew: 256 (184 + 72) of 512 * 128.
     static constexpr bool kDeal = kStreams == 2;
@@ -393,7 +393,7 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
             fill = 2 * static_cast<uint32_t>(u) + kv;
             const uint32_t stage = fill % kRing;
             if (alive && fill >= kRing)
-                alive = __all_sync(0xFFFFFFFFu, wait<!C::kCodes>(sh, C::kCodes ? &sh.widened[stage] : &sh.empty[stage], ((fill / kRing) - 1) & 1, p));
+                alive = __all_sync(0xFFFFFFFFu, wait<true>(sh, C::kCodes ? &sh.widened[stage] : &sh.empty[stage], ((fill / kRing) - 1) & 1, p));
             if (!alive) break;
             uint64_t* bar = C::kCodes ? &sh.coded[stage] : kv && check ? &sh.raw[stage >> 1] : &sh.full[stage];
             if (lane == 0) ptx::mbar_arrive_expect_tx(bar, count * rows * kBoxRow);
@@ -474,7 +474,7 @@ template <int D>
 __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, const uint8_t* raw, uint8_t* ring) {
     using C = Cfg<D, FP8BS_KV_E4M3>;
     constexpr int kThreads = C::kOthers, kPer = D / 16;  // 16-byte pieces of a row
-    constexpr int kStep = kThreads / kPer, kBatch = 4;          // rows between a thread's pieces
+    constexpr int kStep = kThreads / kPer;                      // rows between a thread's pieces
     const int tid = threadIdx.x - (C::kThreads - kThreads), piece = tid % kPer;
     const int first = tid < kStep * kPer ? tid / kPer : C::kKeys;
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
@@ -495,35 +495,26 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, con
             const uint32_t largest = sh.largest[u & 3][kv];
             uint8_t* tile = ring + to * C::kTileBytes;
             const uint8_t* source = raw + from * C::kRawBytes + 16 * piece;
+            // a piece at a time: two at once 1106 us, four 1130 (one 1010), as the softmax
+            // waits for the same issue slots
 #pragma unroll 1
-            for (int r0 = first; r0 < C::kKeys; r0 += kBatch * kStep) {
-                uint4 codes[kBatch];
-                uint32_t scale[kBatch];
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int r = min(r0 + i * kStep, C::kKeys - 1);
-                    codes[i] = *reinterpret_cast<const uint4*>(source + r * D);
-                    scale[i] = sh.row_scale[u & 3][kv][r];
-                }
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int r = r0 + i * kStep;
-                    if (r >= C::kKeys) break;
-                    if (kv && masks) {
-                        const bool key = j0 + r >= at.first && j0 + r < at.past;
-                        if (!key || scale[i] == 255u) {  // see the head of this file
-                            if (key) sh.mark[at.item & (kMarks - 1)] = at.item + 1;
-                            scale[i] = largest;
-                            codes[i] = make_uint4(0, 0, 0, 0);
-                        }
+            for (int r = first; r < C::kKeys; r += kStep) {
+                uint4 codes = *reinterpret_cast<const uint4*>(source + r * D);
+                uint32_t scale = sh.row_scale[u & 3][kv][r];
+                if (kv && masks) {
+                    const bool key = j0 + r >= at.first && j0 + r < at.past;
+                    if (!key || scale == 255u) {  // see the head of this file
+                        if (key) sh.mark[at.item & (kMarks - 1)] = at.item + 1;
+                        scale = largest;
+                        codes = make_uint4(0, 0, 0, 0);
                     }
-                    uint4 lo, hi;
-                    widen(codes[i], scale[i], largest, lo, hi);
-                    uint8_t* line = tile + (piece >> 2) * (C::kKeys * 128) + r * 128;
-                    const int c = 2 * (piece & 3);
-                    *reinterpret_cast<uint4*>(line + ((c ^ (r & 7)) << 4)) = lo;
-                    *reinterpret_cast<uint4*>(line + ((c + 1 ^ (r & 7)) << 4)) = hi;
                 }
+                uint4 lo, hi;
+                widen(codes, scale, largest, lo, hi);
+                uint8_t* line = tile + (piece >> 2) * (C::kKeys * 128) + r * 128;
+                const int c = 2 * (piece & 3);
+                *reinterpret_cast<uint4*>(line + ((c ^ (r & 7)) << 4)) = lo;
+                *reinterpret_cast<uint4*>(line + ((c + 1 ^ (r & 7)) << 4)) = hi;
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
