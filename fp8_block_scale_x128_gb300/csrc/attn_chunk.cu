@@ -530,15 +530,17 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, con
 // The order of the products, in steps: the watcher waits for what a step needs and
 // lets the issuer go through a hardware barrier, as a probe of a barrier in shared
 // memory from the warp that issues would wait behind the products' own reads.  A step's
-// barrier comes round after four steps; the watcher is never further ahead, as it
+// barrier comes round after eight steps; the watcher is never that far ahead, as it
 // waits for what follows from the issuer's steps.
 //   two streams: (first scores of both), then for each unit and stream
-//     [weights, values there; the next unit's keys, the next item's queries]
-//     O += P V, next S = Q K^T
+//     [weights, values there; the next unit's keys]  O += P V, next S = Q K^T
 //   one stream: (first scores), then for each unit
-//     [the next unit's keys, the next item's queries]  next S = Q K^T in the other buffer
-//     [weights, values there]                          O += P V
-constexpr uint32_t kStepBarrier = 2, kStepBarriers = 4;
+//     [the next unit's keys]   next S = Q K^T in the other buffer
+//     [weights, values there]  O += P V
+// After an item's last unit the next S has a step of its own, the last, in which the
+// next item's queries are waited for.  (Weights handed over in halves of a unit's keys,
+// to begin the product earlier, took 757 us where this takes 697.)
+constexpr uint32_t kStepBarrier = 2, kStepBarriers = 8;
 
 template <int D, int KIND>
 __device__ __forceinline__ void watch(const AttnParams& p, Shared& sh) {
@@ -566,21 +568,28 @@ __device__ __forceinline__ void watch(const AttnParams& p, Shared& sh) {
         if (C::kStreams == 2) {
             full(fv);
             if (more) full(fk);
-            if (more && last) need(&sh.query[0], items & 1);
-            need(&sh.weights[0], u & 1);
-            go();
-            if (more && last) need(&sh.query[1], items & 1);
-            need(&sh.weights[1], u & 1);
-            go();
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                need(&sh.weights[s], u & 1);
+                go();
+                if (more && last) {
+                    need(&sh.query[s], items & 1);
+                    go();
+                }
+            }
         } else {
-            if (more) {
+            if (more && !last) {
                 full(fk);
-                if (last) need(&sh.query[0], items & 1);
                 go();
             }
             full(fv);
             need(&sh.weights[u & 1], (u >> 1) & 1);
             go();
+            if (more && last) {
+                full(fk);
+                need(&sh.query[0], items & 1);
+                go();
+            }
         }
     }
 }
@@ -622,32 +631,39 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, 
         const uint32_t fv = 2 * static_cast<uint32_t>(u) + 1, fk = fv + 1;
         const bool more = u + 1 < units, last = unit + 1 == n;
         const int rows_now = rows;
-        come();
-        if (more && last) {
+        auto go_on = [&] {  // to the next item, once the watcher has seen that it is known
             ++item;
             n = sh.items[item & (kItems - 1)].n, rows = sh.items[item & (kItems - 1)].rows;
-        }
+        };
         unit = last ? 0 : unit + 1;
         if constexpr (C::kStreams == 2) {
 #pragma unroll 1
             for (int s = 0; s < 2; ++s) {
-                if (s == 1) come();
+                come();
                 values(s, s, tile(fv), rows_now, first);
                 if (s == 1) ptx::mma_commit_warp(&sh.empty[fv % C::kStages]);
                 if (more) {
+                    if (last) {
+                        come();
+                        if (s == 0) go_on();
+                    }
                     scores(s, s, tile(fk), rows);
                     if (s == 1) ptx::mma_commit_warp(&sh.empty[fk % C::kStages]);
                 }
             }
         } else {
             const int b = u & 1;
-            if (more) {
+            auto next = [&] {
+                come();
+                if (last) go_on();
                 scores(0, b ^ 1, tile(fk), rows);
                 ptx::mma_commit_warp(&sh.empty[fk % C::kStages]);
-                come();
-            }
+            };
+            if (more && !last) next();
+            come();
             values(0, b, tile(fv), rows_now, first);
             ptx::mma_commit_warp(&sh.empty[fv % C::kStages]);
+            if (more && last) next();
         }
         first = last;
     }
