@@ -8,8 +8,7 @@
 //            a line, so keys are a K-major operand and values an MN-major one of the
 //            same layout); codes become fp16 on the way;
 //   one warp issues the products: scores S = Q K^T into tensor memory, then, once
-//            the weights are there, O += P V with P as the operand in tensor memory
-//            in the place of its scores;
+//            the weights are there, O += P V with P as the operand in tensor memory;
 //   a warpgroup a stream takes its rows' softmax, a thread a row: no shuffles.
 // Two streams (heads up to 128) take turns on the tensor core: while one's weights
 // are computed, the other's products run.  One stream (heads of 256) has two score
@@ -75,7 +74,16 @@ struct Cfg {
     static constexpr int kQBytes = kTile * D * 2;
     static constexpr int kOutBytes = 1024;  // of a softmax warp: outputs on their way
     static constexpr int kSmem = kQBytes + kStages * kTileBytes + kRaw * kRawBytes + kSoft * kOutBytes + 1024;
-    static constexpr uint32_t kOut = 256;  // first column of the outputs
+    // Columns of tensor memory: scores from 0 (a buffer's 128), outputs from 256.  The
+    // weights stand beside the scores; with heads of 128, which leave no room, in their
+    // place: the next scores are then issued behind the product that reads the weights, and
+    // the tensor core takes one thread's products, which are all of one shape there, in
+    // the order of their issue.  (To wait for that product first takes 810 us where this
+    // takes 725, at 4096 tokens over 16384 keys.)
+    static constexpr uint32_t kOut = 256;
+    __device__ static constexpr uint32_t weights_of(uint32_t buffer) {
+        return D == 128 ? buffer * 128 : D == 64 ? 384 + buffer * 64 : buffer * 128 + 64;
+    }
 };
 
 struct Shared {
@@ -83,6 +91,9 @@ struct Shared {
     Cursor items[kItems];
     uint64_t known[kItems];  // that an item stands there
     long long next_start;    // units before the next item
+    // scores, weights and joined (outputs): of a score buffer.  A phase's parity is that of
+    // the one before last, too, so a barrier is waited for only where the phase before is
+    // known to be over: a buffer's scores are issued after the product of its last weights.
     uint64_t full[4], raw[2], empty[4], scores[2], weights[2], joined[2], query[2], drained;
     uint64_t coded[3], widened[3];  // of the tiles of codes: they are there, they are free
     uint8_t row_scale[4][2][128];   // of a unit's keys and values
@@ -614,9 +625,9 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, 
     };
     auto values = [&](int stream, int buffer, uint32_t vals, int rows, bool first) {
         if (rows > stream * kRows)
-            mma_values<C::kKeys / 16>(tmem + C::kOut + stream * D, tmem + buffer * 128, desc_mn(vals, C::kKeys * 128), kValueDesc,
+            mma_values<C::kKeys / 16>(tmem + C::kOut + stream * D, tmem + C::weights_of(buffer), desc_mn(vals, C::kKeys * 128), kValueDesc,
                                       !first);
-        ptx::mma_commit_warp(&sh.joined[stream]);
+        ptx::mma_commit_warp(&sh.joined[buffer]);
     };
 
     come();
@@ -796,7 +807,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
     for (int u = 0; u < units; ++u) {
         const int buffer = C::kStreams == 2 ? stream : static_cast<int>(u & 1);
         const uint32_t parity = C::kStreams == 2 ? u & 1 : (u >> 1) & 1;
-        const uint32_t scores = sh.tmem + buffer * 128 + lanes;
+        const uint32_t scores = sh.tmem + buffer * 128 + lanes, weights = sh.tmem + C::weights_of(buffer) + lanes;
         const bool active = at.rows > stream * kRows;
         const int j0 = (at.lo + at.unit) * C::kKeys;
         const bool last = at.unit + 1 == at.n, done = last || u + 1 == units;
@@ -832,7 +843,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
                 sum *= shrink;
                 if (!first) {
                     // the products before this one are in the outputs
-                    if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.joined[stream], (u - 1) & 1, p))) return;
+                    if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.joined[C::kStreams == 2 ? stream : buffer ^ 1], (C::kStreams == 2 ? u - 1 : (u - 1) >> 1) & 1, p))) return;
                     ptx::tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
@@ -860,7 +871,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
                     if (C::kCodes) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(b), "f"(a));
                     else w[i] = pack_bf16(a, b);
                 }
-                tmem_st16(scores + 16 * c, w);
+                tmem_st16(weights + 16 * c, w);
             }
             const float2 both = halves(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
             sum += C::kCodes ? (both.x + both.y) * ex2(-scale.y) : both.x + both.y;
@@ -882,7 +893,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
             fetch_query();
         }
         if (u + 1 < units) query_ready();
-        if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.joined[stream], u & 1, p))) return;
+        if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.joined[buffer], parity, p))) return;
         ptx::tc_fence_after();
         if (active) {
             const bool whole = last && begun, there = stream * kRows + row < was.rows;

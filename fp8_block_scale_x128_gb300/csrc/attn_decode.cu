@@ -50,9 +50,11 @@ struct Cfg {
     static constexpr int kScaleBytes = kCodes ? kWarps * kStages * 2 * kSlice * 4 : 0;
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kSmem = kRing + kRedBytes + kScaleBytes;
-    // of an SM: as many as its shared memory holds (Shared and 1 KB beside), up to four
-    static constexpr int kFit = 228 * 1024 / (kSmem + 7 * 1024);
-    static constexpr int kBlocks = kFit > 4 ? 4 : kFit;
+    // of an SM: as many as its shared memory holds (Shared and 1 KB beside).  Of codes four
+    // at most: three take 98 us at 48 sequences of up to 8192, two 115; of bf16 two, whose
+    // longer shares fill the memory's pages: one token over 131072 keys 87 us, by three 92
+    static constexpr int kFit = 228 * 1024 / (kSmem + 7 * 1024), kMost = kCodes ? 4 : 2;
+    static constexpr int kBlocks = kFit > kMost ? kMost : kFit;
 };
 
 struct Shared {

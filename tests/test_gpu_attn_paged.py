@@ -175,6 +175,20 @@ def test_many_sequences_and_long_ones(dev, codes):
     check(lengths, q, tensors, table, fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens))
 
 
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_long_chunks_are_right_and_the_same_every_time(dev, D, codes):
+    """Many units an item, items that several blocks share, few rows and many."""
+    for lengths in ([(4, 3001), (9, 5000), (3, 64)], [(130, 2777), (60, 1500)]):
+        q, tensors, table, cu, lens = make(lengths, 16, 2, D, codes, 16, "slots", dev, seed=D + codes)
+        cache, ws = fb.KvCache(*tensors), fb.new_attn_workspace(D)
+        o = fb.fp8bs_attn_paged(q, cache, table, cu, lens, workspace=ws)
+        check(lengths, q, tensors, table, o)
+        for _ in range(20):
+            assert torch.equal(o, fb.fp8bs_attn_paged(q, cache, table, cu, lens, workspace=ws))
+        assert fb.fp8bs_check_error(ws) == 0
+
+
 def test_cache_past_32_bit_offsets(dev):
     page, Hk, D = 64, 8, 128
     pages = (1 << 31) // (page * Hk * D) + 9
