@@ -578,7 +578,7 @@ int fp8bs_attn_paged(const uint16_t* q, int64_t ldq, int64_t hsq, int64_t T, int
     a.g_shift += 31;
     a.g_mul = static_cast<uint32_t>(((uint64_t(1) << a.g_shift) + a.G - 1) / a.G);
     a.scale_log2 = scale * 1.44269504088896340736f;
-    a.window = static_cast<int>(window < (1 << 30) ? window : (1 << 30));
+    a.window = static_cast<int>(window < kAttnMaxKeys ? window : 0);
     a.o = o, a.ldo = ldo, a.hso = hso;
     a.err = static_cast<uint32_t*>(workspace);
     a.ws = static_cast<uint8_t*>(workspace) + kWsErrorBytes;

@@ -45,6 +45,7 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream);
 // ---------------------------------------------------------------------------
 
 constexpr int kAttnMaxSeqs = FP8BS_ATTN_MAX_SEQS;
+constexpr int kAttnMaxKeys = 1 << 30;  // of a sequence
 
 struct AttnParams {
     const uint16_t* q;
@@ -100,7 +101,7 @@ struct SeqInfo {
 __device__ __forceinline__ SeqInfo attn_seq(const AttnParams& p, int b) {
     const int c0 = p.cu[b], c1 = p.cu[b + 1], kv = p.len[b];
     // lengths that do not fit the tensors are cut to them
-    const int most = static_cast<int>(min(static_cast<int64_t>(p.table_cols) << p.page_log2, int64_t(0x7FFFFF00)));
+    const int most = static_cast<int>(min(static_cast<int64_t>(p.table_cols) << p.page_log2, int64_t(kAttnMaxKeys)));
     SeqInfo s;
     s.q0 = min(max(c0, 0), p.T);
     s.nq = max(min(max(c1, 0), p.T) - s.q0, 0);
@@ -335,12 +336,6 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-
-// Even and odd bytes of a word as two pairs of bf16 numbers, code values * 2^-120.
-__device__ __forceinline__ uint32_t codes_even(uint32_t w) {
-    return ((w << 8) & 0x80008000u) | ((w << 4) & 0x07F007F0u);
-}
-__device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return (w & 0x80008000u) | ((w >> 4) & 0x07F007F0u); }
 
 // Raises a kernel's dynamic shared memory limit to `bytes`, once per kernel and device.
 template <typename K>

@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
                 for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) qf[ks][n][i] = narrow(qf[ks][n][i]);
-                // 2^-up in two factors: up is in -114 .. 126
+                // (up is in -114 .. 126, so 2^-up is a normal number)
                 const float back = __int_as_float((127 - up) << 23) * p.scale_log2;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) unit[n][i] = __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t + i));

@@ -540,8 +540,8 @@ int fp8bs_rope_freqs(int rotary_dim, double theta, int scaling, double factor, d
  *   q_out, k_out : bf16 [T, heads, D] with strides of their own; may be q and k
  *                themselves with the same strides, else apart from them.
  * All pointers 16-byte aligned and all strides multiples of 8, where not said
- * otherwise; head strides below 2^31.  One launch, dependent on its predecessor (programmatic dependent
- * launch), for which it waits before it touches memory.
+ * otherwise; head strides below 2^31.  One launch, dependent on its predecessor
+ * (programmatic dependent launch), for which it waits before it touches memory.
  * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN, FP8BS_ERR_CUDA. */
 int fp8bs_qk_norm_rope(const uint16_t* q, int64_t ldq, int64_t hsq, const uint16_t* k, int64_t ldk, int64_t hsk,
                        int64_t T, int64_t Hq, int64_t Hk, int64_t D, const int64_t* positions,
@@ -619,7 +619,7 @@ size_t fp8bs_attn_paged_workspace_bytes(int64_t D, int sm_count);
  *   block_table : int32 [B, cols], row stride table_stride >= cols: the pages of each
  *                 sequence in order; entries past its length are not read.
  *   B           : sequences, 0 .. FP8BS_ATTN_MAX_SEQS (0 enqueues nothing).
- *   cu_q        : int32 [B + 1], ascending within 0 .. T.   kv_len : int32 [B].
+ *   cu_q        : int32 [B + 1], ascending within 0 .. T.   kv_len : int32 [B], 0 .. 2^30.
  *                 (All three 4-byte aligned; they are read on the device, so a
  *                 captured call follows their values.)
  *   scale       : > 0, up to 65536.   window : 0 (none) or the keys that a row sees at most.
@@ -631,9 +631,9 @@ size_t fp8bs_attn_paged_workspace_bytes(int64_t D, int sm_count);
  * outside the tensors is touched.  Masked keys and values have no part in a row,
  * whatever they hold; an infinity or a NaN that a row sees makes its results NaN or
  * infinite.  In a cache of codes q, keys and values are below 2^63 in magnitude, and
- * a value's scale below 2^-80 counts as 2^-80.  Results are deterministic, and a row's do not depend on whether other
- * heads or sequences hold NaNs.  Two launches, dependent on their predecessors,
- * for which they wait before they touch memory.
+ * a value's scale below 2^-80 counts as 2^-80.  Results are deterministic, and a row's
+ * do not depend on whether other heads or sequences hold NaNs.  Two launches, dependent
+ * on their predecessors, for which they wait before they touch memory.
  * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN, FP8BS_ERR_WORKSPACE,
  * FP8BS_ERR_CUDA. */
 int fp8bs_attn_paged(const uint16_t* q, int64_t ldq, int64_t hsq, int64_t T, int64_t Hq,

@@ -189,6 +189,72 @@ def test_long_chunks_are_right_and_the_same_every_time(dev, D, codes):
         assert fb.fp8bs_check_error(ws) == 0
 
 
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("page", [1, 2, 64, 256, 1024])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_rows_and_pages_of_all_sizes(dev, D, page, codes):
+    """Also sequences with more new tokens than keys, and with none of either."""
+    lengths = [(40, 300), (33, 33), (20, 7), (18, 0), (0, 12), (50, 1029), (1, 90)]
+    for window in (0, 37):
+        q, tensors, table, cu, lens = make(lengths, 12, 2, D, codes, page, "heads", dev, seed=page + D, behind=3)
+        o, ws = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device=dev), fb.new_attn_workspace(D)
+        fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens, window=window, o=o, workspace=ws)
+        assert fb.fp8bs_check_error(ws) == 0
+        check(lengths, q, tensors, table, o, window)
+        assert bool((o[-3:] == 5).all())
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_keys_and_values_side_by_side(dev, new):
+    """One tensor [pages, head, slot, 2, D] and one [heads, pages, slots, D]: other orders of the axes."""
+    lengths, D, page = [(new, 200), (new, 77)], 128, 16
+    q, tensors, table, cu, lens = make(lengths, 8, 4, D, False, page, "slots", dev, seed=11)
+    pages = tensors[0].shape[0]
+    both = torch.empty((pages, 4, page, 2, D), dtype=torch.bfloat16, device=dev)
+    for i in range(2):
+        both[:, :, :, i] = tensors[i].transpose(1, 2)
+    o = fb.fp8bs_attn_paged(q, fb.KvCache(*[both[:, :, :, i].transpose(1, 2) for i in range(2)]), table, cu, lens)
+    check(lengths, q, tensors, table, o)
+    apart = [t.permute(2, 0, 1, 3).contiguous().permute(1, 2, 0, 3) for t in tensors]
+    assert torch.equal(o, fb.fp8bs_attn_paged(q, fb.KvCache(*apart), table, cu, lens))
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("codes", [False, True])
+def test_the_longest_sequences(dev, new, codes):
+    """2^30 keys, of which a window sees a few; one more is too long."""
+    D, page, cols = 64, 65536, (1 << 14) + 1
+    q, tensors, _, cu, _ = make([(new, page)], 4, 1, D, codes, page, "slots", dev, seed=12, spare=0)
+    table, ws = torch.zeros((1, cols), dtype=torch.int32, device=dev), fb.new_attn_workspace(D)
+    cache = fb.KvCache(*tensors)
+
+    def at(kv):
+        o = fb.fp8bs_attn_paged(q, cache, table, cu, torch.tensor([kv], dtype=torch.int32, device=dev), window=300, workspace=ws)
+        return fb.fp8bs_check_error(ws), o
+
+    rc, o = at(1 << 30)
+    assert rc == 0
+    check([(new, page)], q, tensors, table[:, :1], o, 300)
+    assert at((1 << 30) + 1)[0] == fb.FP8BS_ERR_DEVICE
+
+
+def test_two_graphs_with_one_workspace(dev):
+    D, ws = 128, fb.new_attn_workspace(128)
+    calls = []
+    for lengths in ([(1, 5000), (1, 70)], [(300, 2000), (2, 9)]):
+        q, tensors, table, cu, lens = make(lengths, 8, 2, D, False, 16, "slots", dev, seed=len(calls))
+        cache, o = fb.KvCache(*tensors), torch.empty_like(q)
+        want = fb.fp8bs_attn_paged(q, cache, table, cu, lens)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            fb.fp8bs_attn_paged(q, cache, table, cu, lens, o=o, workspace=ws)
+        calls.append((graph, o, want, (cache, table, cu, lens, q)))
+    for i in (0, 1, 1, 0, 0, 1):
+        calls[i][1].zero_()
+        calls[i][0].replay()
+        assert torch.equal(calls[i][1], calls[i][2])
+
+
 def test_cache_past_32_bit_offsets(dev):
     page, Hk, D = 64, 8, 128
     pages = (1 << 31) // (page * Hk * D) + 9
