@@ -144,31 +144,38 @@ struct Cursor {
 
 struct PlanShared {
     int first[kAttnMaxSeqs + 1];  // tiles before each sequence
-    long long sum[32];
+    long long sums[2][32];        // of the warps
     AttnShare share;
 };
 
-// Inclusive sum over the block; *all: the block's.  Whole block.
-template <int THREADS>
-__device__ __noinline__ long long block_scan(long long v, PlanShared& sh, long long* all) {
+// Inclusive sum over the block; *all: the block's.  Whole block; calls in turn take
+// turns with the places of `sums`.
+template <int THREADS, typename N>
+__device__ __forceinline__ N block_scan(N v, long long* sums, N* all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll 1
+#pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const long long t = __shfl_up_sync(0xFFFFFFFFu, v, off);
+        const N t = __shfl_up_sync(0xFFFFFFFFu, v, off);
         if (lane >= off) v += t;
     }
+    N* of = reinterpret_cast<N*>(sums);
+    if (lane == 31) of[warp] = v;
     __syncthreads();
-    if (lane == 31) sh.sum[warp] = v;
-    __syncthreads();
-    long long before = 0, sum = 0;
+    N before = 0, sum = 0;
 #pragma unroll 4
     for (int w = 0; w < THREADS / 32; ++w) {
-        const long long t = sh.sum[w];
+        const N t = of[w];
         if (w < warp) before += t;
         sum += t;
     }
     *all = sum;
     return before + v;
+}
+
+// a / b, b > 0: a division of 64 bits takes some hundred instructions.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    if ((a | b) >> 32 == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
 }
 
 __device__ __forceinline__ int attn_tile_seq(const PlanShared& sh, int B, int tile) {
@@ -184,17 +191,17 @@ __device__ __forceinline__ int attn_tile_seq(const PlanShared& sh, int B, int ti
 // Whole block; leaves sh.first and sh.share.
 template <int MT, int BN, int THREADS>
 __device__ __noinline__ void attn_share(const AttnParams& p, PlanShared& sh) {
-    const int tid = threadIdx.x, block = blockIdx.x, grid = gridDim.x;
+    const int tid = threadIdx.x, block = blockIdx.x;
     if (tid == 0) sh.first[0] = 0;
-    int tiles = 0;
+    int tiles = 0, turn = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
         const int b = b0 + tid;
-        long long all;
+        int all;
         const int n = b < p.B ? (attn_seq(p, b).nq * p.G + MT - 1) / MT : 0;
-        const int upto = static_cast<int>(block_scan<THREADS>(n, sh, &all));
+        const int upto = block_scan<THREADS, int>(n, sh.sums[turn ^= 1], &all);
         if (b < p.B) sh.first[b + 1] = tiles + upto;
-        tiles += static_cast<int>(all);
+        tiles += all;
     }
     __syncthreads();
     // twice over the tiles: the sum of all units, then the tile that this block's first
@@ -214,7 +221,7 @@ __device__ __noinline__ void attn_share(const AttnParams& p, PlanShared& sh) {
                     const int r0 = (t - sh.first[b]) * MT;
                     n = attn_units<BN>(p, s, r0, min(r0 + MT, s.nq * p.G)).n;
                 }
-                upto = block_scan<THREADS>(n, sh, &all);
+                upto = block_scan<THREADS, long long>(n, sh.sums[turn ^= 1], &all);
             }
             if (pass == 0) {
                 total += all;
@@ -223,21 +230,19 @@ __device__ __noinline__ void attn_share(const AttnParams& p, PlanShared& sh) {
             const long long mine = (before + upto - n) * p.Hk;
             if (n > 0 && mine <= begin && begin < mine + static_cast<long long>(n) * p.Hk) {
                 sh.share.tile = t, sh.share.b = b;
-                sh.share.head = static_cast<int>((begin - mine) / n);
+                sh.share.head = static_cast<int>(divide(begin - mine, n));
                 sh.share.unit = static_cast<int>(begin - mine - static_cast<long long>(sh.share.head) * n);
             }
             before += all;
         }
         if (pass == 0) {
             total *= p.Hk;
-            const long long blocks = min(static_cast<long long>(grid), total);
-            begin = block < blocks ? block * total / blocks : 0;
-            if (tid == 0) {
-                sh.share.total = total;
-                sh.share.blocks = static_cast<int>(blocks);
-                sh.share.begin = begin;
-                sh.share.end = block < blocks ? (block + 1) * total / blocks : 0;
-            }
+            const int blocks = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+            // odd lanes: where the next block begins
+            const long long bound = block < blocks ? divide((block + (tid & 1)) * total, blocks) : 0;
+            begin = __shfl_sync(0xFFFFFFFFu, bound, 0);
+            if (tid == 0) sh.share.total = total, sh.share.blocks = blocks, sh.share.begin = begin;
+            if (tid == 1) sh.share.end = bound;
         }
     }
     __syncthreads();
@@ -271,7 +276,7 @@ __device__ __forceinline__ bool attn_sees_all(const AttnParams& p, const Cursor&
 
 // The block that finishes an item begun in unit `start` of all.
 static __device__ __noinline__ int attn_last_block(const AttnShare& a, long long start, int n) {
-    return static_cast<int>(((start + n) * a.blocks - 1) / a.total);
+    return static_cast<int>(divide((start + n) * a.blocks - 1, a.total));
 }
 
 // What a block leaves for the second launch about an item that it begins and

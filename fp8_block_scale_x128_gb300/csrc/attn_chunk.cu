@@ -99,6 +99,7 @@ struct Shared {
     uint8_t row_scale[4][2][128];   // of a unit's keys and values
     uint32_t largest[4][2];
     float2 scales[8];               // of a unit: 2^e of the keys, e of the values
+    float unscale[2][2 * kRows];    // codes: what a row's scores are multiplied by, of an item and the next
     uint32_t tmem;
     int dead;
     int looked[2];  // warps that have looked a tile through, of either stage
@@ -229,8 +230,8 @@ __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int d
         : "memory");
 }
 
-// The items of the block's share, one after the other: one loader warp finds out what
-// they are, an item ahead, and the other tasks read it.  (The code that does it is
+// The items of the block's share, one after the other: a copy warp, which comes to them
+// first, finds out what they are, and the other tasks read it.  (The code that does it is
 // long, and there is one copy of it: what the instruction cache does not hold costs
 // more than the look-up.)
 template <int ROWS, int UNIT>
@@ -329,10 +330,7 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
     Place at;
     const bool publishes = kv0 == 0 && which == 0;
     auto box = [&](int i) { return (lane + 32 * i) * C::kShare + which; };  // a lane's boxes
-    if (publishes) {
-        publish<C::kTile, C::kKeys>(p, sh, 0);
-        publish<C::kTile, C::kKeys>(p, sh, 1);
-    }
+    if (publishes) publish<C::kTile, C::kKeys>(p, sh, 0);
     bool alive = at.start(p, sh);
     uint32_t fill = 0;  // tiles of both kinds
     int page[kMost];
@@ -385,20 +383,13 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
     for (int u = 0; u < units && alive; ++u) {
         const int j0 = (at.lo + at.unit) * C::kKeys, head = at.head;
         const bool check = !C::kCodes && !attn_sees_all<C::kKeys>(p, at);
-        int now[kMost], count = 0;
+        int count = 0;
 #pragma unroll
         for (int i = 0; i < kMost; ++i) {
             if (32 * i * C::kShare >= boxes) break;
-            now[i] = page[i], count += __popc(__ballot_sync(0xFFFFFFFFu, page[i] >= 0));
+            count += __popc(__ballot_sync(0xFFFFFFFFu, page[i] >= 0));
         }
         if (C::kCodes) keep_scales(u);
-        if (u + 1 < units) {
-            const int item = at.item;
-            alive &= at.next(p, sh);
-            if (alive) find();
-            if (alive && C::kCodes) read_scales();
-            if (at.item != item && publishes) publish<C::kTile, C::kKeys>(p, sh, at.item + 1);
-        }
 #pragma unroll 1
         for (int kv = kv0; kv <= kv1; ++kv) {
             fill = 2 * static_cast<uint32_t>(u) + kv;
@@ -413,12 +404,18 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
 #pragma unroll
             for (int i = 0; i < kMost; ++i) {
                 if (32 * i * C::kShare >= boxes) break;
-                if (now[i] >= 0) {
+                if (page[i] >= 0) {
                     const int q = box(i), part = q % kParts, r = q / kParts * rows;
                     tma_box(tile + part * (C::kKeys * 128) + r * kBoxRow, kv ? mv : mk, kWide * part,
-                            (j0 + r) & ((1 << p.page_log2) - 1), head, now[i], bar);
+                            (j0 + r) & ((1 << p.page_log2) - 1), head, page[i], bar);
                 }
             }
+        }
+        if (u + 1 < units && alive) {  // the next unit's pages, while this one's tiles come
+            if (publishes && at.unit + 1 == at.n) publish<C::kTile, C::kKeys>(p, sh, at.item + 1);
+            alive = at.next(p, sh);
+            if (alive) find();
+            if (alive && C::kCodes) read_scales();
         }
     }
     if (!alive) {  // what is under way lands before the block leaves
@@ -741,64 +738,73 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     const uint32_t out = sh.tmem + C::kOut + stream * D + lanes;
-    const uint32_t mine = ptx::smem_addr(query) + stream * kRows * D * 2 + row * 128;  // this row of the queries
+    const uint32_t own = stream * kRows * D * 2;  // the stream's queries
     uint8_t* staged = way + warp * C::kOutBytes;
     Place at;
     if (!at.start(p, sh)) return;
 
-    // a thread copies its row
-    auto query_row = [&](int* token, int* head) {
-        // rows that are not there look like the last one and are not written
-        const int packed = at.row0 + min(stream * kRows + row, at.rows - 1);
+    auto query_row = [&](int r, int* token, int* head) {  // of the stream; past the last: the last
+        const int packed = at.row0 + min(stream * kRows + r, at.rows - 1);
         *token = div_g(p, packed);
         *head = at.head * p.G + packed - *token * p.G;
     };
+    // The queries: eight lanes a row, four rows of a warp at a time, in turns with the
+    // stream's other warps (few rows are then soon there: a thread a row took 8400 cycles
+    // to bring 32 rows of 256 into fp16).  Rows that are not there keep what lies there:
+    // no row's results depend on another's.
+    const int part = lane & 7;
+    auto piece = [&](int r, int i) { return own + r * 128 + i * (kRows * 128) + ((part ^ (r & 7)) << 4); };
     auto fetch_query = [&] {
-        int token, head;
-        query_row(&token, &head);
-        const bool there = stream * kRows + row < at.rows;
-        const uint16_t* src = p.q + static_cast<int64_t>(at.q0 + token) * p.ldq + head * p.hsq;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-            cp_async16_zfill(mine + (c >> 3) * (kRows * 128) + (((c & 7) ^ (row & 7)) << 4), src + 8 * c, there);
+#pragma unroll 1
+        for (int r0 = 4 * quarter; r0 < min(kRows, at.rows - stream * kRows); r0 += 16) {
+            const int r = r0 + (lane >> 3);
+            int token, head;
+            query_row(r, &token, &head);
+            const uint16_t* src = p.q + static_cast<int64_t>(at.q0 + token) * p.ldq + head * p.hsq + 8 * part;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) cp_async16(ptx::smem_addr(query) + piece(r, i), src + 64 * i);
         }
         cp_commit();
     };
-    float unscale = p.scale_log2;  // what a row's scores are multiplied by, beside their unit's scale
     auto query_ready = [&] {
         cp_wait<0>();
-        if (C::kCodes) {  // the row in fp16, in place
-            uint32_t largest = 0;
-            auto piece = [&](int c) { return reinterpret_cast<uint4*>(query + (mine - ptx::smem_addr(query)) + (c >> 3) * (kRows * 128) + (((c & 7) ^ (row & 7)) << 4)); };
+        if (C::kCodes) {  // the rows in fp16, in place
 #pragma unroll 1
-            for (int c = 0; c < D / 8; ++c) {
-                const uint4 v = *piece(c);
-                const uint32_t lo = max(max(v.x & 0x7FFFu, v.y & 0x7FFFu), max(v.z & 0x7FFFu, v.w & 0x7FFFu));
-                const uint32_t hi = max(max(v.x >> 16 & 0x7FFFu, v.y >> 16 & 0x7FFFu), max(v.z >> 16 & 0x7FFFu, v.w >> 16 & 0x7FFFu));
-                largest = max(largest, max(lo, hi));
-            }
-            // zeros, and rows with an infinity or a NaN, stay
-            const int e = static_cast<int>(largest >> 7), up = largest == 0 || e == 255 ? 0 : min(14 - (e - 127), 126);
-            const float factor = __int_as_float((up + 127) << 23);
-#pragma unroll 1
-            for (int c = 0; c < D / 8; ++c) {
-                uint4* v = piece(c);
-                float x[8];
-                unpack_bf16x8(*v, x);
-                uint32_t h[4];
+            for (int r0 = 4 * quarter; r0 < min(kRows, at.rows - stream * kRows); r0 += 16) {
+                const int r = r0 + (lane >> 3);
+                uint4 v[D / 64];
+                uint32_t largest = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[i]) : "f"(x[2 * i + 1] * factor), "f"(x[2 * i] * factor));
-                *v = make_uint4(h[0], h[1], h[2], h[3]);
+                for (int i = 0; i < D / 64; ++i) {
+                    v[i] = *reinterpret_cast<const uint4*>(query + piece(r, i));
+                    const uint32_t lo = max(max(v[i].x & 0x7FFFu, v[i].y & 0x7FFFu), max(v[i].z & 0x7FFFu, v[i].w & 0x7FFFu));
+                    const uint32_t hi = max(max(v[i].x >> 16 & 0x7FFFu, v[i].y >> 16 & 0x7FFFu), max(v[i].z >> 16 & 0x7FFFu, v[i].w >> 16 & 0x7FFFu));
+                    largest = max(largest, max(lo, hi));
+                }
+#pragma unroll
+                for (int off = 1; off < 8; off <<= 1) largest = max(largest, __shfl_xor_sync(0xFFFFFFFFu, largest, off));
+                // zeros, and rows with an infinity or a NaN, stay
+                const int e = static_cast<int>(largest >> 7), up = largest == 0 || e == 255 ? 0 : min(14 - (e - 127), 126);
+                const float factor = __int_as_float((up + 127) << 23);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    float x[8];
+                    unpack_bf16x8(v[i], x);
+                    uint32_t h[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[k]) : "f"(x[2 * k + 1] * factor), "f"(x[2 * k] * factor));
+                    *reinterpret_cast<uint4*>(query + piece(r, i)) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                if (part == 0) sh.unscale[at.item & 1][stream * kRows + r] = __int_as_float((127 - up) << 23) * p.scale_log2;
             }
-            unscale = __int_as_float((127 - up) << 23) * p.scale_log2;
         }
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(&sh.query[stream]);
     };
     fetch_query();
     query_ready();
-    float now = unscale;  // of the item whose scores come
+    float now = 0.0f;  // codes: what the row's scores are multiplied by, beside their unit's scale
     float most = -INFINITY, sum = 0.0f;
     bool first = true;
     bool begun = at.unit == 0;
@@ -814,9 +820,11 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
         if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.scores[buffer], parity, p))) return;
         ptx::tc_fence_after();
         if (active) {
+            // (the row's warps had it there before they let its scores begin)
+            if (C::kCodes && first) now = sh.unscale[at.item & 1][stream * kRows + row];
             if (!attn_sees_all<C::kKeys>(p, at)) {
                 int token, head;
-                query_row(&token, &head);
+                query_row(row, &token, &head);
                 const int hi = at.base + token - j0;
                 mask_scores<C::kKeys>(scores, hi, p.window ? hi - p.window + 1 : 0);
             }
@@ -887,7 +895,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
         // the item's last unit here: the next one's queries, then this one's rows
         const Place was = at;
         int token, head;
-        query_row(&token, &head);
+        query_row(row, &token, &head);
         if (u + 1 < units) {
             if (!at.enter(p, sh, at.item + 1)) return;
             fetch_query();
@@ -948,7 +956,6 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
         }
         ptx::tc_fence_before();
         most = -INFINITY, sum = 0.0f;
-        now = unscale;
         first = begun = true;
         from = 0;
     }
