@@ -711,13 +711,20 @@ size_t attn_workspace_bytes(int D, int sm_count) {
     return kWsErrorBytes + attn_records_bytes(4 * sm_count) + (few > many ? few : many) * sizeof(float);
 }
 
-// Rows of a sequence, on average, from which the tensor core's kernel takes the call.
-constexpr int64_t kChunkRows = 17;
+// Rows of a sequence, on average, from which the tensor core's kernel takes the call.  This
+// file's kernel reads a sequence's keys once for 16 rows (8 with heads of 256), the other
+// once for 256 (128), at a higher cost of each step.  At 64 sequences of up to 8192 keys
+// (4560 on average), us by this one against the other, with so many rows on average:
+//   heads of 128: 12 rows bf16 204 / 253, codes 281 / 388; 23 rows 366 / 257, 497 / 392
+//   heads of 256: 14 rows bf16 194 / 115, codes 103 / 142; codes 19 rows 137 / 142, 24 172 / 141
+static int64_t chunk_rows(const AttnArgs& a) {
+    return a.D < 256 ? 17 : a.kind == FP8BS_KV_BF16 ? 9 : 20;
+}
 
 cudaError_t launch_attn_paged(const AttnArgs& a, cudaStream_t stream) {
     // (boxes of one row of 64 codes would not begin on 128 bytes of shared memory)
     const bool boxes = a.kind == FP8BS_KV_BF16 || a.D > 64 || a.page_log2 > 0;
-    if (static_cast<int64_t>(a.T) * a.G >= kChunkRows * a.B && boxes) return launch_attn_chunk(a, stream);
+    if (static_cast<int64_t>(a.T) * a.G >= chunk_rows(a) * a.B && boxes) return launch_attn_chunk(a, stream);
     return launch_attn_decode(a, stream);
 }
 
