@@ -503,8 +503,8 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, con
             const uint32_t largest = sh.largest[u & 3][kv];
             uint8_t* tile = ring + to * C::kTileBytes;
             const uint8_t* source = raw + from * C::kRawBytes + 16 * piece;
-            // a piece at a time: two at once 1106 us, four 1130 (one 1010), as the softmax
-            // waits for the same issue slots
+            // a piece at a time: two at once 1106 us, four 1130 (one 1010 then), as the softmax
+            // waits for the same issue slots (nor do eight or ten warps help: 1050, five 997)
 #pragma unroll 1
             for (int r = first; r < C::kKeys; r += kStep) {
                 uint4 codes = *reinterpret_cast<const uint4*>(source + r * D);
@@ -828,16 +828,33 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
                 const int hi = at.base + token - j0;
                 mask_scores<C::kKeys>(scores, hi, p.window ? hi - p.window + 1 : 0);
             }
-            float s[C::kKeys];
+            // Codes: a loop over 32 scores, which are read again for their weights: the loaders'
+            // code is long, and all of it has to stay in the instruction cache (4096 tokens over
+            // 16384 keys 1065 us without, 997 so).  bf16: a row's scores in registers (681 us,
+            // read twice in a loop 746).
+            constexpr int kTimes = C::kCodes ? 1 : C::kKeys / 32;
+            float s[32 * kTimes];
+            if (!C::kCodes) {
 #pragma unroll
-            for (int i = 0; i < C::kKeys / 32; ++i) tmem_ld32(scores + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
-            ptx::tmem_wait_ld();
+                for (int i = 0; i < kTimes; ++i) tmem_ld32(scores + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
+                ptx::tmem_wait_ld();
+            }
+            auto some = [&](int c) {  // scores 32 c and on
+                if (!C::kCodes) return s + 32 * c % (32 * kTimes);
+                tmem_ld32(scores + 32 * c, reinterpret_cast<uint32_t*>(s));
+                ptx::tmem_wait_ld();
+                return s;
+            };
             // eight chains, so that none is long
             float tops[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) tops[i] = fmaxf(s[2 * i], s[2 * i + 1]);
+            for (int i = 0; i < 8; ++i) tops[i] = -INFINITY;
+#pragma unroll kTimes
+            for (int c = 0; c < C::kKeys / 32; ++c) {
+                const float* x = some(c);
 #pragma unroll
-            for (int i = 16; i < C::kKeys; i += 2) tops[(i >> 1) & 7] = fmaxf(tops[(i >> 1) & 7], fmaxf(s[i], s[i + 1]));
+                for (int i = 0; i < 32; i += 2) tops[(i >> 1) & 7] = fmaxf(tops[(i >> 1) & 7], fmaxf(x[i], x[i + 1]));
+            }
             const float2 scale = C::kCodes ? sh.scales[u & 7] : make_float2(1.0f, 0.0f);
             const float factor = C::kCodes ? now * scale.x : p.scale_log2;
             const float top = scale.y + factor * fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
@@ -868,12 +885,13 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
             const float base = (most == -INFINITY ? 0.0f : most) - scale.y - (C::kCodes ? 7.0f : 0.0f);
             const uint64_t factors = pair(factor, factor), minus = pair(-base, -base);
             uint64_t sums[4] = {0, 0, 0, 0};
-#pragma unroll
+#pragma unroll kTimes
             for (int c = 0; c < C::kKeys / 32; ++c) {
+                const float* y = some(c);
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 x = halves(fma2(pair(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), factors, minus));
+                    const float2 x = halves(fma2(pair(y[2 * i], y[2 * i + 1]), factors, minus));
                     const float a = ex2(x.x), b = ex2(x.y);
                     sums[i & 3] = add2(sums[i & 3], pair(a, b));
                     if (C::kCodes) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(b), "f"(a));
@@ -968,6 +986,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
     using C = Cfg<D, KIND>;
     extern __shared__ uint8_t raw[];
     __shared__ Shared sh;
+    static_assert(C::kSmem + sizeof(Shared) <= 227 * 1024, "more shared memory than a block has");
     uint8_t* query = raw + ((1024 - (ptx::smem_addr(raw) & 1023)) & 1023);
     uint8_t* ring = query + C::kQBytes;
     uint8_t* raws = ring + C::kStages * C::kTileBytes;
