@@ -3,7 +3,7 @@
 //
 // A tile is 256 rows (128 with heads of 256), in streams of 128 with their own
 // accumulators in tensor memory.  Warps have one task each:
-//   loaders  copy a unit's keys, then its values, into a ring of shared memory
+//   loaders  copy a unit's keys and its values into a ring of shared memory
 //            tiles in the operand layout (128-byte swizzle; a row's 64 dimensions are
 //            a line, so keys are a K-major operand and values an MN-major one of the
 //            same layout); codes become fp16 on the way;
@@ -29,6 +29,12 @@
 // A value that is not finite and that some row of its unit masks would reach that row
 // as zero times it.  In units with masks the loaders put zeros in the place of such
 // values and mark the item; its rows then add those that they see at their end.
+//
+// 4096 tokens over 16384 keys, 32 + 8 heads of 128, take 681 us (1.41 PFLOP/s, 0.77 of a
+// large matrix product's rate): 3320 cycles a unit, of which a stream's softmax 1800 and its
+// two products 1024 follow one another, beside the other stream's.  Over codes 997 us: the
+// widening shares the issue slots and the shared memory with the softmax.  An item's change
+// costs some 4000 cycles (outputs, next queries).
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -317,6 +323,8 @@ __device__ __forceinline__ uint32_t odd_pair(uint32_t w) { return ((w & 0x7F807F
 // zeros, as do values that are not finite.
 // Codes: boxes go to a ring of their own, with a unit's scales beside them (a lane reads
 // those of four keys), and the other loader warps widen them.
+// The next unit's pages are looked up behind a unit's boxes, in few instructions: two
+// units ahead 4096 tokens over 16384 keys take 857 us, before the boxes 771, so 681.
 template <int D, int KIND>
 __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint8_t* ring, const CUtensorMap* mk,
                                            const CUtensorMap* mv, int kv0, int kv1, int which) {  // keys: 0, values: 1
@@ -482,7 +490,7 @@ template <int D>
 __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, const uint8_t* raw, uint8_t* ring) {
     using C = Cfg<D, FP8BS_KV_E4M3>;
     constexpr int kThreads = C::kOthers, kPer = D / 16;  // 16-byte pieces of a row
-    constexpr int kStep = kThreads / kPer;                      // rows between a thread's pieces
+    constexpr int kStep = kThreads / kPer;               // rows between a thread's pieces
     const int tid = threadIdx.x - (C::kThreads - kThreads), piece = tid % kPer;
     const int first = tid < kStep * kPer ? tid / kPer : C::kKeys;
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);

@@ -13,6 +13,10 @@
 // rounded to fp32, go to sincospif.
 //
 // Everything is fp32 from the bf16 inputs to one rounding at the end.
+//
+// It reads and writes each head once.  8192 tokens of 32 + 8 heads of 128 take 38.5 us
+// (4.4 TB/s, 0.64 of a copy's rate; a block a token, without a ring of its own, 56),
+// 40 + 8 + 8 into a bf16 cache 47.5 (5.0 TB/s; 67).  One token takes 2.2 us in a graph.
 #include "attn.cuh"
 #include "w4.cuh"
 
