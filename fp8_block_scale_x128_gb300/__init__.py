@@ -726,7 +726,7 @@ def fp8bs_attn_paged(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor,
     ldq, hsq, q1 = q.stride()
     rows, one = block_table.stride()
     assert q.dtype is _BF16 and q1 == 1 and D == cache.head_dim
-    assert block_table.dtype is torch.int32 and (one == 1 or cols < 2)
+    assert block_table.dtype is torch.int32 and (one == 1 or cols < 2) and (rows >= cols or B < 2)
     assert cu_q.dtype is torch.int32 and cu_q.shape == (B + 1,) and cu_q.is_contiguous()
     assert kv_len.dtype is torch.int32 and kv_len.shape == (B,) and kv_len.is_contiguous()
     if o is None or workspace is None:

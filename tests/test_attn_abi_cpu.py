@@ -233,3 +233,16 @@ def test_caches_that_do_not_fit_together_are_refused(box):  # noqa: F811
             fb.KvCache(*bad)
     with pytest.raises(fb.Fp8bsError):
         fb.new_kv_cache(2, 16, 2, 128, 7, torch.device("cuda", 0))
+
+
+def test_a_table_whose_rows_overlap_is_refused(box, monkeypatch):  # noqa: F811
+    library, _ = box
+    a = given("fp8bs_attn_paged")
+    for strides in ((0, 1), (4, 1), (10, 2)):  # one row for all, rows into one another, every second entry
+        monkeypatch.setattr(a["block_table"], "stride", lambda s=strides: s, raising=False)
+        with pytest.raises(AssertionError):
+            fb.fp8bs_attn_paged(**a)
+    assert not library.calls
+    monkeypatch.setattr(a["block_table"], "stride", lambda: (9, 1), raising=False)
+    fb.fp8bs_attn_paged(**a)
+    assert library.calls[0][1][7] == 9 and library.calls[0][1][8] == 5
