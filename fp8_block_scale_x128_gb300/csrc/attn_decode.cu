@@ -118,6 +118,9 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
     return r;
 }
 
+// The upper bit of each byte of a word that is a code without a value.
+__device__ __forceinline__ uint32_t odd_codes(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u & 0x80808080u; }
+
 // 2^(b - 127), NaN for 255.
 __device__ __forceinline__ float scale_of(uint32_t b) {
     return b == 255u ? __uint_as_float(0x7FFFFFFFu) : e8m0_to_float(b);
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
                     }
                 }
             bool odd = false;  // a value that is not finite where some row masks its key
-            if (!C::kCodes && !all) {
+            if (!all) {
                 uint32_t acc = 0;
 #pragma unroll 1
                 for (int i = lane; i < SL * kChunks; i += 32) {
@@ -514,11 +517,41 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        acc |= ((w[c] & 0x7F80u) == 0x7F80u) | ((w[c] & 0x7F800000u) == 0x7F800000u);
+                        acc |= C::kCodes ? odd_codes(w[c]) : ((w[c] & 0x7F80u) == 0x7F80u) | ((w[c] & 0x7F800000u) == 0x7F800000u);
                 }
                 odd = __any_sync(0xFFFFFFFFu, acc != 0);
             }
-            if (!odd) {
+            if (C::kCodes && odd) {
+                // NaNs for the rows that see such a code, and a zero in its place.  (A scale of
+                // 255 is in the weights of the rows that see its key.)
+                uint8_t* rows = smem + (vs - ptx::smem_addr(smem));
+#pragma unroll 1
+                for (int key = 0; key < SL; ++key) {
+                    const int j = j0 + key;
+                    bool sees[NT][2];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) sees[n][i] = j <= place[n][i] && (!p.window || j > place[n][i] - p.window);
+#pragma unroll
+                    for (int o = 0; o < kSteps; ++o) {
+                        const uint32_t w = odd_codes(*reinterpret_cast<const uint16_t*>(rows + chunk_at<RB>(key, o) + 2 * g));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if ((w >> (8 * (i >> 1)) & 0x80u) && sees[n][i & 1]) out[o][n][i] = __uint_as_float(0x7FFFFFFFu);
+                    }
+                }
+                __syncwarp();
+#pragma unroll 1
+                for (int i = lane; i < SL * kChunks * 4; i += 32) {
+                    uint32_t* w = reinterpret_cast<uint32_t*>(rows) + i;
+                    *w &= ~((odd_codes(*w) >> 7) * 0xFFu);
+                }
+                __syncwarp();
+            }
+            if (C::kCodes || !odd) {
 #pragma unroll
                 for (int k = 0; k < KT; ++k)
 #pragma unroll

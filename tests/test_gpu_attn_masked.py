@@ -1,0 +1,132 @@
+"""Attention over a paged cache: what a row does not see has no part in it, whatever it holds.
+
+References are those of attn_reference.py, in 64 bits.  Bounds are a row's own: of the keys that it
+sees, and of nothing else.
+
+* A score's D products, its factors and the difference from the maximum, exp2, the sums: as in
+  attn_reference.py.
+* A weight's rounding: `weight` of itself, 2^-11 in fp16 (codes); 2^-8 in bf16, and 2^-16 where two
+  bf16 numbers stand for it.
+* Codes: q is off by 2^-39 of its largest magnitude.  A weight times its value's scale is a number of
+  fp16 of which 2^7 stands for the largest, or for up to 2^14 times that (the scales of a unit's
+  keys may differ by 2^14 before each has its own): below fp16's normal numbers it is off by
+  2^-25 2^-7 2^14 = 2^-18 of the largest, and multiplies the value's code.
+"""
+
+import math
+
+import pytest
+import torch
+
+import fp8_block_scale_x128_gb300 as fb
+from tests import attn_reference as A
+from tests.test_gpu_attn_paged import make
+
+pytestmark = pytest.mark.gpu
+
+STEP = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def dev():
+    fb.build()
+    return torch.device("cuda", 0)
+
+
+def attend(q, k, v, scale, window, weight, units=None):
+    """One sequence: q [n, Hq, D], k and v [kv, Hk, D] in 64 bits; `units`: the scales [kv, Hk] of
+    codes.  Returns o and its bound: row by row, from the keys that the row sees alone."""
+    q = q.double().cpu()
+    n, Hq, D = q.shape
+    kv, G = k.shape[0], Hq // k.shape[1]
+    o, bound = torch.zeros_like(q), torch.zeros_like(q)
+    for i in range(n):
+        place = kv - n + i
+        lo = max(place - window + 1, 0) if window else 0
+        if place < 0:
+            continue
+        for h in range(Hq):
+            kh, vh = k[lo:place + 1, h // G], v[lo:place + 1, h // G]
+            s, size = kh @ q[i, h] * scale, kh.abs() @ q[i, h].abs() * scale
+            most = s.max()
+            w = torch.exp(s - most)
+            total = w.sum()
+            fine = torch.isfinite(vh)
+            vs = torch.where(fine, vh, 0.0)
+            odd = torch.where(fine, 0.0, vh).sum(0)  # a value that is not finite reaches the rows that see it
+            o[i, h] = w @ vs / total + odd
+            off = 2.0 ** -23 * (D / 16 + 16) * size + 4 * STEP * (1.5 * (s.abs() + most.abs()) + 150) + 2.0 ** -21
+            least = 0.0
+            if units is not None:
+                off = off + scale * 2.0 ** -39 * q[i, h].abs().max() * kh.abs().sum(1)
+                unit = units[lo:place + 1, h // G]
+                least = 2.0 ** -18 * w.max() * unit.max() * (vs.abs() / unit.unsqueeze(1)).sum(0) / total
+            # (a score of next to no weight may be off by much)
+            off = torch.exp((s - most + off).clamp(max=30.0)) - w + w * (weight + 2 * STEP * (len(s) / 16 + 16))
+            off = torch.nan_to_num(off, nan=0.0)
+            bound[i, h] = off @ vs.abs() / total + off.sum() / total * (w @ vs.abs() / total) + least
+    return o, bound
+
+
+def check(lengths, q, tensors, table, o, window=0, scale=None, weight=2.0 ** -8):
+    codes = len(tensors) == 4
+    first, D, page = 0, q.shape[2], tensors[0].shape[1]
+    for b, (n, kv) in enumerate(lengths):
+        k, v = A.rows_of(tensors, table[b], kv)
+        units = None
+        if codes:
+            j = torch.arange(kv)
+            z = tensors[3].cpu()[table[b].cpu().long()[j // page], j % page]
+            units = 2.0 ** (torch.where(z == 255, 0, z).double() - 127)
+        ref, bound = attend(q[first:first + n], k, v, D ** -0.5 if scale is None else scale, window,
+                            2.0 ** -11 if codes else weight, units)
+        A.near(o[first:first + n], ref, bound)
+        first += n
+
+
+def at(tensors, table, b, j):
+    """The page and slot of a sequence's key j."""
+    page = tensors[0].shape[1]
+    return int(table[b, j // page]), j % page
+
+
+# ---- values and keys that are not numbers ------------------------------------------
+
+FEW = [(2, 40), (4, 300), (7, 130), (3, 9)]
+
+
+@pytest.mark.parametrize("window", [0, 3, 40])
+@pytest.mark.parametrize("what", ["row", "code", "scale"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq", [2, 4])  # tiles of 8 and of 16 rows
+def test_codes_of_few_rows_that_are_not_numbers_reach_only_rows_that_see_them(dev, Hq, D, what, window):
+    q, tensors, table, cu, lens = make(FEW, Hq, 2, D, True, 16, "slots", dev, seed=D + window)
+    for b, (n, kv) in enumerate(FEW):
+        for j in {kv - 1, kv - 2, max(kv - n - window // 2, 0) if window else kv - 1}:  # drafted tokens; one behind a window
+            place = at(tensors, table, b, j)
+            if what == "row":  # as an append of an infinity or a NaN writes it
+                tensors[1][place][1], tensors[3][place][1] = 0x7F, 255
+            elif what == "code":
+                tensors[1][place][1, 5 + b], tensors[1][place][0, D - 1] = 0x7F, 0xFF
+            else:
+                tensors[3][place][1] = 255
+    o = fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens, window=window)
+    check(FEW, q, tensors, table, o, window)
+
+
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("new", [4, 40])
+def test_a_bad_token_appended_as_codes_leaves_those_before_it(dev, new, what):
+    """The last token's value has a number that is none: the rows before it do not see it."""
+    Hq, Hk, D, page = 4, 2, 128, 16
+    g = torch.Generator(device=dev).manual_seed(new)
+    cache = fb.new_kv_cache(4, page, Hk, D, fb.FP8BS_KV_E4M3)
+    row = torch.randn((new, Hq + 2 * Hk, D), generator=g, device=dev).to(torch.bfloat16)
+    row[-1, Hq + Hk + 1, 9] = what
+    pos = torch.arange(new, device=dev)
+    q = fb.fp8bs_qk_norm_rope_append(row[:, :Hq], row[:, Hq:Hq + Hk], row[:, Hq + Hk:], pos, pos, fb.Rope(D), cache)
+    table = torch.arange(4, dtype=torch.int32, device=dev).unsqueeze(0)
+    cu, lens = (torch.tensor(v, dtype=torch.int32, device=dev) for v in ([0, new], [new]))
+    o = fb.fp8bs_attn_paged(q, cache, table, cu, lens)
+    check([(new, new)], q, cache.tensors, table, o)
+    assert bool(torch.isfinite(o[:-1]).all()) and bool(torch.isnan(o[-1, Hq // Hk:]).all())
