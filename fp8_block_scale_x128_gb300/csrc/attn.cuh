@@ -329,6 +329,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
+// The upper bit of each byte of a word that is a code without a value.
+__device__ __forceinline__ uint32_t odd_codes(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u & 0x80808080u; }
+
+// Zeros in their place.
+__device__ __forceinline__ uint32_t without_odd_codes(uint32_t w) { return w & ~((odd_codes(w) >> 7) * 0xFFu); }
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }

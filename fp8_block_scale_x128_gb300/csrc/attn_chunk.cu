@@ -519,10 +519,13 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, con
                 uint32_t scale = sh.row_scale[u & 3][kv][r];
                 if (kv && masks) {
                     const bool key = j0 + r >= at.first && j0 + r < at.past;
-                    if (!key || scale == 255u) {  // see the head of this file
+                    const bool none = !key || scale == 255u;
+                    if (none || ((odd_codes(codes.x) | odd_codes(codes.y)) | (odd_codes(codes.z) | odd_codes(codes.w)))) {
+                        // see the head of this file
                         if (key) sh.mark[at.item & (kMarks - 1)] = at.item + 1;
-                        scale = largest;
-                        codes = make_uint4(0, 0, 0, 0);
+                        if (none) scale = largest;
+                        codes = none ? make_uint4(0, 0, 0, 0)
+                                     : make_uint4(without_odd_codes(codes.x), without_odd_codes(codes.y), without_odd_codes(codes.z), without_odd_codes(codes.w));
                     }
                 }
                 uint4 lo, hi;
@@ -725,11 +728,12 @@ __device__ __forceinline__ void add_odd(const AttnParams& p, Cursor c, int from,
             if (!attn_page(p, p.table + c.b * p.table_stride, j, &page)) continue;
             const int s = j & ((1 << p.page_log2) - 1);
             const bool codes = KIND == FP8BS_KV_E4M3;
-            if (codes && p.vs[page * p.zpstride + s * p.zsstride + c.head * p.zhstride] != 255) continue;
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v + page * p.pstride + s * p.sstride + c.head * p.hstride);
+            const bool none = codes && p.vs[page * p.zpstride + s * p.zsstride + c.head * p.zhstride] == 255;
+            const uint8_t* v = p.v + page * p.pstride + s * p.sstride + c.head * p.hstride;
 #pragma unroll 1
             for (int i = 0; i < D; ++i) {
-                const float x = codes ? __uint_as_float(0x7FFFFFFFu) : bf16_bits_to_float(v[i]);
+                const float x = codes ? __uint_as_float(none || odd_codes(v[i]) ? 0x7FFFFFFFu : 0u)
+                                      : bf16_bits_to_float(reinterpret_cast<const uint16_t*>(v)[i]);
                 if (isfinite(x)) continue;
                 if (o) o[i] = static_cast<uint16_t>(pack_bf16(bf16_bits_to_float(o[i]) + x, 0.0f));
                 else slot[i] += x;

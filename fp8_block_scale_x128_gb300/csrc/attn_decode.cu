@@ -118,9 +118,6 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
     return r;
 }
 
-// The upper bit of each byte of a word that is a code without a value.
-__device__ __forceinline__ uint32_t odd_codes(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u & 0x80808080u; }
-
 // 2^(b - 127), NaN for 255.
 __device__ __forceinline__ float scale_of(uint32_t b) {
     return b == 255u ? __uint_as_float(0x7FFFFFFFu) : e8m0_to_float(b);
@@ -547,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
 #pragma unroll 1
                 for (int i = lane; i < SL * kChunks * 4; i += 32) {
                     uint32_t* w = reinterpret_cast<uint32_t*>(rows) + i;
-                    *w &= ~((odd_codes(*w) >> 7) * 0xFFu);
+                    *w = without_odd_codes(*w);
                 }
                 __syncwarp();
             }

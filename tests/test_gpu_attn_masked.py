@@ -114,6 +114,25 @@ def test_codes_of_few_rows_that_are_not_numbers_reach_only_rows_that_see_them(de
     check(FEW, q, tensors, table, o, window)
 
 
+@pytest.mark.parametrize("window", [0, 30])
+@pytest.mark.parametrize("what", ["row", "code", "scale"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_codes_of_many_rows_that_are_not_numbers_reach_only_rows_that_see_them(dev, D, what, window):
+    lengths = [(150, 300), (40, 90), (30, 1000)]
+    q, tensors, table, cu, lens = make(lengths, 4, 2, D, True, 16, "slots", dev, seed=D + window)
+    for b, (n, kv) in enumerate(lengths):
+        for j in (kv - 1, kv - 20, kv - n - 2 if window else kv - 5):
+            place = at(tensors, table, b, j)
+            if what == "row":
+                tensors[1][place][1], tensors[3][place][1] = 0x7F, 255
+            elif what == "code":
+                tensors[1][place][1, 5 + b], tensors[1][place][0, D - 1] = 0x7F, 0xFF
+            else:
+                tensors[3][place][1] = 255
+    o = fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens, window=window)
+    check(lengths, q, tensors, table, o, window)
+
+
 @pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("new", [4, 40])
 def test_a_bad_token_appended_as_codes_leaves_those_before_it(dev, new, what):
