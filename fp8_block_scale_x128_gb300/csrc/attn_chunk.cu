@@ -868,7 +868,9 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
                 for (int i = 0; i < 32; i += 2) tops[(i >> 1) & 7] = fmaxf(tops[(i >> 1) & 7], fmaxf(x[i], x[i + 1]));
             }
             const float2 scale = C::kCodes ? sh.scales[u & 7] : make_float2(1.0f, 0.0f);
-            const float factor = C::kCodes ? now * scale.x : p.scale_log2;
+            // (above zero, so that masked scores stay minus infinity; scores are below 2^34, and
+            // 2^-126 of that is nothing)
+            const float factor = C::kCodes ? fminf(fmaxf(now * scale.x, 0x1p-126f), 0x1.fffffep127f) : p.scale_log2;
             const float top = scale.y + factor * fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
                                                        fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
             float shrink = 1.0f;

@@ -149,3 +149,19 @@ def test_a_bad_token_appended_as_codes_leaves_those_before_it(dev, new, what):
     o = fb.fp8bs_attn_paged(q, cache, table, cu, lens)
     check([(new, new)], q, cache.tensors, table, o)
     assert bool(torch.isfinite(o[:-1]).all()) and bool(torch.isnan(o[-1, Hq // Hk:]).all())
+
+
+# ---- scales of codes ---------------------------------------------------------------
+
+@pytest.mark.parametrize("size,scale", [(1e-3, None), (1.0, 1e-6), (1.0, 1e-30), (1e-20, 1e-20)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_keys_of_zeros_and_tiny_scores_under_a_mask(dev, D, size, scale):
+    """Units whose keys are all rows of zeros, and sequences without a key, at scores of next to nothing."""
+    lengths = [(20, 0), (30, 300), (40, 200), (17, 5)]
+    q, tensors, table, cu, lens = make(lengths, 4, 2, D, True, 16, "slots", dev, seed=D, size=size)
+    for b, (n, kv) in enumerate(lengths):
+        for j in range(256 if b == 1 else 0, kv):
+            place = at(tensors, table, b, j)
+            tensors[0][place], tensors[2][place] = 0, 0
+    o = fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens, scale=scale)
+    check(lengths, q, tensors, table, o, scale=scale)
