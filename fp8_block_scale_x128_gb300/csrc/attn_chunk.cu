@@ -21,9 +21,11 @@
 // Codes.  e4m3 codes are exact in fp16, and the products run in it.  A row of q is
 // multiplied by the power of two that brings its largest magnitude into [2^14, 2^15)
 // (exact down to 2^-31 of that).  A code is multiplied by its scale over the largest of
-// its unit, at most 1 (exact down to 2^-15, below off by at most 2^-25 of the largest);
-// the unit's own scale multiplies the scores, and the values' is part of the weights,
-// 2^(x + e), of which the maximum is taken.  2^7 more uses fp16's range: a weight is off
+// its unit, exactly where they differ by 2^14 at most; the unit's own scale multiplies the
+// scores, and the values' is part of the weights, 2^(x + e), of which the maximum is taken.
+// Where the scales of a unit's keys or of its values are further apart, codes stay as they
+// are, and each score has its key's own scale and each weight its value's: a masked key, or
+// one of no weight, may be as large as it likes.  2^7 more uses fp16's range: a weight is off
 // by at most 2^-12 of itself, or 2^-32 of the largest.
 //
 // A value that is not finite and that some row of its unit masks would reach that row
@@ -103,8 +105,8 @@ struct Shared {
     uint64_t full[4], raw[2], empty[4], scores[2], weights[2], joined[2], query[2], drained;
     uint64_t coded[3], widened[3];  // of the tiles of codes: they are there, they are free
     uint8_t row_scale[4][2][128];   // of a unit's keys and values
-    uint32_t largest[4][2];
-    float2 scales[8];               // of a unit: 2^e of the keys, e of the values
+    uint32_t largest[4][2];         // 0: scales too far apart
+    float2 scales[8];               // of a unit: 2^e of the keys, e of the values; 0, 0 if too far apart
     float unscale[2][2 * kRows];    // codes: what a row's scores are multiplied by, of an item and the next
     uint32_t tmem;
     int dead;
@@ -286,11 +288,13 @@ struct Place : Cursor {
     }
 };
 
-// 16 codes -> 16 fp16 numbers times 2^-down (NaN for a scale of 255).
+constexpr uint32_t kApart = 14;  // 2^-14 times a code is exact in fp16
+
+// 16 codes -> 16 fp16 numbers times the scale over the largest, or 1 where that is the
+// smaller (NaN for a scale of 255).
 __device__ __forceinline__ void widen(const uint4& c, uint32_t scale, uint32_t largest, uint4& lo, uint4& hi) {
-    // codes times 2^-14 are exact, so two factors round once
-    const uint32_t down = scale == 255u ? 0u : largest - scale;
-    const uint32_t bits = scale == 255u ? 0x7E00u : (15u - min(down, 14u)) << 10;
+    const uint32_t down = min(largest - min(scale, largest), kApart);  // (more: no key)
+    const uint32_t bits = scale == 255u ? 0x7E00u : (15u - down) << 10;
     const __half2 f = __half2half2(__ushort_as_half(static_cast<unsigned short>(bits)));
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     __half2 r[8];
@@ -301,12 +305,6 @@ __device__ __forceinline__ void widen(const uint4& c, uint32_t scale, uint32_t l
             : "=r"(a), "=r"(b)
             : "r"(w[i]));
         r[2 * i] = __hmul2_rn(*reinterpret_cast<__half2*>(&a), f), r[2 * i + 1] = __hmul2_rn(*reinterpret_cast<__half2*>(&b), f);
-    }
-    if (down > 14u) {
-        const uint32_t more = down - 14u, rest = more <= 14u ? (15u - more) << 10 : more <= 24u ? 1u << (24u - more) : 0u;
-        const __half2 g = __half2half2(__ushort_as_half(static_cast<unsigned short>(rest)));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = __hmul2_rn(r[i], g);
     }
     const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
     lo = make_uint4(u[0], u[1], u[2], u[3]);
@@ -360,7 +358,7 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
 #pragma unroll
         for (int i = 0; i < C::kKeys / 32; ++i) {
             const int j = (at.lo + at.unit) * C::kKeys + lane + 32 * i, id = page_of(j);
-            zk[i] = zv[i] = 0;
+            zk[i] = zv[i] = 256;  // no key
             if (id >= 0) {
                 const long long z = id * p.zpstride + (j & ((1 << p.page_log2) - 1)) * p.zsstride + at.head * p.zhstride;
                 zk[i] = p.ks[z], zv[i] = p.vs[z];
@@ -368,7 +366,7 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
         }
     };
     auto keep_scales = [&](int u) {
-        uint32_t mostk = 0, mostv = 0;
+        uint32_t mostk = 0, mostv = 0, leastk = 255, leastv = 255;
 #pragma unroll
         for (int i = 0; i < C::kKeys / 32; ++i) {
             // a value's scale below 2^-80 counts as that (the sum of the weights, which are
@@ -376,12 +374,14 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
             zv[i] = max(zv[i], 47u);
             sh.row_scale[u & 3][0][lane + 32 * i] = static_cast<uint8_t>(zk[i]);
             sh.row_scale[u & 3][1][lane + 32 * i] = static_cast<uint8_t>(zv[i]);
-            mostk = max(mostk, zk[i] == 255u ? 0u : zk[i]), mostv = max(mostv, zv[i] == 255u ? 0u : zv[i]);
+            if (zk[i] < 255u) mostk = max(mostk, zk[i]), leastk = min(leastk, zk[i]);
+            if (zv[i] < 255u) mostv = max(mostv, zv[i]), leastv = min(leastv, zv[i]);
         }
         mostk = __reduce_max_sync(0xFFFFFFFFu, mostk), mostv = __reduce_max_sync(0xFFFFFFFFu, mostv);
+        const bool apart = __any_sync(0xFFFFFFFFu, mostk > leastk + kApart || mostv > leastv + kApart);
         if (lane == 0) {
-            sh.largest[u & 3][0] = mostk, sh.largest[u & 3][1] = mostv;
-            sh.scales[u & 7] = make_float2(e8m0_to_float(mostk), static_cast<float>(static_cast<int>(mostv) - 127));
+            sh.largest[u & 3][0] = apart ? 0u : mostk, sh.largest[u & 3][1] = apart ? 0u : mostv;
+            sh.scales[u & 7] = apart ? make_float2(0.0f, 0.0f) : make_float2(e8m0_to_float(mostk), static_cast<float>(static_cast<int>(mostv) - 127));
         }
         __syncwarp();
     };
@@ -710,6 +710,38 @@ __device__ __forceinline__ void mask_scores(uint32_t scores, int hi, int lo) {
     ptx::tmem_wait_st();
 }
 
+// Scores that have each its key's own scale, plus the exponents of the values', in units of
+// log2, in the place of a row's scores over codes whose scales are far apart.  Returns the
+// largest x without those exponents and the sum of 2^(x - that).
+template <int KEYS>
+__device__ __forceinline__ float2 scale_scores(uint32_t scores, const uint8_t (&row_scale)[2][128], float factor) {
+    float top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < KEYS; c += 16) {
+        uint32_t s[16];
+        ptx::tmem_ld_32x32b_x16(scores + c, s);
+        ptx::tmem_wait_ld();
+        float most = top;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float x = __uint_as_float(s[i]) * factor * e8m0_to_float(row_scale[0][c + i]);
+            if (s[i] != 0xFF800000u) s[i] = __float_as_uint(x);  // (masked: whatever scale that key has)
+            most = fmaxf(most, __uint_as_float(s[i]));
+        }
+        const float at = most == -INFINITY ? 0.0f : most;
+        sum *= ex2(top - at);
+        top = most;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            sum += ex2(__uint_as_float(s[i]) - at);
+            s[i] = __float_as_uint(__uint_as_float(s[i]) + static_cast<float>(static_cast<int>(row_scale[1][c + i]) - 127));
+        }
+        tmem_st16(scores + c, s);
+    }
+    ptx::tmem_wait_st();
+    return make_float2(top, sum);
+}
+
 // The values that are not finite, among the keys that a row sees in the item's units
 // with masks from `from` on, where zeros stood for them: added to what the row has in
 // o or, without that, in a slot.
@@ -840,6 +872,10 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
                 const int hi = at.base + token - j0;
                 mask_scores<C::kKeys>(scores, hi, p.window ? hi - p.window + 1 : 0);
             }
+            const float2 scale = C::kCodes ? sh.scales[u & 7] : make_float2(1.0f, 0.0f);
+            const bool apart = C::kCodes && scale.x == 0.0f;
+            float2 unit = make_float2(0.0f, 0.0f);  // its largest score and sum
+            if (apart) unit = scale_scores<C::kKeys>(scores, sh.row_scale[u & 3], now);
             // Codes: a loop over 32 scores, which are read again for their weights: the loaders'
             // code is long, and all of it has to stay in the instruction cache (4096 tokens over
             // 16384 keys 1065 us without, 997 so).  bf16: a row's scores in registers (681 us,
@@ -867,10 +903,9 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) tops[(i >> 1) & 7] = fmaxf(tops[(i >> 1) & 7], fmaxf(x[i], x[i + 1]));
             }
-            const float2 scale = C::kCodes ? sh.scales[u & 7] : make_float2(1.0f, 0.0f);
             // (above zero, so that masked scores stay minus infinity; scores are below 2^34, and
             // 2^-126 of that is nothing)
-            const float factor = C::kCodes ? fminf(fmaxf(now * scale.x, 0x1p-126f), 0x1.fffffep127f) : p.scale_log2;
+            const float factor = apart ? 1.0f : C::kCodes ? fminf(fmaxf(now * scale.x, 0x1p-126f), 0x1.fffffep127f) : p.scale_log2;
             const float top = scale.y + factor * fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
                                                        fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
             float shrink = 1.0f;
@@ -914,7 +949,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
                 tmem_st16(weights + 16 * c, w);
             }
             const float2 both = halves(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
-            sum += C::kCodes ? (both.x + both.y) * ex2(-scale.y) : both.x + both.y;
+            sum += apart ? unit.y * ex2(unit.x - base) : C::kCodes ? (both.x + both.y) * ex2(-scale.y) : both.x + both.y;
             ptx::tmem_wait_st();
         }
         ptx::tc_fence_before();

@@ -165,3 +165,34 @@ def test_keys_of_zeros_and_tiny_scores_under_a_mask(dev, D, size, scale):
             tensors[0][place], tensors[2][place] = 0, 0
     o = fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens, scale=scale)
     check(lengths, q, tensors, table, o, scale=scale)
+
+
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("byte", [133, 143, 155, 180])  # 2^6 .. 2^53
+@pytest.mark.parametrize("lengths", [[(4, 300), (7, 130)], [(150, 300), (40, 90)]])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_large_scales_that_are_masked_change_nothing(dev, D, lengths, byte, window):
+    q, tensors, table, cu, lens = make(lengths, 4, 2, D, True, 16, "slots", dev, seed=D + byte)
+    for b, (n, kv) in enumerate(lengths):
+        for j in (kv - 1, kv - n - window // 2 - 2 if window else kv - 2):
+            place = at(tensors, table, b, j)
+            tensors[2][place][0], tensors[3][place][1] = byte, byte
+    o = fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens, window=window)
+    check(lengths, q, tensors, table, o, window)
+
+
+@pytest.mark.parametrize("apart", [-70, -20, 14, 15, 20, 40])
+@pytest.mark.parametrize("lengths", [[(4, 300), (7, 130)], [(150, 300), (40, 90)]])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_large_values_of_next_to_no_weight(dev, D, lengths, apart):
+    """A key far below the others' scores: its value, or its own size, takes nothing from them."""
+    q, tensors, table, cu, lens = make(lengths, 4, 2, D, True, 16, "slots", dev, seed=D)
+    q[:, :, :] = q.abs() + 0.5
+    for b, (n, kv) in enumerate(lengths):
+        for j in (3, kv - n - 5):
+            place = at(tensors, table, b, j)
+            tensors[0][place] = 0xFE  # -448: scores of some -448 sqrt(D) scale
+            tensors[2][place][0], tensors[2][place][1] = 127, 127 + max(apart, 0)
+            tensors[3][place][0] = 119 + apart
+    o = fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens)
+    check(lengths, q, tensors, table, o)
