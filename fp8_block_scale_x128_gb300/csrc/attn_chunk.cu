@@ -374,8 +374,8 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
             zv[i] = max(zv[i], 47u);
             sh.row_scale[u & 3][0][lane + 32 * i] = static_cast<uint8_t>(zk[i]);
             sh.row_scale[u & 3][1][lane + 32 * i] = static_cast<uint8_t>(zv[i]);
-            if (zk[i] < 255u) mostk = max(mostk, zk[i]), leastk = min(leastk, zk[i]);
-            if (zv[i] < 255u) mostv = max(mostv, zv[i]), leastv = min(leastv, zv[i]);
+            mostk = max(mostk, zk[i] < 255u ? zk[i] : 0u), leastk = min(leastk, zk[i]);
+            mostv = max(mostv, zv[i] < 255u ? zv[i] : 0u), leastv = min(leastv, zv[i]);
         }
         mostk = __reduce_max_sync(0xFFFFFFFFu, mostk), mostv = __reduce_max_sync(0xFFFFFFFFu, mostv);
         const bool apart = __any_sync(0xFFFFFFFFu, mostk > leastk + kApart || mostv > leastv + kApart);
@@ -714,7 +714,7 @@ __device__ __forceinline__ void mask_scores(uint32_t scores, int hi, int lo) {
 // log2, in the place of a row's scores over codes whose scales are far apart.  Returns the
 // largest x without those exponents and the sum of 2^(x - that).
 template <int KEYS>
-__device__ __forceinline__ float2 scale_scores(uint32_t scores, const uint8_t (&row_scale)[2][128], float factor) {
+__device__ __noinline__ float2 scale_scores(uint32_t scores, const uint8_t (&row_scale)[2][128], float factor) {
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll 1
     for (int c = 0; c < KEYS; c += 16) {
