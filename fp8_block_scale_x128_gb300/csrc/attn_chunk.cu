@@ -114,6 +114,10 @@ struct Shared {
     int mark[kMarks];
 };
 
+// Cycles in which copies and products that are under way are over, by far: a block in which
+// a wait has run out stays so long, however short that wait's limit is.
+constexpr long long kLanding = 1000000;
+
 // One lane of the warp, the same every time.
 __device__ __forceinline__ bool ptx_elect() {
     uint32_t e;
@@ -425,13 +429,6 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
             if (alive) find();
             if (alive && C::kCodes) read_scales();
         }
-    }
-    if (!alive) {  // what is under way lands before the block leaves
-        const long long began = clock64();
-        for (uint32_t f = fill < kRing ? 0 : fill - kRing; f <= fill; ++f)
-            while (!ptx::mbar_test(C::kCodes ? &sh.coded[f % kRing] : &sh.full[f % kRing], (f / kRing) & 1) &&
-                   clock64() - began < 1000000) {
-            }
     }
 }
 
@@ -1085,12 +1082,16 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
             // nothing of the tensor core's is under way when the memory is given back
             ptx::mma_commit_warp(&sh.drained);
             const long long began = clock64();
-            while (!ptx::mbar_test(&sh.drained, 0) && clock64() - began < p.timeout_cycles) {
+            while (!ptx::mbar_test(&sh.drained, 0) && clock64() - began < kLanding) {
             }
         }
     }
     ptx::tc_fence_before();
     __syncthreads();
+    if (sh.dead) {
+        const long long began = clock64();
+        while (clock64() - began < kLanding) __nanosleep(1000);
+    }
     if (warp == C::kSoft) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(sh.tmem, 512);
