@@ -554,8 +554,10 @@ __device__ __forceinline__ void widen_units(const AttnParams& p, Shared& sh, con
 //     [the next unit's keys]   next S = Q K^T in the other buffer
 //     [weights, values there]  O += P V
 // After an item's last unit the next S has a step of its own, the last, in which the
-// next item's queries are waited for.  (Weights handed over in halves of a unit's keys,
-// to begin the product earlier, took 757 us where this takes 697.)
+// next item's queries are waited for.  Once a wait has run out, here or in another task
+// (sh.dead), the watcher lets one more step go and leaves; the issuer looks before each
+// step, so it finds that step or the mark, and leaves too.  (Weights handed over in halves
+// of a unit's keys, to begin the product earlier, took 757 us where this takes 697.)
 constexpr uint32_t kStepBarrier = 2, kStepBarriers = 8;
 
 template <int D, int KIND>
@@ -564,22 +566,26 @@ __device__ __forceinline__ void watch(const AttnParams& p, Shared& sh) {
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     Place at;
     uint32_t step = 0;
-    bool alive = at.start(p, sh);  // once that fails, every step is let go all the same
+    bool alive = at.start(p, sh);
     auto need = [&](uint64_t* bar, uint32_t parity) {
         if (alive) alive = __all_sync(0xFFFFFFFFu, wait(sh, bar, parity, p));
     };
     auto full = [&](uint32_t fill) { need(&sh.full[fill % C::kStages], (fill / C::kStages) & 1); };
-    auto go = [&] { ptx::named_arrive(kStepBarrier + step++ % kStepBarriers, 64); };
+    auto go = [&] {
+        if (!alive) __threadfence_block();  // the mark is seen with the step
+        ptx::named_arrive(kStepBarrier + step++ % kStepBarriers, 64);
+        return alive;
+    };
     uint32_t items = 0;
     need(&sh.query[0], 0);
     if (C::kStreams == 2) need(&sh.query[1], 0);
     full(0);
-    go();
+    if (!go()) return;
 #pragma unroll 1
     for (int u = 0; u < units; ++u) {
         const uint32_t fv = 2 * static_cast<uint32_t>(u) + 1, fk = fv + 1;
         const bool more = u + 1 < units, last = at.unit + 1 == at.n;
-        if (more && alive) alive = at.next(p, sh);
+        if (more) alive = at.next(p, sh);
         items += last;
         if (C::kStreams == 2) {
             full(fv);
@@ -587,24 +593,24 @@ __device__ __forceinline__ void watch(const AttnParams& p, Shared& sh) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 need(&sh.weights[s], u & 1);
-                go();
+                if (!go()) return;
                 if (more && last) {
                     need(&sh.query[s], items & 1);
-                    go();
+                    if (!go()) return;
                 }
             }
         } else {
             if (more && !last) {
                 full(fk);
-                go();
+                if (!go()) return;
             }
             full(fv);
             need(&sh.weights[u & 1], (u >> 1) & 1);
-            go();
+            if (!go()) return;
             if (more && last) {
                 full(fk);
                 need(&sh.query[0], items & 1);
-                go();
+                if (!go()) return;
             }
         }
     }
@@ -617,9 +623,12 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, 
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     const uint32_t tmem = sh.tmem;
     uint32_t step = 0;
+    auto over = [&] { return __any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int*>(&sh.dead) != 0); };
     auto come = [&] {
+        if (over()) return false;
         ptx::named_sync(kStepBarrier + step++ % kStepBarriers, 64);
         ptx::tc_fence_after();
+        return true;
     };
     auto tile = [&](uint32_t fill) { return ring + fill % C::kStages * C::kTileBytes; };
     auto scores = [&](int stream, int buffer, uint32_t keys, int rows) {
@@ -635,8 +644,9 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, 
         ptx::mma_commit_warp(&sh.joined[buffer]);
     };
 
-    come();
-    // (the watcher has seen that the items which are read here are known)
+    if (!come() || over()) return;
+    // (the watcher has seen that the items which are read here are known; of one that is
+    // not, in the step after a wait has run out, no more is used than how many rows it has)
     int item = 0, unit = sh.plan.share.unit, n = sh.items[0].n, rows = sh.items[0].rows;
     bool first = true;  // the unit is its item's first here
 #pragma unroll 1
@@ -655,12 +665,12 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, 
         if constexpr (C::kStreams == 2) {
 #pragma unroll 1
             for (int s = 0; s < 2; ++s) {
-                come();
+                if (!come()) return;
                 values(s, s, tile(fv), rows_now, first);
                 if (s == 1) ptx::mma_commit_warp(&sh.empty[fv % C::kStages]);
                 if (more) {
                     if (last) {
-                        come();
+                        if (!come()) return;
                         if (s == 0) go_on();
                     }
                     scores(s, s, tile(fk), rows);
@@ -670,16 +680,17 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, Shared& sh, 
         } else {
             const int b = u & 1;
             auto next = [&] {
-                come();
+                if (!come()) return false;
                 if (last) go_on();
                 scores(0, b ^ 1, tile(fk), rows);
                 ptx::mma_commit_warp(&sh.empty[fk % C::kStages]);
+                return true;
             };
-            if (more && !last) next();
-            come();
+            if (more && !last && !next()) return;
+            if (!come()) return;
             values(0, b, tile(fv), rows_now, first);
             ptx::mma_commit_warp(&sh.empty[fv % C::kStages]);
-            if (more && last) next();
+            if (more && last && !next()) return;
         }
         first = last;
     }
