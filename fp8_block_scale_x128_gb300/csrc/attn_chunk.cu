@@ -49,7 +49,10 @@ namespace {
 constexpr int kRows = 128;  // of a stream
 constexpr float kLag = 8.0f;
 constexpr int kMarks = 8;
-constexpr int kItems = 8;  // that may be under way: the loaders are at most three ahead of the outputs
+// That may be under way.  The loaders are at most three ahead of the outputs; warps that look
+// values through wait for nothing in units without masks, so an item's place is given to
+// another only once they have read it (`taken`).
+constexpr int kItems = 8;
 
 template <int D, int KIND>
 struct Cfg {
@@ -98,6 +101,7 @@ struct Shared {
     PlanShared plan;
     Cursor items[kItems];
     uint64_t known[kItems];  // that an item stands there
+    uint64_t taken[kItems];  // that the warps which look values through have read it
     long long next_start;    // units before the next item
     // scores, weights and joined (outputs): of a score buffer.  A phase's parity is that of
     // the one before last, too, so a barrier is waited for only where the phase before is
@@ -246,8 +250,12 @@ __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int d
 // first, finds out what they are, and the other tasks read it.  (The code that does it is
 // long, and there is one copy of it: what the instruction cache does not hold costs
 // more than the look-up.)
-template <int ROWS, int UNIT>
-__device__ __noinline__ void publish(const AttnParams& p, Shared& sh, int item) {
+// PACED: see kItems.  False when that wait ran out.
+template <int ROWS, int UNIT, bool PACED>
+__device__ __noinline__ bool publish(const AttnParams& p, Shared& sh, int item) {
+    if (PACED && item >= kItems &&
+        !__all_sync(0xFFFFFFFFu, wait<true>(sh, &sh.taken[item & (kItems - 1)], (item / kItems - 1) & 1, p)))
+        return false;
     Cursor c;
     if (item == 0) {
         const AttnShare& s0 = sh.plan.share;
@@ -270,6 +278,7 @@ __device__ __noinline__ void publish(const AttnParams& p, Shared& sh, int item) 
         ptx::mbar_arrive(&sh.known[item & (kItems - 1)]);
     }
     __syncwarp();
+    return true;
 }
 
 // A task's place: the unit of an item.
@@ -340,7 +349,7 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
     Place at;
     const bool publishes = kv0 == 0 && which == 0;
     auto box = [&](int i) { return (lane + 32 * i) * C::kShare + which; };  // a lane's boxes
-    if (publishes) publish<C::kTile, C::kKeys>(p, sh, 0);
+    if (publishes) publish<C::kTile, C::kKeys, !C::kCodes>(p, sh, 0);
     bool alive = at.start(p, sh);
     uint32_t fill = 0;  // tiles of both kinds
     int page[kMost];
@@ -424,8 +433,8 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
             }
         }
         if (u + 1 < units && alive) {  // the next unit's pages, while this one's tiles come
-            if (publishes && at.unit + 1 == at.n) publish<C::kTile, C::kKeys>(p, sh, at.item + 1);
-            alive = at.next(p, sh);
+            if (publishes && at.unit + 1 == at.n) alive = publish<C::kTile, C::kKeys, !C::kCodes>(p, sh, at.item + 1);
+            alive = alive && at.next(p, sh);
             if (alive) find();
             if (alive && C::kCodes) read_scales();
         }
@@ -440,6 +449,11 @@ __device__ __forceinline__ void check_units(const AttnParams& p, Shared& sh, uin
     const int units = static_cast<int>(sh.plan.share.end - sh.plan.share.begin);
     Place at;
     bool alive = at.start(p, sh);
+    auto take = [&] {  // the item is read, by all lanes
+        __syncwarp();
+        if ((tid & 31) == 0) ptx::mbar_arrive(&sh.taken[at.item & (kItems - 1)]);
+    };
+    if (alive) take();
     uint32_t checked[2] = {0, 0};
 #pragma unroll 1
     for (int u = 0; u < units && alive; ++u) {
@@ -478,7 +492,11 @@ __device__ __forceinline__ void check_units(const AttnParams& p, Shared& sh, uin
                 }
             }
         }
-        if (alive && u + 1 < units) alive = at.next(p, sh);
+        if (alive && u + 1 < units) {
+            const int item = at.item;
+            alive = at.next(p, sh);
+            if (alive && at.item != item) take();
+        }
     }
 }
 
@@ -1059,7 +1077,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::kThreads, 1) attn_chunk_kernel(c
             ptx::mbar_init(&sh.query[i], 128);
         }
         ptx::mbar_init(&sh.drained, 1);
-        for (int i = 0; i < kItems; ++i) ptx::mbar_init(&sh.known[i], 1);
+        for (int i = 0; i < kItems; ++i) ptx::mbar_init(&sh.known[i], 1), ptx::mbar_init(&sh.taken[i], C::kOthers / 32);
         ptx::fence_mbar_init();
         sh.dead = 0;
         sh.looked[0] = sh.looked[1] = 0;

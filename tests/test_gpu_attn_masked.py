@@ -196,3 +196,21 @@ def test_large_values_of_next_to_no_weight(dev, D, lengths, apart):
             tensors[3][place][0] = 119 + apart
     o = fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens)
     check(lengths, q, tensors, table, o)
+
+
+# ---- the precision of weights ------------------------------------------------------
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_items_without_masks(dev, D, codes):
+    """One token a sequence of many query heads, lengths that end with a unit: nothing to look through."""
+    lengths = [(1, 128 * (1 + b % 2)) for b in range(300)]
+    q, tensors, table, cu, lens = make(lengths, 128, 4, D, codes, 16, "slots", dev, seed=D)
+    cache, ws = fb.KvCache(*tensors), fb.new_attn_workspace(D)
+    o = fb.fp8bs_attn_paged(q, cache, table, cu, lens, workspace=ws)
+    for _ in range(20):
+        assert torch.equal(o, fb.fp8bs_attn_paged(q, cache, table, cu, lens, workspace=ws))
+    assert fb.fp8bs_check_error(ws) == 0
+    rows = [0, 1, 151, 152, 299]
+    first = torch.tensor(rows, device=dev)
+    check([lengths[r] for r in rows], q[first], tensors, table[first], o[first])
