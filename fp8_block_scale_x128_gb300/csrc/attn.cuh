@@ -290,6 +290,10 @@ struct AttnSplit {
     int32_t pad[3];
 };
 
+// The sum of a row's weights where it sees keys, all at scores of minus infinity: values
+// divided by it are NaN.  (Other sums of rows that see keys are above 2^-126.)
+constexpr float kNoWeight = 0x1p-149f;
+
 // Workspace past the error word: a record a block, then two slots a block:
 // slot 0 for an item begun elsewhere, slot 1 for one begun here.  A slot holds
 // values [rows][D], maxima [rows] (in units of log2) and sums [rows], all fp32.

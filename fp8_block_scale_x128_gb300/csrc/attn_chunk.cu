@@ -999,6 +999,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
         if (active) {
             const bool whole = last && begun, there = stream * kRows + row < was.rows;
             const bool odd = *reinterpret_cast<volatile int*>(&sh.mark[was.item & (kMarks - 1)]) == was.item + 1;
+            if (sum == 0.0f && was.base + token >= 0) sum = kNoWeight;
             const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : __frcp_rn(sum);
             uint16_t* dst = p.o + static_cast<int64_t>(was.q0 + token) * p.ldo + head * p.hso;
             const int at_row = stream * kRows + row;

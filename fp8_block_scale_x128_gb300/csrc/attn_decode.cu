@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], off);
+                if (l[n][i] == 0.0f && place[n][i] >= 0) l[n][i] = kNoWeight;
                 if (g == 0) sh.parts[warp][8 * n + 2 * t + i] = make_float2(m[n][i], l[n][i]);
             }
         __syncthreads();
@@ -654,7 +655,7 @@ __global__ void __launch_bounds__(kJoin) attn_join_kernel(const __grid_constant_
                 const float top = fmaxf(most, m), at = top == -INFINITY ? 0.0f : top;
                 const float keep = ex2(most - at), w = ex2(m - at);
                 most = top;
-                sum = fmaf(l, w, sum * keep);
+                sum = m == -INFINITY ? sum + l : fmaf(l, w, sum * keep);
                 v[0] = fmaf(x.x, w, v[0] * keep), v[1] = fmaf(x.y, w, v[1] * keep);
                 v[2] = fmaf(x.z, w, v[2] * keep), v[3] = fmaf(x.w, w, v[3] * keep);
                 v[4] = fmaf(y.x, w, v[4] * keep), v[5] = fmaf(y.y, w, v[5] * keep);
@@ -674,7 +675,7 @@ __global__ void __launch_bounds__(kJoin) attn_join_kernel(const __grid_constant_
                     const float top = fmaxf(most, o[0]), at = top == -INFINITY ? 0.0f : top;
                     const float keep = ex2(most - at), w = ex2(o[0] - at);
                     most = top;
-                    sum = fmaf(o[1], w, sum * keep);
+                    sum = o[0] == -INFINITY ? sum + o[1] : fmaf(o[1], w, sum * keep);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] = fmaf(o[2 + i], w, v[i] * keep);
                 }

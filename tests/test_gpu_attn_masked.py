@@ -198,6 +198,40 @@ def test_large_values_of_next_to_no_weight(dev, D, lengths, apart):
     check(lengths, q, tensors, table, o)
 
 
+# ---- scores of minus infinity ------------------------------------------------------
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("lengths", [[(4, 300), (1, 7), (3, 2), (2, 5000)], [(150, 300), (40, 90), (20, 7), (30, 4000)]])
+def test_rows_whose_scores_are_all_minus_infinity_are_no_numbers(dev, lengths, codes):
+    D = 128
+    q, tensors, table, cu, lens = make(lengths, 4, 2, D, codes, 16, "slots", dev, seed=1)
+    if codes:
+        tensors[0][:, :, 1, 3] = 0xB8  # -1
+        q[:, 3, 3] = math.inf
+    else:
+        tensors[0][:, :, 1, 3] = -math.inf
+        q[:, 3, 3], q[:, 2, 3] = 1.0, -1.0
+    cache, ws = fb.KvCache(*tensors), fb.new_attn_workspace(D)
+    o = fb.fp8bs_attn_paged(q, cache, table, cu, lens, workspace=ws)
+    first = 0
+    for n, kv in lengths:
+        rows = o[first:first + n].float()
+        none = max(n - kv, 0)  # rows that see no key
+        assert bool((rows[:none] == 0).all())
+        assert bool(torch.isnan(rows[none:, 3]).all())
+        assert bool(torch.isfinite(rows[none:, :2]).all())
+        first += n
+
+
+def test_a_score_of_minus_infinity_beside_others_is_no_weight(dev):
+    for lengths in ([(4, 300), (2, 9)], [(150, 300), (40, 90)]):
+        q, tensors, table, cu, lens = make(lengths, 4, 2, 128, False, 16, "slots", dev, seed=2)
+        q[:, :, 3] = q[:, :, 3].abs() + 0.25
+        for b, (n, kv) in enumerate(lengths):
+            tensors[0][at(tensors, table, b, kv - n)][1, 3] = -math.inf
+        check(lengths, q, tensors, table, fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens))
+
+
 # ---- the precision of weights ------------------------------------------------------
 
 @pytest.mark.parametrize("codes", [False, True])
