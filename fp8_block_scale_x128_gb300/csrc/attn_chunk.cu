@@ -1174,7 +1174,15 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     CUtensorMap mk = {}, mv = {};
     const int rows = min(1 << a.page_log2, C::kKeys);
-    if (!describe(&mk, a, a.k, rows) || !describe(&mv, a, a.v, rows)) return cudaErrorInvalidValue;
+    if (!describe(&mk, a, a.k, rows)) {
+        // the first call of a host thread: the device's context is not current in it yet
+        int dev = 0;
+        cudaError_t s = cudaGetDevice(&dev);
+        if (s == cudaSuccess) s = cudaSetDevice(dev);
+        if (s != cudaSuccess) return s;
+        if (!describe(&mk, a, a.k, rows)) return cudaErrorInvalidValue;
+    }
+    if (!describe(&mv, a, a.v, rows)) return cudaErrorInvalidValue;
     const cudaError_t r = w4::launch_dependent(attn_chunk_kernel<D, KIND>, a.sm_count, C::kThreads, C::kSmem, stream,
                                                static_cast<const AttnParams&>(a), mk, mv);
     return r == cudaSuccess ? launch_attn_join(a, C::kTile, a.sm_count, stream) : r;

@@ -234,6 +234,29 @@ def test_a_score_of_minus_infinity_beside_others_is_no_weight(dev):
 
 # ---- the precision of weights ------------------------------------------------------
 
+def test_a_thread_of_its_own(dev):
+    """The first call of a host thread that has made no other."""
+    import threading
+    lengths = [(150, 300)]
+    q, tensors, table, cu, lens = make(lengths, 4, 2, 128, False, 16, "slots", dev, seed=3)
+    cache, ws, o = fb.KvCache(*tensors), fb.new_attn_workspace(128), torch.zeros_like(q)
+    torch.cuda.synchronize()
+    failed = []
+
+    def work():
+        try:
+            fb.fp8bs_attn_paged(q, cache, table, cu, lens, o=o, workspace=ws)
+            torch.cuda.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    assert not failed
+    check(lengths, q, tensors, table, o)
+
+
 @pytest.mark.parametrize("codes", [False, True])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_many_items_without_masks(dev, D, codes):
