@@ -26,7 +26,7 @@
 // Where the scales of a unit's keys or of its values are further apart, codes stay as they
 // are, and each score has its key's own scale and each weight its value's: a masked key, or
 // one of no weight, may be as large as it likes.  2^7 more uses fp16's range: a weight is off
-// by at most 2^-12 of itself, or 2^-32 of the largest.
+// by at most 2^-11 of itself, or 2^-32 of the largest.
 //
 // A value that is not finite and that some row of its unit masks would reach that row
 // as zero times it.  In units with masks the loaders put zeros in the place of such

@@ -21,7 +21,7 @@
 // exact down to 2^-31 of that, below off by at most 2^-39 of it.  A key's scale
 // multiplies its score.  A value's scale 2^e is part of its weight, 2^(x + e), the
 // maximum is taken of these, and 2^7 more uses fp16's range: a weight is off by at most
-// 2^-12 of itself, or 2^-32 of the largest.  (e below -80 counts as that, so that no sum
+// 2^-11 of itself, or 2^-32 of the largest.  (e below -80 counts as that, so that no sum
 // of the weights 2^x alone overflows.)
 // A 16-bit load of two bytes of a row, transposed, gives two dimensions of a key side
 // by side: output tiles hold even dimensions in their upper and odd ones in their lower

@@ -64,7 +64,9 @@ def attend(q, k, v, scale, window, weight, units=None):
             # (a score of next to no weight may be off by much)
             off = torch.exp((s - most + off).clamp(max=30.0)) - w + w * (weight + 2 * STEP * (len(s) / 16 + 16))
             off = torch.nan_to_num(off, nan=0.0)
-            bound[i, h] = off @ vs.abs() / total + off.sum() / total * (w @ vs.abs() / total) + least
+            # (N + n) / (S + e) is off N / S by (|n| + |N / S| |e|) / (S - |e|) at most
+            e = off.sum() / total
+            bound[i, h] = (off @ vs.abs() / total + e * (w @ vs / total).abs()) / (1 - e).clamp(min=1e-6) + least
     return o, bound
 
 
@@ -233,6 +235,22 @@ def test_a_score_of_minus_infinity_beside_others_is_no_weight(dev):
 
 
 # ---- the precision of weights ------------------------------------------------------
+
+@pytest.mark.parametrize("new,codes,weight", [(1, False, 2.0 ** -16), (1, True, None), (200, True, None), (200, False, 2.0 ** -8)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_weights_are_rounded_as_stated(dev, D, new, codes, weight):
+    """Two keys a row, of opposite values: what is left is of the size of the weights' errors."""
+    lengths = [(1, 2)] * 64 if new == 1 else [(new, new + 1)]
+    q, tensors, table, cu, lens = make(lengths, 2, 2, D, codes, 16, "slots", dev, seed=D, size=0.05)
+    for b, (n, kv) in enumerate(lengths):
+        for j in range(1, kv):
+            a, c = at(tensors, table, b, j), at(tensors, table, b, j - 1)
+            tensors[1][a] = tensors[1][c] ^ 0x80 if codes else -tensors[1][c]
+            if codes:
+                tensors[3][a] = tensors[3][c]
+    o = fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens, window=2)
+    check(lengths, q, tensors, table, o, 2, weight=weight)
+
 
 def test_a_thread_of_its_own(dev):
     """The first call of a host thread that has made no other."""
