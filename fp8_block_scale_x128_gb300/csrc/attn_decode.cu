@@ -427,10 +427,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
                     }
                 }
             // scores in units of log2, masked ones at minus infinity
-            const bool all = j0 + SL <= at.lowest + 1 && (p.window == 0 || j0 >= at.past - p.window);
             float most[NT][2], with[KT][NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) most[n][0] = most[n][1] = -INFINITY;
 #pragma unroll
             for (int k = 0; k < KT; ++k)
 #pragma unroll
@@ -442,16 +439,80 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             // codes: twice a factor, as their product may leave fp32's range
-                            float x = C::kCodes ? s[k][n][2 * h + i] * unit[n][i] * scale : s[k][n][2 * h + i] * p.scale_log2;
-                            float y = x + more;  // with the value's scale
-                            if (!all) {
-                                const int j = j0 + key, w = place[n][i];
-                                if (j > w || (p.window && j <= w - p.window)) x = y = -INFINITY;
-                            }
-                            s[k][n][2 * h + i] = x;
-                            if (C::kCodes) with[k][n][2 * h + i] = y;
-                            most[n][i] = fmaxf(most[n][i], C::kCodes ? y : x);
+                            float& x = s[k][n][2 * h + i];
+                            x = C::kCodes ? x * unit[n][i] * scale : x * p.scale_log2;
+                            if (C::kCodes) with[k][n][2 * h + i] = x + more;  // with the value's scale
                         }
+                }
+            bool odd = false;  // a value that is not finite where some row masks its key
+            if (!(j0 + SL <= at.lowest + 1 && (p.window == 0 || j0 >= at.past - p.window))) {
+#pragma unroll
+                for (int k = 0; k < KT; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int j = j0 + k * 16 + 8 * h + g, w = place[n][i];
+                                if (j > w || (p.window && j <= w - p.window)) {
+                                    s[k][n][2 * h + i] = -INFINITY;
+                                    if (C::kCodes) with[k][n][2 * h + i] = -INFINITY;
+                                }
+                            }
+                // (rows of one token see the same keys; the others are zeros here)
+                if (at.lowest + 1 < at.past) {
+                    uint32_t acc = 0;
+#pragma unroll 1
+                    for (int i = lane; i < SL * kChunks; i += 32) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(smem + (vs - ptx::smem_addr(smem)) + 16 * i);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            acc |= C::kCodes ? odd_codes(w[c]) : ((w[c] & 0x7F80u) == 0x7F80u) | ((w[c] & 0x7F800000u) == 0x7F800000u);
+                    }
+                    odd = __any_sync(0xFFFFFFFFu, acc != 0);
+                }
+                if (C::kCodes && odd) {
+                    // NaNs for the rows that see such a code, and a zero in its place.  (A scale of
+                    // 255 is in the weights of the rows that see its key.)
+                    uint8_t* rows = smem + (vs - ptx::smem_addr(smem));
+#pragma unroll 1
+                    for (int key = 0; key < SL; ++key) {
+                        const int j = j0 + key;
+                        bool sees[NT][2];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) sees[n][i] = j <= place[n][i] && (!p.window || j > place[n][i] - p.window);
+#pragma unroll
+                        for (int o = 0; o < kSteps; ++o) {
+                            const uint32_t w = odd_codes(*reinterpret_cast<const uint16_t*>(rows + chunk_at<RB>(key, o) + 2 * g));
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if ((w >> (8 * (i >> 1)) & 0x80u) && sees[n][i & 1]) out[o][n][i] = __uint_as_float(0x7FFFFFFFu);
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll 1
+                    for (int i = lane; i < SL * kChunks * 4; i += 32) {
+                        uint32_t* w = reinterpret_cast<uint32_t*>(rows) + i;
+                        *w = without_odd_codes(*w);
+                    }
+                    __syncwarp();
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    most[n][i] = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < KT; ++k)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) most[n][i] = fmaxf(most[n][i], C::kCodes ? with[k][n][2 * h + i] : s[k][n][2 * h + i]);
                 }
             bool grown = false;
             float shrink[NT][2], from[NT][2];
@@ -506,49 +567,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
                         }
                     }
                 }
-            bool odd = false;  // a value that is not finite where some row masks its key
-            if (!all) {
-                uint32_t acc = 0;
-#pragma unroll 1
-                for (int i = lane; i < SL * kChunks; i += 32) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(smem + (vs - ptx::smem_addr(smem)) + 16 * i);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        acc |= C::kCodes ? odd_codes(w[c]) : ((w[c] & 0x7F80u) == 0x7F80u) | ((w[c] & 0x7F800000u) == 0x7F800000u);
-                }
-                odd = __any_sync(0xFFFFFFFFu, acc != 0);
-            }
-            if (C::kCodes && odd) {
-                // NaNs for the rows that see such a code, and a zero in its place.  (A scale of
-                // 255 is in the weights of the rows that see its key.)
-                uint8_t* rows = smem + (vs - ptx::smem_addr(smem));
-#pragma unroll 1
-                for (int key = 0; key < SL; ++key) {
-                    const int j = j0 + key;
-                    bool sees[NT][2];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) sees[n][i] = j <= place[n][i] && (!p.window || j > place[n][i] - p.window);
-#pragma unroll
-                    for (int o = 0; o < kSteps; ++o) {
-                        const uint32_t w = odd_codes(*reinterpret_cast<const uint16_t*>(rows + chunk_at<RB>(key, o) + 2 * g));
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if ((w >> (8 * (i >> 1)) & 0x80u) && sees[n][i & 1]) out[o][n][i] = __uint_as_float(0x7FFFFFFFu);
-                    }
-                }
-                __syncwarp();
-#pragma unroll 1
-                for (int i = lane; i < SL * kChunks * 4; i += 32) {
-                    uint32_t* w = reinterpret_cast<uint32_t*>(rows) + i;
-                    *w = without_odd_codes(*w);
-                }
-                __syncwarp();
-            }
             if (C::kCodes || !odd) {
 #pragma unroll
                 for (int k = 0; k < KT; ++k)
