@@ -48,6 +48,7 @@ namespace {
 
 constexpr int kRows = 128;  // of a stream
 constexpr float kLag = 8.0f;
+constexpr float kFar = 65536.0f;  // scores whose rounding is 2^-8 and more
 constexpr int kMarks = 8;
 // That may be under way.  The loaders are at most three ahead of the outputs; warps that look
 // values through wait for nothing in units without masks, so an item's place is given to
@@ -736,36 +737,44 @@ __device__ __forceinline__ void mask_scores(uint32_t scores, int hi, int lo) {
     ptx::tmem_wait_st();
 }
 
-// Scores that have each its key's own scale, plus the exponents of the values', in units of
-// log2, in the place of a row's scores over codes whose scales are far apart.  Returns the
-// largest x without those exponents and the sum of 2^(x - that).
+// Scores in units of log2 with the exponents of the values' scales, each rounded for itself,
+// in the place of a row's products with the keys: x factor + e, or, where the scales of a
+// unit are far apart (row_scale), with each key's own.
 template <int KEYS>
-__device__ __noinline__ float2 scale_scores(uint32_t scores, const uint8_t (&row_scale)[2][128], float factor) {
-    float top = -INFINITY, sum = 0.0f;
+__device__ __noinline__ void far_scores(uint32_t scores, const uint8_t (*row_scale)[128], float factor, float e) {
 #pragma unroll 1
     for (int c = 0; c < KEYS; c += 16) {
         uint32_t s[16];
         ptx::tmem_ld_32x32b_x16(scores + c, s);
         ptx::tmem_wait_ld();
-        float most = top;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float x = __uint_as_float(s[i]) * factor * e8m0_to_float(row_scale[0][c + i]);
-            if (s[i] != 0xFF800000u) s[i] = __float_as_uint(x);  // (masked: whatever scale that key has)
-            most = fmaxf(most, __uint_as_float(s[i]));
-        }
-        const float at = most == -INFINITY ? 0.0f : most;
-        sum *= ex2(top - at);
-        top = most;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            sum += ex2(__uint_as_float(s[i]) - at);
-            s[i] = __float_as_uint(__uint_as_float(s[i]) + static_cast<float>(static_cast<int>(row_scale[1][c + i]) - 127));
+            if (s[i] != 0xFF800000u) {  // (masked: whatever scale that key has)
+                const float x = __fmul_rn(__uint_as_float(s[i]), factor);
+                s[i] = __float_as_uint(row_scale ? __fadd_rn(__fmul_rn(x, e8m0_to_float(row_scale[0][c + i])),
+                                                             static_cast<float>(static_cast<int>(row_scale[1][c + i]) - 127))
+                                                 : __fadd_rn(x, e));
+            }
         }
         tmem_st16(scores + c, s);
     }
     ptx::tmem_wait_st();
-    return make_float2(top, sum);
+}
+
+// The sum of a row's weights without the values' scales, which far_scores has put into them.
+template <int KEYS>
+__device__ __noinline__ float far_sum(uint32_t scores, const uint8_t (*row_scale)[128], float base) {
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < KEYS; c += 16) {
+        uint32_t s[16];
+        ptx::tmem_ld_32x32b_x16(scores + c, s);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            sum = fmaf(ex2(__uint_as_float(s[i]) - base), ex2(static_cast<float>(127 - static_cast<int>(row_scale[1][c + i]))), sum);
+    }
+    return sum;
 }
 
 // The values that are not finite, among the keys that a row sees in the item's units
@@ -900,8 +909,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
             }
             const float2 scale = C::kCodes ? sh.scales[u & 7] : make_float2(1.0f, 0.0f);
             const bool apart = C::kCodes && scale.x == 0.0f;
-            float2 unit = make_float2(0.0f, 0.0f);  // its largest score and sum
-            if (apart) unit = scale_scores<C::kKeys>(scores, sh.row_scale[u & 3], now);
+            if (apart) far_scores<C::kKeys>(scores, sh.row_scale[u & 3], now, 0.0f);
             // Codes: a loop over 32 scores, which are read again for their weights: the loaders'
             // code is long, and all of it has to stay in the instruction cache (4096 tokens over
             // 16384 keys 1065 us without, 997 so).  bf16: a row's scores in registers (681 us,
@@ -931,11 +939,23 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
             }
             // (above zero, so that masked scores stay minus infinity; scores are below 2^34, and
             // 2^-126 of that is nothing)
-            const float factor = apart ? 1.0f : C::kCodes ? fminf(fmaxf(now * scale.x, 0x1p-126f), 0x1.fffffep127f) : p.scale_log2;
-            const float top = scale.y + factor * fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
-                                                       fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
+            float factor = apart ? 1.0f : C::kCodes ? fminf(fmaxf(now * scale.x, 0x1p-126f), 0x1.fffffep127f) : p.scale_log2;
+            const float top = __fadd_rn(scale.y, __fmul_rn(factor, fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
+                                                                         fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])))));
+            // A score is not rounded before the maximum, which is, is taken from it.  Where that
+            // rounding is no small part of a power of two, weights would leave their range.
+            float with = scale.y;  // of the maximum, and not of the scores
+            if (__any_sync(0xFFFFFFFFu, fabsf(top) > kFar && top > -INFINITY && stream * kRows + row < at.rows)) {
+                if (!apart) far_scores<C::kKeys>(scores, nullptr, factor, scale.y);
+                if (!C::kCodes) {
+#pragma unroll
+                    for (int i = 0; i < kTimes; ++i) tmem_ld32(scores + 32 * i, reinterpret_cast<uint32_t*>(s) + 32 * i);
+                    ptx::tmem_wait_ld();
+                }
+                factor = 1.0f, with = 0.0f;
+            }
             float shrink = 1.0f;
-            if (top > most + kLag) {
+            if (top > __fadd_rd(most, kLag)) {
                 shrink = ex2(most - top);  // 0 from minus infinity
                 most = top;
             }
@@ -957,7 +977,9 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
                     ptx::tmem_wait_st();
                 }
             }
-            const float base = (most == -INFINITY ? 0.0f : most) - scale.y - (C::kCodes ? 7.0f : 0.0f);
+            const float base = __fsub_ru(most == -INFINITY ? 0.0f : most, with + (C::kCodes ? 7.0f : 0.0f));
+            float own = 0.0f;
+            if (apart) own = far_sum<C::kKeys>(scores, sh.row_scale[u & 3], base);
             const uint64_t factors = pair(factor, factor), minus = pair(-base, -base);
             uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll kTimes
@@ -975,7 +997,7 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
                 tmem_st16(weights + 16 * c, w);
             }
             const float2 both = halves(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
-            sum += apart ? unit.y * ex2(unit.x - base) : C::kCodes ? (both.x + both.y) * ex2(-scale.y) : both.x + both.y;
+            sum += apart ? own : C::kCodes ? (both.x + both.y) * ex2(-scale.y) : both.x + both.y;
             ptx::tmem_wait_st();
         }
         ptx::tc_fence_before();

@@ -427,21 +427,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
                     }
                 }
             // scores in units of log2, masked ones at minus infinity
-            float most[NT][2], with[KT][NT][4];
+            float most[NT][2], back[KT][2];  // of a key: its value's scale, inverted
 #pragma unroll
             for (int k = 0; k < KT; ++k)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int key = k * 16 + 8 * h + g;
                     const float scale = C::kCodes ? z[key] : 0.0f, more = C::kCodes ? z[SL + key] : 0.0f;
+                    if (C::kCodes) back[k][h] = more == more ? ex2(-more) : 1.0f;
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             // codes: twice a factor, as their product may leave fp32's range
                             float& x = s[k][n][2 * h + i];
-                            x = C::kCodes ? x * unit[n][i] * scale : x * p.scale_log2;
-                            if (C::kCodes) with[k][n][2 * h + i] = x + more;  // with the value's scale
+                            x = C::kCodes ? x * unit[n][i] * scale + more : x * p.scale_log2;  // with the value's scale
                         }
                 }
             bool odd = false;  // a value that is not finite where some row masks its key
@@ -455,10 +455,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const int j = j0 + k * 16 + 8 * h + g, w = place[n][i];
-                                if (j > w || (p.window && j <= w - p.window)) {
-                                    s[k][n][2 * h + i] = -INFINITY;
-                                    if (C::kCodes) with[k][n][2 * h + i] = -INFINITY;
-                                }
+                                if (j > w || (p.window && j <= w - p.window)) s[k][n][2 * h + i] = -INFINITY;
                             }
                 // (rows of one token see the same keys; the others are zeros here)
                 if (at.lowest + 1 < at.past) {
@@ -512,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
 #pragma unroll
                     for (int k = 0; k < KT; ++k)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) most[n][i] = fmaxf(most[n][i], C::kCodes ? with[k][n][2 * h + i] : s[k][n][2 * h + i]);
+                        for (int h = 0; h < 2; ++h) most[n][i] = fmaxf(most[n][i], s[k][n][2 * h + i]);
                 }
             bool grown = false;
             float shrink[NT][2], from[NT][2];
@@ -523,12 +520,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) most[n][i] = fmaxf(most[n][i], __shfl_xor_sync(0xFFFFFFFFu, most[n][i], off));
                     shrink[n][i] = 1.0f;
-                    if (most[n][i] > m[n][i] + kLag) {
+                    // (roundings that keep weights of codes within fp16's range, however large scores are)
+                    if (most[n][i] > __fadd_rd(m[n][i], kLag)) {
                         shrink[n][i] = ex2(m[n][i] - most[n][i]);  // 0 from minus infinity
                         m[n][i] = most[n][i];
                         grown = true;
                     }
-                    from[n][i] = (m[n][i] == -INFINITY ? 0.0f : m[n][i]) - (C::kCodes ? 7.0f : 0.0f);
+                    from[n][i] = __fsub_ru(m[n][i] == -INFINITY ? 0.0f : m[n][i], C::kCodes ? 7.0f : 0.0f);
                 }
             if (__any_sync(0xFFFFFFFFu, grown)) {
 #pragma unroll
@@ -551,8 +549,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             w[i] = ex2(s[k][n][2 * h + i] - from[n][i]);
-                            l[n][i] += w[i];
-                            if (C::kCodes) w[i] = ex2(with[k][n][2 * h + i] - from[n][i]);
+                            l[n][i] += C::kCodes ? w[i] * back[k][h] : w[i];
                             s[k][n][2 * h + i] = w[i];
                         }
                         if (C::kCodes) {

@@ -234,6 +234,47 @@ def test_a_score_of_minus_infinity_beside_others_is_no_weight(dev):
         check(lengths, q, tensors, table, fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens))
 
 
+# ---- large scores -------------------------------------------------------------------
+
+@pytest.mark.parametrize("power", [10, 14, 17, 20, 24, 27, 30, 50])
+@pytest.mark.parametrize("lengths", [[(4, 300), (7, 130)], [(150, 300), (40, 90)]])
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scores_of_any_size_leave_numbers(dev, D, codes, lengths, power):
+    """A row of one key has that key's value, whatever its score; a key far below another has no part."""
+    q, tensors, table, cu, lens = make(lengths, 4, 2, D, codes, 16, "slots", dev, seed=D + power)
+    if codes:
+        tensors[2][::2] += power  # pages in turn: units whose scales are far apart, or of one kind
+    else:
+        tensors[0].mul_(2.0 ** power)
+    cache = fb.KvCache(*tensors)
+    o = fb.fp8bs_attn_paged(q, cache, table, cu, lens, window=1)
+    first = 0
+    for b, (n, kv) in enumerate(lengths):
+        _, v = A.rows_of(tensors, table[b], kv)
+        ref = v[kv - n:].repeat_interleave(2, 1)
+        # a weight's rounding, a power of two's, and a score's with its value's exponent
+        A.near(o[first:first + n], ref, (2.0 ** -8 if not codes else 2.0 ** -11 + 2.0 ** -20) * ref.abs())
+        first += n
+    # two keys whose scores are far apart: the upper one's value
+    q = q.abs() + 0.5
+    for b, (n, kv) in enumerate(lengths):
+        for j in range(kv):
+            place = at(tensors, table, b, j)
+            if codes:
+                tensors[0][place], tensors[2][place] = (0x7E if j % 2 else 0xFE), 127 + power
+            else:
+                tensors[0][place] = 2.0 ** power * (8 if j % 2 else -8)
+    o = fb.fp8bs_attn_paged(q, cache, table, cu, lens, window=2)
+    first = 0
+    for b, (n, kv) in enumerate(lengths):
+        _, v = A.rows_of(tensors, table[b], kv)
+        places = torch.arange(kv - n, kv)
+        ref = v[torch.where(places % 2 == 1, places, (places - 1).clamp(min=0))].repeat_interleave(2, 1)
+        A.near(o[first:first + n], ref, (2.0 ** -8 if not codes else 2.0 ** -11 + 2.0 ** -20) * ref.abs())
+        first += n
+
+
 # ---- the precision of weights ------------------------------------------------------
 
 @pytest.mark.parametrize("new,codes,weight", [(1, False, 2.0 ** -16), (1, True, None), (200, True, None), (200, False, 2.0 ** -8)])
