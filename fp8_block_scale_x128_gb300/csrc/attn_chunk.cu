@@ -307,8 +307,8 @@ constexpr uint32_t kApart = 14;  // 2^-14 times a code is exact in fp16
 // 16 codes -> 16 fp16 numbers times the scale over the largest, or 1 where that is the
 // smaller (NaN for a scale of 255).
 __device__ __forceinline__ void widen(const uint4& c, uint32_t scale, uint32_t largest, uint4& lo, uint4& hi) {
-    const uint32_t down = min(largest - min(scale, largest), kApart);  // (more: no key)
-    const uint32_t bits = scale == 255u ? 0x7E00u : (15u - down) << 10;
+    const uint32_t down = largest - min(scale, largest);  // (past kApart: no key, or a row of zeros)
+    const uint32_t bits = scale == 255u ? 0x7E00u : down > kApart ? 0u : (15u - down) << 10;
     const __half2 f = __half2half2(__ushort_as_half(static_cast<unsigned short>(bits)));
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     __half2 r[8];
@@ -380,19 +380,20 @@ __device__ __forceinline__ void copy_units(const AttnParams& p, Shared& sh, uint
         }
     };
     auto keep_scales = [&](int u) {
-        uint32_t mostk = 0, mostv = 0, leastk = 255, leastv = 255;
+        uint32_t mostk = 0, mostv = 47, leastk = 255, leastv = 255;
 #pragma unroll
         for (int i = 0; i < C::kKeys / 32; ++i) {
-            // a value's scale below 2^-80 counts as that (the sum of the weights, which are
-            // taken against those times values, would leave fp32's range)
-            zv[i] = max(zv[i], 47u);
+            // A value's scale below 2^-80 counts as that (the sum of the weights, which are
+            // taken against those times values, would leave fp32's range).  Rows of byte 0, as
+            // rows of zeros have it, are zeros beside others: they set no scales apart.
+            if (zv[i] != 0) zv[i] = max(zv[i], 47u);
             sh.row_scale[u & 3][0][lane + 32 * i] = static_cast<uint8_t>(zk[i]);
             sh.row_scale[u & 3][1][lane + 32 * i] = static_cast<uint8_t>(zv[i]);
-            mostk = max(mostk, zk[i] < 255u ? zk[i] : 0u), leastk = min(leastk, zk[i]);
-            mostv = max(mostv, zv[i] < 255u ? zv[i] : 0u), leastv = min(leastv, zv[i]);
+            mostk = max(mostk, zk[i] < 255u ? zk[i] : 0u), leastk = min(leastk, zk[i] - 1u);
+            mostv = max(mostv, zv[i] < 255u ? zv[i] : 0u), leastv = min(leastv, zv[i] - 1u);
         }
         mostk = __reduce_max_sync(0xFFFFFFFFu, mostk), mostv = __reduce_max_sync(0xFFFFFFFFu, mostv);
-        const bool apart = __any_sync(0xFFFFFFFFu, mostk > leastk + kApart || mostv > leastv + kApart);
+        const bool apart = __any_sync(0xFFFFFFFFu, mostk > leastk + 1 + kApart || mostv > leastv + 1 + kApart);
         if (lane == 0) {
             sh.largest[u & 3][0] = apart ? 0u : mostk, sh.largest[u & 3][1] = apart ? 0u : mostv;
             sh.scales[u & 7] = apart ? make_float2(0.0f, 0.0f) : make_float2(e8m0_to_float(mostk), static_cast<float>(static_cast<int>(mostv) - 127));
@@ -752,7 +753,7 @@ __device__ __noinline__ void far_scores(uint32_t scores, const uint8_t (*row_sca
             if (s[i] != 0xFF800000u) {  // (masked: whatever scale that key has)
                 const float x = __fmul_rn(__uint_as_float(s[i]), factor);
                 s[i] = __float_as_uint(row_scale ? __fadd_rn(__fmul_rn(x, e8m0_to_float(row_scale[0][c + i])),
-                                                             static_cast<float>(static_cast<int>(row_scale[1][c + i]) - 127))
+                                                             static_cast<float>(max(static_cast<int>(row_scale[1][c + i]), 47) - 127))
                                                  : __fadd_rn(x, e));
             }
         }
@@ -772,7 +773,7 @@ __device__ __noinline__ float far_sum(uint32_t scores, const uint8_t (*row_scale
         ptx::tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            sum = fmaf(ex2(__uint_as_float(s[i]) - base), ex2(static_cast<float>(127 - static_cast<int>(row_scale[1][c + i]))), sum);
+            sum = fmaf(ex2(__uint_as_float(s[i]) - base), ex2(static_cast<float>(127 - max(static_cast<int>(row_scale[1][c + i]), 47))), sum);
     }
     return sum;
 }

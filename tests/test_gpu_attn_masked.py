@@ -200,6 +200,22 @@ def test_large_values_of_next_to_no_weight(dev, D, lengths, apart):
     check(lengths, q, tensors, table, o)
 
 
+@pytest.mark.parametrize("lengths", [[(4, 300), (7, 130)], [(150, 300), (40, 90)]])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_of_zeros_beside_others(dev, D, lengths):
+    """Keys and values of zeros, with a scale byte of 0 as an append writes them, and units of nothing else."""
+    q, tensors, table, cu, lens = make(lengths, 4, 2, D, True, 16, "slots", dev, seed=D)
+    g = torch.Generator(device=dev).manual_seed(2)
+    for i in (0, 1):
+        none = torch.rand(tensors[2 + i].shape, generator=g, device=dev) < 0.1
+        for j in range(128, 256):
+            if lengths[0][1] > j:
+                none[at(tensors, table, 0, j)] = True
+        tensors[i][none], tensors[2 + i][none] = 0, 0
+    o = fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens)
+    check(lengths, q, tensors, table, o)
+
+
 # ---- scores of minus infinity ------------------------------------------------------
 
 @pytest.mark.parametrize("codes", [False, True])
