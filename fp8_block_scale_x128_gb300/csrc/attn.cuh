@@ -327,6 +327,14 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+// A sum of weights against a maximum that is 2^-x as large.  (Over codes the maximum is of
+// weights times values' scales, so the sum may be far above it: 2^x alone would be nothing
+// where the sum times it is not.)
+__device__ __forceinline__ float fallen(float sum, float x) {
+    const float half = ex2(0.5f * x);
+    return sum * half * half;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

@@ -773,7 +773,7 @@ __device__ __noinline__ float far_sum(uint32_t scores, const uint8_t (*row_scale
         ptx::tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            sum = fmaf(ex2(__uint_as_float(s[i]) - base), ex2(static_cast<float>(127 - max(static_cast<int>(row_scale[1][c + i]), 47))), sum);
+            sum += ex2(__uint_as_float(s[i]) - base + static_cast<float>(127 - max(static_cast<int>(row_scale[1][c + i]), 47)));
     }
     return sum;
 }
@@ -955,13 +955,14 @@ __device__ __forceinline__ void weigh(const AttnParams& p, Shared& sh, uint8_t* 
                 }
                 factor = 1.0f, with = 0.0f;
             }
-            float shrink = 1.0f;
+            float fall = 0.0f;
             if (top > __fadd_rd(most, kLag)) {
-                shrink = ex2(most - top);  // 0 from minus infinity
+                fall = most - top;
                 most = top;
             }
-            if (__any_sync(0xFFFFFFFFu, shrink != 1.0f)) {
-                sum *= shrink;
+            if (__any_sync(0xFFFFFFFFu, fall != 0.0f)) {
+                const float shrink = ex2(fall);  // 0 from minus infinity
+                sum = fallen(sum, fall);
                 if (!first) {
                     // the products before this one are in the outputs
                     if (!__all_sync(0xFFFFFFFFu, wait(sh, &sh.joined[C::kStreams == 2 ? stream : buffer ^ 1], (C::kStreams == 2 ? u - 1 : (u - 1) >> 1) & 1, p))) return;

@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
             for (int w = 1; w < kWarps; ++w) most = fmaxf(most, sh.parts[w][row].x);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
-                sum += sh.parts[w][row].x == -INFINITY ? sh.parts[w][row].y : sh.parts[w][row].y * ex2(sh.parts[w][row].x - most);
+                sum += sh.parts[w][row].x == -INFINITY ? sh.parts[w][row].y : fallen(sh.parts[w][row].y, sh.parts[w][row].x - most);
             const float4 x = *reinterpret_cast<const float4*>(red + row * C::kPitch + col);
             const float4 y = *reinterpret_cast<const float4*>(red + row * C::kPitch + col + 4);
             if (whole) {
@@ -427,14 +427,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
                     }
                 }
             // scores in units of log2, masked ones at minus infinity
-            float most[NT][2], back[KT][2];  // of a key: its value's scale, inverted
+            float most[NT][2], in[KT][2];  // of a key: what its score has of its value's scale
 #pragma unroll
             for (int k = 0; k < KT; ++k)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int key = k * 16 + 8 * h + g;
                     const float scale = C::kCodes ? z[key] : 0.0f, more = C::kCodes ? z[SL + key] : 0.0f;
-                    if (C::kCodes) back[k][h] = more == more ? ex2(-more) : 1.0f;
+                    if (C::kCodes) in[k][h] = more == more ? more : 0.0f;
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -512,17 +512,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
                         for (int h = 0; h < 2; ++h) most[n][i] = fmaxf(most[n][i], s[k][n][2 * h + i]);
                 }
             bool grown = false;
-            float shrink[NT][2], from[NT][2];
+            float fall[NT][2], from[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) most[n][i] = fmaxf(most[n][i], __shfl_xor_sync(0xFFFFFFFFu, most[n][i], off));
-                    shrink[n][i] = 1.0f;
+                    fall[n][i] = 0.0f;
                     // (roundings that keep weights of codes within fp16's range, however large scores are)
                     if (most[n][i] > __fadd_rd(m[n][i], kLag)) {
-                        shrink[n][i] = ex2(m[n][i] - most[n][i]);  // 0 from minus infinity
+                        fall[n][i] = m[n][i] - most[n][i];
                         m[n][i] = most[n][i];
                         grown = true;
                     }
@@ -531,11 +531,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
             if (__any_sync(0xFFFFFFFFu, grown)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    l[n][0] *= shrink[n][0], l[n][1] *= shrink[n][1];
+                    const float shrink[2] = {ex2(fall[n][0]), ex2(fall[n][1])};  // 0 from minus infinity
+                    l[n][0] = fallen(l[n][0], fall[n][0]), l[n][1] = fallen(l[n][1], fall[n][1]);
 #pragma unroll
                     for (int o = 0; o < kSteps; ++o)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) out[o][n][i] *= shrink[n][i & 1];
+                        for (int i = 0; i < 4; ++i) out[o][n][i] *= shrink[i & 1];
                 }
             }
             uint32_t hi[KT][NT][2], low[KT][NT][2];  // [8 keys]: the product's operand
@@ -548,8 +549,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, KIND, NT>::kBlocks)
                         float w[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            w[i] = ex2(s[k][n][2 * h + i] - from[n][i]);
-                            l[n][i] += C::kCodes ? w[i] * back[k][h] : w[i];
+                            const float x = s[k][n][2 * h + i] - from[n][i];
+                            w[i] = ex2(x);
+                            l[n][i] += C::kCodes ? ex2(x - in[k][h]) : w[i];
                             s[k][n][2 * h + i] = w[i];
                         }
                         if (C::kCodes) {
@@ -669,8 +671,8 @@ __global__ void __launch_bounds__(kJoin) attn_join_kernel(const __grid_constant_
                 const float4 y = *reinterpret_cast<const float4*>(s + row * D + col + 4);
                 const float top = fmaxf(most, m), at = top == -INFINITY ? 0.0f : top;
                 const float keep = ex2(most - at), w = ex2(m - at);
+                sum = m == -INFINITY ? sum + l : fallen(l, m - at) + fallen(sum, most - at);
                 most = top;
-                sum = m == -INFINITY ? sum + l : fmaf(l, w, sum * keep);
                 v[0] = fmaf(x.x, w, v[0] * keep), v[1] = fmaf(x.y, w, v[1] * keep);
                 v[2] = fmaf(x.z, w, v[2] * keep), v[3] = fmaf(x.w, w, v[3] * keep);
                 v[4] = fmaf(y.x, w, v[4] * keep), v[5] = fmaf(y.y, w, v[5] * keep);
@@ -689,8 +691,8 @@ __global__ void __launch_bounds__(kJoin) attn_join_kernel(const __grid_constant_
                     const float* o = met[threadIdx.x + j * kPer];
                     const float top = fmaxf(most, o[0]), at = top == -INFINITY ? 0.0f : top;
                     const float keep = ex2(most - at), w = ex2(o[0] - at);
+                    sum = o[0] == -INFINITY ? sum + o[1] : fallen(o[1], o[0] - at) + fallen(sum, most - at);
                     most = top;
-                    sum = o[0] == -INFINITY ? sum + o[1] : fmaf(o[1], w, sum * keep);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] = fmaf(o[2 + i], w, v[i] * keep);
                 }

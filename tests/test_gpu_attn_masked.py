@@ -216,6 +216,19 @@ def test_rows_of_zeros_beside_others(dev, D, lengths):
     check(lengths, q, tensors, table, o)
 
 
+@pytest.mark.parametrize("lengths", [[(4, 300), (7, 130)], [(150, 300), (40, 90)]])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_of_zeros_beside_the_largest_values(dev, D, lengths):
+    """A value of zeros has its weight in the sum, also beside values of 2^50."""
+    q, tensors, table, cu, lens = make(lengths, 4, 2, D, True, 16, "slots", dev, seed=D)
+    g = torch.Generator(device=dev).manual_seed(3)
+    tensors[3][torch.rand(tensors[3].shape, generator=g, device=dev) < 0.2] += 60
+    none = torch.rand(tensors[3].shape, generator=g, device=dev) < 0.3
+    tensors[1][none], tensors[3][none] = 0, 0
+    o = fb.fp8bs_attn_paged(q, fb.KvCache(*tensors), table, cu, lens)
+    check(lengths, q, tensors, table, o)
+
+
 # ---- scores of minus infinity ------------------------------------------------------
 
 @pytest.mark.parametrize("codes", [False, True])
