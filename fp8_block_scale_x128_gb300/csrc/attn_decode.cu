@@ -670,8 +670,8 @@ __global__ void __launch_bounds__(kJoin) attn_join_kernel(const __grid_constant_
                 const float4 x = *reinterpret_cast<const float4*>(s + row * D + col);
                 const float4 y = *reinterpret_cast<const float4*>(s + row * D + col + 4);
                 const float top = fmaxf(most, m), at = top == -INFINITY ? 0.0f : top;
-                const float keep = ex2(most - at), w = ex2(m - at);
-                sum = m == -INFINITY ? sum + l : fallen(l, m - at) + fallen(sum, most - at);
+                const float keep1 = ex2(0.5f * (most - at)), w1 = ex2(0.5f * (m - at)), keep = keep1 * keep1, w = w1 * w1;
+                sum = m == -INFINITY ? sum + l : fmaf(l * w1, w1, sum * keep1 * keep1);  // (as fallen)
                 most = top;
                 v[0] = fmaf(x.x, w, v[0] * keep), v[1] = fmaf(x.y, w, v[1] * keep);
                 v[2] = fmaf(x.z, w, v[2] * keep), v[3] = fmaf(x.w, w, v[3] * keep);
@@ -690,8 +690,8 @@ __global__ void __launch_bounds__(kJoin) attn_join_kernel(const __grid_constant_
                 for (int j = 1; j < ways; ++j) {
                     const float* o = met[threadIdx.x + j * kPer];
                     const float top = fmaxf(most, o[0]), at = top == -INFINITY ? 0.0f : top;
-                    const float keep = ex2(most - at), w = ex2(o[0] - at);
-                    sum = o[0] == -INFINITY ? sum + o[1] : fallen(o[1], o[0] - at) + fallen(sum, most - at);
+                    const float keep1 = ex2(0.5f * (most - at)), w1 = ex2(0.5f * (o[0] - at)), keep = keep1 * keep1, w = w1 * w1;
+                    sum = o[0] == -INFINITY ? sum + o[1] : fmaf(o[1] * w1, w1, sum * keep1 * keep1);
                     most = top;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] = fmaf(o[2 + i], w, v[i] * keep);
