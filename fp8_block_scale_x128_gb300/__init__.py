@@ -900,9 +900,9 @@ def fp8bs_trace_read():
 
 
 def fp8bs_debug_config(timeout_cycles: int = 0, sm_count_override: int = 0) -> None:
-    """Diagnostic overrides of the fused GEMM's launches (tests only): the
-    bounded waits' limit in SM cycles and the multiprocessor count grids and
-    workspaces are sized for; 0 restores each default."""
+    """Diagnostic overrides (tests only): the limit in SM cycles of the bounded waits
+    inside the fused GEMM and the attention kernel of many rows, and the multiprocessor
+    count grids and workspaces are sized for; 0 restores each default."""
     _check(lib().fp8bs_debug_config(int(timeout_cycles), int(sm_count_override)), "fp8bs_debug_config")
 
 

@@ -30,13 +30,21 @@
 //
 // A value that is not finite and that some row of its unit masks would reach that row
 // as zero times it.  In units with masks the loaders put zeros in the place of such
-// values and mark the item; its rows then add those that they see at their end.
+// values (codes without a value among them) and mark the item; its rows then add those
+// that they see at their end.
 //
-// 4096 tokens over 16384 keys, 32 + 8 heads of 128, take 681 us (1.41 PFLOP/s, 0.77 of a
-// large matrix product's rate): 3320 cycles a unit, of which a stream's softmax 1800 and its
-// two products 1024 follow one another, beside the other stream's.  Over codes 997 us: the
-// widening shares the issue slots and the shared memory with the softmax.  An item's change
-// costs some 4000 cycles (outputs, next queries).
+// Scores from 2^16 on are rounded each for itself before the maximum is taken from them:
+// below that a multiply-add takes a rounded maximum from an unrounded score, which is off by
+// no power of two worth the name.
+//
+// 4096 tokens over 16384 keys, 32 + 8 heads of 128, take 664 to 729 us with pages of 64 (the
+// same inputs again and again, or others each time; 1.44 to 1.32 PFLOP/s, 0.78 to 0.72 of a
+// large matrix product's rate) and 670 to 695 with pages of 16 (the same inputs): some 3300
+// cycles a unit, of which a stream's softmax 1800 and its two products 1024 follow one another,
+// beside the other stream's.  Over codes 888 us with pages of 64, 1015 with pages of 16: the
+// widening shares the issue slots and the shared memory with the softmax, and one warp looks
+// pages up, reads scales and issues boxes.  (Below, what a variant that was not kept took
+// stands beside what this took then.)
 #include <cuda.h>
 #include <cuda_fp16.h>
 

@@ -21,16 +21,22 @@
 // exact down to 2^-31 of that, below off by at most 2^-39 of it.  A key's scale
 // multiplies its score.  A value's scale 2^e is part of its weight, 2^(x + e), the
 // maximum is taken of these, and 2^7 more uses fp16's range: a weight is off by at most
-// 2^-11 of itself, or 2^-32 of the largest.  (e below -80 counts as that, so that no sum
+// 2^-11 of itself, or 2^-32 of the largest.  The sum takes 2^((x + e) - e), so that what
+// the large numbers lose is the same in both.  (e below -80 counts as that, so that no sum
 // of the weights 2^x alone overflows.)
+//
+// Masks.  A slice that some row masks a part of has a branch of its own.  Values that are
+// not finite would reach a row that masks them as zero times them: over bf16 such a slice is
+// weighed key by key; over codes zeros stand in their place, and the rows that see them get
+// their NaNs at once.
 // A 16-bit load of two bytes of a row, transposed, gives two dimensions of a key side
 // by side: output tiles hold even dimensions in their upper and odd ones in their lower
 // half.
 //
-// Over bf16 the memory bounds it: one token over 131072 keys of 8 heads of 128 takes 85 us
-// (6.3 TB/s, 0.93 of a copy's rate).  Over codes their conversion and the weights do: 48
-// tokens over up to 8192 keys 95 us (4.8 TB/s, 0.70).  Few keys wait for two launches:
-// 777 take 9.7 us.
+// Over bf16 the memory bounds it: one token over 131072 keys of 8 heads of 128 takes 86 us
+// (6.2 TB/s, 0.92 of a copy's rate).  Over codes their conversion and the weights do: 48
+// tokens over up to 8192 keys 96 us (4.7 TB/s, 0.70).  Few keys wait for two launches, one
+// behind the other: 777 take 9.7 us, in a graph 9.2.
 #include "attn.cuh"
 #include "w4.cuh"
 
@@ -768,8 +774,9 @@ size_t attn_workspace_bytes(int D, int sm_count) {
 // file's kernel reads a sequence's keys once for 16 rows (8 with heads of 256), the other
 // once for 256 (128), at a higher cost of each step.  At 64 sequences of up to 8192 keys
 // (4560 on average), us by this one against the other, with so many rows on average:
-//   heads of 128: 12 rows bf16 204 / 253, codes 281 / 388; 23 rows 366 / 257, 497 / 392
-//   heads of 256: 14 rows bf16 194 / 115, codes 103 / 142; codes 19 rows 137 / 142, 24 172 / 141
+//   heads of 128: 12 rows bf16 198 / 237, codes 260 / 374; 23 rows 353 / 239, 462 / 377
+//   heads of 256: 14 rows bf16 184 / 109, codes 100 / 145; codes 19 rows 137 / 147, 24 171 / 147
+//   heads of 64 (which take the value of 128): 12 rows 135 / 200, 115 / 352; 23 rows 235 / 200, 186 / 352
 static int64_t chunk_rows(const AttnArgs& a) {
     return a.D < 256 ? 17 : a.kind == FP8BS_KV_BF16 ? 9 : 20;
 }

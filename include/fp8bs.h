@@ -536,7 +536,8 @@ int fp8bs_rope_freqs(int rotary_dim, double theta, int scaling, double factor, d
  *   freqs      : DEVICE uint64 [R/2] from fp8bs_rope_freqs, 8-byte aligned.
  *   R          : 0 (no rotation) .. D, even; a multiple of 16 in the HALF layout.
  *   amplitude  : finite.   gamma_q, gamma_k : bf16 [D], 16-byte aligned, or NULL.
- *   eps        : finite, >= 0.  A row of zeros with eps 0 stays zeros.
+ *   eps        : finite, >= 0.  A row of zeros with eps 0 stays zeros.  (Squares are
+ *                summed in fp32: their mean and eps have to be within its range.)
  *   q_out, k_out : bf16 [T, heads, D] with strides of their own; may be q and k
  *                themselves with the same strides, else apart from them.
  * All pointers 16-byte aligned and all strides multiples of 8, where not said
@@ -608,8 +609,13 @@ size_t fp8bs_attn_paged_workspace_bytes(int64_t D, int sm_count);
  * keys j <= place, with a window only those j > place - window.  For each of its
  * query heads h, with key head h / (Hq / kv_heads):
  *   o = sum_j w_j v_j,  w = softmax_j(scale q . k_j)
- * Scores, maxima, sums and products are kept in fp32; see the sources for how weights
- * enter the product with the values.  A row that sees no key gives zeros.
+ * Scores, maxima, sums and products are kept in fp32.  A weight enters the product with
+ * the values rounded: over codes to fp16, off by at most 2^-11 of itself (or 2^-32 of the
+ * largest weight times the largest scale, where scales differ by up to 2^14; beyond that
+ * each weight has its own value's scale); over bf16 as the sum of two bf16 numbers,
+ * 2^-16, where few rows a sequence are new, and as one, 2^-8, where many are.  Which of
+ * the two it is goes by the call: T * Hq / kv_heads rows to B sequences on average, from
+ * 17 on many (from 9 with heads of 256).  A row that sees no key gives zeros.
  *   q           : bf16 [T, Hq, D], strides ldq, hsq; o: bf16 the same, strides ldo, hso.
  *                 Pointers 16-byte aligned, strides multiples of 8; o apart from all
  *                 inputs.  Rows outside all sequences are left as they were.
@@ -629,11 +635,19 @@ size_t fp8bs_attn_paged_workspace_bytes(int64_t D, int sm_count);
  * Lengths that do not fit T or the table, and pages that the cache does not have,
  * record FP8BS_ERR_DEVICE; the rows of such a sequence are not specified, and nothing
  * outside the tensors is touched.  Masked keys and values have no part in a row,
- * whatever they hold; an infinity or a NaN that a row sees makes its results NaN or
- * infinite.  In a cache of codes q, keys and values are below 2^63 in magnitude, and
- * a value's scale below 2^-80 counts as 2^-80.  Results are deterministic, and a row's
- * do not depend on whether other heads or sequences hold NaNs.  Two launches, dependent
- * on their predecessors, for which they wait before they touch memory.
+ * whatever they hold.  A value that is an infinity or a NaN makes the results of the rows
+ * that see it NaN or infinite in its dimension (a scale byte of 255: in all), and so does
+ * a score that is NaN or plus infinity; one of minus infinity is a weight of zero, and a
+ * row that sees keys, all at that, is NaN.  Scores may be of any size within fp32's range
+ * (in units of log2, and over codes with the exponent of the value's scale; they are
+ * rounded there).  In a cache of codes q, keys and values are below 2^63 in magnitude, a
+ * value's scale below 2^-80 counts as 2^-80, and a row of scale byte 0 may count as
+ * zeros.  Scales more than 2^14 apart among 128 neighbouring keys (64 with heads of 256)
+ * make a call of many rows up to five times as slow there.  Results are deterministic,
+ * and a row's do not depend on whether other heads or sequences hold NaNs.  Waits inside
+ * the kernel are bounded: one that runs out records FP8BS_ERR_TIMEOUT, and the call's
+ * rows are not specified.  Two launches, dependent on their predecessors, for which they
+ * wait before they touch memory.
  * Errors: FP8BS_ERR_ARG, FP8BS_ERR_SHAPE, FP8BS_ERR_ALIGN, FP8BS_ERR_WORKSPACE,
  * FP8BS_ERR_CUDA. */
 int fp8bs_attn_paged(const uint16_t* q, int64_t ldq, int64_t hsq, int64_t T, int64_t Hq,
@@ -708,7 +722,7 @@ int fp8bs_trace_read(void* host_dst, size_t bytes);
 /* ------------------------------------------------------------------------ */
 
 /* Override, for the calls that follow in this process, two settings of the
- * fused GEMM's launches:
+ * fused GEMM's launches (the first also of attention of many rows):
  *   timeout_cycles   : the limit of every bounded wait inside the kernel, in
  *                      SM clock cycles; <= 0 restores the default (2e9,
  *                      about 1 s), which is set far above any legitimate wait.
